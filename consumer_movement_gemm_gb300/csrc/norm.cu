@@ -1,0 +1,305 @@
+// norm.cu -- residual addition and root-mean-square norm of token rows, with
+// a bf16 output and an e4m3 output that has one fp32 scale per group.
+//
+//   r = x + residual            y = r * rsqrt(mean(r^2) + eps) * weight
+//   residual_out = round(r)     out = bf16(y)
+//   scale = max(amax over the group of |y|, 1e-12) / 448,   q = e4m3(y / scale)
+//
+// One pass over memory: a row stays in registers from the load to the last
+// store, everything is fp32 in between.  Rows up to 1024 elements take a warp
+// each (no barrier), longer ones a CTA each (one barrier).  A thread holds
+// groups of 8 consecutive elements, so a scale group of 32, 64 or 128 columns
+// is 4, 8 or 16 neighbouring lanes.
+#include <cuda_bf16.h>
+#include <type_traits>
+#include "common.cuh"
+#include "ops.cuh"
+
+namespace tovl {
+
+namespace {
+
+constexpr float kE4m3Max = 448.f;
+constexpr float kMinAmax = 1e-12f;     // keeps 448 / amax finite
+constexpr int kWarpRows = 8;           // rows per CTA of the warp-per-row form
+constexpr int kWarpRowMax = 1024;      // longest row of the warp-per-row form
+
+// Larger operand, NaN if one is (a NaN shows in its group's scale).
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ float2 unpack2(uint32_t v)
+{
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Eight consecutive elements, of which the first n exist, moved in accesses of
+// W elements.
+template <int W>
+__device__ __forceinline__ void load8(float (&v)[8], const __nv_bfloat16* p, int n)
+{
+    if constexpr (W == 8) {
+        if (n <= 0) return;
+        const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = unpack2(w[i]);
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
+    } else if constexpr (W == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (2 * i < n) {
+                const float2 f = unpack2(__ldg(reinterpret_cast<const uint32_t*>(p) + i));
+                v[2 * i] = f.x;
+                v[2 * i + 1] = f.y;
+            }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) v[i] = __bfloat162float(p[i]);
+    }
+}
+
+template <int W>
+__device__ __forceinline__ void load8(float (&v)[8], const float* p, int n)
+{
+    if constexpr (W == 8) {
+        if (n <= 0) return;
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) v[i] = __ldg(p + i);
+    }
+}
+
+template <int W>
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8], int n)
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = ptx::pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    if constexpr (W == 8) {
+        if (n > 0) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else if constexpr (W == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (2 * i < n) reinterpret_cast<uint32_t*>(p)[i] = w[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) p[i] = __float2bfloat16(v[i]);
+    }
+}
+
+template <int W>
+__device__ __forceinline__ void store8(float* p, const float (&v)[8], int n)
+{
+    if constexpr (W == 8) {
+        if (n <= 0) return;
+        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) p[i] = v[i];
+    }
+}
+
+template <int W>
+__device__ __forceinline__ void store8_e4m3(uint8_t* p, const float (&v)[8], float inv, int n)
+{
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = e4m3x2(v[2 * i] * inv, v[2 * i + 1] * inv);
+    if constexpr (W == 8) {
+        if (n > 0) *reinterpret_cast<uint2*>(p) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+    } else if constexpr (W == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (2 * i < n) reinterpret_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(h[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) p[i] = static_cast<uint8_t>(h[i / 2] >> (8 * (i & 1)));
+    }
+}
+
+// Sum (or NaN-keeping maximum) over the threads of a row; every thread gets
+// the same value, added in the same order.
+template <bool MAX>
+__device__ __forceinline__ float row_reduce(float v, float* buf, bool warp_row)
+{
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+        const float o = __shfl_xor_sync(0xffffffffu, v, d);
+        v = MAX ? max_nan(v, o) : v + o;
+    }
+    if (warp_row) return v;
+    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) buf[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = lane < warps ? buf[lane] : 0.f;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+        const float o = __shfl_xor_sync(0xffffffffu, v, d);
+        v = MAX ? max_nan(v, o) : v + o;
+    }
+    return v;
+}
+
+// RES: 0 none, 1 bf16, 2 fp32.  VPT: groups of 8 elements per thread.
+template <int W, int VPT, int RES>
+__global__ void __launch_bounds__(1024) norm_kernel(const NormParams p, int warp_row)
+{
+    __shared__ float sum_buf[32], max_buf[32];
+    using R = typename std::conditional<RES == 2, float, __nv_bfloat16>::type;
+    const long long row = warp_row ? static_cast<long long>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+    const int tid = warp_row ? threadIdx.x & 31 : threadIdx.x;
+    const int step = (warp_row ? 32 : blockDim.x) * 8;
+    const __nv_bfloat16* weight = static_cast<const __nv_bfloat16*>(p.weight);
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    if (row >= p.T) return;     // whole warps only
+    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x) + row * p.ldx;
+    float v[VPT][8], g[VPT][8];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int c = tid * 8 + j * step;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[j][i] = g[j][i] = 0.f;
+        load8<W>(v[j], x + c, p.H - c);
+        load8<W>(g[j], weight + c, p.H - c);
+    }
+    if (RES) {
+        const R* res = static_cast<const R*>(p.residual) + row * p.ldr;
+        float o[VPT][8];
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int c = tid * 8 + j * step;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[j][i] = 0.f;
+            load8<W>(o[j], res + c, p.H - c);
+        }
+        R* dst = static_cast<R*>(p.residual_out) + row * p.ldr;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int c = tid * 8 + j * step;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[j][i] += o[j][i];
+            store8<W>(dst + c, v[j], p.H - c);
+        }
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(v[j][i], v[j][i], ss);
+    ss = row_reduce<false>(ss, sum_buf, warp_row);
+    const float inv_rms = rsqrtf(ss / p.H + p.eps);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[j][i] = v[j][i] * inv_rms * g[j][i];
+    if (p.out) {
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row * p.ldo;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int c = tid * 8 + j * step;
+            store8<W>(out + c, v[j], p.H - c);
+        }
+    }
+    if (!p.q) return;
+    float amax[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        amax[j] = 0.f;
+        // (elements past the row's end may be 0 * infinity)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (tid * 8 + j * step + i < p.H) amax[j] = max_nan(amax[j], fabsf(v[j][i]));
+    }
+    float* scale = p.q_scale + row * p.n_groups;
+    uint8_t* q = p.q + row * p.H;
+    if (p.group == p.H) {
+        float m = amax[0];
+#pragma unroll
+        for (int j = 1; j < VPT; ++j) m = max_nan(m, amax[j]);
+        m = max_nan(row_reduce<true>(m, max_buf, warp_row), kMinAmax);
+        if (tid == 0) scale[0] = m / kE4m3Max;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int c = tid * 8 + j * step;
+            store8_e4m3<W>(q + c, v[j], kE4m3Max / m, p.H - c);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int c = tid * 8 + j * step;
+            float m = amax[j];
+            m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            if (p.group > 32) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 4));
+            if (p.group > 64) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 8));
+            m = max_nan(m, kMinAmax);
+            if (c % p.group == 0 && c < p.H) scale[c / p.group] = m / kE4m3Max;
+            store8_e4m3<W>(q + c, v[j], kE4m3Max / m, p.H - c);
+        }
+    }
+}
+
+template <int W, int VPT>
+cudaError_t launch(const NormParams& p, const cudaLaunchConfig_t& lc, int warp_row)
+{
+    if (!p.residual) return cudaLaunchKernelEx(&lc, norm_kernel<W, VPT, 0>, p, warp_row);
+    if (!p.residual_f32) return cudaLaunchKernelEx(&lc, norm_kernel<W, VPT, 1>, p, warp_row);
+    return cudaLaunchKernelEx(&lc, norm_kernel<W, VPT, 2>, p, warp_row);
+}
+
+template <int W>
+cudaError_t launch(const NormParams& p, const cudaLaunchConfig_t& lc, int warp_row, int vpt)
+{
+    if (vpt <= 1) return launch<W, 1>(p, lc, warp_row);
+    if (vpt <= 2) return launch<W, 2>(p, lc, warp_row);
+    return launch<W, 4>(p, lc, warp_row);
+}
+
+}  // namespace
+
+cudaError_t launch_norm(const NormParams& p, int width, cudaStream_t stream, bool pdl)
+{
+    const int vecs = (p.H + 7) / 8;
+    const int warp_row = p.H <= kWarpRowMax;
+    int vpt = warp_row ? (vecs + 31) / 32 : (vecs + 1023) / 1024;
+    if (vpt == 3) vpt = 4;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(warp_row ? (p.T + kWarpRows - 1) / kWarpRows : p.T);
+    lc.blockDim = dim3(warp_row ? kWarpRows * 32 : ((vecs + vpt - 1) / vpt + 31) / 32 * 32);
+    lc.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = pdl ? 1 : 0;
+    if (width == 8) return launch<8>(p, lc, warp_row, vpt);
+    if (width == 2) return launch<2>(p, lc, warp_row, vpt);
+    return launch<1>(p, lc, warp_row, vpt);
+}
+
+}  // namespace tovl

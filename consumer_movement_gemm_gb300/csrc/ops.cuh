@@ -1,0 +1,107 @@
+// ops.cuh -- parameter blocks and launchers of the decode-step operators:
+// residual + RMS norm, router top-k, the expert layer for few tokens, products
+// with 4-bit weights.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include "ctrl.cuh"
+
+namespace tovl {
+
+constexpr int kMaxDecodeRows = 64;     // tokens of one moe_decode / matvec_q4 call
+constexpr int kMaxDecodeK = 16;        // experts per token of one moe_decode call
+constexpr int kMaxTopk = 32;           // experts per token of one route_topk call
+constexpr int kXScaleGroup = 128;      // columns per scale of 8-bit activations
+
+// Counters of the split-tile kernels (handle-owned, zero between calls): one
+// arrival counter per first contributor of a split tile, for two phases, then
+// the count of finished tiles and the count of CTAs past the phase barrier.
+constexpr int kMaxGrid = 1024;
+constexpr int kReadyWord = 2 * kMaxGrid;
+constexpr int kExitWord = 2 * kMaxGrid + 32;
+constexpr int kSyncWords = 2 * kMaxGrid + 64;
+
+enum : int { kTypeBf16 = 0, kTypeF32 = 1, kTypeE4m3 = 2 };
+
+struct NormParams {
+    const void* x;          // bf16 [T][H], rows ldx elements apart
+    const void* residual;   // bf16 or fp32 [T][H], rows ldr apart; null = none
+    void* residual_out;     // same type and stride
+    const void* weight;     // bf16 [H]
+    void* out;              // bf16 [T][H] rows ldo apart; null = none
+    uint8_t* q;             // e4m3 [T][H] contiguous; null = none
+    float* q_scale;         // [T][n_groups]
+    long long ldx, ldr, ldo;
+    float eps;
+    int T, H;
+    int group;              // columns per scale (H for one per row)
+    int n_groups;
+    int residual_f32;
+};
+cudaError_t launch_norm(const NormParams& p, int width, cudaStream_t stream, bool pdl);
+
+struct RouteParams {
+    const void* logits;     // [T][E] fp32 or bf16, rows ld elements apart
+    int* topk;              // [T][k]
+    float* gate_w;          // [T][k]
+    long long ld;
+    int T, E, k;
+    int f32;
+    int renormalize;
+};
+cudaError_t launch_route(const RouteParams& p, cudaStream_t stream, bool pdl);
+
+// One weight matrix (or one per expert): bf16 [E][K][N], or packed nibbles
+// [E][K/8][N] with scales and zeros [E][K/group][N].
+struct WeightMaps {
+    CUtensorMap w, scale, zero;
+};
+
+struct MoeParams {
+    WeightMaps w13, w2;
+    const void* x;          // bf16 [T][H], rows ldx apart
+    long long ldx;
+    const int* topk;        // [T][k]
+    const float* gate_w;    // [T][k]
+    void* out;              // bf16 [T][H], rows ldo apart
+    long long ldo;
+    void* h_hi;             // bf16 [T*k][I]: activations between the two products, and
+    void* h_lo;             // what their rounding to bf16 left over
+    float* part1;           // [grid][2][64][128] partial gate/up tiles
+    float* part2;           // [grid][2][T][64] partial output tiles
+    int T, k, E, H, I;
+    int group, has_zero;    // 4-bit weights only
+    int* sync;              // kSyncWords counters
+    int ready_offset;       // fault injection: tiles that never come
+    long long timeout_ns, pipe_timeout_ns;
+    Ctrl ctrl;
+};
+cudaError_t prepare_moe_decode();
+cudaError_t launch_moe_decode(const MoeParams& p, bool q4, int grid, cudaStream_t stream, bool cooperative, bool pdl);
+
+struct MatvecParams {
+    WeightMaps w;
+    const void* x;          // bf16 or e4m3 [T][K], rows ldx apart
+    const float* x_scale;   // [T][ceil(K/128)] for e4m3
+    void* out;              // bf16 [T][N], rows ldo apart
+    float* part;            // [grid][2][32][64] partial tiles
+    long long ldx, ldo;
+    int T, K, N;
+    int group, has_zero;
+    int* sync;
+    long long pipe_timeout_ns;
+    Ctrl ctrl;
+};
+cudaError_t prepare_matvec_q4();
+cudaError_t launch_matvec_q4(const MatvecParams& p, bool e4m3, int grid, cudaStream_t stream, bool pdl);
+
+struct QuantParams {
+    const void* w;          // bf16 [E][K][N]
+    uint32_t* q;            // [E][K/8][N]
+    void* scale;            // bf16 [E][K/group][N]
+    uint8_t* zero;          // [E][K/group][N]; null = symmetric (zero 8)
+    int E, K, N, group;
+};
+cudaError_t launch_quantize_q4(const QuantParams& p, cudaStream_t stream);
+
+}  // namespace tovl

@@ -12,74 +12,9 @@
 #include <new>
 
 #include "tovl.h"
-#include "ctrl.cuh"
+#include "ctx.cuh"
 #include "launch.cuh"
-
-#define TOVL_API extern "C" __attribute__((visibility("default")))
-
-using namespace tovl;
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-struct tovl_ctx {
-    tovl_config cfg;
-    int device = 0;
-    int num_sms = 0;
-    int producers = 0;       // 0 = automatic split per call
-    int last_P = 0, last_C = 0;
-    int consumers = 0;
-    int copy_mode = TOVL_COPY_AUTO;     // vector below 8 KB rows, bulk from 8 KB (measured best per size)
-    int stats = 0;
-    long long timeout_ns = 2000000000LL;
-    int copy_ctas = 0;       // copy sweep copiers (0 = auto)
-    int copy_waiters = 0;    // copy sweep waiters (0 = auto)
-    int fault_gate_offset = 0;  // test hook: gates wait for seq + offset
-    int slices = 1;          // K-slices per chunk watermark (fixed per handle)
-    int pair_mode = 1;       // gather calls use CTA-pair (cta_group::2) consumers when possible
-    int max_pairs = 0;       // co-resident CTA pairs of the pair kernel on this device
-    bool coop_pairs = true;  // cooperative launch accepted together with clusters
-    bool coop_enabled = true;  // fused launches ask for the co-residency guarantee
-    int producer_mode = 0;     // fused producers: 0 vector copies, 1 staged bulk loads
-    int dispatch_align = kBlockRows;  // expert segment alignment: 128, or 256 for CTA-pair tiles
-    bool pdl = true;           // programmatic dependent launch between this library's kernels
-    int role_switch = 1;       // 1: dispatch (single-CTA tiles) and reduce-scatter roles switch; 2: CTA-pair dispatch too
-    int embedded = 1;          // without producer CTAs, the consumer CTAs' spare warps copy: 1 dispatch, 2 also gather
-    int rs_epi = 0;            // 1: reduce-scatter tiles are summed by their owners' idle warps (no producer CTAs)
-    int wide_tiles = 1;        // 1: CTA-pair dispatch tiles (embedded producers) are 256 x 512 where N allows
-    int l2_hints = -1;         // kHint* bits for every fused call; -1 = each call's measured default
-    bool pdl_ok = true;        // cleared if the device rejects the launch attribute
-    long long seq = 0;
-    Ctrl ctrl{};
-    Plan plan{};
-    int max_seg = 0;
-    void* ctrl_mem = nullptr;    // one allocation for the control plane
-    void* plan_mem = nullptr;    // one allocation for plan scratch
-    cudaStream_t last_stream = nullptr;
-    const void* last_dispatched = nullptr;
-    int last_T = 0, last_k = 0, last_E = 0;
-    long long last_tiles = 0;    // tiles and K-slices of the last fused call (trace layout)
-    int last_ks = 0;
-    EncodeTiledFn encode = nullptr;
-    char last_error[256] = {0};
-};
-
-static int cuda_fail(tovl_ctx* h, cudaError_t e, const char* what)
-{
-    if (h) std::snprintf(h->last_error, sizeof h->last_error, "%s: %s", what, cudaGetErrorString(e));
-    return TOVL_ERR_CUDA;
-}
-
-static bool aligned16(const void* p)
-{
-    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
-}
-
-static long long ceil_div(long long a, long long b)
-{
-    return (a + b - 1) / b;
-}
+#include "ops.cuh"
 
 TOVL_API void tovl_default_config(tovl_config* cfg, int device)
 {
@@ -233,6 +168,8 @@ TOVL_API int tovl_create(tovl_handle* out, const tovl_config* cfg_in)
         if ((e = prepare_plan()) != cudaSuccess) { rc = cuda_fail(h, e, "prepare plan"); break; }
         if ((e = prepare_copy()) != cudaSuccess) { rc = cuda_fail(h, e, "prepare copy"); break; }
         if ((e = prepare_combine()) != cudaSuccess) { rc = cuda_fail(h, e, "prepare combine"); break; }
+        if ((e = prepare_moe_decode()) != cudaSuccess) { rc = cuda_fail(h, e, "prepare moe decode"); break; }
+        if ((e = prepare_matvec_q4()) != cudaSuccess) { rc = cuda_fail(h, e, "prepare matvec"); break; }
         if (fused_max_active_per_sm() < 1) { rc = TOVL_ERR_UNSUPPORTED; break; }
         h->max_pairs = fused_max_active_pairs();
 
@@ -241,11 +178,13 @@ TOVL_API int tovl_create(tovl_handle* out, const tovl_config* cfg_in)
         Carve sizing{nullptr, 0};
         Ctrl tmp_ctrl{};
         carve_ctrl(sizing, tmp_ctrl, n_chunks, n_blocks, h->slices);
+        sizing.take<int>(kSyncWords);
         const size_t ctrl_bytes = sizing.off + 256;
         if ((e = cudaMalloc(&h->ctrl_mem, ctrl_bytes)) != cudaSuccess) { rc = TOVL_ERR_OOM; cudaGetLastError(); break; }
         if ((e = cudaMemset(h->ctrl_mem, 0, ctrl_bytes)) != cudaSuccess) { rc = cuda_fail(h, e, "memset"); break; }
         Carve cc{static_cast<char*>(h->ctrl_mem), 0};
         carve_ctrl(cc, h->ctrl, n_chunks, n_blocks, h->slices);
+        h->sync_words = cc.take<int>(kSyncWords);
 
         const int E = cfg.max_experts > 0 ? cfg.max_experts : 1;
         h->max_seg = static_cast<int>(ceil_div(cfg.max_pairs > 0 ? cfg.max_pairs : 1, 1024));
@@ -487,16 +426,6 @@ static int reset_stats(tovl_ctx* h, cudaStream_t s, long long tiles, int ks)
     if (e == cudaSuccess) e = cudaMemsetAsync(h->ctrl.stats + kStatProdStartNs, 0xff, sizeof(unsigned long long), s);
     return e == cudaSuccess ? TOVL_OK : cuda_fail(h, e, "stats reset");
 }
-
-struct DeviceGuard {
-    int prev = 0;
-    explicit DeviceGuard(int dev)
-    {
-        cudaGetDevice(&prev);
-        if (prev != dev) cudaSetDevice(dev);
-    }
-    ~DeviceGuard() { cudaSetDevice(prev); }
-};
 
 // Shared validation of the gather shapes.
 static int check_gather(tovl_ctx* h, const void* const* shards, int S, int R, int K)
@@ -976,6 +905,8 @@ TOVL_API int tovl_sync_status(tovl_handle h)
     if (e != cudaSuccess) return cuda_fail(h, e, "status read");
     if (st != 0) {
         e = cudaMemset(h->ctrl.status, 0, sizeof st);
+        // a kernel that gave up a wait may have left its counters unfinished
+        if (e == cudaSuccess) e = cudaMemset(h->sync_words, 0, kSyncWords * sizeof(int));
         if (e != cudaSuccess) return cuda_fail(h, e, "status clear");
     }
     return st;

@@ -25,6 +25,10 @@ TOVL_COPY_VECTOR = 0
 TOVL_COPY_BULK = 1
 TOVL_COPY_AUTO = 2
 
+TOVL_BF16 = 0
+TOVL_F32 = 1
+TOVL_E4M3 = 2
+
 OPT_PRODUCERS = 1
 OPT_CONSUMERS = 2
 OPT_COPY_MODE = 3
@@ -77,6 +81,7 @@ class tovl_config(ctypes.Structure):
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _LL = ctypes.c_longlong
+_F = ctypes.c_float
 _IP = ctypes.POINTER(ctypes.c_int)
 _LLP = ctypes.POINTER(ctypes.c_longlong)
 _ULLP = ctypes.POINTER(ctypes.c_ulonglong)
@@ -90,6 +95,15 @@ SIGNATURES = {
     "tovl_dispatch_grouped_gemm": ([_P, _P, _I, _I, _P, _I, _I, _P, _I, _P, _P, _P, _P], _I),
     "tovl_combine": ([_P, _P, _I, _P, _P, _P, _P], _I),
     "tovl_gemm_reduce_scatter": ([_P, _P, _I, _I, _I, _P, _I, _P, _P, _P], _I),
+    "tovl_add_rmsnorm": ([_P, _P, _LL, _P, _P, _I, _LL, _P, _F, _I, _I, _P, _LL, _P, _P, _I, _P], _I),
+    "tovl_route_topk": ([_P, _P, _I, _LL, _I, _I, _I, _I, _P, _P, _P], _I),
+    "tovl_moe_decode_workspace": ([_P, _I, _I, _I, _I], _LL),
+    "tovl_moe_decode": ([_P, _P, _LL, _I, _I, _P, _P, _I, _I, _P, _P, _I, _P, _LL, _P, _LL, _P], _I),
+    "tovl_moe_decode_q4": ([_P, _P, _LL, _I, _I, _P, _P, _I, _I, _P, _P, _P, _P, _P, _P, _I, _I, _P, _LL, _P, _LL,
+                            _P], _I),
+    "tovl_matvec_q4_workspace": ([_P, _I, _I], _LL),
+    "tovl_matvec_q4": ([_P, _P, _I, _P, _LL, _I, _I, _P, _P, _P, _I, _I, _P, _LL, _P, _LL, _P], _I),
+    "tovl_quantize_q4": ([_P, _P, _I, _I, _I, _I, _P, _P, _P, _P], _I),
     "tovl_gemm_only": ([_P, _P, _I, _I, _P, _I, _P, _P], _I),
     "tovl_copy_only": ([_P, ctypes.POINTER(_P), _I, _I, _I, _P, _P], _I),
     "tovl_gated_copy": ([_P, _P, _P, _LL, _I, _P, _I, _I, _P], _I),
@@ -155,6 +169,48 @@ def _stream(stream) -> int:
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+_RESIDUAL_TYPES = {"torch.bfloat16": TOVL_BF16, "torch.float32": TOVL_F32}
+_ROW_TYPES = {"torch.bfloat16": TOVL_BF16, "torch.float8_e4m3fn": TOVL_E4M3}
+
+
+def _type_of(name, t, types) -> int:
+    code = types.get(str(t.dtype))
+    if code is None:
+        raise TypeError(f"{name} must be one of {', '.join(types)}, not {t.dtype}")
+    return code
+
+
+def _want(name, t, dtype, shape):
+    if t is None or str(t.dtype) != "torch." + dtype or t.shape != shape:
+        raise TypeError(f"{name} must be {dtype} {shape}")
+
+
+def _want_q4(name, w, E, K, N, group):
+    """A packed matrix (words, scales, zeros or None), stacked E times where E is not None."""
+    lead = () if E is None else (E,)
+    if group not in (32, 64, 128) or K % group:
+        raise TypeError(f"{name}: groups are 32, 64 or 128 rows and divide K")
+    for part, t, dtype, rows in ((" words", w[0], "int32", K // 8), (" scales", w[1], "bfloat16", K // group),
+                                 (" zeros", w[2], "uint8", K // group)):
+        if t is not None or part != " zeros":
+            _want(name + part, t, dtype, lead + (rows, N))
+            _dense(name + part, t)
+
+
+def _dense(name, t):
+    if not t.is_contiguous():
+        raise TypeError(f"{name} must be contiguous")
+
+
+def _rows(name, t, shape) -> int:
+    """Distance of a matrix's rows in elements; its rows must be contiguous."""
+    if t.shape != shape:
+        raise TypeError(f"{name} must have shape {shape}")
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise TypeError(f"{name} must have unit stride in its last dimension")
+    return t.stride(0) if shape[0] > 1 else -(-shape[1] // 16) * 16    # (one row: any distance will do)
 
 
 def default_config(device: int = 0) -> tovl_config:
@@ -255,6 +311,131 @@ class Handle:
             raise TypeError("gate weights must be float32")
         rc = load().tovl_combine(self.h, _ptr(y), N, _ptr(gate_w), _ptr(staging), _ptr(combined), _stream(stream))
         _check(self.h, rc, "tovl_combine")
+
+    # ------------------------------------------------------------ decode step
+    def add_rmsnorm(self, x, weight, eps, residual=None, residual_out=None, out=None, q=None, q_scale=None, group=128,
+                    stream=None):
+        """``r = x + residual``, ``y = r * rsqrt(mean(r^2) + eps) * weight``: ``residual_out`` = r, ``out`` = y in bf16,
+        ``q`` = y in e4m3 with ``q_scale`` [T, ceil(H/group)] (one scale per row with ``group=0``).  Tensors may be
+        slices with unit stride in the last dimension (``q`` and ``q_scale`` contiguous)."""
+        T, H = x.shape
+        _want("x", x, "bfloat16", (T, H))
+        _want("weight", weight, "bfloat16", (H,))
+        rt = ldr = 0
+        if residual is not None:
+            rt = _type_of("residual", residual, _RESIDUAL_TYPES)
+            ldr = _rows("residual", residual, (T, H))
+            if residual_out is None or residual_out.dtype != residual.dtype or _rows("residual_out", residual_out, (T, H)) != ldr:
+                raise TypeError("residual_out must have the type, shape and strides of residual")
+        ldo = 0
+        if out is not None:
+            _want("out", out, "bfloat16", (T, H))
+            ldo = _rows("out", out, (T, H))
+        if q is not None:
+            _want("q", q, "float8_e4m3fn", (T, H))
+            _want("q_scale", q_scale, "float32", (T, -(-H // group) if group else 1))
+            _dense("q", q), _dense("q_scale", q_scale)
+        rc = load().tovl_add_rmsnorm(self.h, _ptr(x), _rows("x", x, (T, H)), _ptr(residual),
+                                     None if residual is None else _ptr(residual_out), rt, ldr, _ptr(weight), eps, T, H,
+                                     _ptr(out), ldo, _ptr(q), _ptr(q_scale), group, _stream(stream))
+        _check(self.h, rc, "tovl_add_rmsnorm")
+
+    def route_topk(self, logits, topk, gate_w, renormalize=True, stream=None):
+        """The k experts of each token (``topk`` int32 [T, k], -1 where none is left) and their softmax weights."""
+        T, E = logits.shape
+        k = topk.shape[1]
+        _want("topk", topk, "int32", (T, k))
+        _want("gate_w", gate_w, "float32", (T, k))
+        _dense("topk", topk), _dense("gate_w", gate_w)
+        rc = load().tovl_route_topk(self.h, _ptr(logits), _type_of("logits", logits, _RESIDUAL_TYPES),
+                                    _rows("logits", logits, (T, E)), T, E, k, 1 if renormalize else 0, _ptr(topk),
+                                    _ptr(gate_w), _stream(stream))
+        _check(self.h, rc, "tovl_route_topk")
+
+    def moe_decode_workspace(self, T: int, k: int, H: int, I: int) -> int:
+        """Bytes of workspace of ``moe_decode`` and ``moe_decode_q4``."""
+        n = load().tovl_moe_decode_workspace(self.h, T, k, H, I)
+        if n < 0:
+            raise TovlError(TOVL_ERR_UNSUPPORTED, "tovl_moe_decode_workspace")
+        return n
+
+    def _moe_args(self, x, topk, gate_w, out):
+        T, H = x.shape
+        k = topk.shape[1]
+        _want("x", x, "bfloat16", (T, H))
+        _want("topk", topk, "int32", (T, k))
+        _want("gate_w", gate_w, "float32", (T, k))
+        _want("out", out, "bfloat16", (T, H))
+        _dense("topk", topk), _dense("gate_w", gate_w)
+        return T, H, k, _rows("x", x, (T, H)), _rows("out", out, (T, H))
+
+    def moe_decode(self, x, topk, gate_w, W13, W2, out, workspace, stream=None):
+        """The gated expert layer for up to 64 tokens: W13 [E, H, 2I] (gate columns, then up columns), W2 [E, I, H]."""
+        T, H, k, ldx, ldo = self._moe_args(x, topk, gate_w, out)
+        E, I = W2.shape[0], W2.shape[1]
+        _want("W13", W13, "bfloat16", (E, H, 2 * I))
+        _want("W2", W2, "bfloat16", (E, I, H))
+        _dense("W13", W13), _dense("W2", W2), _dense("workspace", workspace)
+        rc = load().tovl_moe_decode(self.h, _ptr(x), ldx, T, H, _ptr(topk), _ptr(gate_w), k, E, _ptr(W13), _ptr(W2), I,
+                                    _ptr(out), ldo, _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                    _stream(stream))
+        _check(self.h, rc, "tovl_moe_decode")
+
+    def moe_decode_q4(self, x, topk, gate_w, W13, W2, group, out, workspace, stream=None):
+        """``moe_decode`` with packed experts: W13 and W2 are (words, scales, zeros or None) as ``quantize_q4`` makes."""
+        T, H, k, ldx, ldo = self._moe_args(x, topk, gate_w, out)
+        q13, s13, z13 = W13
+        q2, s2, z2 = W2
+        E, I = q2.shape[0], q2.shape[1] * 8
+        _want_q4("W13", W13, E, H, 2 * I, group)
+        _want_q4("W2", W2, E, I, H, group)
+        _dense("workspace", workspace)
+        rc = load().tovl_moe_decode_q4(self.h, _ptr(x), ldx, T, H, _ptr(topk), _ptr(gate_w), k, E, _ptr(q13), _ptr(s13),
+                                       _ptr(z13), _ptr(q2), _ptr(s2), _ptr(z2), group, I, _ptr(out), ldo,
+                                       _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+        _check(self.h, rc, "tovl_moe_decode_q4")
+
+    def matvec_q4_workspace(self, T: int, N: int) -> int:
+        """Bytes of workspace of ``matvec_q4``."""
+        n = load().tovl_matvec_q4_workspace(self.h, T, N)
+        if n < 0:
+            raise TovlError(TOVL_ERR_UNSUPPORTED, "tovl_matvec_q4_workspace")
+        return n
+
+    def matvec_q4(self, x, wq, w_scale, group, out, workspace, zero=None, x_scale=None, stream=None):
+        """``out = x @ W`` for up to 64 rows and a packed matrix W [K, N]; x bf16, or e4m3 with ``x_scale``
+        [T, ceil(K/128)]."""
+        T, K = x.shape
+        N = wq.shape[1]
+        xt = _type_of("x", x, _ROW_TYPES)
+        if (xt == TOVL_E4M3) != (x_scale is not None):
+            raise TypeError("x_scale goes with e4m3 rows, and only with them")
+        if x_scale is not None:
+            _want("x_scale", x_scale, "float32", (T, -(-K // 128)))
+            _dense("x_scale", x_scale)
+        _want_q4("wq", (wq, w_scale, zero), None, K, N, group)
+        _want("out", out, "bfloat16", (T, N))
+        _dense("workspace", workspace)
+        rc = load().tovl_matvec_q4(self.h, _ptr(x), xt, _ptr(x_scale), _rows("x", x, (T, K)), T, K, _ptr(wq),
+                                   _ptr(w_scale), _ptr(zero), group, N, _ptr(out), _rows("out", out, (T, N)),
+                                   _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+        _check(self.h, rc, "tovl_matvec_q4")
+
+    def quantize_q4(self, W, group=128, zeros=False, stream=None):
+        """Packs bf16 W [E, K, N] or [K, N]: (words int32 [.., K/8, N], scales bf16 [.., K/group, N], zeros uint8 or
+        None)."""
+        import torch
+        _dense("W", W)
+        if W.dtype != torch.bfloat16 or W.dim() not in (2, 3):
+            raise TypeError("W must be a bfloat16 matrix or a stack of them")
+        lead, (K, N) = tuple(W.shape[:-2]), W.shape[-2:]
+        words = torch.empty(*lead, K // 8, N, dtype=torch.int32, device=W.device)
+        scale = torch.empty(*lead, K // group, N, dtype=torch.bfloat16, device=W.device)
+        zero = torch.empty(*lead, K // group, N, dtype=torch.uint8, device=W.device) if zeros else None
+        rc = load().tovl_quantize_q4(self.h, _ptr(W), lead[0] if lead else 1, K, N, group, _ptr(words), _ptr(scale),
+                                     _ptr(zero), _stream(stream))
+        _check(self.h, rc, "tovl_quantize_q4")
+        return words, scale, zero
 
     def gated_copy(self, src, dst, perm, gated=True, stamps=False, stream=None):
         n, rb = src.shape

@@ -235,6 +235,131 @@ int tovl_combine(tovl_handle h, const void* y, int N, const float* gate_w, void*
 int tovl_dispatch_plan_noalloc(const int* topk_idx, int T, int k, int E, int* expert_offsets, int* dst_rows,
                                void* stream);
 
+/* ---------------------------------------------------------------- decode step
+ * Operators of a serving step around the experts, for few tokens as well as
+ * many: the norm before the layer, the router, the whole expert layer for up
+ * to 64 tokens (longer batches take tovl_dispatch_grouped_gemm and
+ * tovl_combine), and products with 4-bit weights.  None of them is a protocol
+ * round: the sequence number stays.  T = 0 is accepted everywhere, does
+ * nothing and reads no tensor.
+ *
+ * Packed 4-bit weights of a matrix W [K][N] (N contiguous): 32-bit words
+ * [K/8][N]; the word of (r, n) holds rows 8r .. 8r+7 of column n, row 8r+2i in
+ * bits 4i .. 4i+3 and row 8r+2i+1 in bits 16+4i .. 16+4i+3.  A group is
+ * `group` rows (32, 64 or 128; K a multiple of it) of one column:
+ *   W[k][n] = (nibble - zero[k/group][n]) * scale[k/group][n],
+ * scale bf16 [K/group][N], zero uint8 [K/group][N] with values 0 .. 127, or a
+ * null pointer for zero = 8 throughout.  N is a multiple of 8, with zeros of
+ * 16; all pointers are 16-byte aligned.  Stacked matrices (one per expert)
+ * are contiguous. */
+
+/* Element types of the calls below. */
+typedef enum {
+    TOVL_BF16 = 0,
+    TOVL_F32 = 1,
+    TOVL_E4M3 = 2              /* 8-bit float, 4 exponent and 3 mantissa bits, largest value 448 */
+} tovl_type;
+
+/* Residual addition, root-mean-square norm and 8-bit output in one pass:
+ *   r = x + residual                        (fp32)
+ *   y = r * rsqrt(mean(r^2) + eps) * weight (fp32, mean over the row)
+ *   residual_out = r, out = y, each rounded once to its type;
+ *   per group of columns: scale = max(max |y|, 1e-12) / 448,
+ *   q = e4m3(y / scale), rounded to nearest even.
+ *   x           device, bf16 [T][H], rows ldx elements apart
+ *   residual    device, [T][H] of residual_type (TOVL_BF16 or TOVL_F32), rows
+ *               ldr elements apart; null = none (r = x; residual_out unused)
+ *   residual_out device, type and row distance of residual; may be residual
+ *   weight      device, bf16 [H]
+ *   out         device, bf16 [T][H], rows ldo apart (may be x); null = not wanted
+ *   q           device, e4m3 [T][H] contiguous; null = not wanted (then
+ *               q_scale and group are ignored).  One of out and q is given.
+ *   q_scale     device, fp32 [T][ceil(H/group)]
+ *   group       32, 64 or 128, or 0 for one scale per row; the last group of
+ *               a row may be shorter
+ * H is 1 .. 32768; pointers need the alignment of their element type only
+ * (rows of 16-byte multiples and alignment are fastest).  A NaN in a row
+ * shows in all of its outputs. */
+int tovl_add_rmsnorm(tovl_handle h, const void* x, long long ldx, const void* residual, void* residual_out,
+                     int residual_type, long long ldr, const void* weight, float eps, int T, int H, void* out,
+                     long long ldo, void* q, float* q_scale, int group, void* stream);
+
+/* Softmax routing: the k largest logits of each token, the lowest expert
+ * first among equal ones, and their softmax weights.
+ *   logits      device, bf16 or fp32 (type) [T][E], rows ld elements apart
+ *   E, k        E 1 .. 512, k 1 .. 32
+ *   renormalize 1: weights over the chosen experts (they sum to 1); 0: over all
+ *   topk_idx    device, int32 [T][k], in descending logits
+ *   gate_w      device, fp32 [T][k]
+ * An expert whose logit is -inf or NaN is masked: never chosen, weight 0.
+ * Slots that no expert is left for hold -1 with weight 0 (a token whose
+ * logits are all masked has nothing but those); +inf counts as the largest
+ * finite logit does. */
+int tovl_route_topk(tovl_handle h, const void* logits, int type, long long ld, int T, int E, int k, int renormalize,
+                    int* topk_idx, float* gate_w, void* stream);
+
+/* Bytes of workspace that tovl_moe_decode[_q4] needs for these sizes on the
+ * handle's device; -1 if the sizes are not supported. */
+long long tovl_moe_decode_workspace(tovl_handle h, int T, int k, int H, int I);
+
+/* The gated expert layer for a few tokens, in one kernel:
+ *   h(t, e) = silu(x[t] W13[e][:, 0:I]) * (x[t] W13[e][:, I:2I]),
+ *   out[t]  = sum over j of gate_w[t][j] * (h(t, e) W2[e]), e = topk_idx[t][j]
+ * with fp32 sums, rounded once to bf16.
+ *   x           device, bf16 [T][H], rows ldx elements apart (a multiple of 8),
+ *               16-byte aligned; T 0 .. 64, H a multiple of 8 up to 32768
+ *   topk_idx    device, int32 [T][k]: experts, or -1 for a slot without one
+ *               (masked, or an expert that lives elsewhere); k 1 .. 16.
+ *               Other ids outside [0, E) make the call a no-op that sets
+ *               TOVL_ERR_INVALID in the status word.
+ *   gate_w      device, fp32 [T][k]; weights of -1 slots are not read
+ *   E           1 .. 512
+ *   W13         device, bf16 [E][H][2I]: gate columns, then up columns
+ *   W2          device, bf16 [E][I][H]; I a multiple of 8 up to 32768
+ *   out         device, bf16 [T][H], rows ldo apart; a token without experts
+ *               gets zeros
+ *   workspace   device, 256-byte aligned, tovl_moe_decode_workspace bytes of
+ *               any content; free again when the call's kernel has ended
+ * The weights of experts that no token names are not read.  The grid meets at
+ * one barrier, so all its CTAs (one per SM) must be resident together: option
+ * 13 keeps the guarantee.  Results are the same bits on every call. */
+int tovl_moe_decode(tovl_handle h, const void* x, long long ldx, int T, int H, const int* topk_idx,
+                    const float* gate_w, int k, int E, const void* W13, const void* W2, int I, void* out,
+                    long long ldo, void* workspace, long long workspace_bytes, void* stream);
+
+/* The same layer with packed 4-bit experts: W13 [E] matrices [H][2I], W2 [E]
+ * matrices [I][H], with zeros for both or for neither; H and I multiples of
+ * group.  Scales are applied to fp32 sums. */
+int tovl_moe_decode_q4(tovl_handle h, const void* x, long long ldx, int T, int H, const int* topk_idx,
+                       const float* gate_w, int k, int E, const void* W13_q, const void* W13_scale,
+                       const void* W13_zero, const void* W2_q, const void* W2_scale, const void* W2_zero, int group,
+                       int I, void* out, long long ldo, void* workspace, long long workspace_bytes, void* stream);
+
+/* Bytes of workspace that tovl_matvec_q4 needs; -1 if not supported. */
+long long tovl_matvec_q4_workspace(tovl_handle h, int T, int N);
+
+/* Few rows times one packed 4-bit matrix: out[t] = x[t] W, fp32 sums, rounded
+ * once to bf16.
+ *   x           device, [T][K], rows ldx elements apart, 16-byte aligned rows:
+ *               bf16, or e4m3 (x_type) with x_scale; T 0 .. 64, K up to 32768
+ *   x_scale     device, fp32 [T][ceil(K/128)]: x[t][k] stands for
+ *               x * x_scale[t][k/128] (the q and q_scale of tovl_add_rmsnorm
+ *               with group 128); null for bf16
+ *   wq, w_scale, w_zero, group  the packed matrix [K][N], N up to 2^24
+ *   out         device, bf16 [T][N], rows ldo apart
+ *   workspace   device, 256-byte aligned, tovl_matvec_q4_workspace bytes of
+ *               any content */
+int tovl_matvec_q4(tovl_handle h, const void* x, int x_type, const float* x_scale, long long ldx, int T, int K,
+                   const void* wq, const void* w_scale, const void* w_zero, int group, int N, void* out,
+                   long long ldo, void* workspace, long long workspace_bytes, void* stream);
+
+/* Quantises bf16 matrices W [E][K][N] into the packed form, rounding to
+ * nearest: without zeros (w_zero null) scale = max |w| / 7, with zeros scale =
+ * (max(w, 0) - min(w, 0)) / 15 and zero = round(-min(w, 0) / scale), the scale
+ * rounded to bf16 first.  Finite weights only. */
+int tovl_quantize_q4(tovl_handle h, const void* W, int E, int K, int N, int group, void* wq, void* w_scale,
+                     void* w_zero, void* stream);
+
 /* ---------------------------------------------------------------- controls
  * The acceptance method of the platform page, section 5, compares the fused
  * kernel with its parts run alone on the same SM counts. */
