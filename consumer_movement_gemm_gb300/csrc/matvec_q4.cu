@@ -6,8 +6,9 @@
 // Products of bf16 (or e4m3, exact in bf16) activations with the integers
 // nibble - zero are exact, a group's sum is fp32, and the scales multiply it
 // in fp32: nothing is rounded before the result.  The stream of weight blocks
-// and the split are skinny.cuh's; rows beyond 32 go through the weights a
-// second time, right behind the first (they come from L2 then).
+// and the split are skinny.cuh's; every 16 rows are a pass over the weights
+// (one pass is the next one's matrix, so large matrices are read again).
+#include <type_traits>
 #include "launch.cuh"
 #include "skinny.cuh"
 
@@ -16,165 +17,110 @@ namespace tovl {
 namespace {
 
 using namespace skinny;
-constexpr int kCta = skinny::kThreads;
-constexpr int kPassRows = 32;
-constexpr int kPartFloats = kPassRows * kCols;
+constexpr int kPassRows = Shape<128>::kPassRows;
+constexpr int kThreads4 = Shape<128>::kThreads;
 
-constexpr int smem_size() { return base_smem(true) + 16; }
-
-template <bool XS>
-struct Worker {
-    const MatvecParams& p;
-    float* red;
-    Ring<true> ring;
-    int warp, lane;
-    uint64_t pol;
-    // blocks to fetch: position inside the (pass, k) blocks of tile f_tile
-    int f_left, f_i, f_tile;
-
-    __device__ __forceinline__ void fetch(int kb, int len)
-    {
-        if (f_left <= 0) return;
-        if (lane == 0) ring.issue(p.w, f_tile * kCols, (f_i % kb) * kRowsQ4, 0, p.group, p.has_zero, pol);
-        ring.filled();
-        --f_left;
-        f_i += kWarps;
-        while (f_i >= len) {
-            f_i -= len;
-            ++f_tile;
-        }
-    }
-
-    // The warp's share of blocks [.., i1) of a pass over rows r0 .. r0 + cnt.
-    template <int NT>
-    __device__ __forceinline__ void pass(int first, int i1, int r0, int cnt, int tile, float* part, int kb, int len)
-    {
-        const int g = lane >> 2, t = lane & 3;
-        float acc[4][NT][4];
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[mt][nt][i] = 0.f;
-        const int n_xs = (p.K + kXScaleGroup - 1) / kXScaleGroup;
-        for (int i = first; i < i1; i += kWarps) {
-            uint4 b[4][NT];
-            float2 sx[NT];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                // a row past the last one repeats the first; its column is never stored
-                const long long r = r0 + (nt * 8 + g < cnt ? nt * 8 + g : 0);
-#pragma unroll
-                for (int R = 0; R < 4; ++R) {
-                    const int k = i * kRowsQ4 + 32 * R + 8 * t;
-                    if (k >= p.K) {
-                        b[R][nt] = make_uint4(0, 0, 0, 0);
-                    } else if (XS) {
-                        const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.x) + r * p.ldx + k));
-                        const uint2 lo = e4m3x4_to_bf16(v.x), hi = e4m3x4_to_bf16(v.y);
-                        b[R][nt] = make_uint4(lo.x, lo.y, hi.x, hi.y);
-                    } else {
-                        b[R][nt] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.x) + r * p.ldx + k));
-                    }
-                }
-                if (XS) {   // accumulator columns 2t and 2t + 1
-                    const int c0 = nt * 8 + 2 * t;
-                    sx[nt].x = c0 < cnt ? __ldg(p.x_scale + static_cast<long long>(r0 + c0) * n_xs + i) : 0.f;
-                    sx[nt].y = c0 + 1 < cnt ? __ldg(p.x_scale + static_cast<long long>(r0 + c0 + 1) * n_xs + i) : 0.f;
-                }
-            }
-            ring.wait(p.ctrl, p.pipe_timeout_ns);
-            block_q4<NT, false, XS>(acc, b, b, sx, ring.stage(), ring.stage_meta(), p.group / 32, p.has_zero, lane);
-            ring.taken();
-            __syncwarp();      // every lane has read the stage before it is filled again
-            fetch(kb, len);
-        }
-        const int col = threadIdx.x & 63, q = threadIdx.x >> 6;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            if (nt * 8 >= cnt) break;
-            store_red<true, NT>(red, acc, nt, warp, lane);
-            __syncthreads();
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int r = q + 4 * u, row = nt * 8 + r;
-                float v = 0.f;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) v += red[(w * 8 + r) * kRedPitch + col];
-                if (row < cnt) {
-                    if (part) part[row * kCols + col] = v;
-                    else if (tile * kCols + col < p.N)
-                        static_cast<__nv_bfloat16*>(p.out)[(r0 + row) * p.ldo + tile * kCols + col] = __float2bfloat16(v);
-                }
-            }
-            __syncthreads();
-        }
-    }
+struct Tables {
+    Product pr;
+    Queue queue;
 };
 
-template <bool XS>
-__global__ void __launch_bounds__(kCta, 1) matvec_q4_kernel(const __grid_constant__ MatvecParams p)
+template <int G>
+constexpr int smem_size() { return 1024 + Shape<G>::kRing + static_cast<int>(sizeof(Tables)) + 16; }
+
+struct Calls {
+    const MatvecParams& p;
+    __device__ __forceinline__ const WeightMaps& maps(int) const { return p.w; }
+    __device__ __forceinline__ int expert(int, int) const { return 0; }
+};
+
+// A segment of a pass over rows r0 .. r0 + cnt.
+template <int NT, bool XS, int G, bool Z>
+__device__ __forceinline__ void run_segment(const MatvecParams& p, Engine<G, Z, Calls>& eng, int r0, int cnt, int tile, int i0,
+                                            int i1, int number)
 {
+    const int g = eng.lane >> 2, t = eng.lane & 3;
+    const int n_xs = (p.K + kXScaleGroup - 1) / kXScaleGroup;
+    long long row[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)      // a row past the last one repeats the first; its column is never stored
+        row[nt] = (r0 + (nt * 8 + g < cnt ? nt * 8 + g : 0)) * p.ldx;
+    float* part = p.part + (static_cast<long long>(number) * p.T + r0) * p.N;
+    eng.template segment<NT, false, XS>(i0, i1, part, p.N, cnt, tile * kTileCols, p.N, [&](Frags<NT, false, true>& b, int i) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int R = 0; R < 4; ++R) {
+                const int k = i * kRowsQ4 + 32 * R + 8 * t;
+                b.v[R][nt] = make_uint4(0, 0, 0, 0);      // (rows of W past the last one are zeros; so must these be)
+                if (k < p.K) {
+                    if (XS) {
+                        const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.x) + row[nt] + k));
+                        const uint2 lo = e4m3x4_to_bf16(v.x), hi = e4m3x4_to_bf16(v.y);
+                        b.v[R][nt] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                    } else {
+                        b.v[R][nt] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.x) + row[nt] + k));
+                    }
+                }
+            }
+            if (XS) {   // accumulator columns 2t and 2t + 1
+                const int c0 = nt * 8 + 2 * t;
+                const float* xs = p.x_scale + static_cast<long long>(r0 + c0) * n_xs + i;
+                b.sx[nt].x = c0 < cnt ? __ldg(xs) : 0.f;
+                b.sx[nt].y = c0 + 1 < cnt ? __ldg(xs + n_xs) : 0.f;
+            }
+        }
+    });
+}
+
+template <bool XS, int G, bool Z>
+__global__ void __launch_bounds__(Shape<G>::kThreads, 1) matvec_q4_kernel(const __grid_constant__ MatvecParams p)
+{
+    using P = Shape<G>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align1024(smem_raw);
-    float* red = reinterpret_cast<float*>(smem + ring_bytes(true) + meta_bytes(true));
-    int* flag = reinterpret_cast<int*>(smem + base_smem(true) - 1024);
-    Worker<XS> w{p, red};
-    w.warp = threadIdx.x >> 5;
-    w.lane = threadIdx.x & 31;
-    w.pol = ptx::l2_policy(0);
-    w.ring.init(smem, w.warp);
-    if (w.lane == 0) {
-        w.ring.init_barriers();
+    Tables& tb = *reinterpret_cast<Tables*>(smem + (P::kRing + 15) / 16 * 16);
+    const Calls calls{p};
+    Engine<G, Z, Calls> eng{calls, &tb.pr, &tb.queue, p.sync + kTicketWord, p.ctrl, p.pipe_timeout_ns, 1};
+    eng.warp = threadIdx.x >> 5;
+    eng.lane = threadIdx.x & 31;
+    eng.ring.init(smem, eng.warp);
+    if (eng.lane == 0) {
+        eng.ring.init_barriers();
         ptx::fence_mbar_init();
         ptx::prefetch_tmap(&p.w.w);
         ptx::prefetch_tmap(&p.w.scale);
     }
-    const int grid = gridDim.x, cta = blockIdx.x;
-    const int kb = (p.K + kRowsQ4 - 1) / kRowsQ4;
-    const int passes = (p.T + kPassRows - 1) / kPassRows;
-    const int len = passes * kb, tiles = (p.N + kCols - 1) / kCols;
-    const int total = tiles * len, per = blocks_per_cta(total, grid);
-    const int b0 = min(cta * per, total), e0 = min(b0 + per, total);
-    const int s0 = b0 + w.warp;
-    w.f_left = e0 > s0 ? (e0 - s0 + kWarps - 1) / kWarps : 0;
-    w.f_i = s0 % len;
-    w.f_tile = s0 / len;
-    __syncwarp();
+    const int grid = gridDim.x;
+    const int passes = (p.T + kPassRows - 1) / kPassRows;      // as matrices of the product
+    if (threadIdx.x == 0) tb.pr.init(passes, p.N, p.K, P::kRows, grid, p.most_parts);
+    for (int i = threadIdx.x; i < kMaxItems + 8; i += P::kThreads) tb.queue.item[i] = kNoItem;
+    __syncthreads();
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
-#pragma unroll 1
-    for (int s = 0; s < Ring<true>::S; ++s) w.fetch(kb, len);
-
-    for (int b = b0; b < e0;) {
-        // (tile, pass): kb blocks, split where the CTA's range ends
-        const int unit = b / kb, t0 = unit * kb, t1 = t0 + kb, end = min(t1, e0);
-        const int tile = unit / passes, r0 = (unit % passes) * kPassRows;
-        const int cnt = min(kPassRows, p.T - r0);
-        const bool whole = b == t0 && end == t1;
-        float* part = whole ? nullptr : p.part + (static_cast<long long>(cta) * 2 + (b == b0 ? 0 : 1)) * kPartFloats;
-        const int first = b - t0 + ((w.warp - (b - b0)) & (kWarps - 1));
-        if (cnt <= 8) w.template pass<1>(first, end - t0, r0, cnt, tile, part, kb, len);
-        else if (cnt <= 16) w.template pass<2>(first, end - t0, r0, cnt, tile, part, kb, len);
-        else w.template pass<4>(first, end - t0, r0, cnt, tile, part, kb, len);
-        if (!whole) {
-            const int c0 = t0 / per, c1 = (t1 - 1) / per;
-            if (last_arrival(p.sync + c0, c1 - c0 + 1, flag)) {
-                const int col = threadIdx.x & 63;
-                if (tile * kCols + col < p.N) {
-                    for (int r = threadIdx.x >> 6; r < cnt; r += kCta / kCols) {
-                        float v = 0.f;
-                        for (int k = c0; k <= c1; ++k)
-                            v += __ldcg(p.part + (static_cast<long long>(k) * 2 + (t0 <= k * per ? 0 : 1)) * kPartFloats +
-                                        r * kCols + col);
-                        static_cast<__nv_bfloat16*>(p.out)[(r0 + r) * p.ldo + tile * kCols + col] = __float2bfloat16(v);
-                    }
-                }
-            }
+    eng.start();
+    eng.walk(0, [&](int matrix, int tile, int i0, int i1, int number) {
+        const int r0 = matrix * kPassRows, cnt = min(kPassRows, p.T - r0);
+        if (cnt <= 8) run_segment<1, XS, G, Z>(p, eng, r0, cnt, tile, i0, i1, number);
+        else run_segment<2, XS, G, Z>(p, eng, r0, cnt, tile, i0, i1, number);
+    });
+    grid_barrier(p.sync + kBarrierWord, grid, p.ctrl, p.timeout_ns);
+    const int quads = p.N / 4;
+    for (int i = blockIdx.x * P::kThreads + threadIdx.x; i < p.T * quads; i += grid * P::kThreads) {
+        const int t = i / quads, n = (i - t * quads) * 4;
+        const int t0 = (t / kPassRows * tb.pr.tiles + n / kTileCols) * tb.pr.kb;
+        const float4 s = add_parts(p.part + static_cast<long long>(t) * p.N + n, tb.pr.parts(t0), static_cast<long long>(p.T) * p.N);
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + t * p.ldo + n;
+        if (p.out_vec) {
+            *reinterpret_cast<uint2*>(out) = make_uint2(ptx::pack_bf16x2(s.x, s.y), ptx::pack_bf16x2(s.z, s.w));
+        } else {
+            out[0] = __float2bfloat16(s.x), out[1] = __float2bfloat16(s.y);
+            out[2] = __float2bfloat16(s.z), out[3] = __float2bfloat16(s.w);
         }
-        b = end;
     }
+    // the last CTA past the barrier clears the counters for the next call
+    if (threadIdx.x == 0 && ptx::atom_add_relaxed_gpu(p.sync + kExitWord, 1) == grid - 1)
+        for (int i = 0; i < kSyncWords; i += kSyncStep) ptx::st_relaxed_gpu(p.sync + i, 0);
 }
 
 // One thread per column and group: the group's range gives scale and zero,
@@ -220,27 +166,40 @@ __global__ void __launch_bounds__(256) quantize_q4_kernel(const QuantParams p)
 
 }  // namespace
 
-cudaError_t prepare_matvec_q4()
+// Calls f with the kernel of an activation type, group and zeros.
+template <class F>
+static cudaError_t with_kernel(bool e4m3, int group, bool zero, F f)
 {
-    cudaError_t e = cudaFuncSetAttribute(matvec_q4_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_size());
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(matvec_q4_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_size());
-    return e;
+    const auto pick = [&](auto xs, auto g) {
+        constexpr int G = decltype(g)::value;
+        return zero ? f(matvec_q4_kernel<decltype(xs)::value, G, true>, smem_size<G>())
+                    : f(matvec_q4_kernel<decltype(xs)::value, G, false>, smem_size<G>());
+    };
+    const auto by_group = [&](auto xs) {
+        if (group == 32) return pick(xs, std::integral_constant<int, 32>());
+        if (group == 64) return pick(xs, std::integral_constant<int, 64>());
+        return pick(xs, std::integral_constant<int, 128>());
+    };
+    return e4m3 ? by_group(std::true_type()) : by_group(std::false_type());
 }
 
-cudaError_t launch_matvec_q4(const MatvecParams& p, bool e4m3, int grid, cudaStream_t stream, bool pdl)
+cudaError_t prepare_matvec_q4()
 {
-    cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(grid);
-    lc.blockDim = dim3(kCta);
-    lc.dynamicSmemBytes = smem_size();
-    lc.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    lc.attrs = attr;
-    lc.numAttrs = pdl ? 1 : 0;
-    return e4m3 ? cudaLaunchKernelEx(&lc, matvec_q4_kernel<true>, p) : cudaLaunchKernelEx(&lc, matvec_q4_kernel<false>, p);
+    for (int i = 0; i < 12; ++i) {
+        const cudaError_t e = with_kernel(i & 1, 32 << (i >> 2), (i >> 1) & 1, [](auto kernel, int smem) {
+            return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        });
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+cudaError_t launch_matvec_q4(const MatvecParams& p, bool e4m3, int group, bool zero, int grid, cudaStream_t stream,
+                             bool cooperative, bool pdl)
+{
+    return with_kernel(e4m3, group, zero, [&](auto kernel, int smem) {
+        return launch_grid(kernel, p, grid, kThreads4, smem, stream, cooperative, pdl);
+    });
 }
 
 cudaError_t launch_quantize_q4(const QuantParams& p, cudaStream_t stream)

@@ -13,13 +13,15 @@ constexpr int kMaxDecodeK = 16;        // experts per token of one moe_decode ca
 constexpr int kMaxTopk = 32;           // experts per token of one route_topk call
 constexpr int kXScaleGroup = 128;      // columns per scale of 8-bit activations
 
-// Counters of the split-tile kernels (handle-owned, zero between calls): one
-// arrival counter per first contributor of a split tile, for two phases, then
-// the count of finished tiles and the count of CTAs past the phase barrier.
-constexpr int kMaxGrid = 1024;
-constexpr int kReadyWord = 2 * kMaxGrid;
-constexpr int kExitWord = 2 * kMaxGrid + 32;
-constexpr int kSyncWords = 2 * kMaxGrid + 64;
+// Counters of the streamed products (handle-owned, zero between calls), each
+// in a 128-byte line of its own: tickets of up to two products, arrivals of up
+// to three grid barriers, CTAs past the last one.
+constexpr int kMaxGrid = 256;
+constexpr int kSyncStep = 32;
+constexpr int kTicketWord = 0;         // tickets of product i at word i * kTicketStep
+constexpr int kBarrierWord = 2 * kSyncStep;
+constexpr int kExitWord = 5 * kSyncStep;
+constexpr int kSyncWords = 6 * kSyncStep;
 
 enum : int { kTypeBf16 = 0, kTypeF32 = 1, kTypeE4m3 = 2 };
 
@@ -65,35 +67,59 @@ struct MoeParams {
     const float* gate_w;    // [T][k]
     void* out;              // bf16 [T][H], rows ldo apart
     long long ldo;
+    int out_vec;            // rows of out allow 8-byte stores
+    int most_parts;         // a tile is cut into most_parts + 1 parts at most
     void* h_hi;             // bf16 [T*k][I]: activations between the two products, and
     void* h_lo;             // what their rounding to bf16 left over
-    float* part1;           // [grid][2][64][128] partial gate/up tiles
-    float* part2;           // [grid][2][T][64] partial output tiles
+    float* part;            // [most_parts + 1][T*k][2I or H] parts of the products
     int T, k, E, H, I;
-    int group, has_zero;    // 4-bit weights only
     int* sync;              // kSyncWords counters
-    int ready_offset;       // fault injection: tiles that never come
+    int ready_offset;       // fault injection: CTAs that never come
     long long timeout_ns, pipe_timeout_ns;
     Ctrl ctrl;
 };
 cudaError_t prepare_moe_decode();
-cudaError_t launch_moe_decode(const MoeParams& p, bool q4, int grid, cudaStream_t stream, bool cooperative, bool pdl);
+// group: rows per scale of 4-bit weights, 0 for bf16
+cudaError_t launch_moe_decode(const MoeParams& p, int group, bool zero, int grid, cudaStream_t stream, bool cooperative,
+                              bool pdl);
 
 struct MatvecParams {
     WeightMaps w;
     const void* x;          // bf16 or e4m3 [T][K], rows ldx apart
     const float* x_scale;   // [T][ceil(K/128)] for e4m3
     void* out;              // bf16 [T][N], rows ldo apart
-    float* part;            // [grid][2][32][64] partial tiles
+    float* part;            // [most_parts + 1][T][N] parts of the product
     long long ldx, ldo;
     int T, K, N;
-    int group, has_zero;
+    int out_vec;
+    int most_parts;
     int* sync;
-    long long pipe_timeout_ns;
+    long long timeout_ns, pipe_timeout_ns;
     Ctrl ctrl;
 };
 cudaError_t prepare_matvec_q4();
-cudaError_t launch_matvec_q4(const MatvecParams& p, bool e4m3, int grid, cudaStream_t stream, bool pdl);
+cudaError_t launch_matvec_q4(const MatvecParams& p, bool e4m3, int group, bool zero, int grid, cudaStream_t stream,
+                             bool cooperative, bool pdl);
+
+// One persistent grid whose CTAs meet at barriers.
+template <class Kernel, class Params>
+cudaError_t launch_grid(Kernel kernel, const Params& p, int grid, int threads, int smem, cudaStream_t stream, bool cooperative,
+                        bool pdl)
+{
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(grid);
+    lc.blockDim = dim3(threads);
+    lc.dynamicSmemBytes = smem;
+    lc.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = cooperative ? 1 : 0;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = pdl ? 2 : 1;
+    return cudaLaunchKernelEx(&lc, kernel, p);
+}
 
 struct QuantParams {
     const void* w;          // bf16 [E][K][N]

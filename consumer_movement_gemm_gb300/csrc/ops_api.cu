@@ -28,13 +28,13 @@ int run(tovl_ctx* h, cudaStream_t s, const char* what, F launch)
     return TOVL_OK;
 }
 
-// A 3-D map [outer][rows][inner] of contiguous matrices; boxes of
-// box_inner x box_rows, out-of-range elements read as zero.
-int encode_3d(tovl_ctx* h, CUtensorMap* map, CUtensorMapDataType type, int elem, const void* base, uint64_t inner,
+// A map of stacked [rows][width] matrices; boxes of box_inner columns x
+// box_rows rows, out-of-range elements read as zero.
+int encode_3d(tovl_ctx* h, CUtensorMap* map, CUtensorMapDataType type, int elem, const void* base, uint64_t width,
               uint64_t rows, uint64_t outer, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swizzle)
 {
-    cuuint64_t dims[3] = {inner, rows, outer};
-    cuuint64_t strides[2] = {inner * elem, inner * elem * rows};
+    cuuint64_t dims[3] = {width, rows, outer};
+    cuuint64_t strides[2] = {width * elem, width * elem * rows};
     cuuint32_t box[3] = {box_inner, box_rows, 1};
     cuuint32_t estr[3] = {1, 1, 1};
     const CUresult r = h->encode(map, type, 3, const_cast<void*>(base), dims, strides, box, estr,
@@ -47,6 +47,7 @@ int encode_3d(tovl_ctx* h, CUtensorMap* map, CUtensorMapDataType type, int elem,
     return TOVL_OK;
 }
 
+// Blocks of one warp: 64 columns x 32 rows of bf16, 32 columns x 128 rows of 4 bits.
 int map_bf16(tovl_ctx* h, WeightMaps* m, const void* w, int E, int K, int N)
 {
     return encode_3d(h, &m->w, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, w, N, K, E, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B);
@@ -56,10 +57,10 @@ int map_q4(tovl_ctx* h, WeightMaps* m, const void* q, const void* scale, const v
 {
     int rc = encode_3d(h, &m->w, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, q, N, K / 8, E, 32, 16, CU_TENSOR_MAP_SWIZZLE_128B);
     if (rc == TOVL_OK)
-        rc = encode_3d(h, &m->scale, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, scale, N, K / group, E, 64, 128 / group,
+        rc = encode_3d(h, &m->scale, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, scale, N, K / group, E, 32, 128 / group,
                        CU_TENSOR_MAP_SWIZZLE_NONE);
     if (rc == TOVL_OK && zero)
-        rc = encode_3d(h, &m->zero, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, zero, N, K / group, E, 64, 128 / group,
+        rc = encode_3d(h, &m->zero, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, zero, N, K / group, E, 32, 128 / group,
                        CU_TENSOR_MAP_SWIZZLE_NONE);
     return rc;
 }
@@ -75,19 +76,21 @@ bool valid_q4(int K, int N, int group, const void* q, const void* scale, const v
     return K % group == 0 && N % (zero ? 16 : 8) == 0 && q && scale && aligned16(q) && aligned16(scale) && aligned16(zero);
 }
 
-constexpr long long kPart1Bytes = 2LL * kMaxDecodeRows * 128 * 4;   // per CTA: two partial gate | up tiles
-
 long long up256(long long v) { return (v + 255) & ~255LL; }
+
+// Limit of a tile's parts (less one) by the rows of a product: few rows can
+// afford a cut for every CTA, many have other tiles to share out.
+int most_parts(long long rows) { return rows <= 64 ? 16 : rows <= 256 ? 8 : 4; }
 
 // Pieces of a moe_decode workspace, in order.
 struct MoeSpace {
-    long long h, part1, part2, total;
-    MoeSpace(int sms, int T, int k, int I)
+    long long h, part, total;
+    MoeSpace(int T, int k, int H, int I)
     {
-        h = up256(2LL * T * k * I);
-        part1 = up256(sms * kPart1Bytes);
-        part2 = up256(sms * 2LL * T * 64 * 4);
-        total = 2 * h + part1 + part2;
+        const long long rows = static_cast<long long>(T) * k;
+        h = up256(2 * rows * I);
+        part = 4 * (most_parts(rows) + 1) * rows * (2 * I > H ? 2 * I : H);
+        total = 2 * h + up256(part);
     }
 };
 
@@ -178,18 +181,18 @@ TOVL_API int tovl_route_topk(tovl_handle h, const void* logits, int type, long l
 TOVL_API long long tovl_moe_decode_workspace(tovl_handle h, int T, int k, int H, int I)
 {
     if (!h || !valid_moe_shape(T, k, H, I) || !fits_moe(T, k, H, I)) return -1;
-    return MoeSpace(h->num_sms, T, k, I).total;
+    return MoeSpace(T, k, H, I).total;
 }
 
-// The part that both weight types share.  `q4`: 4-bit weights.
-static int run_moe(tovl_handle h, MoeParams& p, bool q4, const void* x, long long ldx, int T, int H, const int* topk_idx,
+// The part that both weight types share.  group: rows per scale, 0 for bf16.
+static int run_moe(tovl_handle h, MoeParams& p, int group, bool zero, const void* x, long long ldx, int T, int H, const int* topk_idx,
                    const float* gate_w, int k, int E, int I, void* out, long long ldo, void* workspace,
                    long long workspace_bytes, void* stream)
 {
     if (!x || !topk_idx || !gate_w || !out || !workspace || ldx < H || ldo < H || ldx % 8 || !aligned16(x) ||
         !aligned(out, 2) || !aligned(topk_idx, 4) || !aligned(gate_w, 4) || !aligned(workspace, 256))
         return TOVL_ERR_INVALID;
-    const MoeSpace space(h->num_sms, T, k, I);
+    const MoeSpace space(T, k, H, I);
     if (workspace_bytes < space.total) return TOVL_ERR_INVALID;
     char* ws = static_cast<char*>(workspace);
     p.x = x;
@@ -198,10 +201,11 @@ static int run_moe(tovl_handle h, MoeParams& p, bool q4, const void* x, long lon
     p.gate_w = gate_w;
     p.out = out;
     p.ldo = ldo;
+    p.out_vec = ldo % 4 == 0 && aligned(out, 8);
+    p.most_parts = most_parts(static_cast<long long>(T) * k);
     p.h_hi = ws;
     p.h_lo = ws + space.h;
-    p.part1 = reinterpret_cast<float*>(ws + 2 * space.h);
-    p.part2 = reinterpret_cast<float*>(ws + 2 * space.h + space.part1);
+    p.part = reinterpret_cast<float*>(ws + 2 * space.h);
     p.T = T;
     p.k = k;
     p.E = E;
@@ -214,7 +218,7 @@ static int run_moe(tovl_handle h, MoeParams& p, bool q4, const void* x, long lon
     p.ctrl = h->ctrl;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     return run(h, s, "expert layer launch",
-               [&](bool pdl) { return launch_moe_decode(p, q4, h->num_sms, s, h->coop_enabled, pdl); });
+               [&](bool pdl) { return launch_moe_decode(p, group, zero, h->num_sms, s, h->coop_enabled, pdl); });
 }
 
 TOVL_API int tovl_moe_decode(tovl_handle h, const void* x, long long ldx, int T, int H, const int* topk_idx,
@@ -231,7 +235,7 @@ TOVL_API int tovl_moe_decode(tovl_handle h, const void* x, long long ldx, int T,
     int rc = map_bf16(h, &p.w13, W13, E, H, 2 * I);
     if (rc == TOVL_OK) rc = map_bf16(h, &p.w2, W2, E, I, H);
     if (rc != TOVL_OK) return rc;
-    return run_moe(h, p, false, x, ldx, T, H, topk_idx, gate_w, k, E, I, out, ldo, workspace, workspace_bytes, stream);
+    return run_moe(h, p, 0, false, x, ldx, T, H, topk_idx, gate_w, k, E, I, out, ldo, workspace, workspace_bytes, stream);
 }
 
 TOVL_API int tovl_moe_decode_q4(tovl_handle h, const void* x, long long ldx, int T, int H, const int* topk_idx,
@@ -250,18 +254,17 @@ TOVL_API int tovl_moe_decode_q4(tovl_handle h, const void* x, long long ldx, int
     DeviceGuard g(h->device);
     MoeParams p;
     std::memset(&p, 0, sizeof p);
-    p.group = group;
-    p.has_zero = W13_zero != nullptr;
     int rc = map_q4(h, &p.w13, W13_q, W13_scale, W13_zero, E, H, 2 * I, group);
     if (rc == TOVL_OK) rc = map_q4(h, &p.w2, W2_q, W2_scale, W2_zero, E, I, H, group);
     if (rc != TOVL_OK) return rc;
-    return run_moe(h, p, true, x, ldx, T, H, topk_idx, gate_w, k, E, I, out, ldo, workspace, workspace_bytes, stream);
+    return run_moe(h, p, group, W13_zero != nullptr, x, ldx, T, H, topk_idx, gate_w, k, E, I, out, ldo, workspace,
+                   workspace_bytes, stream);
 }
 
 TOVL_API long long tovl_matvec_q4_workspace(tovl_handle h, int T, int N)
 {
     if (!h || T < 0 || N < 1 || T > kMaxDecodeRows) return -1;
-    return h->num_sms * 2LL * 32 * 64 * 4;
+    return up256(4LL * (most_parts(T) + 1) * T * N);
 }
 
 TOVL_API int tovl_matvec_q4(tovl_handle h, const void* x, int x_type, const float* x_scale, long long ldx, int T, int K,
@@ -288,19 +291,20 @@ TOVL_API int tovl_matvec_q4(tovl_handle h, const void* x, int x_type, const floa
     p.x_scale = x_scale;
     p.out = out;
     p.part = static_cast<float*>(workspace);
+    p.out_vec = ldo % 4 == 0 && aligned(out, 8);
+    p.most_parts = most_parts(T);
+    p.timeout_ns = h->timeout_ns;
     p.ldx = ldx;
     p.ldo = ldo;
     p.T = T;
     p.K = K;
     p.N = N;
-    p.group = group;
-    p.has_zero = w_zero != nullptr;
     p.sync = h->sync_words;
     p.pipe_timeout_ns = 4 * h->timeout_ns + 100000000LL;
     p.ctrl = h->ctrl;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     return run(h, s, "4-bit product launch",
-               [&](bool pdl) { return launch_matvec_q4(p, x_type == TOVL_E4M3, h->num_sms, s, pdl); });
+               [&](bool pdl) { return launch_matvec_q4(p, x_type == TOVL_E4M3, group, w_zero != nullptr, h->num_sms, s, h->coop_enabled, pdl); });
 }
 
 TOVL_API int tovl_quantize_q4(tovl_handle h, const void* W, int E, int K, int N, int group, void* wq, void* w_scale,

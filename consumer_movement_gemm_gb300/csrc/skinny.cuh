@@ -1,25 +1,37 @@
 // skinny.cuh -- products of a few rows with a streamed weight matrix: the
-// parts that the expert layer for few tokens and the 4-bit products share.
+// engine that the expert layer for few tokens and the 4-bit products share.
 //
 // out[r][n] = sum_k x[r][k] W[k][n] with at most 64 rows is bound by reading
 // W once, so W is laid in shared memory by TMA and everything else fits
-// around that stream.  A CTA owns a contiguous range of 4 KB weight blocks
-// (64 columns x 32 rows of bf16, or 64 columns x 128 rows of 4 bits) in the
-// order (tile of 64 columns, k); its 8 warps take the blocks in turn.  Every
-// warp has its own ring of stages, filled by its own lane 0, so no warp waits
-// for another one inside a tile, and the ring runs on across tiles (and
-// across the two products of an expert layer: weights depend on nothing).
-// The sum over a tile's blocks ends in a cross-warp reduction in shared
-// memory; tiles that the even split cuts are finished by the last CTA to
-// arrive, which adds the parts in the order of k (same bits every time).
+// around that stream.
+//
+// Units.  A unit is 512 columns x 32 rows of bf16 (or x 128 rows of 4 bits),
+// 32 KB.  Its columns are dealt to the CTA's warps (8 of 64 columns for bf16;
+// 16 of 32 for 4-bit weights, whose unpacking needs twice the warps to hide
+// its latencies), so neighbouring warps read neighbouring pieces of the same rows at
+// the same time: measured on GB300, a stream of such 1 KB wide rows reaches
+// 6.67 TB/s, the same boxes with the warps along k (each 128-byte piece
+// alone) 5.85.  A warp owns its columns, so nothing is summed across warps and
+// no warp waits for another one; each has its own ring of stages, filled by its
+// own lane 0, that runs on across tiles and across the two products of an
+// expert layer (weights depend on nothing).
+//
+// Items.  The units of a product, in the order (matrix, tile of 512 columns,
+// k), are cut into items of equal length.  With little work there is one item
+// per CTA; else eight, taken by ticket, because the SMs do not get the same
+// share of the memory (an even static deal of 2.3 GB ended between 160 and
+// 229 us).  An item writes the fp32 sums of each tile that it touches to the
+// workspace, under the number of its part of the tile; after a grid barrier all CTAs add
+// the parts in the order of k.  Which CTA took an item changes nothing: the
+// same bits every time.
 //
 // The matrix instruction is the warp-level m16n8k16 with the weights as the
 // 16-row operand: at most 8 rows cost one instruction per 16 columns x 16
 // rows of W, registers feed it directly (4-bit weights never go back to
-// shared memory), and even 64 rows need less of the tensor pipe than the
-// stream leaves time for.
+// shared memory), and the tensor pipe has time for 64 rows of bf16.
 #pragma once
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include "common.cuh"
 #include "ops.cuh"
 #include "sync.cuh"
@@ -27,29 +39,32 @@
 namespace tovl {
 namespace skinny {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kCols = 64;                         // columns of a tile
-constexpr int kBlockBytes = 4096;                 // weight bytes of a block
-constexpr int kRowsBf16 = 32;                     // rows of W in a block, bf16
-constexpr int kRowsQ4 = 128;                      // rows of W in a block, 4 bits
-constexpr int kStagesBf16 = 5;                    // 160 KB in flight per SM
-constexpr int kStagesQ4 = 4;                      // 128 KB + scales
-constexpr int kScaleBytes = 512;                  // scales of a block (group >= 32)
-constexpr int kZeroBytes = 256;
-constexpr int kMetaBytes = kScaleBytes + kZeroBytes;
-constexpr int kRedPitch = kCols + 4;              // 8 x 4 lanes of an accumulator store hit 32 banks
-constexpr int kRedFloats = kWarps * 8 * kRedPitch;
+constexpr int kTileCols = 512;
+constexpr int kRowsBf16 = 32;                     // rows of W in a unit
+constexpr int kRowsQ4 = 128;
+constexpr int kScaleBytes = 256;                  // scales of a 4-bit block (group >= 32)
+constexpr int kZeroBytes = 128;
+constexpr int kItemsPerCta = 8;                   // with tickets
+constexpr int kItemUnits = 12;                    // tickets are worth it from this many units an item
+constexpr int kMaxItems = kMaxGrid * kItemsPerCta;
 
-constexpr int stages(bool q4) { return q4 ? kStagesQ4 : kStagesBf16; }
-constexpr int block_rows(bool q4) { return q4 ? kRowsQ4 : kRowsBf16; }
-// ring (1 KB aligned), block scales, cross-warp reduction, barriers
-constexpr int ring_bytes(bool q4) { return kWarps * stages(q4) * kBlockBytes; }
-constexpr int meta_bytes(bool q4) { return q4 ? kWarps * stages(q4) * kMetaBytes : 0; }
-constexpr int base_smem(bool q4)
-{
-    return 1024 + ring_bytes(q4) + meta_bytes(q4) + kRedFloats * 4 + kWarps * stages(q4) * 8;
-}
+// G: rows per scale (0: bf16 weights).
+template <int G>
+struct Shape {
+    static constexpr bool Q4 = G != 0;
+    static constexpr int kWarps = Q4 ? 16 : 8;
+    static constexpr int kThreads = kWarps * 32;
+    static constexpr int kCols = kTileCols / kWarps;          // columns of a warp
+    static constexpr int kRows = Q4 ? kRowsQ4 : kRowsBf16;    // rows of W in a block
+    static constexpr int kBlockBytes = Q4 ? 2048 : 4096;
+    static constexpr int kMetaBytes = Q4 ? kScaleBytes + kZeroBytes : 0;
+    static constexpr int kStages = 5;                         // 160 KB in flight per SM
+    static constexpr int kMT = kCols / 16;                    // 16-column accumulator tiles
+    static constexpr int kRing = kWarps * kStages * (kBlockBytes + kMetaBytes + 8);   // 1 KB aligned
+    // rows that one pass over a matrix takes: 4-bit blocks keep the sums of a
+    // scale group beside the running ones
+    static constexpr int kPassRows = Q4 ? 16 : 64;
+};
 
 // ------------------------------------------------------------ instructions
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr)
@@ -84,6 +99,15 @@ __device__ __forceinline__ uint32_t ld_shared_u1(uint32_t addr)
     return v;
 }
 
+__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+        "[%2];" ::"r"(ptx::smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(ptx::smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
 // d += a x b: a 16 x 16 (rows: weight columns), b 16 x 8 (columns: tokens)
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1)
@@ -92,6 +116,16 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// d = a x b
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b)
@@ -120,11 +154,12 @@ __device__ __forceinline__ uint2 e4m3x4_to_bf16(uint32_t v)
 }
 
 // ------------------------------------------------------------ the warp's ring
-// Stage s of a warp: 4 KB of weights (1 KB aligned, 128-byte swizzle), for
-// 4-bit weights also the block's scales and zeros, and one mbarrier.
-template <bool Q4>
+// Stage s of a warp: a block of weights (128-byte swizzle), for 4-bit weights
+// also its [group][32] scales and zeros, and one mbarrier.  Z: with zeros.
+template <int G, bool Z>
 struct Ring {
-    static constexpr int S = stages(Q4);
+    using P = Shape<G>;
+    static constexpr int S = P::kStages;
     uint8_t* w;          // this warp's stages
     uint8_t* meta;
     uint64_t* full;
@@ -134,9 +169,9 @@ struct Ring {
 
     __device__ void init(uint8_t* smem, int warp)
     {
-        w = smem + warp * S * kBlockBytes;
-        meta = smem + ring_bytes(Q4) + warp * S * kMetaBytes;
-        full = reinterpret_cast<uint64_t*>(smem + ring_bytes(Q4) + meta_bytes(Q4) + kRedFloats * 4) + warp * S;
+        w = smem + warp * S * P::kBlockBytes;
+        meta = smem + P::kWarps * S * P::kBlockBytes + warp * S * P::kMetaBytes;
+        full = reinterpret_cast<uint64_t*>(smem + P::kWarps * S * (P::kBlockBytes + P::kMetaBytes)) + warp * S;
     }
 
     __device__ void init_barriers()
@@ -144,32 +179,32 @@ struct Ring {
         for (int s = 0; s < S; ++s) ptx::mbar_init(full + s, 1);
     }
 
-    // One lane: fetch block (column n, weight row k, expert e).  `group`:
-    // rows of W per scale (4-bit weights).
-    __device__ void issue(const WeightMaps& m, int n, int k, int e, int group, bool has_zero, uint64_t pol)
+    // One lane: fetch the block at column n, weight row k of matrix e.
+    __device__ __forceinline__ void issue(const WeightMaps& m, int n, int k, int e)
     {
-        uint8_t* dst = w + fill * kBlockBytes;
+        uint8_t* dst = w + fill * P::kBlockBytes;
         uint64_t* bar = full + fill;
-        if constexpr (Q4) {
-            const int groups = kRowsQ4 / group;
-            const uint32_t sb = groups * kCols * 2, zb = has_zero ? groups * kCols : 0;
-            ptx::mbar_arrive_expect_tx(bar, kBlockBytes + sb + zb);
-            ptx::tma_load_3d_hint(dst, &m.w, bar, n, k / 8, e, pol);
-            ptx::tma_load_3d_hint(dst + kBlockBytes / 2, &m.w, bar, n + kCols / 2, k / 8, e, pol);
-            uint8_t* md = meta + fill * kMetaBytes;
-            ptx::tma_load_3d_hint(md, &m.scale, bar, n, k / group, e, pol);
-            if (has_zero) ptx::tma_load_3d_hint(md + kScaleBytes, &m.zero, bar, n, k / group, e, pol);
+        if constexpr (P::Q4) {
+            constexpr int kGroups = kRowsQ4 / G;
+            uint8_t* md = meta + fill * P::kMetaBytes;
+            ptx::mbar_arrive_expect_tx(bar, P::kBlockBytes + kGroups * P::kCols * (Z ? 3 : 2));
+            tma_load_3d(dst, &m.w, bar, n, k / 8, e);
+            tma_load_3d(md, &m.scale, bar, n, k / G, e);
+            if (Z) tma_load_3d(md + kScaleBytes, &m.zero, bar, n, k / G, e);
         } else {
-            ptx::mbar_arrive_expect_tx(bar, kBlockBytes);
-            ptx::tma_load_3d_hint(dst, &m.w, bar, n, k, e, pol);
+            ptx::mbar_arrive_expect_tx(bar, P::kBlockBytes);
+            tma_load_3d(dst, &m.w, bar, n, k, e);
         }
     }
-    __device__ void filled() { fill = fill + 1 == S ? 0 : fill + 1; }
+    __device__ __forceinline__ void filled() { fill = fill + 1 == S ? 0 : fill + 1; }
 
-    __device__ void wait(const Ctrl& ctrl, long long timeout_ns) { mbar_wait(full + take, parity, ctrl, timeout_ns); }
-    __device__ uint32_t stage() const { return ptx::smem_u32(w + take * kBlockBytes); }
-    __device__ uint32_t stage_meta() const { return ptx::smem_u32(meta + take * kMetaBytes); }
-    __device__ void taken()
+    __device__ __forceinline__ void wait(const Ctrl& ctrl, long long timeout_ns)
+    {
+        mbar_wait(full + take, parity, ctrl, timeout_ns);
+    }
+    __device__ __forceinline__ uint32_t block() const { return ptx::smem_u32(w + take * P::kBlockBytes); }
+    __device__ __forceinline__ uint32_t scales() const { return ptx::smem_u32(meta + take * P::kMetaBytes); }
+    __device__ __forceinline__ void taken()
     {
         if (++take == S) {
             take = 0;
@@ -184,11 +219,11 @@ struct Ring {
 // the same, so a lane loads 16 bytes (8 consecutive k, an octet) of its token
 // and both k16 steps of 32 rows of W come from them.
 //
-// bf16 weights: ldmatrix reads 8 rows of W per matrix, and the 128-byte
-// swizzle keeps them apart in the banks only if their indexes differ modulo
-// 8.  Lane t therefore uses pair (t ^ i) of its octet in quarter-step i
-// (rows 8t + 2(t^i) + {0,1}: all different modulo 8), which needs this swap of
-// the loaded pairs.
+// bf16 weights: ldmatrix reads 8 rows of W per matrix, and the swizzle keeps
+// them apart in the banks only if their indexes differ modulo 8.  Lane t
+// therefore uses pair (t ^ i) of its octet in quarter-step i (rows 8t +
+// 2(t^i) + {0,1}: all different modulo 8), which needs this swap of the
+// loaded pairs.
 __device__ __forceinline__ uint4 rotate_pairs(uint4 v, int t)
 {
     if (t & 1) v = make_uint4(v.y, v.x, v.w, v.z);
@@ -196,17 +231,17 @@ __device__ __forceinline__ uint4 rotate_pairs(uint4 v, int t)
     return v;
 }
 
-// acc[mt][nt]: 16 columns x 8 rows.  One block of 32 x 64 bf16 weights.
+// acc[mt][nt] (16 columns x 8 rows each) += a block of 32 x 64 bf16 weights.
 template <int NT, bool LO>
 __device__ __forceinline__ void block_bf16(float (&acc)[4][NT][4], const uint4 (&b)[NT], const uint4 (&bl)[NT],
-                                           uint32_t stage, int lane)
+                                           uint32_t block, int lane)
 {
     const int m = lane >> 3, r = lane & 7;
     const int tp = r >> 1;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         const int low = 2 * (tp ^ (2 * s + (m >> 1))) + (r & 1);   // row of W modulo 8
-        const uint32_t row = stage + (8 * tp + low) * 128;
+        const uint32_t row = block + (8 * tp + low) * 128;
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
             uint32_t a[4];
@@ -220,17 +255,6 @@ __device__ __forceinline__ void block_bf16(float (&acc)[4][NT][4], const uint4 (
     }
 }
 
-// Column of accumulator row g (and g + 8) of m-tile mt.
-template <bool Q4>
-__device__ __forceinline__ int acc_col(int mt, int g, int upper)
-{
-    // 4-bit: lane group g owns four neighbouring columns of each half tile;
-    // the order 0 4 1 5 2 6 3 7 of the groups keeps the 16-byte reads of a
-    // quarter warp in different banks
-    if (Q4) return (mt >> 1) * 32 + 4 * ((g >> 1) | ((g & 1) << 2)) + 2 * (mt & 1) + upper;
-    return mt * 16 + g + 8 * upper;
-}
-
 // The four bf16 pairs (nibble - zero) of a packed word, rows in order.
 // 0x4300 | nibble is the bf16 number 128 + nibble, and 128 + zero is one too,
 // so the difference is exact; the scale is applied to the fp32 sum of the
@@ -241,119 +265,346 @@ __device__ __forceinline__ void unpack(uint32_t (&p)[4], uint32_t word, uint32_t
     for (int i = 0; i < 4; ++i) p[i] = sub_bf16x2(((word >> (4 * i)) & 0x000f000fu) | 0x43004300u, zero2);
 }
 
-// One block of 128 x 64 4-bit weights.  b[R][nt]: octet t of rows 32R .. 32R+31
-// of token g.  sx: the tokens' activation scales (1 for bf16 activations).
-template <int NT, bool LO, bool XS>
-__device__ __forceinline__ void block_q4(float (&acc)[4][NT][4], const uint4 (&b)[4][NT], const uint4 (&bl)[4][NT],
-                                         const float2 (&sx)[NT], uint32_t stage, uint32_t meta, int gsteps, bool has_zero,
-                                         int lane)
+// acc[mt][nt] += a block of 128 x 32 4-bit weights in groups of G rows, with
+// zeros (Z) or 8 for all.  b[R][nt]: octet t of rows 32R .. 32R+31 of token g.
+// sx: the tokens' activation scales (XS).  Lane group g owns four neighbouring
+// columns; the order 0 4 1 5 2 6 3 7 of the groups keeps the 16-byte reads of
+// a quarter warp in different banks.
+template <int NT, bool LO, bool XS, int G, bool Z>
+__device__ __forceinline__ void block_q4(float (&acc)[2][NT][4], const uint4 (&b)[4][NT], const uint4 (*bl)[NT],
+                                         const float2 (&sx)[NT], uint32_t block, uint32_t scales, int lane)
 {
+    constexpr int kSteps = G / 32;
     const int g = lane >> 2, t = lane & 3;
     const int c = (g >> 1) | ((g & 1) << 2);
-    float part[4][NT][4];
-    uint32_t z[2][4];
-    int gi = 0;
+    float part[2][NT][4];
+    uint32_t z[4];
 #pragma unroll
     for (int R = 0; R < 4; ++R) {
-        if ((R & (gsteps - 1)) == 0) {
-            gi = R / gsteps;
+        const bool first = R % kSteps == 0, last = R % kSteps == kSteps - 1;
+        if (first) {
+            const uint32_t zz = Z ? ld_shared_u1(scales + kScaleBytes + (R / kSteps) * 32 + 4 * c) : 0u;
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt)
+            for (int i = 0; i < 4; ++i) z[i] = Z ? 0x43004300u + ((zz >> (8 * i)) & 0x7fu) * 0x00010001u : 0x43084308u;
+        }
+        const int row = 4 * R + t;
+        const uint4 v = ld_shared_u4(block + row * 128 + ((c ^ (row & 7)) << 4));
+        uint32_t p0[4], p1[4], p2[4], p3[4];
+        unpack(p0, v.x, z[0]);
+        unpack(p1, v.y, z[1]);
+        unpack(p2, v.z, z[2]);
+        unpack(p3, v.w, z[3]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const uint4 x = b[R][nt];
+            if (first) {
+                mma_first(part[0][nt], p0[0], p1[0], p0[1], p1[1], x.x, x.y);
+                mma_first(part[1][nt], p2[0], p3[0], p2[1], p3[1], x.x, x.y);
+            } else {
+                mma(part[0][nt], p0[0], p1[0], p0[1], p1[1], x.x, x.y);
+                mma(part[1][nt], p2[0], p3[0], p2[1], p3[1], x.x, x.y);
+            }
+            mma(part[0][nt], p0[2], p1[2], p0[3], p1[3], x.z, x.w);
+            mma(part[1][nt], p2[2], p3[2], p2[3], p3[3], x.z, x.w);
+            if (LO) {
+                const uint4 y = bl[R][nt];
+                mma(part[0][nt], p0[0], p1[0], p0[1], p1[1], y.x, y.y);
+                mma(part[1][nt], p2[0], p3[0], p2[1], p3[1], y.x, y.y);
+                mma(part[0][nt], p0[2], p1[2], p0[3], p1[3], y.z, y.w);
+                mma(part[1][nt], p2[2], p3[2], p2[3], p3[3], y.z, y.w);
+            }
+        }
+        if (last) {
+            const uint2 s2 = ld_shared_u2(scales + (R / kSteps) * 64 + 8 * c);
+            const float s[4] = {bf16_lo(s2.x), bf16_hi(s2.x), bf16_lo(s2.y), bf16_hi(s2.y)};
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) part[mt][nt][i] = 0.f;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t zz = has_zero ? ld_shared_u1(meta + kScaleBytes + gi * kCols + h * 32 + 4 * c) : 0x08080808u;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) z[h][i] = 0x43004300u + ((zz >> (8 * i)) & 0x7fu) * 0x00010001u;
-            }
-        }
-        const int row = 4 * R + t;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint4 v = ld_shared_u4(stage + h * (kBlockBytes / 2) + row * 128 + ((c ^ (row & 7)) << 4));
-            uint32_t p0[4], p1[4], p2[4], p3[4];
-            unpack(p0, v.x, z[h][0]);
-            unpack(p1, v.y, z[h][1]);
-            unpack(p2, v.z, z[h][2]);
-            unpack(p3, v.w, z[h][3]);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const uint4 x = b[R][nt];
-                mma(part[2 * h][nt], p0[0], p1[0], p0[1], p1[1], x.x, x.y);
-                mma(part[2 * h + 1][nt], p2[0], p3[0], p2[1], p3[1], x.x, x.y);
-                mma(part[2 * h][nt], p0[2], p1[2], p0[3], p1[3], x.z, x.w);
-                mma(part[2 * h + 1][nt], p2[2], p3[2], p2[3], p3[3], x.z, x.w);
-                if (LO) {
-                    const uint4 y = bl[R][nt];
-                    mma(part[2 * h][nt], p0[0], p1[0], p0[1], p1[1], y.x, y.y);
-                    mma(part[2 * h + 1][nt], p2[0], p3[0], p2[1], p3[1], y.x, y.y);
-                    mma(part[2 * h][nt], p0[2], p1[2], p0[3], p1[3], y.z, y.w);
-                    mma(part[2 * h + 1][nt], p2[2], p3[2], p2[3], p3[3], y.z, y.w);
-                }
-            }
-        }
-        if ((R & (gsteps - 1)) == gsteps - 1) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint2 s2 = ld_shared_u2(meta + gi * (kCols * 2) + (h * 32 + 4 * c) * 2);
-                const float s[4] = {bf16_lo(s2.x), bf16_hi(s2.x), bf16_lo(s2.y), bf16_hi(s2.y)};
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float f = s[2 * u + (i >> 1)];
-                            if (XS) f *= (i & 1) ? sx[nt].y : sx[nt].x;
-                            acc[2 * h + u][nt][i] = fmaf(f, part[2 * h + u][nt][i], acc[2 * h + u][nt][i]);
-                        }
-            }
+                    for (int i = 0; i < 4; ++i) {
+                        float f = s[2 * mt + (i >> 1)];
+                        if (XS) f *= (i & 1) ? sx[nt].y : sx[nt].x;
+                        acc[mt][nt][i] = fmaf(f, part[mt][nt][i], acc[mt][nt][i]);
+                    }
         }
     }
 }
 
-// ------------------------------------------------------------ cross-warp sums
-// Writes n-tile nt of the warp's accumulators to red[warp][row][column].
-template <bool Q4, int NT>
-__device__ __forceinline__ void store_red(float* red, const float (&acc)[4][NT][4], int nt, int warp, int lane)
+// ------------------------------------------------------------ items
+// One product: matrices x tiles of 512 columns x kb units along k.
+struct Product {
+    int tiles, kb, total;      // tiles per matrix, units per tile, units
+    int per, items;            // units per item, items
+    bool tickets;
+
+    // most_parts: limit of kb / per, so that a tile has at most most_parts + 1 parts
+    __device__ __forceinline__ void init(int matrices, int N, int K, int rows, int grid, int most_parts)
+    {
+        tiles = (N + kTileCols - 1) / kTileCols;
+        kb = (K + rows - 1) / rows;
+        total = matrices * tiles * kb;
+        per = (total + grid - 1) / grid;
+        tickets = per >= 2 * kItemUnits;
+        if (tickets) per = max((per + kItemsPerCta - 1) / kItemsPerCta, kItemUnits);
+        per = max(max(per, (kb + most_parts - 1) / most_parts), 1);
+        items = (total + per - 1) / per;
+    }
+    // parts of the tile whose units start at t0
+    __device__ __forceinline__ int first_item(int t0) const { return t0 / per; }
+    __device__ __forceinline__ int parts(int t0) const { return (t0 + kb - 1) / per - t0 / per + 1; }
+};
+
+// The items that a CTA works on, in order; shared by its warps.  Entry 0 is
+// the CTA's own number; warp 0 takes the others by ticket, two ahead of
+// where it fetches, and the other warps read them here.  Long enough for one
+// CTA to take them all, so that no entry is ever written twice.
+struct Queue {
+    volatile uint16_t item[kMaxItems + 8];
+};
+constexpr int kNoItem = 0xffff;
+
+// Item n of this CTA; product.items or more when there is none.
+__device__ __forceinline__ int item_at(const Product& pr, const Queue& q, int n, const Ctrl& ctrl, long long timeout_ns)
 {
-    const int g = lane >> 2, t = lane & 3;
-    float* r = red + (warp * 8 + 2 * t) * kRedPitch;
-#pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r[(i & 1) * kRedPitch + acc_col<Q4>(mt, g, i >> 1)] = acc[mt][nt][i];
+    if (n == 0) return blockIdx.x;
+    if (!pr.tickets) return pr.items;
+    int v = q.item[n];
+    if (v == kNoItem) {
+        const uint64_t start = ptx::globaltimer();
+        for (int spin = 1; (v = q.item[n]) == kNoItem; ++spin) {
+            if ((spin & 255) == 0 && ptx::globaltimer() - start > static_cast<uint64_t>(timeout_ns)) {
+                record_error(ctrl, kErrTimeout);
+                return pr.items;
+            }
+        }
+    }
+    return v;
 }
 
-// Whole CTA: counts this CTA's arrival on a tile that n CTAs share; true (for
-// every thread) in the last one, whose reads of the others' parts are then
-// ordered after their writes.  The last arrival leaves the counter at zero.
-__device__ __forceinline__ bool last_arrival(int* counter, int n, int* flag)
+// A warp's place among the blocks that it fetches.
+struct Cursor {
+    int n, left;               // item of the CTA's list, units of it still to fetch
+    int i, tile, matrix;       // k unit, tile, matrix of the next one
+};
+
+// Whole CTA: waits until all CTAs of the grid have arrived `round` times on
+// the counter; what any of them wrote before is visible after.  Bounded; the
+// counter is cleared by the last CTA of the launch to leave.
+__device__ __forceinline__ void grid_barrier(int* counter, int target, const Ctrl& ctrl, long long timeout_ns)
 {
     __syncthreads();
     if (threadIdx.x == 0) {
         __threadfence();
-        const bool last = ptx::atom_add_acq_rel_gpu(counter, 1) == n - 1;
-        if (last) ptx::st_relaxed_gpu(counter, 0);
-        *flag = last;
+        ptx::red_add_release_gpu(counter, 1);
+        if (ptx::ld_acquire_gpu(counter) < target) {
+            const uint64_t start = ptx::globaltimer();
+            for (int spin = 1; ptx::ld_acquire_gpu(counter) < target; ++spin) {
+                if ((spin & 63) == 0 && ptx::globaltimer() - start > static_cast<uint64_t>(timeout_ns)) {
+                    record_error(ctrl, kErrTimeout);
+                    break;
+                }
+            }
+        }
         __threadfence();
     }
     __syncthreads();
-    return *flag != 0;
 }
 
-// The even split of `total` blocks: CTA c owns [c * per, (c + 1) * per).
-// At least one block per warp, so that a small product is not cut finer than
-// its CTAs can use.
-__device__ __forceinline__ int blocks_per_cta(int total, int grid)
+// Fragment sets of the rows of one block: one octet per row for bf16, four
+// for 4-bit weights; LO: also of the second parts.
+template <int NT, bool LO, bool Q4>
+struct Frags {
+    static constexpr int R = Q4 ? 4 : 1;
+    uint4 v[R][NT], l[LO ? R : 1][NT];
+    float2 sx[NT];
+};
+
+// Adds `n` parts, `stride` floats apart, of four neighbouring columns.
+__device__ __forceinline__ float4 add_parts(const float* part, int n, long long stride)
 {
-    int per = (total + grid - 1) / grid;
-    if (per < kWarps) per = kWarps;
-    return (per + 1) & ~1;     // even: gate and up blocks stay with the same warps
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(part + i * stride));
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    return s;
 }
+
+// The engine of one warp.  `Calls` provides, for product `ph` (0 or 1):
+//   maps(ph), expert(ph, matrix)     where a matrix' weights are
+//   rows(ph, matrix)                 rows of the product with it, 1 .. kPassRows
+template <int G, bool Z, class Calls>
+struct Engine {
+    using P = Shape<G>;
+    static constexpr bool Q4 = P::Q4;
+    const Calls& c;
+    const Product* pr;         // the call's products, in shared memory
+    Queue* queue;
+    int* tickets;              // global counters, one per product
+    const Ctrl& ctrl;
+    long long timeout_ns;
+    int n_products;
+    int warp, lane;
+    Ring<G, Z> ring;
+    Cursor f;
+    int ph = 0;                // product that is being fetched
+
+    __device__ __forceinline__ void open(int n)
+    {
+        const Product& q = pr[ph];
+        f.n = n;
+        f.left = 0;
+        const int id = item_at(q, queue[ph], n, ctrl, timeout_ns);
+        if (id >= q.items) return;
+        if (q.tickets && warp == 0 && lane == 0) {
+            if (n == 0) queue[ph].item[1] = static_cast<uint16_t>(min(atomicAdd(tickets + ph * kSyncStep, 1) + static_cast<int>(gridDim.x), q.items));
+            queue[ph].item[n + 2] = static_cast<uint16_t>(min(atomicAdd(tickets + ph * kSyncStep, 1) + static_cast<int>(gridDim.x), q.items));
+        }
+        const int b = id * q.per;
+        f.left = min(q.per, q.total - b);
+        const int tile = b / q.kb;
+        f.i = b - tile * q.kb;
+        f.matrix = tile / q.tiles;
+        f.tile = tile - f.matrix * q.tiles;
+    }
+
+    // Fetches the warp's next block, if there is one.
+    __device__ __forceinline__ void fetch()
+    {
+        while (f.left == 0) {
+            // next item, or the next product's first
+            if (ph >= n_products) return;
+            const Product& q = pr[ph];
+            if (f.n >= 0 && item_at(q, queue[ph], f.n, ctrl, timeout_ns) >= q.items) {
+                if (++ph >= n_products) return;
+                open(0);
+            } else {
+                open(f.n + 1);
+            }
+        }
+        if (lane == 0)
+            ring.issue(c.maps(ph), f.tile * kTileCols + warp * P::kCols, f.i * P::kRows, c.expert(ph, f.matrix));
+        ring.filled();
+        --f.left;
+        if (++f.i == pr[ph].kb) {
+            f.i = 0;
+            if (++f.tile == pr[ph].tiles) {
+                f.tile = 0;
+                ++f.matrix;
+            }
+        }
+    }
+
+    __device__ __forceinline__ void start()
+    {
+        open(0);
+#pragma unroll 1
+        for (int s = 0; s < P::kStages; ++s) fetch();
+    }
+
+    // acc += the ring's next block times the rows; the stage is refilled.
+    template <int NT, bool LO, bool XS>
+    __device__ __forceinline__ void multiply(float (&acc)[P::kMT][NT][4], const Frags<NT, LO, Q4>& b)
+    {
+        ring.wait(ctrl, timeout_ns);
+        if constexpr (Q4) {
+            block_q4<NT, LO, XS, G, Z>(acc, b.v, b.l, b.sx, ring.block(), ring.scales(), lane);
+        } else {
+            uint4 v[NT], l[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                v[nt] = rotate_pairs(b.v[0][nt], lane & 3);
+                if (LO) l[nt] = rotate_pairs(b.l[0][nt], lane & 3);
+            }
+            block_bf16<NT, LO>(acc, v, l, ring.block(), lane);
+        }
+        ring.taken();
+        __syncwarp();      // every lane has read the stage before it is filled again
+        fetch();
+    }
+
+    // Sums over k units [i0, i1) of a tile, written to part[row][n], rows
+    // `ld` floats apart (n0: the tile's first column, N: the matrix').
+    // load(b, i) fills b with the rows' fragments of unit i.  The next unit's
+    // are loaded before this one is multiplied where two sets fit the
+    // registers: their latency is longer than a block's work.
+    template <int NT, bool LO, bool XS, class F>
+    __device__ __forceinline__ void segment(int i0, int i1, float* part, long long ld, int rows, int n0, int N, F load)
+    {
+        using B = Frags<NT, LO, Q4>;
+        constexpr bool kTwo = Q4 ? NT == 1 : NT <= 4;
+        float acc[P::kMT][NT][4];
+#pragma unroll
+        for (int mt = 0; mt < P::kMT; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[mt][nt][j] = 0.f;
+        if constexpr (kTwo) {
+            B b[2];
+            load(b[0], i0);
+            for (int i = i0; i < i1; i += 2) {
+                if (i + 1 < i1) load(b[1], i + 1);
+                multiply<NT, LO, XS>(acc, b[0]);
+                if (i + 1 >= i1) break;
+                if (i + 2 < i1) load(b[0], i + 2);
+                multiply<NT, LO, XS>(acc, b[1]);
+            }
+        } else {
+            for (int i = i0; i < i1; ++i) {
+                B b;
+                load(b, i);
+                multiply<NT, LO, XS>(acc, b);
+            }
+        }
+        const int g = lane >> 2, t = lane & 3;
+        n0 += warp * P::kCols;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int row = nt * 8 + 2 * t + j;
+                if (row < rows) {
+                    float* dst = part + row * ld;
+                    if constexpr (Q4) {
+                        const int n = n0 + 4 * ((g >> 1) | ((g & 1) << 2));
+                        if (n < N)
+                            *reinterpret_cast<float4*>(dst + n) = make_float4(acc[0][nt][j], acc[0][nt][j + 2], acc[1][nt][j], acc[1][nt][j + 2]);
+                    } else {
+#pragma unroll
+                        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                const int n = n0 + mt * 16 + g + 8 * u;
+                                if (n < N) dst[n] = acc[mt][nt][j + 2 * u];
+                            }
+                    }
+                }
+            }
+    }
+
+    // Goes through this CTA's items of product p; f(matrix, tile, i0, i1,
+    // part number) works on a segment.
+    template <class F>
+    __device__ __forceinline__ void walk(int p, F f)
+    {
+        const Product& q = pr[p];
+        for (int n = 0;; ++n) {
+            const int id = item_at(q, queue[p], n, ctrl, timeout_ns);
+            if (id >= q.items) return;
+            int b = id * q.per;
+            const int e = min(b + q.per, q.total);
+            while (b < e) {
+                const int tile = b / q.kb, t0 = tile * q.kb, end = min(t0 + q.kb, e);
+                const int matrix = tile / q.tiles;
+                f(matrix, tile - matrix * q.tiles, b - t0, end - t0, id - q.first_item(t0));
+                b = end;
+            }
+        }
+    }
+};
 
 }  // namespace skinny
 }  // namespace tovl
