@@ -6,7 +6,7 @@
 // Products of bf16 (or e4m3, exact in bf16) activations with the integers
 // nibble - zero are exact, a group's sum is fp32, and the scales multiply it
 // in fp32: nothing is rounded before the result.  The stream of weight blocks
-// and the split are skinny.cuh's; every 16 rows are a pass over the weights
+// and the split are skinny.cuh's; every 32 rows are a pass over the weights
 // (one pass is the next one's matrix, so large matrices are read again).
 #include <type_traits>
 #include "launch.cuh"
@@ -26,7 +26,7 @@ struct Tables {
 };
 
 template <int G>
-constexpr int smem_size() { return 1024 + Shape<G>::kRing + static_cast<int>(sizeof(Tables)) + 16; }
+constexpr int smem_size() { return 1024 + Shape<G>::kRing + kRowBuffers + static_cast<int>(sizeof(Tables)) + 16; }
 
 struct Calls {
     const MatvecParams& p;
@@ -39,38 +39,18 @@ template <int NT, bool XS, int G, bool Z>
 __device__ __forceinline__ void run_segment(const MatvecParams& p, Engine<G, Z, Calls>& eng, int r0, int cnt, int tile, int i0,
                                             int i1, int number)
 {
-    const int g = eng.lane >> 2, t = eng.lane & 3;
     const int n_xs = (p.K + kXScaleGroup - 1) / kXScaleGroup;
-    long long row[NT];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)      // a row past the last one repeats the first; its column is never stored
-        row[nt] = (r0 + (nt * 8 + g < cnt ? nt * 8 + g : 0)) * p.ldx;
     float* part = p.part + (static_cast<long long>(number) * p.T + r0) * p.N;
-    eng.template segment<NT, false, XS>(i0, i1, part, p.N, cnt, tile * kTileCols, p.N, [&](Frags<NT, false, true>& b, int i) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int R = 0; R < 4; ++R) {
-                const int k = i * kRowsQ4 + 32 * R + 8 * t;
-                b.v[R][nt] = make_uint4(0, 0, 0, 0);      // (rows of W past the last one are zeros; so must these be)
-                if (k < p.K) {
-                    if (XS) {
-                        const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.x) + row[nt] + k));
-                        const uint2 lo = e4m3x4_to_bf16(v.x), hi = e4m3x4_to_bf16(v.y);
-                        b.v[R][nt] = make_uint4(lo.x, lo.y, hi.x, hi.y);
-                    } else {
-                        b.v[R][nt] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.x) + row[nt] + k));
-                    }
-                }
-            }
-            if (XS) {   // accumulator columns 2t and 2t + 1
-                const int c0 = nt * 8 + 2 * t;
-                const float* xs = p.x_scale + static_cast<long long>(r0 + c0) * n_xs + i;
-                b.sx[nt].x = c0 < cnt ? __ldg(xs) : 0.f;
-                b.sx[nt].y = c0 + 1 < cnt ? __ldg(xs + n_xs) : 0.f;
-            }
-        }
-    });
+    eng.template segment<NT, false, XS>(
+        i0, i1, part, p.N, cnt, tile * kTileCols, p.N, p.K,
+        [&](int r, int k, bool) {
+            const long long at = (r0 + r) * p.ldx + k;
+            if (!XS) return __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.x) + at));
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.x) + at));
+            const uint2 lo = e4m3x4_to_bf16(v.x), hi = e4m3x4_to_bf16(v.y);
+            return make_uint4(lo.x, lo.y, hi.x, hi.y);
+        },
+        [&](int r, int i) { return __ldg(p.x_scale + static_cast<long long>(r0 + r) * n_xs + i); });
 }
 
 template <bool XS, int G, bool Z>
@@ -79,9 +59,10 @@ __global__ void __launch_bounds__(Shape<G>::kThreads, 1) matvec_q4_kernel(const 
     using P = Shape<G>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align1024(smem_raw);
-    Tables& tb = *reinterpret_cast<Tables*>(smem + (P::kRing + 15) / 16 * 16);
+    uint8_t* rows_buf = smem + (P::kRing + 15) / 16 * 16;
+    Tables& tb = *reinterpret_cast<Tables*>(rows_buf + kRowBuffers);
     const Calls calls{p};
-    Engine<G, Z, Calls> eng{calls, &tb.pr, &tb.queue, p.sync + kTicketWord, p.ctrl, p.pipe_timeout_ns, 1};
+    Engine<G, Z, Calls> eng{calls, &tb.pr, &tb.queue, rows_buf, p.sync + kTicketWord, p.ctrl, p.pipe_timeout_ns, 1};
     eng.warp = threadIdx.x >> 5;
     eng.lane = threadIdx.x & 31;
     eng.ring.init(smem, eng.warp);
@@ -102,7 +83,8 @@ __global__ void __launch_bounds__(Shape<G>::kThreads, 1) matvec_q4_kernel(const 
     eng.walk(0, [&](int matrix, int tile, int i0, int i1, int number) {
         const int r0 = matrix * kPassRows, cnt = min(kPassRows, p.T - r0);
         if (cnt <= 8) run_segment<1, XS, G, Z>(p, eng, r0, cnt, tile, i0, i1, number);
-        else run_segment<2, XS, G, Z>(p, eng, r0, cnt, tile, i0, i1, number);
+        else if (cnt <= 16) run_segment<2, XS, G, Z>(p, eng, r0, cnt, tile, i0, i1, number);
+        else run_segment<4, XS, G, Z>(p, eng, r0, cnt, tile, i0, i1, number);
     });
     grid_barrier(p.sync + kBarrierWord, grid, p.ctrl, p.timeout_ns);
     const int quads = p.N / 4;

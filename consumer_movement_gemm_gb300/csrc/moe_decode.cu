@@ -50,7 +50,7 @@ struct Tables {
 };
 
 template <int G>
-constexpr int smem_size() { return 1024 + Shape<G>::kRing + static_cast<int>(sizeof(Tables)) + 16; }
+constexpr int smem_size() { return 1024 + Shape<G>::kRing + kRowBuffers + static_cast<int>(sizeof(Tables)) + 16; }
 
 // Builds the list of experts with rows.  Every CTA builds the same list
 // (ascending experts, ascending tokens), so they agree on row numbers without
@@ -152,7 +152,6 @@ struct Calls {
 template <int G, bool Z>
 struct Worker {
     using P = Shape<G>;
-    static constexpr bool Q4 = P::Q4;
     const MoeParams& p;
     const Tables& tb;
     Engine<G, Z, Calls>& eng;
@@ -161,35 +160,19 @@ struct Worker {
     template <int NT, bool H>
     __device__ __forceinline__ void segment(uint32_t en, int tile, int i0, int i1, int number)
     {
-        const int cnt = entry_rows(en), off = entry_off(en), g = eng.lane >> 2, t = eng.lane & 3;
+        const int cnt = entry_rows(en), off = entry_off(en);
         const int K = H ? p.I : p.H, N = H ? p.H : 2 * p.I;
-        const __nv_bfloat16* row[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            // a row past the last one repeats the first; its column is never stored
-            const int r = off + (nt * 8 + g < cnt ? nt * 8 + g : 0);
-            row[nt] = H ? static_cast<const __nv_bfloat16*>(p.h_hi) + static_cast<long long>(r) * p.I
-                        : static_cast<const __nv_bfloat16*>(p.x) + tb.row_tok[r] * p.ldx;
-        }
-        const long long lo = static_cast<const __nv_bfloat16*>(p.h_lo) - static_cast<const __nv_bfloat16*>(p.h_hi);
         float* part = p.part + (static_cast<long long>(number) * p.T * p.k + off) * N;
-        eng.template segment<NT, H, false>(i0, i1, part, N, cnt, tile * kTileCols, N, [&](Frags<NT, H, Q4>& b, int i) {
-#pragma unroll
-            for (int R = 0; R < Frags<NT, H, Q4>::R; ++R) {
-                const int k = i * P::kRows + 32 * R + 8 * t;
-                const bool in = k < K;      // (rows of W past the last one are zeros; so must these be)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    b.v[R][nt] = make_uint4(0, 0, 0, 0);
-                    if (H) b.l[R][nt] = make_uint4(0, 0, 0, 0);
-                    if (in) {
-                        const uint4* at = reinterpret_cast<const uint4*>(row[nt] + k);
-                        b.v[R][nt] = H ? __ldcg(at) : __ldg(at);
-                        if (H) b.l[R][nt] = __ldcg(reinterpret_cast<const uint4*>(row[nt] + lo + k));
-                    }
+        eng.template segment<NT, H, false>(
+            i0, i1, part, N, cnt, tile * kTileCols, N, K,
+            [&](int r, int k, bool lo) {
+                if (H) {     // (written in this launch)
+                    const __nv_bfloat16* h = static_cast<const __nv_bfloat16*>(lo ? p.h_lo : p.h_hi);
+                    return __ldcg(reinterpret_cast<const uint4*>(h + static_cast<long long>(off + r) * p.I + k));
                 }
-            }
-        });
+                return __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.x) + tb.row_tok[off + r] * p.ldx + k));
+            },
+            [](int, int) { return 1.f; });
     }
 
     template <bool H>
@@ -200,10 +183,8 @@ struct Worker {
             const int cnt = entry_rows(en);
             if (cnt <= 8) segment<1, H>(en, tile, i0, i1, number);
             else if (cnt <= 16) segment<2, H>(en, tile, i0, i1, number);
-            else if constexpr (P::kPassRows > 16) {
-                if (cnt <= 32) segment<4, H>(en, tile, i0, i1, number);
-                else segment<8, H>(en, tile, i0, i1, number);
-            }
+            else if (cnt <= 32) segment<4, H>(en, tile, i0, i1, number);
+            else if constexpr (P::kPassRows > 32) segment<8, H>(en, tile, i0, i1, number);
         });
     }
 
@@ -269,9 +250,10 @@ __global__ void __launch_bounds__(Shape<G>::kThreads, 1) moe_decode_kernel(const
     using P = Shape<G>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align1024(smem_raw);
-    Tables& tb = *reinterpret_cast<Tables*>(smem + (P::kRing + 15) / 16 * 16);
+    uint8_t* rows_buf = smem + (P::kRing + 15) / 16 * 16;
+    Tables& tb = *reinterpret_cast<Tables*>(rows_buf + kRowBuffers);
     const Calls calls{p, tb};
-    Engine<G, Z, Calls> eng{calls, tb.pr, tb.queue, p.sync + kTicketWord, p.ctrl, p.pipe_timeout_ns, 2};
+    Engine<G, Z, Calls> eng{calls, tb.pr, tb.queue, rows_buf, p.sync + kTicketWord, p.ctrl, p.pipe_timeout_ns, 2};
     eng.warp = threadIdx.x >> 5;
     eng.lane = threadIdx.x & 31;
     eng.ring.init(smem, eng.warp);

@@ -14,7 +14,8 @@
 // alone) 5.85.  A warp owns its columns, so nothing is summed across warps and
 // no warp waits for another one; each has its own ring of stages, filled by its
 // own lane 0, that runs on across tiles and across the two products of an
-// expert layer (weights depend on nothing).
+// expert layer (weights depend on nothing).  The few rows of x pass through
+// shared memory once per CTA, as bf16, where all warps read them.
 //
 // Items.  The units of a product, in the order (matrix, tile of 512 columns,
 // k), are cut into items of equal length.  With little work there is one item
@@ -58,13 +59,21 @@ struct Shape {
     static constexpr int kRows = Q4 ? kRowsQ4 : kRowsBf16;    // rows of W in a block
     static constexpr int kBlockBytes = Q4 ? 2048 : 4096;
     static constexpr int kMetaBytes = Q4 ? kScaleBytes + kZeroBytes : 0;
-    static constexpr int kStages = 5;                         // 160 KB in flight per SM
+    static constexpr int kStages = Q4 ? 4 : 5;                // 128 or 160 KB in flight per SM
     static constexpr int kMT = kCols / 16;                    // 16-column accumulator tiles
     static constexpr int kRing = kWarps * kStages * (kBlockBytes + kMetaBytes + 8);   // 1 KB aligned
     // rows that one pass over a matrix takes: 4-bit blocks keep the sums of a
     // scale group beside the running ones
-    static constexpr int kPassRows = Q4 ? 16 : 64;
+    static constexpr int kPassRows = Q4 ? 32 : 64;
 };
+
+// Rows of x wait in shared memory in chunks of units: 16 KB (twice) of bf16
+// for NT * 8 rows, with their second parts (LO) behind them.
+constexpr int kChunkBytes = 16384;
+constexpr int kScalesOfChunk = 256;               // e4m3: a scale per row and unit
+constexpr int kRowBuffers = 2 * (kChunkBytes + kScalesOfChunk * 4);
+template <int G, int NT, bool LO>
+constexpr int chunk_units() { return kChunkBytes / (NT * 8 * (LO ? 2 : 1) * Shape<G>::kRows * 2); }
 
 // ------------------------------------------------------------ instructions
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr)
@@ -216,9 +225,20 @@ struct Ring {
 // ------------------------------------------------------------ the rows' fragments
 // The k16 step's operand b gives lane 4g + t the rows' columns 2t, 2t+1 and
 // 2t+8, 2t+9 of token g.  The order of k is free as long as both operands use
-// the same, so a lane loads 16 bytes (8 consecutive k, an octet) of its token
-// and both k16 steps of 32 rows of W come from them.
-//
+// the same, so a lane reads 16 bytes (8 consecutive k, an octet) of its token
+// and both k16 steps of 32 rows of W come from them.  Octet o of row r lies at
+// r * pitch + 16 * (o ^ 4 (r & 1)): the two rows that a quarter warp reads
+// together use different banks.
+struct RowView {
+    uint32_t even, odd;      // this lane's octet t of an even (odd) group of 32 k, token g of the first 8
+    uint32_t tokens8;        // bytes from one 8 tokens to the next
+    uint32_t second;         // bytes to the second parts
+    __device__ __forceinline__ uint4 get(int R, int nt, bool lo) const
+    {
+        return ld_shared_u4(((R & 1) ? odd : even) + (R >> 1) * 128 + nt * tokens8 + (lo ? second : 0));
+    }
+};
+
 // bf16 weights: ldmatrix reads 8 rows of W per matrix, and the swizzle keeps
 // them apart in the banks only if their indexes differ modulo 8.  Lane t
 // therefore uses pair (t ^ i) of its octet in quarter-step i (rows 8t +
@@ -232,27 +252,30 @@ __device__ __forceinline__ uint4 rotate_pairs(uint4 v, int t)
 }
 
 // acc[mt][nt] (16 columns x 8 rows each) += a block of 32 x 64 bf16 weights.
+// R: the block's 32 k inside the view.
 template <int NT, bool LO>
-__device__ __forceinline__ void block_bf16(float (&acc)[4][NT][4], const uint4 (&b)[NT], const uint4 (&bl)[NT],
-                                           uint32_t block, int lane)
+__device__ __forceinline__ void block_bf16(float (&acc)[4][NT][4], const RowView& x, int R, uint32_t block, int lane)
 {
     const int m = lane >> 3, r = lane & 7;
     const int tp = r >> 1;
+    uint32_t a[2][4][4];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         const int low = 2 * (tp ^ (2 * s + (m >> 1))) + (r & 1);   // row of W modulo 8
         const uint32_t row = block + (8 * tp + low) * 128;
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {
-            uint32_t a[4];
-            ldmatrix_x4_trans(a, row + (((2 * mt + (m & 1)) ^ low) << 4));
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                mma(acc[mt][nt], a[0], a[1], a[2], a[3], s ? b[nt].z : b[nt].x, s ? b[nt].w : b[nt].y);
-                if (LO) mma(acc[mt][nt], a[0], a[1], a[2], a[3], s ? bl[nt].z : bl[nt].x, s ? bl[nt].w : bl[nt].y);
-            }
-        }
+        for (int mt = 0; mt < 4; ++mt) ldmatrix_x4_trans(a[s][mt], row + (((2 * mt + (m & 1)) ^ low) << 4));
     }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int l = 0; l < (LO ? 2 : 1); ++l) {
+            const uint4 b = rotate_pairs(x.get(R, nt, l), lane & 3);
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) mma(acc[mt][nt], a[0][mt][0], a[0][mt][1], a[0][mt][2], a[0][mt][3], b.x, b.y);
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) mma(acc[mt][nt], a[1][mt][0], a[1][mt][1], a[1][mt][2], a[1][mt][3], b.z, b.w);
+        }
 }
 
 // The four bf16 pairs (nibble - zero) of a packed word, rows in order.
@@ -266,13 +289,12 @@ __device__ __forceinline__ void unpack(uint32_t (&p)[4], uint32_t word, uint32_t
 }
 
 // acc[mt][nt] += a block of 128 x 32 4-bit weights in groups of G rows, with
-// zeros (Z) or 8 for all.  b[R][nt]: octet t of rows 32R .. 32R+31 of token g.
-// sx: the tokens' activation scales (XS).  Lane group g owns four neighbouring
+// zeros (Z) or 8 for all.  sx: the tokens' activation scales (XS).  Lane group g owns four neighbouring
 // columns; the order 0 4 1 5 2 6 3 7 of the groups keeps the 16-byte reads of
 // a quarter warp in different banks.
 template <int NT, bool LO, bool XS, int G, bool Z>
-__device__ __forceinline__ void block_q4(float (&acc)[2][NT][4], const uint4 (&b)[4][NT], const uint4 (*bl)[NT],
-                                         const float2 (&sx)[NT], uint32_t block, uint32_t scales, int lane)
+__device__ __forceinline__ void block_q4(float (&acc)[2][NT][4], const RowView& x, const float2 (&sx)[NT],
+                                         uint32_t block, uint32_t scales, int lane)
 {
     constexpr int kSteps = G / 32;
     const int g = lane >> 2, t = lane & 3;
@@ -296,18 +318,18 @@ __device__ __forceinline__ void block_q4(float (&acc)[2][NT][4], const uint4 (&b
         unpack(p3, v.w, z[3]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const uint4 x = b[R][nt];
+            const uint4 v4 = x.get(R, nt, false);
             if (first) {
-                mma_first(part[0][nt], p0[0], p1[0], p0[1], p1[1], x.x, x.y);
-                mma_first(part[1][nt], p2[0], p3[0], p2[1], p3[1], x.x, x.y);
+                mma_first(part[0][nt], p0[0], p1[0], p0[1], p1[1], v4.x, v4.y);
+                mma_first(part[1][nt], p2[0], p3[0], p2[1], p3[1], v4.x, v4.y);
             } else {
-                mma(part[0][nt], p0[0], p1[0], p0[1], p1[1], x.x, x.y);
-                mma(part[1][nt], p2[0], p3[0], p2[1], p3[1], x.x, x.y);
+                mma(part[0][nt], p0[0], p1[0], p0[1], p1[1], v4.x, v4.y);
+                mma(part[1][nt], p2[0], p3[0], p2[1], p3[1], v4.x, v4.y);
             }
-            mma(part[0][nt], p0[2], p1[2], p0[3], p1[3], x.z, x.w);
-            mma(part[1][nt], p2[2], p3[2], p2[3], p3[3], x.z, x.w);
+            mma(part[0][nt], p0[2], p1[2], p0[3], p1[3], v4.z, v4.w);
+            mma(part[1][nt], p2[2], p3[2], p2[3], p3[3], v4.z, v4.w);
             if (LO) {
-                const uint4 y = bl[R][nt];
+                const uint4 y = x.get(R, nt, true);
                 mma(part[0][nt], p0[0], p1[0], p0[1], p1[1], y.x, y.y);
                 mma(part[1][nt], p2[0], p3[0], p2[1], p3[1], y.x, y.y);
                 mma(part[0][nt], p0[2], p1[2], p0[3], p1[3], y.z, y.w);
@@ -382,12 +404,6 @@ __device__ __forceinline__ int item_at(const Product& pr, const Queue& q, int n,
     return v;
 }
 
-// A warp's place among the blocks that it fetches.
-struct Cursor {
-    int n, left;               // item of the CTA's list, units of it still to fetch
-    int i, tile, matrix;       // k unit, tile, matrix of the next one
-};
-
 // Whole CTA: waits until all CTAs of the grid have arrived `round` times on
 // the counter; what any of them wrote before is visible after.  Bounded; the
 // counter is cleared by the last CTA of the launch to leave.
@@ -411,15 +427,6 @@ __device__ __forceinline__ void grid_barrier(int* counter, int target, const Ctr
     __syncthreads();
 }
 
-// Fragment sets of the rows of one block: one octet per row for bf16, four
-// for 4-bit weights; LO: also of the second parts.
-template <int NT, bool LO, bool Q4>
-struct Frags {
-    static constexpr int R = Q4 ? 4 : 1;
-    uint4 v[R][NT], l[LO ? R : 1][NT];
-    float2 sx[NT];
-};
-
 // Adds `n` parts, `stride` floats apart, of four neighbouring columns.
 __device__ __forceinline__ float4 add_parts(const float* part, int n, long long stride)
 {
@@ -434,7 +441,6 @@ __device__ __forceinline__ float4 add_parts(const float* part, int n, long long 
 
 // The engine of one warp.  `Calls` provides, for product `ph` (0 or 1):
 //   maps(ph), expert(ph, matrix)     where a matrix' weights are
-//   rows(ph, matrix)                 rows of the product with it, 1 .. kPassRows
 template <int G, bool Z, class Calls>
 struct Engine {
     using P = Shape<G>;
@@ -442,99 +448,83 @@ struct Engine {
     const Calls& c;
     const Product* pr;         // the call's products, in shared memory
     Queue* queue;
+    uint8_t* rows_buf;         // kRowBuffers bytes
     int* tickets;              // global counters, one per product
     const Ctrl& ctrl;
     long long timeout_ns;
     int n_products;
     int warp, lane;
     Ring<G, Z> ring;
-    Cursor f;
-    int ph = 0;                // product that is being fetched
+    // the next block to fetch: product, item of the CTA's list, units of the
+    // item still to fetch, place of the next one
+    int ph = 0, n = 0, left = 0, i = 0, tile = 0, matrix = 0;
+    int kb = 0, tiles = 0;     // of the product
 
-    __device__ __forceinline__ void open(int n)
+    // Goes on to item n of the product; left stays 0 where there is none.
+    __device__ __forceinline__ void open()
     {
         const Product& q = pr[ph];
-        f.n = n;
-        f.left = 0;
         const int id = item_at(q, queue[ph], n, ctrl, timeout_ns);
         if (id >= q.items) return;
         if (q.tickets && warp == 0 && lane == 0) {
-            if (n == 0) queue[ph].item[1] = static_cast<uint16_t>(min(atomicAdd(tickets + ph * kSyncStep, 1) + static_cast<int>(gridDim.x), q.items));
-            queue[ph].item[n + 2] = static_cast<uint16_t>(min(atomicAdd(tickets + ph * kSyncStep, 1) + static_cast<int>(gridDim.x), q.items));
+            const int grid = gridDim.x;
+            if (n == 0) queue[ph].item[1] = static_cast<uint16_t>(min(atomicAdd(tickets + ph * kSyncStep, 1) + grid, q.items));
+            queue[ph].item[n + 2] = static_cast<uint16_t>(min(atomicAdd(tickets + ph * kSyncStep, 1) + grid, q.items));
         }
         const int b = id * q.per;
-        f.left = min(q.per, q.total - b);
-        const int tile = b / q.kb;
-        f.i = b - tile * q.kb;
-        f.matrix = tile / q.tiles;
-        f.tile = tile - f.matrix * q.tiles;
+        left = min(q.per, q.total - b);
+        kb = q.kb;
+        tiles = q.tiles;
+        const int at = b / kb;
+        i = b - at * kb;
+        matrix = at / tiles;
+        tile = at - matrix * tiles;
     }
 
     // Fetches the warp's next block, if there is one.
     __device__ __forceinline__ void fetch()
     {
-        while (f.left == 0) {
-            // next item, or the next product's first
+        while (left == 0) {
             if (ph >= n_products) return;
-            const Product& q = pr[ph];
-            if (f.n >= 0 && item_at(q, queue[ph], f.n, ctrl, timeout_ns) >= q.items) {
-                if (++ph >= n_products) return;
-                open(0);
-            } else {
-                open(f.n + 1);
+            open();
+            ++n;
+            if (left == 0) {     // the product has no more items for this CTA
+                ++ph;
+                n = 0;
             }
         }
-        if (lane == 0)
-            ring.issue(c.maps(ph), f.tile * kTileCols + warp * P::kCols, f.i * P::kRows, c.expert(ph, f.matrix));
+        if (lane == 0) ring.issue(c.maps(ph), tile * kTileCols + warp * P::kCols, i * P::kRows, c.expert(ph, matrix));
         ring.filled();
-        --f.left;
-        if (++f.i == pr[ph].kb) {
-            f.i = 0;
-            if (++f.tile == pr[ph].tiles) {
-                f.tile = 0;
-                ++f.matrix;
+        --left;
+        if (++i == kb) {
+            i = 0;
+            if (++tile == tiles) {
+                tile = 0;
+                ++matrix;
             }
         }
     }
 
     __device__ __forceinline__ void start()
     {
-        open(0);
 #pragma unroll 1
         for (int s = 0; s < P::kStages; ++s) fetch();
     }
 
-    // acc += the ring's next block times the rows; the stage is refilled.
-    template <int NT, bool LO, bool XS>
-    __device__ __forceinline__ void multiply(float (&acc)[P::kMT][NT][4], const Frags<NT, LO, Q4>& b)
+    // Whole CTA.  Sums over k units [i0, i1) of a tile for `rows` <= NT * 8
+    // rows, written to part[row][n], rows `ld` floats apart (n0: the tile's
+    // first column, N: the matrix').  octet(r, k, lo) gives 8 values of row r
+    // from column k on (k < K), as bf16; scale(r, i) the row's scale in unit i
+    // (XS).  The rows go through shared memory in chunks, once per CTA; the
+    // next chunk is on its way to registers while one is multiplied.
+    template <int NT, bool LO, bool XS, class F, class S>
+    __device__ __forceinline__ void segment(int i0, int i1, float* part, long long ld, int rows, int n0, int N, int K, F octet,
+                                            S scale)
     {
-        ring.wait(ctrl, timeout_ns);
-        if constexpr (Q4) {
-            block_q4<NT, LO, XS, G, Z>(acc, b.v, b.l, b.sx, ring.block(), ring.scales(), lane);
-        } else {
-            uint4 v[NT], l[NT];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                v[nt] = rotate_pairs(b.v[0][nt], lane & 3);
-                if (LO) l[nt] = rotate_pairs(b.l[0][nt], lane & 3);
-            }
-            block_bf16<NT, LO>(acc, v, l, ring.block(), lane);
-        }
-        ring.taken();
-        __syncwarp();      // every lane has read the stage before it is filled again
-        fetch();
-    }
-
-    // Sums over k units [i0, i1) of a tile, written to part[row][n], rows
-    // `ld` floats apart (n0: the tile's first column, N: the matrix').
-    // load(b, i) fills b with the rows' fragments of unit i.  The next unit's
-    // are loaded before this one is multiplied where two sets fit the
-    // registers: their latency is longer than a block's work.
-    template <int NT, bool LO, bool XS, class F>
-    __device__ __forceinline__ void segment(int i0, int i1, float* part, long long ld, int rows, int n0, int N, F load)
-    {
-        using B = Frags<NT, LO, Q4>;
-        constexpr bool kTwo = Q4 ? NT == 1 : NT <= 4;
+        constexpr int kUnits = chunk_units<G, NT, LO>();
+        constexpr int kOctets = kUnits * P::kRows / 8;                 // of a row in a chunk
+        constexpr int kPitch = kOctets * 16;
+        constexpr int kPer = kChunkBytes / 16 / P::kThreads;           // octets of a thread
         float acc[P::kMT][NT][4];
 #pragma unroll
         for (int mt = 0; mt < P::kMT; ++mt)
@@ -542,24 +532,76 @@ struct Engine {
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) acc[mt][nt][j] = 0.f;
-        if constexpr (kTwo) {
-            B b[2];
-            load(b[0], i0);
-            for (int i = i0; i < i1; i += 2) {
-                if (i + 1 < i1) load(b[1], i + 1);
-                multiply<NT, LO, XS>(acc, b[0]);
-                if (i + 1 >= i1) break;
-                if (i + 2 < i1) load(b[0], i + 2);
-                multiply<NT, LO, XS>(acc, b[1]);
-            }
-        } else {
-            for (int i = i0; i < i1; ++i) {
-                B b;
-                load(b, i);
-                multiply<NT, LO, XS>(acc, b);
-            }
-        }
         const int g = lane >> 2, t = lane & 3;
+        const int tid = warp * 32 + lane;
+        uint4 next[kPer];
+        float next_scale = 0.f;
+        // this thread's octets of the chunk that starts at unit u
+        const auto get = [&](int u) {
+#pragma unroll
+            for (int x = 0; x < kPer; ++x) {
+                const int at = tid + x * P::kThreads, r = at / kOctets, k = u * P::kRows + (at % kOctets) * 8;
+                const int row = LO ? r % (NT * 8) : r;
+                next[x] = make_uint4(0, 0, 0, 0);     // (rows of W past the last one are zeros; so must these be)
+                if (row < rows && k < K) next[x] = octet(row, k, LO && r >= NT * 8);
+            }
+            if (XS && tid < kUnits * NT * 8) {
+                const int r = tid / kUnits, v = u + tid % kUnits;
+                next_scale = r < rows && v < i1 ? scale(r, v) : 0.f;
+            }
+        };
+        const auto put = [&](uint8_t* buf) {
+#pragma unroll
+            for (int x = 0; x < kPer; ++x) {
+                const int at = tid + x * P::kThreads, r = at / kOctets, o = at % kOctets;
+                *reinterpret_cast<uint4*>(buf + r * kPitch + ((o ^ ((r & 1) << 2)) << 4)) = next[x];
+            }
+            if (XS && tid < kUnits * NT * 8) reinterpret_cast<float*>(buf + kChunkBytes)[tid] = next_scale;
+        };
+        uint8_t* buf = rows_buf;
+        uint8_t* other = rows_buf + kRowBuffers / 2;
+        get(i0);
+        __syncthreads();       // the segment before this one has read both buffers
+        put(buf);
+        for (int u = i0; u < i1; u += kUnits) {
+            __syncthreads();   // this chunk is complete, the other buffer has been read
+            if (u + kUnits < i1) get(u + kUnits);
+            const uint32_t base = ptx::smem_u32(buf) + g * kPitch;
+            RowView x;
+            x.tokens8 = 8 * kPitch;
+            x.second = NT * 8 * kPitch;
+            const int end = min(kUnits, i1 - u);
+#pragma unroll 1
+            for (int v = 0; v < end; ++v) {
+                // (a bf16 unit is half of a 128-byte row of octets)
+                const uint32_t at = base + (Q4 ? v * 256 : (v >> 1) * 128);
+                x.even = at + ((t ^ ((g & 1) << 2)) << 4);
+                x.odd = at + (((t + 4) ^ ((g & 1) << 2)) << 4);
+                ring.wait(ctrl, timeout_ns);
+                if constexpr (Q4) {
+                    float2 sx[NT];
+                    if (XS) {
+                        const float* sc = reinterpret_cast<const float*>(buf + kChunkBytes) + v;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            sx[nt].x = sc[(nt * 8 + 2 * t) * kUnits];
+                            sx[nt].y = sc[(nt * 8 + 2 * t + 1) * kUnits];
+                        }
+                    }
+                    block_q4<NT, LO, XS, G, Z>(acc, x, sx, ring.block(), ring.scales(), lane);
+                } else {
+                    if (v & 1) x.even = x.odd;
+                    block_bf16<NT, LO>(acc, x, 0, ring.block(), lane);
+                }
+                ring.taken();
+                __syncwarp();      // every lane has read the stage before it is filled again
+                fetch();
+            }
+            if (u + kUnits < i1) put(other);
+            uint8_t* b = buf;
+            buf = other;
+            other = b;
+        }
         n0 += warp * P::kCols;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -576,9 +618,9 @@ struct Engine {
 #pragma unroll
                         for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                const int n = n0 + mt * 16 + g + 8 * u;
-                                if (n < N) dst[n] = acc[mt][nt][j + 2 * u];
+                            for (int w = 0; w < 2; ++w) {
+                                const int n = n0 + mt * 16 + g + 8 * w;
+                                if (n < N) dst[n] = acc[mt][nt][j + 2 * w];
                             }
                     }
                 }
