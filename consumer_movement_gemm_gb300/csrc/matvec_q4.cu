@@ -17,7 +17,7 @@ namespace tovl {
 namespace {
 
 using namespace skinny;
-constexpr int kPassRows = Shape<128>::kPassRows;
+constexpr int kPassRows = 32;
 constexpr int kThreads4 = Shape<128>::kThreads;
 
 struct Tables {
@@ -30,7 +30,7 @@ constexpr int smem_size() { return 1024 + Shape<G>::kRing + kRowBuffers + static
 
 struct Calls {
     const MatvecParams& p;
-    __device__ __forceinline__ const WeightMaps& maps(int) const { return p.w; }
+    __device__ __forceinline__ const WeightMaps* maps(int) const { return &p.w; }
     __device__ __forceinline__ int expert(int, int) const { return 0; }
 };
 
@@ -50,7 +50,7 @@ __device__ __forceinline__ void run_segment(const MatvecParams& p, Engine<G, Z, 
             const uint2 lo = e4m3x4_to_bf16(v.x), hi = e4m3x4_to_bf16(v.y);
             return make_uint4(lo.x, lo.y, hi.x, hi.y);
         },
-        [&](int r, int i) { return __ldg(p.x_scale + static_cast<long long>(r0 + r) * n_xs + i); });
+        [&](int r, int k) { return __ldg(p.x_scale + static_cast<long long>(r0 + r) * n_xs + k / kXScaleGroup); });
 }
 
 template <bool XS, int G, bool Z>
@@ -62,13 +62,11 @@ __global__ void __launch_bounds__(Shape<G>::kThreads, 1) matvec_q4_kernel(const 
     uint8_t* rows_buf = smem + (P::kRing + 15) / 16 * 16;
     Tables& tb = *reinterpret_cast<Tables*>(rows_buf + kRowBuffers);
     const Calls calls{p};
-    Engine<G, Z, Calls> eng{calls, &tb.pr, &tb.queue, rows_buf, p.sync + kTicketWord, p.ctrl, p.pipe_timeout_ns, 1};
+    Engine<G, Z, Calls> eng{calls, &tb.pr, &tb.queue, p.sync + kTicketWord, p.ctrl, p.pipe_timeout_ns, 1};
     eng.warp = threadIdx.x >> 5;
     eng.lane = threadIdx.x & 31;
-    eng.ring.init(smem, eng.warp);
-    if (eng.lane == 0) {
-        eng.ring.init_barriers();
-        ptx::fence_mbar_init();
+    eng.init(smem, rows_buf);
+    if (threadIdx.x == 0) {
         ptx::prefetch_tmap(&p.w.w);
         ptx::prefetch_tmap(&p.w.scale);
     }
@@ -91,7 +89,11 @@ __global__ void __launch_bounds__(Shape<G>::kThreads, 1) matvec_q4_kernel(const 
     for (int i = blockIdx.x * P::kThreads + threadIdx.x; i < p.T * quads; i += grid * P::kThreads) {
         const int t = i / quads, n = (i - t * quads) * 4;
         const int t0 = (t / kPassRows * tb.pr.tiles + n / kTileCols) * tb.pr.kb;
-        const float4 s = add_parts(p.part + static_cast<long long>(t) * p.N + n, tb.pr.parts(t0), static_cast<long long>(p.T) * p.N);
+        const float* const part[1] = {p.part + static_cast<long long>(t) * p.N + n};
+        const int count[1] = {tb.pr.parts(t0)};
+        float4 sums[1];
+        add_parts<1>(sums, part, count, static_cast<long long>(p.T) * p.N);
+        const float4 s = sums[0];
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + t * p.ldo + n;
         if (p.out_vec) {
             *reinterpret_cast<uint2*>(out) = make_uint2(ptx::pack_bf16x2(s.x, s.y), ptx::pack_bf16x2(s.z, s.w));

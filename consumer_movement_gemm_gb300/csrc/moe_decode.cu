@@ -43,11 +43,21 @@ struct Tables {
     float pair_w[kMaxPairs];                // its gate weight, with those of later slots that name the expert too
     uint16_t row_entry[kMaxPairs];
     uint8_t row_tok[kMaxPairs];
-    int16_t topk[kMaxPairs];
-    float gate[kMaxPairs];
-    unsigned long long mask[kMaxExperts];   // tokens of each expert
     int n_entries, n_rows, bad;
 };
+
+// What only building the tables needs; lies where the rows go later.
+struct Building {
+    unsigned long long mask[kMaxExperts];   // tokens of each expert
+    float gate[kMaxPairs];
+    int16_t topk[kMaxPairs];
+};
+static_assert(sizeof(Building) <= kRowBuffers, "the tables' scratch fits the row buffers");
+
+// Rows of an expert that one entry takes: 4-bit blocks keep the sums of a
+// scale group beside the running ones, and both parts of 32 rows of h would
+// not fit a chunk.
+constexpr int pass_rows(int group) { return group ? 16 : 64; }
 
 template <int G>
 constexpr int smem_size() { return 1024 + Shape<G>::kRing + kRowBuffers + static_cast<int>(sizeof(Tables)) + 16; }
@@ -57,7 +67,7 @@ constexpr int smem_size() { return 1024 + Shape<G>::kRing + kRowBuffers + static
 // talking.  A token that names an expert twice has one row with both weights.
 // False if an id is outside [-1, E).
 template <int PASS, int THREADS>
-__device__ bool build_tables(const MoeParams& p, Tables& tb)
+__device__ bool build_tables(const MoeParams& p, Tables& tb, Building& bd)
 {
     const int tid = threadIdx.x, lane = tid & 31;
     const int pairs = p.T * p.k;
@@ -70,7 +80,7 @@ __device__ bool build_tables(const MoeParams& p, Tables& tb)
         id[u] = i < pairs ? __ldg(p.topk + i) : -1;
         w[u] = i < pairs ? __ldg(p.gate_w + i) : 0.f;
     }
-    for (int e = tid; e < p.E; e += THREADS) tb.mask[e] = 0;
+    for (int e = tid; e < p.E; e += THREADS) bd.mask[e] = 0;
     if (tid == 0) tb.bad = 0;
     __syncthreads();
 #pragma unroll
@@ -81,9 +91,9 @@ __device__ bool build_tables(const MoeParams& p, Tables& tb)
                 tb.bad = 1;
                 id[u] = -1;
             }
-            tb.topk[i] = static_cast<int16_t>(id[u]);
-            tb.gate[i] = w[u];
-            if (id[u] >= 0) atomicOr(tb.mask + id[u], 1ull << (i / p.k));
+            bd.topk[i] = static_cast<int16_t>(id[u]);
+            bd.gate[i] = w[u];
+            if (id[u] >= 0) atomicOr(bd.mask + id[u], 1ull << (i / p.k));
         }
     }
     __syncthreads();
@@ -92,7 +102,7 @@ __device__ bool build_tables(const MoeParams& p, Tables& tb)
         int n = 0, rows = 0;
         for (int base = 0; base < p.E; base += 32) {
             const int e = base + lane;
-            unsigned long long m = e < p.E ? tb.mask[e] : 0;
+            unsigned long long m = e < p.E ? bd.mask[e] : 0;
             const int cnt = __popcll(m), passes = (cnt + PASS - 1) / PASS;
             int sn = passes, sr = cnt;
 #pragma unroll
@@ -124,7 +134,7 @@ __device__ bool build_tables(const MoeParams& p, Tables& tb)
 
 // Row and weight of every (token, slot); read after the next barrier.
 template <int THREADS>
-__device__ void build_pairs(const MoeParams& p, Tables& tb)
+__device__ void build_pairs(const MoeParams& p, Tables& tb, const Building& bd)
 {
     for (int i = threadIdx.x; i < p.T * p.k; i += THREADS) tb.pair_row[i] = -1;
     __syncthreads();
@@ -133,9 +143,9 @@ __device__ void build_pairs(const MoeParams& p, Tables& tb)
         int first = -1;
         float w = 0.f;
         for (int j = 0; j < p.k; ++j)
-            if (tb.topk[t * p.k + j] == e) {
+            if (bd.topk[t * p.k + j] == e) {
                 if (first < 0) first = j;
-                w += tb.gate[t * p.k + j];
+                w += bd.gate[t * p.k + j];
             }
         tb.pair_row[t * p.k + first] = static_cast<int16_t>(r);
         tb.pair_w[t * p.k + first] = w;
@@ -145,7 +155,7 @@ __device__ void build_pairs(const MoeParams& p, Tables& tb)
 struct Calls {
     const MoeParams& p;
     const Tables& tb;
-    __device__ __forceinline__ const WeightMaps& maps(int ph) const { return ph ? p.w2 : p.w13; }
+    __device__ __forceinline__ const WeightMaps* maps(int ph) const { return ph ? &p.w2 : &p.w13; }
     __device__ __forceinline__ int expert(int, int matrix) const { return entry_expert(tb.entry[matrix]); }
 };
 
@@ -183,26 +193,32 @@ struct Worker {
             const int cnt = entry_rows(en);
             if (cnt <= 8) segment<1, H>(en, tile, i0, i1, number);
             else if (cnt <= 16) segment<2, H>(en, tile, i0, i1, number);
-            else if (cnt <= 32) segment<4, H>(en, tile, i0, i1, number);
-            else if constexpr (P::kPassRows > 32) segment<8, H>(en, tile, i0, i1, number);
+            else if constexpr (G == 0) {
+                if (cnt <= 32) segment<4, H>(en, tile, i0, i1, number);
+                else segment<8, H>(en, tile, i0, i1, number);
+            }
         });
     }
 
-    // Sum of the parts of four columns of a row of product `ph`.
-    __device__ __forceinline__ float4 total(int ph, int row, int n, int N) const
+    // Where the parts of column n of a row of product `ph` start, and their number.
+    __device__ __forceinline__ const float* parts(int ph, int row, int n, int N, int& count) const
     {
         const Product& q = tb.pr[ph];
-        const int t0 = (tb.row_entry[row] * q.tiles + n / kTileCols) * q.kb;
-        return add_parts(p.part + static_cast<long long>(row) * N + n, q.parts(t0), static_cast<long long>(p.T) * p.k * N);
+        count = q.parts((tb.row_entry[row] * q.tiles + n / kTileCols) * q.kb);
+        return p.part + static_cast<long long>(row) * N + n;
     }
 
     __device__ __forceinline__ void activations()
     {
         const int quads = p.I / 4;
+        const long long stride = static_cast<long long>(p.T) * p.k * 2 * p.I;
         for (int i = blockIdx.x * P::kThreads + threadIdx.x; i < tb.n_rows * quads; i += gridDim.x * P::kThreads) {
             const int row = i / quads, n = (i - row * quads) * 4;
-            const float4 g4 = total(0, row, n, 2 * p.I), u4 = total(0, row, p.I + n, 2 * p.I);
-            const float g[4] = {g4.x, g4.y, g4.z, g4.w}, u[4] = {u4.x, u4.y, u4.z, u4.w};
+            int count[2];
+            const float* part[2] = {parts(0, row, n, 2 * p.I, count[0]), parts(0, row, p.I + n, 2 * p.I, count[1])};
+            float4 s[2];
+            add_parts<2>(s, part, count, stride);
+            const float g[4] = {s[0].x, s[0].y, s[0].z, s[0].w}, u[4] = {s[1].x, s[1].y, s[1].z, s[1].w};
             float hi[4], lo[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -222,23 +238,38 @@ struct Worker {
     __device__ __forceinline__ void outputs()
     {
         const int quads = p.H / 4;
+        const long long stride = static_cast<long long>(p.T) * p.k * p.H;
         for (int i = blockIdx.x * P::kThreads + threadIdx.x; i < p.T * quads; i += gridDim.x * P::kThreads) {
             const int t = i / quads, n = (i - t * quads) * 4;
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int j = 0; j < p.k; ++j) {
-                const int row = tb.pair_row[t * p.k + j];
-                if (row < 0) continue;
-                const float w = tb.pair_w[t * p.k + j];
-                const float4 v = total(1, row, n, p.H);
-                s.x += w * v.x, s.y += w * v.y, s.z += w * v.z, s.w += w * v.w;
+            float4 out4 = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int j = 0; j < p.k; j += 2) {      // two slots' parts together
+                const float* part[2];
+                int count[2];
+                float w[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int row = j + u < p.k ? tb.pair_row[t * p.k + j + u] : -1;
+                    part[u] = p.part;
+                    count[u] = 0;
+                    w[u] = 0.f;
+                    if (row >= 0) {
+                        part[u] = parts(1, row, n, p.H, count[u]);
+                        w[u] = tb.pair_w[t * p.k + j + u];
+                    }
+                }
+                float4 s[2];
+                add_parts<2>(s, part, count, stride);
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    if (count[u])
+                        out4.x += w[u] * s[u].x, out4.y += w[u] * s[u].y, out4.z += w[u] * s[u].z, out4.w += w[u] * s[u].w;
             }
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + t * p.ldo + n;
-            const uint32_t lo = ptx::pack_bf16x2(s.x, s.y), hi = ptx::pack_bf16x2(s.z, s.w);
             if (p.out_vec) {
-                *reinterpret_cast<uint2*>(out) = make_uint2(lo, hi);
+                *reinterpret_cast<uint2*>(out) = make_uint2(ptx::pack_bf16x2(out4.x, out4.y), ptx::pack_bf16x2(out4.z, out4.w));
             } else {
-                out[0] = __float2bfloat16(s.x), out[1] = __float2bfloat16(s.y);
-                out[2] = __float2bfloat16(s.z), out[3] = __float2bfloat16(s.w);
+                out[0] = __float2bfloat16(out4.x), out[1] = __float2bfloat16(out4.y);
+                out[2] = __float2bfloat16(out4.z), out[3] = __float2bfloat16(out4.w);
             }
         }
     }
@@ -252,14 +283,13 @@ __global__ void __launch_bounds__(Shape<G>::kThreads, 1) moe_decode_kernel(const
     uint8_t* smem = align1024(smem_raw);
     uint8_t* rows_buf = smem + (P::kRing + 15) / 16 * 16;
     Tables& tb = *reinterpret_cast<Tables*>(rows_buf + kRowBuffers);
+    Building& bd = *reinterpret_cast<Building*>(rows_buf);
     const Calls calls{p, tb};
-    Engine<G, Z, Calls> eng{calls, tb.pr, tb.queue, rows_buf, p.sync + kTicketWord, p.ctrl, p.pipe_timeout_ns, 2};
+    Engine<G, Z, Calls> eng{calls, tb.pr, tb.queue, p.sync + kTicketWord, p.ctrl, p.pipe_timeout_ns, 2};
     eng.warp = threadIdx.x >> 5;
     eng.lane = threadIdx.x & 31;
-    eng.ring.init(smem, eng.warp);
-    if (eng.lane == 0) {
-        eng.ring.init_barriers();
-        ptx::fence_mbar_init();
+    eng.init(smem, rows_buf);
+    if (threadIdx.x == 0) {
         ptx::prefetch_tmap(&p.w13.w);
         ptx::prefetch_tmap(&p.w2.w);
     }
@@ -268,7 +298,7 @@ __global__ void __launch_bounds__(Shape<G>::kThreads, 1) moe_decode_kernel(const
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
     const int grid = gridDim.x;
-    if (!build_tables<P::kPassRows, P::kThreads>(p, tb)) {
+    if (!build_tables<pass_rows(G), P::kThreads>(p, tb, bd)) {
         if (blockIdx.x == 0 && threadIdx.x == 0) record_error(p.ctrl, kErrInvalid);
         return;
     }
@@ -276,7 +306,8 @@ __global__ void __launch_bounds__(Shape<G>::kThreads, 1) moe_decode_kernel(const
         tb.pr[threadIdx.x].init(tb.n_entries, threadIdx.x ? p.H : 2 * p.I, threadIdx.x ? p.I : p.H, P::kRows, grid, p.most_parts);
     __syncthreads();
     eng.start();
-    build_pairs<P::kThreads>(p, tb);
+    build_pairs<P::kThreads>(p, tb, bd);
+    __syncthreads();       // (the scratch becomes row buffers)
     Worker<G, Z> w{p, tb, eng};
     w.template product<false>();
     grid_barrier(p.sync + kBarrierWord, grid + p.ready_offset, p.ctrl, p.timeout_ns);

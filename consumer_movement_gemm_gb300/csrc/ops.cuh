@@ -16,7 +16,7 @@ constexpr int kXScaleGroup = 128;      // columns per scale of 8-bit activations
 // Counters of the streamed products (handle-owned, zero between calls), each
 // in a 128-byte line of its own: tickets of up to two products, arrivals of up
 // to three grid barriers, CTAs past the last one.
-constexpr int kMaxGrid = 256;
+constexpr int kMaxGrid = 160;
 constexpr int kSyncStep = 32;
 constexpr int kTicketWord = 0;         // tickets of product i at word i * kTicketStep
 constexpr int kBarrierWord = 2 * kSyncStep;
@@ -68,10 +68,10 @@ struct MoeParams {
     void* out;              // bf16 [T][H], rows ldo apart
     long long ldo;
     int out_vec;            // rows of out allow 8-byte stores
-    int most_parts;         // a tile is cut into most_parts + 1 parts at most
+    int most_parts;         // a tile is cut into most_parts + 2 parts at most
     void* h_hi;             // bf16 [T*k][I]: activations between the two products, and
     void* h_lo;             // what their rounding to bf16 left over
-    float* part;            // [most_parts + 1][T*k][2I or H] parts of the products
+    float* part;            // [most_parts + 2][T*k][2I or H] parts of the products
     int T, k, E, H, I;
     int* sync;              // kSyncWords counters
     int ready_offset;       // fault injection: CTAs that never come
@@ -88,7 +88,7 @@ struct MatvecParams {
     const void* x;          // bf16 or e4m3 [T][K], rows ldx apart
     const float* x_scale;   // [T][ceil(K/128)] for e4m3
     void* out;              // bf16 [T][N], rows ldo apart
-    float* part;            // [most_parts + 1][T][N] parts of the product
+    float* part;            // [most_parts + 2][T][N] parts of the product
     long long ldx, ldo;
     int T, K, N;
     int out_vec;

@@ -47,7 +47,7 @@ int encode_3d(tovl_ctx* h, CUtensorMap* map, CUtensorMapDataType type, int elem,
     return TOVL_OK;
 }
 
-// Blocks of one warp: 64 columns x 32 rows of bf16, 32 columns x 128 rows of 4 bits.
+// Blocks of one warp: 64 columns x 32 rows of bf16, 32 columns x 256 rows of 4 bits.
 int map_bf16(tovl_ctx* h, WeightMaps* m, const void* w, int E, int K, int N)
 {
     return encode_3d(h, &m->w, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, w, N, K, E, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B);
@@ -55,12 +55,12 @@ int map_bf16(tovl_ctx* h, WeightMaps* m, const void* w, int E, int K, int N)
 
 int map_q4(tovl_ctx* h, WeightMaps* m, const void* q, const void* scale, const void* zero, int E, int K, int N, int group)
 {
-    int rc = encode_3d(h, &m->w, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, q, N, K / 8, E, 32, 16, CU_TENSOR_MAP_SWIZZLE_128B);
+    int rc = encode_3d(h, &m->w, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, q, N, K / 8, E, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B);
     if (rc == TOVL_OK)
-        rc = encode_3d(h, &m->scale, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, scale, N, K / group, E, 32, 128 / group,
+        rc = encode_3d(h, &m->scale, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, scale, N, K / group, E, 32, 256 / group,
                        CU_TENSOR_MAP_SWIZZLE_NONE);
     if (rc == TOVL_OK && zero)
-        rc = encode_3d(h, &m->zero, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, zero, N, K / group, E, 32, 128 / group,
+        rc = encode_3d(h, &m->zero, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, zero, N, K / group, E, 32, 256 / group,
                        CU_TENSOR_MAP_SWIZZLE_NONE);
     return rc;
 }
@@ -78,7 +78,7 @@ bool valid_q4(int K, int N, int group, const void* q, const void* scale, const v
 
 long long up256(long long v) { return (v + 255) & ~255LL; }
 
-// Limit of a tile's parts (less one) by the rows of a product: few rows can
+// Limit of a tile's parts (less two) by the rows of a product: few rows can
 // afford a cut for every CTA, many have other tiles to share out.
 int most_parts(long long rows) { return rows <= 64 ? 16 : rows <= 256 ? 8 : 4; }
 
@@ -89,7 +89,7 @@ struct MoeSpace {
     {
         const long long rows = static_cast<long long>(T) * k;
         h = up256(2 * rows * I);
-        part = 4 * (most_parts(rows) + 1) * rows * (2 * I > H ? 2 * I : H);
+        part = 4 * (most_parts(rows) + 2) * rows * (2 * I > H ? 2 * I : H);
         total = 2 * h + up256(part);
     }
 };
@@ -264,7 +264,7 @@ TOVL_API int tovl_moe_decode_q4(tovl_handle h, const void* x, long long ldx, int
 TOVL_API long long tovl_matvec_q4_workspace(tovl_handle h, int T, int N)
 {
     if (!h || T < 0 || N < 1 || T > kMaxDecodeRows) return -1;
-    return up256(4LL * (most_parts(T) + 1) * T * N);
+    return up256(4LL * (most_parts(T) + 2) * T * N);
 }
 
 TOVL_API int tovl_matvec_q4(tovl_handle h, const void* x, int x_type, const float* x_scale, long long ldx, int T, int K,

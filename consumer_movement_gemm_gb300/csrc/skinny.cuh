@@ -41,12 +41,10 @@ namespace tovl {
 namespace skinny {
 
 constexpr int kTileCols = 512;
-constexpr int kRowsBf16 = 32;                     // rows of W in a unit
-constexpr int kRowsQ4 = 128;
-constexpr int kScaleBytes = 256;                  // scales of a 4-bit block (group >= 32)
-constexpr int kZeroBytes = 128;
-constexpr int kItemsPerCta = 8;                   // with tickets
-constexpr int kItemUnits = 12;                    // tickets are worth it from this many units an item
+constexpr int kScaleBytes = 512;                  // scales of a 4-bit block (group >= 32)
+constexpr int kZeroBytes = 256;
+constexpr int kItemsPerCta = 8;                   // small items of an even share, with tickets
+constexpr int kItemUnits = 96;                    // units of an even share from which tickets are worth it (32-row units)
 constexpr int kMaxItems = kMaxGrid * kItemsPerCta;
 
 // G: rows per scale (0: bf16 weights).
@@ -56,22 +54,21 @@ struct Shape {
     static constexpr int kWarps = Q4 ? 16 : 8;
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kCols = kTileCols / kWarps;          // columns of a warp
-    static constexpr int kRows = Q4 ? kRowsQ4 : kRowsBf16;    // rows of W in a block
-    static constexpr int kBlockBytes = Q4 ? 2048 : 4096;
+    static constexpr int kRows = Q4 ? 256 : 32;               // rows of W in a block: 4 KB
+    static constexpr int kBlockBytes = 4096;
     static constexpr int kMetaBytes = Q4 ? kScaleBytes + kZeroBytes : 0;
-    static constexpr int kStages = Q4 ? 4 : 5;                // 128 or 160 KB in flight per SM
+    static constexpr int kStages = Q4 ? 2 : 4;                // 128 KB in flight per SM
     static constexpr int kMT = kCols / 16;                    // 16-column accumulator tiles
     static constexpr int kRing = kWarps * kStages * (kBlockBytes + kMetaBytes + 8);   // 1 KB aligned
-    // rows that one pass over a matrix takes: 4-bit blocks keep the sums of a
-    // scale group beside the running ones
-    static constexpr int kPassRows = Q4 ? 32 : 64;
 };
 
-// Rows of x wait in shared memory in chunks of units: 16 KB (twice) of bf16
-// for NT * 8 rows, with their second parts (LO) behind them.
+// Rows of x wait in shared memory in chunks of units: 16 KB of bf16 for NT * 8
+// rows, with their second parts (LO) behind them; three chunks and a barrier
+// for each.
 constexpr int kChunkBytes = 16384;
-constexpr int kScalesOfChunk = 256;               // e4m3: a scale per row and unit
-constexpr int kRowBuffers = 2 * (kChunkBytes + kScalesOfChunk * 4);
+constexpr int kScalesOfChunk = 256;               // e4m3: a scale per row and 128 columns
+constexpr int kChunkStride = kChunkBytes + kScalesOfChunk * 4;
+constexpr int kRowBuffers = 3 * kChunkStride + 32;
 template <int G, int NT, bool LO>
 constexpr int chunk_units() { return kChunkBytes / (NT * 8 * (LO ? 2 : 1) * Shape<G>::kRows * 2); }
 
@@ -101,6 +98,11 @@ __device__ __forceinline__ uint2 ld_shared_u2(uint32_t addr)
     return v;
 }
 
+__device__ __forceinline__ void st_shared_f1(uint32_t addr, float v)
+{
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
 __device__ __forceinline__ uint32_t ld_shared_u1(uint32_t addr)
 {
     uint32_t v;
@@ -108,13 +110,55 @@ __device__ __forceinline__ uint32_t ld_shared_u1(uint32_t addr)
     return v;
 }
 
-__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z)
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z, uint64_t pol)
 {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
-        "[%2];" ::"r"(ptx::smem_u32(smem_dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(ptx::smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%3, %4, "
+        "%5}], [%2], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(pol)
         : "memory");
+}
+
+// mbarriers by shared address
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// Bounded wait (the CTA's own copies and warps; a bound against logic errors).
+__device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, const Ctrl& ctrl, long long timeout_ns)
+{
+    if (mbar_try(bar, parity)) return;
+    const uint64_t start = ptx::globaltimer();
+    for (uint32_t i = 1; !mbar_try(bar, parity); ++i) {
+        if ((i & 255) == 0 && ptx::globaltimer() - start > static_cast<uint64_t>(timeout_ns)) {
+            record_error(ctrl, kErrTimeout);
+            return;
+        }
+    }
 }
 
 // d += a x b: a 16 x 16 (rows: weight columns), b 16 x 8 (columns: tokens)
@@ -169,50 +213,44 @@ template <int G, bool Z>
 struct Ring {
     using P = Shape<G>;
     static constexpr int S = P::kStages;
-    uint8_t* w;          // this warp's stages
-    uint8_t* meta;
-    uint64_t* full;
-    int fill = 0;        // next stage to fill
-    int take = 0;        // next stage to read
+    uint32_t w, meta, full;    // this warp's stages and barriers (shared addresses)
+    int fill = 0;              // next stage to fill
+    int take = 0;              // next stage to read
     uint32_t parity = 0;
 
-    __device__ void init(uint8_t* smem, int warp)
+    __device__ void init(uint32_t smem, int warp)
     {
         w = smem + warp * S * P::kBlockBytes;
         meta = smem + P::kWarps * S * P::kBlockBytes + warp * S * P::kMetaBytes;
-        full = reinterpret_cast<uint64_t*>(smem + P::kWarps * S * (P::kBlockBytes + P::kMetaBytes)) + warp * S;
+        full = smem + P::kWarps * S * (P::kBlockBytes + P::kMetaBytes) + warp * S * 8;
     }
 
     __device__ void init_barriers()
     {
-        for (int s = 0; s < S; ++s) ptx::mbar_init(full + s, 1);
+        for (int s = 0; s < S; ++s) mbar_init(full + s * 8, 1);
     }
 
     // One lane: fetch the block at column n, weight row k of matrix e.
-    __device__ __forceinline__ void issue(const WeightMaps& m, int n, int k, int e)
+    __device__ __forceinline__ void issue(const WeightMaps* m, int n, int k, int e, uint64_t pol)
     {
-        uint8_t* dst = w + fill * P::kBlockBytes;
-        uint64_t* bar = full + fill;
+        const uint32_t dst = w + fill * P::kBlockBytes, bar = full + fill * 8;
         if constexpr (P::Q4) {
-            constexpr int kGroups = kRowsQ4 / G;
-            uint8_t* md = meta + fill * P::kMetaBytes;
-            ptx::mbar_arrive_expect_tx(bar, P::kBlockBytes + kGroups * P::kCols * (Z ? 3 : 2));
-            tma_load_3d(dst, &m.w, bar, n, k / 8, e);
-            tma_load_3d(md, &m.scale, bar, n, k / G, e);
-            if (Z) tma_load_3d(md + kScaleBytes, &m.zero, bar, n, k / G, e);
+            constexpr int kGroups = P::kRows / (G ? G : 1);
+            const uint32_t md = meta + fill * P::kMetaBytes;
+            mbar_expect(bar, P::kBlockBytes + kGroups * P::kCols * (Z ? 3 : 2));
+            tma_load_3d(dst, &m->w, bar, n, k / 8, e, pol);
+            tma_load_3d(md, &m->scale, bar, n, k / G, e, pol);
+            if (Z) tma_load_3d(md + kScaleBytes, &m->zero, bar, n, k / G, e, pol);
         } else {
-            ptx::mbar_arrive_expect_tx(bar, P::kBlockBytes);
-            tma_load_3d(dst, &m.w, bar, n, k, e);
+            mbar_expect(bar, P::kBlockBytes);
+            tma_load_3d(dst, &m->w, bar, n, k, e, pol);
         }
     }
     __device__ __forceinline__ void filled() { fill = fill + 1 == S ? 0 : fill + 1; }
 
-    __device__ __forceinline__ void wait(const Ctrl& ctrl, long long timeout_ns)
-    {
-        mbar_wait(full + take, parity, ctrl, timeout_ns);
-    }
-    __device__ __forceinline__ uint32_t block() const { return ptx::smem_u32(w + take * P::kBlockBytes); }
-    __device__ __forceinline__ uint32_t scales() const { return ptx::smem_u32(meta + take * P::kMetaBytes); }
+    __device__ __forceinline__ void wait(const Ctrl& ctrl, long long timeout_ns) { bar_wait(full + take * 8, parity, ctrl, timeout_ns); }
+    __device__ __forceinline__ uint32_t block() const { return w + take * P::kBlockBytes; }
+    __device__ __forceinline__ uint32_t scales() const { return meta + take * P::kMetaBytes; }
     __device__ __forceinline__ void taken()
     {
         if (++take == S) {
@@ -288,13 +326,13 @@ __device__ __forceinline__ void unpack(uint32_t (&p)[4], uint32_t word, uint32_t
     for (int i = 0; i < 4; ++i) p[i] = sub_bf16x2(((word >> (4 * i)) & 0x000f000fu) | 0x43004300u, zero2);
 }
 
-// acc[mt][nt] += a block of 128 x 32 4-bit weights in groups of G rows, with
+// acc[mt][nt] += half a block, 128 x 32 4-bit weights in groups of G rows, with
 // zeros (Z) or 8 for all.  sx: the tokens' activation scales (XS).  Lane group g owns four neighbouring
 // columns; the order 0 4 1 5 2 6 3 7 of the groups keeps the 16-byte reads of
 // a quarter warp in different banks.
 template <int NT, bool LO, bool XS, int G, bool Z>
 __device__ __forceinline__ void block_q4(float (&acc)[2][NT][4], const RowView& x, const float2 (&sx)[NT],
-                                         uint32_t block, uint32_t scales, int lane)
+                                         uint32_t block, uint32_t scales, uint32_t zeros, int lane)
 {
     constexpr int kSteps = G / 32;
     const int g = lane >> 2, t = lane & 3;
@@ -305,7 +343,7 @@ __device__ __forceinline__ void block_q4(float (&acc)[2][NT][4], const RowView& 
     for (int R = 0; R < 4; ++R) {
         const bool first = R % kSteps == 0, last = R % kSteps == kSteps - 1;
         if (first) {
-            const uint32_t zz = Z ? ld_shared_u1(scales + kScaleBytes + (R / kSteps) * 32 + 4 * c) : 0u;
+            const uint32_t zz = Z ? ld_shared_u1(zeros + (R / kSteps) * 32 + 4 * c) : 0u;
 #pragma unroll
             for (int i = 0; i < 4; ++i) z[i] = Z ? 0x43004300u + ((zz >> (8 * i)) & 0x7fu) * 0x00010001u : 0x43084308u;
         }
@@ -354,27 +392,44 @@ __device__ __forceinline__ void block_q4(float (&acc)[2][NT][4], const RowView& 
 }
 
 // ------------------------------------------------------------ items
-// One product: matrices x tiles of 512 columns x kb units along k.
+// One product: matrices x tiles of 512 columns x kb units along k.  Items 0 ..
+// grid - 1 are `big` units long, the ones behind them `small`.
 struct Product {
     int tiles, kb, total;      // tiles per matrix, units per tile, units
-    int per, items;            // units per item, items
+    int big, small, bigs;      // bigs: units of all big items
+    int items;
     bool tickets;
 
-    // most_parts: limit of kb / per, so that a tile has at most most_parts + 1 parts
+    // min_units: shortest item (a tile of kb units has kb / min_units + 2 parts at most)
     __device__ __forceinline__ void init(int matrices, int N, int K, int rows, int grid, int most_parts)
     {
         tiles = (N + kTileCols - 1) / kTileCols;
         kb = (K + rows - 1) / rows;
         total = matrices * tiles * kb;
-        per = (total + grid - 1) / grid;
-        tickets = per >= 2 * kItemUnits;
-        if (tickets) per = max((per + kItemsPerCta - 1) / kItemsPerCta, kItemUnits);
-        per = max(max(per, (kb + most_parts - 1) / most_parts), 1);
-        items = (total + per - 1) / per;
+        const int share = (total + grid - 1) / grid, least = (kb + most_parts - 1) / most_parts;
+        tickets = share * rows >= kItemUnits * 32 && share > least;
+        big = max(tickets ? share - share / 4 : share, max(least, 1));
+        small = max((share + kItemsPerCta - 1) / kItemsPerCta, max(least, 1));
+        bigs = min(grid * big, total);
+        tickets = tickets && bigs < total;
+        items = tickets ? grid + (total - bigs + small - 1) / small : (total + big - 1) / big;
+    }
+    __device__ __forceinline__ int item_of(int unit) const
+    {
+        return unit < bigs ? unit / big : static_cast<int>(gridDim.x) + (unit - bigs) / small;
+    }
+    __device__ __forceinline__ int begin(int item) const
+    {
+        const int grid = gridDim.x;
+        return item < grid ? min(item * big, total) : bigs + (item - grid) * small;
+    }
+    __device__ __forceinline__ int end(int item) const
+    {
+        const int grid = gridDim.x;
+        return min(item < grid ? min((item + 1) * big, bigs) : bigs + (item - grid + 1) * small, total);
     }
     // parts of the tile whose units start at t0
-    __device__ __forceinline__ int first_item(int t0) const { return t0 / per; }
-    __device__ __forceinline__ int parts(int t0) const { return (t0 + kb - 1) / per - t0 / per + 1; }
+    __device__ __forceinline__ int parts(int t0) const { return item_of(t0 + kb - 1) - item_of(t0) + 1; }
 };
 
 // The items that a CTA works on, in order; shared by its warps.  Entry 0 is
@@ -427,16 +482,31 @@ __device__ __forceinline__ void grid_barrier(int* counter, int target, const Ctr
     __syncthreads();
 }
 
-// Adds `n` parts, `stride` floats apart, of four neighbouring columns.
-__device__ __forceinline__ float4 add_parts(const float* part, int n, long long stride)
+// Adds the parts of M sums of four neighbouring columns: sum m has n[m] parts,
+// `stride` floats apart from part[m] on.  Four parts of every sum are in
+// flight together: the sums are short and the latency is long.
+template <int M>
+__device__ __forceinline__ void add_parts(float4 (&s)[M], const float* const (&part)[M], const int (&n)[M], long long stride)
 {
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(part + i * stride));
-        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    int most = 0;
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+        s[m] = make_float4(0.f, 0.f, 0.f, 0.f);
+        most = max(most, n[m]);
     }
-    return s;
+    for (int i = 0; i < most; i += 4) {
+        float4 v[M][4];
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (i + u < n[m]) v[m][u] = __ldcg(reinterpret_cast<const float4*>(part[m] + (i + u) * stride));
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (i + u < n[m]) s[m].x += v[m][u].x, s[m].y += v[m][u].y, s[m].z += v[m][u].z, s[m].w += v[m][u].w;
+    }
 }
 
 // The engine of one warp.  `Calls` provides, for product `ph` (0 or 1):
@@ -448,7 +518,6 @@ struct Engine {
     const Calls& c;
     const Product* pr;         // the call's products, in shared memory
     Queue* queue;
-    uint8_t* rows_buf;         // kRowBuffers bytes
     int* tickets;              // global counters, one per product
     const Ctrl& ctrl;
     long long timeout_ns;
@@ -459,6 +528,10 @@ struct Engine {
     // item still to fetch, place of the next one
     int ph = 0, n = 0, left = 0, i = 0, tile = 0, matrix = 0;
     int kb = 0, tiles = 0;     // of the product
+    uint64_t pol = 0;          // weights are read once: they leave the L2 to the parts and the rows
+    uint32_t rows_buf;         // kRowBuffers bytes (shared address): chunks of rows
+    uint32_t chunk_bars;       // their barriers
+    uint32_t buf_now = 0, buf_parity = 0;
 
     // Goes on to item n of the product; left stays 0 where there is none.
     __device__ __forceinline__ void open()
@@ -471,8 +544,8 @@ struct Engine {
             if (n == 0) queue[ph].item[1] = static_cast<uint16_t>(min(atomicAdd(tickets + ph * kSyncStep, 1) + grid, q.items));
             queue[ph].item[n + 2] = static_cast<uint16_t>(min(atomicAdd(tickets + ph * kSyncStep, 1) + grid, q.items));
         }
-        const int b = id * q.per;
-        left = min(q.per, q.total - b);
+        const int b = q.begin(id);
+        left = q.end(id) - b;
         kb = q.kb;
         tiles = q.tiles;
         const int at = b / kb;
@@ -493,7 +566,7 @@ struct Engine {
                 n = 0;
             }
         }
-        if (lane == 0) ring.issue(c.maps(ph), tile * kTileCols + warp * P::kCols, i * P::kRows, c.expert(ph, matrix));
+        if (lane == 0) ring.issue(c.maps(ph), tile * kTileCols + warp * P::kCols, i * P::kRows, c.expert(ph, matrix), pol);
         ring.filled();
         --left;
         if (++i == kb) {
@@ -502,6 +575,21 @@ struct Engine {
                 tile = 0;
                 ++matrix;
             }
+        }
+    }
+
+    // Before the first barrier of the CTA.
+    __device__ __forceinline__ void init(uint8_t* smem, uint8_t* rows)
+    {
+        pol = ptx::l2_policy(1);
+        rows_buf = ptx::smem_u32(rows);
+        chunk_bars = rows_buf + 3 * kChunkStride;
+        ring.init(ptx::smem_u32(smem), warp);
+        if (lane == 0) {
+            ring.init_barriers();
+            if (warp == 0)
+                for (int b = 0; b < 3; ++b) mbar_init(chunk_bars + b * 8, P::kWarps);
+            ptx::fence_mbar_init();
         }
     }
 
@@ -514,17 +602,19 @@ struct Engine {
     // Whole CTA.  Sums over k units [i0, i1) of a tile for `rows` <= NT * 8
     // rows, written to part[row][n], rows `ld` floats apart (n0: the tile's
     // first column, N: the matrix').  octet(r, k, lo) gives 8 values of row r
-    // from column k on (k < K), as bf16; scale(r, i) the row's scale in unit i
-    // (XS).  The rows go through shared memory in chunks, once per CTA; the
-    // next chunk is on its way to registers while one is multiplied.
+    // from column k on (k < K), as bf16; scale(r, k) the row's scale there (XS).
+    //  The rows go through shared memory in chunks, once per CTA; the
+    // next chunk is in registers while one is multiplied.
     template <int NT, bool LO, bool XS, class F, class S>
     __device__ __forceinline__ void segment(int i0, int i1, float* part, long long ld, int rows, int n0, int N, int K, F octet,
                                             S scale)
     {
         constexpr int kUnits = chunk_units<G, NT, LO>();
+        static_assert(kUnits >= 1, "rows of one unit fit a chunk");
         constexpr int kOctets = kUnits * P::kRows / 8;                 // of a row in a chunk
         constexpr int kPitch = kOctets * 16;
         constexpr int kPer = kChunkBytes / 16 / P::kThreads;           // octets of a thread
+        constexpr int kScales = XS ? kUnits * P::kRows / kXScaleGroup : 1;   // of a row in a chunk
         float acc[P::kMT][NT][4];
 #pragma unroll
         for (int mt = 0; mt < P::kMT; ++mt)
@@ -538,69 +628,86 @@ struct Engine {
         float next_scale = 0.f;
         // this thread's octets of the chunk that starts at unit u
         const auto get = [&](int u) {
+            const int k0 = u * P::kRows, k1 = min(K, i1 * P::kRows);
 #pragma unroll
             for (int x = 0; x < kPer; ++x) {
-                const int at = tid + x * P::kThreads, r = at / kOctets, k = u * P::kRows + (at % kOctets) * 8;
+                const int at = tid + x * P::kThreads, r = at / kOctets, k = k0 + (at % kOctets) * 8;
                 const int row = LO ? r % (NT * 8) : r;
                 next[x] = make_uint4(0, 0, 0, 0);     // (rows of W past the last one are zeros; so must these be)
-                if (row < rows && k < K) next[x] = octet(row, k, LO && r >= NT * 8);
+                if (row < rows && k < k1) next[x] = octet(row, k, LO && r >= NT * 8);
             }
-            if (XS && tid < kUnits * NT * 8) {
-                const int r = tid / kUnits, v = u + tid % kUnits;
-                next_scale = r < rows && v < i1 ? scale(r, v) : 0.f;
+            if (XS && tid < kScales * NT * 8) {
+                const int r = tid / kScales, k = k0 + tid % kScales * kXScaleGroup;
+                next_scale = r < rows && k < k1 ? scale(r, k) : 0.f;
             }
         };
-        const auto put = [&](uint8_t* buf) {
+        // writes them to buffer c and counts this warp's arrival there
+        const auto put = [&](uint32_t c) {
+            const uint32_t buf = rows_buf + c * kChunkStride;
 #pragma unroll
             for (int x = 0; x < kPer; ++x) {
                 const int at = tid + x * P::kThreads, r = at / kOctets, o = at % kOctets;
-                *reinterpret_cast<uint4*>(buf + r * kPitch + ((o ^ ((r & 1) << 2)) << 4)) = next[x];
+                ptx::st_shared_v4(buf + r * kPitch + ((o ^ ((r & 1) << 2)) << 4), next[x].x, next[x].y, next[x].z, next[x].w);
             }
-            if (XS && tid < kUnits * NT * 8) reinterpret_cast<float*>(buf + kChunkBytes)[tid] = next_scale;
+            if (XS && tid < kScales * NT * 8) st_shared_f1(buf + kChunkBytes + tid * 4, next_scale);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(chunk_bars + c * 8);
         };
-        uint8_t* buf = rows_buf;
-        uint8_t* other = rows_buf + kRowBuffers / 2;
+        // Three buffers in turn.  Chunk c + 1 is written when chunk c begins,
+        // into the buffer of chunk c - 2: every warp has arrived at chunk c
+        // (the writer has just waited for that), which it does not before it
+        // has begun c - 1 and so finished c - 2.  (A segment's first chunk is
+        // written when the last one of the segment before it is finished, later
+        // still.)  A warp may run a whole chunk ahead of another.
         get(i0);
-        __syncthreads();       // the segment before this one has read both buffers
-        put(buf);
+        put(buf_now);
+        if (i0 + kUnits < i1) get(i0 + kUnits);
         for (int u = i0; u < i1; u += kUnits) {
-            __syncthreads();   // this chunk is complete, the other buffer has been read
-            if (u + kUnits < i1) get(u + kUnits);
-            const uint32_t base = ptx::smem_u32(buf) + g * kPitch;
+            bar_wait(chunk_bars + buf_now * 8, buf_parity, ctrl, timeout_ns);
+            const uint32_t buf = rows_buf + buf_now * kChunkStride;
+            if (++buf_now == 3) {
+                buf_now = 0;
+                buf_parity ^= 1;
+            }
+            if (u + kUnits < i1) {
+                put(buf_now);
+                if (u + 2 * kUnits < i1) get(u + 2 * kUnits);
+            }
+            const uint32_t base = buf + g * kPitch;
             RowView x;
             x.tokens8 = 8 * kPitch;
             x.second = NT * 8 * kPitch;
             const int end = min(kUnits, i1 - u);
 #pragma unroll 1
             for (int v = 0; v < end; ++v) {
-                // (a bf16 unit is half of a 128-byte row of octets)
-                const uint32_t at = base + (Q4 ? v * 256 : (v >> 1) * 128);
-                x.even = at + ((t ^ ((g & 1) << 2)) << 4);
-                x.odd = at + (((t + 4) ^ ((g & 1) << 2)) << 4);
                 ring.wait(ctrl, timeout_ns);
                 if constexpr (Q4) {
-                    float2 sx[NT];
-                    if (XS) {
-                        const float* sc = reinterpret_cast<const float*>(buf + kChunkBytes) + v;
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            sx[nt].x = sc[(nt * 8 + 2 * t) * kUnits];
-                            sx[nt].y = sc[(nt * 8 + 2 * t + 1) * kUnits];
+                    for (int s = 0; s < 2; ++s) {
+                        const uint32_t row = base + (v * 2 + s) * 256;
+                        x.even = row + ((t ^ ((g & 1) << 2)) << 4);
+                        x.odd = row + (((t + 4) ^ ((g & 1) << 2)) << 4);
+                        float2 sx[NT];
+                        if (XS) {
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                const uint32_t sc = buf + kChunkBytes + ((nt * 8 + 2 * t) * kScales + v * 2 + s) * 4;
+                                sx[nt].x = __uint_as_float(ld_shared_u1(sc));
+                                sx[nt].y = __uint_as_float(ld_shared_u1(sc + kScales * 4));
+                            }
                         }
+                        block_q4<NT, LO, XS, G, Z>(acc, x, sx, ring.block() + s * 2048, ring.scales() + s * (128 / G) * 64,
+                                                   ring.scales() + kScaleBytes + s * (128 / G) * 32, lane);
                     }
-                    block_q4<NT, LO, XS, G, Z>(acc, x, sx, ring.block(), ring.scales(), lane);
                 } else {
-                    if (v & 1) x.even = x.odd;
+                    // (a bf16 unit is half of a 128-byte row of octets)
+                    x.even = base + (v >> 1) * 128 + (((t + 4 * (v & 1)) ^ ((g & 1) << 2)) << 4);
                     block_bf16<NT, LO>(acc, x, 0, ring.block(), lane);
                 }
                 ring.taken();
                 __syncwarp();      // every lane has read the stage before it is filled again
                 fetch();
             }
-            if (u + kUnits < i1) put(other);
-            uint8_t* b = buf;
-            buf = other;
-            other = b;
         }
         n0 += warp * P::kCols;
 #pragma unroll
@@ -636,12 +743,12 @@ struct Engine {
         for (int n = 0;; ++n) {
             const int id = item_at(q, queue[p], n, ctrl, timeout_ns);
             if (id >= q.items) return;
-            int b = id * q.per;
-            const int e = min(b + q.per, q.total);
+            int b = q.begin(id);
+            const int e = q.end(id);
             while (b < e) {
                 const int tile = b / q.kb, t0 = tile * q.kb, end = min(t0 + q.kb, e);
                 const int matrix = tile / q.tiles;
-                f(matrix, tile - matrix * q.tiles, b - t0, end - t0, id - q.first_item(t0));
+                f(matrix, tile - matrix * q.tiles, b - t0, end - t0, id - q.item_of(t0));
                 b = end;
             }
         }
