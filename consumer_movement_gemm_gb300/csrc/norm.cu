@@ -7,7 +7,7 @@
 //
 // One pass over memory: a row stays in registers from the load to the last
 // store, everything is fp32 in between.  Rows up to 1024 elements take a warp
-// each (no barrier), longer ones a CTA each (one barrier).  A thread holds
+// each (no barrier), longer ones a CTA each (one barrier a reduction).  A thread holds
 // groups of 8 consecutive elements, so a scale group of 32, 64 or 128 columns
 // is 4, 8 or 16 neighbouring lanes.
 #include <cuda_bf16.h>
@@ -51,7 +51,7 @@ __device__ __forceinline__ void load8(float (&v)[8], const __nv_bfloat16* p, int
 {
     if constexpr (W == 8) {
         if (n <= 0) return;
-        const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+        const uint4 u = __ldcg(reinterpret_cast<const uint4*>(p));
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -63,7 +63,7 @@ __device__ __forceinline__ void load8(float (&v)[8], const __nv_bfloat16* p, int
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (2 * i < n) {
-                const float2 f = unpack2(__ldg(reinterpret_cast<const uint32_t*>(p) + i));
+                const float2 f = unpack2(__ldcg(reinterpret_cast<const uint32_t*>(p) + i));
                 v[2 * i] = f.x;
                 v[2 * i + 1] = f.y;
             }
@@ -79,13 +79,13 @@ __device__ __forceinline__ void load8(float (&v)[8], const float* p, int n)
 {
     if constexpr (W == 8) {
         if (n <= 0) return;
-        const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+        const float4 a = __ldcg(reinterpret_cast<const float4*>(p)), b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
         v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
         v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < n) v[i] = __ldg(p + i);
+            if (i < n) v[i] = __ldcg(p + i);
     }
 }
 
@@ -164,7 +164,142 @@ __device__ __forceinline__ float row_reduce(float v, float* buf, bool warp_row)
     return v;
 }
 
-// RES: 0 none, 1 bf16, 2 fp32.  VPT: groups of 8 elements per thread.
+// e4m3 of eight elements from column c on in a group of 32, 64 or 128 columns
+// (4, 8 or 16 neighbouring lanes; whole warps call it).
+template <int W>
+__device__ __forceinline__ void store_group(const NormParams& p, int c, const float (&v)[8], float m, float* scale, uint8_t* q)
+{
+    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    if (p.group > 32) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 4));
+    if (p.group > 64) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 8));
+    m = max_nan(m, kMinAmax);
+    if (c % p.group == 0 && c < p.H) scale[c / p.group] = m / kE4m3Max;
+    store8_e4m3<W>(q + c, v, kE4m3Max / m, p.H - c);
+}
+
+// Sixteen-byte pieces of a row as they come from memory.
+template <int RES>
+struct Raw {
+    uint4 x, r0, r1;      // r1: fp32 residuals only
+};
+
+__device__ __forceinline__ void unpack8(float (&v)[8], const uint4& u)
+{
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack2(w[i]);
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
+}
+
+// Rows of whole 16-byte pieces.  Every CTA (or warp, WARP) goes through rows a
+// grid apart; the next row's loads are issued before this row is reduced, so
+// the memory system never waits for the reduction, and the weights stay in
+// registers.  RES: 0 none, 1 bf16, 2 fp32.  VPT: groups of 8 elements per
+// thread.
+template <int VPT, int RES, bool WARP>
+__global__ void __launch_bounds__(WARP ? kWarpRows * 32 : 512, VPT <= 2 ? 2 : 1) norm_rows_kernel(const NormParams p)
+{
+    __shared__ float sum_buf[2][32], max_buf[2][32];
+    const long long rows_step = static_cast<long long>(gridDim.x) * (WARP ? kWarpRows : 1);
+    long long row = WARP ? static_cast<long long>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+    const int tid = WARP ? threadIdx.x & 31 : threadIdx.x;
+    const int step = (WARP ? 32 : blockDim.x) * 8;
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    if (row >= p.T) return;     // whole warps (WARP), or whole CTAs
+    uint4 weight[VPT];
+    Raw<RES> next[VPT];
+    // (not through the read-only path: the outputs may lie where the inputs do)
+    const auto fetch = [&](long long r) {
+        const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x) + r * p.ldx;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int c = tid * 8 + j * step;
+            next[j].x = next[j].r0 = next[j].r1 = make_uint4(0, 0, 0, 0);
+            if (c >= p.H) continue;
+            next[j].x = __ldcg(reinterpret_cast<const uint4*>(x + c));
+            if (RES == 1) next[j].r0 = __ldcg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.residual) + r * p.ldr + c));
+            if (RES == 2) {
+                const uint4* f = reinterpret_cast<const uint4*>(static_cast<const float*>(p.residual) + r * p.ldr + c);
+                next[j].r0 = __ldcg(f);
+                next[j].r1 = __ldcg(f + 1);
+            }
+        }
+    };
+    fetch(row);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int c = tid * 8 + j * step;
+        weight[j] = make_uint4(0, 0, 0, 0);
+        if (c < p.H) weight[j] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.weight) + c));
+    }
+    for (int turn = 0; row < p.T; row += rows_step, turn ^= 1) {
+        float v[VPT][8], ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int c = tid * 8 + j * step;
+            unpack8(v[j], next[j].x);
+            if (RES == 1) {
+                float o[8];
+                unpack8(o, next[j].r0);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[j][i] += o[i];
+                store8<8>(static_cast<__nv_bfloat16*>(p.residual_out) + row * p.ldr + c, v[j], p.H - c);
+            }
+            if (RES == 2) {
+                const uint32_t o[8] = {next[j].r0.x, next[j].r0.y, next[j].r0.z, next[j].r0.w,
+                                       next[j].r1.x, next[j].r1.y, next[j].r1.z, next[j].r1.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[j][i] += __uint_as_float(o[i]);
+                store8<8>(static_cast<float*>(p.residual_out) + row * p.ldr + c, v[j], p.H - c);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss = fmaf(v[j][i], v[j][i], ss);
+        }
+        if (row + rows_step < p.T) fetch(row + rows_step);
+        ss = row_reduce<false>(ss, sum_buf[turn], WARP);
+        const float inv_rms = rsqrtf(ss / p.H + p.eps);
+        float amax[VPT];
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            float g[8];
+            unpack8(g, weight[j]);
+            amax[j] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[j][i] = v[j][i] * inv_rms * g[i];
+                amax[j] = max_nan(amax[j], fabsf(v[j][i]));
+            }
+            const int c = tid * 8 + j * step;
+            if (c >= p.H) amax[j] = 0.f;       // (zeros times an infinite 1 / rms)
+            if (p.out) store8<8>(static_cast<__nv_bfloat16*>(p.out) + row * p.ldo + c, v[j], p.H - c);
+        }
+        if (!p.q) continue;
+        float* scale = p.q_scale + row * p.n_groups;
+        uint8_t* q = p.q + row * p.H;
+        if (p.group == p.H) {
+            float m = amax[0];
+#pragma unroll
+            for (int j = 1; j < VPT; ++j) m = max_nan(m, amax[j]);
+            m = max_nan(row_reduce<true>(m, max_buf[turn], WARP), kMinAmax);
+            if (tid == 0) scale[0] = m / kE4m3Max;
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int c = tid * 8 + j * step;
+                store8_e4m3<8>(q + c, v[j], kE4m3Max / m, p.H - c);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) store_group<8>(p, tid * 8 + j * step, v[j], amax[j], scale, q);
+        }
+    }
+}
+
+// Rows of any length and alignment, moved in pairs or single elements.
 template <int W, int VPT, int RES>
 __global__ void __launch_bounds__(1024) norm_kernel(const NormParams p, int warp_row)
 {
@@ -250,56 +385,83 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormParams p, int warp
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int c = tid * 8 + j * step;
-            float m = amax[j];
-            m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            if (p.group > 32) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 4));
-            if (p.group > 64) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 8));
-            m = max_nan(m, kMinAmax);
-            if (c % p.group == 0 && c < p.H) scale[c / p.group] = m / kE4m3Max;
-            store8_e4m3<W>(q + c, v[j], kE4m3Max / m, p.H - c);
-        }
+        for (int j = 0; j < VPT; ++j) store_group<W>(p, tid * 8 + j * step, v[j], amax[j], scale, q);
     }
 }
 
-template <int W, int VPT>
-cudaError_t launch(const NormParams& p, const cudaLaunchConfig_t& lc, int warp_row)
+// f(residual kind)
+template <class F>
+cudaError_t by_residual(const NormParams& p, F f)
 {
-    if (!p.residual) return cudaLaunchKernelEx(&lc, norm_kernel<W, VPT, 0>, p, warp_row);
-    if (!p.residual_f32) return cudaLaunchKernelEx(&lc, norm_kernel<W, VPT, 1>, p, warp_row);
-    return cudaLaunchKernelEx(&lc, norm_kernel<W, VPT, 2>, p, warp_row);
+    if (!p.residual) return f(std::integral_constant<int, 0>());
+    if (!p.residual_f32) return f(std::integral_constant<int, 1>());
+    return f(std::integral_constant<int, 2>());
+}
+
+template <int VPT, bool WARP>
+cudaError_t launch_rows(const NormParams& p, cudaLaunchConfig_t lc, int num_sms)
+{
+    return by_residual(p, [&](auto res) {
+        const auto kernel = norm_rows_kernel<VPT, decltype(res)::value, WARP>;
+        const int threads = static_cast<int>(lc.blockDim.x);
+        // as many CTAs as the SMs hold at once
+        int per_sm = 0;
+        cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0);
+        if (e != cudaSuccess) return e;
+        const int most = num_sms * (per_sm > 0 ? per_sm : 1), rows = WARP ? kWarpRows : 1;
+        const int want = (p.T + rows - 1) / rows;
+        lc.gridDim = dim3(want < most ? want : most);
+        return cudaLaunchKernelEx(&lc, kernel, p);
+    });
+}
+
+template <int W, int VPT>
+cudaError_t launch_any(const NormParams& p, const cudaLaunchConfig_t& lc, int warp_row)
+{
+    return by_residual(p, [&](auto res) { return cudaLaunchKernelEx(&lc, norm_kernel<W, VPT, decltype(res)::value>, p, warp_row); });
 }
 
 template <int W>
-cudaError_t launch(const NormParams& p, const cudaLaunchConfig_t& lc, int warp_row, int vpt)
+cudaError_t launch_any(const NormParams& p, const cudaLaunchConfig_t& lc, int warp_row, int vpt)
 {
-    if (vpt <= 1) return launch<W, 1>(p, lc, warp_row);
-    if (vpt <= 2) return launch<W, 2>(p, lc, warp_row);
-    return launch<W, 4>(p, lc, warp_row);
+    if (vpt <= 1) return launch_any<W, 1>(p, lc, warp_row);
+    if (vpt <= 2) return launch_any<W, 2>(p, lc, warp_row);
+    return launch_any<W, 4>(p, lc, warp_row);
 }
+
+int up32(int n) { return (n + 31) / 32 * 32; }
 
 }  // namespace
 
-cudaError_t launch_norm(const NormParams& p, int width, cudaStream_t stream, bool pdl)
+cudaError_t launch_norm(const NormParams& p, int width, int num_sms, cudaStream_t stream, bool pdl)
 {
     const int vecs = (p.H + 7) / 8;
     const int warp_row = p.H <= kWarpRowMax;
-    int vpt = warp_row ? (vecs + 31) / 32 : (vecs + 1023) / 1024;
-    if (vpt == 3) vpt = 4;
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(warp_row ? (p.T + kWarpRows - 1) / kWarpRows : p.T);
-    lc.blockDim = dim3(warp_row ? kWarpRows * 32 : ((vecs + vpt - 1) / vpt + 31) / 32 * 32);
     lc.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = attr;
     lc.numAttrs = pdl ? 1 : 0;
-    if (width == 8) return launch<8>(p, lc, warp_row, vpt);
-    if (width == 2) return launch<2>(p, lc, warp_row, vpt);
-    return launch<1>(p, lc, warp_row, vpt);
+    if (width == 8) {
+        if (warp_row) {
+            lc.blockDim = dim3(kWarpRows * 32);
+            if (vecs <= 32) return launch_rows<1, true>(p, lc, num_sms);
+            if (vecs <= 64) return launch_rows<2, true>(p, lc, num_sms);
+            return launch_rows<4, true>(p, lc, num_sms);
+        }
+        const int vpt = vecs <= 1024 ? 2 : vecs <= 2048 ? 4 : 8;
+        lc.blockDim = dim3(up32((vecs + vpt - 1) / vpt));
+        if (vpt == 2) return launch_rows<2, false>(p, lc, num_sms);
+        if (vpt == 4) return launch_rows<4, false>(p, lc, num_sms);
+        return launch_rows<8, false>(p, lc, num_sms);
+    }
+    int vpt = warp_row ? (vecs + 31) / 32 : (vecs + 1023) / 1024;
+    if (vpt == 3) vpt = 4;
+    lc.gridDim = dim3(warp_row ? (p.T + kWarpRows - 1) / kWarpRows : p.T);
+    lc.blockDim = dim3(warp_row ? kWarpRows * 32 : up32((vecs + vpt - 1) / vpt));
+    return width == 2 ? launch_any<2>(p, lc, warp_row, vpt) : launch_any<1>(p, lc, warp_row, vpt);
 }
 
 }  // namespace tovl

@@ -150,7 +150,7 @@ TOVL_API int tovl_add_rmsnorm(tovl_handle h, const void* x, long long ldx, const
     const int width = fits(8) ? 8 : fits(2) ? 2 : 1;
     DeviceGuard g(h->device);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return run(h, s, "norm launch", [&](bool pdl) { return launch_norm(p, width, s, pdl); });
+    return run(h, s, "norm launch", [&](bool pdl) { return launch_norm(p, width, h->num_sms, s, pdl); });
 }
 
 TOVL_API int tovl_route_topk(tovl_handle h, const void* logits, int type, long long ld, int T, int E, int k,
