@@ -403,12 +403,10 @@ cudaError_t launch_rows(const NormParams& p, cudaLaunchConfig_t lc, int num_sms)
 {
     return by_residual(p, [&](auto res) {
         const auto kernel = norm_rows_kernel<VPT, decltype(res)::value, WARP>;
+        // about as many CTAs as the SMs hold at once (64, 128 and up to 176 registers a thread)
         const int threads = static_cast<int>(lc.blockDim.x);
-        // as many CTAs as the SMs hold at once
-        int per_sm = 0;
-        cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0);
-        if (e != cudaSuccess) return e;
-        const int most = num_sms * (per_sm > 0 ? per_sm : 1), rows = WARP ? kWarpRows : 1;
+        const int per_sm = WARP ? (VPT == 1 ? 3 : VPT == 2 ? 2 : 1) : (VPT <= 2 ? 1024 : 512) / threads;
+        const int most = num_sms * per_sm, rows = WARP ? kWarpRows : 1;
         const int want = (p.T + rows - 1) / rows;
         lc.gridDim = dim3(want < most ? want : most);
         return cudaLaunchKernelEx(&lc, kernel, p);

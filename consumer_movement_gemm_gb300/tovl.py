@@ -171,46 +171,59 @@ def _stream(stream) -> int:
     return stream.cuda_stream
 
 
-_RESIDUAL_TYPES = {"torch.bfloat16": TOVL_BF16, "torch.float32": TOVL_F32}
-_ROW_TYPES = {"torch.bfloat16": TOVL_BF16, "torch.float8_e4m3fn": TOVL_E4M3}
+# element types of the decode-step calls by torch dtype, filled in by the
+# first such call (importing this module does not import torch)
+_types = {}
+_BF16 = _F32 = _E4M3 = _I32 = _U8 = None
 
 
-def _type_of(name, t, types) -> int:
-    code = types.get(str(t.dtype))
-    if code is None:
-        raise TypeError(f"{name} must be one of {', '.join(types)}, not {t.dtype}")
+def _load_types():
+    global _BF16, _F32, _E4M3, _I32, _U8
+    import torch
+    _BF16, _F32, _E4M3, _I32, _U8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.int32, torch.uint8
+    _types.update({_BF16: TOVL_BF16, _F32: TOVL_F32, _E4M3: TOVL_E4M3})
+
+
+def _type_of(name, t, allowed) -> int:
+    code = _types.get(t.dtype)
+    if code not in allowed:
+        raise TypeError(f"{name} must not be {t.dtype}")
     return code
 
 
-def _want(name, t, dtype, shape):
-    if t is None or str(t.dtype) != "torch." + dtype or t.shape != shape:
+def _matrix(name, t, dtype, rows, cols) -> int:
+    """Checks a [rows, cols] tensor whose rows are contiguous; returns the distance of its rows in elements."""
+    if t is None or t.dtype is not dtype or t.shape != (rows, cols):
+        raise TypeError(f"{name} must be {dtype} ({rows}, {cols})")
+    s = t.stride()
+    if s[1] != 1 and cols > 1:
+        raise TypeError(f"{name} must have unit stride in its last dimension")
+    return s[0] if rows > 1 else (cols + 15) // 16 * 16    # (one row: any distance will do)
+
+
+def _dense(name, t, dtype, shape):
+    """Checks a contiguous tensor; returns its address."""
+    if t is None or t.dtype is not dtype or t.shape != shape:
         raise TypeError(f"{name} must be {dtype} {shape}")
-
-
-def _want_q4(name, w, E, K, N, group):
-    """A packed matrix (words, scales, zeros or None), stacked E times where E is not None."""
-    lead = () if E is None else (E,)
-    if group not in (32, 64, 128) or K % group:
-        raise TypeError(f"{name}: groups are 32, 64 or 128 rows and divide K")
-    for part, t, dtype, rows in ((" words", w[0], "int32", K // 8), (" scales", w[1], "bfloat16", K // group),
-                                 (" zeros", w[2], "uint8", K // group)):
-        if t is not None or part != " zeros":
-            _want(name + part, t, dtype, lead + (rows, N))
-            _dense(name + part, t)
-
-
-def _dense(name, t):
     if not t.is_contiguous():
         raise TypeError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _rows(name, t, shape) -> int:
-    """Distance of a matrix's rows in elements; its rows must be contiguous."""
-    if t.shape != shape:
-        raise TypeError(f"{name} must have shape {shape}")
-    if shape[1] > 1 and t.stride(1) != 1:
-        raise TypeError(f"{name} must have unit stride in its last dimension")
-    return t.stride(0) if shape[0] > 1 else -(-shape[1] // 16) * 16    # (one row: any distance will do)
+def _bytes(name, t) -> int:
+    if not t.is_contiguous():
+        raise TypeError(f"{name} must be contiguous")
+    return t.numel() * t.element_size()
+
+
+def _packed(name, w, lead, K, N, group):
+    """Checks a packed matrix (words, scales, zeros or None), stacked where lead is (E,); returns its addresses."""
+    if group not in (32, 64, 128) or K % group:
+        raise TypeError(f"{name}: groups are 32, 64 or 128 rows and divide K")
+    words, scales, zeros = w
+    return (_dense(name + " words", words, _I32, lead + (K // 8, N)),
+            _dense(name + " scales", scales, _BF16, lead + (K // group, N)),
+            None if zeros is None else _dense(name + " zeros", zeros, _U8, lead + (K // group, N)))
 
 
 def default_config(device: int = 0) -> tovl_config:
@@ -318,39 +331,42 @@ class Handle:
         """``r = x + residual``, ``y = r * rsqrt(mean(r^2) + eps) * weight``: ``residual_out`` = r, ``out`` = y in bf16,
         ``q`` = y in e4m3 with ``q_scale`` [T, ceil(H/group)] (one scale per row with ``group=0``).  Tensors may be
         slices with unit stride in the last dimension (``q`` and ``q_scale`` contiguous)."""
+        if _BF16 is None:
+            _load_types()
         T, H = x.shape
-        _want("x", x, "bfloat16", (T, H))
-        _want("weight", weight, "bfloat16", (H,))
-        rt = ldr = 0
+        ldx = _matrix("x", x, _BF16, T, H)
+        res = res_out = q_ptr = s_ptr = out_ptr = None
+        rt = ldr = ldo = 0
         if residual is not None:
-            rt = _type_of("residual", residual, _RESIDUAL_TYPES)
-            ldr = _rows("residual", residual, (T, H))
-            if residual_out is None or residual_out.dtype != residual.dtype or _rows("residual_out", residual_out, (T, H)) != ldr:
-                raise TypeError("residual_out must have the type, shape and strides of residual")
-        ldo = 0
+            rt = _type_of("residual", residual, (TOVL_BF16, TOVL_F32))
+            ldr = _matrix("residual", residual, residual.dtype, T, H)
+            if _matrix("residual_out", residual_out, residual.dtype, T, H) != ldr:
+                raise TypeError("residual_out must have the strides of residual")
+            res, res_out = residual.data_ptr(), residual_out.data_ptr()
         if out is not None:
-            _want("out", out, "bfloat16", (T, H))
-            ldo = _rows("out", out, (T, H))
+            ldo = _matrix("out", out, _BF16, T, H)
+            out_ptr = out.data_ptr()
         if q is not None:
-            _want("q", q, "float8_e4m3fn", (T, H))
-            _want("q_scale", q_scale, "float32", (T, -(-H // group) if group else 1))
-            _dense("q", q), _dense("q_scale", q_scale)
-        rc = load().tovl_add_rmsnorm(self.h, _ptr(x), _rows("x", x, (T, H)), _ptr(residual),
-                                     None if residual is None else _ptr(residual_out), rt, ldr, _ptr(weight), eps, T, H,
-                                     _ptr(out), ldo, _ptr(q), _ptr(q_scale), group, _stream(stream))
-        _check(self.h, rc, "tovl_add_rmsnorm")
+            q_ptr = _dense("q", q, _E4M3, (T, H))
+            s_ptr = _dense("q_scale", q_scale, _F32, (T, -(-H // group) if group else 1))
+        rc = (_lib or load()).tovl_add_rmsnorm(self.h, x.data_ptr(), ldx, res, res_out, rt, ldr,
+                                               _dense("weight", weight, _BF16, (H,)), eps, T, H, out_ptr, ldo, q_ptr, s_ptr,
+                                               group, _stream(stream))
+        if rc:
+            _check(self.h, rc, "tovl_add_rmsnorm")
 
     def route_topk(self, logits, topk, gate_w, renormalize=True, stream=None):
         """The k experts of each token (``topk`` int32 [T, k], -1 where none is left) and their softmax weights."""
+        if _BF16 is None:
+            _load_types()
         T, E = logits.shape
         k = topk.shape[1]
-        _want("topk", topk, "int32", (T, k))
-        _want("gate_w", gate_w, "float32", (T, k))
-        _dense("topk", topk), _dense("gate_w", gate_w)
-        rc = load().tovl_route_topk(self.h, _ptr(logits), _type_of("logits", logits, _RESIDUAL_TYPES),
-                                    _rows("logits", logits, (T, E)), T, E, k, 1 if renormalize else 0, _ptr(topk),
-                                    _ptr(gate_w), _stream(stream))
-        _check(self.h, rc, "tovl_route_topk")
+        rc = (_lib or load()).tovl_route_topk(self.h, logits.data_ptr(), _type_of("logits", logits, (TOVL_BF16, TOVL_F32)),
+                                              _matrix("logits", logits, logits.dtype, T, E), T, E, k, 1 if renormalize else 0,
+                                              _dense("topk", topk, _I32, (T, k)), _dense("gate_w", gate_w, _F32, (T, k)),
+                                              _stream(stream))
+        if rc:
+            _check(self.h, rc, "tovl_route_topk")
 
     def moe_decode_workspace(self, T: int, k: int, H: int, I: int) -> int:
         """Bytes of workspace of ``moe_decode`` and ``moe_decode_q4``."""
@@ -359,41 +375,35 @@ class Handle:
             raise TovlError(TOVL_ERR_UNSUPPORTED, "tovl_moe_decode_workspace")
         return n
 
-    def _moe_args(self, x, topk, gate_w, out):
-        T, H = x.shape
-        k = topk.shape[1]
-        _want("x", x, "bfloat16", (T, H))
-        _want("topk", topk, "int32", (T, k))
-        _want("gate_w", gate_w, "float32", (T, k))
-        _want("out", out, "bfloat16", (T, H))
-        _dense("topk", topk), _dense("gate_w", gate_w)
-        return T, H, k, _rows("x", x, (T, H)), _rows("out", out, (T, H))
-
     def moe_decode(self, x, topk, gate_w, W13, W2, out, workspace, stream=None):
         """The gated expert layer for up to 64 tokens: W13 [E, H, 2I] (gate columns, then up columns), W2 [E, I, H]."""
-        T, H, k, ldx, ldo = self._moe_args(x, topk, gate_w, out)
+        if _BF16 is None:
+            _load_types()
+        T, H = x.shape
+        k = topk.shape[1]
         E, I = W2.shape[0], W2.shape[1]
-        _want("W13", W13, "bfloat16", (E, H, 2 * I))
-        _want("W2", W2, "bfloat16", (E, I, H))
-        _dense("W13", W13), _dense("W2", W2), _dense("workspace", workspace)
-        rc = load().tovl_moe_decode(self.h, _ptr(x), ldx, T, H, _ptr(topk), _ptr(gate_w), k, E, _ptr(W13), _ptr(W2), I,
-                                    _ptr(out), ldo, _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                    _stream(stream))
-        _check(self.h, rc, "tovl_moe_decode")
+        rc = (_lib or load()).tovl_moe_decode(
+            self.h, x.data_ptr(), _matrix("x", x, _BF16, T, H), T, H, _dense("topk", topk, _I32, (T, k)),
+            _dense("gate_w", gate_w, _F32, (T, k)), k, E, _dense("W13", W13, _BF16, (E, H, 2 * I)),
+            _dense("W2", W2, _BF16, (E, I, H)), I, out.data_ptr(), _matrix("out", out, _BF16, T, H), workspace.data_ptr(),
+            _bytes("workspace", workspace), _stream(stream))
+        if rc:
+            _check(self.h, rc, "tovl_moe_decode")
 
     def moe_decode_q4(self, x, topk, gate_w, W13, W2, group, out, workspace, stream=None):
         """``moe_decode`` with packed experts: W13 and W2 are (words, scales, zeros or None) as ``quantize_q4`` makes."""
-        T, H, k, ldx, ldo = self._moe_args(x, topk, gate_w, out)
-        q13, s13, z13 = W13
-        q2, s2, z2 = W2
-        E, I = q2.shape[0], q2.shape[1] * 8
-        _want_q4("W13", W13, E, H, 2 * I, group)
-        _want_q4("W2", W2, E, I, H, group)
-        _dense("workspace", workspace)
-        rc = load().tovl_moe_decode_q4(self.h, _ptr(x), ldx, T, H, _ptr(topk), _ptr(gate_w), k, E, _ptr(q13), _ptr(s13),
-                                       _ptr(z13), _ptr(q2), _ptr(s2), _ptr(z2), group, I, _ptr(out), ldo,
-                                       _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
-        _check(self.h, rc, "tovl_moe_decode_q4")
+        if _BF16 is None:
+            _load_types()
+        T, H = x.shape
+        k = topk.shape[1]
+        E, I = W2[0].shape[0], W2[0].shape[1] * 8
+        rc = (_lib or load()).tovl_moe_decode_q4(
+            self.h, x.data_ptr(), _matrix("x", x, _BF16, T, H), T, H, _dense("topk", topk, _I32, (T, k)),
+            _dense("gate_w", gate_w, _F32, (T, k)), k, E, *_packed("W13", W13, (E,), H, 2 * I, group),
+            *_packed("W2", W2, (E,), I, H, group), group, I, out.data_ptr(), _matrix("out", out, _BF16, T, H),
+            workspace.data_ptr(), _bytes("workspace", workspace), _stream(stream))
+        if rc:
+            _check(self.h, rc, "tovl_moe_decode_q4")
 
     def matvec_q4_workspace(self, T: int, N: int) -> int:
         """Bytes of workspace of ``matvec_q4``."""
@@ -405,29 +415,27 @@ class Handle:
     def matvec_q4(self, x, wq, w_scale, group, out, workspace, zero=None, x_scale=None, stream=None):
         """``out = x @ W`` for up to 64 rows and a packed matrix W [K, N]; x bf16, or e4m3 with ``x_scale``
         [T, ceil(K/128)]."""
+        if _BF16 is None:
+            _load_types()
         T, K = x.shape
         N = wq.shape[1]
-        xt = _type_of("x", x, _ROW_TYPES)
+        xt = _type_of("x", x, (TOVL_BF16, TOVL_E4M3))
         if (xt == TOVL_E4M3) != (x_scale is not None):
             raise TypeError("x_scale goes with e4m3 rows, and only with them")
-        if x_scale is not None:
-            _want("x_scale", x_scale, "float32", (T, -(-K // 128)))
-            _dense("x_scale", x_scale)
-        _want_q4("wq", (wq, w_scale, zero), None, K, N, group)
-        _want("out", out, "bfloat16", (T, N))
-        _dense("workspace", workspace)
-        rc = load().tovl_matvec_q4(self.h, _ptr(x), xt, _ptr(x_scale), _rows("x", x, (T, K)), T, K, _ptr(wq),
-                                   _ptr(w_scale), _ptr(zero), group, N, _ptr(out), _rows("out", out, (T, N)),
-                                   _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
-        _check(self.h, rc, "tovl_matvec_q4")
+        rc = (_lib or load()).tovl_matvec_q4(
+            self.h, x.data_ptr(), xt, None if x_scale is None else _dense("x_scale", x_scale, _F32, (T, -(-K // 128))),
+            _matrix("x", x, x.dtype, T, K), T, K, *_packed("wq", (wq, w_scale, zero), (), K, N, group), group, N,
+            out.data_ptr(), _matrix("out", out, _BF16, T, N), workspace.data_ptr(), _bytes("workspace", workspace),
+            _stream(stream))
+        if rc:
+            _check(self.h, rc, "tovl_matvec_q4")
 
     def quantize_q4(self, W, group=128, zeros=False, stream=None):
         """Packs bf16 W [E, K, N] or [K, N]: (words int32 [.., K/8, N], scales bf16 [.., K/group, N], zeros uint8 or
         None)."""
         import torch
-        _dense("W", W)
-        if W.dtype != torch.bfloat16 or W.dim() not in (2, 3):
-            raise TypeError("W must be a bfloat16 matrix or a stack of them")
+        if W.dtype != torch.bfloat16 or W.dim() not in (2, 3) or not W.is_contiguous():
+            raise TypeError("W must be a contiguous bfloat16 matrix or a stack of them")
         lead, (K, N) = tuple(W.shape[:-2]), W.shape[-2:]
         words = torch.empty(*lead, K // 8, N, dtype=torch.int32, device=W.device)
         scale = torch.empty(*lead, K // group, N, dtype=torch.bfloat16, device=W.device)
