@@ -3,9 +3,10 @@
 //
 //   out[t][n] = sum_g scale[g][n] * sum_{k in g} xs[t][k / 128] * x[t][k] * (nibble[k][n] - zero[g][n])
 //
-// Products of bf16 (or e4m3, exact in bf16) activations with the integers
-// nibble - zero are exact, a group's sum is fp32, and the scales multiply it
-// in fp32: nothing is rounded before the result.  The stream of weight blocks
+// The activations enter the tensor core as fp16 (e4m3 exactly, bf16 with a
+// power of two per 128 columns), their products with the integers nibble -
+// zero are exact, a group's sum is fp32, and the scales multiply it in fp32:
+// nothing is rounded before the result.  The stream of weight blocks
 // and the split are skinny.cuh's; every 32 rows are a pass over the weights
 // (one pass is the next one's matrix, so large matrices are read again).
 #include <type_traits>
@@ -17,11 +18,12 @@ namespace tovl {
 namespace {
 
 using namespace skinny;
-constexpr int kPassRows = 32;
+constexpr int kPassRows = 16;
 constexpr int kThreads4 = Shape<128>::kThreads;
 
 struct Tables {
     Product pr;
+    int last;
     Queue queue;
 };
 
@@ -41,14 +43,13 @@ __device__ __forceinline__ void run_segment(const MatvecParams& p, Engine<G, Z, 
 {
     const int n_xs = (p.K + kXScaleGroup - 1) / kXScaleGroup;
     float* part = p.part + (static_cast<long long>(number) * p.T + r0) * p.N;
-    eng.template segment<NT, false, XS>(
+    eng.template segment<NT, XS ? Rows::kE4m3 : Rows::kBf16>(
         i0, i1, part, p.N, cnt, tile * kTileCols, p.N, p.K,
         [&](int r, int k, bool) {
             const long long at = (r0 + r) * p.ldx + k;
             if (!XS) return __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.x) + at));
             const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.x) + at));
-            const uint2 lo = e4m3x4_to_bf16(v.x), hi = e4m3x4_to_bf16(v.y);
-            return make_uint4(lo.x, lo.y, hi.x, hi.y);
+            return make_uint4(v.x, v.y, 0, 0);
         },
         [&](int r, int k) { return __ldg(p.x_scale + static_cast<long long>(r0 + r) * n_xs + k / kXScaleGroup); });
 }
@@ -72,7 +73,7 @@ __global__ void __launch_bounds__(Shape<G>::kThreads, 1) matvec_q4_kernel(const 
     }
     const int grid = gridDim.x;
     const int passes = (p.T + kPassRows - 1) / kPassRows;      // as matrices of the product
-    if (threadIdx.x == 0) tb.pr.init(passes, p.N, p.K, P::kRows, grid, p.most_parts);
+    if (threadIdx.x == 0) tb.pr.init(passes, p.N, p.K, P::kRows, P::kUnitBytes, grid, p.most_parts);
     for (int i = threadIdx.x; i < kMaxItems + 8; i += P::kThreads) tb.queue.item[i] = kNoItem;
     __syncthreads();
     ptx::grid_dep_wait();
@@ -81,30 +82,44 @@ __global__ void __launch_bounds__(Shape<G>::kThreads, 1) matvec_q4_kernel(const 
     eng.walk(0, [&](int matrix, int tile, int i0, int i1, int number) {
         const int r0 = matrix * kPassRows, cnt = min(kPassRows, p.T - r0);
         if (cnt <= 8) run_segment<1, XS, G, Z>(p, eng, r0, cnt, tile, i0, i1, number);
-        else if (cnt <= 16) run_segment<2, XS, G, Z>(p, eng, r0, cnt, tile, i0, i1, number);
-        else run_segment<4, XS, G, Z>(p, eng, r0, cnt, tile, i0, i1, number);
-    });
-    grid_barrier(p.sync + kBarrierWord, grid, p.ctrl, p.timeout_ns);
-    const int quads = p.N / 4;
-    for (int i = blockIdx.x * P::kThreads + threadIdx.x; i < p.T * quads; i += grid * P::kThreads) {
-        const int t = i / quads, n = (i - t * quads) * 4;
-        const int t0 = (t / kPassRows * tb.pr.tiles + n / kTileCols) * tb.pr.kb;
-        const float* const part[1] = {p.part + static_cast<long long>(t) * p.N + n};
-        const int count[1] = {tb.pr.parts(t0)};
-        float4 sums[1];
-        add_parts<1>(sums, part, count, static_cast<long long>(p.T) * p.N);
-        const float4 s = sums[0];
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + t * p.ldo + n;
-        if (p.out_vec) {
-            *reinterpret_cast<uint2*>(out) = make_uint2(ptx::pack_bf16x2(s.x, s.y), ptx::pack_bf16x2(s.z, s.w));
-        } else {
-            out[0] = __float2bfloat16(s.x), out[1] = __float2bfloat16(s.y);
-            out[2] = __float2bfloat16(s.z), out[3] = __float2bfloat16(s.w);
+        else run_segment<2, XS, G, Z>(p, eng, r0, cnt, tile, i0, i1, number);
+        // the last CTA to finish a part of the tile adds them all (no CTA
+        // waits for another one, so none has to be resident)
+        const int t0 = (matrix * tb.pr.tiles + tile) * tb.pr.kb, parts = tb.pr.parts(t0);
+        __syncthreads();
+        if (parts > 1) {
+            if (threadIdx.x == 0) {
+                __threadfence();
+                int* counter = p.sync + kPartWord + tb.pr.item_of(t0);
+                const bool last = ptx::atom_add_acq_rel_gpu(counter, 1) == parts - 1;
+                if (last) ptx::st_relaxed_gpu(counter, 0);
+                tb.last = last;
+                __threadfence();
+            }
+            __syncthreads();
+            if (!tb.last) return;
         }
+        const int quads = min(kTileCols, p.N - tile * kTileCols) / 4;
+        for (int i = threadIdx.x; i < cnt * quads; i += P::kThreads) {
+            const int r = i / quads, n = tile * kTileCols + (i - r * quads) * 4;
+            const float* const part[1] = {p.part + static_cast<long long>(r0 + r) * p.N + n};
+            const int count[1] = {parts};
+            float4 s[1];
+            add_parts<1>(s, part, count, static_cast<long long>(p.T) * p.N);
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (r0 + r) * p.ldo + n;
+            if (p.out_vec) {
+                *reinterpret_cast<uint2*>(out) = make_uint2(ptx::pack_bf16x2(s[0].x, s[0].y), ptx::pack_bf16x2(s[0].z, s[0].w));
+            } else {
+                out[0] = __float2bfloat16(s[0].x), out[1] = __float2bfloat16(s[0].y);
+                out[2] = __float2bfloat16(s[0].z), out[3] = __float2bfloat16(s[0].w);
+            }
+        }
+    });
+    // the last CTA to leave clears the tickets for the next call
+    if (tb.pr.tickets && threadIdx.x == 0 && ptx::atom_add_relaxed_gpu(p.sync + kExitWord, 1) == grid - 1) {
+        ptx::st_relaxed_gpu(p.sync + kTicketWord, 0);
+        ptx::st_relaxed_gpu(p.sync + kExitWord, 0);
     }
-    // the last CTA past the barrier clears the counters for the next call
-    if (threadIdx.x == 0 && ptx::atom_add_relaxed_gpu(p.sync + kExitWord, 1) == grid - 1)
-        for (int i = 0; i < kSyncWords; i += kSyncStep) ptx::st_relaxed_gpu(p.sync + i, 0);
 }
 
 // One thread per column and group: the group's range gives scale and zero,
@@ -179,10 +194,10 @@ cudaError_t prepare_matvec_q4()
 }
 
 cudaError_t launch_matvec_q4(const MatvecParams& p, bool e4m3, int group, bool zero, int grid, cudaStream_t stream,
-                             bool cooperative, bool pdl)
+                             bool pdl)
 {
     return with_kernel(e4m3, group, zero, [&](auto kernel, int smem) {
-        return launch_grid(kernel, p, grid, kThreads4, smem, stream, cooperative, pdl);
+        return launch_grid(kernel, p, grid, kThreads4, smem, stream, false, pdl);
     });
 }
 

@@ -12,10 +12,12 @@
 // listed, each with the tokens that name it as its rows.
 //
 // Roundings: x and the weights are bf16 (or 4-bit with their scales applied
-// in fp32), sums are fp32.  h is split into two bf16 numbers, its rounding
-// and the rest, and the second product multiplies both (the second one rides
-// on the same weight fragments): one bf16 h would raise the error of the
-// result from its own rounding's 1.7e-3 to 2.4e-3, the pair leaves it alone.
+// in fp32), sums are fp32.  With bf16 weights h is split into two bf16
+// numbers, its rounding and the rest, and the second product multiplies both
+// (the second one rides on the same weight fragments): one bf16 h would raise
+// the error of the result from its own rounding's 1.7e-3 to 2.4e-3, the pair
+// leaves it alone.  With 4-bit weights h is fp16 with a power of two per 128
+// columns: 2^-12 of rounding, a hundredth of the result's own error.
 #include <type_traits>
 #include "launch.cuh"
 #include "skinny.cuh"
@@ -55,8 +57,7 @@ struct Building {
 static_assert(sizeof(Building) <= kRowBuffers, "the tables' scratch fits the row buffers");
 
 // Rows of an expert that one entry takes: 4-bit blocks keep the sums of a
-// scale group beside the running ones, and both parts of 32 rows of h would
-// not fit a chunk.
+// scale group beside the running ones.
 constexpr int pass_rows(int group) { return group ? 16 : 64; }
 
 template <int G>
@@ -173,17 +174,21 @@ struct Worker {
         const int cnt = entry_rows(en), off = entry_off(en);
         const int K = H ? p.I : p.H, N = H ? p.H : 2 * p.I;
         float* part = p.part + (static_cast<long long>(number) * p.T * p.k + off) * N;
-        eng.template segment<NT, H, false>(
+        constexpr Rows kind = !H ? Rows::kBf16 : G ? Rows::kHalf : Rows::kPair;
+        eng.template segment<NT, kind>(
             i0, i1, part, N, cnt, tile * kTileCols, N, K,
             [&](int r, int k, bool lo) {
                 if (H) {     // (written in this launch)
-                    const __nv_bfloat16* h = static_cast<const __nv_bfloat16*>(lo ? p.h_lo : p.h_hi);
+                    const uint16_t* h = static_cast<const uint16_t*>(lo ? p.h_lo : p.h_hi);
                     return __ldcg(reinterpret_cast<const uint4*>(h + static_cast<long long>(off + r) * p.I + k));
                 }
                 return __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.x) + tb.row_tok[off + r] * p.ldx + k));
             },
-            [](int, int) { return 1.f; });
+            [&](int r, int k) { return __ldcg(static_cast<const float*>(p.h_lo) + (off + r) * scale_groups() + k / kXScaleGroup); });
     }
+
+    // 4-bit weights: h_lo holds the scales of h, fp32 [row][ceil(I / 128)]
+    __device__ __forceinline__ int scale_groups() const { return (p.I + kXScaleGroup - 1) / kXScaleGroup; }
 
     template <bool H>
     __device__ __forceinline__ void product()
@@ -208,30 +213,47 @@ struct Worker {
         return p.part + static_cast<long long>(row) * N + n;
     }
 
+    // A warp takes 128 columns of a row at a time, a lane four.
     __device__ __forceinline__ void activations()
     {
-        const int quads = p.I / 4;
+        const int groups = scale_groups();
         const long long stride = static_cast<long long>(p.T) * p.k * 2 * p.I;
-        for (int i = blockIdx.x * P::kThreads + threadIdx.x; i < tb.n_rows * quads; i += gridDim.x * P::kThreads) {
-            const int row = i / quads, n = (i - row * quads) * 4;
+        const int lane = threadIdx.x & 31;
+        for (int i = spread_thread() >> 5; i < tb.n_rows * groups; i += gridDim.x * P::kWarps) {
+            const int row = i / groups, n = (i - row * groups) * kXScaleGroup + lane * 4;
+            const bool in = n < p.I;
             int count[2];
-            const float* part[2] = {parts(0, row, n, 2 * p.I, count[0]), parts(0, row, p.I + n, 2 * p.I, count[1])};
+            const float* part[2] = {parts(0, row, in ? n : 0, 2 * p.I, count[0]), parts(0, row, p.I + (in ? n : 0), 2 * p.I, count[1])};
             float4 s[2];
             add_parts<2>(s, part, count, stride);
             const float g[4] = {s[0].x, s[0].y, s[0].z, s[0].w}, u[4] = {s[1].x, s[1].y, s[1].z, s[1].w};
-            float hi[4], lo[4];
+            float h[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float h = g[j] / (1.f + expf(-g[j])) * u[j];
-                hi[j] = __bfloat162float(__float2bfloat16(h));
-                // (an overflowed h has no second part)
-                lo[j] = fabsf(h - hi[j]) < INFINITY ? h - hi[j] : 0.f;
-            }
+            for (int j = 0; j < 4; ++j) h[j] = in ? g[j] / (1.f + expf(-g[j])) * u[j] : 0.f;
             const long long at = static_cast<long long>(row) * p.I + n;
-            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.h_hi) + at) =
-                make_uint2(ptx::pack_bf16x2(hi[0], hi[1]), ptx::pack_bf16x2(hi[2], hi[3]));
-            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.h_lo) + at) =
-                make_uint2(ptx::pack_bf16x2(lo[0], lo[1]), ptx::pack_bf16x2(lo[2], lo[3]));
+            if constexpr (G != 0) {
+                uint32_t e = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) e = max(e, (__float_as_uint(h[j]) >> 23) & 255u);
+                e = __reduce_max_sync(0xffffffffu, e);
+                const float f = half_scale(e);
+                if (in)
+                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.h_hi) + at) =
+                        make_uint2(pack_h2(h[0] * f, h[1] * f), pack_h2(h[2] * f, h[3] * f));
+                if (lane == 0) static_cast<float*>(p.h_lo)[i] = half_unscale(e);
+            } else if (in) {
+                float hi[4], lo[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    hi[j] = __bfloat162float(__float2bfloat16(h[j]));
+                    // (an overflowed h has no second part)
+                    lo[j] = fabsf(h[j] - hi[j]) < INFINITY ? h[j] - hi[j] : 0.f;
+                }
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.h_hi) + at) =
+                    make_uint2(ptx::pack_bf16x2(hi[0], hi[1]), ptx::pack_bf16x2(hi[2], hi[3]));
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.h_lo) + at) =
+                    make_uint2(ptx::pack_bf16x2(lo[0], lo[1]), ptx::pack_bf16x2(lo[2], lo[3]));
+            }
         }
     }
 
@@ -239,7 +261,7 @@ struct Worker {
     {
         const int quads = p.H / 4;
         const long long stride = static_cast<long long>(p.T) * p.k * p.H;
-        for (int i = blockIdx.x * P::kThreads + threadIdx.x; i < p.T * quads; i += gridDim.x * P::kThreads) {
+        for (int i = spread_thread(); i < p.T * quads; i += gridDim.x * P::kThreads) {
             const int t = i / quads, n = (i - t * quads) * 4;
             float4 out4 = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int j = 0; j < p.k; j += 2) {      // two slots' parts together
@@ -303,7 +325,8 @@ __global__ void __launch_bounds__(Shape<G>::kThreads, 1) moe_decode_kernel(const
         return;
     }
     if (threadIdx.x < 2)
-        tb.pr[threadIdx.x].init(tb.n_entries, threadIdx.x ? p.H : 2 * p.I, threadIdx.x ? p.I : p.H, P::kRows, grid, p.most_parts);
+        tb.pr[threadIdx.x].init(tb.n_entries, threadIdx.x ? p.H : 2 * p.I, threadIdx.x ? p.I : p.H, P::kRows, P::kUnitBytes, grid,
+                               p.most_parts);
     __syncthreads();
     eng.start();
     build_pairs<P::kThreads>(p, tb, bd);
@@ -318,7 +341,7 @@ __global__ void __launch_bounds__(Shape<G>::kThreads, 1) moe_decode_kernel(const
     w.outputs();
     // the last CTA past the last barrier clears the counters for the next call
     if (threadIdx.x == 0 && ptx::atom_add_relaxed_gpu(p.sync + kExitWord, 1) == grid - 1)
-        for (int i = 0; i < kSyncWords; i += kSyncStep) ptx::st_relaxed_gpu(p.sync + i, 0);
+        for (int i = 0; i <= kExitWord; i += kSyncStep) ptx::st_relaxed_gpu(p.sync + i, 0);
 }
 
 }  // namespace

@@ -14,14 +14,15 @@ constexpr int kMaxTopk = 32;           // experts per token of one route_topk ca
 constexpr int kXScaleGroup = 128;      // columns per scale of 8-bit activations
 
 // Counters of the streamed products (handle-owned, zero between calls), each
-// in a 128-byte line of its own: tickets of up to two products, arrivals of up
-// to three grid barriers, CTAs past the last one.
+// of the first six in a 128-byte line of its own: tickets of up to two
+// products, arrivals of three grid barriers, CTAs past the last one.
 constexpr int kMaxGrid = 160;
 constexpr int kSyncStep = 32;
 constexpr int kTicketWord = 0;         // tickets of product i at word i * kTicketStep
 constexpr int kBarrierWord = 2 * kSyncStep;
 constexpr int kExitWord = 5 * kSyncStep;
-constexpr int kSyncWords = 6 * kSyncStep;
+constexpr int kPartWord = 6 * kSyncStep;                 // arrivals at a cut tile, by its first item (matvec_q4)
+constexpr int kSyncWords = kPartWord + kMaxGrid * 8;
 
 enum : int { kTypeBf16 = 0, kTypeF32 = 1, kTypeE4m3 = 2 };
 
@@ -69,8 +70,8 @@ struct MoeParams {
     long long ldo;
     int out_vec;            // rows of out allow 8-byte stores
     int most_parts;         // a tile is cut into most_parts + 2 parts at most
-    void* h_hi;             // bf16 [T*k][I]: activations between the two products, and
-    void* h_lo;             // what their rounding to bf16 left over
+    void* h_hi;             // activations between the two products [T*k][I]: bf16, and
+    void* h_lo;             // what the rounding left over; 4-bit weights: fp16, and its scales
     float* part;            // [most_parts + 2][T*k][2I or H] parts of the products
     int T, k, E, H, I;
     int* sync;              // kSyncWords counters
@@ -99,7 +100,7 @@ struct MatvecParams {
 };
 cudaError_t prepare_matvec_q4();
 cudaError_t launch_matvec_q4(const MatvecParams& p, bool e4m3, int group, bool zero, int grid, cudaStream_t stream,
-                             bool cooperative, bool pdl);
+                             bool pdl);
 
 // One persistent grid whose CTAs meet at barriers.
 template <class Kernel, class Params>

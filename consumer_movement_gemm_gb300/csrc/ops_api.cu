@@ -304,7 +304,7 @@ TOVL_API int tovl_matvec_q4(tovl_handle h, const void* x, int x_type, const floa
     p.ctrl = h->ctrl;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     return run(h, s, "4-bit product launch",
-               [&](bool pdl) { return launch_matvec_q4(p, x_type == TOVL_E4M3, group, w_zero != nullptr, h->num_sms, s, h->coop_enabled, pdl); });
+               [&](bool pdl) { return launch_matvec_q4(p, x_type == TOVL_E4M3, group, w_zero != nullptr, h->num_sms, s, pdl); });
 }
 
 TOVL_API int tovl_quantize_q4(tovl_handle h, const void* W, int E, int K, int N, int group, void* wq, void* w_scale,

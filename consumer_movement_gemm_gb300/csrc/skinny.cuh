@@ -44,7 +44,7 @@ constexpr int kTileCols = 512;
 constexpr int kScaleBytes = 512;                  // scales of a 4-bit block (group >= 32)
 constexpr int kZeroBytes = 256;
 constexpr int kItemsPerCta = 8;                   // small items of an even share, with tickets
-constexpr int kItemUnits = 96;                    // units of an even share from which tickets are worth it (32-row units)
+constexpr int kTicketBytes = 3 << 20;             // an even share of the weights from which tickets are worth it
 constexpr int kMaxItems = kMaxGrid * kItemsPerCta;
 
 // G: rows per scale (0: bf16 weights).
@@ -56,6 +56,7 @@ struct Shape {
     static constexpr int kCols = kTileCols / kWarps;          // columns of a warp
     static constexpr int kRows = Q4 ? 256 : 32;               // rows of W in a block: 4 KB
     static constexpr int kBlockBytes = 4096;
+    static constexpr int kUnitBytes = kBlockBytes * kWarps;
     static constexpr int kMetaBytes = Q4 ? kScaleBytes + kZeroBytes : 0;
     static constexpr int kStages = Q4 ? 2 : 4;                // 128 KB in flight per SM
     static constexpr int kMT = kCols / 16;                    // 16-column accumulator tiles
@@ -69,6 +70,14 @@ constexpr int kChunkBytes = 16384;
 constexpr int kScalesOfChunk = 256;               // e4m3: a scale per row and 128 columns
 constexpr int kChunkStride = kChunkBytes + kScalesOfChunk * 4;
 constexpr int kRowBuffers = 3 * kChunkStride + 32;
+
+// What the rows of a product are.
+enum class Rows {
+    kBf16,      // bf16; with 4-bit weights turned into fp16 with a power of two per 128 columns
+    kPair,      // bf16 and what its rounding left over, bf16 (bf16 weights only)
+    kHalf,      // fp16 with a scale per 128 columns (4-bit weights only)
+    kE4m3       // e4m3 with a scale per 128 columns (4-bit weights only)
+};
 template <int G, int NT, bool LO>
 constexpr int chunk_units() { return kChunkBytes / (NT * 8 * (LO ? 2 : 1) * Shape<G>::kRows * 2); }
 
@@ -171,39 +180,77 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// d = a x b
-__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                          uint32_t b1)
+// The same in fp16.
+__device__ __forceinline__ void mma_h(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1)
 {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// d = a x b
+__device__ __forceinline__ void mma_h_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                            uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%10, %10, %10, %10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b)
+__device__ __forceinline__ uint32_t sub_h2(uint32_t a, uint32_t b)
 {
-    const __nv_bfloat162 d = __hsub2(reinterpret_cast<const __nv_bfloat162&>(a), reinterpret_cast<const __nv_bfloat162&>(b));
-    return reinterpret_cast<const uint32_t&>(d);
+    uint32_t d;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t fma_h2(uint32_t a, uint32_t b, uint32_t c)
+{
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi)
+{
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
-// Four e4m3 values as two bf16 pairs (exact: 4 significant bits, exponents
-// from -9 to 8).
-__device__ __forceinline__ uint2 e4m3x4_to_bf16(uint32_t v)
+// Four e4m3 values as two fp16 pairs (exact).
+__device__ __forceinline__ uint2 e4m3x4_to_half(uint32_t v)
 {
-    uint32_t h0, h1;
+    uint2 h;
     asm("{.reg .b16 l, h;\n\t"
         "mov.b32 {l, h}, %2;\n\t"
         "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
         "cvt.rn.f16x2.e4m3x2 %1, h;}"
-        : "=r"(h0), "=r"(h1)
+        : "=r"(h.x), "=r"(h.y)
         : "r"(v));
-    const float2 a = __half22float2(reinterpret_cast<const __half2&>(h0));
-    const float2 b = __half22float2(reinterpret_cast<const __half2&>(h1));
-    return make_uint2(ptx::pack_bf16x2(a.x, a.y), ptx::pack_bf16x2(b.x, b.y));
+    return h;
+}
+
+// The power of two that brings numbers of largest exponent field e (bf16, 0
+// to 255) below 2^15, and its inverse.  In fp16 so scaled, a bf16 number keeps
+// all its bits down to 2^-32 of the largest, and what a smaller one loses is
+// 2^-40 of the largest: nothing beside the fp32 sums' own 2^-24.
+__device__ __forceinline__ float half_scale(uint32_t e) { return __uint_as_float(min(268u - e, 253u) << 23); }
+__device__ __forceinline__ float half_unscale(uint32_t e) { return __uint_as_float((254u - min(268u - e, 253u)) << 23); }
+
+// Largest exponent field of eight bf16 numbers.
+__device__ __forceinline__ uint32_t max_exponent(const uint4& u)
+{
+    const uint32_t m = 0x7f807f80u;
+    const uint32_t a = max((u.x & m) >> 16, (u.y & m) >> 16), b = max((u.z & m) >> 16, (u.w & m) >> 16);
+    const uint32_t c = max(u.x & 0x7f80u, u.y & 0x7f80u), d = max(u.z & 0x7f80u, u.w & 0x7f80u);
+    return max(max(a, b), max(c, d)) >> 7;
 }
 
 // ------------------------------------------------------------ the warp's ring
@@ -316,21 +363,26 @@ __device__ __forceinline__ void block_bf16(float (&acc)[4][NT][4], const RowView
         }
 }
 
-// The four bf16 pairs (nibble - zero) of a packed word, rows in order.
-// 0x4300 | nibble is the bf16 number 128 + nibble, and 128 + zero is one too,
-// so the difference is exact; the scale is applied to the fp32 sum of the
-// group, so no weight is rounded.
-__device__ __forceinline__ void unpack(uint32_t (&p)[4], uint32_t word, uint32_t zero2)
+// The four fp16 pairs (nibble - zero) of a packed word, rows in order.  fp16
+// has room for two nibbles in its fraction: 0x6400 | n is 1024 + n and
+// 0x6400 | 16 n is 1024 + 16 n, so one shift serves four pairs; subtracting
+// 1024 + zero, or 64 + zero after a sixteenth, is exact.  The scale is applied
+// to the fp32 sum of the group: no weight is rounded.
+// z0: 1024 + zero, z1: -(64 + zero), in both halves.
+__device__ __forceinline__ void unpack(uint32_t (&p)[4], uint32_t word, uint32_t z0, uint32_t z1)
 {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = sub_bf16x2(((word >> (4 * i)) & 0x000f000fu) | 0x43004300u, zero2);
+    const uint32_t high = word >> 8, sixteenth = 0x2c002c00u;
+    p[0] = sub_h2((word & 0x000f000fu) | 0x64006400u, z0);
+    p[1] = fma_h2((word & 0x00f000f0u) | 0x64006400u, sixteenth, z1);
+    p[2] = sub_h2((high & 0x000f000fu) | 0x64006400u, z0);
+    p[3] = fma_h2((high & 0x00f000f0u) | 0x64006400u, sixteenth, z1);
 }
 
 // acc[mt][nt] += half a block, 128 x 32 4-bit weights in groups of G rows, with
-// zeros (Z) or 8 for all.  sx: the tokens' activation scales (XS).  Lane group g owns four neighbouring
-// columns; the order 0 4 1 5 2 6 3 7 of the groups keeps the 16-byte reads of
-// a quarter warp in different banks.
-template <int NT, bool LO, bool XS, int G, bool Z>
+// zeros (Z) or 8 for all.  sx: the tokens' activation scales.  Lane group g
+// owns four neighbouring columns; the order 0 4 1 5 2 6 3 7 of the groups
+// keeps the 16-byte reads of a quarter warp in different banks.
+template <int NT, int G, bool Z>
 __device__ __forceinline__ void block_q4(float (&acc)[2][NT][4], const RowView& x, const float2 (&sx)[NT],
                                          uint32_t block, uint32_t scales, uint32_t zeros, int lane)
 {
@@ -338,41 +390,38 @@ __device__ __forceinline__ void block_q4(float (&acc)[2][NT][4], const RowView& 
     const int g = lane >> 2, t = lane & 3;
     const int c = (g >> 1) | ((g & 1) << 2);
     float part[2][NT][4];
-    uint32_t z[4];
+    uint32_t z0[4], z1[4];
 #pragma unroll
     for (int R = 0; R < 4; ++R) {
         const bool first = R % kSteps == 0, last = R % kSteps == kSteps - 1;
         if (first) {
             const uint32_t zz = Z ? ld_shared_u1(zeros + (R / kSteps) * 32 + 4 * c) : 0u;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) z[i] = Z ? 0x43004300u + ((zz >> (8 * i)) & 0x7fu) * 0x00010001u : 0x43084308u;
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t z = Z ? ((zz >> (8 * i)) & 0x3fu) * 0x00010001u : 0x00080008u;
+                z0[i] = 0x64006400u + z;
+                z1[i] = 0xd400d400u + 16 * z;
+            }
         }
         const int row = 4 * R + t;
         const uint4 v = ld_shared_u4(block + row * 128 + ((c ^ (row & 7)) << 4));
         uint32_t p0[4], p1[4], p2[4], p3[4];
-        unpack(p0, v.x, z[0]);
-        unpack(p1, v.y, z[1]);
-        unpack(p2, v.z, z[2]);
-        unpack(p3, v.w, z[3]);
+        unpack(p0, v.x, z0[0], z1[0]);
+        unpack(p1, v.y, z0[1], z1[1]);
+        unpack(p2, v.z, z0[2], z1[2]);
+        unpack(p3, v.w, z0[3], z1[3]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const uint4 v4 = x.get(R, nt, false);
+            const uint4 b = x.get(R, nt, false);
             if (first) {
-                mma_first(part[0][nt], p0[0], p1[0], p0[1], p1[1], v4.x, v4.y);
-                mma_first(part[1][nt], p2[0], p3[0], p2[1], p3[1], v4.x, v4.y);
+                mma_h_first(part[0][nt], p0[0], p1[0], p0[1], p1[1], b.x, b.y);
+                mma_h_first(part[1][nt], p2[0], p3[0], p2[1], p3[1], b.x, b.y);
             } else {
-                mma(part[0][nt], p0[0], p1[0], p0[1], p1[1], v4.x, v4.y);
-                mma(part[1][nt], p2[0], p3[0], p2[1], p3[1], v4.x, v4.y);
+                mma_h(part[0][nt], p0[0], p1[0], p0[1], p1[1], b.x, b.y);
+                mma_h(part[1][nt], p2[0], p3[0], p2[1], p3[1], b.x, b.y);
             }
-            mma(part[0][nt], p0[2], p1[2], p0[3], p1[3], v4.z, v4.w);
-            mma(part[1][nt], p2[2], p3[2], p2[3], p3[3], v4.z, v4.w);
-            if (LO) {
-                const uint4 y = x.get(R, nt, true);
-                mma(part[0][nt], p0[0], p1[0], p0[1], p1[1], y.x, y.y);
-                mma(part[1][nt], p2[0], p3[0], p2[1], p3[1], y.x, y.y);
-                mma(part[0][nt], p0[2], p1[2], p0[3], p1[3], y.z, y.w);
-                mma(part[1][nt], p2[2], p3[2], p2[3], p3[3], y.z, y.w);
-            }
+            mma_h(part[0][nt], p0[2], p1[2], p0[3], p1[3], b.z, b.w);
+            mma_h(part[1][nt], p2[2], p3[2], p2[3], p3[3], b.z, b.w);
         }
         if (last) {
             const uint2 s2 = ld_shared_u2(scales + (R / kSteps) * 64 + 8 * c);
@@ -382,11 +431,8 @@ __device__ __forceinline__ void block_q4(float (&acc)[2][NT][4], const RowView& 
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float f = s[2 * mt + (i >> 1)];
-                        if (XS) f *= (i & 1) ? sx[nt].y : sx[nt].x;
-                        acc[mt][nt][i] = fmaf(f, part[mt][nt][i], acc[mt][nt][i]);
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        acc[mt][nt][i] = fmaf(s[2 * mt + (i >> 1)] * ((i & 1) ? sx[nt].y : sx[nt].x), part[mt][nt][i], acc[mt][nt][i]);
         }
     }
 }
@@ -401,13 +447,13 @@ struct Product {
     bool tickets;
 
     // min_units: shortest item (a tile of kb units has kb / min_units + 2 parts at most)
-    __device__ __forceinline__ void init(int matrices, int N, int K, int rows, int grid, int most_parts)
+    __device__ __forceinline__ void init(int matrices, int N, int K, int rows, int unit_bytes, int grid, int most_parts)
     {
         tiles = (N + kTileCols - 1) / kTileCols;
         kb = (K + rows - 1) / rows;
         total = matrices * tiles * kb;
         const int share = (total + grid - 1) / grid, least = (kb + most_parts - 1) / most_parts;
-        tickets = share * rows >= kItemUnits * 32 && share > least;
+        tickets = static_cast<long long>(share) * unit_bytes >= kTicketBytes && share > least;
         big = max(tickets ? share - share / 4 : share, max(least, 1));
         small = max((share + kItemsPerCta - 1) / kItemsPerCta, max(least, 1));
         bigs = min(grid * big, total);
@@ -482,8 +528,15 @@ __device__ __forceinline__ void grid_barrier(int* counter, int target, const Ctr
     __syncthreads();
 }
 
+// The calling thread's number when neighbouring warps of the numbering lie in
+// different CTAs: little work is spread over all SMs.
+__device__ __forceinline__ int spread_thread()
+{
+    return ((threadIdx.x >> 5) * gridDim.x + blockIdx.x) * 32 + (threadIdx.x & 31);
+}
+
 // Adds the parts of M sums of four neighbouring columns: sum m has n[m] parts,
-// `stride` floats apart from part[m] on.  Four parts of every sum are in
+// `stride` floats apart from part[m] on.  Eight parts of every sum are in
 // flight together: the sums are short and the latency is long.
 template <int M>
 __device__ __forceinline__ void add_parts(float4 (&s)[M], const float* const (&part)[M], const int (&n)[M], long long stride)
@@ -494,17 +547,17 @@ __device__ __forceinline__ void add_parts(float4 (&s)[M], const float* const (&p
         s[m] = make_float4(0.f, 0.f, 0.f, 0.f);
         most = max(most, n[m]);
     }
-    for (int i = 0; i < most; i += 4) {
-        float4 v[M][4];
+    for (int i = 0; i < most; i += 8) {
+        float4 v[M][8];
 #pragma unroll
         for (int m = 0; m < M; ++m)
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
+            for (int u = 0; u < 8; ++u)
                 if (i + u < n[m]) v[m][u] = __ldcg(reinterpret_cast<const float4*>(part[m] + (i + u) * stride));
 #pragma unroll
         for (int m = 0; m < M; ++m)
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
+            for (int u = 0; u < 8; ++u)
                 if (i + u < n[m]) s[m].x += v[m][u].x, s[m].y += v[m][u].y, s[m].z += v[m][u].z, s[m].w += v[m][u].w;
     }
 }
@@ -601,20 +654,23 @@ struct Engine {
 
     // Whole CTA.  Sums over k units [i0, i1) of a tile for `rows` <= NT * 8
     // rows, written to part[row][n], rows `ld` floats apart (n0: the tile's
-    // first column, N: the matrix').  octet(r, k, lo) gives 8 values of row r
-    // from column k on (k < K), as bf16; scale(r, k) the row's scale there (XS).
-    //  The rows go through shared memory in chunks, once per CTA; the
-    // next chunk is in registers while one is multiplied.
-    template <int NT, bool LO, bool XS, class F, class S>
+    // first column, N: the matrix').  octet(r, k, lo) gives 8 elements of row
+    // r from column k on (k < K) as they lie in memory, of the second parts if
+    // lo; scale(r, k) the row's scale there.  The rows go through shared
+    // memory in chunks, once per CTA; the next chunk is in registers while one
+    // is multiplied.
+    template <int NT, Rows X, class F, class S>
     __device__ __forceinline__ void segment(int i0, int i1, float* part, long long ld, int rows, int n0, int N, int K, F octet,
                                             S scale)
     {
+        constexpr bool LO = X == Rows::kPair;
+        constexpr bool kGiven = X == Rows::kHalf || X == Rows::kE4m3;  // scales come with the rows
         constexpr int kUnits = chunk_units<G, NT, LO>();
         static_assert(kUnits >= 1, "rows of one unit fit a chunk");
         constexpr int kOctets = kUnits * P::kRows / 8;                 // of a row in a chunk
         constexpr int kPitch = kOctets * 16;
         constexpr int kPer = kChunkBytes / 16 / P::kThreads;           // octets of a thread
-        constexpr int kScales = XS ? kUnits * P::kRows / kXScaleGroup : 1;   // of a row in a chunk
+        constexpr int kScales = Q4 ? kUnits * P::kRows / kXScaleGroup : 1;   // of a row in a chunk
         float acc[P::kMT][NT][4];
 #pragma unroll
         for (int mt = 0; mt < P::kMT; ++mt)
@@ -636,7 +692,7 @@ struct Engine {
                 next[x] = make_uint4(0, 0, 0, 0);     // (rows of W past the last one are zeros; so must these be)
                 if (row < rows && k < k1) next[x] = octet(row, k, LO && r >= NT * 8);
             }
-            if (XS && tid < kScales * NT * 8) {
+            if (kGiven && tid < kScales * NT * 8) {
                 const int r = tid / kScales, k = k0 + tid % kScales * kXScaleGroup;
                 next_scale = r < rows && k < k1 ? scale(r, k) : 0.f;
             }
@@ -647,9 +703,24 @@ struct Engine {
 #pragma unroll
             for (int x = 0; x < kPer; ++x) {
                 const int at = tid + x * P::kThreads, r = at / kOctets, o = at % kOctets;
-                ptx::st_shared_v4(buf + r * kPitch + ((o ^ ((r & 1) << 2)) << 4), next[x].x, next[x].y, next[x].z, next[x].w);
+                uint4 v = next[x];
+                if constexpr (X == Rows::kE4m3) {
+                    const uint2 a = e4m3x4_to_half(v.x), b = e4m3x4_to_half(v.y);
+                    v = make_uint4(a.x, a.y, b.x, b.y);
+                }
+                if constexpr (Q4 && X == Rows::kBf16) {
+                    // 16 neighbouring lanes hold the 128 columns
+                    uint32_t e = max_exponent(v);
+#pragma unroll
+                    for (int d = 1; d < 16; d <<= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, d));
+                    const float f = half_scale(e);
+                    v = make_uint4(pack_h2(bf16_lo(v.x) * f, bf16_hi(v.x) * f), pack_h2(bf16_lo(v.y) * f, bf16_hi(v.y) * f),
+                                   pack_h2(bf16_lo(v.z) * f, bf16_hi(v.z) * f), pack_h2(bf16_lo(v.w) * f, bf16_hi(v.w) * f));
+                    if ((lane & 15) == 0) st_shared_f1(buf + kChunkBytes + (r * kScales + o / 16) * 4, half_unscale(e));
+                }
+                ptx::st_shared_v4(buf + r * kPitch + ((o ^ ((r & 1) << 2)) << 4), v.x, v.y, v.z, v.w);
             }
-            if (XS && tid < kScales * NT * 8) st_shared_f1(buf + kChunkBytes + tid * 4, next_scale);
+            if (kGiven && tid < kScales * NT * 8) st_shared_f1(buf + kChunkBytes + tid * 4, next_scale);
             __syncwarp();
             if (lane == 0) mbar_arrive(chunk_bars + c * 8);
         };
@@ -688,15 +759,13 @@ struct Engine {
                         x.even = row + ((t ^ ((g & 1) << 2)) << 4);
                         x.odd = row + (((t + 4) ^ ((g & 1) << 2)) << 4);
                         float2 sx[NT];
-                        if (XS) {
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                const uint32_t sc = buf + kChunkBytes + ((nt * 8 + 2 * t) * kScales + v * 2 + s) * 4;
-                                sx[nt].x = __uint_as_float(ld_shared_u1(sc));
-                                sx[nt].y = __uint_as_float(ld_shared_u1(sc + kScales * 4));
-                            }
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const uint32_t sc = buf + kChunkBytes + ((nt * 8 + 2 * t) * kScales + v * 2 + s) * 4;
+                            sx[nt].x = __uint_as_float(ld_shared_u1(sc));
+                            sx[nt].y = __uint_as_float(ld_shared_u1(sc + kScales * 4));
                         }
-                        block_q4<NT, LO, XS, G, Z>(acc, x, sx, ring.block() + s * 2048, ring.scales() + s * (128 / G) * 64,
+                        block_q4<NT, G, Z>(acc, x, sx, ring.block() + s * 2048, ring.scales() + s * (128 / G) * 64,
                                                    ring.scales() + kScaleBytes + s * (128 / G) * 32, lane);
                     }
                 } else {
