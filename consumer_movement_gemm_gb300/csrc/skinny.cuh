@@ -69,7 +69,7 @@ struct Shape {
 constexpr int kChunkBytes = 16384;
 constexpr int kScalesOfChunk = 256;               // e4m3: a scale per row and 128 columns
 constexpr int kChunkStride = kChunkBytes + kScalesOfChunk * 4;
-constexpr int kRowBuffers = 3 * kChunkStride + 32;
+constexpr int kRowBuffers = 3 * kChunkStride + 32 + 16 * 32;    // also the chunks' barriers and the warps' places
 
 // What the rows of a product are.
 enum class Rows {
@@ -261,7 +261,6 @@ struct Ring {
     using P = Shape<G>;
     static constexpr int S = P::kStages;
     uint32_t w, meta, full;    // this warp's stages and barriers (shared addresses)
-    int fill = 0;              // next stage to fill
     int take = 0;              // next stage to read
     uint32_t parity = 0;
 
@@ -277,8 +276,8 @@ struct Ring {
         for (int s = 0; s < S; ++s) mbar_init(full + s * 8, 1);
     }
 
-    // One lane: fetch the block at column n, weight row k of matrix e.
-    __device__ __forceinline__ void issue(const WeightMaps* m, int n, int k, int e, uint64_t pol)
+    // One lane: fetch the block at column n, weight row k of matrix e into a stage.
+    __device__ __forceinline__ void issue(int fill, const WeightMaps* m, int n, int k, int e, uint64_t pol) const
     {
         const uint32_t dst = w + fill * P::kBlockBytes, bar = full + fill * 8;
         if constexpr (P::Q4) {
@@ -293,8 +292,6 @@ struct Ring {
             tma_load_3d(dst, &m->w, bar, n, k, e, pol);
         }
     }
-    __device__ __forceinline__ void filled() { fill = fill + 1 == S ? 0 : fill + 1; }
-
     __device__ __forceinline__ void wait(const Ctrl& ctrl, long long timeout_ns) { bar_wait(full + take * 8, parity, ctrl, timeout_ns); }
     __device__ __forceinline__ uint32_t block() const { return w + take * P::kBlockBytes; }
     __device__ __forceinline__ uint32_t scales() const { return meta + take * P::kMetaBytes; }
@@ -562,6 +559,13 @@ __device__ __forceinline__ void add_parts(float4 (&s)[M], const float* const (&p
     }
 }
 
+// The next block that a warp fetches: product, next item of the CTA's list,
+// units left of the current one, place of the next.
+struct Place {
+    int ph, n, left, k, col, matrix, k_end, col_end;
+};
+static_assert(sizeof(Place) == 32, "16 places behind the row buffers");
+
 // The engine of one warp.  `Calls` provides, for product `ph` (0 or 1):
 //   maps(ph), expert(ph, matrix)     where a matrix' weights are
 template <int G, bool Z, class Calls>
@@ -577,71 +581,73 @@ struct Engine {
     int n_products;
     int warp, lane;
     Ring<G, Z> ring;
-    // the next block to fetch: product, item of the CTA's list, units of the
-    // item still to fetch, place of the next one
-    int ph = 0, n = 0, left = 0, i = 0, tile = 0, matrix = 0;
-    int kb = 0, tiles = 0;     // of the product
-    uint64_t pol = 0;          // weights are read once: they leave the L2 to the parts and the rows
+    uint32_t place;            // this warp's Place (shared address)
     uint32_t rows_buf;         // kRowBuffers bytes (shared address): chunks of rows
     uint32_t chunk_bars;       // their barriers
     uint32_t buf_now = 0, buf_parity = 0;
 
-    // Goes on to item n of the product; left stays 0 where there is none.
-    __device__ __forceinline__ void open()
+    // Lane 0: goes on to the next item, of this product or the next one;
+    // false where there is none.
+    __device__ __forceinline__ bool advance(Place& f) const
     {
-        const Product& q = pr[ph];
-        const int id = item_at(q, queue[ph], n, ctrl, timeout_ns);
-        if (id >= q.items) return;
-        if (q.tickets && warp == 0 && lane == 0) {
-            const int grid = gridDim.x;
-            if (n == 0) queue[ph].item[1] = static_cast<uint16_t>(min(atomicAdd(tickets + ph * kSyncStep, 1) + grid, q.items));
-            queue[ph].item[n + 2] = static_cast<uint16_t>(min(atomicAdd(tickets + ph * kSyncStep, 1) + grid, q.items));
+        for (; f.ph < n_products; ++f.ph, f.n = 0) {
+            const Product& q = pr[f.ph];
+            const int n = f.n, id = item_at(q, queue[f.ph], n, ctrl, timeout_ns);
+            if (id >= q.items) continue;
+            ++f.n;
+            if (q.tickets && warp == 0) {
+                const int grid = gridDim.x;
+                int* counter = tickets + f.ph * kSyncStep;
+                if (n == 0) queue[f.ph].item[1] = static_cast<uint16_t>(min(atomicAdd(counter, 1) + grid, q.items));
+                queue[f.ph].item[n + 2] = static_cast<uint16_t>(min(atomicAdd(counter, 1) + grid, q.items));
+            }
+            const int b = q.begin(id), at = b / q.kb;
+            f.left = q.end(id) - b;
+            f.k = (b - at * q.kb) * P::kRows;
+            f.matrix = at / q.tiles;
+            f.col = (at - f.matrix * q.tiles) * kTileCols;
+            f.k_end = q.kb * P::kRows;
+            f.col_end = q.tiles * kTileCols;
+            return true;
         }
-        const int b = q.begin(id);
-        left = q.end(id) - b;
-        kb = q.kb;
-        tiles = q.tiles;
-        const int at = b / kb;
-        i = b - at * kb;
-        matrix = at / tiles;
-        tile = at - matrix * tiles;
+        return false;
     }
 
-    // Fetches the warp's next block, if there is one.
-    __device__ __forceinline__ void fetch()
+    // Fetches the warp's next block, if there is one (lane 0; the place lives
+    // in shared memory, the registers belong to the sums).
+    __device__ __forceinline__ void fetch(int stage)
     {
-        while (left == 0) {
-            if (ph >= n_products) return;
-            open();
-            ++n;
-            if (left == 0) {     // the product has no more items for this CTA
-                ++ph;
-                n = 0;
+        if (lane != 0) return;
+        Place& f = *reinterpret_cast<Place*>(__cvta_shared_to_generic(place));
+        if (f.left == 0 && !advance(f)) return;
+        const int k = f.k, col = f.col, matrix = f.matrix, ph = f.ph;
+        --f.left;
+        f.k = k + P::kRows;
+        if (k + P::kRows == f.k_end) {
+            f.k = 0;
+            f.col = col + kTileCols;
+            if (col + kTileCols == f.col_end) {
+                f.col = 0;
+                f.matrix = matrix + 1;
             }
         }
-        if (lane == 0) ring.issue(c.maps(ph), tile * kTileCols + warp * P::kCols, i * P::kRows, c.expert(ph, matrix), pol);
-        ring.filled();
-        --left;
-        if (++i == kb) {
-            i = 0;
-            if (++tile == tiles) {
-                tile = 0;
-                ++matrix;
-            }
-        }
+        // weights are read once: they leave the L2 to the parts and the rows
+        ring.issue(stage, c.maps(ph), col + warp * P::kCols, k, c.expert(ph, matrix), ptx::l2_policy(1));
     }
 
     // Before the first barrier of the CTA.
     __device__ __forceinline__ void init(uint8_t* smem, uint8_t* rows)
     {
-        pol = ptx::l2_policy(1);
         rows_buf = ptx::smem_u32(rows);
         chunk_bars = rows_buf + 3 * kChunkStride;
+        place = chunk_bars + 32 + warp * static_cast<int>(sizeof(Place));
         ring.init(ptx::smem_u32(smem), warp);
         if (lane == 0) {
             ring.init_barriers();
             if (warp == 0)
                 for (int b = 0; b < 3; ++b) mbar_init(chunk_bars + b * 8, P::kWarps);
+            Place& f = *reinterpret_cast<Place*>(__cvta_shared_to_generic(place));
+            f.ph = f.n = f.left = 0;
             ptx::fence_mbar_init();
         }
     }
@@ -649,7 +655,7 @@ struct Engine {
     __device__ __forceinline__ void start()
     {
 #pragma unroll 1
-        for (int s = 0; s < P::kStages; ++s) fetch();
+        for (int s = 0; s < P::kStages; ++s) fetch(s);
     }
 
     // Whole CTA.  Sums over k units [i0, i1) of a tile for `rows` <= NT * 8
@@ -773,9 +779,9 @@ struct Engine {
                     x.even = base + (v >> 1) * 128 + (((t + 4 * (v & 1)) ^ ((g & 1) << 2)) << 4);
                     block_bf16<NT, LO>(acc, x, 0, ring.block(), lane);
                 }
-                ring.taken();
                 __syncwarp();      // every lane has read the stage before it is filled again
-                fetch();
+                fetch(ring.take);
+                ring.taken();
             }
         }
         n0 += warp * P::kCols;
