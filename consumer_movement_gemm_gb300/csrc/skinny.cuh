@@ -214,6 +214,14 @@ __device__ __forceinline__ uint32_t fma_h2(uint32_t a, uint32_t b, uint32_t c)
     return d;
 }
 
+// (a & mask) | bits in one instruction.
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t bits)
+{
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(a), "r"(mask), "r"(bits));
+    return d;
+}
+
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi)
 {
     uint32_t d;
@@ -369,10 +377,10 @@ __device__ __forceinline__ void block_bf16(float (&acc)[4][NT][4], const RowView
 __device__ __forceinline__ void unpack(uint32_t (&p)[4], uint32_t word, uint32_t z0, uint32_t z1)
 {
     const uint32_t high = word >> 8, sixteenth = 0x2c002c00u;
-    p[0] = sub_h2((word & 0x000f000fu) | 0x64006400u, z0);
-    p[1] = fma_h2((word & 0x00f000f0u) | 0x64006400u, sixteenth, z1);
-    p[2] = sub_h2((high & 0x000f000fu) | 0x64006400u, z0);
-    p[3] = fma_h2((high & 0x00f000f0u) | 0x64006400u, sixteenth, z1);
+    p[0] = sub_h2(and_or(word, 0x000f000fu, 0x64006400u), z0);
+    p[1] = fma_h2(and_or(word, 0x00f000f0u, 0x64006400u), sixteenth, z1);
+    p[2] = sub_h2(and_or(high, 0x000f000fu, 0x64006400u), z0);
+    p[3] = fma_h2(and_or(high, 0x00f000f0u, 0x64006400u), sixteenth, z1);
 }
 
 // acc[mt][nt] += half a block, 128 x 32 4-bit weights in groups of G rows, with
@@ -388,6 +396,8 @@ __device__ __forceinline__ void block_q4(float (&acc)[2][NT][4], const RowView& 
     const int c = (g >> 1) | ((g & 1) << 2);
     float part[2][NT][4];
     uint32_t z0[4], z1[4];
+    // this lane's words of octet rows t and t + 4
+    const uint32_t low = block + t * 128 + ((c ^ t) << 4), high = block + (t + 4) * 128 + ((c ^ (t + 4)) << 4);
 #pragma unroll
     for (int R = 0; R < 4; ++R) {
         const bool first = R % kSteps == 0, last = R % kSteps == kSteps - 1;
@@ -400,8 +410,7 @@ __device__ __forceinline__ void block_q4(float (&acc)[2][NT][4], const RowView& 
                 z1[i] = 0xd400d400u + 16 * z;
             }
         }
-        const int row = 4 * R + t;
-        const uint4 v = ld_shared_u4(block + row * 128 + ((c ^ (row & 7)) << 4));
+        const uint4 v = ld_shared_u4(((R & 1) ? high : low) + (R >> 1) * 1024);
         uint32_t p0[4], p1[4], p2[4], p3[4];
         unpack(p0, v.x, z0[0], z1[0]);
         unpack(p1, v.y, z0[1], z1[1]);
