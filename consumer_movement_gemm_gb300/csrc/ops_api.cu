@@ -78,9 +78,14 @@ bool valid_q4(int K, int N, int group, const void* q, const void* scale, const v
 
 long long up256(long long v) { return (v + 255) & ~255LL; }
 
-// Limit of a tile's parts (less two) by the rows of a product: few rows can
-// afford a cut for every CTA, many have other tiles to share out.
-int most_parts(long long rows) { return rows <= 64 ? 16 : rows <= 256 ? 8 : 4; }
+// Limit of a tile's parts (less two) by the rows of a product and its tiles of
+// 512 columns: few rows and few tiles can afford a cut for every CTA, many have
+// other tiles to share out.
+int most_parts(long long rows, long long N)
+{
+    const int by_rows = rows <= 64 ? 16 : rows <= 256 ? 8 : 4, by_tiles = N < 64 * 512 ? 16 : N < 256 * 512 ? 8 : 4;
+    return by_rows < by_tiles ? by_rows : by_tiles;
+}
 
 // Pieces of a moe_decode workspace, in order.
 struct MoeSpace {
@@ -89,7 +94,7 @@ struct MoeSpace {
     {
         const long long rows = static_cast<long long>(T) * k;
         h = up256(2 * rows * I);
-        part = 4 * (most_parts(rows) + 2) * rows * (2 * I > H ? 2 * I : H);
+        part = 4 * (most_parts(rows, 0) + 2) * rows * (2 * I > H ? 2 * I : H);
         total = 2 * h + up256(part);
     }
 };
@@ -202,7 +207,7 @@ static int run_moe(tovl_handle h, MoeParams& p, int group, bool zero, const void
     p.out = out;
     p.ldo = ldo;
     p.out_vec = ldo % 4 == 0 && aligned(out, 8);
-    p.most_parts = most_parts(static_cast<long long>(T) * k);
+    p.most_parts = most_parts(static_cast<long long>(T) * k, 0);
     p.h_hi = ws;
     p.h_lo = ws + space.h;
     p.part = reinterpret_cast<float*>(ws + 2 * space.h);
@@ -264,7 +269,7 @@ TOVL_API int tovl_moe_decode_q4(tovl_handle h, const void* x, long long ldx, int
 TOVL_API long long tovl_matvec_q4_workspace(tovl_handle h, int T, int N)
 {
     if (!h || T < 0 || N < 1 || T > kMaxDecodeRows) return -1;
-    return up256(4LL * (most_parts(T) + 2) * T * N);
+    return up256(4LL * (most_parts(T, N) + 2) * T * N);
 }
 
 TOVL_API int tovl_matvec_q4(tovl_handle h, const void* x, int x_type, const float* x_scale, long long ldx, int T, int K,
@@ -292,7 +297,7 @@ TOVL_API int tovl_matvec_q4(tovl_handle h, const void* x, int x_type, const floa
     p.out = out;
     p.part = static_cast<float*>(workspace);
     p.out_vec = ldo % 4 == 0 && aligned(out, 8);
-    p.most_parts = most_parts(T);
+    p.most_parts = most_parts(T, N);
     p.timeout_ns = h->timeout_ns;
     p.ldx = ldx;
     p.ldo = ldo;

@@ -6,7 +6,8 @@ Tolerances are error bounds, not fits:
     warps, groups and parts) each lose 2^-23 of a partial sum, which is at most
     the sum of the terms' magnitudes;
   * a result rounded to bf16: 2^-8 of itself at most (half a unit is 2^-9, and
-    the error before it may move it across one boundary);
+    the error before it may move it across one boundary); below 2^-126 the unit
+    is 2^-133 whatever the value;
   * e4m3: half a unit, 2^-4 of the value or 2^-10 among the subnormals.
 """
 import math
@@ -271,7 +272,7 @@ def check_matvec(h, x, xs, w, group, out, workspace, intact=None, stream=None):
     if xs is not None:
         xd = xd * xs.to(D).repeat_interleave(128, 1)[:, :x.shape[1]]
     want = xd @ W
-    bound = U16 * want.abs() + sum_bound(x.shape[1] + x.shape[1] / group * 16, xd.abs() @ W.abs())
+    bound = U16 * want.abs() + 2.0 ** -133 + sum_bound(x.shape[1] + x.shape[1] / group * 16, xd.abs() @ W.abs())
     within(out, want, bound, "out")
     assert intact is None or intact()
 
@@ -324,6 +325,44 @@ def test_matvec_rows_do_not_touch_each_other(h):
     keep = [0, 1, 3, 5]
     check_matvec(h, x[keep], None, w, 64, torch.empty(4, N, dtype=BF16, device=DEV), ws)
     assert torch.isfinite(out[keep].float()).all()
+
+
+def test_matvec_takes_any_magnitude(h):
+    """bf16 rows of 1e-30 and 1e30, and rows whose elements span 2^40, inside the bound of the fp32 sums: the
+    activations' 16-bit form inside the kernel has to carry its own exponent."""
+    g = gen(24)
+    K, N, T = 512, 96, 9
+    x = randn(g, T, K, dtype=F32)
+    x[0] *= 1e-30
+    x[1] *= 1e30
+    x[2, ::2] *= 2.0 ** -40
+    x[3] *= torch.exp2(torch.randint(-60, 60, (K,), generator=g, device=DEV).float())
+    x[4, :128], x[4, 128:256] = 0, x[4, 128:256] * 1e20
+    x[5] = 2.0 ** -126
+    x[6] = 3e38 * torch.sign(x[6])
+    w = packed(g, (), K, N, 128, True)
+    w = (w[0], (w[1].float() * 2.0 ** -8).to(BF16), w[2])
+    check_matvec(h, x.to(BF16), None, w, 128, torch.empty(T, N, dtype=BF16, device=DEV), space(h.matvec_q4_workspace(T, N)))
+
+
+@pytest.mark.parametrize("T,K,N,kind", [(3, 8192, 131072 + 16, "bf16"), (17, 8192, 131072, "e4m3")])
+def test_matvec_large_enough_for_tickets(h, T, K, N, kind):
+    """Over 3 MB of weights a CTA: most items are taken by ticket; the bits stay the same."""
+    g = gen(T)
+    xs = None
+    if kind == "bf16":
+        x = randn(g, T, K)
+    else:
+        x = randn(g, T, K, scale=100, dtype=F32).clamp_(-448, 448).to(E4M3)
+        xs = (torch.rand(T, K // 128, generator=g, device=DEV) + 0.5) * 0.01
+    w = packed(g, (), K, N, 128, kind == "bf16")
+    out, ws = torch.empty(T, N, dtype=BF16, device=DEV), space(h.matvec_q4_workspace(T, N))
+    check_matvec(h, x, xs, w, 128, out, ws)
+    first = out.clone()
+    for _ in range(3):
+        out.zero_()
+        h.matvec_q4(x, w[0], w[1], 128, out, ws, zero=w[2], x_scale=xs)
+        assert torch.equal(out, first)
 
 
 def test_norm_rows_feed_the_matvec(h):
@@ -464,6 +503,40 @@ def test_moe_strided_rows_streams_and_repeats(h):
     for _ in range(4):       # the same bits every time, on any stream
         out = check_moe(h, x, topk, gate, *W, stream=side)
         assert torch.equal(out, first)
+
+
+@pytest.mark.parametrize("T,E,k,H,I,quant", [(5, 8, 4, 4096, 4096, None), (40, 8, 2, 4096, 4104, None),
+                                             (20, 16, 4, 7168, 4096, 128)])
+def test_moe_large_enough_for_tickets(h, T, E, k, H, I, quant):
+    """Over 3 MB of weights a CTA: most items are taken by ticket; the bits stay the same."""
+    g = gen(T)
+    topk, gate = routing(g, T, E, k)
+    x = randn(g, T, H)
+    if quant:
+        w = packed(g, (E,), H, 2 * I, quant, True), packed(g, (E,), I, H, quant, True)
+    else:
+        w = bf16_experts(g, E, H, I)
+    first = check_moe(h, x, topk, gate, *w, quant=quant).clone()
+    ws, out = space(h.moe_decode_workspace(T, k, H, I)), torch.empty_like(first)
+    for _ in range(3):
+        out.zero_()
+        if quant:
+            h.moe_decode_q4(x, topk, gate, *w, quant, out, ws)
+        else:
+            h.moe_decode(x, topk, gate, *w, out, ws)
+        assert torch.equal(out, first)
+    assert h.sync_status() == 0
+
+
+@pytest.mark.parametrize("quant", [None, 64])
+def test_moe_takes_any_magnitude(h, quant):
+    """Rows of x from 1e-18 to 1e15: gate and up values, h and the result stay inside the bound."""
+    g = gen(36)
+    T, E, k, H, I = 6, 3, 2, 256, 192
+    topk, gate = routing(g, T, E, k)
+    x = (torch.randn(T, H, generator=g, device=DEV) * torch.tensor([1e-18, 1e-6, 1.0, 1e3, 1e9, 1e15], device=DEV)[:, None]).to(BF16)
+    w = bf16_experts(g, E, H, I) if quant is None else (packed(g, (E,), H, 2 * I, 64, True), packed(g, (E,), I, H, 64, True))
+    check_moe(h, x, topk, gate, *w, quant=quant)
 
 
 def test_moe_back_to_back_calls_of_other_shapes(h):
