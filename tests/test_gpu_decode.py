@@ -596,6 +596,11 @@ def test_decode_step(h):
                                                             torch.ones(T, k - 1, dtype=torch.bool, device=DEV))
 
 
+def test_the_example_runs():
+    from examples import decode_step
+    assert 0 < decode_step.main(5) < 0.3      # (4-bit experts are near the bf16 ones, and not they)
+
+
 # ------------------------------------------------------------------ refusals
 def test_device_errors_are_reported_and_cleared(h):
     g = gen(51)
