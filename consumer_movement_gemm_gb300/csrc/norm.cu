@@ -449,11 +449,15 @@ cudaError_t launch_norm(const NormParams& p, int width, int num_sms, cudaStream_
             if (vecs <= 64) return launch_rows<2, true>(p, lc, num_sms);
             return launch_rows<4, true>(p, lc, num_sms);
         }
-        const int vpt = vecs <= 1024 ? 2 : vecs <= 2048 ? 4 : 8;
-        lc.blockDim = dim3(up32((vecs + vpt - 1) / vpt));
-        if (vpt == 2) return launch_rows<2, false>(p, lc, num_sms);
-        if (vpt == 4) return launch_rows<4, false>(p, lc, num_sms);
-        return launch_rows<8, false>(p, lc, num_sms);
+        if (vecs <= 2048) {
+            const int vpt = vecs <= 1024 ? 2 : 4;
+            lc.blockDim = dim3(up32((vecs + vpt - 1) / vpt));
+            return vpt == 2 ? launch_rows<2, false>(p, lc, num_sms) : launch_rows<4, false>(p, lc, num_sms);
+        }
+        // longer rows fill the registers without a second row in flight
+        lc.gridDim = dim3(p.T);
+        lc.blockDim = dim3(up32((vecs + 3) / 4));
+        return launch_any<8>(p, lc, 0, 4);
     }
     int vpt = warp_row ? (vecs + 31) / 32 : (vecs + 1023) / 1024;
     if (vpt == 3) vpt = 4;
