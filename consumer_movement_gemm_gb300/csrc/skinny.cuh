@@ -402,12 +402,20 @@ __device__ __forceinline__ void block_q4(float (&acc)[2][NT][4], const RowView& 
     for (int R = 0; R < 4; ++R) {
         const bool first = R % kSteps == 0, last = R % kSteps == kSteps - 1;
         if (first) {
-            const uint32_t zz = Z ? ld_shared_u1(zeros + (R / kSteps) * 32 + 4 * c) : 0u;
+            if constexpr (Z) {
+                // the byte of column i under 0x64 (1024 + z), sixteen times it under 0xd4 (-(64 + z))
+                const uint32_t zz = ld_shared_u1(zeros + (R / kSteps) * 32 + 4 * c) & 0x0f0f0f0fu;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t z = Z ? ((zz >> (8 * i)) & 0x3fu) * 0x00010001u : 0x00080008u;
-                z0[i] = 0x64006400u + z;
-                z1[i] = 0xd400d400u + 16 * z;
+                for (int i = 0; i < 4; ++i) {
+                    z0[i] = __byte_perm(zz, 0x64u, 0x4040u | i | i << 8);
+                    z1[i] = __byte_perm(zz << 4, 0xd4u, 0x4040u | i | i << 8);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    z0[i] = 0x64086408u;
+                    z1[i] = 0xd480d480u;
+                }
             }
         }
         const uint4 v = ld_shared_u4(((R & 1) ? high : low) + (R >> 1) * 1024);

@@ -248,7 +248,7 @@ int tovl_dispatch_plan_noalloc(const int* topk_idx, int T, int k, int E, int* ex
  * bits 4i .. 4i+3 and row 8r+2i+1 in bits 16+4i .. 16+4i+3.  A group is
  * `group` rows (32, 64 or 128; K a multiple of it) of one column:
  *   W[k][n] = (nibble - zero[k/group][n]) * scale[k/group][n],
- * scale bf16 [K/group][N], zero uint8 [K/group][N] with values 0 .. 63, or a
+ * scale bf16 [K/group][N], zero uint8 [K/group][N] with values 0 .. 15, or a
  * null pointer for zero = 8 throughout.  N is a multiple of 8, with zeros of
  * 16; all pointers are 16-byte aligned.  Stacked matrices (one per expert)
  * are contiguous. */
