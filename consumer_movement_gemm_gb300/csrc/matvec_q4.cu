@@ -6,11 +6,19 @@
 // The activations enter the tensor core as fp16 (e4m3 exactly, bf16 with a
 // power of two per 128 columns), their products with the integers nibble -
 // zero are exact, a group's sum is fp32, and the scales multiply it in fp32:
-// nothing is rounded before the result.  The stream of weight blocks
-// and the split are skinny.cuh's; every 32 rows are a pass over the weights
-// (one pass is the next one's matrix, so large matrices are read again).
+// nothing is rounded before the result.  Every 16 rows are a pass over
+// the weights (fp16 rows and their sums, two 8-row tiles of the instruction, are
+// what the registers hold), a pass the next one's matrix, so large matrices are
+// read again.
+//
+// Large products stream the weights through skinny.cuh's rings, small ones read
+// them straight into registers (matvec_q4_direct.cuh); use_direct is the rule.
+// What bounds the ring: instruction issue, about 400 instructions per 2 KB of
+// weights with 9 to 16 rows and 335 with up to 8.  16 x 7168 x 32768: 45 us, 2.8
+// TB/s; 1 x 8192 x 28672: 31.6 us, 3.8 TB/s.
 #include <type_traits>
 #include "launch.cuh"
+#include "matvec_q4_direct.cuh"
 #include "skinny.cuh"
 
 namespace tovl {
@@ -193,9 +201,61 @@ cudaError_t prepare_matvec_q4()
     return cudaSuccess;
 }
 
+template <int NT, bool XS, int G>
+static cudaError_t launch_direct(const MatvecParams& p, bool zero, int sms, cudaStream_t stream, bool pdl)
+{
+    const int tiles = (p.N + kDirectCols - 1) / kDirectCols, passes = (p.T + 15) / 16, blocks = (p.K + 127) / 128;
+    // One CTA of 16 warps per SM where that is all of them; else CTAs of 8, two
+    // on an SM, whose starts and ends overlap (one row: 128 tiles, 11008 x 4096,
+    // 9.9 us with 16 and 11.3 with 8; 344 tiles, 4096 x 11008, 12.5 and 11.1).
+    // Clusters as long as they fit the SMs and leave each warp a block (28672 x
+    // 1024: 20.9 us without, 8.2 with four CTAs; eight are no faster than four:
+    // 28672 x 512 9.5 and 8.2).
+    const int warps = tiles * passes <= sms ? kDirectWarps : kDirectWarps / 2;
+    int split = 1;
+    while (split < kDirectCluster && tiles * passes * split * 2 <= sms && split * warps < blocks) split *= 2;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(tiles, split, passes);
+    lc.blockDim = dim3(warps * 32);
+    lc.stream = stream;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (split > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = 1;
+        attr[n].val.clusterDim.y = split;
+        attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (pdl) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
+    lc.attrs = attr;
+    lc.numAttrs = n;
+    return zero ? cudaLaunchKernelEx(&lc, matvec_q4_direct_kernel<NT, XS, G, true>, p)
+                : cudaLaunchKernelEx(&lc, matvec_q4_direct_kernel<NT, XS, G, false>, p);
+}
+
+template <int NT, bool XS>
+static cudaError_t launch_direct(const MatvecParams& p, int group, bool zero, int sms, cudaStream_t stream, bool pdl)
+{
+    if (group == 32) return launch_direct<NT, XS, 32>(p, zero, sms, stream, pdl);
+    if (group == 64) return launch_direct<NT, XS, 64>(p, zero, sms, stream, pdl);
+    return launch_direct<NT, XS, 128>(p, zero, sms, stream, pdl);
+}
+
 cudaError_t launch_matvec_q4(const MatvecParams& p, bool e4m3, int group, bool zero, int grid, cudaStream_t stream,
                              bool pdl)
 {
+    if (use_direct(p.T, p.K, p.N)) {
+        if (p.T <= 8)
+            return e4m3 ? launch_direct<1, true>(p, group, zero, grid, stream, pdl)
+                        : launch_direct<1, false>(p, group, zero, grid, stream, pdl);
+        return e4m3 ? launch_direct<2, true>(p, group, zero, grid, stream, pdl)
+                    : launch_direct<2, false>(p, group, zero, grid, stream, pdl);
+    }
     return with_kernel(e4m3, group, zero, [&](auto kernel, int smem) {
         return launch_grid(kernel, p, grid, kThreads4, smem, stream, false, pdl);
     });

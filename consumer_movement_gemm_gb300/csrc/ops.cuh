@@ -84,12 +84,21 @@ cudaError_t prepare_moe_decode();
 cudaError_t launch_moe_decode(const MoeParams& p, int group, bool zero, int grid, cudaStream_t stream, bool cooperative,
                               bool pdl);
 
+// 4-bit products that read the matrix straight into registers: those of fewer
+// than 2^26 weights, counted once per 16 rows.  At the edge, 8192 x 8192: one
+// row 14.4 us so and 14.3 through the ring, 16 rows 24.0 and 21.5; below it, 4096
+// x 11008: 11.1 and 15.5, 18.7 and 22.6; above it, 8192 x 28672: 39 and 31.6.
+inline bool use_direct(int T, int K, int N) { return static_cast<long long>((T + 15) / 16) * K * N < (1LL << 26); }
+
 struct MatvecParams {
     WeightMaps w;
     const void* x;          // bf16 or e4m3 [T][K], rows ldx apart
     const float* x_scale;   // [T][ceil(K/128)] for e4m3
     void* out;              // bf16 [T][N], rows ldo apart
     float* part;            // [most_parts + 2][T][N] parts of the product
+    const void* wq;         // the matrix itself, for the form without a ring
+    const void* w_scale;
+    const void* w_zero;
     long long ldx, ldo;
     int T, K, N;
     int out_vec;

@@ -290,8 +290,13 @@ TOVL_API int tovl_matvec_q4(tovl_handle h, const void* x, int x_type, const floa
     DeviceGuard g(h->device);
     MatvecParams p;
     std::memset(&p, 0, sizeof p);
-    const int rc = map_q4(h, &p.w, wq, w_scale, w_zero, 1, K, N, group);
-    if (rc != TOVL_OK) return rc;
+    p.wq = wq;
+    p.w_scale = w_scale;
+    p.w_zero = w_zero;
+    if (!use_direct(T, K, N)) {
+        const int rc = map_q4(h, &p.w, wq, w_scale, w_zero, 1, K, N, group);
+        if (rc != TOVL_OK) return rc;
+    }
     p.x = x;
     p.x_scale = x_scale;
     p.out = out;

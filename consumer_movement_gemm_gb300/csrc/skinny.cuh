@@ -100,6 +100,22 @@ __device__ __forceinline__ uint4 ld_shared_u4(uint32_t addr)
     return v;
 }
 
+// 16 bytes that are read once
+__device__ __forceinline__ uint4 ld_stream(const uint32_t* p)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// Number in another CTA of the cluster, by its shared::cluster address.
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v)
+{
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
 __device__ __forceinline__ uint2 ld_shared_u2(uint32_t addr)
 {
     uint2 v;
@@ -252,6 +268,13 @@ __device__ __forceinline__ uint2 e4m3x4_to_half(uint32_t v)
 __device__ __forceinline__ float half_scale(uint32_t e) { return __uint_as_float(min(268u - e, 253u) << 23); }
 __device__ __forceinline__ float half_unscale(uint32_t e) { return __uint_as_float((254u - min(268u - e, 253u)) << 23); }
 
+// Eight bf16 numbers times f as fp16.
+__device__ __forceinline__ uint4 bf16x8_to_half(const uint4& v, float f)
+{
+    return make_uint4(pack_h2(bf16_lo(v.x) * f, bf16_hi(v.x) * f), pack_h2(bf16_lo(v.y) * f, bf16_hi(v.y) * f),
+                      pack_h2(bf16_lo(v.z) * f, bf16_hi(v.z) * f), pack_h2(bf16_lo(v.w) * f, bf16_hi(v.w) * f));
+}
+
 // Largest exponent field of eight bf16 numbers.
 __device__ __forceinline__ uint32_t max_exponent(const uint4& u)
 {
@@ -383,28 +406,29 @@ __device__ __forceinline__ void unpack(uint32_t (&p)[4], uint32_t word, uint32_t
     p[3] = fma_h2(and_or(high, 0x00f000f0u, 0x64006400u), sixteenth, z1);
 }
 
-// acc[mt][nt] += half a block, 128 x 32 4-bit weights in groups of G rows, with
-// zeros (Z) or 8 for all.  sx: the tokens' activation scales.  Lane group g
-// owns four neighbouring columns; the order 0 4 1 5 2 6 3 7 of the groups
-// keeps the 16-byte reads of a quarter warp in different banks.
-template <int NT, int G, bool Z>
-__device__ __forceinline__ void block_q4(float (&acc)[2][NT][4], const RowView& x, const float2 (&sx)[NT],
-                                         uint32_t block, uint32_t scales, uint32_t zeros, int lane)
+// acc[mt][nt] += 128 x 32 4-bit weights in groups of G rows, with zeros (Z) or
+// 8 for all.  Lane group g owns the four neighbouring columns 4 c(g), in the
+// order c = 0 4 1 5 2 6 3 7 of the groups, and octet rows t, t + 4, ..:
+//   words(R)    the four columns' words of octet row 4 R + t
+//   zero(q)     their zeros in group q, one a byte (0 .. 15)
+//   scale(q)    their scales in group q, bf16
+//   x(R, nt)    octet t of rows 32 R .. 32 R + 31 of token g, fp16
+// sx: scales of the tokens 2 t and 2 t + 1.
+__device__ __forceinline__ int column_group(int g) { return (g >> 1) | ((g & 1) << 2); }
+
+template <int NT, int G, bool Z, class W, class ZF, class SF, class XF>
+__device__ __forceinline__ void multiply_q4(float (&acc)[2][NT][4], const float2 (&sx)[NT], W words, ZF zero, SF scale, XF x)
 {
     constexpr int kSteps = G / 32;
-    const int g = lane >> 2, t = lane & 3;
-    const int c = (g >> 1) | ((g & 1) << 2);
     float part[2][NT][4];
     uint32_t z0[4], z1[4];
-    // this lane's words of octet rows t and t + 4
-    const uint32_t low = block + t * 128 + ((c ^ t) << 4), high = block + (t + 4) * 128 + ((c ^ (t + 4)) << 4);
 #pragma unroll
     for (int R = 0; R < 4; ++R) {
         const bool first = R % kSteps == 0, last = R % kSteps == kSteps - 1;
         if (first) {
             if constexpr (Z) {
                 // the byte of column i under 0x64 (1024 + z), sixteen times it under 0xd4 (-(64 + z))
-                const uint32_t zz = ld_shared_u1(zeros + (R / kSteps) * 32 + 4 * c) & 0x0f0f0f0fu;
+                const uint32_t zz = zero(R / kSteps) & 0x0f0f0f0fu;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     z0[i] = __byte_perm(zz, 0x64u, 0x4040u | i | i << 8);
@@ -418,7 +442,7 @@ __device__ __forceinline__ void block_q4(float (&acc)[2][NT][4], const RowView& 
                 }
             }
         }
-        const uint4 v = ld_shared_u4(((R & 1) ? high : low) + (R >> 1) * 1024);
+        const uint4 v = words(R);
         uint32_t p0[4], p1[4], p2[4], p3[4];
         unpack(p0, v.x, z0[0], z1[0]);
         unpack(p1, v.y, z0[1], z1[1]);
@@ -426,7 +450,7 @@ __device__ __forceinline__ void block_q4(float (&acc)[2][NT][4], const RowView& 
         unpack(p3, v.w, z0[3], z1[3]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const uint4 b = x.get(R, nt, false);
+            const uint4 b = x(R, nt);
             if (first) {
                 mma_h_first(part[0][nt], p0[0], p1[0], p0[1], p1[1], b.x, b.y);
                 mma_h_first(part[1][nt], p2[0], p3[0], p2[1], p3[1], b.x, b.y);
@@ -438,7 +462,7 @@ __device__ __forceinline__ void block_q4(float (&acc)[2][NT][4], const RowView& 
             mma_h(part[1][nt], p2[2], p3[2], p2[3], p3[3], b.z, b.w);
         }
         if (last) {
-            const uint2 s2 = ld_shared_u2(scales + (R / kSteps) * 64 + 8 * c);
+            const uint2 s2 = scale(R / kSteps);
             const float s[4] = {bf16_lo(s2.x), bf16_hi(s2.x), bf16_lo(s2.y), bf16_hi(s2.y)};
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
@@ -449,6 +473,21 @@ __device__ __forceinline__ void block_q4(float (&acc)[2][NT][4], const RowView& 
                         acc[mt][nt][i] = fmaf(s[2 * mt + (i >> 1)] * ((i & 1) ? sx[nt].y : sx[nt].x), part[mt][nt][i], acc[mt][nt][i]);
         }
     }
+}
+
+// The same with the weights of half a ring block: its words (128-byte
+// swizzle; the order of the column groups keeps the 16-byte reads of a quarter
+// warp in different banks), scales and zeros.
+template <int NT, int G, bool Z>
+__device__ __forceinline__ void block_q4(float (&acc)[2][NT][4], const RowView& x, const float2 (&sx)[NT],
+                                         uint32_t block, uint32_t scales, uint32_t zeros, int lane)
+{
+    const int t = lane & 3, c = column_group(lane >> 2);
+    const uint32_t low = block + t * 128 + ((c ^ t) << 4), high = block + (t + 4) * 128 + ((c ^ (t + 4)) << 4);
+    multiply_q4<NT, G, Z>(
+        acc, sx, [&](int R) { return ld_shared_u4(((R & 1) ? high : low) + (R >> 1) * 1024); },
+        [&](int q) { return ld_shared_u1(zeros + q * 32 + 4 * c); }, [&](int q) { return ld_shared_u2(scales + q * 64 + 8 * c); },
+        [&](int R, int nt) { return x.get(R, nt, false); });
 }
 
 // ------------------------------------------------------------ items
@@ -737,8 +776,7 @@ struct Engine {
 #pragma unroll
                     for (int d = 1; d < 16; d <<= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, d));
                     const float f = half_scale(e);
-                    v = make_uint4(pack_h2(bf16_lo(v.x) * f, bf16_hi(v.x) * f), pack_h2(bf16_lo(v.y) * f, bf16_hi(v.y) * f),
-                                   pack_h2(bf16_lo(v.z) * f, bf16_hi(v.z) * f), pack_h2(bf16_lo(v.w) * f, bf16_hi(v.w) * f));
+                    v = bf16x8_to_half(v, f);
                     if ((lane & 15) == 0) st_shared_f1(buf + kChunkBytes + (r * kScales + o / 16) * 4, half_unscale(e));
                 }
                 ptx::st_shared_v4(buf + r * kPitch + ((o ^ ((r & 1) << 2)) << 4), v.x, v.y, v.z, v.w);
@@ -810,7 +848,7 @@ struct Engine {
                 if (row < rows) {
                     float* dst = part + row * ld;
                     if constexpr (Q4) {
-                        const int n = n0 + 4 * ((g >> 1) | ((g & 1) << 2));
+                        const int n = n0 + 4 * column_group(g);
                         if (n < N)
                             *reinterpret_cast<float4*>(dst + n) = make_float4(acc[0][nt][j], acc[0][nt][j + 2], acc[1][nt][j], acc[1][nt][j + 2]);
                     } else {

@@ -365,6 +365,62 @@ def test_matvec_large_enough_for_tickets(h, T, K, N, kind):
         assert torch.equal(out, first)
 
 
+def matvec_inputs(g, T, K, kind):
+    if kind == "bf16":
+        return randn(g, T, K), None
+    x = randn(g, T, K, scale=100, dtype=F32).clamp_(-448, 448).to(E4M3)
+    return x, (torch.rand(T, -(-K // 128), generator=g, device=DEV) + 0.5) * 0.01
+
+
+# both sides of 2^26 weights (counted once per 16 rows), where another kernel begins
+@pytest.mark.parametrize("T,K,N,group,zeros,kind", [
+    (2, 16416, 4112, 32, True, "bf16"), (8, 8192, 8184, 64, False, "bf16"), (8, 8192, 8192, 64, False, "bf16"),
+    (9, 10240, 6560, 128, True, "e4m3"), (16, 16384, 4104, 32, False, "e4m3"), (17, 5888, 5712, 128, False, "e4m3"),
+    (33, 4832, 4640, 32, True, "e4m3"), (48, 4800, 4672, 64, True, "bf16"), (64, 4160, 4104, 64, False, "bf16"),
+    (64, 4096, 4080, 128, True, "bf16")])
+def test_matvec_of_large_matrices(h, T, K, N, group, zeros, kind):
+    g = gen(T + K + N)
+    x, xs = matvec_inputs(g, T, K, kind)
+    out, intact = guarded(T, N)
+    check_matvec(h, x, xs, packed(g, (), K, N, group, zeros), group, out, space(h.matvec_q4_workspace(T, N)), intact)
+
+
+# few columns (their rows are shared out to several CTAs) and many (smaller CTAs)
+@pytest.mark.parametrize("K,N,group", [(28672, 16, 128), (16416, 48, 32), (4224, 1040, 64), (2176, 2432, 128), (512, 8208, 64),
+                                       (160, 20000, 32)])
+@pytest.mark.parametrize("T,kind", [(1, "bf16"), (7, "e4m3"), (12, "bf16"), (16, "e4m3"), (40, "bf16")])
+def test_matvec_of_few_and_many_columns(h, K, N, group, T, kind):
+    g = gen(T + K + N)
+    x, xs = matvec_inputs(g, T, K, kind)
+    out, intact = guarded(T, N)
+    w = packed(g, (), K, N, group, T != 12)
+    ws = space(h.matvec_q4_workspace(T, N))
+    check_matvec(h, x, xs, w, group, out, ws, intact)
+    first = out.clone()
+    h.matvec_q4(x, w[0], w[1], group, out, ws, zero=w[2], x_scale=xs)
+    assert torch.equal(out, first)
+
+
+def test_matvec_of_large_matrices_takes_any_magnitude(h):
+    g = gen(25)
+    K, N, T = 4096, 4112, 64
+    x = randn(g, T, K, dtype=F32)
+    x *= torch.exp2(torch.randint(-100, 100, (T, 1), generator=g, device=DEV).float())
+    x[3] *= torch.exp2(torch.randint(-20, 20, (K,), generator=g, device=DEV).float())
+    x[5], x[6, :2048], x[7, 40], x[8, 41] = 0, 0, float("inf"), float("nan")
+    w = packed(g, (), K, N, 128, True)
+    w = (w[0], (w[1].float() * 2.0 ** -8).to(BF16), w[2])
+    out, ws = torch.empty(T, N, dtype=BF16, device=DEV), space(h.matvec_q4_workspace(T, N))
+    h.matvec_q4(x.to(BF16), w[0], w[1], 128, out, ws, zero=w[2])
+    assert torch.isnan(out[8].float()).all() and not torch.isfinite(out[7].float()).any()
+    keep = [i for i in range(T) if i not in (7, 8)]
+    clean = x.clone()
+    clean[7], clean[8] = 1, 1
+    again = torch.empty_like(out)
+    check_matvec(h, clean.to(BF16), None, w, 128, again, ws)
+    assert torch.equal(out[keep], again[keep])
+
+
 def test_norm_rows_feed_the_matvec(h):
     """The 8-bit rows and scales of the norm are the 8-bit rows and scales that the product takes."""
     g = gen(23)
