@@ -1,4 +1,5 @@
-// moe_decode.cu -- a whole gated expert layer for up to 64 tokens in one kernel.
+// moe_decode.cu -- a whole gated expert layer for up to 64 tokens in one kernel
+// (moe_direct.cu has the small ones; use_direct_moe is the rule).
 //
 //   h[t, e]  = silu(x[t] W13[e][:, :I]) * (x[t] W13[e][:, I:])      for the experts e that token t names
 //   out[t]   = sum over those e of gate[t, e] * (h[t, e] W2[e])

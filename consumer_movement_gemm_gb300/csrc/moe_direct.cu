@@ -1,0 +1,500 @@
+// moe_direct.cu -- the expert layer of moe_decode.cu where its time is latency:
+// two kernels without rings, counters or grid barriers.
+//
+// The first gives h = silu(x W13[e][:, :I]) * (x W13[e][:, I:]), a CTA 32 (4-bit
+// weights: 16) of its columns for one expert, gate and up columns side by side
+// in one tile.  The second gives 64 (32) columns of the result, the sums over
+// all experts and rows of W2 shared out to its warps as one list; a warp adds
+// what it has to the CTA's sums in shared memory, times the gate weight, each
+// time its expert changes.  Warps read their weights straight into registers,
+// a block ahead of the one that is multiplied; with few tiles a cluster of two
+// or four CTAs shares out the rows and its first CTA gets the others' sums.  The
+// second kernel reads the routing and its first weights while the first ends.
+//
+// Eight tokens at a time are the columns of the tensor core's second operand,
+// whether or not they name the expert (zeros, and their results dropped), so
+// nothing is gathered.  More tokens are more CTAs, which find the weights of
+// experts that they share in L2.
+//
+// h is fp32 in memory.  With bf16 weights it enters the second product as two
+// bf16 numbers, its rounding and the rest; with 4-bit weights as fp16 with a
+// power of two per 128 columns.  Sums are fp32, in a fixed order.
+#include <type_traits>
+#include "launch.cuh"
+#include "skinny.cuh"
+
+namespace tovl {
+
+namespace {
+
+using namespace skinny;
+
+constexpr int kWarps = 16;             // at most; CTAs of 8 share an SM
+constexpr int kTokens = 8;
+constexpr int kCluster = 4;
+constexpr int kMaxActive = kTokens * kMaxDecodeK;
+
+struct Routing {
+    uint32_t mask[kMaxExperts];        // tokens of each expert
+    int id[kTokens * kMaxDecodeK];
+    float gate[kTokens * kMaxDecodeK];
+    int active[kMaxActive];            // the experts with tokens, ascending
+    int n;
+};
+
+// Routing of the tokens t0 .. t0 + cnt.  False if an id (of any token) is
+// outside [-1, E).
+__device__ bool read_routing(const MoeParams& p, Routing& rt, int t0, int cnt)
+{
+    const int tid = threadIdx.x;
+    bool bad = false;
+    for (int i = tid; i < p.T * p.k; i += blockDim.x) {
+        const int e = __ldcg(p.topk + i);
+        bad |= e < -1 || e >= p.E;
+    }
+    for (int e = tid; e < p.E; e += blockDim.x) rt.mask[e] = 0;
+    const bool own = tid < cnt * p.k;
+    int id = -1;
+    if (own) {
+        id = __ldcg(p.topk + t0 * p.k + tid);
+        rt.id[tid] = id;
+        rt.gate[tid] = __ldcg(p.gate_w + t0 * p.k + tid);
+    }
+    if (__syncthreads_or(bad)) return false;
+    if (id >= 0) atomicOr(rt.mask + id, 1u << (tid / p.k));
+    __syncthreads();
+    if (tid < 32) {
+        int n = 0;
+        for (int base = 0; base < p.E; base += 32) {
+            const bool on = base + tid < p.E && rt.mask[base + tid];
+            const uint32_t m = __ballot_sync(0xffffffffu, on);
+            if (on) rt.active[n + __popc(m & ((1u << tid) - 1))] = base + tid;
+            n += __popc(m);
+        }
+        if (tid == 0) rt.n = n;
+    }
+    __syncthreads();
+    return true;
+}
+
+// The slot of token t that names e first (-1: none), and the weights of all that do.
+__device__ __forceinline__ int find_slot(const MoeParams& p, const Routing& rt, int t, int e, float& gate)
+{
+    int first = -1;
+    gate = 0.f;
+    for (int j = 0; j < p.k; ++j)
+        if (rt.id[t * p.k + j] == e) {
+            if (first < 0) first = j;
+            gate += rt.gate[t * p.k + j];
+        }
+    return first;
+}
+
+// A lane's part of a block of weights.  bf16: rows 8t .. 8t + 7 of 32, eight
+// columns.  4-bit: octet rows t, t + 4, .. of 128 rows, four columns.
+template <int G, bool Z>
+struct Weights {
+    static constexpr int kRows = 128, kLaneCols = 4, kGroups = 128 / G;
+    uint4 w[4];
+    uint2 scale[kGroups];
+    uint32_t zero[kGroups];
+
+    __device__ __forceinline__ void load(const MoeWeights& m, int e, int b, int K, int N, int n, bool col, int t)
+    {
+        const long long row = static_cast<long long>(e) * (K / 8);
+#pragma unroll
+        for (int R = 0; R < 4; ++R) {
+            const int octet = b * 16 + 4 * R + t;
+            w[R] = make_uint4(0, 0, 0, 0);
+            if (col && octet * 8 < K) w[R] = ld_stream(static_cast<const uint32_t*>(m.w) + (row + octet) * N + n);
+        }
+        const long long group = static_cast<long long>(e) * (K / G) + b * kGroups;
+#pragma unroll
+        for (int q = 0; q < kGroups; ++q) {
+            const bool in = col && b * 128 + q * G < K;
+            const long long at = (group + q) * N + n;
+            scale[q] = in ? __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(m.scale) + at)) : make_uint2(0, 0);
+            zero[q] = Z && in ? __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(m.zero) + at)) : 0u;
+        }
+    }
+};
+template <>
+struct Weights<0, false> {
+    static constexpr int kRows = 32, kLaneCols = 8;
+    uint4 w[8];
+
+    __device__ __forceinline__ void load(const MoeWeights& m, int e, int b, int K, int N, int n, bool col, int t)
+    {
+        const int k = b * 32 + 8 * t;
+        const __nv_bfloat16* at = static_cast<const __nv_bfloat16*>(m.w) + (static_cast<long long>(e) * K + k) * N + n;
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            w[r] = col && k < K ? ld_stream(reinterpret_cast<const uint32_t*>(at + static_cast<long long>(r) * N)) : make_uint4(0, 0, 0, 0);
+    }
+};
+
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+// Sums of a warp: token columns 2t, 2t + 1 of the lane group's four or eight
+// weight columns.
+template <int G, bool Z>
+struct Sums {
+    static constexpr int kTiles = G ? 2 : 4;
+    static constexpr int kCols = G ? 32 : 64;
+    float v[kTiles][1][4];
+
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[m][0][i] = 0.f;
+    }
+
+    // bf16: two steps of 16 rows, column pair m of the lanes is the tile m; the rows'
+    // pairs of a column come out of two rows' words by byte permutation
+    template <bool LO>
+    __device__ __forceinline__ void add(const Weights<0, false>& a, const uint4& b, const uint4& lo)
+    {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const uint32_t r0 = word(a.w[4 * s], m), r1 = word(a.w[4 * s + 1], m);
+                const uint32_t r2 = word(a.w[4 * s + 2], m), r3 = word(a.w[4 * s + 3], m);
+                const uint32_t a0 = __byte_perm(r0, r1, 0x5410), a1 = __byte_perm(r0, r1, 0x7632);
+                const uint32_t a2 = __byte_perm(r2, r3, 0x5410), a3 = __byte_perm(r2, r3, 0x7632);
+                mma(v[m][0], a0, a1, a2, a3, s ? b.z : b.x, s ? b.w : b.y);
+                if (LO) mma(v[m][0], a0, a1, a2, a3, s ? lo.z : lo.x, s ? lo.w : lo.y);
+            }
+    }
+
+    // column 0 .. of the lane group for token 2t + j, four of them (half: the next four)
+    __device__ __forceinline__ float4 four(int j, int half) const
+    {
+        const int m = half * 2;
+        return make_float4(v[m][0][j], v[m][0][j + 2], v[m + 1][0][j], v[m + 1][0][j + 2]);
+    }
+};
+
+// The warps' sums of a CTA, [token][column] a warp.  Fours of columns are
+// stored by (half, group ^ 2t), which keeps a quarter warp's in different banks.
+template <int COLS>
+struct Joined {
+    float red[kWarps][kTokens][COLS];
+    float join[kCluster - 1][kTokens][COLS];
+
+    static __device__ __forceinline__ int four_of(int g, int half, int t) { return half * 8 + (g ^ (2 * t)); }
+    static __device__ __forceinline__ int place(int r, int c)
+    {
+        const int g = COLS == 64 ? c >> 3 : c >> 2, half = COLS == 64 ? (c >> 2) & 1 : 0;
+        return four_of(g, half, (r >> 1) & 3) * 4 + (c & 3);
+    }
+    __device__ __forceinline__ float4& at(int warp, int g, int t, int j, int half)
+    {
+        return *reinterpret_cast<float4*>(&red[warp][2 * t + j][four_of(g, half, t) * 4]);
+    }
+    __device__ __forceinline__ float sum(int r, int c, int warps) const
+    {
+        const int at = place(r, c);
+        float v = 0.f;
+#pragma unroll
+        for (int i = 0; i < kWarps / 2; ++i) v += red[i][r][at];
+        if (warps > kWarps / 2) {
+#pragma unroll
+            for (int i = kWarps / 2; i < kWarps; ++i) v += red[i][r][at];
+        }
+        return v;
+    }
+    // The CTA's sums to the first CTA of the cluster.  False in the others.
+    __device__ __forceinline__ bool gather(int rank, int split, int rows, int warps)
+    {
+        if (split == 1) return true;
+        __syncwarp();
+        ptx::cluster_wait();           // the first CTA runs
+        if (rank > 0)
+            for (int i = threadIdx.x; i < rows * COLS; i += blockDim.x) {
+                const int r = i / COLS, c = i % COLS;
+                st_cluster_f32(ptx::mapa_shared(ptx::smem_u32(&join[rank - 1][r][c]), 0), sum(r, c, warps));
+            }
+        __syncwarp();
+        ptx::cluster_sync();
+        return rank == 0;
+    }
+    __device__ __forceinline__ float total(int r, int c, int split, int warps) const
+    {
+        float v = sum(r, c, warps);
+        for (int i = 1; i < split; ++i) v += join[i - 1][r][c];
+        return v;
+    }
+};
+
+__device__ __forceinline__ uint32_t max_exponent(const float4& v)
+{
+    const uint32_t a = max(__float_as_uint(v.x) & 0x7f800000u, __float_as_uint(v.y) & 0x7f800000u);
+    const uint32_t b = max(__float_as_uint(v.z) & 0x7f800000u, __float_as_uint(v.w) & 0x7f800000u);
+    return max(a, b) >> 23;
+}
+
+// Scale of this lane's token g to those of the sums' tokens 2t and 2t + 1.
+__device__ __forceinline__ float2 of_sums(float v, int t)
+{
+    return make_float2(__shfl_sync(0xffffffffu, v, 8 * t), __shfl_sync(0xffffffffu, v, 8 * t + 4));
+}
+
+// Largest of a lane's four (its token's part of 128 columns).
+__device__ __forceinline__ uint32_t max_of_token(uint32_t e)
+{
+    e = max(e, __shfl_xor_sync(0xffffffffu, e, 1));
+    return max(e, __shfl_xor_sync(0xffffffffu, e, 2));
+}
+
+// Two numbers as bf16 pairs: their roundings and what those left over (nothing,
+// where a number has overflowed).
+__device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint32_t& lo)
+{
+    hi = ptx::pack_bf16x2(a, b);
+    const float da = a - bf16_lo(hi), db = b - bf16_hi(hi);
+    lo = ptx::pack_bf16x2(fabsf(da) < INFINITY ? da : 0.f, fabsf(db) < INFINITY ? db : 0.f);
+}
+
+// grid: tiles of columns, CTAs of a cluster, (eight tokens, expert of theirs)
+template <int G, bool Z>
+__global__ void __launch_bounds__(kWarps * 32, 1) moe_up_kernel(const __grid_constant__ MoeParams p, int most_active)
+{
+    using W = Weights<G, Z>;
+    using S = Sums<G, Z>;
+    constexpr int kHalf = S::kCols / 2;
+    __shared__ Routing rt;
+    __shared__ __align__(16) Joined<S::kCols> sums;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int warps = blockDim.x >> 5, split = gridDim.y, rank = blockIdx.y;
+    const int t0 = blockIdx.z / most_active * kTokens, cnt = min(kTokens, p.T - t0), a = blockIdx.z % most_active;
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    if (!read_routing(p, rt, t0, cnt)) {
+        if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) record_error(p.ctrl, kErrInvalid);
+        return;
+    }
+    if (a >= rt.n) return;
+    if (split > 1) ptx::cluster_arrive_relaxed();
+    const int e = rt.active[a];
+    const bool use = rt.mask[e] >> g & 1;
+    const int i0 = blockIdx.x * kHalf, in_half = i0 + (g & 3) * W::kLaneCols, n = (g >> 2) * p.I + in_half;
+    const bool col = in_half < p.I;
+    const int blocks = (p.H + W::kRows - 1) / W::kRows, stride = warps * split;
+    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x) + (t0 + g) * p.ldx;
+    S acc;
+    acc.clear();
+    W next;
+    constexpr int kOctets = W::kRows / 32;
+    uint4 next_x[kOctets];
+    const auto fetch = [&](int b) {
+        next.load(p.up, e, b, p.H, 2 * p.I, n, col, t);
+#pragma unroll
+        for (int R = 0; R < kOctets; ++R) {
+            const int k = b * W::kRows + 32 * R + 8 * t;
+            next_x[R] = use && k < p.H ? __ldg(reinterpret_cast<const uint4*>(x + k)) : make_uint4(0, 0, 0, 0);
+        }
+    };
+    int b = rank * warps + warp;
+    if (b < blocks) fetch(b);
+    for (; b < blocks; b += stride) {
+        const W w = next;
+        uint4 xb[kOctets];
+#pragma unroll
+        for (int R = 0; R < kOctets; ++R) xb[R] = next_x[R];
+        if (b + stride < blocks) fetch(b + stride);
+        if constexpr (G == 0) {
+            acc.template add<false>(w, xb[0], xb[0]);
+        } else {
+            uint32_t ex = 0;
+#pragma unroll
+            for (int R = 0; R < 4; ++R) ex = max(ex, skinny::max_exponent(xb[R]));
+            ex = max_of_token(ex);
+            const float f = half_scale(ex);
+#pragma unroll
+            for (int R = 0; R < 4; ++R) xb[R] = bf16x8_to_half(xb[R], f);
+            const float2 sx[1] = {of_sums(half_unscale(ex), t)};
+            multiply_q4<1, G, Z>(
+                acc.v, sx, [&](int R) { return w.w[R]; }, [&](int q) { return w.zero[q]; }, [&](int q) { return w.scale[q]; },
+                [&](int R, int) { return xb[R]; });
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int half = 0; half < S::kTiles / 2; ++half) sums.at(warp, g, t, j, half) = acc.four(j, half);
+    __syncthreads();
+    if (!sums.gather(rank, split, cnt, warps)) return;
+    for (int i = threadIdx.x; i < cnt * kHalf; i += blockDim.x) {
+        const int r = i / kHalf, c = i % kHalf;
+        float gate;
+        const int j = find_slot(p, rt, r, e, gate);
+        if (j < 0 || i0 + c >= p.I) continue;
+        const float v = sums.total(r, c, split, warps), u = sums.total(r, kHalf + c, split, warps);
+        static_cast<float*>(p.h_hi)[((t0 + r) * p.k + j) * static_cast<long long>(p.I) + i0 + c] = v / (1.f + expf(-v)) * u;
+    }
+}
+
+// grid: tiles of columns, CTAs of a cluster, eight tokens
+template <int G, bool Z>
+__global__ void __launch_bounds__(kWarps * 32, 1) moe_down_kernel(const __grid_constant__ MoeParams p)
+{
+    using W = Weights<G, Z>;
+    using S = Sums<G, Z>;
+    __shared__ Routing rt;
+    __shared__ __align__(16) Joined<S::kCols> sums;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int warps = blockDim.x >> 5, split = gridDim.y, rank = blockIdx.y;
+    const int t0 = blockIdx.z * kTokens, cnt = min(kTokens, p.T - t0);
+    // (what came before the first kernel is complete: that kernel has waited for
+    // it before it let this one start)
+    if (!read_routing(p, rt, t0, cnt)) {
+        ptx::grid_dep_wait();
+        return;
+    }
+    if (split > 1) ptx::cluster_arrive_relaxed();
+    const int n = blockIdx.x * S::kCols + g * W::kLaneCols;
+    const bool col = n < p.H;
+    const int per = (p.I + W::kRows - 1) / W::kRows;      // blocks of an expert
+    const int items = rt.n * per, share = rank * warps + warp, shares = warps * split;
+    int item = items * share / shares;
+    const int end = items * (share + 1) / shares;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int half = 0; half < S::kTiles / 2; ++half) sums.at(warp, g, t, j, half) = make_float4(0.f, 0.f, 0.f, 0.f);
+    W next;
+    int a = item / per, b = item - a * per;
+    if (item < end) next.load(p.down, rt.active[a], b, p.I, p.H, n, col, t);
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    S acc;
+    acc.clear();
+    const float* h = nullptr;          // this lane's token's row for the expert; null: it does not name it
+    float gate = 0.f;
+    bool fresh = true;
+    for (; item < end; ++item) {
+        const W w = next;
+        if (fresh) {
+            const int j = g < cnt ? find_slot(p, rt, g, rt.active[a], gate) : -1;
+            h = j < 0 ? nullptr : static_cast<const float*>(p.h_hi) + ((t0 + g) * p.k + j) * static_cast<long long>(p.I);
+        }
+        constexpr int kOctets = W::kRows / 32;
+        float4 lo4[kOctets], hi4[kOctets];
+#pragma unroll
+        for (int R = 0; R < kOctets; ++R) {
+            const int k = b * W::kRows + 32 * R + 8 * t;
+            const bool in = h && k < p.I;
+            lo4[R] = in ? __ldcg(reinterpret_cast<const float4*>(h + k)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            hi4[R] = in ? __ldcg(reinterpret_cast<const float4*>(h + k + 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        int na = a, nb = b + 1;
+        if (nb == per) na = a + 1, nb = 0;
+        if (item + 1 < end) next.load(p.down, rt.active[na], nb, p.I, p.H, n, col, t);
+        if constexpr (G == 0) {
+            uint4 x, rest;
+            split_pair(lo4[0].x, lo4[0].y, x.x, rest.x);
+            split_pair(lo4[0].z, lo4[0].w, x.y, rest.y);
+            split_pair(hi4[0].x, hi4[0].y, x.z, rest.z);
+            split_pair(hi4[0].z, hi4[0].w, x.w, rest.w);
+            acc.template add<true>(w, x, rest);
+        } else {
+            uint32_t ex = 0;
+#pragma unroll
+            for (int R = 0; R < 4; ++R) ex = max(ex, max(max_exponent(lo4[R]), max_exponent(hi4[R])));
+            ex = max_of_token(ex);
+            const float f = half_scale(ex);
+            uint4 x[4];
+#pragma unroll
+            for (int R = 0; R < 4; ++R)
+                x[R] = make_uint4(pack_h2(lo4[R].x * f, lo4[R].y * f), pack_h2(lo4[R].z * f, lo4[R].w * f),
+                                  pack_h2(hi4[R].x * f, hi4[R].y * f), pack_h2(hi4[R].z * f, hi4[R].w * f));
+            const float2 sx[1] = {of_sums(half_unscale(ex), t)};
+            multiply_q4<1, G, Z>(
+                acc.v, sx, [&](int R) { return w.w[R]; }, [&](int q) { return w.zero[q]; }, [&](int q) { return w.scale[q]; },
+                [&](int R, int) { return x[R]; });
+        }
+        fresh = na != a;
+        if (fresh || item + 1 == end) {
+            const float2 gates = of_sums(gate, t);
+            const uint32_t named = __ballot_sync(0xffffffffu, h != nullptr);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (named >> (8 * t + 4 * j) & 1) {
+                    const float w1 = j ? gates.y : gates.x;
+#pragma unroll
+                    for (int half = 0; half < S::kTiles / 2; ++half) {
+                        float4& s = sums.at(warp, g, t, j, half);
+                        const float4 v = acc.four(j, half);
+                        s = make_float4(fmaf(w1, v.x, s.x), fmaf(w1, v.y, s.y), fmaf(w1, v.z, s.z), fmaf(w1, v.w, s.w));
+                    }
+                }
+            acc.clear();
+        }
+        a = na;
+        b = nb;
+    }
+    __syncthreads();
+    if (!sums.gather(rank, split, cnt, warps)) return;
+    for (int i = threadIdx.x; i < cnt * S::kCols; i += blockDim.x) {
+        const int r = i / S::kCols, c = i % S::kCols, at = blockIdx.x * S::kCols + c;
+        if (at < p.H) static_cast<__nv_bfloat16*>(p.out)[(t0 + r) * p.ldo + at] = __float2bfloat16(sums.total(r, c, split, warps));
+    }
+}
+
+// One CTA of 16 warps per SM where that is all of them, else CTAs of 8, two on
+// an SM; clusters as long as they fit the SMs and leave each warp a block.
+cudaLaunchConfig_t shape(cudaLaunchAttribute (&attr)[2], int tiles, int z, int blocks, int sms, cudaStream_t stream, bool pdl)
+{
+    const int warps = tiles * z <= sms ? kWarps : kWarps / 2;
+    int split = 1;
+    while (split < kCluster && tiles * z * split * 2 <= sms && split * warps < blocks) split *= 2;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(tiles, split, z);
+    lc.blockDim = dim3(warps * 32);
+    lc.stream = stream;
+    lc.attrs = attr;
+    if (split > 1) {
+        attr[lc.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attr[lc.numAttrs].val.clusterDim.x = 1;
+        attr[lc.numAttrs].val.clusterDim.y = split;
+        attr[lc.numAttrs].val.clusterDim.z = 1;
+        ++lc.numAttrs;
+    }
+    if (pdl) {
+        attr[lc.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[lc.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+        ++lc.numAttrs;
+    }
+    return lc;
+}
+
+template <int G, bool Z>
+cudaError_t launch(const MoeParams& p, int sms, cudaStream_t stream, bool pdl)
+{
+    constexpr int kCols = Sums<G, Z>::kCols, kRows = Weights<G, Z>::kRows;
+    const int passes = (p.T + kTokens - 1) / kTokens, names = (p.T < kTokens ? p.T : kTokens) * p.k;
+    const int active = names < p.E ? names : p.E;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t lc = shape(attr, (2 * p.I + kCols - 1) / kCols, passes * active, (p.H + kRows - 1) / kRows, sms, stream, pdl);
+    const cudaError_t e = cudaLaunchKernelEx(&lc, moe_up_kernel<G, Z>, p, active);
+    if (e != cudaSuccess) return e;
+    lc = shape(attr, (p.H + kCols - 1) / kCols, passes, active * ((p.I + kRows - 1) / kRows), sms, stream, pdl);
+    return cudaLaunchKernelEx(&lc, moe_down_kernel<G, Z>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_moe_direct(const MoeParams& p, int group, bool zero, int sms, cudaStream_t stream, bool pdl)
+{
+    switch (group) {
+    case 32: return zero ? launch<32, true>(p, sms, stream, pdl) : launch<32, false>(p, sms, stream, pdl);
+    case 64: return zero ? launch<64, true>(p, sms, stream, pdl) : launch<64, false>(p, sms, stream, pdl);
+    case 128: return zero ? launch<128, true>(p, sms, stream, pdl) : launch<128, false>(p, sms, stream, pdl);
+    default: return launch<0, false>(p, sms, stream, pdl);
+    }
+}
+
+}  // namespace tovl

@@ -60,8 +60,16 @@ struct WeightMaps {
     CUtensorMap w, scale, zero;
 };
 
+// The same as addresses.
+struct MoeWeights {
+    const void* w;
+    const void* scale;
+    const void* zero;
+};
+
 struct MoeParams {
     WeightMaps w13, w2;
+    MoeWeights up, down;    // W13, W2
     const void* x;          // bf16 [T][H], rows ldx apart
     long long ldx;
     const int* topk;        // [T][k]
@@ -79,6 +87,19 @@ struct MoeParams {
     long long timeout_ns, pipe_timeout_ns;
     Ctrl ctrl;
 };
+// Expert layers without rings and barriers: those of fewer than 2^26 weights,
+// counted for the experts that eight tokens can name, once per eight tokens.
+// Below the rule (direct and through the rings): 1 token, 2 of 8 experts, 4096 x
+// 2048, bf16 24.6 and 32.1 us, 4-bit 16.2 and 21.9; 8 tokens of 2048 x 1024 23.6
+// and 29.3, 17.4 and 21.7; 1 token of 256 x 128 5.5 and 14.9.  Above it: 16 tokens
+// of 2048 x 1024 38.1 and 32.4, 26.6 and 22.6; 4 tokens of 4096 x 2048 69 and 61,
+// 39.7 and 34.3; 64 tokens of 1024 x 512 33 and 25, 31 and 24.
+inline bool use_direct_moe(int T, int k, int E, int H, int I)
+{
+    const int names = (T < 8 ? T : 8) * k;
+    return 3LL * ((T + 7) / 8) * (names < E ? names : E) * H * I < (1LL << 26);
+}
+cudaError_t launch_moe_direct(const MoeParams& p, int group, bool zero, int sms, cudaStream_t stream, bool pdl);
 cudaError_t prepare_moe_decode();
 // group: rows per scale of 4-bit weights, 0 for bf16
 cudaError_t launch_moe_decode(const MoeParams& p, int group, bool zero, int grid, cudaStream_t stream, bool cooperative,

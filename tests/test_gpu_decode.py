@@ -505,6 +505,69 @@ def test_moe_q4_matches_the_formula(h, T, E, k, H, I, group, zeros):
               quant=group)
 
 
+# both sides of 2^26 weights (counted for the experts of eight tokens, once per eight tokens), where other kernels begin
+@pytest.mark.parametrize("T,E,k,H,I,group,zeros", [
+    (1, 2, 1, 7168, 3136, 0, False), (1, 2, 1, 7168, 3112, 0, False), (7, 3, 2, 3592, 2088, 0, False), (9, 4, 4, 2056, 1368, 0, False),
+    (17, 2, 2, 4096, 920, 0, False), (33, 3, 2, 2048, 744, 0, False), (40, 16, 2, 1032, 296, 0, False), (64, 2, 2, 1544, 912, 0, False),
+    (64, 8, 2, 1024, 360, 0, False), (64, 8, 2, 1024, 336, 0, False),
+    (1, 3, 2, 4096, 2752, 64, True), (1, 3, 2, 4096, 2688, 64, True), (8, 4, 4, 2176, 2688, 128, False), (15, 2, 2, 3200, 1792, 128, True),
+    (17, 2, 2, 4064, 928, 32, False), (33, 3, 2, 2048, 768, 128, True), (48, 16, 4, 1024, 320, 64, False), (64, 8, 2, 1024, 352, 32, True)])
+def test_moe_of_large_experts(h, T, E, k, H, I, group, zeros):
+    g = gen(T + E + H + I)
+    topk, gate = routing(g, T, E, k)
+    if group:
+        w = packed(g, (E,), H, 2 * I, group, zeros), packed(g, (E,), I, H, group, zeros)
+    else:
+        w = bf16_experts(g, E, H, I)
+    check_moe(h, randn(g, T, H), topk, gate, *w, quant=group or None)
+
+
+# few columns (their rows are shared out to several CTAs), many experts, one long axis
+@pytest.mark.parametrize("T,E,k,H,I", [(1, 2, 1, 8192, 32), (3, 2, 1, 32, 8192), (2, 4, 2, 4128, 96), (8, 64, 16, 96, 64),
+                                       (11, 512, 4, 64, 32), (1, 4, 4, 2112, 1056), (16, 3, 1, 704, 32)])
+@pytest.mark.parametrize("quant", [None, 32])
+def test_moe_of_few_columns(h, T, E, k, H, I, quant):
+    g = gen(T + E + H + I)
+    topk, gate = routing(g, T, E, k)
+    w = bf16_experts(g, E, H, I) if quant is None else (packed(g, (E,), H, 2 * I, quant, True), packed(g, (E,), I, H, quant, True))
+    x = randn(g, T, H)
+    first = check_moe(h, x, topk, gate, *w, quant=quant).clone()
+    assert torch.equal(check_moe(h, x, topk, gate, *w, quant=quant), first)
+
+
+@pytest.mark.parametrize("T,H,I", [(20, 192, 128), (20, 2560, 1600)])
+@pytest.mark.parametrize("quant", [None, 64])
+def test_moe_special_cases_of_routing_and_values(h, T, H, I, quant):
+    """Missing and repeated experts, tokens without any, infinities and NaN in tokens and in one expert's weights:
+    small and large experts."""
+    g = gen(37)
+    E, k = 7, 3
+    topk, gate = routing(g, T, E - 1, k)
+    topk[torch.rand(T, k, generator=g, device=DEV) < 0.3] = -1
+    topk[0], topk[1] = -1, 2
+    topk[5, 1], gate[5, 1] = 6, 0.5               # expert 6 is token 5's alone
+    gate[topk < 0] = float("nan")
+    w = bf16_experts(g, E, H, I) if quant is None else (packed(g, (E,), H, 2 * I, quant, True), packed(g, (E,), I, H, quant, True))
+    x = randn(g, T, H)
+    clean = check_moe(h, x, topk, gate, *w, quant=quant).clone()
+    assert (clean[0] == 0).all()
+    # the same call (the order of the sums depends on which experts are named) with NaN and infinities in expert 6
+    for m in w:
+        (m if quant is None else m[1])[6] = float("nan")
+    (w[0] if quant is None else w[0][1])[6, 0] = float("inf")
+    x[9, 3], x[10, 0] = float("inf"), float("nan")
+    out, ws = torch.empty_like(clean), space(h.moe_decode_workspace(T, k, H, I))
+    if quant is None:
+        h.moe_decode(x, topk, gate, *w, out, ws)
+    else:
+        h.moe_decode_q4(x, topk, gate, *w, quant, out, ws)
+    assert h.sync_status() == 0
+    hit = {5} | {t for t in (9, 10) if (topk[t] >= 0).any()}
+    keep = [t for t in range(T) if t not in (5, 9, 10)]
+    assert torch.equal(out[keep], clean[keep])
+    assert not torch.isfinite(out[sorted(hit)].float()).any()
+
+
 @pytest.mark.parametrize("quant", [None, 64])
 def test_moe_missing_and_repeated_experts(h, quant):
     g = gen(31)
