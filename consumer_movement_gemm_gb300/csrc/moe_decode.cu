@@ -258,26 +258,33 @@ struct Worker {
         }
     }
 
+    // Four columns of a token to a thread; with few tokens to up to eight
+    // neighbouring lanes, which share out its experts (one token, four experts
+    // of 7168 columns: 3.0 us with one lane, 1.6 with four).
     __device__ __forceinline__ void outputs()
     {
-        const int quads = p.H / 4;
+        const int quads = p.H / 4, total = p.T * quads;
         const long long stride = static_cast<long long>(p.T) * p.k * p.H;
-        for (int i = spread_thread(); i < p.T * quads; i += gridDim.x * P::kThreads) {
-            const int t = i / quads, n = (i - t * quads) * 4;
+        const int threads = gridDim.x * P::kThreads, me = spread_thread();
+        int log = 0;
+        while (log < 3 && 1 << log < p.k && total << (log + 1) <= threads) ++log;
+        const int lanes = 1 << log, own = me & (lanes - 1);
+        for (int base = (me & ~31) >> log; base < total; base += threads >> log) {       // (a warp goes on together)
+            const int i = base + ((me & 31) >> log), q = min(i, total - 1), t = q / quads, n = (q - t * quads) * 4;
             float4 out4 = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int j = 0; j < p.k; j += 2) {      // two slots' parts together
+            for (int j = own; j < p.k; j += 2 * lanes) {      // two slots' parts together
                 const float* part[2];
                 int count[2];
                 float w[2];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const int row = j + u < p.k ? tb.pair_row[t * p.k + j + u] : -1;
+                    const int slot = j + u * lanes, row = slot < p.k ? tb.pair_row[t * p.k + slot] : -1;
                     part[u] = p.part;
                     count[u] = 0;
                     w[u] = 0.f;
                     if (row >= 0) {
                         part[u] = parts(1, row, n, p.H, count[u]);
-                        w[u] = tb.pair_w[t * p.k + j + u];
+                        w[u] = tb.pair_w[t * p.k + slot];
                     }
                 }
                 float4 s[2];
@@ -287,6 +294,11 @@ struct Worker {
                     if (count[u])
                         out4.x += w[u] * s[u].x, out4.y += w[u] * s[u].y, out4.z += w[u] * s[u].z, out4.w += w[u] * s[u].w;
             }
+            for (int d = 1; d < lanes; d *= 2) {
+                out4.x += __shfl_xor_sync(0xffffffffu, out4.x, d), out4.y += __shfl_xor_sync(0xffffffffu, out4.y, d);
+                out4.z += __shfl_xor_sync(0xffffffffu, out4.z, d), out4.w += __shfl_xor_sync(0xffffffffu, out4.w, d);
+            }
+            if (own > 0 || i >= total) continue;
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + t * p.ldo + n;
             if (p.out_vec) {
                 *reinterpret_cast<uint2*>(out) = make_uint2(ptx::pack_bf16x2(out4.x, out4.y), ptx::pack_bf16x2(out4.z, out4.w));
