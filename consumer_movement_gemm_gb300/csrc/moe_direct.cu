@@ -1,5 +1,6 @@
 // moe_direct.cu -- the expert layer of moe_decode.cu where its time is latency:
-// two kernels without rings, counters or grid barriers.
+// two kernels without rings, counters or grid barriers (use_direct_moe is the
+// rule).
 //
 // The first gives h = silu(x W13[e][:, :I]) * (x W13[e][:, I:]), a CTA 32 (4-bit
 // weights: 16) of its columns for one expert, gate and up columns side by side
@@ -11,14 +12,20 @@
 // or four CTAs shares out the rows and its first CTA gets the others' sums.  The
 // second kernel reads the routing and its first weights while the first ends.
 //
-// Eight tokens at a time are the columns of the tensor core's second operand,
-// whether or not they name the expert (zeros, and their results dropped), so
-// nothing is gathered.  More tokens are more CTAs, which find the weights of
-// experts that they share in L2.
+// Eight tokens at a time (of more than eight, sixteen) are the columns of the
+// tensor core's second operand, whether or not they name the expert (zeros, and
+// their results dropped), so nothing is gathered.  More tokens are more CTAs,
+// which find the weights of experts that they share in L2.
 //
 // h is fp32 in memory.  With bf16 weights it enters the second product as two
 // bf16 numbers, its rounding and the rest; with 4-bit weights as fp16 with a
 // power of two per 128 columns.  Sums are fp32, in a fixed order.
+//
+// What bounds it: at small sizes two launches and a CTA's dependent loads (1
+// token, 256 x 128: 5.3 us, 1024 x 512: 7.7, through the rings 14.9 and 19.8); at
+// large ones the bytes in flight, one block a warp (1 token, 2 of 8 experts of
+// 4096 x 2048, bf16: 24.4 us, 4.1 TB/s, through the rings 31.9).  Two blocks a warp
+// spill registers: 27.1.
 #include <type_traits>
 #include "launch.cuh"
 #include "skinny.cuh"
@@ -30,14 +37,14 @@ namespace {
 using namespace skinny;
 
 constexpr int kWarps = 16;             // at most; CTAs of 8 share an SM
-constexpr int kTokens = 8;
+constexpr int kMaxTokens = 16;
 constexpr int kCluster = 4;
-constexpr int kMaxActive = kTokens * kMaxDecodeK;
+constexpr int kMaxActive = kMaxTokens * kMaxDecodeK;
 
 struct Routing {
     uint32_t mask[kMaxExperts];        // tokens of each expert
-    int id[kTokens * kMaxDecodeK];
-    float gate[kTokens * kMaxDecodeK];
+    int id[kMaxTokens * kMaxDecodeK];
+    float gate[kMaxTokens * kMaxDecodeK];
     int active[kMaxActive];            // the experts with tokens, ascending
     int n;
 };
@@ -53,7 +60,7 @@ __device__ bool read_routing(const MoeParams& p, Routing& rt, int t0, int cnt)
         bad |= e < -1 || e >= p.E;
     }
     for (int e = tid; e < p.E; e += blockDim.x) rt.mask[e] = 0;
-    const bool own = tid < cnt * p.k;
+    const bool own = tid < cnt * p.k;      // (256 threads at least)
     int id = -1;
     if (own) {
         id = __ldcg(p.topk + t0 * p.k + tid);
@@ -135,26 +142,28 @@ struct Weights<0, false> {
 
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-// Sums of a warp: token columns 2t, 2t + 1 of the lane group's four or eight
-// weight columns.
-template <int G, bool Z>
+// Sums of a warp: token columns 2t, 2t + 1 of each eight, of the lane group's
+// four or eight weight columns.
+template <int NT, int G, bool Z>
 struct Sums {
     static constexpr int kTiles = G ? 2 : 4;
     static constexpr int kCols = G ? 32 : 64;
-    float v[kTiles][1][4];
+    float v[kTiles][NT][4];
 
     __device__ __forceinline__ void clear()
     {
 #pragma unroll
         for (int m = 0; m < kTiles; ++m)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[m][0][i] = 0.f;
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[m][nt][i] = 0.f;
     }
 
     // bf16: two steps of 16 rows, column pair m of the lanes is the tile m; the rows'
     // pairs of a column come out of two rows' words by byte permutation
     template <bool LO>
-    __device__ __forceinline__ void add(const Weights<0, false>& a, const uint4& b, const uint4& lo)
+    __device__ __forceinline__ void add(const Weights<0, false>& a, const uint4 (&b)[NT], const uint4 (&lo)[NT])
     {
 #pragma unroll
         for (int s = 0; s < 2; ++s)
@@ -164,25 +173,28 @@ struct Sums {
                 const uint32_t r2 = word(a.w[4 * s + 2], m), r3 = word(a.w[4 * s + 3], m);
                 const uint32_t a0 = __byte_perm(r0, r1, 0x5410), a1 = __byte_perm(r0, r1, 0x7632);
                 const uint32_t a2 = __byte_perm(r2, r3, 0x5410), a3 = __byte_perm(r2, r3, 0x7632);
-                mma(v[m][0], a0, a1, a2, a3, s ? b.z : b.x, s ? b.w : b.y);
-                if (LO) mma(v[m][0], a0, a1, a2, a3, s ? lo.z : lo.x, s ? lo.w : lo.y);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma(v[m][nt], a0, a1, a2, a3, s ? b[nt].z : b[nt].x, s ? b[nt].w : b[nt].y);
+                    if (LO) mma(v[m][nt], a0, a1, a2, a3, s ? lo[nt].z : lo[nt].x, s ? lo[nt].w : lo[nt].y);
+                }
             }
     }
 
-    // column 0 .. of the lane group for token 2t + j, four of them (half: the next four)
-    __device__ __forceinline__ float4 four(int j, int half) const
+    // column 0 .. of the lane group for token 8 nt + 2t + j, four of them (half: the next four)
+    __device__ __forceinline__ float4 four(int nt, int j, int half) const
     {
         const int m = half * 2;
-        return make_float4(v[m][0][j], v[m][0][j + 2], v[m + 1][0][j], v[m + 1][0][j + 2]);
+        return make_float4(v[m][nt][j], v[m][nt][j + 2], v[m + 1][nt][j], v[m + 1][nt][j + 2]);
     }
 };
 
 // The warps' sums of a CTA, [token][column] a warp.  Fours of columns are
 // stored by (half, group ^ 2t), which keeps a quarter warp's in different banks.
-template <int COLS>
+template <int NT, int COLS>
 struct Joined {
-    float red[kWarps][kTokens][COLS];
-    float join[kCluster - 1][kTokens][COLS];
+    float red[kWarps][NT * 8][COLS];
+    float join[kCluster - 1][NT * 8][COLS];
 
     static __device__ __forceinline__ int four_of(int g, int half, int t) { return half * 8 + (g ^ (2 * t)); }
     static __device__ __forceinline__ int place(int r, int c)
@@ -190,9 +202,9 @@ struct Joined {
         const int g = COLS == 64 ? c >> 3 : c >> 2, half = COLS == 64 ? (c >> 2) & 1 : 0;
         return four_of(g, half, (r >> 1) & 3) * 4 + (c & 3);
     }
-    __device__ __forceinline__ float4& at(int warp, int g, int t, int j, int half)
+    __device__ __forceinline__ float4& at(int warp, int g, int t, int nt, int j, int half)
     {
-        return *reinterpret_cast<float4*>(&red[warp][2 * t + j][four_of(g, half, t) * 4]);
+        return *reinterpret_cast<float4*>(&red[warp][nt * 8 + 2 * t + j][four_of(g, half, t) * 4]);
     }
     __device__ __forceinline__ float sum(int r, int c, int warps) const
     {
@@ -258,18 +270,20 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint3
     lo = ptx::pack_bf16x2(fabsf(da) < INFINITY ? da : 0.f, fabsf(db) < INFINITY ? db : 0.f);
 }
 
-// grid: tiles of columns, CTAs of a cluster, (eight tokens, expert of theirs)
-template <int G, bool Z>
+// grid: tiles of columns, CTAs of a cluster, (NT * 8 tokens, expert of theirs)
+template <int NT, int G, bool Z>
 __global__ void __launch_bounds__(kWarps * 32, 1) moe_up_kernel(const __grid_constant__ MoeParams p, int most_active)
 {
     using W = Weights<G, Z>;
-    using S = Sums<G, Z>;
-    constexpr int kHalf = S::kCols / 2;
+    using S = Sums<NT, G, Z>;
+    using J = Joined<NT, S::kCols>;
+    constexpr int kHalf = S::kCols / 2, kOctets = W::kRows / 32;
     __shared__ Routing rt;
-    __shared__ __align__(16) Joined<S::kCols> sums;
+    extern __shared__ __align__(16) uint8_t smem[];
+    J& sums = *reinterpret_cast<J*>(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int warps = blockDim.x >> 5, split = gridDim.y, rank = blockIdx.y;
-    const int t0 = blockIdx.z / most_active * kTokens, cnt = min(kTokens, p.T - t0), a = blockIdx.z % most_active;
+    const int t0 = blockIdx.z / most_active * (NT * 8), cnt = min(NT * 8, p.T - t0), a = blockIdx.z % most_active;
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
     if (!read_routing(p, rt, t0, cnt)) {
@@ -279,52 +293,63 @@ __global__ void __launch_bounds__(kWarps * 32, 1) moe_up_kernel(const __grid_con
     if (a >= rt.n) return;
     if (split > 1) ptx::cluster_arrive_relaxed();
     const int e = rt.active[a];
-    const bool use = rt.mask[e] >> g & 1;
+    const uint32_t use = rt.mask[e] >> g;
     const int i0 = blockIdx.x * kHalf, in_half = i0 + (g & 3) * W::kLaneCols, n = (g >> 2) * p.I + in_half;
     const bool col = in_half < p.I;
     const int blocks = (p.H + W::kRows - 1) / W::kRows, stride = warps * split;
     const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x) + (t0 + g) * p.ldx;
+    const auto octet = [&](int b, int R, int nt) {
+        const int k = b * W::kRows + 32 * R + 8 * t;
+        return (use >> (8 * nt) & 1) && k < p.H ? __ldg(reinterpret_cast<const uint4*>(x + nt * 8 * p.ldx + k)) : make_uint4(0, 0, 0, 0);
+    };
+    constexpr bool kRowsAhead = NT == 1;       // (more would not fit the registers)
     S acc;
     acc.clear();
     W next;
-    constexpr int kOctets = W::kRows / 32;
     uint4 next_x[kOctets];
     const auto fetch = [&](int b) {
         next.load(p.up, e, b, p.H, 2 * p.I, n, col, t);
+        if (kRowsAhead) {
 #pragma unroll
-        for (int R = 0; R < kOctets; ++R) {
-            const int k = b * W::kRows + 32 * R + 8 * t;
-            next_x[R] = use && k < p.H ? __ldg(reinterpret_cast<const uint4*>(x + k)) : make_uint4(0, 0, 0, 0);
+            for (int R = 0; R < kOctets; ++R) next_x[R] = octet(b, R, 0);
         }
     };
     int b = rank * warps + warp;
     if (b < blocks) fetch(b);
     for (; b < blocks; b += stride) {
         const W w = next;
-        uint4 xb[kOctets];
+        uint4 xb[kOctets][NT];
 #pragma unroll
-        for (int R = 0; R < kOctets; ++R) xb[R] = next_x[R];
+        for (int R = 0; R < kOctets; ++R)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) xb[R][nt] = kRowsAhead ? next_x[R] : octet(b, R, nt);
         if (b + stride < blocks) fetch(b + stride);
         if constexpr (G == 0) {
             acc.template add<false>(w, xb[0], xb[0]);
         } else {
-            uint32_t ex = 0;
+            float2 sx[NT];
 #pragma unroll
-            for (int R = 0; R < 4; ++R) ex = max(ex, skinny::max_exponent(xb[R]));
-            ex = max_of_token(ex);
-            const float f = half_scale(ex);
+            for (int nt = 0; nt < NT; ++nt) {
+                uint32_t ex = 0;
 #pragma unroll
-            for (int R = 0; R < 4; ++R) xb[R] = bf16x8_to_half(xb[R], f);
-            const float2 sx[1] = {of_sums(half_unscale(ex), t)};
-            multiply_q4<1, G, Z>(
+                for (int R = 0; R < 4; ++R) ex = max(ex, skinny::max_exponent(xb[R][nt]));
+                ex = max_of_token(ex);
+                const float f = half_scale(ex);
+#pragma unroll
+                for (int R = 0; R < 4; ++R) xb[R][nt] = bf16x8_to_half(xb[R][nt], f);
+                sx[nt] = of_sums(half_unscale(ex), t);
+            }
+            multiply_q4<NT, G, Z>(
                 acc.v, sx, [&](int R) { return w.w[R]; }, [&](int q) { return w.zero[q]; }, [&](int q) { return w.scale[q]; },
-                [&](int R, int) { return xb[R]; });
+                [&](int R, int nt) { return xb[R][nt]; });
         }
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int half = 0; half < S::kTiles / 2; ++half) sums.at(warp, g, t, j, half) = acc.four(j, half);
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int half = 0; half < S::kTiles / 2; ++half) sums.at(warp, g, t, nt, j, half) = acc.four(nt, j, half);
     __syncthreads();
     if (!sums.gather(rank, split, cnt, warps)) return;
     for (int i = threadIdx.x; i < cnt * kHalf; i += blockDim.x) {
@@ -337,17 +362,20 @@ __global__ void __launch_bounds__(kWarps * 32, 1) moe_up_kernel(const __grid_con
     }
 }
 
-// grid: tiles of columns, CTAs of a cluster, eight tokens
-template <int G, bool Z>
+// grid: tiles of columns, CTAs of a cluster, NT * 8 tokens
+template <int NT, int G, bool Z>
 __global__ void __launch_bounds__(kWarps * 32, 1) moe_down_kernel(const __grid_constant__ MoeParams p)
 {
     using W = Weights<G, Z>;
-    using S = Sums<G, Z>;
+    using S = Sums<NT, G, Z>;
+    using J = Joined<NT, S::kCols>;
+    constexpr int kOctets = W::kRows / 32;
     __shared__ Routing rt;
-    __shared__ __align__(16) Joined<S::kCols> sums;
+    extern __shared__ __align__(16) uint8_t smem[];
+    J& sums = *reinterpret_cast<J*>(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int warps = blockDim.x >> 5, split = gridDim.y, rank = blockIdx.y;
-    const int t0 = blockIdx.z * kTokens, cnt = min(kTokens, p.T - t0);
+    const int t0 = blockIdx.z * (NT * 8), cnt = min(NT * 8, p.T - t0);
     // (what came before the first kernel is complete: that kernel has waited for
     // it before it let this one start)
     if (!read_routing(p, rt, t0, cnt)) {
@@ -362,9 +390,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) moe_down_kernel(const __grid_c
     int item = items * share / shares;
     const int end = items * (share + 1) / shares;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int half = 0; half < S::kTiles / 2; ++half) sums.at(warp, g, t, j, half) = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int half = 0; half < S::kTiles / 2; ++half) sums.at(warp, g, t, nt, j, half) = make_float4(0.f, 0.f, 0.f, 0.f);
     W next;
     int a = item / per, b = item - a * per;
     if (item < end) next.load(p.down, rt.active[a], b, p.I, p.H, n, col, t);
@@ -372,65 +402,86 @@ __global__ void __launch_bounds__(kWarps * 32, 1) moe_down_kernel(const __grid_c
     ptx::grid_dep_launch();
     S acc;
     acc.clear();
-    const float* h = nullptr;          // this lane's token's row for the expert; null: it does not name it
-    float gate = 0.f;
+    int row[NT];                       // of h, of this lane's tokens for the expert; -1: they do not name it
+    float gate[NT];
     bool fresh = true;
     for (; item < end; ++item) {
         const W w = next;
         if (fresh) {
-            const int j = g < cnt ? find_slot(p, rt, g, rt.active[a], gate) : -1;
-            h = j < 0 ? nullptr : static_cast<const float*>(p.h_hi) + ((t0 + g) * p.k + j) * static_cast<long long>(p.I);
-        }
-        constexpr int kOctets = W::kRows / 32;
-        float4 lo4[kOctets], hi4[kOctets];
 #pragma unroll
-        for (int R = 0; R < kOctets; ++R) {
-            const int k = b * W::kRows + 32 * R + 8 * t;
-            const bool in = h && k < p.I;
-            lo4[R] = in ? __ldcg(reinterpret_cast<const float4*>(h + k)) : make_float4(0.f, 0.f, 0.f, 0.f);
-            hi4[R] = in ? __ldcg(reinterpret_cast<const float4*>(h + k + 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int nt = 0; nt < NT; ++nt) {
+                const int r = nt * 8 + g, j = r < cnt ? find_slot(p, rt, r, rt.active[a], gate[nt]) : -1;
+                row[nt] = j < 0 ? -1 : (t0 + r) * p.k + j;
+                if (j < 0) gate[nt] = 0.f;
+            }
         }
         int na = a, nb = b + 1;
         if (nb == per) na = a + 1, nb = 0;
-        if (item + 1 < end) next.load(p.down, rt.active[na], nb, p.I, p.H, n, col, t);
+        const bool more = item + 1 < end;
+        // eight numbers of h of a token
+        const auto octet = [&](int R, int nt, float4 (&v)[2]) {
+            const int k = b * W::kRows + 32 * R + 8 * t;
+            const float4* h = reinterpret_cast<const float4*>(static_cast<const float*>(p.h_hi) + row[nt] * static_cast<long long>(p.I) + k);
+            const bool in = row[nt] >= 0 && k < p.I;
+            v[0] = in ? __ldcg(h) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[1] = in ? __ldcg(h + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+        };
         if constexpr (G == 0) {
-            uint4 x, rest;
-            split_pair(lo4[0].x, lo4[0].y, x.x, rest.x);
-            split_pair(lo4[0].z, lo4[0].w, x.y, rest.y);
-            split_pair(hi4[0].x, hi4[0].y, x.z, rest.z);
-            split_pair(hi4[0].z, hi4[0].w, x.w, rest.w);
+            float4 v[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) octet(0, nt, v[nt]);
+            if (more) next.load(p.down, rt.active[na], nb, p.I, p.H, n, col, t);
+            uint4 x[NT], rest[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                split_pair(v[nt][0].x, v[nt][0].y, x[nt].x, rest[nt].x);
+                split_pair(v[nt][0].z, v[nt][0].w, x[nt].y, rest[nt].y);
+                split_pair(v[nt][1].x, v[nt][1].y, x[nt].z, rest[nt].z);
+                split_pair(v[nt][1].z, v[nt][1].w, x[nt].w, rest[nt].w);
+            }
             acc.template add<true>(w, x, rest);
         } else {
-            uint32_t ex = 0;
+            uint4 x[4][NT];
+            float2 sx[NT];
 #pragma unroll
-            for (int R = 0; R < 4; ++R) ex = max(ex, max(max_exponent(lo4[R]), max_exponent(hi4[R])));
-            ex = max_of_token(ex);
-            const float f = half_scale(ex);
-            uint4 x[4];
+            for (int nt = 0; nt < NT; ++nt) {
+                float4 v[4][2];
 #pragma unroll
-            for (int R = 0; R < 4; ++R)
-                x[R] = make_uint4(pack_h2(lo4[R].x * f, lo4[R].y * f), pack_h2(lo4[R].z * f, lo4[R].w * f),
-                                  pack_h2(hi4[R].x * f, hi4[R].y * f), pack_h2(hi4[R].z * f, hi4[R].w * f));
-            const float2 sx[1] = {of_sums(half_unscale(ex), t)};
-            multiply_q4<1, G, Z>(
+                for (int R = 0; R < 4; ++R) octet(R, nt, v[R]);
+                if (nt == 0 && more) next.load(p.down, rt.active[na], nb, p.I, p.H, n, col, t);
+                uint32_t ex = 0;
+#pragma unroll
+                for (int R = 0; R < 4; ++R) ex = max(ex, max(max_exponent(v[R][0]), max_exponent(v[R][1])));
+                ex = max_of_token(ex);
+                const float f = half_scale(ex);
+#pragma unroll
+                for (int R = 0; R < 4; ++R)
+                    x[R][nt] = make_uint4(pack_h2(v[R][0].x * f, v[R][0].y * f), pack_h2(v[R][0].z * f, v[R][0].w * f),
+                                          pack_h2(v[R][1].x * f, v[R][1].y * f), pack_h2(v[R][1].z * f, v[R][1].w * f));
+                sx[nt] = of_sums(half_unscale(ex), t);
+            }
+            multiply_q4<NT, G, Z>(
                 acc.v, sx, [&](int R) { return w.w[R]; }, [&](int q) { return w.zero[q]; }, [&](int q) { return w.scale[q]; },
-                [&](int R, int) { return x[R]; });
+                [&](int R, int nt) { return x[R][nt]; });
         }
         fresh = na != a;
-        if (fresh || item + 1 == end) {
-            const float2 gates = of_sums(gate, t);
-            const uint32_t named = __ballot_sync(0xffffffffu, h != nullptr);
+        if (fresh || !more) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                if (named >> (8 * t + 4 * j) & 1) {
-                    const float w1 = j ? gates.y : gates.x;
+            for (int nt = 0; nt < NT; ++nt) {
+                const float2 gates = of_sums(gate[nt], t);
+                const uint32_t named = __ballot_sync(0xffffffffu, row[nt] >= 0);
 #pragma unroll
-                    for (int half = 0; half < S::kTiles / 2; ++half) {
-                        float4& s = sums.at(warp, g, t, j, half);
-                        const float4 v = acc.four(j, half);
-                        s = make_float4(fmaf(w1, v.x, s.x), fmaf(w1, v.y, s.y), fmaf(w1, v.z, s.z), fmaf(w1, v.w, s.w));
+                for (int j = 0; j < 2; ++j)
+                    if (named >> (8 * t + 4 * j) & 1) {
+                        const float w1 = j ? gates.y : gates.x;
+#pragma unroll
+                        for (int half = 0; half < S::kTiles / 2; ++half) {
+                            float4& s = sums.at(warp, g, t, nt, j, half);
+                            const float4 v = acc.four(nt, j, half);
+                            s = make_float4(fmaf(w1, v.x, s.x), fmaf(w1, v.y, s.y), fmaf(w1, v.z, s.z), fmaf(w1, v.w, s.w));
+                        }
                     }
-                }
+            }
             acc.clear();
         }
         a = na;
@@ -446,7 +497,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) moe_down_kernel(const __grid_c
 
 // One CTA of 16 warps per SM where that is all of them, else CTAs of 8, two on
 // an SM; clusters as long as they fit the SMs and leave each warp a block.
-cudaLaunchConfig_t shape(cudaLaunchAttribute (&attr)[2], int tiles, int z, int blocks, int sms, cudaStream_t stream, bool pdl)
+cudaLaunchConfig_t shape(cudaLaunchAttribute (&attr)[2], int tiles, int z, int blocks, int smem, int sms, cudaStream_t stream, bool pdl)
 {
     const int warps = tiles * z <= sms ? kWarps : kWarps / 2;
     int split = 1;
@@ -454,6 +505,7 @@ cudaLaunchConfig_t shape(cudaLaunchAttribute (&attr)[2], int tiles, int z, int b
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3(tiles, split, z);
     lc.blockDim = dim3(warps * 32);
+    lc.dynamicSmemBytes = smem;
     lc.stream = stream;
     lc.attrs = attr;
     if (split > 1) {
@@ -471,30 +523,64 @@ cudaLaunchConfig_t shape(cudaLaunchAttribute (&attr)[2], int tiles, int z, int b
     return lc;
 }
 
-template <int G, bool Z>
+template <int NT, int G, bool Z>
 cudaError_t launch(const MoeParams& p, int sms, cudaStream_t stream, bool pdl)
 {
-    constexpr int kCols = Sums<G, Z>::kCols, kRows = Weights<G, Z>::kRows;
-    const int passes = (p.T + kTokens - 1) / kTokens, names = (p.T < kTokens ? p.T : kTokens) * p.k;
+    constexpr int kCols = Sums<NT, G, Z>::kCols, kRows = Weights<G, Z>::kRows;
+    constexpr int kSmem = static_cast<int>(sizeof(Joined<NT, kCols>));
+    const int passes = (p.T + NT * 8 - 1) / (NT * 8), names = (p.T < NT * 8 ? p.T : NT * 8) * p.k;
     const int active = names < p.E ? names : p.E;
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t lc = shape(attr, (2 * p.I + kCols - 1) / kCols, passes * active, (p.H + kRows - 1) / kRows, sms, stream, pdl);
-    const cudaError_t e = cudaLaunchKernelEx(&lc, moe_up_kernel<G, Z>, p, active);
+    cudaLaunchConfig_t lc = shape(attr, (2 * p.I + kCols - 1) / kCols, passes * active, (p.H + kRows - 1) / kRows, kSmem, sms, stream, pdl);
+    const cudaError_t e = cudaLaunchKernelEx(&lc, moe_up_kernel<NT, G, Z>, p, active);
     if (e != cudaSuccess) return e;
-    lc = shape(attr, (p.H + kCols - 1) / kCols, passes, active * ((p.I + kRows - 1) / kRows), sms, stream, pdl);
-    return cudaLaunchKernelEx(&lc, moe_down_kernel<G, Z>, p);
+    lc = shape(attr, (p.H + kCols - 1) / kCols, passes, active * ((p.I + kRows - 1) / kRows), kSmem, sms, stream, pdl);
+    return cudaLaunchKernelEx(&lc, moe_down_kernel<NT, G, Z>, p);
+}
+
+template <int NT, int G, bool Z>
+cudaError_t prepare()
+{
+    constexpr int kSmem = static_cast<int>(sizeof(Joined<NT, Sums<NT, G, Z>::kCols>));
+    const cudaError_t e = cudaFuncSetAttribute(moe_up_kernel<NT, G, Z>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(moe_down_kernel<NT, G, Z>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+}
+
+// Calls f with the kernels' types: 8 or 16 tokens at a time, a group, zeros.
+template <class F>
+cudaError_t with_types(bool wide, int group, bool zero, F f)
+{
+    const auto zeros = [&](auto nt, auto g) {
+        return zero ? f(nt, g, std::true_type()) : f(nt, g, std::false_type());
+    };
+    const auto groups = [&](auto nt) {
+        if (group == 32) return zeros(nt, std::integral_constant<int, 32>());
+        if (group == 64) return zeros(nt, std::integral_constant<int, 64>());
+        if (group == 128) return zeros(nt, std::integral_constant<int, 128>());
+        return f(nt, std::integral_constant<int, 0>(), std::false_type());
+    };
+    return wide ? groups(std::integral_constant<int, 2>()) : groups(std::integral_constant<int, 1>());
 }
 
 }  // namespace
 
+cudaError_t prepare_moe_direct()
+{
+    for (int i = 0; i < 16; ++i) {
+        const cudaError_t e = with_types(i & 1, (i >> 2) * 32 + (i >> 2 == 3 ? 32 : 0), i >> 1 & 1, [](auto nt, auto g, auto z) {
+            return prepare<decltype(nt)::value, decltype(g)::value, decltype(z)::value>();
+        });
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
 cudaError_t launch_moe_direct(const MoeParams& p, int group, bool zero, int sms, cudaStream_t stream, bool pdl)
 {
-    switch (group) {
-    case 32: return zero ? launch<32, true>(p, sms, stream, pdl) : launch<32, false>(p, sms, stream, pdl);
-    case 64: return zero ? launch<64, true>(p, sms, stream, pdl) : launch<64, false>(p, sms, stream, pdl);
-    case 128: return zero ? launch<128, true>(p, sms, stream, pdl) : launch<128, false>(p, sms, stream, pdl);
-    default: return launch<0, false>(p, sms, stream, pdl);
-    }
+    return with_types(p.T > 8, group, zero, [&](auto nt, auto g, auto z) {
+        return launch<decltype(nt)::value, decltype(g)::value, decltype(z)::value>(p, sms, stream, pdl);
+    });
 }
 
 }  // namespace tovl

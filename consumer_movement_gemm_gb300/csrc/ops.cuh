@@ -87,18 +87,22 @@ struct MoeParams {
     long long timeout_ns, pipe_timeout_ns;
     Ctrl ctrl;
 };
-// Expert layers without rings and barriers: those of fewer than 2^26 weights,
-// counted for the experts that eight tokens can name, once per eight tokens.
-// Below the rule (direct and through the rings): 1 token, 2 of 8 experts, 4096 x
-// 2048, bf16 24.6 and 32.1 us, 4-bit 16.2 and 21.9; 8 tokens of 2048 x 1024 23.6
-// and 29.3, 17.4 and 21.7; 1 token of 256 x 128 5.5 and 14.9.  Above it: 16 tokens
-// of 2048 x 1024 38.1 and 32.4, 26.6 and 22.6; 4 tokens of 4096 x 2048 69 and 61,
-// 39.7 and 34.3; 64 tokens of 1024 x 512 33 and 25, 31 and 24.
+// Expert layers without rings and barriers (moe_direct.cu): by the weights of the
+// experts that 8 tokens (up to 8 in all) or 16 can name, once per that many,
+// fewer than 2^26 or 2^25.  Direct and through the rings, bf16 / 4-bit, us:
+//   1 token, 2 of 8 experts of 4096 x 2048 (48M)     24.4 / 16.4    31.9 / 21.0
+//   3 tokens, 6 of 32 of 2048 x 512 (54M)            24.6 / 18.8    31.1 / 21.4
+//   4 tokens, 2 of 8 of 4096 x 2048 (192M)           68.5 / 39.8    60.5 / 33.9
+//   12 tokens, 2 of 8 of 512 x 256 (3M)               9.4 / 7.8     19.8 / 18.9
+//   32 tokens, 2 of 8 of 1024 x 512 (24M)            18.3 / 15.9    21.7 / 22.0
+//   20 tokens, 4 of 32 of 512 x 256 (24M)            20.8 / 15.9    19.5 / 19.4
+//   64 tokens, 2 of 8 of 1024 x 512 (48M)            28.5 / 24.3    25.4 / 23.7
 inline bool use_direct_moe(int T, int k, int E, int H, int I)
 {
-    const int names = (T < 8 ? T : 8) * k;
-    return 3LL * ((T + 7) / 8) * (names < E ? names : E) * H * I < (1LL << 26);
+    const int most = T <= 8 ? 8 : 16, names = (T < most ? T : most) * k;
+    return 3LL * ((T + most - 1) / most) * (names < E ? names : E) * H * I < (T <= 8 ? 1LL << 26 : 1LL << 25);
 }
+cudaError_t prepare_moe_direct();
 cudaError_t launch_moe_direct(const MoeParams& p, int group, bool zero, int sms, cudaStream_t stream, bool pdl);
 cudaError_t prepare_moe_decode();
 // group: rows per scale of 4-bit weights, 0 for bf16

@@ -168,6 +168,7 @@ TOVL_API int tovl_create(tovl_handle* out, const tovl_config* cfg_in)
         if ((e = prepare_plan()) != cudaSuccess) { rc = cuda_fail(h, e, "prepare plan"); break; }
         if ((e = prepare_copy()) != cudaSuccess) { rc = cuda_fail(h, e, "prepare copy"); break; }
         if ((e = prepare_combine()) != cudaSuccess) { rc = cuda_fail(h, e, "prepare combine"); break; }
+        if ((e = prepare_moe_direct()) != cudaSuccess) { rc = cuda_fail(h, e, "prepare moe direct"); break; }
         if ((e = prepare_moe_decode()) != cudaSuccess) { rc = cuda_fail(h, e, "prepare moe decode"); break; }
         if ((e = prepare_matvec_q4()) != cudaSuccess) { rc = cuda_fail(h, e, "prepare matvec"); break; }
         if (fused_max_active_per_sm() < 1) { rc = TOVL_ERR_UNSUPPORTED; break; }
