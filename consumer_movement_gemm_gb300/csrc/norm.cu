@@ -10,6 +10,11 @@
 // each (no barrier), longer ones a CTA each (one barrier a reduction).  A thread holds
 // groups of 8 consecutive elements, so a scale group of 32, 64 or 128 columns
 // is 4, 8 or 16 neighbouring lanes.
+//
+// What bounds it: memory.  Rows of whole 16-byte pieces (norm_rows_kernel): 16384 x
+// 7168, bf16 residual, both outputs, 172 us, 6.2 TB/s; 16384 x 8192 203 us, 6.0;
+// 333 x 7168, fp32 residual, 8.3 us (one to three rows an SM: their latency); 1 x
+// 4096 2.7 us.  Rows that start elsewhere: norm_offset_kernel, norm_kernel.
 #include <cuda_bf16.h>
 #include <type_traits>
 #include "common.cuh"
@@ -23,6 +28,7 @@ constexpr float kE4m3Max = 448.f;
 constexpr float kMinAmax = 1e-12f;     // keeps 448 / amax finite
 constexpr int kWarpRows = 8;           // rows per CTA of the warp-per-row form
 constexpr int kWarpRowMax = 1024;      // longest row of the warp-per-row form
+constexpr int kOffsetThreads = 1024;   // at most, of a CTA whose rows start off the boundaries
 
 // Larger operand, NaN if one is (a NaN shows in its group's scale).
 __device__ __forceinline__ float max_nan(float a, float b)
@@ -299,7 +305,8 @@ __global__ void __launch_bounds__(WARP ? kWarpRows * 32 : 512, VPT <= 2 ? 2 : 1)
     }
 }
 
-// Rows of any length and alignment, moved in pairs or single elements.
+// Rows of any length and alignment, moved in pairs or single elements (W = 8:
+// whole pieces, for rows too long for a second one in the registers).
 template <int W, int VPT, int RES>
 __global__ void __launch_bounds__(1024) norm_kernel(const NormParams p, int warp_row)
 {
@@ -389,6 +396,201 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormParams p, int warp
     }
 }
 
+// Rows of any length that start at the same distance from a 16-byte boundary in
+// every tensor (contiguous ones do): a thread's eight elements are an aligned
+// piece, `s` elements before a multiple of eight columns, and only the row's
+// first and last piece go by single elements.  The weights, whose distance
+// differs, come as two pieces that are shifted together.  A scale group ends
+// inside a piece, always after s elements: the maxima of both sides, and the
+// scales, cross to the neighbouring thread.  A row to a warp (WARP) or a CTA,
+// one piece to a thread as far as a CTA goes: with four the straight code of a row
+// (64 KB) ran as fast as its instructions came from L2 (16384 x 777: 118 us, 44
+// with one).  What bounds it: the barriers and the dependent loads of a row, two
+// or three rows an SM in flight (16384 x 5001, 228 us, 3.2 TB/s).
+__device__ __forceinline__ uint4 shift_eight(const uint4& a, const uint4& b, int s)
+{
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (s & 4) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (s & 2) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    if (s & 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The elements [first, last) of a piece; the others stay as they are.
+template <class T>
+__device__ __forceinline__ void load_piece(float (&v)[8], const T* p, int first, int last)
+{
+    if (first == 0 && last == 8) {
+        load8<8>(v, p, 8);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i >= first && i < last) v[i] = static_cast<float>(p[i]);
+    }
+}
+
+template <class T>
+__device__ __forceinline__ void store_piece(T* p, const float (&v)[8], int first, int last)
+{
+    if (first == 0 && last == 8) {
+        store8<8>(p, v, 8);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i >= first && i < last) p[i] = static_cast<T>(v[i]);
+    }
+}
+
+template <int VPT, int RES, bool WARP>
+__global__ void __launch_bounds__(WARP ? kWarpRows * 32 : kOffsetThreads) norm_offset_kernel(const NormParams p)
+{
+    constexpr int kGroups = WARP ? kWarpRowMax / 32 : kOffsetThreads * VPT * 8 / 32;
+    using R = typename std::conditional<RES == 2, float, __nv_bfloat16>::type;
+    __shared__ float sum_buf[32], max_buf[32], edge[VPT][33], inverse[WARP ? kWarpRows : 1][kGroups];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long row = WARP ? static_cast<long long>(blockIdx.x) * kWarpRows + warp : blockIdx.x;
+    const int threads = WARP ? 32 : blockDim.x, tid = WARP ? lane : threadIdx.x;
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    if (row >= p.T) return;     // whole warps only
+    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x) + row * p.ldx;
+    const __nv_bfloat16* weight = static_cast<const __nv_bfloat16*>(p.weight);
+    const int s = static_cast<int>(reinterpret_cast<uintptr_t>(x) >> 1) & 7;
+    float v[VPT][8], g[VPT][8];
+    int lo[VPT], first[VPT], last[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        lo[j] = (tid + j * threads) * 8 - s;
+        first[j] = max(0, -lo[j]);
+        last[j] = min(8, p.H - lo[j]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[j][i] = g[j][i] = 0.f;
+        load_piece(v[j], x + lo[j], first[j], last[j]);
+        const int c = lo[j] + s;
+        if (s == 0) {
+            load_piece(g[j], weight + lo[j], first[j], last[j]);
+        } else if (c < 8 || c + 8 > p.H) {       // (no aligned piece of the weights, even if it is one of the row's)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i >= first[j] && i < last[j]) g[j][i] = __bfloat162float(weight[lo[j] + i]);
+        } else {
+            const uint4* w = reinterpret_cast<const uint4*>(weight + c);
+            const uint4 u = shift_eight(__ldg(w - 1), __ldg(w), 8 - s);
+            unpack8(g[j], u);
+        }
+    }
+    if constexpr (RES != 0) {
+        const R* res = static_cast<const R*>(p.residual) + row * p.ldr;
+        R* dst = static_cast<R*>(p.residual_out) + row * p.ldr;
+        float o[VPT][8];
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[j][i] = 0.f;
+            load_piece(o[j], res + lo[j], first[j], last[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[j][i] += o[j][i];
+            store_piece(dst + lo[j], v[j], first[j], last[j]);
+        }
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(v[j][i], v[j][i], ss);
+    ss = row_reduce<false>(ss, sum_buf, WARP);
+    const float inv_rms = rsqrtf(ss / p.H + p.eps);
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row * p.ldo;
+    float before[VPT], after[VPT];      // largest magnitudes of the elements before and from s on
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        before[j] = after[j] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[j][i] = v[j][i] * inv_rms * g[j][i];
+            const float a = i >= first[j] && i < last[j] ? fabsf(v[j][i]) : 0.f;    // (0 * infinity past the ends)
+            if (i < s) before[j] = max_nan(before[j], a);
+            else after[j] = max_nan(after[j], a);
+        }
+        if (p.out) store_piece(out + lo[j], v[j], first[j], last[j]);
+    }
+    if (!p.q) return;
+    float* scale = p.q_scale + row * p.n_groups;
+    uint8_t* q = p.q + row * p.H;
+    float* inv = inverse[WARP ? warp : 0];
+    int shift = 31;                     // of a column to its group
+    if (p.group == p.H) {
+        float m = 0.f;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) m = max_nan(m, max_nan(before[j], after[j]));
+        m = max_nan(row_reduce<true>(m, max_buf, WARP), kMinAmax);
+        if (tid == 0) {
+            scale[0] = m / kE4m3Max;
+            inv[0] = kE4m3Max / m;
+        }
+    } else {
+        shift = 31 - __clz(p.group);
+        if (!WARP) {
+            if (lane == 0) {
+#pragma unroll
+                for (int j = 0; j < VPT; ++j) edge[j][warp] = before[j];
+            }
+            __syncthreads();
+        }
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            float next = __shfl_down_sync(0xffffffffu, before[j], 1);
+            if (WARP) {
+                const float over = j + 1 < VPT ? __shfl_sync(0xffffffffu, before[j + 1 < VPT ? j + 1 : 0], 0) : 0.f;
+                if (lane == 31) next = over;
+            } else if (lane == 31) {
+                next = warp + 1 < threads / 32 ? edge[j][warp + 1] : j + 1 < VPT ? edge[j + 1 < VPT ? j + 1 : 0][0] : 0.f;
+            }
+            float m = max_nan(after[j], next);
+            m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            if (p.group > 32) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 4));
+            if (p.group > 64) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 8));
+            m = max_nan(m, kMinAmax);
+            const int c = lo[j] + s;
+            if ((c & (p.group - 1)) == 0 && c < p.H) {
+                scale[c >> shift] = m / kE4m3Max;
+                inv[c >> shift] = kE4m3Max / m;
+            }
+        }
+    }
+    if (WARP) __syncwarp();
+    else __syncthreads();
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        if (last[j] <= 0) continue;
+        const int c = lo[j] + s;
+        const float i0 = inv[max(c - 8, 0) >> shift], i1 = inv[min(c, p.H - 1) >> shift];
+        uint32_t h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = e4m3x2(v[j][2 * i] * (2 * i < s ? i0 : i1), v[j][2 * i + 1] * (2 * i + 1 < s ? i0 : i1));
+        if (first[j] == 0 && last[j] == 8) {
+            *reinterpret_cast<uint2*>(q + lo[j]) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i >= first[j] && i < last[j]) q[lo[j] + i] = static_cast<uint8_t>(h[i / 2] >> (8 * (i & 1)));
+        }
+    }
+}
+
 // f(residual kind)
 template <class F>
 cudaError_t by_residual(const NormParams& p, F f)
@@ -429,9 +631,17 @@ cudaError_t launch_any(const NormParams& p, const cudaLaunchConfig_t& lc, int wa
 
 int up32(int n) { return (n + 31) / 32 * 32; }
 
+template <int VPT, bool WARP>
+cudaError_t launch_offset(const NormParams& p, cudaLaunchConfig_t lc, int pieces)
+{
+    lc.gridDim = dim3(WARP ? (p.T + kWarpRows - 1) / kWarpRows : p.T);
+    lc.blockDim = dim3(WARP ? kWarpRows * 32 : up32((pieces + VPT - 1) / VPT));
+    return by_residual(p, [&](auto res) { return cudaLaunchKernelEx(&lc, norm_offset_kernel<VPT, decltype(res)::value, WARP>, p); });
+}
+
 }  // namespace
 
-cudaError_t launch_norm(const NormParams& p, int width, int num_sms, cudaStream_t stream, bool pdl)
+cudaError_t launch_norm(const NormParams& p, int width, bool same_offset, int num_sms, cudaStream_t stream, bool pdl)
 {
     const int vecs = (p.H + 7) / 8;
     const int warp_row = p.H <= kWarpRowMax;
@@ -458,6 +668,16 @@ cudaError_t launch_norm(const NormParams& p, int width, int num_sms, cudaStream_
         lc.gridDim = dim3(p.T);
         lc.blockDim = dim3(up32((vecs + 3) / 4));
         return launch_any<8>(p, lc, 0, 4);
+    }
+    // Pieces, where the rows allow them, against pairs: 16384 x 1002 46 us and 102,
+    // 16384 x 2002 88 and 88, 16384 x 2934 142 and 118 (fewer barriers); against
+    // single elements: 16384 x 777 44 and 101, 16384 x 5001 228 and 515.  (Up to
+    // seven elements of a row's first piece are not the row's.)
+    const int pieces = (p.H + 14) / 8;
+    if (same_offset && pieces <= 2 * kOffsetThreads && (width == 1 || warp_row)) {
+        if (pieces <= 32) return launch_offset<1, true>(p, lc, pieces);
+        if (pieces <= kOffsetThreads) return launch_offset<1, false>(p, lc, pieces);
+        return launch_offset<2, false>(p, lc, pieces);
     }
     int vpt = warp_row ? (vecs + 31) / 32 : (vecs + 1023) / 1024;
     if (vpt == 3) vpt = 4;

@@ -41,7 +41,7 @@ struct NormParams {
     int n_groups;
     int residual_f32;
 };
-cudaError_t launch_norm(const NormParams& p, int width, int num_sms, cudaStream_t stream, bool pdl);
+cudaError_t launch_norm(const NormParams& p, int width, bool same_offset, int num_sms, cudaStream_t stream, bool pdl);
 
 struct RouteParams {
     const void* logits;     // [T][E] fp32 or bf16, rows ld elements apart

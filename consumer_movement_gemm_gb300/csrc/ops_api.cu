@@ -153,9 +153,15 @@ TOVL_API int tovl_add_rmsnorm(tovl_handle h, const void* x, long long ldx, const
                               aligned(residual_out, w == 8 ? 16 : res_size * w)));
     };
     const int width = fits(8) ? 8 : fits(2) ? 2 : 1;
+    // every tensor's rows start at the same distance from a 16-byte boundary (8 bytes of e4m3)
+    const auto offset = [](const void* ptr, int size, int piece) { return static_cast<int>(reinterpret_cast<uintptr_t>(ptr) / size) & (piece - 1); };
+    const int off = offset(x, 2, 8), piece = res_size == 4 ? 4 : 8;
+    const auto like_x = [&](const void* ptr, long long ld, int size, int n) { return (T == 1 || (ld - ldx) % n == 0) && offset(ptr, size, n) == (off & (n - 1)); };
+    const bool same_offset = aligned16(weight) && (!out || like_x(out, ldo, 2, 8)) && (!q || like_x(q, H, 1, 8)) &&
+                             (!residual || (like_x(residual, ldr, res_size, piece) && like_x(residual_out, ldr, res_size, piece)));
     DeviceGuard g(h->device);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return run(h, s, "norm launch", [&](bool pdl) { return launch_norm(p, width, h->num_sms, s, pdl); });
+    return run(h, s, "norm launch", [&](bool pdl) { return launch_norm(p, width, same_offset, h->num_sms, s, pdl); });
 }
 
 TOVL_API int tovl_route_topk(tovl_handle h, const void* logits, int type, long long ld, int T, int E, int k,

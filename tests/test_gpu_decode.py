@@ -126,6 +126,31 @@ def test_norm_strided_and_misaligned_rows(h, H, off, pad):
     check_norm(x, weight, 1e-6, res2, ro, out, None, None, 0)
 
 
+@pytest.mark.parametrize("T", [1, 5])
+@pytest.mark.parametrize("H", [9, 15, 33, 121, 127, 249, 250, 257, 393, 777, 1002, 1017, 1018, 1019, 1023, 2049, 4089, 4111, 8177,
+                               8185, 8186, 8191, 12001, 16377, 16379])
+@pytest.mark.parametrize("group,residual", [(128, "bf16"), (64, "f32"), (32, "none"), (0, "f32")])
+def test_norm_of_odd_rows(h, T, H, group, residual):
+    """Rows off the 16-byte boundaries, contiguous (every tensor the same distance off) and with x alone strided."""
+    g = gen(T * 100003 + H)
+    weight = randn(g, H) + 1
+    for pad in (0, 3):
+        x = randn(g, T, H + pad)[:, :H]
+        res = None if residual == "none" else randn(g, T, H, scale=3, dtype=BF16 if residual == "bf16" else F32)
+        ro = None if res is None else torch.empty_like(res)
+        out, q = torch.empty(T, H, dtype=BF16, device=DEV), torch.full((T * H + 8,), 99, dtype=torch.uint8, device=DEV)
+        scale = torch.full((T, -(-H // group) if group else 1), float("nan"), device=DEV)
+        h.add_rmsnorm(x, weight, 1e-5, residual=res, residual_out=ro, out=out, q=q[:T * H].view(E4M3).view(T, H), q_scale=scale,
+                      group=group)
+        assert h.sync_status() == 0
+        check_norm(x, weight, 1e-5, res, ro, out, q[:T * H].view(E4M3).view(T, H), scale, group)
+        assert (q[T * H:] == 99).all()
+        if res is not None and pad == 0:          # in place: the same bits
+            x2, res2 = x.clone(), res.clone()
+            h.add_rmsnorm(x2, weight, 1e-5, residual=res2, residual_out=res2, out=x2)
+            assert torch.equal(x2, out) and torch.equal(res2, ro)
+
+
 def test_norm_in_place_and_single_outputs(h):
     g = gen(5)
     x, weight, res = randn(g, 9, 768), randn(g, 768), randn(g, 9, 768)
