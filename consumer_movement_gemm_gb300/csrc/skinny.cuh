@@ -5,31 +5,44 @@
 // W once, so W is laid in shared memory by TMA and everything else fits
 // around that stream.
 //
-// Units.  A unit is 512 columns x 32 rows of bf16 (or x 128 rows of 4 bits),
-// 32 KB.  Its columns are dealt to the CTA's warps (8 of 64 columns for bf16;
-// 16 of 32 for 4-bit weights, whose unpacking needs twice the warps to hide
-// its latencies), so neighbouring warps read neighbouring pieces of the same rows at
-// the same time: measured on GB300, a stream of such 1 KB wide rows reaches
-// 6.67 TB/s, the same boxes with the warps along k (each 128-byte piece
-// alone) 5.85.  A warp owns its columns, so nothing is summed across warps and
-// no warp waits for another one; each has its own ring of stages, filled by its
-// own lane 0, that runs on across tiles and across the two products of an
+// Units.  A unit is 512 columns x 32 rows of bf16 (32 KB) or x 256 rows of 4
+// bits (64 KB).  Its columns are dealt to the CTA's warps (8 of 64 columns for
+// bf16; 16 of 32 for 4-bit weights, whose unpacking needs twice the warps to
+// hide its latencies), a 4 KB block each, so neighbouring warps read neighbouring
+// pieces of the same rows at the same time: measured on GB300, a stream of such
+// 1 KB wide rows reaches 6.67 TB/s, the same boxes with the warps along k (each
+// 128-byte piece alone) 5.85.  A warp owns its columns, so nothing is summed
+// across warps and no warp waits for another one; each has its own ring of
+// stages (4 blocks of bf16 weights, 2 of 4-bit weights: 128 KB in flight per SM), filled by
+// its own lane 0, that runs on across tiles and across the two products of an
 // expert layer (weights depend on nothing).  The few rows of x pass through
-// shared memory once per CTA, as bf16, where all warps read them.
+// shared memory once per CTA in 16 KB chunks, as bf16 or (4-bit weights) turned
+// into fp16, where all warps read them.
 //
 // Items.  The units of a product, in the order (matrix, tile of 512 columns,
-// k), are cut into items of equal length.  With little work there is one item
-// per CTA; else eight, taken by ticket, because the SMs do not get the same
-// share of the memory (an even static deal of 2.3 GB ended between 160 and
-// 229 us).  An item writes the fp32 sums of each tile that it touches to the
-// workspace, under the number of its part of the tile; after a grid barrier all CTAs add
-// the parts in the order of k.  Which CTA took an item changes nothing: the
-// same bits every time.
+// k), are cut into items.  With little work there is one item per CTA; from 3 MB
+// of weights per CTA on, one of three quarters of an even share and then small
+// ones, an eighth of it, by ticket, because the SMs do not get the same share of
+// the memory (an even static deal of 2.3 GB ended between 160 and 229 us).  An
+// item writes the fp32 sums of each tile that it touches to the workspace, under
+// the number of its part of the tile; then all CTAs, after a grid barrier (expert
+// layer), or the last CTA to finish a part of the tile (product alone) add the
+// parts in the order of k.  Which CTA took an item changes nothing: the same bits
+// every time.
 //
 // The matrix instruction is the warp-level m16n8k16 with the weights as the
 // 16-row operand: at most 8 rows cost one instruction per 16 columns x 16
 // rows of W, registers feed it directly (4-bit weights never go back to
-// shared memory), and the tensor pipe has time for 64 rows of bf16.
+// shared memory), and the tensor pipe has time for 64 rows of bf16.  4-bit
+// weights as the tensor-memory operand of tcgen05.mma were built and dropped: two
+// barriers and 520 instructions per 2 KB against 400, 16 x 7168 x 32768 57 us
+// against 46.
+//
+// What bounds it.  bf16: memory (13 tokens of an expert layer, 2.3 GB, 6.5 TB/s).
+// 4 bits: the instructions that turn a block into operands, about 335 per 2 KB
+// with up to 8 rows and 400 with 16, four warps a scheduler to hide their
+// latencies (49 % of the issue slots, 36 % of the integer pipe, 32 % of the tensor
+// pipe): 2.8 TB/s with 16 rows, 3.8 with one.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -499,7 +512,7 @@ struct Product {
     int items;
     bool tickets;
 
-    // min_units: shortest item (a tile of kb units has kb / min_units + 2 parts at most)
+    // An item has no fewer units than leave a tile most_parts + 2 parts at most.
     __device__ __forceinline__ void init(int matrices, int N, int K, int rows, int unit_bytes, int grid, int most_parts)
     {
         tiles = (N + kTileCols - 1) / kTileCols;

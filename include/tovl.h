@@ -278,7 +278,8 @@ typedef enum {
  *   group       32, 64 or 128, or 0 for one scale per row; the last group of
  *               a row may be shorter
  * H is 1 .. 32768; pointers need the alignment of their element type only
- * (rows of 16-byte multiples and alignment are fastest).  A NaN in a row
+ * (rows of 16-byte multiples and alignment are fastest, then tensors whose
+ * rows start equally far from a 16-byte boundary).  A NaN in a row
  * shows in all of its outputs. */
 int tovl_add_rmsnorm(tovl_handle h, const void* x, long long ldx, const void* residual, void* residual_out,
                      int residual_type, long long ldr, const void* weight, float eps, int T, int H, void* out,
@@ -302,7 +303,7 @@ int tovl_route_topk(tovl_handle h, const void* logits, int type, long long ld, i
  * handle's device; -1 if the sizes are not supported. */
 long long tovl_moe_decode_workspace(tovl_handle h, int T, int k, int H, int I);
 
-/* The gated expert layer for a few tokens, in one kernel:
+/* The gated expert layer for a few tokens:
  *   h(t, e) = silu(x[t] W13[e][:, 0:I]) * (x[t] W13[e][:, I:2I]),
  *   out[t]  = sum over j of gate_w[t][j] * (h(t, e) W2[e]), e = topk_idx[t][j]
  * with fp32 sums, rounded once to bf16.
@@ -319,10 +320,11 @@ long long tovl_moe_decode_workspace(tovl_handle h, int T, int k, int H, int I);
  *   out         device, bf16 [T][H], rows ldo apart; a token without experts
  *               gets zeros
  *   workspace   device, 256-byte aligned, tovl_moe_decode_workspace bytes of
- *               any content; free again when the call's kernel has ended
- * The weights of experts that no token names are not read.  The grid meets at
- * one barrier, so all its CTAs (one per SM) must be resident together: option
- * 13 keeps the guarantee.  Results are the same bits on every call. */
+ *               any content; free again when the call's kernels have ended
+ * The weights of experts that no token names are not read.  Small layers take
+ * two kernels, others one whose grid meets at three barriers: all its CTAs (one
+ * per SM) must be resident together, and option 13 keeps the guarantee.
+ * Results are the same bits on every call with the same arguments. */
 int tovl_moe_decode(tovl_handle h, const void* x, long long ldx, int T, int H, const int* topk_idx,
                     const float* gate_w, int k, int E, const void* W13, const void* W2, int I, void* out,
                     long long ldo, void* workspace, long long workspace_bytes, void* stream);
