@@ -22,10 +22,11 @@
 // power of two per 128 columns.  Sums are fp32, in a fixed order.
 //
 // What bounds it: at small sizes two launches and a CTA's dependent loads (1
-// token, 256 x 128: 5.3 us, 1024 x 512: 7.7, through the rings 14.9 and 19.8); at
-// large ones the bytes in flight, one block a warp (1 token, 2 of 8 experts of
-// 4096 x 2048, bf16: 24.4 us, 4.1 TB/s, through the rings 31.9).  Two blocks a warp
-// spill registers: 27.1.
+// token, 256 x 128: 5.1 us, 1024 x 512: 7.4, through the rings 14.9 and 19.8); at
+// large ones the bytes in flight, one block a warp, and the start of two grids (1
+// token, 2 of 8 experts of 4096 x 2048, bf16: 23.9 us, 4.2 TB/s, of 4096 x 4096: 40.1,
+// 5.0 TB/s; through the rings 31.9 and 45.2).  Two blocks a warp spill registers:
+// 27.1 us for the first.
 #include <type_traits>
 #include "launch.cuh"
 #include "skinny.cuh"
@@ -286,14 +287,40 @@ __global__ void __launch_bounds__(kWarps * 32, 1) moe_up_kernel(const __grid_con
     const int t0 = blockIdx.z / most_active * (NT * 8), cnt = min(NT * 8, p.T - t0), a = blockIdx.z % most_active;
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
-    if (!read_routing(p, rt, t0, cnt)) {
-        if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) record_error(p.ctrl, kErrInvalid);
-        return;
+    int e;
+    uint32_t named;                    // tokens that name e
+    if (p.T * p.k <= 32) {
+        // One name a lane: every warp finds the expert by itself, without a barrier
+        // before the first weights (1 token, 1024 x 512: 7.8 -> 7.4 us); the experts
+        // in the order of their first names.
+        const int id = lane < p.T * p.k ? __ldcg(p.topk + lane) : -1;
+        const float weight = lane < p.T * p.k ? __ldcg(p.gate_w + lane) : 0.f;
+        const uint32_t same = __match_any_sync(0xffffffffu, id);
+        const uint32_t firsts = __ballot_sync(0xffffffffu, id >= 0 && __ffs(same) - 1 == lane);
+        if (__any_sync(0xffffffffu, id < -1 || id >= p.E)) {
+            if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) record_error(p.ctrl, kErrInvalid);
+            return;
+        }
+        if (a >= __popc(firsts)) return;
+        const int first = __fns(firsts, 0, a + 1);
+        e = __shfl_sync(0xffffffffu, id, first);
+        const bool mine = lane < p.T * p.k && id == e;
+        named = __reduce_or_sync(0xffffffffu, mine ? 1u << (lane / p.k) : 0u);
+        if (warp == 0 && lane < p.T * p.k) {       // (read after the next barrier)
+            rt.id[lane] = id;
+            rt.gate[lane] = weight;
+        }
+    } else {
+        if (!read_routing(p, rt, t0, cnt)) {
+            if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) record_error(p.ctrl, kErrInvalid);
+            return;
+        }
+        if (a >= rt.n) return;
+        e = rt.active[a];
+        named = rt.mask[e];
     }
-    if (a >= rt.n) return;
     if (split > 1) ptx::cluster_arrive_relaxed();
-    const int e = rt.active[a];
-    const uint32_t use = rt.mask[e] >> g;
+    const uint32_t use = named >> g;
     const int i0 = blockIdx.x * kHalf, in_half = i0 + (g & 3) * W::kLaneCols, n = (g >> 2) * p.I + in_half;
     const bool col = in_half < p.I;
     const int blocks = (p.H + W::kRows - 1) / W::kRows, stride = warps * split;

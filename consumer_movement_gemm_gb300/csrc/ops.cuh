@@ -87,20 +87,24 @@ struct MoeParams {
     long long timeout_ns, pipe_timeout_ns;
     Ctrl ctrl;
 };
-// Expert layers without rings and barriers (moe_direct.cu): by the weights of the
-// experts that 8 tokens (up to 8 in all) or 16 can name, once per that many,
-// fewer than 2^26 or 2^25.  Direct and through the rings, bf16 / 4-bit, us:
-//   1 token, 2 of 8 experts of 4096 x 2048 (48M)     24.4 / 16.4    31.9 / 21.0
-//   3 tokens, 6 of 32 of 2048 x 512 (54M)            24.6 / 18.8    31.1 / 21.4
-//   4 tokens, 2 of 8 of 4096 x 2048 (192M)           68.5 / 39.8    60.5 / 33.9
+// Expert layers without rings and barriers (moe_direct.cu), by the weights of the
+// experts that the tokens can name: up to 8 tokens fewer than 2^27 (bf16) or 2^26
+// (4-bit); more tokens fewer than 2^25 for 16 tokens, once per 16.  Direct and
+// through the rings, bf16 / 4-bit, us:
+//   1 token, 2 of 8 experts of 4096 x 2048 (48M)     23.9 / 15.9    31.9 / 21.0
+//   3 tokens, 6 of 32 of 2048 x 512 (54M)            24.3 / 18.4    31.1 / 21.4
+//   2 tokens, 2 of 8 of 4096 x 2048 (96M)            40.0 / 27.8    44.7 / 26.9
+//   1 token, 4 of 8 of 4096 x 4096 (192M)            74.8 / 47.1    72.3 / 35.9
+//   4 tokens, 4 of 32 of 4096 x 1024 (192M)          71.3           66.3
 //   12 tokens, 2 of 8 of 512 x 256 (3M)               9.4 / 7.8     19.8 / 18.9
 //   32 tokens, 2 of 8 of 1024 x 512 (24M)            18.3 / 15.9    21.7 / 22.0
 //   20 tokens, 4 of 32 of 512 x 256 (24M)            20.8 / 15.9    19.5 / 19.4
 //   64 tokens, 2 of 8 of 1024 x 512 (48M)            28.5 / 24.3    25.4 / 23.7
-inline bool use_direct_moe(int T, int k, int E, int H, int I)
+inline bool use_direct_moe(int T, int k, int E, int H, int I, int group)
 {
     const int most = T <= 8 ? 8 : 16, names = (T < most ? T : most) * k;
-    return 3LL * ((T + most - 1) / most) * (names < E ? names : E) * H * I < (T <= 8 ? 1LL << 26 : 1LL << 25);
+    const long long weights = 3LL * ((T + most - 1) / most) * (names < E ? names : E) * H * I;
+    return weights < (T > 8 ? 1LL << 25 : group ? 1LL << 26 : 1LL << 27);
 }
 cudaError_t prepare_moe_direct();
 cudaError_t launch_moe_direct(const MoeParams& p, int group, bool zero, int sms, cudaStream_t stream, bool pdl);

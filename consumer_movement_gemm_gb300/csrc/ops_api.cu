@@ -197,9 +197,9 @@ TOVL_API long long tovl_moe_decode_workspace(tovl_handle h, int T, int k, int H,
 
 // The part that both weight types share.  group: rows per scale, 0 for bf16.
 // (the injected fault is a barrier's, which the direct form does not have)
-static bool direct_moe(tovl_ctx* h, int T, int k, int E, int H, int I)
+static bool direct_moe(tovl_ctx* h, int T, int k, int E, int H, int I, int group)
 {
-    return !h->fault_gate_offset && use_direct_moe(T, k, E, H, I);
+    return !h->fault_gate_offset && use_direct_moe(T, k, E, H, I, group);
 }
 
 static int run_moe(tovl_handle h, MoeParams& p, int group, bool zero, const void* x, long long ldx, int T, int H, const int* topk_idx,
@@ -234,7 +234,7 @@ static int run_moe(tovl_handle h, MoeParams& p, int group, bool zero, const void
     p.pipe_timeout_ns = 4 * h->timeout_ns + 100000000LL;
     p.ctrl = h->ctrl;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (direct_moe(h, T, k, E, H, I))
+    if (direct_moe(h, T, k, E, H, I, group))
         return run(h, s, "expert layer launch", [&](bool pdl) { return launch_moe_direct(p, group, zero, h->num_sms, s, pdl); });
     return run(h, s, "expert layer launch",
                [&](bool pdl) { return launch_moe_decode(p, group, zero, h->num_sms, s, h->coop_enabled, pdl); });
@@ -253,7 +253,7 @@ TOVL_API int tovl_moe_decode(tovl_handle h, const void* x, long long ldx, int T,
     std::memset(&p, 0, sizeof p);
     p.up = {W13, nullptr, nullptr};
     p.down = {W2, nullptr, nullptr};
-    if (!direct_moe(h, T, k, E, H, I)) {
+    if (!direct_moe(h, T, k, E, H, I, 0)) {
         int rc = map_bf16(h, &p.w13, W13, E, H, 2 * I);
         if (rc == TOVL_OK) rc = map_bf16(h, &p.w2, W2, E, I, H);
         if (rc != TOVL_OK) return rc;
@@ -279,7 +279,7 @@ TOVL_API int tovl_moe_decode_q4(tovl_handle h, const void* x, long long ldx, int
     std::memset(&p, 0, sizeof p);
     p.up = {W13_q, W13_scale, W13_zero};
     p.down = {W2_q, W2_scale, W2_zero};
-    if (!direct_moe(h, T, k, E, H, I)) {
+    if (!direct_moe(h, T, k, E, H, I, group)) {
         int rc = map_q4(h, &p.w13, W13_q, W13_scale, W13_zero, E, H, 2 * I, group);
         if (rc == TOVL_OK) rc = map_q4(h, &p.w2, W2_q, W2_scale, W2_zero, E, I, H, group);
         if (rc != TOVL_OK) return rc;

@@ -530,10 +530,10 @@ def test_moe_q4_matches_the_formula(h, T, E, k, H, I, group, zeros):
               quant=group)
 
 
-# both sides of the size where other kernels begin: 2^26 weights of the experts that up to 8 tokens name, else 2^25 of those
-# that 16 name, once per 16
+# both sides of the size where other kernels begin: 2^27 (4-bit 2^26) weights of the experts that up to 8 tokens name, else
+# 2^25 of those that 16 name, once per 16
 @pytest.mark.parametrize("T,E,k,H,I,group,zeros", [
-    (1, 2, 1, 7168, 3136, 0, False), (1, 2, 1, 7168, 3112, 0, False), (7, 3, 2, 3592, 2088, 0, False), (9, 4, 4, 2056, 1368, 0, False),
+    (1, 2, 1, 8192, 5464, 0, False), (1, 2, 1, 8192, 5456, 0, False), (8, 4, 4, 3592, 3120, 0, False), (7, 3, 2, 3592, 2088, 0, False), (9, 4, 4, 2056, 1368, 0, False),
     (17, 2, 2, 4096, 920, 0, False), (33, 3, 2, 2048, 744, 0, False), (40, 16, 2, 1032, 296, 0, False), (64, 2, 2, 1544, 912, 0, False),
     (64, 8, 2, 1024, 360, 0, False), (64, 8, 2, 1024, 336, 0, False),
     (1, 3, 2, 4096, 2752, 64, True), (1, 3, 2, 4096, 2688, 64, True), (8, 4, 4, 2176, 2688, 128, False), (15, 2, 2, 3200, 1792, 128, True),
