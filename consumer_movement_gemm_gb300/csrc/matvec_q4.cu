@@ -97,12 +97,10 @@ __global__ void __launch_bounds__(Shape<G>::kThreads, 1) matvec_q4_kernel(const 
         __syncthreads();
         if (parts > 1) {
             if (threadIdx.x == 0) {
-                __threadfence();
                 int* counter = p.sync + kPartWord + tb.pr.item_of(t0);
                 const bool last = ptx::atom_add_acq_rel_gpu(counter, 1) == parts - 1;
                 if (last) ptx::st_relaxed_gpu(counter, 0);
                 tb.last = last;
-                __threadfence();
             }
             __syncthreads();
             if (!tb.last) return;

@@ -576,9 +576,8 @@ __device__ __forceinline__ int item_at(const Product& pr, const Queue& q, int n,
 // counter is cleared by the last CTA of the launch to leave.
 __device__ __forceinline__ void grid_barrier(int* counter, int target, const Ctrl& ctrl, long long timeout_ns)
 {
-    __syncthreads();
+    __syncthreads();       // (what the CTA wrote before it is released with thread 0's arrival)
     if (threadIdx.x == 0) {
-        __threadfence();
         ptx::red_add_release_gpu(counter, 1);
         if (ptx::ld_acquire_gpu(counter) < target) {
             const uint64_t start = ptx::globaltimer();
@@ -589,7 +588,6 @@ __device__ __forceinline__ void grid_barrier(int* counter, int target, const Ctr
                 }
             }
         }
-        __threadfence();
     }
     __syncthreads();
 }
