@@ -14,8 +14,8 @@
 // Large products stream the weights through skinny.cuh's rings, small ones read
 // them straight into registers (matvec_q4_direct.cuh); use_direct is the rule.
 // What bounds the ring: instruction issue, about 400 instructions per 2 KB of
-// weights with 9 to 16 rows and 335 with up to 8.  16 x 7168 x 32768: 45 us, 2.8
-// TB/s; 1 x 8192 x 28672: 31.6 us, 3.8 TB/s.
+// weights with 9 to 16 rows and 335 with up to 8.  16 x 7168 x 32768: 43.7 us, 2.8
+// TB/s; 1 x 8192 x 28672: 30.4 us, 4.0 TB/s.
 #include <type_traits>
 #include "launch.cuh"
 #include "matvec_q4_direct.cuh"

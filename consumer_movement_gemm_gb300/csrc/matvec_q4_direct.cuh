@@ -9,9 +9,9 @@
 // What it costs: the rows of the activations come from L2 once per 32 columns
 // and lane (the ring stages them once per 512 columns), and a CTA's first loads
 // and its join are bare.  What bounds it: the dependent loads of a CTA, launch to
-// store, at small sizes (512 x 512: 1.9 us, 2048 x 2048: 3.2, 4096 x 4096: 4.8
-// with one row, where the ring takes 7.9, 8.1 and 8.9), the loads in flight at
-// large ones (3.1 TB/s with one row, the ring 3.8).
+// store, at small sizes (512 x 512: 1.9 us, 2048 x 2048: 3.2, 4096 x 4096: 4.9
+// with one row, where the ring takes 7.6, 7.6 and 8.4), the loads in flight at
+// large ones (3.1 TB/s with one row, the ring 4.0).
 #pragma once
 #include "skinny.cuh"
 

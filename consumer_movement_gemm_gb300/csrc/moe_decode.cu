@@ -13,11 +13,11 @@
 // listed, each with the tokens that name it as its rows.
 //
 // What bounds it: the weights' stream (13 tokens, 4 of 32 experts of 7168 x 2048,
-// bf16, 2.3 GB: 357 us, 6.5 TB/s; 64 tokens, 2.8 GB: 452 us; 4-bit, 24 tokens, 2 of 8
-// of 4096 x 2048, 110 MB: 47.5 us, instructions) and about 15 us that do not depend
-// on it: launch and tables 4.5, three barriers 1.4 each, the sums of the parts 2
-// and 1.5, the CTAs' different ends 2 to 6 (4-bit, 1 token, 4 experts of 7168 x
-// 2048, 91 MB: 34.3 us).
+// bf16, 2.3 GB: 356 us, 6.5 TB/s; 64 tokens, 2.8 GB: 452 us; 4-bit, 24 tokens, 2 of 8
+// of 4096 x 2048, 110 MB: 45.9 us, instructions) and about 14 us that do not depend
+// on it: launch and tables 4.5, three barriers 1 each, the sums of the parts 2 and
+// 1.5, the CTAs' different ends 2 to 6 (4-bit, 1 token, 4 experts of 7168 x 2048, 91
+// MB: 33.0 us).
 //
 // Roundings: x and the weights are bf16 (or 4-bit with their scales applied
 // in fp32), sums are fp32.  With bf16 weights h is split into two bf16
@@ -267,7 +267,7 @@ struct Worker {
 
     // Four columns of a token to a thread; with few tokens to up to eight
     // neighbouring lanes, which share out its experts (one token, four experts
-    // of 7168 columns: 3.0 us with one lane, 1.6 with four).
+    // of 7168 columns: 3.0 us with one lane, 1.5 with four).
     __device__ __forceinline__ void outputs()
     {
         const int quads = p.H / 4, total = p.T * quads;

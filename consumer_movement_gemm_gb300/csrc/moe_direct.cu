@@ -22,10 +22,10 @@
 // power of two per 128 columns.  Sums are fp32, in a fixed order.
 //
 // What bounds it: at small sizes two launches and a CTA's dependent loads (1
-// token, 256 x 128: 5.1 us, 1024 x 512: 7.4, through the rings 14.9 and 19.8); at
+// token, 256 x 128: 5.2 us, 1024 x 512: 7.4, through the rings 14.4 and 19.2); at
 // large ones the bytes in flight, one block a warp, and the start of two grids (1
-// token, 2 of 8 experts of 4096 x 2048, bf16: 23.9 us, 4.2 TB/s, of 4096 x 4096: 40.1,
-// 5.0 TB/s; through the rings 31.9 and 45.2).  Two blocks a warp spill registers:
+// token, 2 of 8 experts of 4096 x 2048, bf16: 23.9 us, 4.2 TB/s, of 4096 x 4096: 39.9,
+// 5.0 TB/s; through the rings 30.6 and 43.9).  Two blocks a warp spill registers:
 // 27.1 us for the first.
 #include <type_traits>
 #include "launch.cuh"

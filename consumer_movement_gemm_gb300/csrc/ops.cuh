@@ -91,15 +91,17 @@ struct MoeParams {
 // experts that the tokens can name: up to 8 tokens fewer than 2^27 (bf16) or 2^26
 // (4-bit); more tokens fewer than 2^25 for 16 tokens, once per 16.  Direct and
 // through the rings, bf16 / 4-bit, us:
-//   1 token, 2 of 8 experts of 4096 x 2048 (48M)     23.9 / 15.9    31.9 / 21.0
-//   3 tokens, 6 of 32 of 2048 x 512 (54M)            24.3 / 18.4    31.1 / 21.4
-//   2 tokens, 2 of 8 of 4096 x 2048 (96M)            40.0 / 27.8    44.7 / 26.9
-//   1 token, 4 of 8 of 4096 x 4096 (192M)            74.8 / 47.1    72.3 / 35.9
-//   4 tokens, 4 of 32 of 4096 x 1024 (192M)          71.3           66.3
-//   12 tokens, 2 of 8 of 512 x 256 (3M)               9.4 / 7.8     19.8 / 18.9
-//   32 tokens, 2 of 8 of 1024 x 512 (24M)            18.3 / 15.9    21.7 / 22.0
-//   20 tokens, 4 of 32 of 512 x 256 (24M)            20.8 / 15.9    19.5 / 19.4
-//   64 tokens, 2 of 8 of 1024 x 512 (48M)            28.5 / 24.3    25.4 / 23.7
+//   1 token, 2 of 8 experts of 256 x 128 (0.2M)       5.2 / 5.0     14.4 / 16.5
+//   1 token, 2 of 8 of 4096 x 2048 (48M)             23.9 / 15.9    30.6 / 20.2
+//   3 tokens, 6 of 32 of 2048 x 512 (54M)            24.3 / 18.4    29.4 / 20.3
+//   1 token, 2 of 8 of 4096 x 4096 (96M)             39.9 / 27.1    43.9 / 24.9
+//   2 tokens, 2 of 8 of 4096 x 2048 (96M)            40.0 / 27.1    42.8 / 24.6
+//   1 token, 4 of 8 of 4096 x 4096 (192M)            74.6 / 47.2    71.0 / 34.5
+//   4 tokens, 4 of 32 of 4096 x 1024 (192M)          71.1 / 42.9    64.4 / 33.4
+//   12 tokens, 2 of 8 of 512 x 256 (3M)               8.9 / 7.7     18.7 / 18.1
+//   32 tokens, 2 of 8 of 1024 x 512 (24M)            18.4 / 15.8    20.1 / 20.9
+//   20 tokens, 4 of 32 of 512 x 256 (24M)            20.7 / 15.8    18.0 / 18.3
+//   64 tokens, 2 of 8 of 1024 x 512 (48M)            28.4 / 24.3    23.6 / 22.5
 inline bool use_direct_moe(int T, int k, int E, int H, int I, int group)
 {
     const int most = T <= 8 ? 8 : 16, names = (T < most ? T : most) * k;
@@ -114,9 +116,10 @@ cudaError_t launch_moe_decode(const MoeParams& p, int group, bool zero, int grid
                               bool pdl);
 
 // 4-bit products that read the matrix straight into registers: those of fewer
-// than 2^26 weights, counted once per 16 rows.  At the edge, 8192 x 8192: one
-// row 14.4 us so and 14.3 through the ring, 16 rows 24.0 and 21.5; below it, 4096
-// x 11008: 11.1 and 15.5, 18.7 and 22.6; above it, 8192 x 28672: 39 and 31.6.
+// than 2^26 weights, counted once per 16 rows.  So and through the ring, one row
+// and 16, us: below it, 4096 x 4096 4.9 / 7.1 and 8.4 / 15.6, 4096 x 11008 11.0 /
+// 18.5 and 14.3 / 21.3; at the edge, 8192 x 8192 14.6 / 24.0 and 13.7 / 20.8; above
+// it, 8192 x 28672 39 and 30.4.
 inline bool use_direct(int T, int K, int N) { return static_cast<long long>((T + 15) / 16) * K * N < (1LL << 26); }
 
 struct MatvecParams {

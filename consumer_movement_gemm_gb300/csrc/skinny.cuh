@@ -42,7 +42,7 @@
 // 4 bits: the instructions that turn a block into operands, about 335 per 2 KB
 // with up to 8 rows and 400 with 16, four warps a scheduler to hide their
 // latencies (49 % of the issue slots, 36 % of the integer pipe, 32 % of the tensor
-// pipe): 2.8 TB/s with 16 rows, 3.8 with one.
+// pipe): 2.8 TB/s with 16 rows, 4.0 with one.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
