@@ -319,6 +319,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) moe_up_kernel(const __grid_con
         e = rt.active[a];
         named = rt.mask[e];
     }
+    __syncwarp();
     if (split > 1) ptx::cluster_arrive_relaxed();
     const uint32_t use = named >> g;
     const int i0 = blockIdx.x * kHalf, in_half = i0 + (g & 3) * W::kLaneCols, n = (g >> 2) * p.I + in_half;

@@ -151,6 +151,40 @@ def test_norm_of_odd_rows(h, T, H, group, residual):
             assert torch.equal(x2, out) and torch.equal(res2, ro)
 
 
+@pytest.mark.parametrize("H,off", [(64, 1), (128, 7), (776, 3), (1024, 5), (2048, 1), (4104, 6), (8176, 3)])
+@pytest.mark.parametrize("group,residual", [(128, "bf16"), (32, "f32"), (0, "none")])
+def test_norm_rows_equally_far_from_a_boundary(h, H, off, group, residual):
+    """Whole multiples of eight elements, every tensor `off` elements past a 16-byte boundary."""
+    g = gen(H + off)
+    T, ld = 5, H + 8
+
+    def shifted(dtype, fill=None):
+        t = torch.full((T * ld + 32,), 7.0 if fill is None else fill, dtype=dtype, device=DEV)
+        return t, t[off:off + T * ld].view(T, ld)[:, :H]
+
+    weight = randn(g, H) + 1
+    _, x = shifted(BF16)
+    x.copy_(randn(g, T, H))
+    res = ro = None
+    if residual != "none":
+        dtype = BF16 if residual == "bf16" else F32
+        _, res = shifted(dtype)
+        res.copy_(randn(g, T, H, scale=3, dtype=dtype))
+        ro_all, ro = shifted(dtype)
+    out_all, out = shifted(BF16)
+    q_all = torch.full((T * H + 32,), 99, dtype=torch.uint8, device=DEV)
+    q = q_all[off:off + T * H].view(E4M3).view(T, H)
+    scale = torch.full((T, -(-H // group) if group else 1), float("nan"), device=DEV)
+    h.add_rmsnorm(x, weight, 1e-5, residual=res, residual_out=ro, out=out, q=q, q_scale=scale, group=group)
+    assert h.sync_status() == 0
+    check_norm(x, weight, 1e-5, res, ro, out, q, scale, group)
+    out.fill_(7.0), q_all[off:off + T * H].fill_(99)
+    assert (out_all == 7).all() and (q_all == 99).all()
+    if ro is not None:
+        ro.fill_(7.0)
+        assert (ro_all == 7).all()
+
+
 def test_norm_in_place_and_single_outputs(h):
     g = gen(5)
     x, weight, res = randn(g, 9, 768), randn(g, 768), randn(g, 9, 768)
