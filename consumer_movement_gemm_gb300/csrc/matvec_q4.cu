@@ -130,7 +130,9 @@ __global__ void __launch_bounds__(Shape<G>::kThreads, 1) matvec_q4_kernel(const 
 
 // One thread per column and group: the group's range gives scale and zero,
 // then eight rows at a time become a word.  Reads the group twice (the second
-// time from L1 / L2); runs once per weight matrix.
+// time from L1 / L2); runs once per weight matrix.  8192 x 28672: 319 us, bound by
+// a division and its rounding per weight (with the group in registers and one
+// pass over memory, at half the warps, 380).
 //
 //   symmetric   scale = bf16(amax / 7),         nibble = 8 + round(w / scale), zero 8
 //   with zeros  scale = bf16((max - min) / 15), zero = round(-min / scale), min <= 0 <= max
