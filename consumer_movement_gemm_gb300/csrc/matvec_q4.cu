@@ -202,7 +202,7 @@ cudaError_t prepare_matvec_q4()
 }
 
 template <int NT, bool XS, int G>
-static cudaError_t launch_direct(const MatvecParams& p, bool zero, int sms, cudaStream_t stream, bool pdl)
+static cudaError_t launch_direct(const MatvecDirectParams& p, bool zero, int sms, cudaStream_t stream, bool pdl)
 {
     const int tiles = (p.N + kDirectCols - 1) / kDirectCols, passes = (p.T + 15) / 16, blocks = (p.K + 127) / 128;
     // One CTA of 16 warps per SM where that is all of them; else CTAs of 8, two
@@ -239,23 +239,24 @@ static cudaError_t launch_direct(const MatvecParams& p, bool zero, int sms, cuda
 }
 
 template <int NT, bool XS>
-static cudaError_t launch_direct(const MatvecParams& p, int group, bool zero, int sms, cudaStream_t stream, bool pdl)
+static cudaError_t launch_direct(const MatvecDirectParams& p, int group, bool zero, int sms, cudaStream_t stream, bool pdl)
 {
     if (group == 32) return launch_direct<NT, XS, 32>(p, zero, sms, stream, pdl);
     if (group == 64) return launch_direct<NT, XS, 64>(p, zero, sms, stream, pdl);
     return launch_direct<NT, XS, 128>(p, zero, sms, stream, pdl);
 }
 
+cudaError_t launch_matvec_q4_direct(const MatvecDirectParams& p, bool e4m3, int group, bool zero, int sms, cudaStream_t stream,
+                                    bool pdl)
+{
+    if (p.T <= 8)
+        return e4m3 ? launch_direct<1, true>(p, group, zero, sms, stream, pdl) : launch_direct<1, false>(p, group, zero, sms, stream, pdl);
+    return e4m3 ? launch_direct<2, true>(p, group, zero, sms, stream, pdl) : launch_direct<2, false>(p, group, zero, sms, stream, pdl);
+}
+
 cudaError_t launch_matvec_q4(const MatvecParams& p, bool e4m3, int group, bool zero, int grid, cudaStream_t stream,
                              bool pdl)
 {
-    if (use_direct(p.T, p.K, p.N)) {
-        if (p.T <= 8)
-            return e4m3 ? launch_direct<1, true>(p, group, zero, grid, stream, pdl)
-                        : launch_direct<1, false>(p, group, zero, grid, stream, pdl);
-        return e4m3 ? launch_direct<2, true>(p, group, zero, grid, stream, pdl)
-                    : launch_direct<2, false>(p, group, zero, grid, stream, pdl);
-    }
     return with_kernel(e4m3, group, zero, [&](auto kernel, int smem) {
         return launch_grid(kernel, p, grid, kThreads4, smem, stream, false, pdl);
     });

@@ -32,7 +32,7 @@ struct DirectBlock {
     uint32_t zero[kGroups];
     float xs[NT];
 
-    __device__ __forceinline__ void load_weights(const MatvecParams& p, int b, int n, bool col, int t)
+    __device__ __forceinline__ void load_weights(const MatvecDirectParams& p, int b, int n, bool col, int t)
     {
 #pragma unroll
         for (int R = 0; R < 4; ++R) {
@@ -41,7 +41,7 @@ struct DirectBlock {
             if (col && octet * 8 < p.K) w[R] = ld_stream(static_cast<const uint32_t*>(p.wq) + static_cast<long long>(octet) * p.N + n);
         }
     }
-    __device__ __forceinline__ void load_scales(const MatvecParams& p, int b, int n, bool col)
+    __device__ __forceinline__ void load_scales(const MatvecDirectParams& p, int b, int n, bool col)
     {
 #pragma unroll
         for (int q = 0; q < kGroups; ++q) {
@@ -52,7 +52,7 @@ struct DirectBlock {
         }
     }
     // as they are in memory; a row past the last one repeats the first, its result is not stored
-    __device__ __forceinline__ void load_rows(const MatvecParams& p, int b, int r0, int cnt, int g, int t)
+    __device__ __forceinline__ void load_rows(const MatvecDirectParams& p, int b, int r0, int cnt, int g, int t)
     {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -104,7 +104,7 @@ struct DirectBlock {
 };
 
 template <int NT, bool XS, int G, bool Z>
-__global__ void __launch_bounds__(kDirectWarps * 32, 1) matvec_q4_direct_kernel(const __grid_constant__ MatvecParams p)
+__global__ void __launch_bounds__(kDirectWarps * 32, 1) matvec_q4_direct_kernel(const __grid_constant__ MatvecDirectParams p)
 {
     // (columns in fours, the four of token r exchanged by r / 2: no bank conflicts)
     __shared__ __align__(16) float red[kDirectWarps][NT * 8][kDirectCols];

@@ -52,7 +52,7 @@ struct Routing {
 
 // Routing of the tokens t0 .. t0 + cnt.  False if an id (of any token) is
 // outside [-1, E).
-__device__ bool read_routing(const MoeParams& p, Routing& rt, int t0, int cnt)
+__device__ bool read_routing(const MoeDirectParams& p, Routing& rt, int t0, int cnt)
 {
     const int tid = threadIdx.x;
     bool bad = false;
@@ -86,7 +86,7 @@ __device__ bool read_routing(const MoeParams& p, Routing& rt, int t0, int cnt)
 }
 
 // The slot of token t that names e first (-1: none), and the weights of all that do.
-__device__ __forceinline__ int find_slot(const MoeParams& p, const Routing& rt, int t, int e, float& gate)
+__device__ __forceinline__ int find_slot(const MoeDirectParams& p, const Routing& rt, int t, int e, float& gate)
 {
     int first = -1;
     gate = 0.f;
@@ -273,7 +273,7 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint3
 
 // grid: tiles of columns, CTAs of a cluster, (NT * 8 tokens, expert of theirs)
 template <int NT, int G, bool Z>
-__global__ void __launch_bounds__(kWarps * 32, 1) moe_up_kernel(const __grid_constant__ MoeParams p, int most_active)
+__global__ void __launch_bounds__(kWarps * 32, 1) moe_up_kernel(const __grid_constant__ MoeDirectParams p, int most_active)
 {
     using W = Weights<G, Z>;
     using S = Sums<NT, G, Z>;
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) moe_up_kernel(const __grid_con
 
 // grid: tiles of columns, CTAs of a cluster, NT * 8 tokens
 template <int NT, int G, bool Z>
-__global__ void __launch_bounds__(kWarps * 32, 1) moe_down_kernel(const __grid_constant__ MoeParams p)
+__global__ void __launch_bounds__(kWarps * 32, 1) moe_down_kernel(const __grid_constant__ MoeDirectParams p)
 {
     using W = Weights<G, Z>;
     using S = Sums<NT, G, Z>;
@@ -552,7 +552,7 @@ cudaLaunchConfig_t shape(cudaLaunchAttribute (&attr)[2], int tiles, int z, int b
 }
 
 template <int NT, int G, bool Z>
-cudaError_t launch(const MoeParams& p, int sms, cudaStream_t stream, bool pdl)
+cudaError_t launch(const MoeDirectParams& p, int sms, cudaStream_t stream, bool pdl)
 {
     constexpr int kCols = Sums<NT, G, Z>::kCols, kRows = Weights<G, Z>::kRows;
     constexpr int kSmem = static_cast<int>(sizeof(Joined<NT, kCols>));
@@ -604,7 +604,7 @@ cudaError_t prepare_moe_direct()
     return cudaSuccess;
 }
 
-cudaError_t launch_moe_direct(const MoeParams& p, int group, bool zero, int sms, cudaStream_t stream, bool pdl)
+cudaError_t launch_moe_direct(const MoeDirectParams& p, int group, bool zero, int sms, cudaStream_t stream, bool pdl)
 {
     return with_types(p.T > 8, group, zero, [&](auto nt, auto g, auto z) {
         return launch<decltype(nt)::value, decltype(g)::value, decltype(z)::value>(p, sms, stream, pdl);

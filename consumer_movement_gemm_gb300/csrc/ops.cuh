@@ -67,25 +67,34 @@ struct MoeWeights {
     const void* zero;
 };
 
-struct MoeParams {
-    WeightMaps w13, w2;
-    MoeWeights up, down;    // W13, W2
+// A call of the expert layer; the small form, whose time can be the host's, takes
+// no more (a launch copies its parameters).
+struct MoeCall {
     const void* x;          // bf16 [T][H], rows ldx apart
     long long ldx;
     const int* topk;        // [T][k]
     const float* gate_w;    // [T][k]
     void* out;              // bf16 [T][H], rows ldo apart
     long long ldo;
+    void* h_hi;             // activations between the two products [T*k][I]: bf16, and
+    void* h_lo;             // what the rounding left over; 4-bit weights: fp16, and its scales;
+                            // small form: fp32 from h_hi on
+    int T, k, E, H, I;
+    Ctrl ctrl;
+};
+
+struct MoeDirectParams : MoeCall {
+    MoeWeights up, down;    // W13, W2
+};
+
+struct MoeParams : MoeCall {
+    WeightMaps w13, w2;
     int out_vec;            // rows of out allow 8-byte stores
     int most_parts;         // a tile is cut into most_parts + 2 parts at most
-    void* h_hi;             // activations between the two products [T*k][I]: bf16, and
-    void* h_lo;             // what the rounding left over; 4-bit weights: fp16, and its scales
     float* part;            // [most_parts + 2][T*k][2I or H] parts of the products
-    int T, k, E, H, I;
     int* sync;              // kSyncWords counters
     int ready_offset;       // fault injection: CTAs that never come
     long long timeout_ns, pipe_timeout_ns;
-    Ctrl ctrl;
 };
 // Expert layers without rings and barriers (moe_direct.cu), by the weights of the
 // experts that the tokens can name: up to 8 tokens fewer than 2^27 (bf16) or 2^26
@@ -109,7 +118,7 @@ inline bool use_direct_moe(int T, int k, int E, int H, int I, int group)
     return weights < (T > 8 ? 1LL << 25 : group ? 1LL << 26 : 1LL << 27);
 }
 cudaError_t prepare_moe_direct();
-cudaError_t launch_moe_direct(const MoeParams& p, int group, bool zero, int sms, cudaStream_t stream, bool pdl);
+cudaError_t launch_moe_direct(const MoeDirectParams& p, int group, bool zero, int sms, cudaStream_t stream, bool pdl);
 cudaError_t prepare_moe_decode();
 // group: rows per scale of 4-bit weights, 0 for bf16
 cudaError_t launch_moe_decode(const MoeParams& p, int group, bool zero, int grid, cudaStream_t stream, bool cooperative,
@@ -122,23 +131,31 @@ cudaError_t launch_moe_decode(const MoeParams& p, int group, bool zero, int grid
 // it, 8192 x 28672 39 and 30.4.
 inline bool use_direct(int T, int K, int N) { return static_cast<long long>((T + 15) / 16) * K * N < (1LL << 26); }
 
-struct MatvecParams {
-    WeightMaps w;
+struct MatvecCall {
     const void* x;          // bf16 or e4m3 [T][K], rows ldx apart
     const float* x_scale;   // [T][ceil(K/128)] for e4m3
     void* out;              // bf16 [T][N], rows ldo apart
-    float* part;            // [most_parts + 2][T][N] parts of the product
-    const void* wq;         // the matrix itself, for the form without a ring
-    const void* w_scale;
-    const void* w_zero;
     long long ldx, ldo;
     int T, K, N;
-    int out_vec;
+};
+
+struct MatvecDirectParams : MatvecCall {
+    const void* wq;
+    const void* w_scale;
+    const void* w_zero;
+};
+
+struct MatvecParams : MatvecCall {
+    WeightMaps w;
+    float* part;            // [most_parts + 2][T][N] parts of the product
+    int out_vec;            // rows of out allow 8-byte stores
     int most_parts;
     int* sync;
     long long timeout_ns, pipe_timeout_ns;
     Ctrl ctrl;
 };
+cudaError_t launch_matvec_q4_direct(const MatvecDirectParams& p, bool e4m3, int group, bool zero, int sms, cudaStream_t stream,
+                                    bool pdl);
 cudaError_t prepare_matvec_q4();
 cudaError_t launch_matvec_q4(const MatvecParams& p, bool e4m3, int group, bool zero, int grid, cudaStream_t stream,
                              bool pdl);

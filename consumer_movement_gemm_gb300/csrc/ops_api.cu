@@ -196,14 +196,8 @@ TOVL_API long long tovl_moe_decode_workspace(tovl_handle h, int T, int k, int H,
 }
 
 // The part that both weight types share.  group: rows per scale, 0 for bf16.
-// (the injected fault is a barrier's, which the direct form does not have)
-static bool direct_moe(tovl_ctx* h, int T, int k, int E, int H, int I, int group)
-{
-    return !h->fault_gate_offset && use_direct_moe(T, k, E, H, I, group);
-}
-
-static int run_moe(tovl_handle h, MoeParams& p, int group, bool zero, const void* x, long long ldx, int T, int H, const int* topk_idx,
-                   const float* gate_w, int k, int E, int I, void* out, long long ldo, void* workspace,
+static int run_moe(tovl_handle h, const MoeWeights& up, const MoeWeights& down, int group, const void* x, long long ldx, int T, int H,
+                   const int* topk_idx, const float* gate_w, int k, int E, int I, void* out, long long ldo, void* workspace,
                    long long workspace_bytes, void* stream)
 {
     if (!x || !topk_idx || !gate_w || !out || !workspace || ldx < H || ldo < H || ldx % 8 || !aligned16(x) ||
@@ -211,31 +205,44 @@ static int run_moe(tovl_handle h, MoeParams& p, int group, bool zero, const void
         return TOVL_ERR_INVALID;
     const MoeSpace space(T, k, H, I);
     if (workspace_bytes < space.total) return TOVL_ERR_INVALID;
+    DeviceGuard g(h->device);
+    const bool zero = up.zero != nullptr;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
-    p.x = x;
-    p.ldx = ldx;
-    p.topk = topk_idx;
-    p.gate_w = gate_w;
-    p.out = out;
-    p.ldo = ldo;
+    MoeCall c = {};
+    c.x = x;
+    c.ldx = ldx;
+    c.topk = topk_idx;
+    c.gate_w = gate_w;
+    c.out = out;
+    c.ldo = ldo;
+    c.h_hi = ws;
+    c.h_lo = ws + space.h;
+    c.T = T;
+    c.k = k;
+    c.E = E;
+    c.H = H;
+    c.I = I;
+    c.ctrl = h->ctrl;
+    // (an injected fault is a barrier's, which the small form does not have)
+    if (!h->fault_gate_offset && use_direct_moe(T, k, E, H, I, group)) {
+        MoeDirectParams p = {c, up, down};
+        return run(h, s, "expert layer launch", [&](bool pdl) { return launch_moe_direct(p, group, zero, h->num_sms, s, pdl); });
+    }
+    MoeParams p;
+    std::memset(&p, 0, sizeof p);
+    static_cast<MoeCall&>(p) = c;
+    int rc = group ? map_q4(h, &p.w13, up.w, up.scale, up.zero, E, H, 2 * I, group) : map_bf16(h, &p.w13, up.w, E, H, 2 * I);
+    if (rc == TOVL_OK)
+        rc = group ? map_q4(h, &p.w2, down.w, down.scale, down.zero, E, I, H, group) : map_bf16(h, &p.w2, down.w, E, I, H);
+    if (rc != TOVL_OK) return rc;
     p.out_vec = ldo % 4 == 0 && aligned(out, 8);
     p.most_parts = most_parts(static_cast<long long>(T) * k, 0);
-    p.h_hi = ws;
-    p.h_lo = ws + space.h;
     p.part = reinterpret_cast<float*>(ws + 2 * space.h);
-    p.T = T;
-    p.k = k;
-    p.E = E;
-    p.H = H;
-    p.I = I;
     p.sync = h->sync_words;
     p.ready_offset = h->fault_gate_offset;
     p.timeout_ns = h->timeout_ns;
     p.pipe_timeout_ns = 4 * h->timeout_ns + 100000000LL;
-    p.ctrl = h->ctrl;
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (direct_moe(h, T, k, E, H, I, group))
-        return run(h, s, "expert layer launch", [&](bool pdl) { return launch_moe_direct(p, group, zero, h->num_sms, s, pdl); });
     return run(h, s, "expert layer launch",
                [&](bool pdl) { return launch_moe_decode(p, group, zero, h->num_sms, s, h->coop_enabled, pdl); });
 }
@@ -248,17 +255,8 @@ TOVL_API int tovl_moe_decode(tovl_handle h, const void* x, long long ldx, int T,
     if (!valid_moe_shape(T, k, H, I) || E < 1 || !W13 || !W2 || !aligned16(W13) || !aligned16(W2)) return TOVL_ERR_INVALID;
     if (!fits_moe(T, k, H, I) || E > kMaxExperts || h->num_sms > kMaxGrid) return TOVL_ERR_UNSUPPORTED;
     if (T == 0) return TOVL_OK;
-    DeviceGuard g(h->device);
-    MoeParams p;
-    std::memset(&p, 0, sizeof p);
-    p.up = {W13, nullptr, nullptr};
-    p.down = {W2, nullptr, nullptr};
-    if (!direct_moe(h, T, k, E, H, I, 0)) {
-        int rc = map_bf16(h, &p.w13, W13, E, H, 2 * I);
-        if (rc == TOVL_OK) rc = map_bf16(h, &p.w2, W2, E, I, H);
-        if (rc != TOVL_OK) return rc;
-    }
-    return run_moe(h, p, 0, false, x, ldx, T, H, topk_idx, gate_w, k, E, I, out, ldo, workspace, workspace_bytes, stream);
+    return run_moe(h, {W13, nullptr, nullptr}, {W2, nullptr, nullptr}, 0, x, ldx, T, H, topk_idx, gate_w, k, E, I, out, ldo, workspace,
+                   workspace_bytes, stream);
 }
 
 TOVL_API int tovl_moe_decode_q4(tovl_handle h, const void* x, long long ldx, int T, int H, const int* topk_idx,
@@ -274,18 +272,8 @@ TOVL_API int tovl_moe_decode_q4(tovl_handle h, const void* x, long long ldx, int
         return TOVL_ERR_INVALID;
     if (!fits_moe(T, k, H, I) || E > kMaxExperts || h->num_sms > kMaxGrid) return TOVL_ERR_UNSUPPORTED;
     if (T == 0) return TOVL_OK;
-    DeviceGuard g(h->device);
-    MoeParams p;
-    std::memset(&p, 0, sizeof p);
-    p.up = {W13_q, W13_scale, W13_zero};
-    p.down = {W2_q, W2_scale, W2_zero};
-    if (!direct_moe(h, T, k, E, H, I, group)) {
-        int rc = map_q4(h, &p.w13, W13_q, W13_scale, W13_zero, E, H, 2 * I, group);
-        if (rc == TOVL_OK) rc = map_q4(h, &p.w2, W2_q, W2_scale, W2_zero, E, I, H, group);
-        if (rc != TOVL_OK) return rc;
-    }
-    return run_moe(h, p, group, W13_zero != nullptr, x, ldx, T, H, topk_idx, gate_w, k, E, I, out, ldo, workspace,
-                   workspace_bytes, stream);
+    return run_moe(h, {W13_q, W13_scale, W13_zero}, {W2_q, W2_scale, W2_zero}, group, x, ldx, T, H, topk_idx, gate_w, k, E, I, out, ldo,
+                   workspace, workspace_bytes, stream);
 }
 
 TOVL_API long long tovl_matvec_q4_workspace(tovl_handle h, int T, int N)
@@ -310,33 +298,28 @@ TOVL_API int tovl_matvec_q4(tovl_handle h, const void* x, int x_type, const floa
         !aligned(x_scale, 4) || !aligned(workspace, 256) || workspace_bytes < tovl_matvec_q4_workspace(h, T, N))
         return TOVL_ERR_INVALID;
     DeviceGuard g(h->device);
+    const bool e4m3 = x_type == TOVL_E4M3, zero = w_zero != nullptr;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const MatvecCall c = {x, x_scale, out, ldx, ldo, T, K, N};
+    if (use_direct(T, K, N)) {
+        const MatvecDirectParams p = {c, wq, w_scale, w_zero};
+        return run(h, s, "4-bit product launch",
+                   [&](bool pdl) { return launch_matvec_q4_direct(p, e4m3, group, zero, h->num_sms, s, pdl); });
+    }
     MatvecParams p;
     std::memset(&p, 0, sizeof p);
-    p.wq = wq;
-    p.w_scale = w_scale;
-    p.w_zero = w_zero;
-    if (!use_direct(T, K, N)) {
-        const int rc = map_q4(h, &p.w, wq, w_scale, w_zero, 1, K, N, group);
-        if (rc != TOVL_OK) return rc;
-    }
-    p.x = x;
-    p.x_scale = x_scale;
-    p.out = out;
+    static_cast<MatvecCall&>(p) = c;
+    const int rc = map_q4(h, &p.w, wq, w_scale, w_zero, 1, K, N, group);
+    if (rc != TOVL_OK) return rc;
     p.part = static_cast<float*>(workspace);
     p.out_vec = ldo % 4 == 0 && aligned(out, 8);
     p.most_parts = most_parts(T, N);
-    p.timeout_ns = h->timeout_ns;
-    p.ldx = ldx;
-    p.ldo = ldo;
-    p.T = T;
-    p.K = K;
-    p.N = N;
     p.sync = h->sync_words;
+    p.timeout_ns = h->timeout_ns;
     p.pipe_timeout_ns = 4 * h->timeout_ns + 100000000LL;
     p.ctrl = h->ctrl;
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
     return run(h, s, "4-bit product launch",
-               [&](bool pdl) { return launch_matvec_q4(p, x_type == TOVL_E4M3, group, w_zero != nullptr, h->num_sms, s, pdl); });
+               [&](bool pdl) { return launch_matvec_q4(p, e4m3, group, zero, h->num_sms, s, pdl); });
 }
 
 TOVL_API int tovl_quantize_q4(tovl_handle h, const void* W, int E, int K, int N, int group, void* wq, void* w_scale,

@@ -213,7 +213,7 @@ def _dense(name, t, dtype, shape):
 def _bytes(name, t) -> int:
     if not t.is_contiguous():
         raise TypeError(f"{name} must be contiguous")
-    return t.numel() * t.element_size()
+    return t.nbytes
 
 
 def _packed(name, w, lead, K, N, group):
@@ -221,9 +221,14 @@ def _packed(name, w, lead, K, N, group):
     if group not in (32, 64, 128) or K % group:
         raise TypeError(f"{name}: groups are 32, 64 or 128 rows and divide K")
     words, scales, zeros = w
-    return (_dense(name + " words", words, _I32, lead + (K // 8, N)),
-            _dense(name + " scales", scales, _BF16, lead + (K // group, N)),
-            None if zeros is None else _dense(name + " zeros", zeros, _U8, lead + (K // group, N)))
+    rows, groups = lead + (K // 8, N), lead + (K // group, N)
+    if not (words is not None and words.dtype is _I32 and words.shape == rows and words.is_contiguous()):
+        _dense(name + " words", words, _I32, rows)
+    if not (scales is not None and scales.dtype is _BF16 and scales.shape == groups and scales.is_contiguous()):
+        _dense(name + " scales", scales, _BF16, groups)
+    if zeros is None:
+        return words.data_ptr(), scales.data_ptr(), None
+    return words.data_ptr(), scales.data_ptr(), _dense("zeros", zeros, _U8, groups)
 
 
 def default_config(device: int = 0) -> tovl_config:
@@ -381,7 +386,7 @@ class Handle:
             _load_types()
         T, H = x.shape
         k = topk.shape[1]
-        E, I = W2.shape[0], W2.shape[1]
+        E, I = W2.shape[:2]
         rc = (_lib or load()).tovl_moe_decode(
             self.h, x.data_ptr(), _matrix("x", x, _BF16, T, H), T, H, _dense("topk", topk, _I32, (T, k)),
             _dense("gate_w", gate_w, _F32, (T, k)), k, E, _dense("W13", W13, _BF16, (E, H, 2 * I)),
@@ -396,7 +401,8 @@ class Handle:
             _load_types()
         T, H = x.shape
         k = topk.shape[1]
-        E, I = W2[0].shape[0], W2[0].shape[1] * 8
+        E, I8 = W2[0].shape[:2]
+        I = I8 * 8
         rc = (_lib or load()).tovl_moe_decode_q4(
             self.h, x.data_ptr(), _matrix("x", x, _BF16, T, H), T, H, _dense("topk", topk, _I32, (T, k)),
             _dense("gate_w", gate_w, _F32, (T, k)), k, E, *_packed("W13", W13, (E,), H, 2 * I, group),
