@@ -289,10 +289,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) moe_up_kernel(const __grid_con
     ptx::grid_dep_launch();
     int e;
     uint32_t named;                    // tokens that name e
-    if (p.T * p.k <= 32) {
+    if (p.T <= NT * 8 && p.T * p.k <= 32) {
         // One name a lane: every warp finds the expert by itself, without a barrier
         // before the first weights (1 token, 1024 x 512: 7.8 -> 7.4 us); the experts
-        // in the order of their first names.
+        // in the order of their first names.  Of a call whose tokens are all here
+        // (t0 = 0): tokens and names are counted from the call's first.
         const int id = lane < p.T * p.k ? __ldcg(p.topk + lane) : -1;
         const float weight = lane < p.T * p.k ? __ldcg(p.gate_w + lane) : 0.f;
         const uint32_t same = __match_any_sync(0xffffffffu, id);

@@ -1,0 +1,100 @@
+"""Decode-step operators at the edges of their kernels' variants, against plain 64-bit implementations.
+
+The tolerances are those of test_gpu_decode.py, error bounds and not fits, with one of their own: with 4-bit
+weights h, the activation between the two products, is fp16 times a power of two per 128 columns, which brings
+the largest of them to [2^14, 2^15).  Rounding to the nearest of 11 significant bits is 2^-11 of the value at
+most, and below 2^-14 half of a unit of 2^-24, which is 2^-39 of the largest.  With bf16 weights h is two bf16
+numbers, which leave 2^-16.
+"""
+import pytest
+import torch
+
+from consumer_movement_gemm_gb300 import tovl
+from tests.test_gpu_decode import (BF16, D, DEV, E4M3, F32, U16, U32, bf16_experts, gen, guarded, h, packed, randn,  # noqa: F401
+                                   routing, space, sum_bound, unpack, within)
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ the expert layer
+def moe_bound(x, topk, gate, W13, W2, quant):
+    """out and the bound of its error, in 64 bits."""
+    T, H = x.shape
+    if quant:
+        W13, W2 = unpack(*W13, quant), unpack(*W2, quant)
+    I = W2.shape[1]
+    out = torch.zeros(T, H, dtype=D, device=DEV)
+    bound = torch.zeros(T, H, dtype=D, device=DEV)
+    for e in torch.unique(topk[topk >= 0]).tolist():
+        t, j = torch.nonzero(topk == e, as_tuple=True)
+        a, b = x[t].to(D), W13[e].to(D)
+        z, dz = a @ b, sum_bound(H, a.abs() @ b.abs())
+        zg, zu, dg, du = z[:, :I], z[:, I:], dz[:, :I], dz[:, I:]
+        s = zg * torch.sigmoid(zg)
+        hh = s * zu
+        # |silu'| <= 1.1; exp and the division: 8 units
+        dh = 1.1 * dg * zu.abs() + (s.abs() + 1.1 * dg) * du + (8 * U32 + (2.0 ** -11 if quant else 2.0 ** -16)) * hh.abs()
+        if quant:
+            top = torch.cat([p.abs().amax(1, keepdim=True).expand_as(p) for p in hh.split(128, 1)], 1)
+            dh = dh + 2.0 ** -39 * top
+        w2, w = W2[e].to(D), gate[t, j].to(D)[:, None]
+        mag = (hh.abs() + dh) @ w2.abs()
+        out.index_add_(0, t, (hh @ w2) * w)
+        bound.index_add_(0, t, w.abs() * (dh @ w2.abs() + sum_bound(2 * I, mag)))
+    return out, bound + U16 * out.abs()
+
+
+def experts(g, E, H, I, quant, zeros=True):
+    if quant:
+        return packed(g, (E,), H, 2 * I, quant, zeros), packed(g, (E,), I, H, quant, zeros)
+    return bf16_experts(g, E, H, I)
+
+
+def run_moe(h, x, topk, gate, w, quant, out, ws, stream=None):  # noqa: F811
+    if quant:
+        h.moe_decode_q4(x, topk, gate, *w, quant, out, ws, stream=stream)
+    else:
+        h.moe_decode(x, topk, gate, *w, out, ws, stream=stream)
+
+
+def absent(g, topk, share=0.25):
+    topk[torch.rand(topk.shape, generator=g, device=DEV) < share] = -1
+    return topk
+
+
+# one pass of the small form takes up to 16 tokens, and up to 32 names are found by every warp by itself: both sides of
+# either edge, more experts than one pass can name, and calls that end inside a pass
+@pytest.mark.parametrize("T", [8, 9, 15, 16, 17, 20, 31, 32, 33])
+@pytest.mark.parametrize("k", [1, 2, 4])
+@pytest.mark.parametrize("E", [4, 19, 62])
+@pytest.mark.parametrize("quant", [None, 32])
+def test_moe_of_few_names(h, T, k, E, quant):  # noqa: F811
+    g = gen(T * 1000 + E * 10 + k)
+    H, I = 160, 96
+    topk, gate = routing(g, T, E, k)
+    absent(g, topk)
+    w = experts(g, E, H, I, quant)
+    x = torch.full((T + 32, H), float("nan"), dtype=BF16, device=DEV)[:T]      # what lies behind the rows shows where it is used
+    x.copy_(randn(g, T, H))
+    want, bound = moe_bound(x, topk, gate, *w, quant)
+    ws = space(h.moe_decode_workspace(T, k, H, I))
+    for _ in range(2):
+        out, intact = guarded(T, H)
+        run_moe(h, x, topk, gate, w, quant, out, ws)
+        assert h.sync_status() == 0
+        within(out, want, bound, "out")
+        assert intact()
+
+
+@pytest.mark.parametrize("quant", [None, 64])
+def test_moe_of_one_name_a_token(h, quant):  # noqa: F811
+    """Top-1 routing: every token an expert of its own, more of them than a pass has tokens, in the two-kernel form."""
+    g = gen(61)
+    T, E, k, H, I = 32, 32, 1, 512, 256
+    topk = torch.randperm(E, generator=g, device=DEV).to(torch.int32)[:, None].contiguous()
+    gate = torch.rand(T, k, generator=g, device=DEV) + 0.5
+    w, x = experts(g, E, H, I, quant), randn(g, T, H)
+    out, ws = torch.empty(T, H, dtype=BF16, device=DEV), space(h.moe_decode_workspace(T, k, H, I))
+    run_moe(h, x, topk, gate, w, quant, out, ws)
+    assert h.sync_status() == 0
+    within(out, *moe_bound(x, topk, gate, *w, quant), "out")
