@@ -12,7 +12,7 @@
 // is 4, 8 or 16 neighbouring lanes.
 //
 // What bounds it: memory.  Rows of whole 16-byte pieces (norm_rows_kernel): 16384 x
-// 7168, bf16 residual, both outputs, 172 us, 6.2 TB/s; 16384 x 8192 203 us, 6.0;
+// 7168, bf16 residual, both outputs, 167 us, 6.3 TB/s; 16384 x 8192 203 us, 6.0;
 // 333 x 7168, fp32 residual, 8.3 us (one to three rows an SM: their latency); 1 x
 // 4096 2.7 us.  Rows that start elsewhere: norm_offset_kernel, norm_kernel.
 #include <cuda_bf16.h>
@@ -49,6 +49,25 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
 }
+
+// A group's scale and what its elements' quotients by it are made with.  A product
+// with 448 / max rounds twice, and its e4m3 is the wrong neighbour where y / scale
+// lies half way between two, as 175 / 7 does; one residual of the fused
+// multiply-add takes the quotient to 2^-46 before its own rounding (Markstein 1990,
+// "Computation of elementary functions on the IBM RISC System/6000 processor").
+// 16384 x 7168: 167 us with the residual, 172 with the product alone, 186 with a
+// division; off the boundaries (16384 x 777) 45.5, 43.5 and 53.
+struct Scale {
+    float s, inverse;
+    __device__ __forceinline__ explicit Scale(float amax) : s(max_nan(amax, kMinAmax) / kE4m3Max), inverse(1.f / s) {}
+    __device__ __forceinline__ explicit Scale(float2 of) : s(of.x), inverse(of.y) {}
+    __device__ __forceinline__ float divide(float y) const
+    {
+        // (an infinite scale: no residual, the quotients are 0, or NaN of an infinity)
+        const float q = y * inverse;
+        return fmaf(fmaf(-q, s == INFINITY ? 0.f : s, y), inverse, q);
+    }
+};
 
 // Eight consecutive elements, of which the first n exist, moved in accesses of
 // W elements.
@@ -129,11 +148,11 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8], int n)
 }
 
 template <int W>
-__device__ __forceinline__ void store8_e4m3(uint8_t* p, const float (&v)[8], float inv, int n)
+__device__ __forceinline__ void store8_e4m3(uint8_t* p, const float (&v)[8], const Scale& scale, int n)
 {
     uint32_t h[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = e4m3x2(v[2 * i] * inv, v[2 * i + 1] * inv);
+    for (int i = 0; i < 4; ++i) h[i] = e4m3x2(scale.divide(v[2 * i]), scale.divide(v[2 * i + 1]));
     if constexpr (W == 8) {
         if (n > 0) *reinterpret_cast<uint2*>(p) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
     } else if constexpr (W == 2) {
@@ -179,9 +198,9 @@ __device__ __forceinline__ void store_group(const NormParams& p, int c, const fl
     m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
     if (p.group > 32) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 4));
     if (p.group > 64) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 8));
-    m = max_nan(m, kMinAmax);
-    if (c % p.group == 0 && c < p.H) scale[c / p.group] = m / kE4m3Max;
-    store8_e4m3<W>(q + c, v, kE4m3Max / m, p.H - c);
+    const Scale of(m);
+    if (c % p.group == 0 && c < p.H) scale[c / p.group] = of.s;
+    store8_e4m3<W>(q + c, v, of, p.H - c);
 }
 
 // Sixteen-byte pieces of a row as they come from memory.
@@ -291,12 +310,12 @@ __global__ void __launch_bounds__(WARP ? kWarpRows * 32 : 512, VPT <= 2 ? 2 : 1)
             float m = amax[0];
 #pragma unroll
             for (int j = 1; j < VPT; ++j) m = max_nan(m, amax[j]);
-            m = max_nan(row_reduce<true>(m, max_buf[turn], WARP), kMinAmax);
-            if (tid == 0) scale[0] = m / kE4m3Max;
+            const Scale of(row_reduce<true>(m, max_buf[turn], WARP));
+            if (tid == 0) scale[0] = of.s;
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
                 const int c = tid * 8 + j * step;
-                store8_e4m3<8>(q + c, v[j], kE4m3Max / m, p.H - c);
+                store8_e4m3<8>(q + c, v[j], of, p.H - c);
             }
         } else {
 #pragma unroll
@@ -383,12 +402,12 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormParams p, int warp
         float m = amax[0];
 #pragma unroll
         for (int j = 1; j < VPT; ++j) m = max_nan(m, amax[j]);
-        m = max_nan(row_reduce<true>(m, max_buf, warp_row), kMinAmax);
-        if (tid == 0) scale[0] = m / kE4m3Max;
+        const Scale of(row_reduce<true>(m, max_buf, warp_row));
+        if (tid == 0) scale[0] = of.s;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int c = tid * 8 + j * step;
-            store8_e4m3<W>(q + c, v[j], kE4m3Max / m, p.H - c);
+            store8_e4m3<W>(q + c, v[j], of, p.H - c);
         }
     } else {
 #pragma unroll
@@ -404,9 +423,9 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormParams p, int warp
 // inside a piece, always after s elements: the maxima of both sides, and the
 // scales, cross to the neighbouring thread.  A row to a warp (WARP) or a CTA,
 // one piece to a thread as far as a CTA goes: with four the straight code of a row
-// (64 KB) ran as fast as its instructions came from L2 (16384 x 777: 118 us, 44
-// with one).  What bounds it: the barriers and the dependent loads of a row, two
-// or three rows an SM in flight (16384 x 5001, 228 us, 3.2 TB/s).
+// (64 KB) ran as fast as its instructions came from L2 (16384 x 777: 2.7 times the
+// time with one).  What bounds it: the barriers and the dependent loads of a row, two
+// or three rows an SM in flight (16384 x 5001, 242 us, 3.1 TB/s).
 __device__ __forceinline__ uint4 shift_eight(const uint4& a, const uint4& b, int s)
 {
     uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
@@ -455,7 +474,8 @@ __global__ void __launch_bounds__(WARP ? kWarpRows * 32 : kOffsetThreads) norm_o
 {
     constexpr int kGroups = WARP ? kWarpRowMax / 32 : kOffsetThreads * VPT * 8 / 32;
     using R = typename std::conditional<RES == 2, float, __nv_bfloat16>::type;
-    __shared__ float sum_buf[32], max_buf[32], edge[VPT][33], inverse[WARP ? kWarpRows : 1][kGroups];
+    __shared__ float sum_buf[32], max_buf[32], edge[VPT][33];
+    __shared__ float2 of_groups[WARP ? kWarpRows : 1][kGroups];    // Scale of each
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long row = WARP ? static_cast<long long>(blockIdx.x) * kWarpRows + warp : blockIdx.x;
     const int threads = WARP ? 32 : blockDim.x, tid = WARP ? lane : threadIdx.x;
@@ -529,16 +549,16 @@ __global__ void __launch_bounds__(WARP ? kWarpRows * 32 : kOffsetThreads) norm_o
     if (!p.q) return;
     float* scale = p.q_scale + row * p.n_groups;
     uint8_t* q = p.q + row * p.H;
-    float* inv = inverse[WARP ? warp : 0];
+    float2* own = of_groups[WARP ? warp : 0];
     int shift = 31;                     // of a column to its group
     if (p.group == p.H) {
         float m = 0.f;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) m = max_nan(m, max_nan(before[j], after[j]));
-        m = max_nan(row_reduce<true>(m, max_buf, WARP), kMinAmax);
+        const Scale of(row_reduce<true>(m, max_buf, WARP));
         if (tid == 0) {
-            scale[0] = m / kE4m3Max;
-            inv[0] = kE4m3Max / m;
+            scale[0] = of.s;
+            own[0] = make_float2(of.s, of.inverse);
         }
     } else {
         shift = 31 - __clz(p.group);
@@ -563,11 +583,11 @@ __global__ void __launch_bounds__(WARP ? kWarpRows * 32 : kOffsetThreads) norm_o
             m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
             if (p.group > 32) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 4));
             if (p.group > 64) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 8));
-            m = max_nan(m, kMinAmax);
             const int c = lo[j] + s;
             if ((c & (p.group - 1)) == 0 && c < p.H) {
-                scale[c >> shift] = m / kE4m3Max;
-                inv[c >> shift] = kE4m3Max / m;
+                const Scale of(m);
+                scale[c >> shift] = of.s;
+                own[c >> shift] = make_float2(of.s, of.inverse);
             }
         }
     }
@@ -577,10 +597,10 @@ __global__ void __launch_bounds__(WARP ? kWarpRows * 32 : kOffsetThreads) norm_o
     for (int j = 0; j < VPT; ++j) {
         if (last[j] <= 0) continue;
         const int c = lo[j] + s;
-        const float i0 = inv[max(c - 8, 0) >> shift], i1 = inv[min(c, p.H - 1) >> shift];
+        const Scale s0(own[max(c - 8, 0) >> shift]), s1(own[min(c, p.H - 1) >> shift]);
         uint32_t h[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = e4m3x2(v[j][2 * i] * (2 * i < s ? i0 : i1), v[j][2 * i + 1] * (2 * i + 1 < s ? i0 : i1));
+        for (int i = 0; i < 4; ++i) h[i] = e4m3x2((2 * i < s ? s0 : s1).divide(v[j][2 * i]), (2 * i + 1 < s ? s0 : s1).divide(v[j][2 * i + 1]));
         if (first[j] == 0 && last[j] == 8) {
             *reinterpret_cast<uint2*>(q + lo[j]) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
         } else {
@@ -669,9 +689,9 @@ cudaError_t launch_norm(const NormParams& p, int width, bool same_offset, int nu
         lc.blockDim = dim3(up32((vecs + 3) / 4));
         return launch_any<8>(p, lc, 0, 4);
     }
-    // Pieces, where the rows allow them, against pairs: 16384 x 1002 46 us and 102,
-    // 16384 x 2002 88 and 88, 16384 x 2934 142 and 118 (fewer barriers); against
-    // single elements: 16384 x 777 44 and 101, 16384 x 5001 228 and 515.  (Up to
+    // Pieces, where the rows allow them, against pairs: 16384 x 1002 47 us and 103,
+    // 16384 x 2002 92 and 87, 16384 x 2934 149 and 133 (fewer barriers); against
+    // single elements: 16384 x 777 45 and 97, 16384 x 5001 242 and 509.  (Up to
     // seven elements of a row's first piece are not the row's.)
     const int pieces = (p.H + 14) / 8;
     if (same_offset && pieces <= 2 * kOffsetThreads && (width == 1 || warp_row)) {

@@ -98,3 +98,31 @@ def test_moe_of_one_name_a_token(h, quant):  # noqa: F811
     run_moe(h, x, topk, gate, w, quant, out, ws)
     assert h.sync_status() == 0
     within(out, *moe_bound(x, topk, gate, *w, quant), "out")
+
+
+# ------------------------------------------------------------------ norm
+# aligned rows a warp and a CTA each, two pieces a thread and more, rows off the boundaries, pairs and single elements
+@pytest.mark.parametrize("H,pad", [(384, 0), (1024, 0), (2048, 0), (10240, 0), (20480, 0), (203, 0), (2051, 0), (9001, 0), (2050, 0), (514, 3)])
+@pytest.mark.parametrize("group", [32, 128, 0])
+def test_norm_rounds_the_quotient(h, H, pad, group):  # noqa: F811
+    """Rows of +-1 with eps = 0 give y = +-weight exactly, the groups' largest make the scales small odd numbers, and the
+    quotients lie half way between two e4m3 numbers or are such numbers: q is e4m3(y / scale), ties to even."""
+    g = gen(H + group)
+    T, n = 3, group or H
+    pick = lambda values, size: torch.tensor(values, device=DEV)[torch.randint(len(values), (size,), generator=g, device=DEV)]  # noqa: E731
+    # odd * 25 and odd * 29 have eight bits at most, as bf16 has; so has 448 * odd
+    scale = pick([1.0, 3.0, 5.0, 7.0], -(-H // n))
+    ratio = pick([25.0, 29.0, 17.0, 27.0, 16.0, 7.5], H) * torch.exp2(pick([0.0, 1.0, 2.0, 3.0, -5.0, -11.0], H))
+    ratio[torch.arange(H, device=DEV) % n == 0] = 448
+    ratio *= pick([1.0, -1.0], H)
+    weight = (ratio * scale.repeat_interleave(n)[:H]).to(BF16)
+    want = weight.to(D) / scale.repeat_interleave(n)[:H].to(D)
+    assert torch.equal(want.float(), ratio)
+    sign = pick([1.0, -1.0], T * H).view(T, H)
+    x = torch.empty(T, H + pad, dtype=BF16, device=DEV)[:, :H]
+    x.copy_(sign)
+    q, got = torch.empty(T, H, dtype=E4M3, device=DEV), torch.empty(T, len(scale), device=DEV)
+    h.add_rmsnorm(x, weight, 0.0, q=q, q_scale=got, group=group)
+    assert h.sync_status() == 0
+    assert torch.equal(got, scale.expand(T, -1))
+    assert torch.equal(q.float(), (sign * ratio).to(E4M3).float())
