@@ -151,10 +151,11 @@ __global__ void __launch_bounds__(256) quantize_q4_kernel(const QuantParams p)
         lo = fminf(lo, v);
         hi = fmaxf(hi, v);
     }
-    // the scale that the products use is the rounded one
-    const float want = p.zero ? (hi - lo) / 15.f : fmaxf(hi, -lo) / 7.f;
+    // the scale that the products use is the rounded one (halves: hi - lo may be
+    // over the largest number)
+    const float want = p.zero ? (0.5f * hi - 0.5f * lo) / 7.5f : fmaxf(hi, -lo) / 7.f;
     __nv_bfloat16 sb = __float2bfloat16(want);
-    if (__bfloat162float(sb) < 1e-30f) sb = __float2bfloat16(1.f);    // a group of zeros
+    if (__bfloat162float(sb) == 0.f) sb = __float2bfloat16(1.f);      // a group of zeros
     const float s = __bfloat162float(sb);
     const int z = p.zero ? min(15, max(0, __float2int_rn(-lo / s))) : 8;
     static_cast<__nv_bfloat16*>(p.scale)[eg * p.N + n] = sb;

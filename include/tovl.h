@@ -358,7 +358,8 @@ int tovl_matvec_q4(tovl_handle h, const void* x, int x_type, const float* x_scal
 /* Quantises bf16 matrices W [E][K][N] into the packed form, rounding to
  * nearest: without zeros (w_zero null) scale = max |w| / 7, with zeros scale =
  * (max(w, 0) - min(w, 0)) / 15 and zero = round(-min(w, 0) / scale), the scale
- * rounded to bf16 first.  Finite weights only. */
+ * rounded to bf16 first; 1 (and nothing but zeros) where that rounds to 0.
+ * Any finite weights. */
 int tovl_quantize_q4(tovl_handle h, const void* W, int E, int K, int N, int group, void* wq, void* w_scale,
                      void* w_zero, void* stream);
 

@@ -126,3 +126,32 @@ def test_norm_rounds_the_quotient(h, H, pad, group):  # noqa: F811
     assert h.sync_status() == 0
     assert torch.equal(got, scale.expand(T, -1))
     assert torch.equal(q.float(), (sign * ratio).to(E4M3).float())
+
+
+# ------------------------------------------------------------------ packed weights
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_quantize_takes_any_finite_weights(h, group, zeros):  # noqa: F811
+    """Columns of every magnitude that bf16 has, ranges over its largest number and below its normal ones."""
+    g = gen(group)
+    K, N = 256, 32
+    top = torch.tensor([3e38, 1e38, 1e30, 1.0, 1e-20, 1e-29, 1e-30, 1e-32, 1e-36, 1e-38, 1e-39, 2.0 ** -130, 2.0 ** -132, 2.0 ** -133, 0.0, 3.3e38],
+                       dtype=D, device=DEV).repeat(2)
+    w = ((torch.rand(K, N, generator=g, device=DEV).to(D) * 2 - 1) * top).to(BF16)
+    w[::group, :] = top.to(BF16)                       # the range is the column's: its ends in every group
+    w[1::group, :16] = -top[:16].to(BF16)
+    w[:, 16:] = w[:, 16:].abs()
+    q, scale, zero = h.quantize_q4(w, group, zeros)
+    assert h.sync_status() == 0
+    parts = w.float().view(K // group, group, N)
+    hi, lo = parts.amax(1).clamp_min(0), parts.amin(1).clamp_max(0)
+    want = (hi / 2 - lo / 2) / 7.5 if zeros else torch.maximum(hi, -lo) / 7
+    none = want.to(BF16) == 0                          # nothing that bf16 can tell from zero: zeros, under any scale
+    assert torch.equal(scale, torch.where(none, 1.0, want).to(BF16))
+    got = unpack(q, scale, zero, group)
+    # half a level, with zeros half a level more, and what the rounded scale's 7 or 15 levels are short of the range;
+    # dividing in fp32 may take a weight over the middle of two levels
+    s = scale.to(D)
+    bound = s * ((1.0 if zeros else 0.5) + 2.0 ** -18) + (15 if zeros else 7) * (s - want.to(D)).abs()
+    within(got, w.to(D), torch.where(none, (hi - lo).to(D), bound).repeat_interleave(group, 0), "quantised weights")
+    assert (got.view(K // group, group, N)[none[:, None, :].expand(-1, group, -1)] == 0).all()
