@@ -97,25 +97,45 @@ struct MoeParams : MoeCall {
     long long timeout_ns, pipe_timeout_ns;
 };
 // Expert layers without rings and barriers (moe_direct.cu), by the weights of the
-// experts that the tokens can name: up to 8 tokens fewer than 2^27 (bf16) or 2^26
-// (4-bit); more tokens fewer than 2^25 for 16 tokens, once per 16.  Direct and
-// through the rings, bf16 / 4-bit, us:
+// experts that the tokens can name, counted once per 16 tokens: up to 8 tokens
+// fewer than 2^27 (bf16) or 2^26 (4-bit), more tokens fewer than 2^25.  Many small
+// experts share those weights out to more CTAs with shorter sums, so the limit is
+// lower for them.  Direct and through the rings, bf16 / 4-bit, us:
 //   1 token, 2 of 8 experts of 256 x 128 (0.2M)       5.2 / 5.0     14.4 / 16.5
-//   1 token, 2 of 8 of 4096 x 2048 (48M)             23.9 / 15.9    30.6 / 20.2
-//   3 tokens, 6 of 32 of 2048 x 512 (54M)            24.3 / 18.4    29.4 / 20.3
+//   1 token, 2 of 8 of 4096 x 2048 (48M)             23.7 / 15.8    30.7 / 20.0
 //   1 token, 2 of 8 of 4096 x 4096 (96M)             39.9 / 27.1    43.9 / 24.9
-//   2 tokens, 2 of 8 of 4096 x 2048 (96M)            40.0 / 27.1    42.8 / 24.6
+//   2 tokens, 2 of 8 of 4096 x 2048 (96M)            36.1 / 26.9    34.7 / 24.5
+//   4 tokens, 2 of 8 of 4096 x 1024 (96M)            32.4 / 21.6    33.4 / 24.7
 //   1 token, 4 of 8 of 4096 x 4096 (192M)            74.6 / 47.2    71.0 / 34.5
-//   4 tokens, 4 of 32 of 4096 x 1024 (192M)          71.1 / 42.9    64.4 / 33.4
+// 16 experts and more, bf16, up to 8 tokens: 2^26
+//   2 tokens, 8 of 64 of 1024 x 512 (24M)            18.0 / 13.1    21.6 / 17.8
+//   4 tokens, 4 of 32 of 1024 x 1024 (48M)           28.0 / 18.0    26.7 / 19.6
+//   8 tokens, 4 of 32 of 1024 x 512 (48M)            26.6 / 17.7    24.8 / 19.5
+//   4 tokens, 4 of 32 of 2048 x 1024 (96M)           40.6 / 27.0    34.8 / 25.0
+//   8 tokens, 4 of 32 of 1024 x 1024 (96M)           39.0 / 29.2    32.6 / 24.9
+// 64 (4-bit: 128): half of that
+//   8 tokens, 8 of 64 of 512 x 256 (24M)             20.6 / 15.7    20.8 / 18.2
+//   8 tokens, 16 of 128 of 512 x 256 (48M)           35.2 / 27.6    25.8 / 21.2
+//   8 tokens, 8 of 64 of 1024 x 512 (96M)            41.4 / 29.7    34.3 / 25.6
+// more than 8 tokens: 2^25
 //   12 tokens, 2 of 8 of 512 x 256 (3M)               8.9 / 7.7     18.7 / 18.1
-//   32 tokens, 2 of 8 of 1024 x 512 (24M)            18.4 / 15.8    20.1 / 20.9
-//   20 tokens, 4 of 32 of 512 x 256 (24M)            20.7 / 15.8    18.0 / 18.3
-//   64 tokens, 2 of 8 of 1024 x 512 (48M)            28.4 / 24.3    23.6 / 22.5
+//   32 tokens, 2 of 8 of 1024 x 512 (24M)            18.8 / 15.8    20.0 / 20.4
+//   33 tokens, 2 of 16 of 512 x 256 (18M)            14.9 / 13.7    17.2 / 19.1
+//   32 tokens, 2 of 16 of 768 x 512 (36M)            26.3 / 23.7    20.9 / 18.4
+//   64 tokens, 2 of 8 of 1024 x 512 (48M)            28.6 / 24.2    23.0 / 21.9
+// more than 8 tokens, 64 (4-bit: 128) experts and more, counted once per 16 tokens: 2^24
+//   20 tokens, 8 of 64 of 256 x 128 (12M)            18.7 / 15.8    17.6 / 18.7
+//   64 tokens, 4 of 32 of 256 x 128 (12M)            16.5 / 16.7    17.8 / 20.3
+//   48 tokens, 8 of 64 of 256 x 128 (18M)            24.5 / 23.9    19.7 / 21.4
+//   20 tokens, 4 of 32 of 512 x 256 (24M)            22.0 / 16.2    17.9 / 18.1
+//   16 tokens, 8 of 64 of 512 x 256 (24M)            31.1 / 22.4    22.3 / 18.8
+//   64 tokens, 8 of 64 of 256 x 128 (24M)            27.2 / 28.9    21.1 / 22.2
 inline bool use_direct_moe(int T, int k, int E, int H, int I, int group)
 {
     const int most = T <= 8 ? 8 : 16, names = (T < most ? T : most) * k;
-    const long long weights = 3LL * ((T + most - 1) / most) * (names < E ? names : E) * H * I;
-    return weights < (T > 8 ? 1LL << 25 : group ? 1LL << 26 : 1LL << 27);
+    const int experts = (T + most - 1) / most * (names < E ? names : E);
+    const int log = (T > 8 ? 25 : group ? 26 : experts < 16 ? 27 : 26) - (experts >= (group ? 128 : 64) ? 1 : 0);
+    return 3LL * experts * H * I < 1LL << log;
 }
 cudaError_t prepare_moe_direct();
 cudaError_t launch_moe_direct(const MoeDirectParams& p, int group, bool zero, int sms, cudaStream_t stream, bool pdl);
