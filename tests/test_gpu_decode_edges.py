@@ -1,10 +1,10 @@
 """Decode-step operators at the edges of their kernels' variants, against plain 64-bit implementations.
 
 The tolerances are those of test_gpu_decode.py, error bounds and not fits, with one of their own: with 4-bit
-weights h, the activation between the two products, is fp16 times a power of two per 128 columns, which brings
-the largest of them to [2^14, 2^15).  Rounding to the nearest of 11 significant bits is 2^-11 of the value at
-most, and below 2^-14 half of a unit of 2^-24, which is 2^-39 of the largest.  With bf16 weights h is two bf16
-numbers, which leave 2^-16.
+weights h, the activation between the two products, is fp16 times a power of two per 128 columns (2^126 at most),
+which brings the largest of them to [2^14, 2^15).  Rounding to the nearest of 11 significant bits is 2^-11 of the
+value at most, and below 2^-14 half of a unit of 2^-24, which is 2^-39 of the largest, or 2^-151 where the power
+ends.  With bf16 weights h is two bf16 numbers, which leave 2^-16.
 """
 import pytest
 import torch
@@ -36,12 +36,12 @@ def moe_bound(x, topk, gate, W13, W2, quant):
         dh = 1.1 * dg * zu.abs() + (s.abs() + 1.1 * dg) * du + (8 * U32 + (2.0 ** -11 if quant else 2.0 ** -16)) * hh.abs()
         if quant:
             top = torch.cat([p.abs().amax(1, keepdim=True).expand_as(p) for p in hh.split(128, 1)], 1)
-            dh = dh + 2.0 ** -39 * top
+            dh = dh + 2.0 ** -39 * top + 2.0 ** -151
         w2, w = W2[e].to(D), gate[t, j].to(D)[:, None]
         mag = (hh.abs() + dh) @ w2.abs()
         out.index_add_(0, t, (hh @ w2) * w)
         bound.index_add_(0, t, w.abs() * (dh @ w2.abs() + sum_bound(2 * I, mag)))
-    return out, bound + U16 * out.abs()
+    return out, bound + U16 * out.abs() + 2.0 ** -133
 
 
 def experts(g, E, H, I, quant, zeros=True):
@@ -155,3 +155,208 @@ def test_quantize_takes_any_finite_weights(h, group, zeros):  # noqa: F811
     bound = s * ((1.0 if zeros else 0.5) + 2.0 ** -18) + (15 if zeros else 7) * (s - want.to(D)).abs()
     within(got, w.to(D), torch.where(none, (hi - lo).to(D), bound).repeat_interleave(group, 0), "quantised weights")
     assert (got.view(K // group, group, N)[none[:, None, :].expand(-1, group, -1)] == 0).all()
+
+
+# Tokens and layers (7 experts, 3 a token) of the two-kernel form and of the rings: their weights lie on both sides of the
+# rule's limits.  The products of 4-bit weights likewise, by their matrix.
+FORMS = [(20, 192, 128), (20, 2560, 1600)]
+E7, K3 = 7, 3
+PRODUCTS = [(512, 256), (8192, 8320)]
+
+
+def layer(h, g, T, H, I, quant):  # noqa: F811
+    topk, gate = routing(g, T, E7, K3)
+    return topk, gate, experts(g, E7, H, I, quant), space(h.moe_decode_workspace(T, K3, H, I))
+
+
+@pytest.mark.parametrize("T,H,I", FORMS)
+@pytest.mark.parametrize("quant", [None, 64])
+def test_moe_strided_rows_on_a_side_stream(h, T, H, I, quant):  # noqa: F811
+    """Rows of x apart, rows of out that allow only single elements; the same bits on every call and any stream."""
+    g = gen(H)
+    topk, gate, w, ws = layer(h, g, T, H, I, quant)
+    x = randn(g, T, H + 72)[:, 24:24 + H]
+    want, bound = moe_bound(x, topk, gate, *w, quant)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    first = None
+    for pad, stream in ((8, None), (1, None), (3, side), (8, side)):
+        out, intact = guarded(T, H, pad=pad)
+        torch.cuda.synchronize()
+        run_moe(h, x, topk, gate, w, quant, out, ws, stream=stream)
+        assert h.sync_status() == 0
+        within(out, want, bound, "out")
+        assert intact()
+        first = out.clone() if first is None else first
+        assert torch.equal(out, first)
+
+
+@pytest.mark.parametrize("T,H,I", FORMS)
+@pytest.mark.parametrize("quant", [None, 64])
+def test_moe_takes_any_magnitude_in_either_form(h, T, H, I, quant):  # noqa: F811
+    g = gen(H + 1)
+    topk, gate, w, ws = layer(h, g, T, H, I, quant)
+    size = torch.tensor([1e-18, 1e-6, 1.0, 1e3, 1e9, 1e15], device=DEV).repeat(4)[:T, None]
+    x = (torch.randn(T, H, generator=g, device=DEV) * size).to(BF16)
+    out = torch.empty(T, H, dtype=BF16, device=DEV)
+    run_moe(h, x, topk, gate, w, quant, out, ws)
+    assert h.sync_status() == 0
+    within(out, *moe_bound(x, topk, gate, *w, quant), "out")
+
+
+@pytest.mark.parametrize("T,H,I", FORMS + [(3, 192, 128)])
+@pytest.mark.parametrize("quant", [None, 64])
+@pytest.mark.parametrize("bad", [E7, -2, 2 ** 31 - 1, -2 ** 31])
+def test_moe_refuses_ids_outside(h, T, H, I, quant, bad):  # noqa: F811
+    """More and fewer than 32 names, in either form: nothing written, an error status, and the next call is right."""
+    g = gen(H + 2)
+    topk, gate, w, ws = layer(h, g, T, H, I, quant)
+    x, out = randn(g, T, H), torch.full((T, H), 5.0, dtype=BF16, device=DEV)
+    worse = topk.clone()
+    worse[T - 1, 1] = bad
+    run_moe(h, x, worse, gate, w, quant, out, ws)
+    assert h.sync_status() == tovl.TOVL_ERR_INVALID
+    assert (out == 5).all()
+    run_moe(h, x, topk, gate, w, quant, out, ws)
+    assert h.sync_status() == 0
+    within(out, *moe_bound(x, topk, gate, *w, quant), "out")
+
+
+# ------------------------------------------------------------------ 4-bit products
+def product(h, g, T, K, N, e4m3):  # noqa: F811
+    """Rows, their scales, a packed matrix, a workspace."""
+    x, xs = randn(g, T, K), None
+    if e4m3:
+        x = (torch.randn(T, K, generator=g, device=DEV) * 100).clamp_(-448, 448).to(E4M3)
+        xs = (torch.rand(T, -(-K // 128), generator=g, device=DEV) + 0.5) * 0.01
+    return x, xs, packed(g, (), K, N, 64, True), space(h.matvec_q4_workspace(T, N))
+
+
+def product_bound(x, xs, w):
+    W, xd = unpack(*w, 64), x.float().to(D)
+    if xs is not None:
+        xd = xd * xs.to(D).repeat_interleave(128, 1)[:, :x.shape[1]]
+    want = xd @ W
+    return want, U16 * want.abs() + 2.0 ** -133 + sum_bound(x.shape[1] + x.shape[1] / 64 * 16, xd.abs() @ W.abs())
+
+
+@pytest.mark.parametrize("K,N", PRODUCTS)
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_matvec_strided_rows_on_a_side_stream(h, K, N, e4m3):  # noqa: F811
+    g = gen(K + 3)
+    T = 18
+    x, xs, w, ws = product(h, g, T, K, N, e4m3)
+    x = torch.cat([x, x[:, :96]], 1)[:, :K]              # rows K + 96 apart
+    want, bound = product_bound(x, xs, w)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    first = None
+    for pad, stream in ((8, None), (1, None), (3, side), (8, side)):
+        out, intact = guarded(T, N, pad=pad)
+        torch.cuda.synchronize()
+        h.matvec_q4(x, w[0], w[1], 64, out, ws, zero=w[2], x_scale=xs, stream=stream)
+        assert h.sync_status() == 0
+        within(out, want, bound, "out")
+        assert intact()
+        first = out.clone() if first is None else first
+        assert torch.equal(out, first)
+
+
+# ------------------------------------------------------------------ together
+class Jobs:
+    """Layers and products of both forms and both weight types, on one workspace and one handle."""
+
+    def __init__(self, h, g, rows):  # noqa: F811
+        self.h, self.calls = h, []
+        sizes = []
+        for (_, H, I), T, quant in [(f, T, q) for f in FORMS for T in rows for q in (None, 64)]:
+            topk, gate, w, ws = layer(h, g, T, H, I, quant)
+            self.calls.append(("moe", randn(g, T, H), topk, gate, w, quant, torch.empty(T, H, dtype=BF16, device=DEV)))
+            sizes.append(len(ws))
+        for (K, N), T, e4m3 in [(p, T, e) for p in PRODUCTS for T in rows for e in (False, True)]:
+            x, xs, w, ws = product(h, g, T, K, N, e4m3)
+            self.calls.append(("product", x, xs, w, torch.empty(T, N, dtype=BF16, device=DEV)))
+            sizes.append(len(ws))
+        self.ws = space(max(sizes))
+        order = torch.randperm(len(self.calls), generator=torch.Generator().manual_seed(3)).tolist()
+        self.calls = [self.calls[i] for i in order]
+
+    def run(self):
+        for kind, *c in self.calls:
+            if kind == "moe":
+                x, topk, gate, w, quant, out = c
+                run_moe(self.h, x, topk, gate, w, quant, out, self.ws)
+            else:
+                x, xs, w, out = c
+                self.h.matvec_q4(x, w[0], w[1], 64, out, self.ws, zero=w[2], x_scale=xs)
+
+    def new_rows(self, g):
+        for kind, x, *c in self.calls:
+            x.copy_(randn(g, *x.shape) if x.dtype is BF16 else randn(g, *x.shape, scale=100, dtype=F32).clamp_(-448, 448))
+            if kind == "moe":
+                c[0].copy_(routing(g, len(x), E7, K3)[0])
+
+    def check(self):
+        assert self.h.sync_status() == 0
+        for kind, *c in self.calls:
+            want, bound = moe_bound(*c[:3], *c[3], c[4]) if kind == "moe" else product_bound(*c[:3])
+            within(c[-1], want, bound, kind)
+
+    def outputs(self):
+        return [c[-1] for c in self.calls]
+
+
+def test_back_to_back_calls_of_both_forms(h):  # noqa: F811
+    """Calls in a row without a synchronisation share the handle's counters and a workspace; the same bits every time."""
+    jobs = Jobs(h, gen(71), (9, 24))
+    jobs.run()
+    jobs.check()
+    first = [o.clone() for o in jobs.outputs()]
+    for _ in range(5):
+        for o in jobs.outputs():
+            o.zero_()
+        for _ in range(2):
+            jobs.run()
+        assert h.sync_status() == 0
+        assert all(torch.equal(o, f) for o, f in zip(jobs.outputs(), first))
+
+
+@pytest.mark.parametrize("option,value", [(None, None), (tovl.OPT_COOPERATIVE, 0), (tovl.OPT_PDL, 0)])
+def test_a_decode_step_in_a_graph(option, value):
+    """Norm, router, layers and products of both forms captured once and replayed on new inputs, also without the cooperative
+    attribute and without programmatic launches."""
+    g = gen(72)
+    with tovl.Handle(0, max_rows=4096, max_pairs=4096) as h:  # noqa: F811
+        if option is not None:
+            h.set_option(option, value)
+        jobs = Jobs(h, g, (12,))
+        T, H, E, k = 12, 1280, 32, 4
+        x, res, weight = randn(g, T, H), randn(g, T, H, dtype=F32), randn(g, H, scale=0.1) + 1
+        ro, y = torch.empty_like(res), torch.empty_like(x)
+        logits, topk, gate = randn(g, T, E, dtype=F32), torch.empty(T, k, dtype=torch.int32, device=DEV), torch.empty(T, k, device=DEV)
+
+        def step():
+            h.add_rmsnorm(x, weight, 1e-5, residual=res, residual_out=ro, out=y)
+            h.route_topk(logits, topk, gate)
+            jobs.run()
+
+        step()
+        assert h.sync_status() == 0
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        for seed in (1, 2):
+            g = gen(seed)
+            x.copy_(randn(g, T, H)), res.copy_(randn(g, T, H, dtype=F32)), logits.copy_(randn(g, T, E, dtype=F32))
+            jobs.new_rows(g)
+            graph.replay()
+            torch.cuda.synchronize()
+            jobs.check()
+            r = x.to(D) + res.to(D)
+            want = r / torch.sqrt((r * r).mean(1, keepdim=True) + 1e-5) * weight.to(D)
+            within(y, want, (U16 + (H + 24) * U32) * want.abs(), "norm")
+            p, ids = torch.softmax(logits.to(D), 1).topk(k)
+            assert torch.equal(topk.long(), ids)
+            p = p / p.sum(1, keepdim=True)
+            # exp (2 units and the rounded difference of arguments below 20), a sum of four, one division
+            within(gate, p, 32 * U32 * p, "gate_w")
