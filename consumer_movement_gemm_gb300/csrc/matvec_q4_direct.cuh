@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kDirectWarps * 32, 1) matvec_q4_direct_kernel(
     const int warps = blockDim.x >> 5, split = gridDim.y, rank = blockIdx.y;      // the cluster: CTAs (1, split, 1)
     const int r0 = blockIdx.z * 16, cnt = min(16, p.T - r0);
     const int n = blockIdx.x * kDirectCols + 4 * column_group(g);
-    const bool col = n < p.N;                 // (N is a multiple of 16: four columns are in or out together)
+    const bool col = n < p.N;                 // (N is a multiple of 8: four columns are in or out together)
     const int blocks = (p.K + 127) / 128, stride = warps * split;
     if (split > 1) ptx::cluster_arrive_relaxed();
     ptx::grid_dep_wait();

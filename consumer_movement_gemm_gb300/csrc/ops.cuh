@@ -24,8 +24,6 @@ constexpr int kExitWord = 5 * kSyncStep;
 constexpr int kPartWord = 6 * kSyncStep;                 // arrivals at a cut tile, by its first item (matvec_q4)
 constexpr int kSyncWords = kPartWord + kMaxGrid * 8;
 
-enum : int { kTypeBf16 = 0, kTypeF32 = 1, kTypeE4m3 = 2 };
-
 struct NormParams {
     const void* x;          // bf16 [T][H], rows ldx elements apart
     const void* residual;   // bf16 or fp32 [T][H], rows ldr apart; null = none

@@ -276,8 +276,10 @@ __device__ __forceinline__ uint2 e4m3x4_to_half(uint32_t v)
 
 // The power of two that brings numbers of largest exponent field e (bf16, 0
 // to 255) below 2^15, and its inverse.  In fp16 so scaled, a bf16 number keeps
-// all its bits down to 2^-32 of the largest, and what a smaller one loses is
-// 2^-40 of the largest: nothing beside the fp32 sums' own 2^-24.
+// all its bits down to 2^-31 of the largest, and what a smaller one loses is
+// 2^-39 of the largest: nothing beside the fp32 sums' own 2^-24.  (The power ends at
+// 2^126.  Where the largest is below 2^-112 / scale, the inverse times a weight's
+// scale is a subnormal number, and a group's sum loses 2^-124 at most.)
 __device__ __forceinline__ float half_scale(uint32_t e) { return __uint_as_float(min(268u - e, 253u) << 23); }
 __device__ __forceinline__ float half_unscale(uint32_t e) { return __uint_as_float((254u - min(268u - e, 253u)) << 23); }
 

@@ -126,7 +126,8 @@ long long tovl_dispatch_rows_aligned(int T, int k, int E, int align);
  * followed by a grouped GEMM per expert (notify-stage counting of the DeepEP
  * FIFO-pipeline page; row-block counters with padding seeds of section 5).
  *   x           device, bf16 [T][H] (may be null when T = 0)
- *   topk_idx    device, int32 [T][k]: expert of pair (t, j), each in [0, E)
+ *   topk_idx    device, int32 [T][k]: expert of pair (t, j), each in [0, E);
+ *               not the -1 that tovl_route_topk leaves in a masked slot
  *               (may be null when T = 0: a round without tokens, whose plan
  *               is empty and whose call still counts as one round)
  *   H           multiple of 64, at most 32768 (the GEMM K)
@@ -238,10 +239,12 @@ int tovl_dispatch_plan_noalloc(const int* topk_idx, int T, int k, int E, int* ex
 /* ---------------------------------------------------------------- decode step
  * Operators of a serving step around the experts, for few tokens as well as
  * many: the norm before the layer, the router, the whole expert layer for up
- * to 64 tokens (longer batches take tovl_dispatch_grouped_gemm and
- * tovl_combine), and products with 4-bit weights.  None of them is a protocol
- * round: the sequence number stays.  T = 0 is accepted everywhere, does
- * nothing and reads no tensor.
+ * to 64 tokens, and products of up to 64 rows with 4-bit weights.  Longer
+ * batches have no gated layer here: tovl_dispatch_grouped_gemm multiplies
+ * scattered rows by one bf16 matrix per expert and tovl_combine adds its rows
+ * up, with no activation between and no slots without an expert.  None of the
+ * calls below is a protocol round: the sequence number stays.  T = 0 is
+ * accepted everywhere, does nothing and reads no tensor.
  *
  * Packed 4-bit weights of a matrix W [K][N] (N contiguous): 32-bit words
  * [K/8][N]; the word of (r, n) holds rows 8r .. 8r+7 of column n, row 8r+2i in
@@ -295,7 +298,8 @@ int tovl_add_rmsnorm(tovl_handle h, const void* x, long long ldx, const void* re
  * An expert whose logit is -inf or NaN is masked: never chosen, weight 0.
  * Slots that no expert is left for hold -1 with weight 0 (a token whose
  * logits are all masked has nothing but those); +inf counts as the largest
- * finite logit does. */
+ * finite logit does.  tovl_moe_decode takes the -1; tovl_dispatch_grouped_gemm
+ * does not: routing for it needs k experts that are not masked per token. */
 int tovl_route_topk(tovl_handle h, const void* logits, int type, long long ld, int T, int E, int k, int renormalize,
                     int* topk_idx, float* gate_w, void* stream);
 
@@ -306,7 +310,10 @@ long long tovl_moe_decode_workspace(tovl_handle h, int T, int k, int H, int I);
 /* The gated expert layer for a few tokens:
  *   h(t, e) = silu(x[t] W13[e][:, 0:I]) * (x[t] W13[e][:, I:2I]),
  *   out[t]  = sum over j of gate_w[t][j] * (h(t, e) W2[e]), e = topk_idx[t][j]
- * with fp32 sums, rounded once to bf16.
+ * with fp32 sums, rounded once to bf16.  Between the two products h is kept as
+ * two bf16 numbers, which leave 2^-16 of it (an h over bf16's largest number
+ * is infinite).  Weights are finite; a sum with an infinite one may be
+ * infinite or NaN.
  *   x           device, bf16 [T][H], rows ldx elements apart (a multiple of 8),
  *               16-byte aligned; T 0 .. 64, H a multiple of 8 up to 32768
  *   topk_idx    device, int32 [T][k]: experts, or -1 for a slot without one
@@ -331,7 +338,9 @@ int tovl_moe_decode(tovl_handle h, const void* x, long long ldx, int T, int H, c
 
 /* The same layer with packed 4-bit experts: W13 [E] matrices [H][2I], W2 [E]
  * matrices [I][H], with zeros for both or for neither; H and I multiples of
- * group.  Scales are applied to fp32 sums. */
+ * group.  Scales are applied to fp32 sums.  h is rounded to fp16 times a power
+ * of two per 128 columns of I: 2^-11 of it at most, and below 2^-28 of the
+ * largest of the 128 an absolute 2^-39 of that. */
 int tovl_moe_decode_q4(tovl_handle h, const void* x, long long ldx, int T, int H, const int* topk_idx,
                        const float* gate_w, int k, int E, const void* W13_q, const void* W13_scale,
                        const void* W13_zero, const void* W2_q, const void* W2_scale, const void* W2_zero, int group,
