@@ -63,7 +63,8 @@ struct Scale {
     __device__ __forceinline__ explicit Scale(float2 of) : s(of.x), inverse(of.y) {}
     __device__ __forceinline__ float divide(float y) const
     {
-        // (an infinite scale: no residual, the quotients are 0, or NaN of an infinity)
+        // (an infinite scale: no residual, the quotients are 0, or NaN of an infinity; -0
+        // gives +0)
         const float q = y * inverse;
         return fmaf(fmaf(-q, s == INFINITY ? 0.f : s, y), inverse, q);
     }
