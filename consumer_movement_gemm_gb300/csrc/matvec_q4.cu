@@ -268,7 +268,7 @@ cudaError_t launch_quantize_q4(const QuantParams& p, cudaStream_t stream)
     const long long eg = static_cast<long long>(p.K / p.group) * p.E;
     const unsigned y = eg < 32768 ? static_cast<unsigned>(eg) : 32768u;
     const unsigned z = static_cast<unsigned>((eg + y - 1) / y);
-    quantize_q4_kernel<<<dim3((p.N + 255) / 256, y, z), 256, 0, stream>>>(p);
+    quantize_q4_kernel<<<dim3((p.N - 1) / 256 + 1, y, z), 256, 0, stream>>>(p);
     return cudaGetLastError();
 }
 

@@ -630,7 +630,7 @@ cudaError_t launch_rows(const NormParams& p, cudaLaunchConfig_t lc, int num_sms)
         const int threads = static_cast<int>(lc.blockDim.x);
         const int per_sm = WARP ? (VPT == 1 ? 3 : VPT == 2 ? 2 : 1) : (VPT <= 2 ? 1024 : 512) / threads;
         const int most = num_sms * per_sm, rows = WARP ? kWarpRows : 1;
-        const int want = (p.T + rows - 1) / rows;
+        const int want = (p.T - 1) / rows + 1;
         lc.gridDim = dim3(want < most ? want : most);
         return cudaLaunchKernelEx(&lc, kernel, p);
     });
@@ -655,7 +655,7 @@ int up32(int n) { return (n + 31) / 32 * 32; }
 template <int VPT, bool WARP>
 cudaError_t launch_offset(const NormParams& p, cudaLaunchConfig_t lc, int pieces)
 {
-    lc.gridDim = dim3(WARP ? (p.T + kWarpRows - 1) / kWarpRows : p.T);
+    lc.gridDim = dim3(WARP ? (p.T - 1) / kWarpRows + 1 : p.T);
     lc.blockDim = dim3(WARP ? kWarpRows * 32 : up32((pieces + VPT - 1) / VPT));
     return by_residual(p, [&](auto res) { return cudaLaunchKernelEx(&lc, norm_offset_kernel<VPT, decltype(res)::value, WARP>, p); });
 }
@@ -702,7 +702,7 @@ cudaError_t launch_norm(const NormParams& p, int width, bool same_offset, int nu
     }
     int vpt = warp_row ? (vecs + 31) / 32 : (vecs + 1023) / 1024;
     if (vpt == 3) vpt = 4;
-    lc.gridDim = dim3(warp_row ? (p.T + kWarpRows - 1) / kWarpRows : p.T);
+    lc.gridDim = dim3(warp_row ? (p.T - 1) / kWarpRows + 1 : p.T);
     lc.blockDim = dim3(warp_row ? kWarpRows * 32 : up32((vecs + vpt - 1) / vpt));
     return width == 2 ? launch_any<2>(p, lc, warp_row, vpt) : launch_any<1>(p, lc, warp_row, vpt);
 }

@@ -252,7 +252,7 @@ cudaError_t launch(const RouteParams& p, cudaStream_t stream, bool pdl)
     cudaLaunchConfig_t lc = {};
     // (32 tokens a warp with more than 16 slots each would take over 48 KB)
     const int warps = p.k > 16 ? kWarps / 2 : kWarps;
-    lc.gridDim = dim3((p.T + warps * kAll - 1) / (warps * kAll));
+    lc.gridDim = dim3((p.T - 1) / (warps * kAll) + 1);
     lc.blockDim = dim3(warps * 32);
     lc.dynamicSmemBytes = warps * kAll * (3 * p.k + 1) * 4;
     lc.stream = stream;

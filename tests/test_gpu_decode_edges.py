@@ -360,3 +360,25 @@ def test_a_decode_step_in_a_graph(option, value):
             p = p / p.sum(1, keepdim=True)
             # exp (2 units and the rounded difference of arguments below 20), a sum of four, one division
             within(gate, p, 32 * U32 * p, "gate_w")
+
+
+# ------------------------------------------------------------------ sizes at the end of int
+def test_route_and_norm_of_as_many_rows_as_there_can_be(h):  # noqa: F811
+    """2^31 - 1 rows: neither the grid's size nor an offset wraps."""
+    T = 2 ** 31 - 1
+    logits = torch.zeros(T, 1, dtype=BF16, device=DEV)
+    topk, gate = torch.full((T, 1), 7, dtype=torch.int32, device=DEV), torch.zeros(T, 1, device=DEV)
+    h.route_topk(logits, topk, gate)
+    assert h.sync_status() == 0
+    assert int(topk.max()) == 0 and int(topk.min()) == 0 and float(gate.min()) == 1 and float(gate.max()) == 1
+    del topk, gate
+    x, out, weight = logits.fill_(2), torch.empty(T, 1, dtype=BF16, device=DEV), torch.full((1,), 3, dtype=BF16, device=DEV)
+    h.add_rmsnorm(x, weight, 0.0, out=out)                # contiguous rows: pieces
+    assert h.sync_status() == 0
+    assert float(out.min()) == 3 and float(out.max()) == 3
+    out.zero_()
+    h.add_rmsnorm(x, torch.full((2,), 3, dtype=BF16, device=DEV)[1:], 0.0, out=out)       # a weight off the boundary: elements
+    assert h.sync_status() == 0
+    assert float(out.min()) == 3 and float(out.max()) == 3
+    del x, out, logits
+    torch.cuda.empty_cache()
