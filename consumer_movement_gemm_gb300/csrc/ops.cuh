@@ -22,7 +22,9 @@ constexpr int kTicketWord = 0;         // tickets of product i at word i * kTick
 constexpr int kBarrierWord = 2 * kSyncStep;
 constexpr int kExitWord = 5 * kSyncStep;
 constexpr int kPartWord = 6 * kSyncStep;                 // arrivals at a cut tile, by its first item (matvec_q4)
-constexpr int kSyncWords = kPartWord + kMaxGrid * 8;
+constexpr int kAttnWord = kPartWord + kMaxGrid * 8;      // arrivals at a shared segment, by its first CTA (attn_decode)
+constexpr int kPagePlanWord = kAttnWord + kMaxGrid;      // CTAs past their reads (page_plan)
+constexpr int kSyncWords = kPagePlanWord + kSyncStep;
 
 struct NormParams {
     const void* x;          // bf16 [T][H], rows ldx elements apart

@@ -7,27 +7,6 @@
 
 namespace {
 
-bool aligned(const void* p, unsigned n)
-{
-    return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
-}
-
-// Launch with programmatic dependent launch if the device takes it.
-template <class F>
-int run(tovl_ctx* h, cudaStream_t s, const char* what, F launch)
-{
-    const bool pdl = h->pdl && h->pdl_ok;
-    cudaError_t e = launch(pdl);
-    if (e != cudaSuccess && pdl) {
-        cudaGetLastError();
-        e = launch(false);
-        if (e == cudaSuccess) h->pdl_ok = false;
-    }
-    if (e != cudaSuccess) return cuda_fail(h, e, what);
-    h->last_stream = s;
-    return TOVL_OK;
-}
-
 // A map of stacked [rows][width] matrices; boxes of box_inner columns x
 // box_rows rows, out-of-range elements read as zero.
 int encode_3d(tovl_ctx* h, CUtensorMap* map, CUtensorMapDataType type, int elem, const void* base, uint64_t width,

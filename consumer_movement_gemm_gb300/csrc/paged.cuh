@@ -1,0 +1,77 @@
+// paged.cuh -- parameter blocks and launchers of the paged attention step:
+// pages for new tokens, rotary embedding with the cache writes, attention of
+// one new token per request.
+#pragma once
+#include <cuda_runtime.h>
+#include "ctrl.cuh"
+#include "ops.cuh"
+
+namespace tovl {
+
+constexpr int kMaxRequests = 4096;     // of one page_plan call
+constexpr int kMaxHeadDim = 256;
+
+// tovl_kv_cache with strides in bytes.
+struct KvCache {
+    uint8_t* k;
+    uint8_t* v;
+    float* k_scale;         // [pages][heads][page]; e4m3 only
+    float* v_scale;
+    long long page_stride, slot_stride, head_stride;
+    int pages, page, heads, dim;
+    int page_shift;         // log2(page), or -1
+};
+
+struct PagePlanParams {
+    const int* length;      // [B]
+    const int* add;         // [B]
+    int* table;             // [B][width], rows ldt apart
+    int* ring;              // [pages]
+    const int* state;       // [4]
+    int* length_out;
+    int* state_out;
+    int* slots;             // [cap]
+    int* positions;         // [cap]
+    int* starts;            // [B + 1]
+    long long ldt;
+    int B, width, pages, page, cap;
+    int* counter;           // handle-owned, zero between calls
+    Ctrl ctrl;
+};
+cudaError_t prepare_page_plan();
+cudaError_t launch_page_plan(const PagePlanParams& p, int num_sms, cudaStream_t stream, bool pdl);
+
+struct RopeParams {
+    const void* q;          // bf16 [T][Hq][D], rows ldq elements apart
+    const void* k;          // bf16 [T][heads][D]
+    const void* v;
+    void* q_out;
+    const int* positions;   // [T]
+    const int* slots;       // [T]
+    const float* cos_sin;   // [max_pos][rot]
+    long long ldq, ldk, ldv, ldqo;
+    int T, Hq, rot, max_pos, interleaved;
+    KvCache cache;
+    Ctrl ctrl;
+};
+cudaError_t launch_rope_append(const RopeParams& p, bool e4m3, int num_sms, cudaStream_t stream, bool pdl);
+
+struct AttnParams {
+    const void* q;          // bf16 [B][Hq][D], rows ldq elements apart
+    void* out;              // rows ldo apart
+    float* lse;             // [B][Hq]; null = not wanted
+    const int* table;       // [B][width], rows ldt apart
+    const int* length;      // [B]
+    long long ldq, ldo, ldt;
+    int B, Hq, group, width, window;
+    float scale_log2;       // scale * log2(e)
+    KvCache cache;
+    float* part;            // workspace
+    int* counter;           // [kMaxGrid], handle-owned, zero between calls
+    Ctrl ctrl;
+};
+long long attn_decode_workspace(int group, int dim, int num_sms);
+cudaError_t prepare_attn_decode();
+cudaError_t launch_attn_decode(const AttnParams& p, bool e4m3, int num_sms, cudaStream_t stream, bool pdl);
+
+}  // namespace tovl

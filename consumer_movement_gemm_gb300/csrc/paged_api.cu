@@ -1,0 +1,176 @@
+// paged_api.cu -- host side of the paged attention step declared in
+// include/tovl.h: argument checks and launches.  None of the calls is a
+// protocol round (the handle's sequence number stays).
+#include <climits>
+#include "ctx.cuh"
+#include "paged.cuh"
+
+namespace {
+
+constexpr int kMaxQueryHeads = 4096;
+constexpr int kMaxDecodeBatch = 65536;
+
+// The cache as the kernels take it.
+int check_cache(const tovl_kv_cache* c, KvCache* out)
+{
+    if (!c || (c->type != TOVL_BF16 && c->type != TOVL_E4M3) || c->pages < 1 || c->page < 1 || c->heads < 1 || c->dim < 1)
+        return TOVL_ERR_INVALID;
+    const int size = c->type == TOVL_BF16 ? 2 : 1;
+    if (c->dim > kMaxHeadDim || c->dim * size % 16 || c->heads > kMaxQueryHeads ||
+        static_cast<long long>(c->pages) * c->page > INT_MAX)
+        return TOVL_ERR_UNSUPPORTED;
+    if (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v)) return TOVL_ERR_INVALID;
+    if (size == 1 && (!c->k_scale || !c->v_scale || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))) return TOVL_ERR_INVALID;
+    const long long strides[3] = {c->page_stride, c->slot_stride, c->head_stride};
+    const int extents[3] = {c->pages, c->page, c->heads};
+    for (int i = 0; i < 3; ++i)
+        if (extents[i] > 1 && (strides[i] < c->dim || strides[i] * size % 16)) return TOVL_ERR_INVALID;
+    out->k = static_cast<uint8_t*>(c->k);
+    out->v = static_cast<uint8_t*>(c->v);
+    out->k_scale = c->k_scale;
+    out->v_scale = c->v_scale;
+    out->page_stride = c->pages > 1 ? c->page_stride * size : 0;
+    out->slot_stride = c->page > 1 ? c->slot_stride * size : 0;
+    out->head_stride = c->heads > 1 ? c->head_stride * size : 0;
+    out->pages = c->pages;
+    out->page = c->page;
+    out->heads = c->heads;
+    out->dim = c->dim;
+    out->page_shift = -1;
+    for (int s = 0; s < 31; ++s)
+        if (c->page == 1 << s) out->page_shift = s;
+    return TOVL_OK;
+}
+
+// Rows of whole 16-byte pieces.
+bool valid_rows(const void* p, long long ld, long long width)
+{
+    return p && aligned16(p) && ld >= width && ld % 8 == 0;
+}
+
+}  // namespace
+
+TOVL_API int tovl_page_plan(tovl_handle h, const int* length, const int* add, int B, int* table, long long ldt, int width,
+                            int* ring, int pages, int page, const int* state, int* length_out, int* state_out, int* slots,
+                            int* positions, int cap, int* starts, void* stream)
+{
+    if (!h) return TOVL_ERR_INVALID;
+    if (B < 0 || width < 1 || pages < 1 || page < 1 || cap < 0) return TOVL_ERR_INVALID;
+    if (B > kMaxRequests || static_cast<long long>(pages) * page > INT_MAX) return TOVL_ERR_UNSUPPORTED;
+    if (B == 0) return TOVL_OK;
+    if (!length || !add || !table || !ring || !state || !length_out || !state_out || !starts || (cap && (!slots || !positions)) ||
+        ldt < width)
+        return TOVL_ERR_INVALID;
+    const void* all[] = {length, add, table, ring, state, length_out, state_out, slots, positions, starts};
+    for (const void* p : all)
+        if (!aligned(p, 4)) return TOVL_ERR_INVALID;
+    PagePlanParams p = {};
+    p.length = length;
+    p.add = add;
+    p.table = table;
+    p.ring = ring;
+    p.state = state;
+    p.length_out = length_out;
+    p.state_out = state_out;
+    p.slots = slots;
+    p.positions = positions;
+    p.starts = starts;
+    p.ldt = ldt;
+    p.B = B;
+    p.width = width;
+    p.pages = pages;
+    p.page = page;
+    p.cap = cap;
+    p.counter = h->sync_words + kPagePlanWord;
+    p.ctrl = h->ctrl;
+    DeviceGuard g(h->device);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return run(h, s, "page plan launch", [&](bool pdl) { return launch_page_plan(p, h->num_sms, s, pdl); });
+}
+
+TOVL_API int tovl_rope_append(tovl_handle h, const void* q, long long ldq, const void* k, long long ldk, const void* v,
+                              long long ldv, const int* positions, const int* slots, const float* cos_sin, int max_pos,
+                              int rot, int interleaved, int T, int Hq, const tovl_kv_cache* cache, void* q_out,
+                              long long ldqo, void* stream)
+{
+    if (!h) return TOVL_ERR_INVALID;
+    RopeParams p = {};
+    const int rc = check_cache(cache, &p.cache);
+    if (rc != TOVL_OK) return rc;
+    const int D = p.cache.dim;
+    if (T < 0 || Hq < 1 || rot < 0 || rot > D || (rot && (!cos_sin || max_pos < 1))) return TOVL_ERR_INVALID;
+    if (rot % 16 || Hq > kMaxQueryHeads ||
+        static_cast<long long>(T) * (Hq + 2LL * p.cache.heads) > static_cast<long long>(INT_MAX) * 16)
+        return TOVL_ERR_UNSUPPORTED;
+    if (T == 0) return TOVL_OK;
+    if (!positions || !slots || !aligned(positions, 4) || !aligned(slots, 4) || !aligned16(cos_sin)) return TOVL_ERR_INVALID;
+    const long long wide_q = static_cast<long long>(Hq) * D, wide_k = static_cast<long long>(p.cache.heads) * D;
+    if (!valid_rows(q, ldq, wide_q) || !valid_rows(k, ldk, wide_k) || !valid_rows(v, ldv, wide_k) || !valid_rows(q_out, ldqo, wide_q))
+        return TOVL_ERR_INVALID;
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.q_out = q_out;
+    p.positions = positions;
+    p.slots = slots;
+    p.cos_sin = cos_sin;
+    p.ldq = ldq;
+    p.ldk = ldk;
+    p.ldv = ldv;
+    p.ldqo = ldqo;
+    p.T = T;
+    p.Hq = Hq;
+    p.rot = rot;
+    p.max_pos = max_pos;
+    p.interleaved = interleaved != 0;
+    p.ctrl = h->ctrl;
+    DeviceGuard g(h->device);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return run(h, s, "rotary embedding launch",
+               [&](bool pdl) { return launch_rope_append(p, cache->type == TOVL_E4M3, h->num_sms, s, pdl); });
+}
+
+TOVL_API long long tovl_attn_decode_workspace(tovl_handle h, int Hq, int heads, int dim)
+{
+    if (!h || heads < 1 || Hq < 1 || Hq % heads || Hq > kMaxQueryHeads || dim < 1 || dim > kMaxHeadDim || dim % 8) return -1;
+    return attn_decode_workspace(Hq / heads, dim, h->num_sms);
+}
+
+TOVL_API int tovl_attn_decode(tovl_handle h, const void* q, long long ldq, int B, int Hq, const tovl_kv_cache* cache,
+                              const int* table, long long ldt, int width, const int* length, float scale, int window,
+                              void* out, long long ldo, float* lse, void* workspace, long long workspace_bytes, void* stream)
+{
+    if (!h) return TOVL_ERR_INVALID;
+    AttnParams p = {};
+    const int rc = check_cache(cache, &p.cache);
+    if (rc != TOVL_OK) return rc;
+    if (B < 0 || Hq < 1 || Hq % p.cache.heads || width < 1 || window < 0) return TOVL_ERR_INVALID;
+    if (Hq > kMaxQueryHeads || B > kMaxDecodeBatch || h->num_sms > kMaxGrid) return TOVL_ERR_UNSUPPORTED;
+    if (B == 0) return TOVL_OK;
+    const long long wide = static_cast<long long>(Hq) * p.cache.dim;
+    if (!valid_rows(q, ldq, wide) || !valid_rows(out, ldo, wide) || !table || !length || ldt < width || !aligned(table, 4) ||
+        !aligned(length, 4) || !aligned(lse, 4) || !workspace || !aligned(workspace, 256) ||
+        workspace_bytes < tovl_attn_decode_workspace(h, Hq, p.cache.heads, p.cache.dim))
+        return TOVL_ERR_INVALID;
+    p.q = q;
+    p.out = out;
+    p.lse = lse;
+    p.table = table;
+    p.length = length;
+    p.ldq = ldq;
+    p.ldo = ldo;
+    p.ldt = ldt;
+    p.B = B;
+    p.Hq = Hq;
+    p.group = Hq / p.cache.heads;
+    p.width = width;
+    p.window = window;
+    p.scale_log2 = scale * 1.44269504088896340736f;
+    p.part = static_cast<float*>(workspace);
+    p.counter = h->sync_words + kAttnWord;
+    p.ctrl = h->ctrl;
+    DeviceGuard g(h->device);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return run(h, s, "attention launch",
+               [&](bool pdl) { return launch_attn_decode(p, cache->type == TOVL_E4M3, h->num_sms, s, pdl); });
+}

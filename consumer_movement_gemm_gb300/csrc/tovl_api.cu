@@ -15,6 +15,7 @@
 #include "ctx.cuh"
 #include "launch.cuh"
 #include "ops.cuh"
+#include "paged.cuh"
 
 TOVL_API void tovl_default_config(tovl_config* cfg, int device)
 {
@@ -171,6 +172,8 @@ TOVL_API int tovl_create(tovl_handle* out, const tovl_config* cfg_in)
         if ((e = prepare_moe_direct()) != cudaSuccess) { rc = cuda_fail(h, e, "prepare moe direct"); break; }
         if ((e = prepare_moe_decode()) != cudaSuccess) { rc = cuda_fail(h, e, "prepare moe decode"); break; }
         if ((e = prepare_matvec_q4()) != cudaSuccess) { rc = cuda_fail(h, e, "prepare matvec"); break; }
+        if ((e = prepare_page_plan()) != cudaSuccess) { rc = cuda_fail(h, e, "prepare page plan"); break; }
+        if ((e = prepare_attn_decode()) != cudaSuccess) { rc = cuda_fail(h, e, "prepare attention"); break; }
         if (fused_max_active_per_sm() < 1) { rc = TOVL_ERR_UNSUPPORTED; break; }
         h->max_pairs = fused_max_active_pairs();
 

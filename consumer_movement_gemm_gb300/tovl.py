@@ -77,6 +77,23 @@ class tovl_config(ctypes.Structure):
     ]
 
 
+class tovl_kv_cache(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("type", ctypes.c_int),
+        ("pages", ctypes.c_int),
+        ("page", ctypes.c_int),
+        ("heads", ctypes.c_int),
+        ("dim", ctypes.c_int),
+        ("page_stride", ctypes.c_longlong),
+        ("slot_stride", ctypes.c_longlong),
+        ("head_stride", ctypes.c_longlong),
+    ]
+
+
 # every exported symbol of include/tovl.h with its ctypes signature
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -104,6 +121,10 @@ SIGNATURES = {
     "tovl_matvec_q4_workspace": ([_P, _I, _I], _LL),
     "tovl_matvec_q4": ([_P, _P, _I, _P, _LL, _I, _I, _P, _P, _P, _I, _I, _P, _LL, _P, _LL, _P], _I),
     "tovl_quantize_q4": ([_P, _P, _I, _I, _I, _I, _P, _P, _P, _P], _I),
+    "tovl_page_plan": ([_P, _P, _P, _I, _P, _LL, _I, _P, _I, _I, _P, _P, _P, _P, _P, _I, _P, _P], _I),
+    "tovl_rope_append": ([_P, _P, _LL, _P, _LL, _P, _LL, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _LL, _P], _I),
+    "tovl_attn_decode_workspace": ([_P, _I, _I, _I], _LL),
+    "tovl_attn_decode": ([_P, _P, _LL, _I, _I, _P, _P, _LL, _I, _P, _F, _I, _P, _LL, _P, _P, _LL, _P], _I),
     "tovl_gemm_only": ([_P, _P, _I, _I, _P, _I, _P, _P], _I),
     "tovl_copy_only": ([_P, ctypes.POINTER(_P), _I, _I, _I, _P, _P], _I),
     "tovl_gated_copy": ([_P, _P, _P, _LL, _I, _P, _I, _I, _P], _I),
@@ -210,6 +231,13 @@ def _dense(name, t, dtype, shape):
     return t.data_ptr()
 
 
+def _count(name, t) -> int:
+    """Checks a contiguous int32 vector; returns its length."""
+    if t is None or t.dtype is not _I32 or t.dim() != 1 or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous {_I32} vector")
+    return t.shape[0]
+
+
 def _bytes(name, t) -> int:
     if not t.is_contiguous():
         raise TypeError(f"{name} must be contiguous")
@@ -229,6 +257,41 @@ def _packed(name, w, lead, K, N, group):
     if zeros is None:
         return words.data_ptr(), scales.data_ptr(), None
     return words.data_ptr(), scales.data_ptr(), _dense("zeros", zeros, _U8, groups)
+
+
+def _heads(name, t, rows, heads, dim) -> int:
+    """Checks a bf16 [rows, heads, dim] tensor whose rows are contiguous; returns the distance of its rows in elements."""
+    if t is None or t.dtype is not _BF16 or t.shape != (rows, heads, dim):
+        raise TypeError(f"{name} must be {_BF16} ({rows}, {heads}, {dim})")
+    s = t.stride()
+    if (s[2] != 1 and dim > 1) or (s[1] != dim and heads > 1):
+        raise TypeError(f"{name} must have contiguous heads")
+    return s[0] if rows > 1 else (heads * dim + 7) // 8 * 8
+
+
+class KVCache:
+    """A paged cache: k and v [pages, page, heads, dim], bf16 or e4m3, of the same strides (any, e.g. transposed from
+    [pages, heads, page, dim] or halves of one tensor; the last is 1); e4m3 with fp32 scales [pages, heads, page].  Keeps
+    the tensors alive and the struct that the calls take."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if _BF16 is None:
+            _load_types()
+        code = _type_of("k", k, (TOVL_BF16, TOVL_E4M3))
+        if k.dim() != 4 or v.dtype is not k.dtype or v.shape != k.shape:
+            raise TypeError("k and v must be [pages, page, heads, dim] of one type and shape")
+        shape = pages, page, heads, dim = tuple(k.shape)
+        s = k.stride()
+        if any(a != b for a, b, n in zip(s, v.stride(), shape) if n > 1) or (s[3] != 1 and dim > 1):
+            raise TypeError("k and v must have the same strides, of 1 in the last dimension")
+        if (code == TOVL_E4M3) != (k_scale is not None) or (code == TOVL_E4M3) != (v_scale is not None):
+            raise TypeError("scales go with an e4m3 cache, and only with it")
+        scales = [None if x is None else _dense(n, x, _F32, (pages, heads, page)) for n, x in (("k_scale", k_scale),
+                                                                                             ("v_scale", v_scale))]
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.pages, self.page, self.heads, self.dim = shape
+        self.struct = tovl_kv_cache(k.data_ptr(), v.data_ptr(), *scales, code, *shape, s[0], s[1], s[2])
+        self.ref = ctypes.addressof(self.struct)
 
 
 def default_config(device: int = 0) -> tovl_config:
@@ -450,6 +513,70 @@ class Handle:
                                      _ptr(zero), _stream(stream))
         _check(self.h, rc, "tovl_quantize_q4")
         return words, scale, zero
+
+    # ------------------------------------------------------------ paged attention step
+    def page_plan(self, length, add, table, ring, state, page, length_out, state_out, slots, positions, starts, stream=None):
+        """Pages, cache slots and positions of ``add`` [B] new tokens (-1: the request has ended) of requests that hold
+        ``length`` tokens: takes pages from ``ring`` into ``table`` [B, width] and gives ended requests' back;
+        ``length_out`` and ``state_out`` may be ``length`` and ``state``.  All int32."""
+        if _BF16 is None:
+            _load_types()
+        B, width = table.shape
+        cap = slots.shape[0]
+        rc = (_lib or load()).tovl_page_plan(
+            self.h, _dense("length", length, _I32, (B,)), _dense("add", add, _I32, (B,)), B, table.data_ptr(),
+            _matrix("table", table, _I32, B, width), width, ring.data_ptr(), _count("ring", ring), page,
+            _dense("state", state, _I32, (4,)), _dense("length_out", length_out, _I32, (B,)),
+            _dense("state_out", state_out, _I32, (4,)), _dense("slots", slots, _I32, (cap,)),
+            _dense("positions", positions, _I32, (cap,)), cap, _dense("starts", starts, _I32, (B + 1,)), _stream(stream))
+        if rc:
+            _check(self.h, rc, "tovl_page_plan")
+
+    def rope_append(self, q, k, v, positions, slots, cos_sin, cache, q_out, interleaved=False, stream=None):
+        """Rotary embedding of q [T, Hq, dim] into ``q_out`` and of k [T, heads, dim], k and v to their ``slots`` of a
+        ``KVCache`` (-1: not written); ``cos_sin`` fp32 [positions, rot] (None: no rotation).  Tensors may be slices of one
+        projection's rows."""
+        if _BF16 is None:
+            _load_types()
+        T, Hq, D = q.shape
+        if D != cache.dim:
+            raise TypeError(f"q must have {cache.dim} columns")
+        far = rot = 0
+        table = None
+        if cos_sin is not None:
+            far, rot = cos_sin.shape
+            table = _dense("cos_sin", cos_sin, _F32, (far, rot))
+        rc = (_lib or load()).tovl_rope_append(
+            self.h, q.data_ptr(), _heads("q", q, T, Hq, D), k.data_ptr(), _heads("k", k, T, cache.heads, D), v.data_ptr(),
+            _heads("v", v, T, cache.heads, D), _dense("positions", positions, _I32, (T,)), _dense("slots", slots, _I32, (T,)),
+            table, far, rot, 1 if interleaved else 0, T, Hq, cache.ref, q_out.data_ptr(), _heads("q_out", q_out, T, Hq, D),
+            _stream(stream))
+        if rc:
+            _check(self.h, rc, "tovl_rope_append")
+
+    def attn_decode_workspace(self, Hq: int, heads: int, dim: int) -> int:
+        """Bytes of workspace of ``attn_decode``, any batch and lengths."""
+        n = load().tovl_attn_decode_workspace(self.h, Hq, heads, dim)
+        if n < 0:
+            raise TovlError(TOVL_ERR_UNSUPPORTED, "tovl_attn_decode_workspace")
+        return n
+
+    def attn_decode(self, q, cache, table, length, scale, out, workspace, window=0, lse=None, stream=None):
+        """Attention of one new token per request: q [B, Hq, dim] over the ``length`` [B] cached tokens (the last
+        ``window`` of them) in the pages of ``table`` [B, width]; ``lse`` fp32 [B, Hq]."""
+        if _BF16 is None:
+            _load_types()
+        B, Hq, D = q.shape
+        if D != cache.dim:
+            raise TypeError(f"q must have {cache.dim} columns")
+        width = table.shape[1]
+        rc = (_lib or load()).tovl_attn_decode(
+            self.h, q.data_ptr(), _heads("q", q, B, Hq, D), B, Hq, cache.ref, table.data_ptr(),
+            _matrix("table", table, _I32, B, width), width, _dense("length", length, _I32, (B,)), scale, window,
+            out.data_ptr(), _heads("out", out, B, Hq, D), None if lse is None else _dense("lse", lse, _F32, (B, Hq)),
+            workspace.data_ptr(), _bytes("workspace", workspace), _stream(stream))
+        if rc:
+            _check(self.h, rc, "tovl_attn_decode")
 
     def gated_copy(self, src, dst, perm, gated=True, stamps=False, stream=None):
         n, rb = src.shape

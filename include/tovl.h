@@ -372,6 +372,121 @@ int tovl_matvec_q4(tovl_handle h, const void* x, int x_type, const float* x_scal
 int tovl_quantize_q4(tovl_handle h, const void* W, int E, int K, int N, int group, void* wq, void* w_scale,
                      void* w_zero, void* stream);
 
+/* ---------------------------------------------------------------- paged attention step
+ * Operators of a serving step around the key-value cache: pages and cache
+ * slots for the step's new tokens, their rotary embedding with the cache
+ * writes, and attention of one new token per request.  A cache is pages of
+ * `page` slots that requests own through a block table: token t of request b
+ * lies in slot t % page of page table[b][t / page].  None of the calls is a
+ * protocol round; a batch of 0 requests or tokens does nothing.  Tensors do
+ * not overlap unless said so. */
+
+/* Element (page p, slot s, head g, column d) of the keys and of the values is
+ * p * page_stride + s * slot_stride + g * head_stride + d elements from k and
+ * v.  An e4m3 cache has one fp32 scale per slot and head for each of the two:
+ * a row stands for its elements times k_scale (v_scale) [p][g][s], positive
+ * and contiguous.  k and v are 16-byte aligned, dim and the strides multiples
+ * of 16 bytes, strides at least dim (those of extents of 1 are not used). */
+typedef struct {
+    void* k;
+    void* v;
+    float* k_scale;            /* [pages][heads][page]; null for bf16 */
+    float* v_scale;
+    int type;                  /* TOVL_BF16 or TOVL_E4M3 */
+    int pages;                 /* pages * page < 2^31 */
+    int page;                  /* slots of a page, any number */
+    int heads;
+    int dim;                   /* columns, up to 256 */
+    long long page_stride, slot_stride, head_stride;   /* elements */
+} tovl_kv_cache;
+
+/* Pages, cache slots and positions of a step's new tokens, in one kernel.
+ *   length      device, int32 [B]: tokens that each request holds; B 0 .. 4096
+ *   add         device, int32 [B]: new tokens (0 for none), or -1 for a request
+ *               that has ended and gives its pages back
+ *   table       device, int32 [B][width], rows ldt apart: pages of each request,
+ *               ceil(length / page) of them in use; receives the new ones behind
+ *   ring        device, int32 [pages]: free pages, from entry state[0] on (it
+ *               goes on at entry 0 behind the last); given-back pages are
+ *               written behind the free ones
+ *   state       device, int32 [4]: first free entry, number of free pages; the
+ *               other two are not read
+ *   length_out  device, int32 [B]: length + add, 0 for a request that has ended;
+ *               may be length
+ *   state_out   device, int32 [4]: the new state, then the number of new tokens
+ *               and of lacking pages; may be state
+ *   slots, positions device, int32 [cap]: for the new tokens of request 0, 1, ...
+ *               in the order of their positions page * table[b][position / page]
+ *               + position % page and position; behind the last -1 and 0
+ *   starts      device, int32 [B+1]: first new token of each request in slots,
+ *               and their number
+ * New pages are taken from the ring in the order of requests and positions;
+ * pages that a call gives back serve from the next call on, in the same order.
+ * With too few free pages nothing changes: no new tokens (slots all -1),
+ * length_out = length, state_out[3] = the pages that are lacking.  Counts that
+ * cannot be (a length below 0 or add below -1, more tokens than width pages or
+ * cap hold, more free pages than there are) leave everything as it was too, with
+ * state_out[3] = -1, and set TOVL_ERR_INVALID in the status word. */
+int tovl_page_plan(tovl_handle h, const int* length, const int* add, int B, int* table, long long ldt, int width,
+                   int* ring, int pages, int page, const int* state, int* length_out, int* state_out, int* slots,
+                   int* positions, int cap, int* starts, void* stream);
+
+/* Rotary embedding of queries and keys; keys and values to their cache slots.
+ * With c and s the cosine and sine of pair i at the token's position,
+ *   (x, y) -> (x c - y s, y c + x s), i = 0 .. rot/2 - 1,
+ * of columns (i, i + rot/2), or (2 i, 2 i + 1) with interleaved; columns from
+ * rot on stay.  In fp32, rounded once to bf16; to an e4m3 cache
+ *   scale = max(max |x|, 1e-12) / 448 of the row, e4m3(x / scale), ties to even.
+ *   q           device, bf16 [T][Hq][dim], tokens ldq elements apart
+ *   k, v        device, bf16 [T][heads][dim], ldk and ldv apart
+ *   positions   device, int32 [T], in [0, max_pos)
+ *   slots       device, int32 [T]: page * page id + slot, all different; -1: the
+ *               token is not written (its position is not checked, its q_out
+ *               means nothing if it is out of range)
+ *   cos_sin     device, fp32 [max_pos][rot]: rot/2 cosines, rot/2 sines
+ *   rot         a multiple of 16 up to dim, 0 for none (cos_sin unused)
+ *   q_out       device, bf16 [T][Hq][dim], ldqo apart; may be q
+ * Token rows are 16-byte aligned, their distances multiples of 8 elements.
+ * Another slot or position sets TOVL_ERR_INVALID in the status word; its keys
+ * and values are not written.  A NaN in a row of an e4m3 cache makes its scale
+ * NaN. */
+int tovl_rope_append(tovl_handle h, const void* q, long long ldq, const void* k, long long ldk, const void* v,
+                     long long ldv, const int* positions, const int* slots, const float* cos_sin, int max_pos,
+                     int rot, int interleaved, int T, int Hq, const tovl_kv_cache* cache, void* q_out,
+                     long long ldqo, void* stream);
+
+/* Bytes of workspace that tovl_attn_decode needs on the handle's device, any
+ * batch and lengths; -1 if the sizes are not supported. */
+long long tovl_attn_decode_workspace(tovl_handle h, int Hq, int heads, int dim);
+
+/* Attention of one new token per request over its cached tokens, the new one
+ * among them:
+ *   z[t] = scale * q[b][g] . k[t], t from max(0, length - window) (0 without a
+ *   window) to length - 1, k and v of head g / (Hq / heads),
+ *   out[b][g] = sum of softmax(z)[t] v[t], lse[b][g] = ln sum exp z[t]
+ * with fp32 sums, rounded once to bf16.  Weights are off by 2^-15 of themselves with
+ * a bf16 cache; with an e4m3 one 2^-11, and weights times scales below 2^-14 of
+ * a row's largest an absolute 2^-25 of that.
+ *   q           device, bf16 [B][Hq][dim], requests ldq elements apart (a
+ *               multiple of 8), 16-byte aligned; Hq a multiple of heads
+ *   table       device, int32 [B][width], rows ldt apart
+ *   length      device, int32 [B], 0 .. width * page; B 0 .. 65536
+ *   window      the last tokens that are seen; 0 = all
+ *   out         device, bf16 [B][Hq][dim], ldo apart, like q; a request of
+ *               length 0 gets zeros and an lse of -inf
+ *   lse         device, fp32 [B][Hq]; null = not wanted
+ *   workspace   device, 256-byte aligned, any content; free again when the
+ *               call's kernel has ended
+ * Entries of the table outside the pages that hold seen tokens are not read,
+ * nor are slots outside them.  A page outside [0, pages) or a length out of range sets
+ * TOVL_ERR_INVALID in the status word; the request's result means nothing then.
+ * Numbers that are infinite or NaN in seen rows show in the results that see
+ * them.  The result of a call depends on its arguments alone (the same bits on
+ * every call on the same device). */
+int tovl_attn_decode(tovl_handle h, const void* q, long long ldq, int B, int Hq, const tovl_kv_cache* cache,
+                     const int* table, long long ldt, int width, const int* length, float scale, int window,
+                     void* out, long long ldo, float* lse, void* workspace, long long workspace_bytes, void* stream);
+
 /* ---------------------------------------------------------------- controls
  * The acceptance method of the platform page, section 5, compares the fused
  * kernel with its parts run alone on the same SM counts. */

@@ -1,0 +1,153 @@
+"""The paged attention step's entry points without a GPU: the host's argument checks (csrc/paged_api.cu, its launches
+replaced by ones that count) refuse what the kernels do not take, and nothing else."""
+import ctypes
+import subprocess
+
+import pytest
+
+from consumer_movement_gemm_gb300 import build as tovl_build
+from consumer_movement_gemm_gb300 import tovl
+
+OK, INVALID, UNSUPPORTED = tovl.TOVL_OK, tovl.TOVL_ERR_INVALID, tovl.TOVL_ERR_UNSUPPORTED
+NAMES = ("tovl_page_plan", "tovl_rope_append", "tovl_attn_decode")
+BIG = 1 << 20
+
+
+@pytest.fixture(scope="module")
+def lib(tmp_path_factory):
+    at = tmp_path_factory.mktemp("paged")
+    src = at / "paged.cu"
+    src.write_text('#include "paged_api.cu"\n'
+                   "static int launches;\n"
+                   "namespace tovl {\n"
+                   "cudaError_t launch_page_plan(const PagePlanParams&, int, cudaStream_t, bool) { ++launches; return cudaSuccess; }\n"
+                   "cudaError_t launch_rope_append(const RopeParams&, bool, int, cudaStream_t, bool) { ++launches; return cudaSuccess; }\n"
+                   "cudaError_t launch_attn_decode(const AttnParams&, bool, int, cudaStream_t, bool) { ++launches; return cudaSuccess; }\n"
+                   "long long attn_decode_workspace(int, int, int) { return 4096; }\n"
+                   "}\n"
+                   'TOVL_API void* make() { auto* h = new tovl_ctx(); h->num_sms = 152; return h; }\n'
+                   'TOVL_API int count() { return launches; }\n')
+    so = at / "paged.so"
+    subprocess.run([tovl_build._nvcc(), *tovl_build._flags(), "-shared", "-cudart", "shared", "-o", str(so), str(src)], check=True,
+                   capture_output=True)
+    lib = ctypes.CDLL(str(so))
+    for n in NAMES + ("tovl_attn_decode_workspace",):
+        getattr(lib, n).argtypes, getattr(lib, n).restype = tovl.SIGNATURES[n]
+    lib.make.restype = ctypes.c_void_p
+    return lib
+
+
+# addresses that are never followed
+P = 1 << 16
+
+
+def cache(**change):
+    f = dict(k=P, v=P, k_scale=None, v_scale=None, type=tovl.TOVL_BF16, pages=9, page=16, heads=2, dim=64, page_stride=2048,
+             slot_stride=128, head_stride=64)
+    f.update(change)
+    c = tovl.tovl_kv_cache(**f)
+    cache.alive = c
+    return ctypes.addressof(c)
+
+
+PLAN = dict(length=P, add=P, B=3, table=P, ldt=5, width=5, ring=P, pages=9, page=16, state=P, length_out=P, state_out=P, slots=P,
+            positions=P, cap=8, starts=P, stream=None)
+ROPE = dict(q=P, ldq=256, k=P, ldk=128, v=P, ldv=128, positions=P, slots=P, cos_sin=P, max_pos=7, rot=64, interleaved=0, T=3, Hq=4,
+            cache={}, q_out=P, ldqo=256, stream=None)
+ATTN = dict(q=P, ldq=256, B=3, Hq=4, cache={}, table=P, ldt=5, width=5, length=P, scale=0.125, window=0, out=P, ldo=256, lse=P,
+            workspace=P, workspace_bytes=4096, stream=None)
+
+
+def call(lib, name, base, **change):
+    a = {**base, **change}
+    if "cache" in a and a["cache"] is not None:
+        a["cache"] = cache(**a["cache"])
+    before = lib.count()
+    rc = getattr(lib, name)(lib.make(), *a.values())
+    return rc, lib.count() - before
+
+
+def test_what_fits_is_launched(lib):
+    e4m3 = dict(type=tovl.TOVL_E4M3, k_scale=P, v_scale=P)
+    for name, base, changes in (
+            ("tovl_page_plan", PLAN, [{}, dict(B=4096), dict(cap=0, slots=None, positions=None), dict(ldt=700)]),
+            ("tovl_rope_append", ROPE, [{}, dict(rot=0, cos_sin=None, max_pos=0), dict(rot=16), dict(ldq=264, ldk=1024), dict(cache=e4m3)]),
+            ("tovl_attn_decode", ATTN, [{}, dict(lse=None), dict(window=1 << 30), dict(cache=e4m3), dict(cache=dict(page=1, slot_stride=0)),
+                                        dict(cache=dict(page=1000, page_stride=128000)), dict(cache=dict(head_stride=1024, slot_stride=64)),
+                                        dict(cache=dict(heads=1, head_stride=3, slot_stride=64, page_stride=1024)), dict(B=65536)])):
+        for c in changes:
+            assert call(lib, name, base, **c) == (OK, 1), (name, c)
+
+
+def test_nothing_to_do_is_not_launched(lib):
+    for name, base, n in (("tovl_page_plan", PLAN, "B"), ("tovl_rope_append", ROPE, "T"), ("tovl_attn_decode", ATTN, "B")):
+        nothing = {k: None for k, v in base.items() if v == P}
+        assert call(lib, name, base, **{**nothing, n: 0, **({"cos_sin": P} if n == "T" else {})}) == (OK, 0), name
+
+
+@pytest.mark.parametrize("name,base", [("tovl_page_plan", PLAN), ("tovl_rope_append", ROPE), ("tovl_attn_decode", ATTN)])
+def test_null_and_misaligned_pointers_are_refused(lib, name, base):
+    for k, v in base.items():
+        if v != P:
+            continue
+        if k != "lse":
+            assert call(lib, name, base, **{k: None}) == (INVALID, 0), k
+        assert call(lib, name, base, **{k: P + 2}) == (INVALID, 0), k
+
+
+def test_plan_refusals(lib):
+    for c, rc in ((dict(B=-1), INVALID), (dict(B=4097), UNSUPPORTED), (dict(width=0), INVALID), (dict(ldt=4), INVALID),
+                  (dict(pages=0), INVALID), (dict(page=0), INVALID), (dict(cap=-1), INVALID), (dict(pages=BIG, page=2048), UNSUPPORTED)):
+        assert call(lib, "tovl_page_plan", PLAN, **c) == (rc, 0), c
+
+
+def test_append_refusals(lib):
+    for c, rc in ((dict(T=-1), INVALID), (dict(Hq=0), INVALID), (dict(rot=-16), INVALID), (dict(rot=80), INVALID), (dict(rot=24), UNSUPPORTED),
+                  (dict(max_pos=0), INVALID), (dict(ldq=248), INVALID), (dict(ldq=260), INVALID), (dict(ldk=120), INVALID),
+                  (dict(ldv=132), INVALID), (dict(ldqo=192), INVALID), (dict(q=P + 8), INVALID), (dict(cos_sin=P + 8), INVALID),
+                  (dict(T=2 ** 31 - 1, Hq=4096, ldq=4096 * 64, ldqo=4096 * 64), UNSUPPORTED), (dict(cache=None), INVALID)):
+        assert call(lib, "tovl_rope_append", ROPE, **c) == (rc, 0), c
+
+
+def test_attention_refusals(lib):
+    for c, rc in ((dict(B=-1), INVALID), (dict(B=65537), UNSUPPORTED), (dict(Hq=3), INVALID), (dict(Hq=0), INVALID), (dict(Hq=4098), UNSUPPORTED),
+                  (dict(window=-1), INVALID), (dict(width=0), INVALID), (dict(ldt=4), INVALID), (dict(ldq=252), INVALID), (dict(ldo=248), INVALID),
+                  (dict(workspace=P + 128), INVALID), (dict(workspace_bytes=4095), INVALID), (dict(cache=None), INVALID)):
+        assert call(lib, "tovl_attn_decode", ATTN, **c) == (rc, 0), c
+
+
+@pytest.mark.parametrize("name,base", [("tovl_rope_append", ROPE), ("tovl_attn_decode", ATTN)])
+def test_cache_refusals(lib, name, base):
+    e4m3 = dict(type=tovl.TOVL_E4M3, k_scale=P, v_scale=P)
+    for c, rc in ((dict(type=tovl.TOVL_F32), INVALID), (dict(k=None), INVALID), (dict(v=P + 8), INVALID), (dict(pages=0), INVALID),
+                  (dict(page=0), INVALID), (dict(heads=0), INVALID), (dict(dim=0), INVALID), (dict(dim=260), UNSUPPORTED),
+                  (dict(dim=264), UNSUPPORTED), (dict(dim=60), UNSUPPORTED), (dict(pages=BIG, page=2048), UNSUPPORTED), (dict(head_stride=56), INVALID),
+                  (dict(slot_stride=132), INVALID), (dict(page_stride=-2048), INVALID), (dict(heads=5000), UNSUPPORTED),
+                  ({**e4m3, "dim": 72}, UNSUPPORTED), ({**e4m3, "k_scale": None}, INVALID), ({**e4m3, "v_scale": P + 2}, INVALID),
+                  ({**e4m3, "slot_stride": 136}, INVALID)):
+        assert call(lib, name, base, cache=c) == (rc, 0), c
+
+
+def test_workspace_sizes(lib):
+    h = lib.make()
+    assert lib.tovl_attn_decode_workspace(h, 8, 2, 64) == 4096
+    for a in ((0, 1, 64), (8, 0, 64), (8, 3, 64), (8, 2, 0), (8, 2, 260), (8, 2, 60), (8192, 2, 64)):
+        assert lib.tovl_attn_decode_workspace(h, *a) == -1, a
+
+
+def test_null_handles_are_refused():
+    tovl_build.build()
+    for name in NAMES:
+        args = [0 if a is not tovl._P else None for a in tovl.SIGNATURES[name][0]]
+        assert getattr(tovl.load(), name)(*args) == INVALID, name
+    assert tovl.load().tovl_attn_decode_workspace(None, 8, 2, 64) == -1
+
+
+def test_the_binding_and_the_header_agree_on_the_cache():
+    import os
+    import re
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(tovl.__file__))), "include", "tovl.h")).read()
+    body = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    body = re.search(r"typedef struct \{([^}]*)\} tovl_kv_cache;", body).group(1)
+    names = [n.strip(" *") for line in body.split(";") if line.strip() for n in re.sub(r"^\s*(void|float|int|long long)", "", line).split(",")]
+    assert names == [n for n, _ in tovl.tovl_kv_cache._fields_]
