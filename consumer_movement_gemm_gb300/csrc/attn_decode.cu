@@ -42,27 +42,35 @@ struct Shape {
     static constexpr int NT = NT_;                 // blocks of 8 query heads
     static constexpr int kHeads = 8 * NT;
     static constexpr int kRow = DP * (F8 ? 1 : 2);
-    static constexpr int kPitch = kRow + 16;       // rows start 4 banks apart
-    static constexpr int kTile = kRow <= 128 ? 32 : 16;
+    static constexpr int kBlockRow = kRow < 128 ? kRow : 128;          // bytes of a row in a column block
+    static constexpr int CB = kRow / kBlockRow;
+    static constexpr int kTile = kRow <= 64 ? 64 : kRow <= 128 ? 32 : 16;
+    static constexpr int kBlock = kTile * kBlockRow;
+    static constexpr int kRows = CB * kBlock;      // all of k or of v
     static constexpr int MT = kTile / 16;
     static constexpr int JT = DP / 16;             // blocks of 16 columns
-    static constexpr int kScales = 2 * kTile * kPitch;                 // offset in a stage
-    static constexpr int kMeta = kScales + (F8 ? 2 * kTile * 4 : 0);
-    static constexpr int kStage = kMeta + 16;
-    static constexpr int kWarps = kStage > 16000 ? 4 : 8;
-    static constexpr int kFit = (224 * 1024) / (kWarps * kStage);
-    static constexpr int kStages = kFit > 6 ? 6 : kFit;
+    static constexpr int kScales = 2 * kRows;      // offset in a stage
+    static constexpr int kStage = 2 * kRows + (F8 ? 1024 : 0);
+    static constexpr int kWarps = kRow > 256 ? 6 : 8;
+    static constexpr int kFit = (222 * 1024) / (kWarps * kStage);
+    static constexpr int kStages = kFit > 4 ? 4 : kFit;
     static constexpr int kThreads = kWarps * 32;
-    static constexpr int kSmem = kWarps * kStages * kStage;
+    static constexpr int kRing = kStages * kStage;
+    static constexpr int kSmem = kWarps * kRing + 1024;
     static constexpr int kFrag = NT * JT * 32;     // float4 of one O
     static constexpr int kPart = kFrag * 4 + 2 * kHeads;               // floats of a part: O, m, sum
-    static_assert(kStages >= 3, "ring");
+    // the 16-byte pieces of row r of a block are exchanged by XOR with this
+    // (so that 8 rows' pieces lie in different banks; the copies' swizzle)
+    static __host__ __device__ constexpr int phase(int r) { return kBlockRow == 128 ? r & 7 : (r >> 1) & 3; }
+    static_assert(kBlockRow == 64 || kBlockRow == 128, "swizzle");
+    static_assert(kStages >= 2 && kBlock % 1024 == 0 && kPart * 4 <= kRing, "ring");
 };
 
 // What is left behind of a segment that does not lie within one warp's share.
 struct Open {
-    long long first, end;      // its tiles in the order of the call
-    int b, vh;                 // end == 0: none
+    long long first, end;      // its tiles in the order of the call; end == 0: none
+    const float* part;
+    int b, vh;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes)
@@ -78,6 +86,36 @@ template <int N>
 __device__ __forceinline__ void cp_wait()
 {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// One box of a cache: `cols` columns of one head, `rows` slots of one page.
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z, int w)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
+        "[%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+__device__ __forceinline__ void load_bulk(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// Bounded wait for a stage's copies (a bound against logic errors).
+__device__ __forceinline__ bool wait_full(uint64_t* bar, uint32_t parity, const AttnParams& p)
+{
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    const uint64_t start = ptx::globaltimer();
+    for (uint32_t i = 1; !ptx::mbar_try_wait(bar, parity); ++i) {
+        if ((i & 255) == 0 && ptx::globaltimer() - start > static_cast<uint64_t>(p.timeout_ns)) {
+            record_error(p.ctrl, kErrTimeout);
+            return false;
+        }
+    }
+    return true;
 }
 
 __device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr)
@@ -233,47 +271,82 @@ __device__ __forceinline__ float lse_of(float m, float l)
     return l > 0.f || l != l ? (m + log2f(l) - (S::F8 ? kShift : 0.f)) * 0.693147180559945309f : -INFINITY;
 }
 
-// Joins `count` parts (part(i): its floats) of one segment; f gets each float4
-// and where it belongs, g the statistics.  All threads of the CTA.
-template <class S, class Part, class F, class G>
-__device__ __forceinline__ void join(int count, Part part, F f, G g)
+// Element e of the joined parts of one segment, with the statistics of its two
+// heads, in the order of the parts; four are in flight at a time.
+template <class S, bool FAR, class Part>
+__device__ __forceinline__ float4 join(int count, Part part, int e, int h, float2& m, float2& l)
 {
-    for (int e = threadIdx.x; e < S::kFrag; e += S::kThreads) {
-        const int lane = e & 31, j = e / 32 % S::JT, nt = e / 32 / S::JT;
-        const int h = nt * 8 + 2 * (lane & 3);
-        float m0 = -INFINITY, m1 = -INFINITY;
-        for (int i = 0; i < count; ++i) {
-            const float2 m = __ldcg(reinterpret_cast<const float2*>(part(i) + S::kFrag * 4 + h));
-            m0 = fmaxf(m0, m.x), m1 = fmaxf(m1, m.y);
+    constexpr int kAhead = 4;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    m = make_float2(-INFINITY, -INFINITY), l = make_float2(0.f, 0.f);
+    for (int i = 0; i < count; i += kAhead) {
+        float2 pm[kAhead], pl[kAhead];
+        float4 v[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            pm[k] = make_float2(-INFINITY, -INFINITY), pl[k] = make_float2(0.f, 0.f), v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i + k >= count) continue;
+            const float* q = part(i + k);
+            const float2* stats = reinterpret_cast<const float2*>(q + S::kFrag * 4 + h);
+            if (FAR) {
+                pm[k] = __ldcg(stats), pl[k] = __ldcg(stats + S::kHeads / 2), v[k] = __ldcg(reinterpret_cast<const float4*>(q) + e);
+            } else {
+                pm[k] = *stats, pl[k] = stats[S::kHeads / 2], v[k] = reinterpret_cast<const float4*>(q)[e];
+            }
         }
-        const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        float l0 = 0.f, l1 = 0.f;
-        for (int i = 0; i < count; ++i) {
-            const float* q = part(i);
-            const float2 m = __ldcg(reinterpret_cast<const float2*>(q + S::kFrag * 4 + h));
-            const float2 l = __ldcg(reinterpret_cast<const float2*>(q + S::kFrag * 4 + S::kHeads + h));
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(q) + e);
-            const float w0 = ex2(m.x - u0), w1 = ex2(m.y - u1);
-            o.x += v.x * w0, o.y += v.y * w1, o.z += v.z * w0, o.w += v.w * w1;
-            l0 += l.x * w0, l1 += l.y * w1;
+        float2 top = m;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) top.x = fmaxf(top.x, pm[k].x), top.y = fmaxf(top.y, pm[k].y);
+        const float u0 = top.x == -INFINITY ? 0.f : top.x, u1 = top.y == -INFINITY ? 0.f : top.y;
+        const float c0 = ex2(m.x - u0), c1 = ex2(m.y - u1);
+        o.x *= c0, o.y *= c1, o.z *= c0, o.w *= c1, l.x *= c0, l.y *= c1;
+        m = top;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const float w0 = ex2(pm[k].x - u0), w1 = ex2(pm[k].y - u1);
+            o.x += v[k].x * w0, o.y += v[k].y * w1, o.z += v[k].z * w0, o.w += v[k].w * w1;
+            l.x += pl[k].x * w0, l.y += pl[k].y * w1;
         }
-        f(e, nt, j, lane, o, l0, l1);
-        if (j == 0 && lane < 4) g(h, m0, m1, l0, l1);
     }
+    return o;
+}
+
+// CTAs that share a segment join in groups where there are more than kFlat.
+constexpr int kFlat = 24;
+constexpr int kGroup = 12;
+
+// First tile of CTA c's share, and the CTA of a tile.
+__device__ __forceinline__ long long share_of(long long total, int ctas, int c)
+{
+    if (total < (1 << 24)) return static_cast<unsigned>(total) * c / ctas;
+    return total * c / ctas;
+}
+__device__ __forceinline__ int cta_of(long long total, int ctas, long long tile)
+{
+    if (total < (1 << 24)) return (static_cast<unsigned>(tile + 1) * ctas - 1) / static_cast<unsigned>(total);
+    return static_cast<int>(((tile + 1) * ctas - 1) / total);
 }
 
 template <class S>
-__global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnParams p)
+__global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __grid_constant__ AttnParams p)
 {
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t s_full[S::kWarps][S::kStages];
+    __shared__ int4 s_meta[S::kWarps][S::kStages];
     __shared__ long long s_sum[S::kWarps];
     __shared__ Cursor<S> s_start[S::kWarps];
     __shared__ Open s_open[S::kWarps * 2];
     __shared__ int s_last;
-    constexpr int kTile = S::kTile, NT = S::NT, JT = S::JT, MT = S::MT, kStages = S::kStages;
+    constexpr int kTile = S::kTile, NT = S::NT, JT = S::JT, MT = S::MT, kStages = S::kStages, CB = S::CB;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        ptx::prefetch_tmap(&p.k_map);
+        ptx::prefetch_tmap(&p.v_map);
+    }
+    if (lane < kStages) ptx::mbar_init(&s_full[warp][lane], 1);
+    if (lane < 2) s_open[warp * 2 + lane].end = 0;
+    ptx::fence_mbar_init();
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
 
@@ -294,7 +367,6 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
         if (lane >= d) before += o;
     }
     if (lane == 31) s_sum[warp] = before;
-    if (lane < 2) s_open[warp * 2 + lane].end = 0;
     __syncthreads();
     long long total = 0;
 #pragma unroll
@@ -302,12 +374,12 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
         if (w < warp) before += s_sum[w];
         total += s_sum[w];
     }
-    before -= sum;
+    before = (before - sum) * heads;
+    sum *= heads;
     total *= heads;
     // CTAs that get work: as many as the warps' tiles need, or all
-    const long long want = (total + S::kWarps - 1) / S::kWarps;
-    const int ctas = static_cast<int>(want < gridDim.x ? want : gridDim.x), warps = ctas * S::kWarps;
     const int cta = blockIdx.x;
+    const int ctas = static_cast<int>(min((total + S::kWarps - 1) / S::kWarps, static_cast<long long>(gridDim.x)));
     // requests without tokens: nothing of theirs is in the order
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
         if (__ldg(p.length + b) > 0) continue;
@@ -317,87 +389,134 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
             for (int i = tid; i < p.Hq; i += S::kThreads) p.lse[static_cast<long long>(b) * p.Hq + i] = -INFINITY;
     }
     if (cta >= ctas) return;
-    for (int w = 0; w < S::kWarps; ++w) {
-        const long long from = (static_cast<long long>(cta) * S::kWarps + w) * total / warps;
-        const long long to = (static_cast<long long>(cta) * S::kWarps + w + 1) * total / warps;
-        if (from < before * heads || from >= (before + sum) * heads) continue;
-        Cursor<S> c;
-        c.left = to - from;
-        c.at = from;
-        long long r = from - before * heads;
-        for (c.b = b0;; ++c.b) {
-            c.enter(p);
-            if (r < static_cast<long long>(c.count) * heads) break;
-            r -= static_cast<long long>(c.count) * heads;
+    const long long cta_from = share_of(total, ctas, cta), cta_to = share_of(total, ctas, cta + 1);
+    if (cta_from < before + sum && cta_to > before) {
+        // the warps' shares that begin in this thread's requests
+        for (int w = 0; w < S::kWarps; ++w) {
+            const long long from = cta_from + (cta_to - cta_from) * w / S::kWarps, to = cta_from + (cta_to - cta_from) * (w + 1) / S::kWarps;
+            if (from < before || from >= before + sum) continue;
+            Cursor<S> c;
+            c.left = to - from;
+            c.at = from;
+            long long r = from - before;
+            for (c.b = b0;; ++c.b) {
+                c.enter(p);
+                if (r < static_cast<long long>(c.count) * heads) break;
+                r -= static_cast<long long>(c.count) * heads;
+            }
+            if (r < (1LL << 31)) {
+                c.vh = static_cast<int>(static_cast<unsigned>(r) / static_cast<unsigned>(c.count));
+            } else {
+                c.vh = static_cast<int>(r / c.count);
+            }
+            c.tile = c.first + static_cast<int>(r - static_cast<long long>(c.vh) * c.count);
+            s_start[w] = c;
         }
-        c.vh = static_cast<int>(r / c.count);
-        c.tile = c.first + static_cast<int>(r % c.count);
-        s_start[w] = c;
     }
     __syncthreads();
 
     // ---------------------------------------------------------------- a warp's stream
-    float* const scratch = p.part + (static_cast<long long>(cta) * S::kWarps + warp) * 2 * S::kPart;
-    uint8_t* const ring = smem + warp * kStages * S::kStage;
+    uint8_t* const ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023)) + warp * S::kRing;
     const uint32_t ring_u = ptx::smem_u32(ring);
     Cursor<S> put = s_start[warp];
     const long long tiles = put.left;
-    int page_id = -1;
-    const auto find_page = [&]() {
-        const int t = put.tile * kTile + lane;
+    const auto page_of = [&](int t) {
+        return p.cache.page_shift >= 0 ? t >> p.cache.page_shift : static_cast<int>(static_cast<unsigned>(t) / static_cast<unsigned>(p.cache.page));
+    };
+    // boxes: lane (k or v, column block, piece of the tile's rows)
+    const int pieces_log = p.pieces_log, box_rows = kTile >> pieces_log;
+    const int piece = lane & ((1 << pieces_log) - 1), box_col = (lane >> pieces_log) % CB, box_kv = (lane >> pieces_log) / CB;
+    const uint32_t box_at = box_kv * S::kRows + box_col * S::kBlock + piece * box_rows * S::kBlockRow;
+    // what the next tile needs from this lane: a box's page and first slot, or (rows
+    // one by one) those of the rows lane and lane + 32
+    constexpr int kOwn = kTile > 32 ? 2 : 1;
+    int page_id[kOwn], page_in[kOwn];
+    const auto find_pages = [&]() {
         const int lo = p.window && put.len > p.window ? put.len - p.window : 0;
-        page_id = -1;
-        if (put.left > 0 && lane < kTile && t >= lo && t < put.len) {
-            const int slot = p.cache.page_shift >= 0 ? t >> p.cache.page_shift : static_cast<int>(static_cast<unsigned>(t) / static_cast<unsigned>(p.cache.page));
-            page_id = __ldg(p.table + put.b * p.ldt + slot);
-            if (static_cast<unsigned>(page_id) >= static_cast<unsigned>(p.cache.pages)) page_id = -2;
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            const int row = p.boxed ? piece * box_rows : i * 32 + lane, t = put.tile * kTile + row, rows = p.boxed ? box_rows : 1;
+            page_id[i] = -1;
+            if (put.left > 0 && row < kTile && t < put.len && t + rows > lo) {
+                const int n = page_of(t);
+                page_in[i] = t - n * p.cache.page;
+                page_id[i] = __ldg(p.table + put.b * p.ldt + n);
+                if (static_cast<unsigned>(page_id[i]) >= static_cast<unsigned>(p.cache.pages)) page_id[i] = -2;
+            }
         }
     };
     // starts the copies of the tile at `put` and moves on
     const auto fetch = [&](int stage) {
         if (put.left > 0) {
             const uint32_t dst = ring_u + stage * S::kStage;
-            const int t = put.tile * kTile + lane, head = put.vh / per_head;
-            long long off = -1;
-            if (page_id >= 0) {
-                const int in = p.cache.page_shift >= 0 ? t & (p.cache.page - 1) : static_cast<int>(static_cast<unsigned>(t) % static_cast<unsigned>(p.cache.page));
-                off = page_id * p.cache.page_stride + in * p.cache.slot_stride + head * p.cache.head_stride;
-                if (S::F8) {
-                    const long long at = (static_cast<long long>(page_id) * p.cache.heads + head) * p.cache.page + in;
-                    cp_async4(dst + S::kScales + lane * 4, p.cache.k_scale + at, 4);
-                    cp_async4(dst + S::kScales + (kTile + lane) * 4, p.cache.v_scale + at, 4);
-                }
-            } else {
-                if (page_id == -2) record_error(p.ctrl, kErrInvalid);
-                if (S::F8 && lane < kTile) {
-                    float* scales = reinterpret_cast<float*>(ring + stage * S::kStage + S::kScales);
-                    scales[lane] = 0.f, scales[kTile + lane] = 0.f;
-                }
-            }
-            constexpr int kPerRow = S::kRow / 16;
-            const int bytes = p.cache.dim * (S::F8 ? 1 : 2);
-#pragma unroll
-            for (int i = 0; i < kTile * kPerRow / 32; ++i) {
-                const int c = i * 32 + lane, row = c / kPerRow, col = c % kPerRow * 16;
-                const long long o = __shfl_sync(0xffffffffu, off, row);
-                const bool in = o >= 0 && col < bytes;
-                const long long src = in ? o + col : 0;
-                cp_async16(dst + row * S::kPitch + col, p.cache.k + src, in ? 16 : 0);
-                cp_async16(dst + (kTile + row) * S::kPitch + col, p.cache.v + src, in ? 16 : 0);
-            }
+            const int head = put.vh / per_head;
             if (lane == 0) {
                 const int last = put.first + put.count - 1;
-                *reinterpret_cast<int4*>(ring + stage * S::kStage + S::kMeta) =
-                    make_int4(put.b, put.vh, put.tile | (put.tile == put.first ? 1 << 30 : 0) | (put.tile == last ? 1 << 31 : 0), put.len);
+                s_meta[warp][stage] = make_int4(put.b, put.vh, put.tile | (put.tile == put.first ? 1 << 30 : 0) | (put.tile == last ? 1 << 31 : 0), put.len);
+            }
+            if (page_id[0] == -2 || page_id[kOwn - 1] == -2) record_error(p.ctrl, kErrInvalid);
+            if (p.boxed) {
+                // what holds no token of this tile is outside the tensor: zeros, and nothing read
+                uint64_t* const full = &s_full[warp][stage];
+                const uint32_t bar = ptx::smem_u32(full);
+                const bool in = page_id[0] >= 0;
+                uint32_t bytes = 2 * S::kRows;
+                if (S::F8) bytes += 8 * box_rows * __popc(__ballot_sync(0xffffffffu, in && lane < 1 << pieces_log));
+                if (lane == 0) ptx::mbar_arrive_expect_tx(full, bytes);
+                if (lane < 2 * CB << pieces_log) {
+                    const int x = box_col * (S::kBlockRow / (S::F8 ? 1 : 2)), page = in ? page_id[0] : p.cache.pages, slot = in ? page_in[0] : 0;
+                    load_box(dst + box_at, box_kv ? &p.v_map : &p.k_map, bar, x, p.slots_first ? slot : head, p.slots_first ? head : slot, page);
+                    if (S::F8 && in && box_col == 0) {
+                        const long long at = (static_cast<long long>(page) * p.cache.heads + head) * p.cache.page + slot;
+                        load_bulk(dst + S::kScales + (box_kv * kTile + piece * box_rows) * 4, (box_kv ? p.cache.v_scale : p.cache.k_scale) + at,
+                                  box_rows * 4, bar);
+                    }
+                }
+            } else {
+                long long off[kOwn];
+#pragma unroll
+                for (int i = 0; i < kOwn; ++i) {
+                    off[i] = -1;
+                    if (page_id[i] >= 0) {
+                        off[i] = page_id[i] * p.cache.page_stride + page_in[i] * p.cache.slot_stride + head * p.cache.head_stride;
+                        if (S::F8) {
+                            const long long at = (static_cast<long long>(page_id[i]) * p.cache.heads + head) * p.cache.page + page_in[i];
+                            cp_async4(dst + S::kScales + (i * 32 + lane) * 4, p.cache.k_scale + at, 4);
+                            cp_async4(dst + S::kScales + (kTile + i * 32 + lane) * 4, p.cache.v_scale + at, 4);
+                        }
+                    }
+                }
+                constexpr int kPerRow = S::kRow / 16, kPerBlock = S::kBlockRow / 16;
+                const int bytes = p.cache.dim * (S::F8 ? 1 : 2);
+#pragma unroll
+                for (int i = 0; i < kTile * kPerRow / 32; ++i) {
+                    const int row = i * 32 / kPerRow + lane / kPerRow, c = lane % kPerRow;
+                    static_assert(kPerRow <= 32, "a row is one instruction's at most");
+                    const long long o = __shfl_sync(0xffffffffu, off[i * 32 / kPerRow / 32], row & 31);
+                    const bool in = o >= 0 && c * 16 < bytes;
+                    const long long src = in ? o + c * 16 : 0;
+                    const uint32_t at = dst + c / kPerBlock * S::kBlock + row * S::kBlockRow + ((c % kPerBlock ^ S::phase(row)) << 4);
+                    cp_async16(at, p.cache.k + src, in ? 16 : 0);
+                    cp_async16(at + S::kRows, p.cache.v + src, in ? 16 : 0);
+                }
             }
             put.next(p, heads);
-            find_page();
+            find_pages();
         }
         cp_commit();
     };
     if (tiles > 0) {
-        find_page();
+        find_pages();
         for (int s = 0; s < kStages - 1; ++s) fetch(s);
+        // fragments of k: row lane % 16, 16 bytes lane / 16; of v: the same (e4m3),
+        // or row lane % 8 + 8 (lane / 16), 16 bytes lane / 8 % 2
+        const int k_row = lane & 15, v_row = S::F8 ? k_row : (lane & 7) + (lane >> 4) * 8;
+        const uint32_t k_base = k_row * S::kBlockRow, v_base = v_row * S::kBlockRow;
+        const uint32_t k_turn = ((lane >> 4) ^ S::phase(k_row)) << 4, v_turn = ((S::F8 ? lane >> 4 : (lane >> 3) & 1) ^ S::phase(v_row)) << 4;
+        // 16-byte piece c (even; the lanes add the last bit) of 16 rows from row `row` on
+        const auto piece_at = [](uint32_t base, uint32_t turn, int row, int c) {
+            return base + c / (S::kBlockRow / 16) * S::kBlock + row * S::kBlockRow + (turn ^ (c % (S::kBlockRow / 16) << 4));
+        };
 
         float4 o[NT][JT];
         uint32_t q[NT][JT][2];
@@ -405,13 +524,25 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
         long long seg_first = 0;
         bool began = false, fresh = true;
         int stage = 0;
+        uint32_t parity = 0;
         for (long long it = 0; it < tiles; ++it) {
-            cp_wait<kStages - 2>();
+            if (p.boxed) {
+                if (!wait_full(&s_full[warp][stage], parity, p)) {
+                    // the other copies in flight, then out
+                    for (int s = 1; s < kStages - 1 && it + s < tiles; ++s) {
+                        if (++stage == kStages) stage = 0, parity ^= 1;
+                        wait_full(&s_full[warp][stage], parity, p);
+                    }
+                    break;
+                }
+            } else {
+                cp_wait<kStages - 2>();
+            }
             __syncwarp();
             fetch(stage == 0 ? kStages - 1 : stage - 1);
-            const uint8_t* st = ring + stage * S::kStage;
+            uint8_t* const st = ring + stage * S::kStage;
             const uint32_t st_u = ring_u + stage * S::kStage;
-            const int4 meta = *reinterpret_cast<const int4*>(st + S::kMeta);
+            const int4 meta = s_meta[warp][stage];
             const int b = meta.x, vh = meta.y, tile = meta.z & 0x3fffffff, len = meta.w;
             const int head0 = vh / per_head * p.group + vh % per_head * S::kHeads;
             const int n_heads = min(S::kHeads, p.group - vh % per_head * S::kHeads);
@@ -472,14 +603,14 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) s[nt][mt] = make_float4(0.f, 0.f, 0.f, 0.f);
-            const uint32_t k_at = st_u + (lane & 15) * S::kPitch + (lane >> 4) * 16;
+            const uint32_t k_at = st_u + k_base;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 if constexpr (S::F8) {
 #pragma unroll
                     for (int j = 0; j < JT; j += 2) {
                         uint32_t a[4];
-                        ldsm(a, k_at + mt * 16 * S::kPitch + j * 16);
+                        ldsm(a, piece_at(k_at, k_turn, mt * 16, j));
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const uint32_t r0 = a[2 * i], r1 = a[2 * i + 1];
@@ -492,7 +623,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
 #pragma unroll
                     for (int j = 0; j < JT; ++j) {
                         uint32_t a[4];
-                        ldsm(a, k_at + mt * 16 * S::kPitch + j * 32);
+                        ldsm(a, piece_at(k_at, k_turn, mt * 16, 2 * j));
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) mma<false>(s[nt][mt], a[0], a[1], a[2], a[3], q[nt][j][0], q[nt][j][1]);
                     }
@@ -500,6 +631,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
             }
             // rows of this tile that count
             const int lo = (p.window && len > p.window ? len - p.window : 0) - tile * kTile, hi = len - tile * kTile;
+            const bool partial = lo > 0 || hi < kTile;
             const float* scales = reinterpret_cast<const float*>(st + S::kScales);
             float vs[MT][2], vl[MT][2];
 #pragma unroll
@@ -507,7 +639,6 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int r = mt * 16 + i * 8 + (lane >> 2);
-                    const bool in = r >= lo && r < hi;
                     float ks = 1.f;
                     vs[mt][i] = 1.f, vl[mt][i] = 0.f;
                     if (S::F8) {
@@ -519,10 +650,33 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
                     for (int nt = 0; nt < NT; ++nt) {
                         float& x = i ? s[nt][mt].z : s[nt][mt].x;
                         float& y = i ? s[nt][mt].w : s[nt][mt].y;
-                        x = in ? x * (q_unit[nt][0] * ks) : -INFINITY;
-                        y = in ? y * (q_unit[nt][1] * ks) : -INFINITY;
+                        x *= q_unit[nt][0] * ks;
+                        y *= q_unit[nt][1] * ks;
                     }
                 }
+            if (partial) {
+                // other rows (of this page, or zeros) have no weight, and no value that a weight of 0 could not stand
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int r = mt * 16 + i * 8 + (lane >> 2);
+                        if (r >= lo && r < hi) continue;
+                        vs[mt][i] = vl[mt][i] = 0.f;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if (i) s[nt][mt].z = s[nt][mt].w = -INFINITY;
+                            else s[nt][mt].x = s[nt][mt].y = -INFINITY;
+                        }
+                    }
+                for (int i = lane; i < S::kRows / 16; i += 32) {
+                    const int r = i * 16 % S::kBlock / S::kBlockRow;
+                    if (r < lo || r >= hi) *reinterpret_cast<uint4*>(st + S::kRows + i * 16) = make_uint4(0, 0, 0, 0);
+                }
+                // (before the copies that come to this stage next)
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+            }
             uint32_t ph[NT][MT][2], pl[NT][MT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -564,15 +718,14 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
                 }
             }
             // O^T += V^T P^T
-            const uint32_t v_at = st_u + kTile * S::kPitch;
+            const uint32_t v_at = st_u + S::kRows + v_base;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 if constexpr (S::F8) {
-                    const uint32_t at = v_at + (mt * 16 + (lane & 15)) * S::kPitch + (lane >> 4) * 16;
 #pragma unroll
                     for (int j = 0; j < JT; j += 2) {
                         uint32_t a[4];
-                        ldsm_t(a, at + j * 16);
+                        ldsm_t(a, piece_at(v_at, v_turn, mt * 16, j));
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             // bytes: row 0's columns 0, 1, row 1's -> column 0 of both rows, column 1 of both
@@ -583,11 +736,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
                         }
                     }
                 } else {
-                    const uint32_t at = v_at + (mt * 16 + (lane & 7) + (lane >> 4) * 8) * S::kPitch + ((lane >> 3) & 1) * 16;
 #pragma unroll
                     for (int j = 0; j < JT; ++j) {
                         uint32_t a[4];
-                        ldsm_t(a, at + j * 32);
+                        ldsm_t(a, piece_at(v_at, v_turn, mt * 16, 2 * j));
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             mma<false>(o[nt][j], a[0], a[1], a[2], a[3], ph[nt][mt][0], ph[nt][mt][1]);
@@ -624,8 +776,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
                     }
                 } else {
                     // what began before this share first, what goes on behind it second
+                    // (in the ring, where no more tiles come)
                     const int which = began ? 1 : 0;
-                    float* part = scratch + which * S::kPart;
+                    float* const part = it + 1 == tiles ? reinterpret_cast<float*>(ring) : p.part + (static_cast<long long>(cta) * S::kWarps + warp) * S::kPart;
+                    __syncwarp();
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -642,18 +796,28 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
                         w.first = seg_first;
                         w.end = seg_first + tiles_of<kTile>(p, len, f);
                         w.b = b, w.vh = vh;
+                        w.part = part;
                     }
                 }
             }
-            stage = stage + 1 == kStages ? 0 : stage + 1;
+            if (++stage == kStages) stage = 0, parity ^= 1;
         }
     }
     __syncthreads();
 
     // ---------------------------------------------------------------- joins
-    const long long cta_from = static_cast<long long>(cta) * S::kWarps * total / warps, cta_to = (static_cast<long long>(cta) + 1) * S::kWarps * total / warps;
-    const float* const cta_scratch = p.part + static_cast<long long>(cta) * S::kWarps * 2 * S::kPart;
-    float* const cta_parts = p.part + static_cast<long long>(gridDim.x) * S::kWarps * 2 * S::kPart;
+    float* const cta_parts = p.part + static_cast<long long>(gridDim.x) * S::kWarps * S::kPart;
+    float* const group_parts = cta_parts + static_cast<long long>(gridDim.x) * 2 * S::kPart;
+    const auto last_of = [&](int* counter, int n) {
+        __syncthreads();
+        if (tid == 0) {
+            const bool last = ptx::atom_add_acq_rel_gpu(counter, 1) == n - 1;
+            if (last) ptx::st_relaxed_gpu(counter, 0);
+            s_last = last;
+        }
+        __syncthreads();
+        return s_last != 0;
+    };
     for (int i = 0; i < 2 * S::kWarps;) {
         const Open seg = s_open[i];
         if (seg.end == 0) {
@@ -672,44 +836,56 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
         i = next;
         const int head0 = seg.vh / per_head * p.group + seg.vh % per_head * S::kHeads;
         const int n_heads = min(S::kHeads, p.group - seg.vh % per_head * S::kHeads);
-        const auto finish = [&](int e, int nt, int j, int ln, float4 o, float l0, float l1) {
-            const float i0 = over<S>(l0), i1 = over<S>(l1);
+        // to: where a joined part goes; null: it is the result
+        const auto put_joined = [&](float* to, int e, float4 o, float2 m, float2 l) {
+            const int ln = e & 31, j = e / 32 % JT, nt = e / 32 / JT, h = nt * 8 + 2 * (ln & 3);
+            const bool stats = j == 0 && ln < 4;
+            if (to) {
+                reinterpret_cast<float4*>(to)[e] = o;
+                if (stats) {
+                    *reinterpret_cast<float2*>(to + S::kFrag * 4 + h) = m;
+                    *reinterpret_cast<float2*>(to + S::kFrag * 4 + S::kHeads + h) = l;
+                }
+                return;
+            }
+            const float i0 = over<S>(l.x), i1 = over<S>(l.y);
             store_one<S>(p, seg.b, head0 + nt * 8, n_heads - nt * 8, j, ln, make_float4(o.x * i0, o.y * i1, o.z * i0, o.w * i1));
+            if (stats && p.lse) {
+                float* lse = p.lse + static_cast<long long>(seg.b) * p.Hq + head0;
+                if (h < n_heads) lse[h] = lse_of<S>(m.x, l.x);
+                if (h + 1 < n_heads) lse[h + 1] = lse_of<S>(m.y, l.y);
+            }
         };
-        const auto finish_stats = [&](int h, float m0, float m1, float l0, float l1) {
-            if (!p.lse) return;
-            float* lse = p.lse + static_cast<long long>(seg.b) * p.Hq + head0;
-            if (h < n_heads) lse[h] = lse_of<S>(m0, l0);
-            if (h + 1 < n_heads) lse[h + 1] = lse_of<S>(m1, l1);
-        };
-        const auto own_part = [&](int k) { return cta_scratch + static_cast<long long>(slot[k]) * S::kPart; };
-        if (seg.first >= cta_from && seg.end <= cta_to) {
-            join<S>(n, own_part, finish, finish_stats);
-            continue;
+        const auto head_of = [](int e) { return e / 32 / JT * 8 + 2 * (e & 3); };
+        const bool whole = seg.first >= cta_from && seg.end <= cta_to;
+        // CTAs c0 .. c1 share the segment; a CTA has two parts at most, the first of
+        // what began before its share or with it
+        const int c0 = whole ? cta : cta_of(total, ctas, seg.first), c1 = whole ? cta : cta_of(total, ctas, seg.end - 1);
+        const int second = seg.first != share_of(total, ctas, c0) ? 1 : 0;      // (of c0)
+        const auto index_of = [&](int c) { return 2 * c + (c == c0 ? second : 0); };
+        float* to = whole ? nullptr : cta_parts + index_of(cta) * static_cast<long long>(S::kPart);
+        for (int e = tid; e < S::kFrag; e += S::kThreads) {
+            float2 m, l;
+            const float4 o = join<S, false>(n, [&](int k) { return s_open[slot[k]].part; }, e, head_of(e), m, l);
+            put_joined(to, e, o, m, l);
         }
-        float* part = cta_parts + (2 * cta + (seg.first <= cta_from ? 0 : 1)) * static_cast<long long>(S::kPart);
-        join<S>(
-            n, own_part, [&](int e, int, int, int, float4 o, float, float) { reinterpret_cast<float4*>(part)[e] = o; },
-            [&](int h, float m0, float m1, float l0, float l1) {
-                *reinterpret_cast<float2*>(part + S::kFrag * 4 + h) = make_float2(m0, m1);
-                *reinterpret_cast<float2*>(part + S::kFrag * 4 + S::kHeads + h) = make_float2(l0, l1);
-            });
-        // the CTA of a tile: the last one whose share begins at it or before
-        const int c0 = static_cast<int>(((seg.first + 1) * ctas - 1) / total), c1 = static_cast<int>((seg.end * ctas - 1) / total);
-        __syncthreads();
-        if (tid == 0) {
-            int* counter = p.counter + c0;
-            const bool last = ptx::atom_add_acq_rel_gpu(counter, 1) == c1 - c0;
-            if (last) ptx::st_relaxed_gpu(counter, 0);
-            s_last = last;
-        }
-        __syncthreads();
-        if (s_last) {
-            const bool whole = seg.first == static_cast<long long>(c0) * S::kWarps * total / warps;
-            const auto part_of = [&](int k) {
-                return cta_parts + (2 * (c0 + k) + (k == 0 && !whole ? 1 : 0)) * static_cast<long long>(S::kPart);
-            };
-            join<S>(c1 - c0 + 1, part_of, finish, finish_stats);
+        // few CTAs: the last joins all; many: the last of each group, and the last of those
+        const bool grouped = c1 - c0 >= kFlat;
+        int level = grouped ? 0 : 1;
+        while (to) {
+            const int g0 = level == 0 ? c0 + (cta - c0) / kGroup * kGroup : c0;
+            const int count = level == 0 ? min(kGroup, c1 + 1 - g0) : grouped ? (c1 - c0) / kGroup + 1 : c1 - c0 + 1;
+            int* const counter = p.counter + (level == 0 ? kMaxGrid + index_of(g0) : c0);
+            if (!last_of(counter, count)) break;
+            const float* const base = level == 1 && grouped ? group_parts : cta_parts;
+            const int step = level == 1 && grouped ? kGroup : 1;
+            to = level == 0 ? group_parts + index_of(g0) * static_cast<long long>(S::kPart) : nullptr;
+            for (int e = tid; e < S::kFrag; e += S::kThreads) {
+                float2 m, l;
+                const float4 o = join<S, true>(count, [&](int k) { return base + index_of(g0 + k * step) * static_cast<long long>(S::kPart); }, e, head_of(e), m, l);
+                put_joined(to, e, o, m, l);
+            }
+            level = 1;
         }
         __syncthreads();
     }
@@ -738,10 +914,19 @@ auto with_shape(int dim, bool e4m3, int group, F f)
 template <class S>
 long long parts_bytes(int num_sms)
 {
-    return 4LL * S::kPart * num_sms * 2 * (S::kWarps + 1);
+    return 4LL * S::kPart * num_sms * (S::kWarps + 4);
 }
 
 }  // namespace
+
+void attn_decode_tile(int dim, bool e4m3, int group, int* rows, int* box_bytes)
+{
+    with_shape(dim, e4m3, group, [&](auto s) {
+        using S = decltype(s);
+        *rows = S::kTile, *box_bytes = S::kBlockRow;
+        return 0;
+    });
+}
 
 long long attn_decode_workspace(int group, int dim, int num_sms)
 {

@@ -2,6 +2,7 @@
 // pages for new tokens, rotary embedding with the cache writes, attention of
 // one new token per request.
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include "ctrl.cuh"
 #include "ops.cuh"
@@ -66,11 +67,20 @@ struct AttnParams {
     int B, Hq, group, width, window;
     float scale_log2;       // scale * log2(e)
     KvCache cache;
+    // boxed: pages are copied in boxes of 64 or 128 bytes of columns x rows of one
+    // head; dimensions of the maps: columns, heads, slots (slots_first: slots,
+    // heads), pages
+    CUtensorMap k_map, v_map;
+    int boxed, slots_first;
+    int pieces_log;         // log2 of the boxes that make the rows of a tile
     float* part;            // workspace
-    int* counter;           // [kMaxGrid], handle-owned, zero between calls
+    int* counter;           // [3 * kMaxGrid], handle-owned, zero between calls
+    long long timeout_ns;
     Ctrl ctrl;
 };
 long long attn_decode_workspace(int group, int dim, int num_sms);
+// Rows of a tile, bytes of a box's columns.
+void attn_decode_tile(int dim, bool e4m3, int group, int* rows, int* box_bytes);
 cudaError_t prepare_attn_decode();
 cudaError_t launch_attn_decode(const AttnParams& p, bool e4m3, int num_sms, cudaStream_t stream, bool pdl);
 

@@ -2,6 +2,7 @@
 // include/tovl.h: argument checks and launches.  None of the calls is a
 // protocol round (the handle's sequence number stays).
 #include <climits>
+#include <cstring>
 #include "ctx.cuh"
 #include "paged.cuh"
 
@@ -46,6 +47,43 @@ int check_cache(const tovl_kv_cache* c, KvCache* out)
 bool valid_rows(const void* p, long long ld, long long width)
 {
     return p && aligned16(p) && ld >= width && ld % 8 == 0;
+}
+
+// Maps of a cache's keys and values for boxes of `rows` slots, where the layout
+// allows them: whole boxes of at least 8 slots in a page (1024 bytes of shared
+// memory, the swizzle's period), strides that nest.  False: rows one by one.
+bool map_cache(tovl_ctx* h, AttnParams* p, bool e4m3)
+{
+    int tile, box_bytes;
+    attn_decode_tile(p->cache.dim, e4m3, p->group, &tile, &box_bytes);
+    int rows = tile;
+    while (rows > 1 && p->cache.page % rows) rows /= 2;
+    if (rows * box_bytes < 1024) return false;
+    if (e4m3 && (!aligned16(p->cache.k_scale) || !aligned16(p->cache.v_scale))) return false;
+    const int size = e4m3 ? 1 : 2;
+    const KvCache& c = p->cache;
+    const cuuint64_t row = static_cast<cuuint64_t>(c.dim) * size;
+    // the dimension with the smaller stride first; extents of 1 take any
+    p->slots_first = c.heads > 1 && c.page > 1 && c.slot_stride < c.head_stride;
+    cuuint64_t n[2] = {static_cast<cuuint64_t>(c.heads), static_cast<cuuint64_t>(c.page)};
+    cuuint64_t step[2] = {static_cast<cuuint64_t>(c.head_stride), static_cast<cuuint64_t>(c.slot_stride)};
+    cuuint32_t in_box[2] = {1, static_cast<cuuint32_t>(rows)};
+    const int a = p->slots_first ? 1 : 0, b = 1 - a;
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.dim), n[a], n[b], static_cast<cuuint64_t>(c.pages)};
+    cuuint64_t strides[3] = {n[a] > 1 ? step[a] : row, 0, 0};
+    strides[1] = n[b] > 1 ? step[b] : strides[0] * n[a];
+    strides[2] = c.pages > 1 ? static_cast<cuuint64_t>(c.page_stride) : strides[1] * n[b];
+    if (strides[1] % strides[0] || strides[2] % strides[1] || strides[2] >> 40) return false;
+    cuuint32_t box[4] = {static_cast<cuuint32_t>(box_bytes / size), in_box[a], in_box[b], 1};
+    cuuint32_t every[4] = {1, 1, 1, 1};
+    const auto encode = [&](CUtensorMap* map, void* base) {
+        return h->encode(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, every,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                         CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    if (!encode(&p->k_map, c.k) || !encode(&p->v_map, c.v)) return false;
+    while (rows << p->pieces_log < tile) ++p->pieces_log;
+    return true;
 }
 
 }  // namespace
@@ -141,7 +179,8 @@ TOVL_API int tovl_attn_decode(tovl_handle h, const void* q, long long ldq, int B
                               void* out, long long ldo, float* lse, void* workspace, long long workspace_bytes, void* stream)
 {
     if (!h) return TOVL_ERR_INVALID;
-    AttnParams p = {};
+    AttnParams p;
+    std::memset(&p, 0, sizeof p);
     const int rc = check_cache(cache, &p.cache);
     if (rc != TOVL_OK) return rc;
     if (B < 0 || Hq < 1 || Hq % p.cache.heads || width < 1 || window < 0) return TOVL_ERR_INVALID;
@@ -168,8 +207,10 @@ TOVL_API int tovl_attn_decode(tovl_handle h, const void* q, long long ldq, int B
     p.scale_log2 = scale * 1.44269504088896340736f;
     p.part = static_cast<float*>(workspace);
     p.counter = h->sync_words + kAttnWord;
+    p.timeout_ns = 4 * h->timeout_ns + 100000000LL;
     p.ctrl = h->ctrl;
     DeviceGuard g(h->device);
+    p.boxed = map_cache(h, &p, cache->type == TOVL_E4M3);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     return run(h, s, "attention launch",
                [&](bool pdl) { return launch_attn_decode(p, cache->type == TOVL_E4M3, h->num_sms, s, pdl); });

@@ -23,9 +23,20 @@ def lib(tmp_path_factory):
                    "cudaError_t launch_page_plan(const PagePlanParams&, int, cudaStream_t, bool) { ++launches; return cudaSuccess; }\n"
                    "cudaError_t launch_rope_append(const RopeParams&, bool, int, cudaStream_t, bool) { ++launches; return cudaSuccess; }\n"
                    "cudaError_t launch_attn_decode(const AttnParams&, bool, int, cudaStream_t, bool) { ++launches; return cudaSuccess; }\n"
+                   "void attn_decode_tile(int, bool, int, int* rows, int* box_bytes) { *rows = 16; *box_bytes = 128; }\n"
                    "long long attn_decode_workspace(int, int, int) { return 4096; }\n"
                    "}\n"
-                   'TOVL_API void* make() { auto* h = new tovl_ctx(); h->num_sms = 152; return h; }\n'
+                   "static long long maps[16];      // of the last map: dims, strides, box, how many\n"
+                   "static CUresult encode(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t* dims, const cuuint64_t* strides,\n"
+                   "                       const cuuint32_t* box, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,\n"
+                   "                       CUtensorMapFloatOOBfill)\n"
+                   "{\n"
+                   "    for (int i = 0; i < 4; ++i) maps[i] = dims[i], maps[4 + i] = i < 3 ? strides[i] : 0, maps[8 + i] = box[i];\n"
+                   "    ++maps[12];\n"
+                   "    return CUDA_SUCCESS;\n"
+                   "}\n"
+                   'TOVL_API void* make() { auto* h = new tovl_ctx(); h->num_sms = 152; h->encode = encode; maps[12] = 0; return h; }\n'
+                   'TOVL_API const long long* last_map() { return maps; }\n'
                    'TOVL_API int count() { return launches; }\n')
     so = at / "paged.so"
     subprocess.run([tovl_build._nvcc(), *tovl_build._flags(), "-shared", "-cudart", "shared", "-o", str(so), str(src)], check=True,
@@ -34,6 +45,7 @@ def lib(tmp_path_factory):
     for n in NAMES + ("tovl_attn_decode_workspace",):
         getattr(lib, n).argtypes, getattr(lib, n).restype = tovl.SIGNATURES[n]
     lib.make.restype = ctypes.c_void_p
+    lib.last_map.restype = ctypes.POINTER(ctypes.c_longlong)
     return lib
 
 
@@ -93,6 +105,25 @@ def test_null_and_misaligned_pointers_are_refused(lib, name, base):
         if k != "lse":
             assert call(lib, name, base, **{k: None}) == (INVALID, 0), k
         assert call(lib, name, base, **{k: P + 2}) == (INVALID, 0), k
+
+
+def test_caches_are_mapped_in_boxes_where_their_layout_allows_it(lib):
+    """Dimensions of a map: columns, the smaller of head and slot stride, the larger, pages; every stride a multiple of
+    the one before.  Boxes lie in one page and have 8 rows at least."""
+    def mapped(**c):
+        assert call(lib, "tovl_attn_decode", ATTN, cache=c, Hq=4 * c.get("heads", 2), ldq=4096, ldo=4096) == (OK, 1)
+        m = lib.last_map()
+        return None if m[12] == 0 else (list(m[0:4]), list(m[4:7]), list(m[8:12]))
+
+    assert mapped() == ([64, 2, 16, 9], [128, 256, 4096], [64, 1, 16, 1])
+    assert mapped(head_stride=1024, slot_stride=64) == ([64, 16, 2, 9], [128, 2048, 4096], [64, 16, 1, 1])      # heads first
+    assert mapped(page=24, page_stride=24 * 128) == ([64, 2, 24, 9], [128, 256, 24 * 256], [64, 1, 8, 1])
+    assert mapped(page=64, page_stride=2 * 64 * 128) == ([64, 2, 64, 9], [128, 256, 4 * 64 * 128], [64, 1, 16, 1])
+    assert mapped(heads=1, head_stride=5, slot_stride=64, page_stride=1024) == ([64, 1, 16, 9], [128, 128, 2048], [64, 1, 16, 1])
+    assert mapped(pages=1, page_stride=3) == ([64, 2, 16, 1], [128, 256, 4096], [64, 1, 16, 1])
+    for c in (dict(page=4, page_stride=512), dict(page=1, page_stride=128), dict(page=20, page_stride=2560), dict(page=1000 // 8 * 8 + 4, page_stride=1 << 20),
+              dict(slot_stride=136, page_stride=136 * 16), dict(page_stride=2056), dict(head_stride=72, slot_stride=160)):
+        assert mapped(**c) is None, c
 
 
 def test_plan_refusals(lib):
