@@ -70,7 +70,7 @@ struct Shape {
 struct Open {
     long long first, end;      // its tiles in the order of the call; end == 0: none
     const float* part;
-    int b, vh;
+    int b, head0, n_heads;     // its request and query heads
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes)
@@ -207,12 +207,13 @@ __device__ __forceinline__ int length_of(const AttnParams& p, int b)
     return len < 0 ? 0 : len > most ? static_cast<int>(most) : len;
 }
 
-// A place in the order of the call: request, block of heads, tile.
+// A place in the order of the call: request, key head, block of its query
+// heads, tile.
 template <class S>
 struct Cursor {
     long long left;            // tiles of the share from here on
     long long at;              // linear tile
-    int b, vh, tile;
+    int b, head, block, tile;
     int len, first, count;     // of the request
 
     __device__ __forceinline__ void enter(const AttnParams& p)
@@ -220,17 +221,20 @@ struct Cursor {
         len = length_of(p, b);
         count = tiles_of<S::kTile>(p, len, first);
     }
-    __device__ __forceinline__ void next(const AttnParams& p, int heads)
+    __device__ __forceinline__ void next(const AttnParams& p, int per_head)
     {
         --left;
         ++at;
         if (++tile < first + count || left == 0) return;
-        if (++vh == heads) {
-            vh = 0;
-            do {
-                ++b;
-                enter(p);
-            } while (count == 0);       // (a share ends at the last request with tiles)
+        if (++block == per_head) {
+            block = 0;
+            if (++head == p.cache.heads) {
+                head = 0;
+                do {
+                    ++b;
+                    enter(p);
+                } while (count == 0);       // (a share ends at the last request with tiles)
+            }
         }
         tile = first;
     }
@@ -240,35 +244,38 @@ struct Cursor {
 template <class S>
 __device__ __forceinline__ float over(float l)
 {
-    return l == 0.f ? 0.f : (S::F8 ? 0x1p40f : 1.f) / l;
+    return l == 0.f ? 0.f : __fdividef(S::F8 ? 0x1p40f : 1.f, l);
 }
 
-// Column c (0 .. 3 of a float4) of the fragment block j of lane `lane` is
-// element dim_of(), head 2 (lane % 4) + (c & 1).
-template <bool F8>
-__device__ __forceinline__ int dim_of(int j, int lane, int c)
-{
-    const int g = lane >> 2;
-    return 16 * j + (F8 ? 2 * g + (c >> 1) : g + 8 * (c >> 1));
-}
-
-// out and lse of one float4 of a segment's result
+// Stores float4 j of a lane's O^T, times i0 and i1 (its two heads'): rows of out
+// from `out` on.  x and z are of head 2 (lane % 4), y and w of the next; x and y of
+// one column, z and w of the next (e4m3) or the eighth after it, whose lanes
+// exchange numbers for pairs of columns.  All lanes of a warp.
 template <class S>
-__device__ __forceinline__ void store_one(const AttnParams& p, int b, int head0, int heads, int j, int lane, float4 o)
+__device__ __forceinline__ void store_pair(__nv_bfloat16* out, int dim, int heads, int j, int lane, float4 o, float i0, float i1)
 {
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + b * p.ldo;
-    const float v[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const int d = dim_of<S::F8>(j, lane, c), h = 2 * (lane & 3) + (c & 1);
-        if (h < heads && d < p.cache.dim) out[static_cast<long long>(head0 + h) * p.cache.dim + d] = __float2bfloat16(v[c]);
+    const int g = lane >> 2, h = 2 * (lane & 3);
+    if constexpr (S::F8) {
+        const int d = 16 * j + 2 * g;
+        if (d >= dim) return;
+        if (h < heads) *reinterpret_cast<uint32_t*>(out + h * dim + d) = ptx::pack_bf16x2(o.x * i0, o.z * i0);
+        if (h + 1 < heads) *reinterpret_cast<uint32_t*>(out + (h + 1) * dim + d) = ptx::pack_bf16x2(o.y * i1, o.w * i1);
+    } else {
+        const bool odd = g & 1;
+        const uint32_t a = ptx::pack_bf16x2(o.x * i0, o.z * i0), b = ptx::pack_bf16x2(o.y * i1, o.w * i1);
+        const uint32_t mine = odd ? b : a, other = __shfl_xor_sync(0xffffffffu, odd ? a : b, 4);
+        const int d = 16 * j + (g & ~1), row = h + (odd ? 1 : 0);
+        if (row >= heads) return;
+        out += row * dim + d;
+        if (d < dim) *reinterpret_cast<uint32_t*>(out) = odd ? __byte_perm(other, mine, 0x5410) : __byte_perm(mine, other, 0x5410);
+        if (d + 8 < dim) *reinterpret_cast<uint32_t*>(out + 8) = odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x7632);
     }
 }
 
 template <class S>
 __device__ __forceinline__ float lse_of(float m, float l)
 {
-    return l > 0.f || l != l ? (m + log2f(l) - (S::F8 ? kShift : 0.f)) * 0.693147180559945309f : -INFINITY;
+    return l == 0.f ? -INFINITY : (m + lg2(l) - (S::F8 ? kShift : 0.f)) * 0.693147180559945309f;
 }
 
 // Element e of the joined parts of one segment, with the statistics of its two
@@ -334,9 +341,9 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
     __shared__ uint64_t s_full[S::kWarps][S::kStages];
     __shared__ int4 s_meta[S::kWarps][S::kStages];
     __shared__ long long s_sum[S::kWarps];
-    __shared__ Cursor<S> s_start[S::kWarps];
+    __shared__ long long s_before[S::kThreads];
     __shared__ Open s_open[S::kWarps * 2];
-    __shared__ int s_last;
+    __shared__ int s_last[2];
     constexpr int kTile = S::kTile, NT = S::NT, JT = S::JT, MT = S::MT, kStages = S::kStages, CB = S::CB;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -354,11 +361,13 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
     const int per_head = (p.group + S::kHeads - 1) / S::kHeads, heads = p.cache.heads * per_head;
     const int chunk = (p.B + S::kThreads - 1) / S::kThreads, b0 = tid * chunk;
     long long sum = 0;
+    bool none = false;
     for (int b = b0; b < min(p.B, b0 + chunk); ++b) {
         const int len = __ldg(p.length + b);
         int first;
         if (len < 0 || len > static_cast<long long>(p.width) * p.cache.page) record_error(p.ctrl, kErrInvalid);
         sum += tiles_of<kTile>(p, length_of(p, b), first);
+        none |= len <= 0;
     }
     long long before = sum;                  // inclusive prefix
 #pragma unroll
@@ -367,7 +376,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
         if (lane >= d) before += o;
     }
     if (lane == 31) s_sum[warp] = before;
-    __syncthreads();
+    none = __syncthreads_or(none);
     long long total = 0;
 #pragma unroll
     for (int w = 0; w < S::kWarps; ++w) {
@@ -381,7 +390,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
     const int cta = blockIdx.x;
     const int ctas = static_cast<int>(min((total + S::kWarps - 1) / S::kWarps, static_cast<long long>(gridDim.x)));
     // requests without tokens: nothing of theirs is in the order
-    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    for (int b = blockIdx.x; none && b < p.B; b += gridDim.x) {
         if (__ldg(p.length + b) > 0) continue;
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + b * p.ldo;
         for (int i = tid; i < p.Hq * p.cache.dim; i += S::kThreads) out[i] = __float2bfloat16(0.f);
@@ -390,36 +399,34 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
     }
     if (cta >= ctas) return;
     const long long cta_from = share_of(total, ctas, cta), cta_to = share_of(total, ctas, cta + 1);
-    if (cta_from < before + sum && cta_to > before) {
-        // the warps' shares that begin in this thread's requests
-        for (int w = 0; w < S::kWarps; ++w) {
-            const long long from = cta_from + (cta_to - cta_from) * w / S::kWarps, to = cta_from + (cta_to - cta_from) * (w + 1) / S::kWarps;
-            if (from < before || from >= before + sum) continue;
-            Cursor<S> c;
-            c.left = to - from;
-            c.at = from;
-            long long r = from - before;
-            for (c.b = b0;; ++c.b) {
-                c.enter(p);
-                if (r < static_cast<long long>(c.count) * heads) break;
-                r -= static_cast<long long>(c.count) * heads;
-            }
-            if (r < (1LL << 31)) {
-                c.vh = static_cast<int>(static_cast<unsigned>(r) / static_cast<unsigned>(c.count));
-            } else {
-                c.vh = static_cast<int>(r / c.count);
-            }
-            c.tile = c.first + static_cast<int>(r - static_cast<long long>(c.vh) * c.count);
-            s_start[w] = c;
-        }
-    }
+    s_before[tid] = before;
     __syncthreads();
+
+    // this warp's share: the last thread's requests that begin at its first tile or before
+    Cursor<S> put;
+    {
+        const long long share = cta_to - cta_from, from = cta_from + share * warp / S::kWarps;
+        put.left = cta_from + share * (warp + 1) / S::kWarps - from;
+        put.at = from;
+        constexpr int kPer = S::kThreads / 32;
+        const int coarse = __popc(__ballot_sync(0xffffffffu, s_before[lane * kPer] <= from)) - 1;
+        const int at = coarse * kPer + __popc(__ballot_sync(0xffffffffu, lane < kPer && s_before[coarse * kPer + min(lane, kPer - 1)] <= from)) - 1;
+        long long r = from - s_before[at];
+        for (put.b = at * chunk;; ++put.b) {
+            put.enter(p);
+            if (r < static_cast<long long>(put.count) * heads) break;
+            r -= static_cast<long long>(put.count) * heads;
+        }
+        const int vh = r < (1LL << 31) ? static_cast<int>(static_cast<unsigned>(r) / static_cast<unsigned>(put.count)) : static_cast<int>(r / put.count);
+        put.head = per_head == 1 ? vh : vh / per_head;
+        put.block = vh - put.head * per_head;
+        put.tile = put.first + static_cast<int>(r - static_cast<long long>(vh) * put.count);
+    }
 
     // ---------------------------------------------------------------- a warp's stream
     uint8_t* const ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023)) + warp * S::kRing;
     const uint32_t ring_u = ptx::smem_u32(ring);
-    Cursor<S> put = s_start[warp];
-    const long long tiles = put.left;
+    const long long tiles = put.left, warp_from = put.at;
     const auto page_of = [&](int t) {
         return p.cache.page_shift >= 0 ? t >> p.cache.page_shift : static_cast<int>(static_cast<unsigned>(t) / static_cast<unsigned>(p.cache.page));
     };
@@ -449,10 +456,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
     const auto fetch = [&](int stage) {
         if (put.left > 0) {
             const uint32_t dst = ring_u + stage * S::kStage;
-            const int head = put.vh / per_head;
+            const int head = put.head;
             if (lane == 0) {
                 const int last = put.first + put.count - 1;
-                s_meta[warp][stage] = make_int4(put.b, put.vh, put.tile | (put.tile == put.first ? 1 << 30 : 0) | (put.tile == last ? 1 << 31 : 0), put.len);
+                s_meta[warp][stage] = make_int4(put.b, put.head | put.block << 16, put.tile | (put.tile == put.first ? 1 << 30 : 0) | (put.tile == last ? 1 << 31 : 0), put.len);
             }
             if (page_id[0] == -2 || page_id[kOwn - 1] == -2) record_error(p.ctrl, kErrInvalid);
             if (p.boxed) {
@@ -500,13 +507,14 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
                     cp_async16(at + S::kRows, p.cache.v + src, in ? 16 : 0);
                 }
             }
-            put.next(p, heads);
+            put.next(p, per_head);
             find_pages();
         }
         cp_commit();
     };
     if (tiles > 0) {
         find_pages();
+#pragma unroll 1
         for (int s = 0; s < kStages - 1; ++s) fetch(s);
         // fragments of k: row lane % 16, 16 bytes lane / 16; of v: the same (e4m3),
         // or row lane % 8 + 8 (lane / 16), 16 bytes lane / 8 % 2
@@ -526,33 +534,17 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
         int stage = 0;
         uint32_t parity = 0;
         for (long long it = 0; it < tiles; ++it) {
-            if (p.boxed) {
-                if (!wait_full(&s_full[warp][stage], parity, p)) {
-                    // the other copies in flight, then out
-                    for (int s = 1; s < kStages - 1 && it + s < tiles; ++s) {
-                        if (++stage == kStages) stage = 0, parity ^= 1;
-                        wait_full(&s_full[warp][stage], parity, p);
-                    }
-                    break;
-                }
-            } else {
-                cp_wait<kStages - 2>();
-            }
             __syncwarp();
-            fetch(stage == 0 ? kStages - 1 : stage - 1);
-            uint8_t* const st = ring + stage * S::kStage;
-            const uint32_t st_u = ring_u + stage * S::kStage;
             const int4 meta = s_meta[warp][stage];
-            const int b = meta.x, vh = meta.y, tile = meta.z & 0x3fffffff, len = meta.w;
-            const int head0 = vh / per_head * p.group + vh % per_head * S::kHeads;
-            const int n_heads = min(S::kHeads, p.group - vh % per_head * S::kHeads);
+            const int b = meta.x, tile = meta.z & 0x3fffffff, len = meta.w;
+            const int block = meta.y >> 16, head0 = (meta.y & 0xffff) * p.group + block * S::kHeads, n_heads = min(S::kHeads, p.group - block * S::kHeads);
             if (fresh) {
                 // the segment's queries
                 fresh = false;
                 began = meta.z & (1 << 30);
                 int f;
                 tiles_of<kTile>(p, len, f);
-                seg_first = s_start[warp].at + it - (tile - f);
+                seg_first = warp_from + it - (tile - f);
                 const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(p.q) + b * p.ldq;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -596,6 +588,22 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
                     for (int j = 0; j < JT; ++j) o[nt][j] = make_float4(0.f, 0.f, 0.f, 0.f);
                 }
             }
+            if (p.boxed) {
+                if (!wait_full(&s_full[warp][stage], parity, p)) {
+                    // the other copies in flight, then out
+                    for (int s = 1; s < kStages - 1 && it + s < tiles; ++s) {
+                        if (++stage == kStages) stage = 0, parity ^= 1;
+                        wait_full(&s_full[warp][stage], parity, p);
+                    }
+                    break;
+                }
+            } else {
+                cp_wait<kStages - 2>();
+            }
+            __syncwarp();
+            fetch(stage == 0 ? kStages - 1 : stage - 1);
+            uint8_t* const st = ring + stage * S::kStage;
+            const uint32_t st_u = ring_u + stage * S::kStage;
 
             // scores: rows lane / 4 and + 8 of each 16, heads 2 (lane % 4) and + 1
             float4 s[NT][MT];
@@ -762,11 +770,9 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         const float i0 = over<S>(l[nt][0]), i1 = over<S>(l[nt][1]);
+                        __nv_bfloat16* const row = static_cast<__nv_bfloat16*>(p.out) + b * p.ldo + static_cast<long long>(head0 + nt * 8) * p.cache.dim;
 #pragma unroll
-                        for (int j = 0; j < JT; ++j) {
-                            const float4 v = o[nt][j];
-                            store_one<S>(p, b, head0 + nt * 8, n_heads - nt * 8, j, lane, make_float4(v.x * i0, v.y * i1, v.z * i0, v.w * i1));
-                        }
+                        for (int j = 0; j < JT; ++j) store_pair<S>(row, p.cache.dim, n_heads - nt * 8, j, lane, o[nt][j], i0, i1);
                         const int h = nt * 8 + 2 * (lane & 3);
                         if (p.lse && lane < 4) {
                             float* lse = p.lse + static_cast<long long>(b) * p.Hq + head0;
@@ -795,7 +801,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
                         Open& w = s_open[warp * 2 + which];
                         w.first = seg_first;
                         w.end = seg_first + tiles_of<kTile>(p, len, f);
-                        w.b = b, w.vh = vh;
+                        w.b = b, w.head0 = head0, w.n_heads = n_heads;
                         w.part = part;
                     }
                 }
@@ -808,86 +814,130 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
     // ---------------------------------------------------------------- joins
     float* const cta_parts = p.part + static_cast<long long>(gridDim.x) * S::kWarps * S::kPart;
     float* const group_parts = cta_parts + static_cast<long long>(gridDim.x) * 2 * S::kPart;
-    const auto last_of = [&](int* counter, int n) {
-        __syncthreads();
-        if (tid == 0) {
-            const bool last = ptx::atom_add_acq_rel_gpu(counter, 1) == n - 1;
-            if (last) ptx::st_relaxed_gpu(counter, 0);
-            s_last = last;
+    // the warps' open slots, a lane each; those of one segment follow one another
+    const Open mine = s_open[min(lane, 2 * S::kWarps - 1)];
+    const bool any = lane < 2 * S::kWarps && mine.end != 0;
+    const uint32_t open = __ballot_sync(0xffffffffu, any), lower = open & ((1u << lane) - 1);
+    const long long previous = __shfl_sync(0xffffffffu, mine.first, lower ? 31 - __clz(lower) : 0);
+    const bool leads = any && (!lower || previous != mine.first);
+    const uint32_t leaders = __ballot_sync(0xffffffffu, leads);
+    const uint32_t inside = __ballot_sync(0xffffffffu, leads && mine.first >= cta_from && mine.end <= cta_to);
+
+    // what a thread does with its share of a segment's join; to: where a joined part
+    // goes, null: it is the result
+    const auto put_joined = [&](const Open& seg, float* to, int e, float4 o, float2 m, float2 l) {
+        const int ln = e & 31, j = e / 32 % JT, nt = e / 32 / JT, h = nt * 8 + 2 * (ln & 3);
+        const bool stats = j == 0 && ln < 4;
+        if (to) {
+            reinterpret_cast<float4*>(to)[e] = o;
+            if (stats) {
+                *reinterpret_cast<float2*>(to + S::kFrag * 4 + h) = m;
+                *reinterpret_cast<float2*>(to + S::kFrag * 4 + S::kHeads + h) = l;
+            }
+            return;
         }
-        __syncthreads();
-        return s_last != 0;
+        const int head0 = seg.head0, n_heads = seg.n_heads;
+        store_pair<S>(static_cast<__nv_bfloat16*>(p.out) + seg.b * p.ldo + static_cast<long long>(head0 + nt * 8) * p.cache.dim, p.cache.dim,
+                      n_heads - nt * 8, j, ln, o, over<S>(l.x), over<S>(l.y));
+        if (stats && p.lse) {
+            float* lse = p.lse + static_cast<long long>(seg.b) * p.Hq + head0;
+            if (h < n_heads) lse[h] = lse_of<S>(m.x, l.x);
+            if (h + 1 < n_heads) lse[h + 1] = lse_of<S>(m.y, l.y);
+        }
     };
-    for (int i = 0; i < 2 * S::kWarps;) {
-        const Open seg = s_open[i];
-        if (seg.end == 0) {
-            ++i;
-            continue;
-        }
-        // its parts: this CTA's open slots that follow with the same segment
-        int n = 1, next = i + 1, slot[S::kWarps];
-        slot[0] = i;
-        for (; next < 2 * S::kWarps; ++next) {
-            const Open& w = s_open[next];
-            if (w.end == 0) continue;
-            if (w.first != seg.first) break;
-            slot[n++] = next;
-        }
-        i = next;
-        const int head0 = seg.vh / per_head * p.group + seg.vh % per_head * S::kHeads;
-        const int n_heads = min(S::kHeads, p.group - seg.vh % per_head * S::kHeads);
-        // to: where a joined part goes; null: it is the result
-        const auto put_joined = [&](float* to, int e, float4 o, float2 m, float2 l) {
-            const int ln = e & 31, j = e / 32 % JT, nt = e / 32 / JT, h = nt * 8 + 2 * (ln & 3);
-            const bool stats = j == 0 && ln < 4;
-            if (to) {
-                reinterpret_cast<float4*>(to)[e] = o;
-                if (stats) {
-                    *reinterpret_cast<float2*>(to + S::kFrag * 4 + h) = m;
-                    *reinterpret_cast<float2*>(to + S::kFrag * 4 + S::kHeads + h) = l;
-                }
-                return;
-            }
-            const float i0 = over<S>(l.x), i1 = over<S>(l.y);
-            store_one<S>(p, seg.b, head0 + nt * 8, n_heads - nt * 8, j, ln, make_float4(o.x * i0, o.y * i1, o.z * i0, o.w * i1));
-            if (stats && p.lse) {
-                float* lse = p.lse + static_cast<long long>(seg.b) * p.Hq + head0;
-                if (h < n_heads) lse[h] = lse_of<S>(m.x, l.x);
-                if (h + 1 < n_heads) lse[h + 1] = lse_of<S>(m.y, l.y);
-            }
-        };
-        const auto head_of = [](int e) { return e / 32 / JT * 8 + 2 * (e & 3); };
-        const bool whole = seg.first >= cta_from && seg.end <= cta_to;
-        // CTAs c0 .. c1 share the segment; a CTA has two parts at most, the first of
-        // what began before its share or with it
-        const int c0 = whole ? cta : cta_of(total, ctas, seg.first), c1 = whole ? cta : cta_of(total, ctas, seg.end - 1);
-        const int second = seg.first != share_of(total, ctas, c0) ? 1 : 0;      // (of c0)
-        const auto index_of = [&](int c) { return 2 * c + (c == c0 ? second : 0); };
-        float* to = whole ? nullptr : cta_parts + index_of(cta) * static_cast<long long>(S::kPart);
-        for (int e = tid; e < S::kFrag; e += S::kThreads) {
+    const auto head_of = [](int e) { return e / 32 / JT * 8 + 2 * (e & 3); };
+    // this CTA's parts of the segment that slot `lead` leads
+    const auto join_own = [&](int lead, float* to, int first, int step) {
+        const Open& seg = s_open[lead];
+        const uint32_t next = leaders & ~((2u << lead) - 1);
+        const uint32_t slots = open & ~((1u << lead) - 1) & (next ? (next & -next) - 1 : 0xffffffffu);
+        for (int e = first; e < S::kFrag; e += step) {
             float2 m, l;
-            const float4 o = join<S, false>(n, [&](int k) { return s_open[slot[k]].part; }, e, head_of(e), m, l);
-            put_joined(to, e, o, m, l);
+            uint32_t left = slots;
+            const float4 o = join<S, false>(__popc(slots), [&](int) {
+                const float* part = s_open[__ffs(left) - 1].part;
+                left &= left - 1;
+                return part;
+            }, e, head_of(e), m, l);
+            put_joined(seg, to, e, o, m, l);
         }
-        // few CTAs: the last joins all; many: the last of each group, and the last of those
-        const bool grouped = c1 - c0 >= kFlat;
-        int level = grouped ? 0 : 1;
-        while (to) {
-            const int g0 = level == 0 ? c0 + (cta - c0) / kGroup * kGroup : c0;
-            const int count = level == 0 ? min(kGroup, c1 + 1 - g0) : grouped ? (c1 - c0) / kGroup + 1 : c1 - c0 + 1;
-            int* const counter = p.counter + (level == 0 ? kMaxGrid + index_of(g0) : c0);
-            if (!last_of(counter, count)) break;
+    };
+    // segments inside this CTA's share: shared out to its warps
+    if (inside) {
+        const int count = __popc(inside), teams = min(count, S::kWarps), team = warp % teams, mates = (S::kWarps - team + teams - 1) / teams;
+        uint32_t left = inside;
+        for (int k = 0; left; ++k, left &= left - 1)
+            if (k % teams == team) join_own(__ffs(left) - 1, nullptr, warp / teams * 32 + lane, mates * 32);
+    }
+    // segments that other CTAs share, two at most: CTAs c0 .. c1.  The first of a
+    // CTA's two parts is of what began before its share or with it.
+    uint32_t shared = leaders & ~inside;
+    if (!shared) return;
+    struct Shared {
+        int lead, c0, c1, second, level;
+    } segs[2];
+    const int n_shared = __popc(shared);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if (i >= n_shared) continue;
+        Shared& s = segs[i];
+        s.lead = __ffs(shared) - 1;
+        shared &= shared - 1;
+        const Open& seg = s_open[s.lead];
+        s.c0 = cta_of(total, ctas, seg.first), s.c1 = cta_of(total, ctas, seg.end - 1);
+        s.second = seg.first != share_of(total, ctas, s.c0) ? 1 : 0;      // (of c0)
+        s.level = s.c1 - s.c0 >= kFlat ? 0 : 1;
+        join_own(s.lead, cta_parts + (2 * cta + (cta == s.c0 ? s.second : 0)) * static_cast<long long>(S::kPart), tid, S::kThreads);
+    }
+    // few CTAs: the last joins all; many: the last of each group, and the last of those
+    for (int round = 0; round < 2; ++round) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (tid != 32 * i) continue;
+            s_last[i] = 0;
+            if (i >= n_shared || segs[i].level < 0) continue;
+            const Shared& s = segs[i];
+            const int g0 = s.c0 + (cta - s.c0) / kGroup * kGroup;
+            int* counter = p.counter + s.c0;
+            int count = s.c1 - s.c0 + 1;
+            if (s.level == 0) {
+                counter = p.counter + kMaxGrid + 2 * g0 + (g0 == s.c0 ? s.second : 0);
+                count = min(kGroup, s.c1 + 1 - g0);
+            } else if (count > kFlat) {
+                count = (count + kGroup - 1) / kGroup;
+            }
+            const bool last = ptx::atom_add_acq_rel_gpu(counter, 1) == count - 1;
+            if (last) ptx::st_relaxed_gpu(counter, 0);
+            s_last[i] = last;
+        }
+        __syncthreads();
+        bool more = false;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (i >= n_shared) continue;
+            Shared& s = segs[i];
+            const int level = s.level;
+            s.level = -1;
+            if (!s_last[i]) continue;
+            const bool grouped = s.c1 - s.c0 >= kFlat;
+            const int g0 = level == 0 ? s.c0 + (cta - s.c0) / kGroup * kGroup : s.c0;
+            const int count = level == 0 ? min(kGroup, s.c1 + 1 - g0) : grouped ? (s.c1 - s.c0) / kGroup + 1 : s.c1 - s.c0 + 1;
             const float* const base = level == 1 && grouped ? group_parts : cta_parts;
             const int step = level == 1 && grouped ? kGroup : 1;
-            to = level == 0 ? group_parts + index_of(g0) * static_cast<long long>(S::kPart) : nullptr;
+            const auto part = [&](int k) {
+                const int c = g0 + k * step;
+                return base + (2 * c + (c == s.c0 ? s.second : 0)) * static_cast<long long>(S::kPart);
+            };
+            float* const to = level == 0 ? group_parts + (2 * g0 + (g0 == s.c0 ? s.second : 0)) * static_cast<long long>(S::kPart) : nullptr;
             for (int e = tid; e < S::kFrag; e += S::kThreads) {
                 float2 m, l;
-                const float4 o = join<S, true>(count, [&](int k) { return base + index_of(g0 + k * step) * static_cast<long long>(S::kPart); }, e, head_of(e), m, l);
-                put_joined(to, e, o, m, l);
+                const float4 o = join<S, true>(count, part, e, head_of(e), m, l);
+                put_joined(s_open[s.lead], to, e, o, m, l);
             }
-            level = 1;
+            if (level == 0) s.level = 1, more = true;
         }
-        __syncthreads();
+        if (!more) break;
     }
 }
 
