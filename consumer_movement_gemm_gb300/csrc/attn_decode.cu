@@ -49,14 +49,15 @@ struct Shape {
     static constexpr int kRows = CB * kBlock;      // all of k or of v
     static constexpr int MT = kTile / 16;
     static constexpr int JT = DP / 16;             // blocks of 16 columns
-    static constexpr int kScales = 2 * kRows;      // offset in a stage
-    static constexpr int kStage = 2 * kRows + (F8 ? 1024 : 0);
-    static constexpr int kWarps = kRow > 256 ? 6 : 8;
-    static constexpr int kFit = (222 * 1024) / (kWarps * kStage);
+    static constexpr int kStage = 2 * kRows;
+    static constexpr int kScaleStage = F8 ? 2 * kTile * 4 : 0;
+    static constexpr int kWarps = kRow > 256 ? 6 : NT == 1 ? 12 : 8;
+    static constexpr int kFit = (222 * 1024) / (kWarps * (kStage + kScaleStage));
     static constexpr int kStages = kFit > 4 ? 4 : kFit;
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kRing = kStages * kStage;
-    static constexpr int kSmem = kWarps * kRing + 1024;
+    static constexpr int kScales = kStages * kScaleStage;               // of a warp, behind all rings
+    static constexpr int kSmem = kWarps * (kRing + kScales) + 1024;
     static constexpr int kFrag = NT * JT * 32;     // float4 of one O
     static constexpr int kPart = kFrag * 4 + 2 * kHeads;               // floats of a part: O, m, sum
     // the 16-byte pieces of row r of a block are exchanged by XOR with this
@@ -71,6 +72,7 @@ struct Open {
     long long first, end;      // its tiles in the order of the call; end == 0: none
     const float* part;
     int b, head0, n_heads;     // its request and query heads
+    int beside;                // which of the heads that go together
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes)
@@ -213,7 +215,7 @@ template <class S>
 struct Cursor {
     long long left;            // tiles of the share from here on
     long long at;              // linear tile
-    int b, head, block, tile;
+    int b, vh, head, block, tile;
     int len, first, count;     // of the request
 
     __device__ __forceinline__ void enter(const AttnParams& p)
@@ -221,20 +223,27 @@ struct Cursor {
         len = length_of(p, b);
         count = tiles_of<S::kTile>(p, len, first);
     }
-    __device__ __forceinline__ void next(const AttnParams& p, int per_head)
+    __device__ __forceinline__ void at_head(int v, int per_head)
+    {
+        vh = v;
+        head = per_head == 1 ? v : v / per_head;
+        block = v - head * per_head;
+    }
+    // together: blocks of heads that neighbouring warps take side by side
+    __device__ __forceinline__ void next(const AttnParams& p, int per_head, int together)
     {
         --left;
         ++at;
         if (++tile < first + count || left == 0) return;
-        if (++block == per_head) {
-            block = 0;
-            if (++head == p.cache.heads) {
-                head = 0;
-                do {
-                    ++b;
-                    enter(p);
-                } while (count == 0);       // (a share ends at the last request with tiles)
-            }
+        const int heads = p.cache.heads * per_head, v = vh + together;
+        if (v >= heads) {
+            at_head(v - heads, per_head);
+            do {
+                ++b;
+                enter(p);
+            } while (count == 0);       // (a share ends at the last request with tiles)
+        } else {
+            at_head(v, per_head);
         }
         tile = first;
     }
@@ -318,9 +327,19 @@ __device__ __forceinline__ float4 join(int count, Part part, int e, int h, float
     return o;
 }
 
+// Tiles that a warp gets before more CTAs share a segment.
+constexpr int kLeast = 3;
+
 // CTAs that share a segment join in groups where there are more than kFlat.
 constexpr int kFlat = 24;
 constexpr int kGroup = 12;
+
+// n i / turns, i <= turns <= 8
+__device__ __forceinline__ long long part_of(long long n, int turns, int i)
+{
+    if (n < (1 << 28)) return static_cast<unsigned>(n) * i / static_cast<unsigned>(turns);
+    return n * i / turns;
+}
 
 // First tile of CTA c's share, and the CTA of a tile.
 __device__ __forceinline__ long long share_of(long long total, int ctas, int c)
@@ -341,9 +360,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
     __shared__ uint64_t s_full[S::kWarps][S::kStages];
     __shared__ int4 s_meta[S::kWarps][S::kStages];
     __shared__ long long s_sum[S::kWarps];
+    __shared__ int s_flags[S::kWarps];
     __shared__ long long s_before[S::kThreads];
     __shared__ Open s_open[S::kWarps * 2];
-    __shared__ int s_last[2];
+    __shared__ uint32_t s_won;
     constexpr int kTile = S::kTile, NT = S::NT, JT = S::JT, MT = S::MT, kStages = S::kStages, CB = S::CB;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -358,16 +378,21 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
     ptx::grid_dep_launch();
 
     // ---------------------------------------------------------------- shares
-    const int per_head = (p.group + S::kHeads - 1) / S::kHeads, heads = p.cache.heads * per_head;
+    const int per_head = (p.group + S::kHeads - 1) / S::kHeads, together = 1 << p.together_log;
+    const int groups = p.cache.heads * per_head >> p.together_log;
+    const int beside = warp & (together - 1), turn = warp >> p.together_log, turns = S::kWarps >> p.together_log;
     const int chunk = (p.B + S::kThreads - 1) / S::kThreads, b0 = tid * chunk;
     long long sum = 0;
-    bool none = false;
+    bool none = false, equal = true;
+    int first_count, unused;
+    first_count = tiles_of<kTile>(p, length_of(p, 0), unused);
     for (int b = b0; b < min(p.B, b0 + chunk); ++b) {
         const int len = __ldg(p.length + b);
-        int first;
         if (len < 0 || len > static_cast<long long>(p.width) * p.cache.page) record_error(p.ctrl, kErrInvalid);
-        sum += tiles_of<kTile>(p, length_of(p, b), first);
+        const int count = tiles_of<kTile>(p, length_of(p, b), unused);
+        sum += count;
         none |= len <= 0;
+        equal &= count == first_count;
     }
     long long before = sum;                  // inclusive prefix
 #pragma unroll
@@ -376,21 +401,30 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
         if (lane >= d) before += o;
     }
     if (lane == 31) s_sum[warp] = before;
-    none = __syncthreads_or(none);
+    none = __any_sync(0xffffffffu, none), equal = __all_sync(0xffffffffu, equal);
+    if (lane == 31) s_flags[warp] = (none ? 1 : 0) | (equal ? 0 : 2);
+    __syncthreads();
+    int flags = 0;
     long long total = 0;
 #pragma unroll
     for (int w = 0; w < S::kWarps; ++w) {
         if (w < warp) before += s_sum[w];
         total += s_sum[w];
+        flags |= s_flags[w];
     }
-    before = (before - sum) * heads;
-    sum *= heads;
-    total *= heads;
-    // CTAs that get work: as many as the warps' tiles need, or all
+    before = (before - sum) * groups;
+    total *= groups;
+    // CTAs that get work: all, or so many that a warp has kLeast tiles; with segments
+    // of one length a multiple of them, so that few CTAs (or one) share a segment
     const int cta = blockIdx.x;
-    const int ctas = static_cast<int>(min((total + S::kWarps - 1) / S::kWarps, static_cast<long long>(gridDim.x)));
+    int ctas = gridDim.x;
+    if (total < static_cast<long long>(gridDim.x) * turns * kLeast) {
+        const int segments = p.B * groups, per_segment = (first_count + turns * kLeast - 1) / (turns * kLeast);
+        const bool even = !(flags & 2) && static_cast<long long>(segments) * per_segment <= static_cast<int>(gridDim.x);
+        ctas = even ? segments * per_segment : (static_cast<int>(total) + turns * kLeast - 1) / (turns * kLeast);
+    }
     // requests without tokens: nothing of theirs is in the order
-    for (int b = blockIdx.x; none && b < p.B; b += gridDim.x) {
+    for (int b = blockIdx.x; (flags & 1) && b < p.B; b += gridDim.x) {
         if (__ldg(p.length + b) > 0) continue;
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + b * p.ldo;
         for (int i = tid; i < p.Hq * p.cache.dim; i += S::kThreads) out[i] = __float2bfloat16(0.f);
@@ -405,8 +439,8 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
     // this warp's share: the last thread's requests that begin at its first tile or before
     Cursor<S> put;
     {
-        const long long share = cta_to - cta_from, from = cta_from + share * warp / S::kWarps;
-        put.left = cta_from + share * (warp + 1) / S::kWarps - from;
+        const long long share = cta_to - cta_from, from = cta_from + part_of(share, turns, turn);
+        put.left = cta_from + part_of(share, turns, turn + 1) - from;
         put.at = from;
         constexpr int kPer = S::kThreads / 32;
         const int coarse = __popc(__ballot_sync(0xffffffffu, s_before[lane * kPer] <= from)) - 1;
@@ -414,18 +448,18 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
         long long r = from - s_before[at];
         for (put.b = at * chunk;; ++put.b) {
             put.enter(p);
-            if (r < static_cast<long long>(put.count) * heads) break;
-            r -= static_cast<long long>(put.count) * heads;
+            if (r < static_cast<long long>(put.count) * groups) break;
+            r -= static_cast<long long>(put.count) * groups;
         }
-        const int vh = r < (1LL << 31) ? static_cast<int>(static_cast<unsigned>(r) / static_cast<unsigned>(put.count)) : static_cast<int>(r / put.count);
-        put.head = per_head == 1 ? vh : vh / per_head;
-        put.block = vh - put.head * per_head;
-        put.tile = put.first + static_cast<int>(r - static_cast<long long>(vh) * put.count);
+        const int group = r < (1LL << 31) ? static_cast<int>(static_cast<unsigned>(r) / static_cast<unsigned>(put.count)) : static_cast<int>(r / put.count);
+        put.at_head(group * together + beside, per_head);
+        put.tile = put.first + static_cast<int>(r - static_cast<long long>(group) * put.count);
     }
 
     // ---------------------------------------------------------------- a warp's stream
     uint8_t* const ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023)) + warp * S::kRing;
-    const uint32_t ring_u = ptx::smem_u32(ring);
+    uint8_t* const ring_scales = ring + (S::kWarps - warp) * S::kRing + warp * S::kScales;
+    const uint32_t ring_u = ptx::smem_u32(ring), scales_u = ptx::smem_u32(ring_scales);
     const long long tiles = put.left, warp_from = put.at;
     const auto page_of = [&](int t) {
         return p.cache.page_shift >= 0 ? t >> p.cache.page_shift : static_cast<int>(static_cast<unsigned>(t) / static_cast<unsigned>(p.cache.page));
@@ -475,7 +509,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
                     load_box(dst + box_at, box_kv ? &p.v_map : &p.k_map, bar, x, p.slots_first ? slot : head, p.slots_first ? head : slot, page);
                     if (S::F8 && in && box_col == 0) {
                         const long long at = (static_cast<long long>(page) * p.cache.heads + head) * p.cache.page + slot;
-                        load_bulk(dst + S::kScales + (box_kv * kTile + piece * box_rows) * 4, (box_kv ? p.cache.v_scale : p.cache.k_scale) + at,
+                        load_bulk(scales_u + stage * S::kScaleStage + (box_kv * kTile + piece * box_rows) * 4, (box_kv ? p.cache.v_scale : p.cache.k_scale) + at,
                                   box_rows * 4, bar);
                     }
                 }
@@ -488,8 +522,8 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
                         off[i] = page_id[i] * p.cache.page_stride + page_in[i] * p.cache.slot_stride + head * p.cache.head_stride;
                         if (S::F8) {
                             const long long at = (static_cast<long long>(page_id[i]) * p.cache.heads + head) * p.cache.page + page_in[i];
-                            cp_async4(dst + S::kScales + (i * 32 + lane) * 4, p.cache.k_scale + at, 4);
-                            cp_async4(dst + S::kScales + (kTile + i * 32 + lane) * 4, p.cache.v_scale + at, 4);
+                            cp_async4(scales_u + stage * S::kScaleStage + (i * 32 + lane) * 4, p.cache.k_scale + at, 4);
+                            cp_async4(scales_u + stage * S::kScaleStage + (kTile + i * 32 + lane) * 4, p.cache.v_scale + at, 4);
                         }
                     }
                 }
@@ -507,7 +541,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
                     cp_async16(at + S::kRows, p.cache.v + src, in ? 16 : 0);
                 }
             }
-            put.next(p, per_head);
+            put.next(p, per_head, together);
             find_pages();
         }
         cp_commit();
@@ -640,7 +674,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
             // rows of this tile that count
             const int lo = (p.window && len > p.window ? len - p.window : 0) - tile * kTile, hi = len - tile * kTile;
             const bool partial = lo > 0 || hi < kTile;
-            const float* scales = reinterpret_cast<const float*>(st + S::kScales);
+            const float* scales = reinterpret_cast<const float*>(ring_scales + stage * S::kScaleStage);
             float vs[MT][2], vl[MT][2];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
@@ -798,10 +832,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
                     }
                     if (lane == 0) {
                         int f;
-                        Open& w = s_open[warp * 2 + which];
+                        Open& w = s_open[(beside * turns + turn) * 2 + which];
                         w.first = seg_first;
                         w.end = seg_first + tiles_of<kTile>(p, len, f);
-                        w.b = b, w.head0 = head0, w.n_heads = n_heads;
+                        w.b = b, w.head0 = head0, w.n_heads = n_heads, w.beside = beside;
                         w.part = part;
                     }
                 }
@@ -812,16 +846,28 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
     __syncthreads();
 
     // ---------------------------------------------------------------- joins
-    float* const cta_parts = p.part + static_cast<long long>(gridDim.x) * S::kWarps * S::kPart;
-    float* const group_parts = cta_parts + static_cast<long long>(gridDim.x) * 2 * S::kPart;
     // the warps' open slots, a lane each; those of one segment follow one another
     const Open mine = s_open[min(lane, 2 * S::kWarps - 1)];
     const bool any = lane < 2 * S::kWarps && mine.end != 0;
     const uint32_t open = __ballot_sync(0xffffffffu, any), lower = open & ((1u << lane) - 1);
-    const long long previous = __shfl_sync(0xffffffffu, mine.first, lower ? 31 - __clz(lower) : 0);
-    const bool leads = any && (!lower || previous != mine.first);
+    const int before_me = lower ? 31 - __clz(lower) : 0;
+    const long long previous = __shfl_sync(0xffffffffu, mine.first, before_me);
+    const int previous_head = __shfl_sync(0xffffffffu, mine.head0, before_me);
+    const bool leads = any && (!lower || previous != mine.first || previous_head != mine.head0);
     const uint32_t leaders = __ballot_sync(0xffffffffu, leads);
-    const uint32_t inside = __ballot_sync(0xffffffffu, leads && mine.first >= cta_from && mine.end <= cta_to);
+    // a segment that this CTA does not have to itself: CTAs c0 .. c1 do.  Of a CTA's
+    // two parts of a block of heads the first is of what began before its share or with it.
+    const bool shares = leads && (mine.first < cta_from || mine.end > cta_to);
+    const uint32_t shared = __ballot_sync(0xffffffffu, shares);
+    int c0 = cta, c1 = cta, second = 0;
+    if (shares) {
+        c0 = cta_of(total, ctas, mine.first), c1 = cta_of(total, ctas, mine.end - 1);
+        second = mine.first != share_of(total, ctas, c0) ? 1 : 0;      // (of c0)
+    }
+    const int g0 = c0 + (cta - c0) / kGroup * kGroup;       // first CTA of this one's group
+    const auto index_of = [&](int c, int from, int sec, int which) { return ((2 * c + (c == from ? sec : 0)) << p.together_log) + which; };
+    float* const cta_parts = p.part + static_cast<long long>(gridDim.x) * S::kWarps * S::kPart;
+    float* const group_parts = cta_parts + (static_cast<long long>(gridDim.x) * 2 << p.together_log) * S::kPart;
 
     // what a thread does with its share of a segment's join; to: where a joined part
     // goes, null: it is the result
@@ -846,11 +892,19 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
         }
     };
     const auto head_of = [](int e) { return e / 32 / JT * 8 + 2 * (e & 3); };
-    // this CTA's parts of the segment that slot `lead` leads
-    const auto join_own = [&](int lead, float* to, int first, int step) {
-        const Open& seg = s_open[lead];
+    // f(slot, first element, step) for the slots of a mask, shared out to the warps
+    const auto each = [&](uint32_t slots, auto f) {
+        if (!slots) return;
+        const int count = __popc(slots), teams = min(count, S::kWarps), team = warp % teams, mates = (S::kWarps - team + teams - 1) / teams;
+        for (int k = 0; slots; ++k, slots &= slots - 1)
+            if (k % teams == team) f(__ffs(slots) - 1, warp / teams * 32 + lane, mates * 32);
+    };
+    // this CTA's parts of each segment
+    each(leaders, [&](int lead, int first, int step) {
         const uint32_t next = leaders & ~((2u << lead) - 1);
         const uint32_t slots = open & ~((1u << lead) - 1) & (next ? (next & -next) - 1 : 0xffffffffu);
+        const int index = __shfl_sync(0xffffffffu, index_of(cta, c0, second, mine.beside), lead);
+        float* const to = shared >> lead & 1 ? cta_parts + index * static_cast<long long>(S::kPart) : nullptr;
         for (int e = first; e < S::kFrag; e += step) {
             float2 m, l;
             uint32_t left = slots;
@@ -859,85 +913,46 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
                 left &= left - 1;
                 return part;
             }, e, head_of(e), m, l);
-            put_joined(seg, to, e, o, m, l);
+            put_joined(s_open[lead], to, e, o, m, l);
         }
-    };
-    // segments inside this CTA's share: shared out to its warps
-    if (inside) {
-        const int count = __popc(inside), teams = min(count, S::kWarps), team = warp % teams, mates = (S::kWarps - team + teams - 1) / teams;
-        uint32_t left = inside;
-        for (int k = 0; left; ++k, left &= left - 1)
-            if (k % teams == team) join_own(__ffs(left) - 1, nullptr, warp / teams * 32 + lane, mates * 32);
-    }
-    // segments that other CTAs share, two at most: CTAs c0 .. c1.  The first of a
-    // CTA's two parts is of what began before its share or with it.
-    uint32_t shared = leaders & ~inside;
+    });
     if (!shared) return;
-    struct Shared {
-        int lead, c0, c1, second, level;
-    } segs[2];
-    const int n_shared = __popc(shared);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        if (i >= n_shared) continue;
-        Shared& s = segs[i];
-        s.lead = __ffs(shared) - 1;
-        shared &= shared - 1;
-        const Open& seg = s_open[s.lead];
-        s.c0 = cta_of(total, ctas, seg.first), s.c1 = cta_of(total, ctas, seg.end - 1);
-        s.second = seg.first != share_of(total, ctas, s.c0) ? 1 : 0;      // (of c0)
-        s.level = s.c1 - s.c0 >= kFlat ? 0 : 1;
-        join_own(s.lead, cta_parts + (2 * cta + (cta == s.c0 ? s.second : 0)) * static_cast<long long>(S::kPart), tid, S::kThreads);
-    }
-    // few CTAs: the last joins all; many: the last of each group, and the last of those
-    for (int round = 0; round < 2; ++round) {
+    // few CTAs: the last joins all; many: the last of each group does, and the last of those
+    const bool grouped = c1 - c0 >= kFlat;
+    uint32_t arriving = shared;
+#pragma unroll 1
+    for (int round = 0; arriving; ++round) {
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (tid != 32 * i) continue;
-            s_last[i] = 0;
-            if (i >= n_shared || segs[i].level < 0) continue;
-            const Shared& s = segs[i];
-            const int g0 = s.c0 + (cta - s.c0) / kGroup * kGroup;
-            int* counter = p.counter + s.c0;
-            int count = s.c1 - s.c0 + 1;
-            if (s.level == 0) {
-                counter = p.counter + kMaxGrid + 2 * g0 + (g0 == s.c0 ? s.second : 0);
-                count = min(kGroup, s.c1 + 1 - g0);
-            } else if (count > kFlat) {
-                count = (count + kGroup - 1) / kGroup;
+        const bool in_group = grouped && round == 0;
+        if (warp == 0) {
+            bool last = false;
+            if (arriving >> lane & 1) {
+                const int count = in_group ? min(kGroup, c1 + 1 - g0) : grouped ? (c1 - c0) / kGroup + 1 : c1 - c0 + 1;
+                int* const counter = p.counter + (in_group ? kMaxGrid * 8 + (2 * g0 + (g0 == c0 ? second : 0)) * 8 : c0 * 8) + mine.beside;
+                last = ptx::atom_add_acq_rel_gpu(counter, 1) == count - 1;
+                if (last) ptx::st_relaxed_gpu(counter, 0);
             }
-            const bool last = ptx::atom_add_acq_rel_gpu(counter, 1) == count - 1;
-            if (last) ptx::st_relaxed_gpu(counter, 0);
-            s_last[i] = last;
+            const uint32_t won = __ballot_sync(0xffffffffu, last);
+            if (lane == 0) s_won = won;
         }
         __syncthreads();
-        bool more = false;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (i >= n_shared) continue;
-            Shared& s = segs[i];
-            const int level = s.level;
-            s.level = -1;
-            if (!s_last[i]) continue;
-            const bool grouped = s.c1 - s.c0 >= kFlat;
-            const int g0 = level == 0 ? s.c0 + (cta - s.c0) / kGroup * kGroup : s.c0;
-            const int count = level == 0 ? min(kGroup, s.c1 + 1 - g0) : grouped ? (s.c1 - s.c0) / kGroup + 1 : s.c1 - s.c0 + 1;
-            const float* const base = level == 1 && grouped ? group_parts : cta_parts;
-            const int step = level == 1 && grouped ? kGroup : 1;
-            const auto part = [&](int k) {
-                const int c = g0 + k * step;
-                return base + (2 * c + (c == s.c0 ? s.second : 0)) * static_cast<long long>(S::kPart);
-            };
-            float* const to = level == 0 ? group_parts + (2 * g0 + (g0 == s.c0 ? s.second : 0)) * static_cast<long long>(S::kPart) : nullptr;
-            for (int e = tid; e < S::kFrag; e += S::kThreads) {
+        const uint32_t won = s_won;
+        each(won, [&](int lead, int first, int step) {
+            const bool group = __shfl_sync(0xffffffffu, in_group, lead), of_groups = __shfl_sync(0xffffffffu, grouped, lead) && !group;
+            const int from = __shfl_sync(0xffffffffu, c0, lead), sec = __shfl_sync(0xffffffffu, second, lead), which = __shfl_sync(0xffffffffu, mine.beside, lead);
+            const int start = group ? __shfl_sync(0xffffffffu, g0, lead) : from, to_cta = __shfl_sync(0xffffffffu, c1, lead);
+            const int count = group ? min(kGroup, to_cta + 1 - start) : of_groups ? (to_cta - from) / kGroup + 1 : to_cta - from + 1;
+            const float* const base = of_groups ? group_parts : cta_parts;
+            const int stride = of_groups ? kGroup : 1;
+            const auto part = [&](int k) { return base + index_of(start + k * stride, from, sec, which) * static_cast<long long>(S::kPart); };
+            float* const to = group ? group_parts + index_of(start, from, sec, which) * static_cast<long long>(S::kPart) : nullptr;
+            for (int e = first; e < S::kFrag; e += step) {
                 float2 m, l;
                 const float4 o = join<S, true>(count, part, e, head_of(e), m, l);
-                put_joined(s_open[s.lead], to, e, o, m, l);
+                put_joined(s_open[lead], to, e, o, m, l);
             }
-            if (level == 0) s.level = 1, more = true;
-        }
-        if (!more) break;
+        });
+        arriving = won & __ballot_sync(0xffffffffu, in_group);
     }
 }
 
@@ -962,27 +977,39 @@ auto with_shape(int dim, bool e4m3, int group, F f)
 }
 
 template <class S>
-long long parts_bytes(int num_sms)
+long long parts_bytes(int num_sms, int together)
 {
-    return 4LL * S::kPart * num_sms * (S::kWarps + 4);
+    return 4LL * S::kPart * num_sms * (S::kWarps + 4 * together);
 }
 
 }  // namespace
 
-void attn_decode_tile(int dim, bool e4m3, int group, int* rows, int* box_bytes)
+AttnShape attn_decode_shape(int dim, bool e4m3, int group)
 {
-    with_shape(dim, e4m3, group, [&](auto s) {
+    return with_shape(dim, e4m3, group, [&](auto s) {
         using S = decltype(s);
-        *rows = S::kTile, *box_bytes = S::kBlockRow;
-        return 0;
+        return AttnShape{S::kTile, S::kBlockRow, S::kWarps, S::kHeads};
     });
 }
 
-long long attn_decode_workspace(int group, int dim, int num_sms)
+int attn_decode_together(const AttnShape& s, int heads, int dim, bool e4m3, int group)
 {
-    const auto bytes = [&](auto s) { return parts_bytes<decltype(s)>(num_sms); };
-    const long long a = with_shape(dim, false, group, bytes), b = with_shape(dim, true, group, bytes);
-    return a > b ? a : b;
+    const int blocks = (group + s.heads - 1) / s.heads, row = dim * (e4m3 ? 1 : 2);
+    int n = 1;
+    while (blocks == 1 && n < 8 && n * row % 128 && heads % (2 * n) == 0 && s.warps % (2 * n) == 0) n *= 2;
+    return n;
+}
+
+long long attn_decode_workspace(int heads, int group, int dim, int num_sms)
+{
+    long long most = 0;
+    for (int e4m3 = 0; e4m3 < 2; ++e4m3) {
+        const AttnShape shape = attn_decode_shape(dim, e4m3, group);
+        const int together = attn_decode_together(shape, heads, dim, e4m3, group);
+        const long long bytes = with_shape(dim, e4m3, group, [&](auto s) { return parts_bytes<decltype(s)>(num_sms, together); });
+        if (bytes > most) most = bytes;
+    }
+    return most;
 }
 
 cudaError_t prepare_attn_decode()

@@ -23,7 +23,7 @@ constexpr int kBarrierWord = 2 * kSyncStep;
 constexpr int kExitWord = 5 * kSyncStep;
 constexpr int kPartWord = 6 * kSyncStep;                 // arrivals at a cut tile, by its first item (matvec_q4)
 constexpr int kAttnWord = kPartWord + kMaxGrid * 8;      // arrivals at a shared segment, by its first CTA (attn_decode)
-constexpr int kPagePlanWord = kAttnWord + 3 * kMaxGrid;  // CTAs past their reads (page_plan)
+constexpr int kPagePlanWord = kAttnWord + 24 * kMaxGrid; // CTAs past their reads (page_plan)
 constexpr int kSyncWords = kPagePlanWord + kSyncStep;
 
 struct NormParams {

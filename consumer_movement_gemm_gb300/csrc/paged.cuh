@@ -74,13 +74,24 @@ struct AttnParams {
     int boxed, slots_first;
     int pieces_log;         // log2 of the boxes that make the rows of a tile
     float* part;            // workspace
-    int* counter;           // [3 * kMaxGrid], handle-owned, zero between calls
+    int together_log;       // log2 of attn_decode_together
+    int* counter;           // [24 * kMaxGrid], handle-owned, zero between calls
     long long timeout_ns;
     Ctrl ctrl;
 };
-long long attn_decode_workspace(int group, int dim, int num_sms);
-// Rows of a tile, bytes of a box's columns.
-void attn_decode_tile(int dim, bool e4m3, int group, int* rows, int* box_bytes);
+// Rows of a tile, bytes of a box's columns, warps of a CTA, query heads that a
+// warp takes.
+struct AttnShape {
+    int rows, box_bytes, warps, heads;
+};
+AttnShape attn_decode_shape(int dim, bool e4m3, int group);
+// Key heads that neighbouring warps take side by side (1, 2, 4 or 8) where the
+// heads of a slot are adjacent: so many that their rows are whole 128-byte lines.
+// Read at other times, a line's halves come from memory twice.  Alone and side by
+// side, us: 64 requests of 8192 tokens, 8 heads of 64, e4m3 197 and 139, bf16 198
+// and 182; 64 of 4096, 8 heads of 80, bf16 186 and 138.
+int attn_decode_together(const AttnShape& s, int heads, int dim, bool e4m3, int group);
+long long attn_decode_workspace(int heads, int group, int dim, int num_sms);
 cudaError_t prepare_attn_decode();
 cudaError_t launch_attn_decode(const AttnParams& p, bool e4m3, int num_sms, cudaStream_t stream, bool pdl);
 

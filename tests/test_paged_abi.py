@@ -23,8 +23,9 @@ def lib(tmp_path_factory):
                    "cudaError_t launch_page_plan(const PagePlanParams&, int, cudaStream_t, bool) { ++launches; return cudaSuccess; }\n"
                    "cudaError_t launch_rope_append(const RopeParams&, bool, int, cudaStream_t, bool) { ++launches; return cudaSuccess; }\n"
                    "cudaError_t launch_attn_decode(const AttnParams&, bool, int, cudaStream_t, bool) { ++launches; return cudaSuccess; }\n"
-                   "void attn_decode_tile(int, bool, int, int* rows, int* box_bytes) { *rows = 16; *box_bytes = 128; }\n"
-                   "long long attn_decode_workspace(int, int, int) { return 4096; }\n"
+                   "AttnShape attn_decode_shape(int, bool, int) { return {16, 128, 8, 8}; }\n"
+                   "int attn_decode_together(const AttnShape&, int, int, bool, int) { return 1; }\n"
+                   "long long attn_decode_workspace(int, int, int, int) { return 4096; }\n"
                    "}\n"
                    "static long long maps[16];      // of the last map: dims, strides, box, how many\n"
                    "static CUresult encode(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t* dims, const cuuint64_t* strides,\n"
