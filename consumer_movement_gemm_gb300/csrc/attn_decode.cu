@@ -52,7 +52,7 @@ struct Shape {
     static constexpr int kStage = 2 * kRows;
     static constexpr int kScaleStage = F8 ? 2 * kTile * 4 : 0;
     static constexpr int kWarps = kRow > 256 ? 6 : NT == 1 ? 12 : 8;
-    static constexpr int kFit = (222 * 1024) / (kWarps * (kStage + kScaleStage));
+    static constexpr int kFit = (214 * 1024) / (kWarps * (kStage + kScaleStage));
     static constexpr int kStages = kFit > 4 ? 4 : kFit;
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kRing = kStages * kStage;
@@ -69,10 +69,17 @@ struct Shape {
 
 // What is left behind of a segment that does not lie within one warp's share.
 struct Open {
-    long long first, end;      // its tiles in the order of the call; end == 0: none
     const float* part;
+    int first, end;            // its tiles in the order of the call; end == 0: none
     int b, head0, n_heads;     // its request and query heads
     int beside;                // which of the heads that go together
+};
+
+// A segment whose parts are joined.
+struct Joined {
+    float* to;                 // where the joined part goes; null: it is the result
+    int entry, n;              // its parts in the CTA's list
+    int b, head0, n_heads;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes)
@@ -84,6 +91,19 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Parts lie in shared memory or in the workspace, where another SM may have written them.
+__device__ __forceinline__ float ld_part(const float* p)
+{
+    float v;
+    asm volatile("ld.relaxed.gpu.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_part(const float4* p)
+{
+    float4 v;
+    asm volatile("ld.relaxed.gpu.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p) : "memory");
+    return v;
+}
 template <int N>
 __device__ __forceinline__ void cp_wait()
 {
@@ -213,8 +233,7 @@ __device__ __forceinline__ int length_of(const AttnParams& p, int b)
 // heads, tile.
 template <class S>
 struct Cursor {
-    long long left;            // tiles of the share from here on
-    long long at;              // linear tile
+    int left;                  // tiles of the share from here on
     int b, vh, head, block, tile;
     int len, first, count;     // of the request
 
@@ -233,7 +252,6 @@ struct Cursor {
     __device__ __forceinline__ void next(const AttnParams& p, int per_head, int together)
     {
         --left;
-        ++at;
         if (++tile < first + count || left == 0) return;
         const int heads = p.cache.heads * per_head, v = vh + together;
         if (v >= heads) {
@@ -287,71 +305,38 @@ __device__ __forceinline__ float lse_of(float m, float l)
     return l == 0.f ? -INFINITY : (m + lg2(l) - (S::F8 ? kShift : 0.f)) * 0.693147180559945309f;
 }
 
-// Element e of the joined parts of one segment, with the statistics of its two
-// heads, in the order of the parts; four are in flight at a time.
-template <class S, bool FAR, class Part>
-__device__ __forceinline__ float4 join(int count, Part part, int e, int h, float2& m, float2& l)
-{
-    constexpr int kAhead = 4;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    m = make_float2(-INFINITY, -INFINITY), l = make_float2(0.f, 0.f);
-    for (int i = 0; i < count; i += kAhead) {
-        float2 pm[kAhead], pl[kAhead];
-        float4 v[kAhead];
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            pm[k] = make_float2(-INFINITY, -INFINITY), pl[k] = make_float2(0.f, 0.f), v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (i + k >= count) continue;
-            const float* q = part(i + k);
-            const float2* stats = reinterpret_cast<const float2*>(q + S::kFrag * 4 + h);
-            if (FAR) {
-                pm[k] = __ldcg(stats), pl[k] = __ldcg(stats + S::kHeads / 2), v[k] = __ldcg(reinterpret_cast<const float4*>(q) + e);
-            } else {
-                pm[k] = *stats, pl[k] = stats[S::kHeads / 2], v[k] = reinterpret_cast<const float4*>(q)[e];
-            }
-        }
-        float2 top = m;
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) top.x = fmaxf(top.x, pm[k].x), top.y = fmaxf(top.y, pm[k].y);
-        const float u0 = top.x == -INFINITY ? 0.f : top.x, u1 = top.y == -INFINITY ? 0.f : top.y;
-        const float c0 = ex2(m.x - u0), c1 = ex2(m.y - u1);
-        o.x *= c0, o.y *= c1, o.z *= c0, o.w *= c1, l.x *= c0, l.y *= c1;
-        m = top;
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const float w0 = ex2(pm[k].x - u0), w1 = ex2(pm[k].y - u1);
-            o.x += v[k].x * w0, o.y += v[k].y * w1, o.z += v[k].z * w0, o.w += v[k].w * w1;
-            l.x += pl[k].x * w0, l.y += pl[k].y * w1;
-        }
-    }
-    return o;
-}
-
 // Tiles that a warp gets before more CTAs share a segment.
 constexpr int kLeast = 3;
+// Tiles of a call, times groups of heads.
+constexpr unsigned kMostTiles = 0x7fffffffu;
 
-// CTAs that share a segment join in groups where there are more than kFlat.
+// CTAs that share a segment join in groups of kGroup where there are more than kFlat.
 constexpr int kFlat = 24;
 constexpr int kGroup = 12;
+constexpr int kAtOnce = 4;     // segments of other CTAs that are joined at a time
 
-// n i / turns, i <= turns <= 8
-__device__ __forceinline__ long long part_of(long long n, int turns, int i)
-{
-    if (n < (1 << 28)) return static_cast<unsigned>(n) * i / static_cast<unsigned>(turns);
-    return n * i / turns;
-}
-
-// First tile of CTA c's share, and the CTA of a tile.
-__device__ __forceinline__ long long share_of(long long total, int ctas, int c)
-{
-    if (total < (1 << 24)) return static_cast<unsigned>(total) * c / ctas;
-    return total * c / ctas;
-}
-__device__ __forceinline__ int cta_of(long long total, int ctas, long long tile)
-{
-    if (total < (1 << 24)) return (static_cast<unsigned>(tile + 1) * ctas - 1) / static_cast<unsigned>(total);
-    return static_cast<int>(((tile + 1) * ctas - 1) / total);
-}
+// What each CTA gets of the call's tiles: as much as the others, the first `rest`
+// one more; or, where all segments have `count` tiles, a part of one of them.
+struct Shares {
+    int ctas, each, rest;
+    int count, parts;          // parts == 0: the former
+    __device__ __forceinline__ int start(int c) const
+    {
+        if (!parts) return c * each + min(c, rest);
+        const int s = c / parts;
+        return s * count + count * (c - s * parts) / parts;
+    }
+    // the CTA that a tile belongs to
+    __device__ __forceinline__ int owner(int tile) const
+    {
+        if (parts) {
+            const int s = tile / count;
+            return s * parts + ((tile - s * count + 1) * parts - 1) / count;
+        }
+        const int longer = rest * (each + 1);
+        return tile < longer ? tile / (each + 1) : rest + (tile - longer) / each;
+    }
+};
 
 template <class S>
 __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __grid_constant__ AttnParams p)
@@ -359,10 +344,13 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t s_full[S::kWarps][S::kStages];
     __shared__ int4 s_meta[S::kWarps][S::kStages];
-    __shared__ long long s_sum[S::kWarps];
+    constexpr int kEntries = kAtOnce * kFlat > 2 * S::kWarps ? kAtOnce * kFlat : 2 * S::kWarps;
+    __shared__ unsigned s_sum[S::kWarps], s_upto[S::kThreads];
     __shared__ int s_flags[S::kWarps];
-    __shared__ long long s_before[S::kThreads];
     __shared__ Open s_open[S::kWarps * 2];
+    __shared__ const float* s_part[kEntries];
+    __shared__ float s_weight[kEntries * S::kHeads];
+    __shared__ Joined s_joined[S::kWarps * 2];
     __shared__ uint32_t s_won;
     constexpr int kTile = S::kTile, NT = S::NT, JT = S::JT, MT = S::MT, kStages = S::kStages, CB = S::CB;
 
@@ -382,85 +370,95 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
     const int groups = p.cache.heads * per_head >> p.together_log;
     const int beside = warp & (together - 1), turn = warp >> p.together_log, turns = S::kWarps >> p.together_log;
     const int chunk = (p.B + S::kThreads - 1) / S::kThreads, b0 = tid * chunk;
-    long long sum = 0;
+    int unused;
+    const int first_count = tiles_of<kTile>(p, length_of(p, 0), unused);
+    unsigned upto = 0;                       // tiles of a head, of requests up to this thread's; the sums stop at the most
     bool none = false, equal = true;
-    int first_count, unused;
-    first_count = tiles_of<kTile>(p, length_of(p, 0), unused);
     for (int b = b0; b < min(p.B, b0 + chunk); ++b) {
         const int len = __ldg(p.length + b);
         if (len < 0 || len > static_cast<long long>(p.width) * p.cache.page) record_error(p.ctrl, kErrInvalid);
         const int count = tiles_of<kTile>(p, length_of(p, b), unused);
-        sum += count;
+        upto = min(upto + count, kMostTiles);
         none |= len <= 0;
         equal &= count == first_count;
     }
-    long long before = sum;                  // inclusive prefix
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
-        const long long o = __shfl_up_sync(0xffffffffu, before, d);
-        if (lane >= d) before += o;
+        const unsigned o = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto = min(upto + o, kMostTiles);
     }
-    if (lane == 31) s_sum[warp] = before;
+    s_upto[tid] = upto;
     none = __any_sync(0xffffffffu, none), equal = __all_sync(0xffffffffu, equal);
-    if (lane == 31) s_flags[warp] = (none ? 1 : 0) | (equal ? 0 : 2);
+    if (lane == 31) s_sum[warp] = upto, s_flags[warp] = (none ? 1 : 0) | (equal ? 0 : 2);
     __syncthreads();
-    int flags = 0;
-    long long total = 0;
+    unsigned sums = lane < S::kWarps ? s_sum[lane] : 0;       // of the warps up to `lane`
+    const int flag = lane < S::kWarps ? s_flags[lane] : 0;
 #pragma unroll
-    for (int w = 0; w < S::kWarps; ++w) {
-        if (w < warp) before += s_sum[w];
-        total += s_sum[w];
-        flags |= s_flags[w];
+    for (int d = 1; d < S::kWarps; d *= 2) {
+        const unsigned o = __shfl_up_sync(0xffffffffu, sums, d);
+        if (lane >= d) sums = min(sums + o, kMostTiles);
     }
-    before = (before - sum) * groups;
-    total *= groups;
+    none = __any_sync(0xffffffffu, flag & 1), equal = !__any_sync(0xffffffffu, flag & 2);
+    const unsigned all = __shfl_sync(0xffffffffu, sums, S::kWarps - 1);
+    if (all > kMostTiles / groups) {
+        if (tid == 0) record_error(p.ctrl, kErrUnsupported);
+        return;
+    }
+    const int total = all * groups, cta = blockIdx.x;
     // CTAs that get work: all, or so many that a warp has kLeast tiles; with segments
     // of one length a multiple of them, so that few CTAs (or one) share a segment
-    const int cta = blockIdx.x;
-    int ctas = gridDim.x;
-    if (total < static_cast<long long>(gridDim.x) * turns * kLeast) {
-        const int segments = p.B * groups, per_segment = (first_count + turns * kLeast - 1) / (turns * kLeast);
-        const bool even = !(flags & 2) && static_cast<long long>(segments) * per_segment <= static_cast<int>(gridDim.x);
-        ctas = even ? segments * per_segment : (static_cast<int>(total) + turns * kLeast - 1) / (turns * kLeast);
+    Shares shares = {static_cast<int>(gridDim.x), 0, 0, first_count, 0};
+    if (total < static_cast<int>(gridDim.x) * turns * kLeast) {
+        const int segments = p.B * groups, parts = (first_count + turns * kLeast - 1) / (turns * kLeast);
+        if (equal && segments * parts <= static_cast<int>(gridDim.x)) {
+            shares.parts = parts;
+            shares.ctas = segments * parts;
+        } else {
+            shares.ctas = (total + turns * kLeast - 1) / (turns * kLeast);
+        }
     }
     // requests without tokens: nothing of theirs is in the order
-    for (int b = blockIdx.x; (flags & 1) && b < p.B; b += gridDim.x) {
+    for (int b = blockIdx.x; none && b < p.B; b += gridDim.x) {
         if (__ldg(p.length + b) > 0) continue;
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + b * p.ldo;
         for (int i = tid; i < p.Hq * p.cache.dim; i += S::kThreads) out[i] = __float2bfloat16(0.f);
         if (p.lse)
             for (int i = tid; i < p.Hq; i += S::kThreads) p.lse[static_cast<long long>(b) * p.Hq + i] = -INFINITY;
     }
-    if (cta >= ctas) return;
-    const long long cta_from = share_of(total, ctas, cta), cta_to = share_of(total, ctas, cta + 1);
-    s_before[tid] = before;
-    __syncthreads();
+    if (total == 0 || cta >= shares.ctas) return;
+    if (!shares.parts) shares.each = total / shares.ctas, shares.rest = total - shares.each * shares.ctas;
+    const int cta_from = shares.start(cta), cta_to = shares.start(cta + 1);
 
-    // this warp's share: the last thread's requests that begin at its first tile or before
+    // this warp's share, and the request that its first tile lies in
     Cursor<S> put;
+    int warp_from;
     {
-        const long long share = cta_to - cta_from, from = cta_from + part_of(share, turns, turn);
-        put.left = cta_from + part_of(share, turns, turn + 1) - from;
-        put.at = from;
-        constexpr int kPer = S::kThreads / 32;
-        const int coarse = __popc(__ballot_sync(0xffffffffu, s_before[lane * kPer] <= from)) - 1;
-        const int at = coarse * kPer + __popc(__ballot_sync(0xffffffffu, lane < kPer && s_before[coarse * kPer + min(lane, kPer - 1)] <= from)) - 1;
-        long long r = from - s_before[at];
-        for (put.b = at * chunk;; ++put.b) {
+        const int n = cta_to - cta_from, each = n / turns, rest = n - each * turns;
+        put.left = each + (turn < rest ? 1 : 0);
+        warp_from = cta_from + turn * each + min(turn, rest);
+    }
+    if (put.left > 0) {
+        const unsigned tile = static_cast<unsigned>(warp_from) / groups;
+        const int w = __popc(__ballot_sync(0xffffffffu, lane < S::kWarps && sums <= tile));
+        const unsigned base = w ? __shfl_sync(0xffffffffu, sums, w - 1) : 0, reach = base + s_upto[min(w, S::kWarps - 1) * 32 + lane];
+        const int i = __popc(__ballot_sync(0xffffffffu, reach <= tile));
+        const unsigned start = __shfl_sync(0xffffffffu, reach, max(i - 1, 0));
+        int r = warp_from - (i ? start : base) * groups;
+        for (put.b = (w * 32 + i) * chunk;; ++put.b) {
             put.enter(p);
-            if (r < static_cast<long long>(put.count) * groups) break;
-            r -= static_cast<long long>(put.count) * groups;
+            if (r < put.count * groups) break;
+            r -= put.count * groups;
         }
-        const int group = r < (1LL << 31) ? static_cast<int>(static_cast<unsigned>(r) / static_cast<unsigned>(put.count)) : static_cast<int>(r / put.count);
+        const int group = r / put.count;
         put.at_head(group * together + beside, per_head);
-        put.tile = put.first + static_cast<int>(r - static_cast<long long>(group) * put.count);
+        put.tile = put.first + r - group * put.count;
     }
 
     // ---------------------------------------------------------------- a warp's stream
     uint8_t* const ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023)) + warp * S::kRing;
     uint8_t* const ring_scales = ring + (S::kWarps - warp) * S::kRing + warp * S::kScales;
     const uint32_t ring_u = ptx::smem_u32(ring), scales_u = ptx::smem_u32(ring_scales);
-    const long long tiles = put.left, warp_from = put.at;
+    const int tiles = put.left;
     const auto page_of = [&](int t) {
         return p.cache.page_shift >= 0 ? t >> p.cache.page_shift : static_cast<int>(static_cast<unsigned>(t) / static_cast<unsigned>(p.cache.page));
     };
@@ -563,11 +561,11 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
         float4 o[NT][JT];
         uint32_t q[NT][JT][2];
         float m[NT][2], l[NT][2], q_unit[NT][2];
-        long long seg_first = 0;
+        int seg_first = 0;
         bool began = false, fresh = true;
         int stage = 0;
         uint32_t parity = 0;
-        for (long long it = 0; it < tiles; ++it) {
+        for (int it = 0; it < tiles; ++it) {
             __syncwarp();
             const int4 meta = s_meta[warp][stage];
             const int b = meta.x, tile = meta.z & 0x3fffffff, len = meta.w;
@@ -851,108 +849,140 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
     const bool any = lane < 2 * S::kWarps && mine.end != 0;
     const uint32_t open = __ballot_sync(0xffffffffu, any), lower = open & ((1u << lane) - 1);
     const int before_me = lower ? 31 - __clz(lower) : 0;
-    const long long previous = __shfl_sync(0xffffffffu, mine.first, before_me);
-    const int previous_head = __shfl_sync(0xffffffffu, mine.head0, before_me);
+    const int previous = __shfl_sync(0xffffffffu, mine.first, before_me), previous_head = __shfl_sync(0xffffffffu, mine.head0, before_me);
     const bool leads = any && (!lower || previous != mine.first || previous_head != mine.head0);
     const uint32_t leaders = __ballot_sync(0xffffffffu, leads);
     // a segment that this CTA does not have to itself: CTAs c0 .. c1 do.  Of a CTA's
     // two parts of a block of heads the first is of what began before its share or with it.
-    const bool shares = leads && (mine.first < cta_from || mine.end > cta_to);
-    const uint32_t shared = __ballot_sync(0xffffffffu, shares);
+    const bool shared = leads && (mine.first < cta_from || mine.end > cta_to);
+    uint32_t arriving = __ballot_sync(0xffffffffu, shared);
     int c0 = cta, c1 = cta, second = 0;
-    if (shares) {
-        c0 = cta_of(total, ctas, mine.first), c1 = cta_of(total, ctas, mine.end - 1);
-        second = mine.first != share_of(total, ctas, c0) ? 1 : 0;      // (of c0)
+    if (shared) {
+        c0 = shares.owner(mine.first), c1 = shares.owner(mine.end - 1);
+        second = mine.first != shares.start(c0) ? 1 : 0;       // (of c0)
     }
-    const int g0 = c0 + (cta - c0) / kGroup * kGroup;       // first CTA of this one's group
-    const auto index_of = [&](int c, int from, int sec, int which) { return ((2 * c + (c == from ? sec : 0)) << p.together_log) + which; };
+    const bool grouped = c1 - c0 >= kFlat;
+    const int g0 = c0 + (cta - c0) / kGroup * kGroup;          // first CTA of this one's group
+    const auto index_of = [&](int c) { return ((2 * c + (c == c0 ? second : 0)) << p.together_log) + mine.beside; };
     float* const cta_parts = p.part + static_cast<long long>(gridDim.x) * S::kWarps * S::kPart;
     float* const group_parts = cta_parts + (static_cast<long long>(gridDim.x) * 2 << p.together_log) * S::kPart;
 
-    // what a thread does with its share of a segment's join; to: where a joined part
-    // goes, null: it is the result
-    const auto put_joined = [&](const Open& seg, float* to, int e, float4 o, float2 m, float2 l) {
-        const int ln = e & 31, j = e / 32 % JT, nt = e / 32 / JT, h = nt * 8 + 2 * (ln & 3);
-        const bool stats = j == 0 && ln < 4;
-        if (to) {
-            reinterpret_cast<float4*>(to)[e] = o;
-            if (stats) {
-                *reinterpret_cast<float2*>(to + S::kFrag * 4 + h) = m;
-                *reinterpret_cast<float2*>(to + S::kFrag * 4 + S::kHeads + h) = l;
-            }
-            return;
-        }
-        const int head0 = seg.head0, n_heads = seg.n_heads;
-        store_pair<S>(static_cast<__nv_bfloat16*>(p.out) + seg.b * p.ldo + static_cast<long long>(head0 + nt * 8) * p.cache.dim, p.cache.dim,
-                      n_heads - nt * 8, j, ln, o, over<S>(l.x), over<S>(l.y));
-        if (stats && p.lse) {
-            float* lse = p.lse + static_cast<long long>(seg.b) * p.Hq + head0;
-            if (h < n_heads) lse[h] = lse_of<S>(m.x, l.x);
-            if (h + 1 < n_heads) lse[h + 1] = lse_of<S>(m.y, l.y);
-        }
-    };
-    const auto head_of = [](int e) { return e / 32 / JT * 8 + 2 * (e & 3); };
-    // f(slot, first element, step) for the slots of a mask, shared out to the warps
-    const auto each = [&](uint32_t slots, auto f) {
-        if (!slots) return;
-        const int count = __popc(slots), teams = min(count, S::kWarps), team = warp % teams, mates = (S::kWarps - team + teams - 1) / teams;
-        for (int k = 0; slots; ++k, slots &= slots - 1)
-            if (k % teams == team) f(__ffs(slots) - 1, warp / teams * 32 + lane, mates * 32);
-    };
-    // this CTA's parts of each segment
-    each(leaders, [&](int lead, int first, int step) {
-        const uint32_t next = leaders & ~((2u << lead) - 1);
-        const uint32_t slots = open & ~((1u << lead) - 1) & (next ? (next & -next) - 1 : 0xffffffffu);
-        const int index = __shfl_sync(0xffffffffu, index_of(cta, c0, second, mine.beside), lead);
-        float* const to = shared >> lead & 1 ? cta_parts + index * static_cast<long long>(S::kPart) : nullptr;
-        for (int e = first; e < S::kFrag; e += step) {
-            float2 m, l;
-            uint32_t left = slots;
-            const float4 o = join<S, false>(__popc(slots), [&](int) {
-                const float* part = s_open[__ffs(left) - 1].part;
-                left &= left - 1;
-                return part;
-            }, e, head_of(e), m, l);
-            put_joined(s_open[lead], to, e, o, m, l);
-        }
-    });
-    if (!shared) return;
-    // few CTAs: the last joins all; many: the last of each group does, and the last of those
-    const bool grouped = c1 - c0 >= kFlat;
-    uint32_t arriving = shared;
-#pragma unroll 1
-    for (int round = 0; arriving; ++round) {
-        __syncthreads();
+    // First the CTA's own parts of each segment; then, of segments that CTAs share,
+    // the one that arrives last joins theirs.  Many CTAs: the last of each group
+    // joins the group's, and the last of those.
+    if (any) s_part[__popc(lower)] = mine.part;      // (every warp writes the same)
+    __syncwarp();
+    uint32_t list = leaders, won = 0;
+    for (int round = -1;;) {
+        // weights of the parts: a warp for a segment, a lane for a head
         const bool in_group = grouped && round == 0;
-        if (warp == 0) {
-            bool last = false;
-            if (arriving >> lane & 1) {
-                const int count = in_group ? min(kGroup, c1 + 1 - g0) : grouped ? (c1 - c0) / kGroup + 1 : c1 - c0 + 1;
-                int* const counter = p.counter + (in_group ? kMaxGrid * 8 + (2 * g0 + (g0 == c0 ? second : 0)) * 8 : c0 * 8) + mine.beside;
-                last = ptx::atom_add_acq_rel_gpu(counter, 1) == count - 1;
-                if (last) ptx::st_relaxed_gpu(counter, 0);
+        int k = 0;
+        for (uint32_t left = list; left; left &= left - 1, ++k) {
+            if (k % S::kWarps != warp) continue;
+            const int lead = __ffs(left) - 1;
+            int entry, n;
+            float* to = nullptr;
+            if (round < 0) {
+                const uint32_t next = leaders & ~((2u << lead) - 1), after = open & ~((1u << lead) - 1);
+                entry = __popc(open & ((1u << lead) - 1));
+                n = __popc(next ? after & ((next & -next) - 1) : after);
+                const int index = __shfl_sync(0xffffffffu, index_of(cta), lead);
+                if (arriving >> lead & 1) to = cta_parts + index * static_cast<long long>(S::kPart);
+            } else {
+                entry = k * kFlat;
+                // (of the lane that leads)
+                const int start = in_group ? g0 : c0, step = grouped && !in_group ? kGroup : 1;
+                const int parts = in_group ? min(kGroup, c1 + 1 - g0) : (c1 - c0) / step + 1;
+                n = __shfl_sync(0xffffffffu, parts, lead);
+                const int index0 = __shfl_sync(0xffffffffu, index_of(start), lead), c = __shfl_sync(0xffffffffu, start, lead);
+                const int by = __shfl_sync(0xffffffffu, step, lead), beside0 = __shfl_sync(0xffffffffu, mine.beside, lead);
+                const bool group = __shfl_sync(0xffffffffu, in_group, lead);
+                const int index = lane ? (2 * (c + lane * by) << p.together_log) + beside0 : index0;
+                if (lane < n) s_part[entry + lane] = (by > 1 ? group_parts : cta_parts) + index * static_cast<long long>(S::kPart);
+                if (group) to = group_parts + index0 * static_cast<long long>(S::kPart);
+                __syncwarp();
             }
-            const uint32_t won = __ballot_sync(0xffffffffu, last);
-            if (lane == 0) s_won = won;
+            constexpr int kSub = 32 / S::kHeads, kMany = (kFlat + kSub - 1) / kSub;
+            const int h = lane % S::kHeads, sub = lane / S::kHeads;
+            float pm[kMany], pl[kMany], top = -INFINITY, l = 0.f;
+#pragma unroll
+            for (int i = 0; i < kMany; ++i) {
+                pm[i] = -INFINITY, pl[i] = 0.f;
+                if (i * kSub + sub >= n) continue;
+                const float* stats = s_part[entry + i * kSub + sub] + S::kFrag * 4 + h;
+                pm[i] = ld_part(stats), pl[i] = ld_part(stats + S::kHeads);
+            }
+#pragma unroll
+            for (int i = 0; i < kMany; ++i) top = fmaxf(top, pm[i]);
+#pragma unroll
+            for (int d = S::kHeads; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const float u = top == -INFINITY ? 0.f : top;
+#pragma unroll
+            for (int i = 0; i < kMany; ++i) {
+                pm[i] = ex2(pm[i] - u);
+                l += pl[i] * pm[i];
+            }
+#pragma unroll
+            for (int d = S::kHeads; d < 32; d *= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
+            const float unit = to ? 1.f : over<S>(l);
+#pragma unroll
+            for (int i = 0; i < kMany; ++i)
+                if (i * kSub + sub < n) s_weight[(entry + i * kSub + sub) * S::kHeads + h] = pm[i] * unit;
+            const Open& seg = s_open[lead];
+            if (sub == 0) {
+                if (to) {
+                    to[S::kFrag * 4 + h] = top, to[S::kFrag * 4 + S::kHeads + h] = l;
+                } else if (p.lse && h < seg.n_heads) {
+                    p.lse[static_cast<long long>(seg.b) * p.Hq + seg.head0 + h] = lse_of<S>(top, l);
+                }
+            }
+            if (lane == 0) s_joined[k] = {to, entry, n, seg.b, seg.head0, seg.n_heads};
         }
         __syncthreads();
-        const uint32_t won = s_won;
-        each(won, [&](int lead, int first, int step) {
-            const bool group = __shfl_sync(0xffffffffu, in_group, lead), of_groups = __shfl_sync(0xffffffffu, grouped, lead) && !group;
-            const int from = __shfl_sync(0xffffffffu, c0, lead), sec = __shfl_sync(0xffffffffu, second, lead), which = __shfl_sync(0xffffffffu, mine.beside, lead);
-            const int start = group ? __shfl_sync(0xffffffffu, g0, lead) : from, to_cta = __shfl_sync(0xffffffffu, c1, lead);
-            const int count = group ? min(kGroup, to_cta + 1 - start) : of_groups ? (to_cta - from) / kGroup + 1 : to_cta - from + 1;
-            const float* const base = of_groups ? group_parts : cta_parts;
-            const int stride = of_groups ? kGroup : 1;
-            const auto part = [&](int k) { return base + index_of(start + k * stride, from, sec, which) * static_cast<long long>(S::kPart); };
-            float* const to = group ? group_parts + index_of(start, from, sec, which) * static_cast<long long>(S::kPart) : nullptr;
-            for (int e = first; e < S::kFrag; e += step) {
-                float2 m, l;
-                const float4 o = join<S, true>(count, part, e, head_of(e), m, l);
-                put_joined(s_open[lead], to, e, o, m, l);
+        // the weighted sums: a warp for 32 float4
+        for (int at = tid; at < k * S::kFrag; at += S::kThreads) {
+            const Joined seg = s_joined[at / S::kFrag];
+            const int e = at % S::kFrag, j = e / 32 % JT, nt = e / 32 / JT;
+            const float* const weight = s_weight + seg.entry * S::kHeads + nt * 8 + 2 * (lane & 3);
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int i = 0; i < seg.n; ++i) {
+                const float2 w = *reinterpret_cast<const float2*>(weight + i * S::kHeads);
+                const float4 v = ld_part(reinterpret_cast<const float4*>(s_part[seg.entry + i]) + e);
+                sum.x += v.x * w.x, sum.y += v.y * w.y, sum.z += v.z * w.x, sum.w += v.w * w.y;
             }
-        });
-        arriving = won & __ballot_sync(0xffffffffu, in_group);
+            if (seg.to) {
+                reinterpret_cast<float4*>(seg.to)[e] = sum;
+            } else {
+                __nv_bfloat16* const row = static_cast<__nv_bfloat16*>(p.out) + seg.b * p.ldo + static_cast<long long>(seg.head0 + nt * 8) * p.cache.dim;
+                store_pair<S>(row, p.cache.dim, seg.n_heads - nt * 8, j, lane, sum, 1.f, 1.f);
+            }
+        }
+        if (round >= 0) arriving |= list & __ballot_sync(0xffffffffu, in_group);
+        if (!won) {
+            if (!arriving) return;
+            ++round;
+            __syncthreads();
+            if (warp == 0) {
+                bool last = false;
+                if (arriving >> lane & 1) {
+                    const bool of_group = grouped && round == 0;
+                    const int count = of_group ? min(kGroup, c1 + 1 - g0) : grouped ? (c1 - c0) / kGroup + 1 : c1 - c0 + 1;
+                    int* const counter = p.counter + (of_group ? kMaxGrid * 8 + (2 * g0 + (g0 == c0 ? second : 0)) * 8 : c0 * 8) + mine.beside;
+                    last = ptx::atom_add_acq_rel_gpu(counter, 1) == count - 1;
+                    if (last) ptx::st_relaxed_gpu(counter, 0);
+                }
+                const uint32_t who = __ballot_sync(0xffffffffu, last);
+                if (lane == 0) s_won = who;
+            }
+            arriving = 0;
+        }
+        __syncthreads();
+        if (!won) won = s_won;
+        if (!won) return;
+        list = 0;
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) list |= won & -won, won &= won - 1;
     }
 }
 
