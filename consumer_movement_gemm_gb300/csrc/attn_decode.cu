@@ -306,7 +306,7 @@ __device__ __forceinline__ float lse_of(float m, float l)
 }
 
 // Tiles that a warp gets before more CTAs share a segment.
-constexpr int kLeast = 3;
+constexpr int kLeast = 2;
 // Tiles of a call, times groups of heads.
 constexpr unsigned kMostTiles = 0x7fffffffu;
 
@@ -405,17 +405,17 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
         return;
     }
     const int total = all * groups, cta = blockIdx.x;
-    // CTAs that get work: all, or so many that a warp has kLeast tiles; with segments
-    // of one length a multiple of them, so that few CTAs (or one) share a segment
+    // CTAs that get work: all, or so many that a warp has kLeast tiles; with few
+    // segments of one length a multiple of them, so that few CTAs (or one) share a segment
     Shares shares = {static_cast<int>(gridDim.x), 0, 0, first_count, 0};
-    if (total < static_cast<int>(gridDim.x) * turns * kLeast) {
-        const int segments = p.B * groups, parts = (first_count + turns * kLeast - 1) / (turns * kLeast);
-        if (equal && segments * parts <= static_cast<int>(gridDim.x)) {
-            shares.parts = parts;
-            shares.ctas = segments * parts;
-        } else {
-            shares.ctas = (total + turns * kLeast - 1) / (turns * kLeast);
+    const int grid = gridDim.x, few = grid * turns * kLeast;
+    if (total < 2 * few) {
+        const int segments = p.B * groups;
+        if (equal && segments <= grid) {
+            const int want = (first_count + turns * kLeast - 1) / (turns * kLeast), parts = min(want, grid / segments);
+            if (parts == want || segments * parts * 5 >= grid * 4) shares.parts = parts, shares.ctas = segments * parts;
         }
+        if (!shares.parts && total < few) shares.ctas = (total + turns * kLeast - 1) / (turns * kLeast);
     }
     // requests without tokens: nothing of theirs is in the order
     for (int b = blockIdx.x; none && b < p.B; b += gridDim.x) {

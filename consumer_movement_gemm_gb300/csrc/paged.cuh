@@ -36,6 +36,8 @@ struct PagePlanParams {
     int* starts;            // [B + 1]
     long long ldt;
     int B, width, pages, page, cap;
+    int page_shift;         // log2(page), or -1
+    int in_place;           // length_out is length, or state_out state
     int* counter;           // handle-owned, zero between calls
     Ctrl ctrl;
 };

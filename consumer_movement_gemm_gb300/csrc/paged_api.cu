@@ -10,6 +10,15 @@ namespace {
 
 constexpr int kMaxQueryHeads = 4096;
 constexpr int kMaxDecodeBatch = 65536;
+constexpr int kMaxNewTokens = 1 << 30;
+
+// log2(n), or -1
+int shift_of(int n)
+{
+    for (int s = 0; s < 31; ++s)
+        if (n == 1 << s) return s;
+    return -1;
+}
 
 // The cache as the kernels take it.
 int check_cache(const tovl_kv_cache* c, KvCache* out)
@@ -37,9 +46,7 @@ int check_cache(const tovl_kv_cache* c, KvCache* out)
     out->page = c->page;
     out->heads = c->heads;
     out->dim = c->dim;
-    out->page_shift = -1;
-    for (int s = 0; s < 31; ++s)
-        if (c->page == 1 << s) out->page_shift = s;
+    out->page_shift = shift_of(c->page);
     return TOVL_OK;
 }
 
@@ -93,7 +100,7 @@ TOVL_API int tovl_page_plan(tovl_handle h, const int* length, const int* add, in
 {
     if (!h) return TOVL_ERR_INVALID;
     if (B < 0 || width < 1 || pages < 1 || page < 1 || cap < 0) return TOVL_ERR_INVALID;
-    if (B > kMaxRequests || static_cast<long long>(pages) * page > INT_MAX) return TOVL_ERR_UNSUPPORTED;
+    if (B > kMaxRequests || cap > kMaxNewTokens || static_cast<long long>(pages) * page > INT_MAX) return TOVL_ERR_UNSUPPORTED;
     if (B == 0) return TOVL_OK;
     if (!length || !add || !table || !ring || !state || !length_out || !state_out || !starts || (cap && (!slots || !positions)) ||
         ldt < width)
@@ -118,6 +125,8 @@ TOVL_API int tovl_page_plan(tovl_handle h, const int* length, const int* add, in
     p.pages = pages;
     p.page = page;
     p.cap = cap;
+    p.page_shift = shift_of(page);
+    p.in_place = length_out == length || state_out == state;
     p.counter = h->sync_words + kPagePlanWord;
     p.ctrl = h->ctrl;
     DeviceGuard g(h->device);
@@ -136,9 +145,7 @@ TOVL_API int tovl_rope_append(tovl_handle h, const void* q, long long ldq, const
     if (rc != TOVL_OK) return rc;
     const int D = p.cache.dim;
     if (T < 0 || Hq < 1 || rot < 0 || rot > D || (rot && (!cos_sin || max_pos < 1))) return TOVL_ERR_INVALID;
-    if (rot % 16 || Hq > kMaxQueryHeads ||
-        static_cast<long long>(T) * (Hq + 2LL * p.cache.heads) > static_cast<long long>(INT_MAX) * 16)
-        return TOVL_ERR_UNSUPPORTED;
+    if (rot % 16 || Hq > kMaxQueryHeads) return TOVL_ERR_UNSUPPORTED;
     if (T == 0) return TOVL_OK;
     if (!positions || !slots || !aligned(positions, 4) || !aligned(slots, 4) || !aligned16(cos_sin)) return TOVL_ERR_INVALID;
     const long long wide_q = static_cast<long long>(Hq) * D, wide_k = static_cast<long long>(p.cache.heads) * D;

@@ -1,13 +1,13 @@
 // rope_append.cu -- rotary embedding of a step's queries and keys, new keys and
 // values written to their cache slots.
 //
-// A row is one head of one token; L threads (a power of two) share it, 16
-// columns each as two pieces of 8: the two halves of eight rotated pairs, or
-// neighbours where nothing is rotated.  So a thread has both numbers of every
-// pair and eight cosines and sines, which it keeps for several heads of the same
-// token.  Pairs are (i, i + rot/2), or (2 i, 2 i + 1) where they are
-// interleaved.  Arithmetic is fp32, rounded once to bf16, or, for an e4m3 cache,
-// to e4m3(x / scale) with scale = max(max |x|, 1e-12) / 448 of the row.
+// A row is one head of one token; ceil(dim / 16) lanes share it, 16 columns each
+// as two pieces of 8, half of what is rotated (or is not) apart, so that a warp's
+// accesses are whole lines.  So a lane has both numbers of every pair, (i, i +
+// rot/2) or interleaved (2 i, 2 i + 1), and eight cosines and sines, which it keeps
+// for one to four heads of its token; a CTA has one token.  Arithmetic is fp32,
+// rounded once to bf16, or, for an e4m3 cache, to e4m3(x / scale) with scale =
+// max(max |x|, 1e-12) / 448 of the row.
 //
 // What bounds it: a launch and dependent loads (position, slot, table) for few
 // tokens; HBM for many.
@@ -20,7 +20,7 @@ namespace tovl {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kMostWarps = 8;          // of a CTA
 
 __device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8])
 {
@@ -61,21 +61,43 @@ __device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const float
     }
 }
 
+// The quotients of a row by its scale, taken to 2^-46 by one residual before their
+// own rounding (Markstein 1990): a product with the inverse alone would round
+// twice, and miss ties.  16384 tokens of 48 heads of 128: FIGURES
+struct Scale {
+    float s, inverse;
+    __device__ __forceinline__ explicit Scale(float top) : s((top < 1e-12f ? 1e-12f : top) / 448.f), inverse(1.f / s) {}
+    __device__ __forceinline__ float divide(float x) const
+    {
+        const float q = x * inverse;
+        return fmaf(fmaf(-q, s == INFINITY ? 0.f : s, x), inverse, q);
+    }
+};
+
+__device__ __forceinline__ uint2 to_e4m3x8(const float (&x)[8], const Scale& s)
+{
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = to_e4m3x2(s.divide(x[2 * i]), s.divide(x[2 * i + 1]));
+    return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+}
+
+// lanes: of a row; units: groups of N rows of a token
 template <bool E4M3, int N>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeParams p, int lanes, int units)
+__global__ void __launch_bounds__(kMostWarps * 32) rope_append_kernel(const RopeParams p, int lanes, int units)
 {
     const KvCache& cache = p.cache;
-    const int D = cache.dim, rows = p.Hq + 2 * cache.heads;
-    const int j = threadIdx.x & (lanes - 1);
-    const long long u = (static_cast<long long>(blockIdx.x) * kRopeThreads + threadIdx.x) / lanes;
-    const long long t = u / units;
-    const int r0 = static_cast<int>(u - t * units) * N;
-    const bool on = t < p.T;
+    const int D = cache.dim, rows = p.Hq + 2 * cache.heads, lane = threadIdx.x & 31;
+    const int per_warp = 32 / lanes, mine = lane / lanes, j = lane - mine * lanes;
+    const int unit = ((blockIdx.y * blockDim.x + threadIdx.x) / 32) * per_warp + mine;
+    const long long t = blockIdx.x;
+    const int r0 = unit * N;
+    const bool on = mine < per_warp && unit < units;
     const bool turned = j < p.rot / 16;
-    // pieces of 8 columns
-    const int a = turned ? (p.interleaved ? 2 * j : j) : 2 * j;
-    const int b = turned && !p.interleaved ? j + p.rot / 16 : a + 1;
-    const bool has_a = a < D / 8, has_b = b < D / 8;
+    // pieces of 8 columns: the halves of what is rotated, then those of the rest
+    const int half = turned ? p.rot / 16 : (D / 8 - p.rot / 8 + 1) / 2;
+    const int a = turned ? j : p.rot / 8 + j - p.rot / 16, b = a + half;
+    const bool has_a = turned || j - p.rot / 16 < half, has_b = has_a && b < D / 8;
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
 
@@ -103,10 +125,12 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopePar
     }
     float c[8], s[8];
     if (turned && on) {
-        const float* at = p.cos_sin + static_cast<long long>(min(max(pos, 0), p.max_pos - 1)) * p.rot + 8 * j;
+        // angles of the pairs (a's first and b's first column, ..), or of a's four and of b's four
+        const float* at = p.cos_sin + static_cast<long long>(min(max(pos, 0), p.max_pos - 1)) * p.rot;
 #pragma unroll
         for (int i = 0; i < 8; i += 4) {
-            const float4 v = __ldg(reinterpret_cast<const float4*>(at + i)), w = __ldg(reinterpret_cast<const float4*>(at + p.rot / 2 + i));
+            const float* pairs = at + (!p.interleaved ? 8 * j + i : 4 * (i ? b : a));
+            const float4 v = __ldg(reinterpret_cast<const float4*>(pairs)), w = __ldg(reinterpret_cast<const float4*>(pairs + p.rot / 2));
             c[i] = v.x, c[i + 1] = v.y, c[i + 2] = v.z, c[i + 3] = v.w;
             s[i] = w.x, s[i + 1] = w.y, s[i + 2] = w.z, s[i + 3] = w.w;
         }
@@ -123,15 +147,16 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopePar
         unpack8(xa[i], fa);
         unpack8(xb[i], fb);
         if (turned && live && (is_q || is_k)) rotate(fa, fb, c, s, p.interleaved);
-        float inv = 0.f;
-        if constexpr (E4M3) {
-            // the largest magnitude by its bits, which put NaN on top
-            uint32_t top = 0;
+        uint32_t top = 0;
+        if (E4M3 && __any_sync(0xffffffffu, live && !is_q)) {
+            // the row's largest magnitude by its bits, which put NaN on top
 #pragma unroll
             for (int k = 0; k < 8; ++k) top = max(top, max(__float_as_uint(fa[k]) & 0x7fffffffu, __float_as_uint(fb[k]) & 0x7fffffffu));
-            for (int d = 1; d < lanes; d *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-            const float m = __uint_as_float(top);
-            inv = (m < 1e-12f ? 1e-12f : m) / 448.f;
+            for (int d = 1; d < lanes; d *= 2) {
+                const uint32_t o = __shfl_down_sync(0xffffffffu, top, d);
+                if (j + d < lanes) top = max(top, o);
+            }
+            top = __shfl_sync(0xffffffffu, top, lane - j);
         }
         if (!live) continue;
         if (is_q) {
@@ -141,13 +166,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopePar
         } else if (write) {
             uint8_t* o = (is_k ? cache.k : cache.v) + page * cache.page_stride + in * cache.slot_stride + h * cache.head_stride;
             if constexpr (E4M3) {
-                const auto eight = [&](const float (&x)[8]) {
-                    const float y[8] = {x[0] / inv, x[1] / inv, x[2] / inv, x[3] / inv, x[4] / inv, x[5] / inv, x[6] / inv, x[7] / inv};
-                    return make_uint2(to_e4m3x2(y[0], y[1]) | to_e4m3x2(y[2], y[3]) << 16, to_e4m3x2(y[4], y[5]) | to_e4m3x2(y[6], y[7]) << 16);
-                };
-                if (has_a) *reinterpret_cast<uint2*>(o + a * 8) = eight(fa);
-                if (has_b) *reinterpret_cast<uint2*>(o + b * 8) = eight(fb);
-                if (j == 0) (is_k ? cache.k_scale : cache.v_scale)[(static_cast<long long>(page) * cache.heads + h) * cache.page + in] = inv;
+                const Scale scale(__uint_as_float(top));
+                if (has_a) *reinterpret_cast<uint2*>(o + a * 8) = to_e4m3x8(fa, scale);
+                if (has_b) *reinterpret_cast<uint2*>(o + b * 8) = to_e4m3x8(fb, scale);
+                if (j == 0) (is_k ? cache.k_scale : cache.v_scale)[(static_cast<long long>(page) * cache.heads + h) * cache.page + in] = scale.s;
             } else {
                 if (has_a) *reinterpret_cast<uint4*>(o + a * 16) = pack8(fa);
                 if (has_b) *reinterpret_cast<uint4*>(o + b * 16) = pack8(fb);
@@ -157,17 +179,13 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopePar
 }
 
 template <int N>
-cudaError_t launch(const RopeParams& p, bool e4m3, cudaStream_t stream, bool pdl)
+cudaError_t launch(const RopeParams& p, bool e4m3, int lanes, cudaStream_t stream, bool pdl)
 {
-    int lanes = 1;
-    while (lanes * 16 < p.cache.dim) lanes *= 2;
-    const int units = (p.Hq + 2 * p.cache.heads + N - 1) / N;
-    const long long threads = static_cast<long long>(p.T) * units * lanes;
-    const long long grid = (threads + kRopeThreads - 1) / kRopeThreads;
-    if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+    const int units = (p.Hq + 2 * p.cache.heads + N - 1) / N, warps = (units + 32 / lanes - 1) / (32 / lanes);
+    const int blocks = (warps + kMostWarps - 1) / kMostWarps;
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(static_cast<unsigned>(grid));
-    lc.blockDim = dim3(kRopeThreads);
+    lc.gridDim = dim3(static_cast<unsigned>(p.T), static_cast<unsigned>(blocks));
+    lc.blockDim = dim3(static_cast<unsigned>((warps + blocks - 1) / blocks) * 32);
     lc.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -182,9 +200,14 @@ cudaError_t launch(const RopeParams& p, bool e4m3, cudaStream_t stream, bool pdl
 
 cudaError_t launch_rope_append(const RopeParams& p, bool e4m3, int num_sms, cudaStream_t stream, bool pdl)
 {
-    // four heads a thread where that leaves several CTAs for every SM
-    const long long rows = static_cast<long long>(p.T) * (p.Hq + 2 * p.cache.heads);
-    return rows * p.cache.dim / 16 >= 8LL * kRopeThreads * num_sms * 4 ? launch<4>(p, e4m3, stream, pdl) : launch<1>(p, e4m3, stream, pdl);
+    const int lanes = (p.cache.dim + 15) / 16, per_warp = 32 / lanes, rows = p.Hq + 2 * p.cache.heads;
+    // several heads a lane where that leaves eight warps for every SM, three or four by
+    // the lanes that stay idle.  16384 tokens, 32 + 2 x 8 heads, three / four, us: of 128
+    // 72.2 / 72.7 (two 79), of 64 36.7 / 40.8, of 80 53.1 / 50.6, of 256 (8 + 2 x 2)
+    // 38.0 / 41.8; e4m3, of 128 81.5 / 87.9.  One is as good up to 256 tokens.
+    if (static_cast<long long>(p.T) * rows * lanes / 32 < 32LL * num_sms) return launch<1>(p, e4m3, lanes, stream, pdl);
+    const auto slots = [&](int n) { return ((rows + n - 1) / n + per_warp - 1) / per_warp * per_warp * n; };
+    return slots(3) <= slots(4) ? launch<3>(p, e4m3, lanes, stream, pdl) : launch<4>(p, e4m3, lanes, stream, pdl);
 }
 
 }  // namespace tovl

@@ -415,7 +415,7 @@ typedef struct {
  *               may be length
  *   state_out   device, int32 [4]: the new state, then the number of new tokens
  *               and of lacking pages; may be state
- *   slots, positions device, int32 [cap]: for the new tokens of request 0, 1, ...
+ *   slots, positions device, int32 [cap], cap up to 2^30: for the new tokens of request 0, 1, ...
  *               in the order of their positions page * table[b][position / page]
  *               + position % page and position; behind the last -1 and 0
  *   starts      device, int32 [B+1]: first new token of each request in slots,

@@ -129,7 +129,7 @@ def test_caches_are_mapped_in_boxes_where_their_layout_allows_it(lib):
 
 def test_plan_refusals(lib):
     for c, rc in ((dict(B=-1), INVALID), (dict(B=4097), UNSUPPORTED), (dict(width=0), INVALID), (dict(ldt=4), INVALID),
-                  (dict(pages=0), INVALID), (dict(page=0), INVALID), (dict(cap=-1), INVALID), (dict(pages=BIG, page=2048), UNSUPPORTED)):
+                  (dict(pages=0), INVALID), (dict(page=0), INVALID), (dict(cap=-1), INVALID), (dict(cap=(1 << 30) + 1), UNSUPPORTED), (dict(pages=BIG, page=2048), UNSUPPORTED)):
         assert call(lib, "tovl_page_plan", PLAN, **c) == (rc, 0), c
 
 
@@ -137,7 +137,7 @@ def test_append_refusals(lib):
     for c, rc in ((dict(T=-1), INVALID), (dict(Hq=0), INVALID), (dict(rot=-16), INVALID), (dict(rot=80), INVALID), (dict(rot=24), UNSUPPORTED),
                   (dict(max_pos=0), INVALID), (dict(ldq=248), INVALID), (dict(ldq=260), INVALID), (dict(ldk=120), INVALID),
                   (dict(ldv=132), INVALID), (dict(ldqo=192), INVALID), (dict(q=P + 8), INVALID), (dict(cos_sin=P + 8), INVALID),
-                  (dict(T=2 ** 31 - 1, Hq=4096, ldq=4096 * 64, ldqo=4096 * 64), UNSUPPORTED), (dict(cache=None), INVALID)):
+                  (dict(Hq=4098, ldq=4098 * 64, ldqo=4098 * 64), UNSUPPORTED), (dict(cache=None), INVALID)):
         assert call(lib, "tovl_rope_append", ROPE, **c) == (rc, 0), c
 
 
