@@ -193,12 +193,10 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi)
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
     return d;
 }
-// two e4m3 numbers (exactly)
-__device__ __forceinline__ uint32_t e4m3_to_h2(uint32_t two)
+// four e4m3 numbers, the lower two and the upper two (exactly)
+__device__ __forceinline__ void e4m3_to_h2(uint32_t four, uint32_t& lower, uint32_t& upper)
 {
-    uint32_t d;
-    asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t; }" : "=r"(d) : "r"(two));
-    return d;
+    asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }" : "=r"(lower), "=r"(upper) : "r"(four));
 }
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
@@ -653,8 +651,9 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
                         ldsm(a, piece_at(k_at, k_turn, mt * 16, j));
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const uint32_t r0 = a[2 * i], r1 = a[2 * i + 1];
-                            const uint32_t a0 = e4m3_to_h2(r0 & 0xffff), a2 = e4m3_to_h2(r0 >> 16), a1 = e4m3_to_h2(r1 & 0xffff), a3 = e4m3_to_h2(r1 >> 16);
+                            uint32_t a0, a1, a2, a3;
+                            e4m3_to_h2(a[2 * i], a0, a2);
+                            e4m3_to_h2(a[2 * i + 1], a1, a3);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) mma<true>(s[nt][mt], a0, a1, a2, a3, q[nt][j + i][0], q[nt][j + i][1]);
                         }
@@ -769,8 +768,9 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             // bytes: row 0's columns 0, 1, row 1's -> column 0 of both rows, column 1 of both
-                            const uint32_t r0 = __byte_perm(a[2 * i], 0, 0x3120), r1 = __byte_perm(a[2 * i + 1], 0, 0x3120);
-                            const uint32_t a0 = e4m3_to_h2(r0 & 0xffff), a1 = e4m3_to_h2(r0 >> 16), a2 = e4m3_to_h2(r1 & 0xffff), a3 = e4m3_to_h2(r1 >> 16);
+                            uint32_t a0, a1, a2, a3;
+                            e4m3_to_h2(__byte_perm(a[2 * i], 0, 0x3120), a0, a1);
+                            e4m3_to_h2(__byte_perm(a[2 * i + 1], 0, 0x3120), a2, a3);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) mma<true>(o[nt][j + i], a0, a1, a2, a3, ph[nt][mt][0], ph[nt][mt][1]);
                         }
