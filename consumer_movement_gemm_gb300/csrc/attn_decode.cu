@@ -206,10 +206,15 @@ __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 
 __device__ __forceinline__ float rest(float w) { return fmaxf(w - bf_hi(__float_as_uint(w)), w * 0x1p-30f); }
 
 // The weight of e4m3 rows is exp2(score - m) times the row's scale, m the
-// largest score + log2(scale), so that the product's operand is 1 at most.  The
+// largest score + log2(scale), so that the product's operand is 2^kSlack at most.  The
 // sum takes the same exponential without the scale; the shift keeps it inside
 // fp32 for any scale that a row of finite bf16 numbers can have (2^-49 .. 2^120).
 constexpr float kShift = 40.f;
+
+// A score may be over the maximum that weights are taken relative to by this much
+// (weights up to 256) before it becomes the maximum: a tile then costs one vote,
+// not a reduction over the rows for each head.
+constexpr float kSlack = 8.f;
 
 // First tile and number of tiles of a request.
 template <int TILE>
@@ -716,30 +721,43 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
             }
+            // the maximum so far stays where no score is over it by more than kSlack
+            float top[NT][2];
+            bool over_it = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                top[nt][0] = top[nt][1] = -INFINITY;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    top[nt][0] = fmaxf(top[nt][0], fmaxf(s[nt][mt].x + vl[mt][0], s[nt][mt].z + vl[mt][1]));
+                    top[nt][1] = fmaxf(top[nt][1], fmaxf(s[nt][mt].y + vl[mt][0], s[nt][mt].w + vl[mt][1]));
+                }
+                over_it |= top[nt][0] > m[nt][0] + kSlack || top[nt][1] > m[nt][1] + kSlack;
+            }
+            if (__any_sync(0xffffffffu, over_it)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float v = top[nt][i];
+#pragma unroll
+                        for (int d = 4; d < 32; d *= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+                        v = fmaxf(v, m[nt][i]);
+                        const float c = m[nt][i] == -INFINITY ? 0.f : ex2(m[nt][i] - v);
+                        m[nt][i] = v;
+                        l[nt][i] *= c;
+#pragma unroll
+                        for (int j = 0; j < JT; ++j) {
+                            if (i) o[nt][j].y *= c, o[nt][j].w *= c;
+                            else o[nt][j].x *= c, o[nt][j].z *= c;
+                        }
+                    }
+            }
             uint32_t ph[NT][MT][2], pl[NT][MT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float m0 = -INFINITY, m1 = -INFINITY;
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    m0 = fmaxf(m0, fmaxf(s[nt][mt].x + vl[mt][0], s[nt][mt].z + vl[mt][1]));
-                    m1 = fmaxf(m1, fmaxf(s[nt][mt].y + vl[mt][0], s[nt][mt].w + vl[mt][1]));
-                }
-#pragma unroll
-                for (int d = 4; d < 32; d *= 2) {
-                    m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, d));
-                    m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, d));
-                }
-                m0 = fmaxf(m0, m[nt][0]), m1 = fmaxf(m1, m[nt][1]);
                 // (all scores -inf so far: weights of 0)
-                const float u0 = (m0 == -INFINITY ? 0.f : m0) - (S::F8 ? kShift : 0.f), u1 = (m1 == -INFINITY ? 0.f : m1) - (S::F8 ? kShift : 0.f);
-                if (__any_sync(0xffffffffu, m0 != m[nt][0] || m1 != m[nt][1])) {
-                    const float c0 = m[nt][0] == -INFINITY ? 0.f : ex2(m[nt][0] - m0), c1 = m[nt][1] == -INFINITY ? 0.f : ex2(m[nt][1] - m1);
-                    l[nt][0] *= c0, l[nt][1] *= c1;
-#pragma unroll
-                    for (int j = 0; j < JT; ++j) o[nt][j].x *= c0, o[nt][j].y *= c1, o[nt][j].z *= c0, o[nt][j].w *= c1;
-                    m[nt][0] = m0, m[nt][1] = m1;
-                }
+                const float u0 = (m[nt][0] == -INFINITY ? 0.f : m[nt][0]) - (S::F8 ? kShift : 0.f), u1 = (m[nt][1] == -INFINITY ? 0.f : m[nt][1]) - (S::F8 ? kShift : 0.f);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
                     float4& v = s[nt][mt];
