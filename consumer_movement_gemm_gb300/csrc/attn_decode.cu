@@ -423,8 +423,8 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
     // requests without tokens: nothing of theirs is in the order
     for (int b = blockIdx.x; none && b < p.B; b += gridDim.x) {
         if (__ldg(p.length + b) > 0) continue;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + b * p.ldo;
-        for (int i = tid; i < p.Hq * p.cache.dim; i += S::kThreads) out[i] = __float2bfloat16(0.f);
+        uint4* const out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + b * p.ldo);
+        for (int i = tid; i < p.Hq * p.cache.dim / 8; i += S::kThreads) out[i] = make_uint4(0, 0, 0, 0);
         if (p.lse)
             for (int i = tid; i < p.Hq; i += S::kThreads) p.lse[static_cast<long long>(b) * p.Hq + i] = -INFINITY;
     }
