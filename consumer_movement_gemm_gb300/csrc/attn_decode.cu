@@ -35,11 +35,13 @@ namespace tovl {
 
 namespace {
 
-template <int DP_, bool F8_, int NT_>
+// PAIR: two warps take two blocks of the same key head's query heads from one ring.
+template <int DP_, bool F8_, int NT_, bool PAIR_ = false>
 struct Shape {
     static constexpr int DP = DP_;                 // head dimension, filled up
     static constexpr bool F8 = F8_;
     static constexpr int NT = NT_;                 // blocks of 8 query heads
+    static constexpr int kRingLog = PAIR_ ? 1 : 0;
     static constexpr int kHeads = 8 * NT;
     static constexpr int kRow = DP * (F8 ? 1 : 2);
     static constexpr int kBlockRow = kRow < 128 ? kRow : 128;          // bytes of a row in a column block
@@ -51,9 +53,9 @@ struct Shape {
     static constexpr int JT = DP / 16;             // blocks of 16 columns
     static constexpr int kStage = 2 * kRows;
     static constexpr int kScaleStage = F8 ? 2 * kTile * 4 : 0;
-    static constexpr int kWarps = kRow > 256 ? 6 : NT == 1 ? 12 : 8;
+    static constexpr int kWarps = kRow > 256 && !PAIR_ ? 6 : NT == 1 ? 12 : 8;
     static constexpr int kFit = (214 * 1024) / (kWarps * (kStage + kScaleStage));
-    static constexpr int kStages = kFit > 4 ? 4 : kFit;
+    static constexpr int kStages = kFit > 4 ? 4 : kFit;                 // a warp's share of its ring's
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kRing = kStages * kStage;
     static constexpr int kScales = kStages * kScaleStage;               // of a warp, behind all rings
@@ -64,7 +66,7 @@ struct Shape {
     // (so that 8 rows' pieces lie in different banks; the copies' swizzle)
     static __host__ __device__ constexpr int phase(int r) { return kBlockRow == 128 ? r & 7 : (r >> 1) & 3; }
     static_assert(kBlockRow == 64 || kBlockRow == 128, "swizzle");
-    static_assert(kStages >= 2 && kBlock % 1024 == 0 && kPart * 4 <= kRing, "ring");
+    static_assert(kStages << kRingLog >= 2 && kBlock % 1024 == 0 && kPart * 4 <= kRing, "ring");
 };
 
 // What is left behind of a segment that does not lie within one warp's share.
@@ -345,8 +347,8 @@ template <class S>
 __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __grid_constant__ AttnParams p)
 {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t s_full[S::kWarps][S::kStages];
-    __shared__ int4 s_meta[S::kWarps][S::kStages];
+    __shared__ uint64_t s_full[S::kWarps * S::kStages], s_empty[S::kWarps * S::kStages];
+    __shared__ int4 s_meta[S::kWarps * S::kStages];
     constexpr int kEntries = kAtOnce * kFlat > 2 * S::kWarps ? kAtOnce * kFlat : 2 * S::kWarps;
     __shared__ unsigned s_sum[S::kWarps], s_upto[S::kThreads];
     __shared__ int s_flags[S::kWarps];
@@ -362,7 +364,8 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
         ptx::prefetch_tmap(&p.k_map);
         ptx::prefetch_tmap(&p.v_map);
     }
-    if (lane < kStages) ptx::mbar_init(&s_full[warp][lane], 1);
+    constexpr int kRingLog = S::kRingLog, kRingStages = kStages << kRingLog;
+    if (lane < kStages) ptx::mbar_init(&s_full[warp * kStages + lane], 1), ptx::mbar_init(&s_empty[warp * kStages + lane], 1 << kRingLog);
     if (lane < 2) s_open[warp * 2 + lane].end = 0;
     ptx::fence_mbar_init();
     ptx::grid_dep_wait();
@@ -458,8 +461,12 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
     }
 
     // ---------------------------------------------------------------- a warp's stream
-    uint8_t* const ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023)) + warp * S::kRing;
-    uint8_t* const ring_scales = ring + (S::kWarps - warp) * S::kRing + warp * S::kScales;
+    const int owner = warp >> kRingLog << kRingLog;      // the ring's first warp, which fetches
+    uint8_t* const rings = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t* const ring = rings + owner * S::kRing;
+    uint8_t* const ring_scales = rings + S::kWarps * S::kRing + owner * S::kScales;
+    uint64_t *const full = s_full + owner * kStages, *const empty = s_empty + owner * kStages;
+    int4* const metas = s_meta + owner * kStages;
     const uint32_t ring_u = ptx::smem_u32(ring), scales_u = ptx::smem_u32(ring_scales);
     const int tiles = put.left;
     const auto page_of = [&](int t) {
@@ -494,17 +501,16 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
             const int head = put.head;
             if (lane == 0) {
                 const int last = put.first + put.count - 1;
-                s_meta[warp][stage] = make_int4(put.b, put.head | put.block << 16, put.tile | (put.tile == put.first ? 1 << 30 : 0) | (put.tile == last ? 1 << 31 : 0), put.len);
+                metas[stage] = make_int4(put.b, put.head | put.block << 16, put.tile | (put.tile == put.first ? 1 << 30 : 0) | (put.tile == last ? 1 << 31 : 0), put.len);
             }
             if (page_id[0] == -2 || page_id[kOwn - 1] == -2) record_error(p.ctrl, kErrInvalid);
             if (p.boxed) {
                 // what holds no token of this tile is outside the tensor: zeros, and nothing read
-                uint64_t* const full = &s_full[warp][stage];
-                const uint32_t bar = ptx::smem_u32(full);
+                const uint32_t bar = ptx::smem_u32(full + stage);
                 const bool in = page_id[0] >= 0;
                 uint32_t bytes = 2 * S::kRows;
                 if (S::F8) bytes += 8 * box_rows * __popc(__ballot_sync(0xffffffffu, in && lane < 1 << pieces_log));
-                if (lane == 0) ptx::mbar_arrive_expect_tx(full, bytes);
+                if (lane == 0) ptx::mbar_arrive_expect_tx(full + stage, bytes);
                 if (lane < 2 * CB << pieces_log) {
                     const int x = box_col * (S::kBlockRow / (S::F8 ? 1 : 2)), page = in ? page_id[0] : p.cache.pages, slot = in ? page_in[0] : 0;
                     load_box(dst + box_at, box_kv ? &p.v_map : &p.k_map, bar, x, p.slots_first ? slot : head, p.slots_first ? head : slot, page);
@@ -548,9 +554,11 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
         cp_commit();
     };
     if (tiles > 0) {
-        find_pages();
+        if (warp == owner) {
+            find_pages();
 #pragma unroll 1
-        for (int s = 0; s < kStages - 1; ++s) fetch(s);
+            for (int s = 0; s < kRingStages - 1; ++s) fetch(s);
+        }
         // fragments of k: row lane % 16, 16 bytes lane / 16; of v: the same (e4m3),
         // or row lane % 8 + 8 (lane / 16), 16 bytes lane / 8 % 2
         const int k_row = lane & 15, v_row = S::F8 ? k_row : (lane & 7) + (lane >> 4) * 8;
@@ -569,10 +577,25 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
         int stage = 0;
         uint32_t parity = 0;
         for (int it = 0; it < tiles; ++it) {
+            const auto wait = [&]() {
+                if (!p.boxed) {
+                    cp_wait<kRingStages - 2>();
+                    return true;
+                }
+                if (wait_full(full + stage, parity, p)) return true;
+                // the other copies in flight, then out
+                for (int s = 1; s < kRingStages - 1 && it + s < tiles; ++s) {
+                    if (++stage == kRingStages) stage = 0, parity ^= 1;
+                    wait_full(full + stage, parity, p);
+                }
+                return false;
+            };
             __syncwarp();
-            const int4 meta = s_meta[warp][stage];
+            // (a shared ring's other warps learn of a tile by its arrival)
+            if (kRingLog && !wait()) break;
+            const int4 meta = metas[stage];
             const int b = meta.x, tile = meta.z & 0x3fffffff, len = meta.w;
-            const int block = meta.y >> 16, head0 = (meta.y & 0xffff) * p.group + block * S::kHeads, n_heads = min(S::kHeads, p.group - block * S::kHeads);
+            const int block = (meta.y >> 16) + (kRingLog ? beside & 1 : 0), head0 = (meta.y & 0xffff) * p.group + block * S::kHeads, n_heads = min(S::kHeads, p.group - block * S::kHeads);
             if (fresh) {
                 // the segment's queries
                 fresh = false;
@@ -623,20 +646,14 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
                     for (int j = 0; j < JT; ++j) o[nt][j] = make_float4(0.f, 0.f, 0.f, 0.f);
                 }
             }
-            if (p.boxed) {
-                if (!wait_full(&s_full[warp][stage], parity, p)) {
-                    // the other copies in flight, then out
-                    for (int s = 1; s < kStages - 1 && it + s < tiles; ++s) {
-                        if (++stage == kStages) stage = 0, parity ^= 1;
-                        wait_full(&s_full[warp][stage], parity, p);
-                    }
-                    break;
-                }
-            } else {
-                cp_wait<kStages - 2>();
-            }
+            if (!kRingLog && !wait()) break;
             __syncwarp();
-            fetch(stage == 0 ? kStages - 1 : stage - 1);
+            if (warp == owner) {
+                // into the stage of the tile before, when the ring's warps are through with it
+                const int to = stage == 0 ? kRingStages - 1 : stage - 1;
+                if (kRingLog && it && put.left > 0 && !wait_full(empty + to, stage == 0 ? parity ^ 1 : parity, p)) put.left = 0;
+                fetch(to);
+            }
             uint8_t* const st = ring + stage * S::kStage;
             const uint32_t st_u = ring_u + stage * S::kStage;
 
@@ -807,6 +824,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
                 }
             }
 
+            if (kRingLog) {
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(empty + stage);
+            }
             const bool ended = meta.z & (1 << 31);
             if (ended || it + 1 == tiles) {
                 fresh = true;
@@ -832,9 +853,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
                     }
                 } else {
                     // what began before this share first, what goes on behind it second
-                    // (in the ring, where no more tiles come)
+                    // (in the ring, where no more tiles come and its warps are through)
                     const int which = began ? 1 : 0;
-                    float* const part = it + 1 == tiles ? reinterpret_cast<float*>(ring) : p.part + (static_cast<long long>(cta) * S::kWarps + warp) * S::kPart;
+                    const bool last = it + 1 == tiles && (!kRingLog || wait_full(empty + stage, parity, p));
+                    float* const part = last ? reinterpret_cast<float*>(rings + warp * S::kRing) : p.part + (static_cast<long long>(cta) * S::kWarps + warp) * S::kPart;
                     __syncwarp();
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
@@ -856,7 +878,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
                     }
                 }
             }
-            if (++stage == kStages) stage = 0, parity ^= 1;
+            if (++stage == kRingStages) stage = 0, parity ^= 1;
         }
     }
     __syncthreads();
@@ -1013,9 +1035,12 @@ cudaError_t launch(const AttnParams& p, int num_sms, cudaStream_t stream, bool p
 // Calls f with the kernel's shape: 16 heads at a time where the group has more
 // than 8 (256 columns: their sums do not fit the registers).
 template <class F>
-auto with_shape(int dim, bool e4m3, int group, F f)
+auto with_shape(int dim, bool e4m3, int group, bool pair, F f)
 {
-    if (dim > 128) return e4m3 ? f(Shape<256, true, 1>()) : f(Shape<256, false, 1>());
+    if (dim > 128) {
+        if (pair) return f(Shape<256, false, 1, true>());
+        return e4m3 ? f(Shape<256, true, 1>()) : f(Shape<256, false, 1>());
+    }
     if (dim > 64) {
         if (group > 8) return e4m3 ? f(Shape<128, true, 2>()) : f(Shape<128, false, 2>());
         return e4m3 ? f(Shape<128, true, 1>()) : f(Shape<128, false, 1>());
@@ -1032,29 +1057,32 @@ long long parts_bytes(int num_sms, int together)
 
 }  // namespace
 
-AttnShape attn_decode_shape(int dim, bool e4m3, int group)
+AttnShape attn_decode_shape(int dim, bool e4m3, int group, bool pair)
 {
-    return with_shape(dim, e4m3, group, [&](auto s) {
+    return with_shape(dim, e4m3, group, pair, [&](auto s) {
         using S = decltype(s);
         return AttnShape{S::kTile, S::kBlockRow, S::kWarps, S::kHeads};
     });
 }
 
-int attn_decode_together(const AttnShape& s, int heads, int dim, bool e4m3, int group)
+bool attn_decode_pairs(int dim, bool e4m3, int group) { return dim > 128 && !e4m3 && (group + 7) / 8 % 2 == 0; }
+
+int attn_decode_together(const AttnShape& s, int heads, int dim, bool e4m3)
 {
-    const int blocks = (group + s.heads - 1) / s.heads, row = dim * (e4m3 ? 1 : 2);
+    const int row = dim * (e4m3 ? 1 : 2);
     int n = 1;
-    while (blocks == 1 && n < 8 && n * row % 128 && heads % (2 * n) == 0 && s.warps % (2 * n) == 0) n *= 2;
+    while (n < 8 && n * row % 128 && heads % (2 * n) == 0 && s.warps % (2 * n) == 0) n *= 2;
     return n;
 }
 
 long long attn_decode_workspace(int heads, int group, int dim, int num_sms)
 {
     long long most = 0;
-    for (int e4m3 = 0; e4m3 < 2; ++e4m3) {
-        const AttnShape shape = attn_decode_shape(dim, e4m3, group);
-        const int together = attn_decode_together(shape, heads, dim, e4m3, group);
-        const long long bytes = with_shape(dim, e4m3, group, [&](auto s) { return parts_bytes<decltype(s)>(num_sms, together); });
+    for (int i = 0; i < 3; ++i) {
+        const bool e4m3 = i == 1, pair = i == 2;
+        if (pair && !attn_decode_pairs(dim, e4m3, group)) continue;
+        const int together = pair ? 2 : attn_decode_together(attn_decode_shape(dim, e4m3, group, false), heads, dim, e4m3);
+        const long long bytes = with_shape(dim, e4m3, group, pair, [&](auto s) { return parts_bytes<decltype(s)>(num_sms, together); });
         if (bytes > most) most = bytes;
     }
     return most;
@@ -1063,8 +1091,9 @@ long long attn_decode_workspace(int heads, int group, int dim, int num_sms)
 cudaError_t prepare_attn_decode()
 {
     const int dims[3] = {64, 128, 256};
-    for (int i = 0; i < 12; ++i) {
-        const cudaError_t e = with_shape(dims[i / 4], i & 1, i & 2 ? 16 : 8, [](auto s) {
+    for (int i = 0; i < 13; ++i) {
+        const bool pair = i == 12;
+        const cudaError_t e = with_shape(pair ? 256 : dims[i / 4], !pair && (i & 1), i & 2 ? 16 : 8, pair, [](auto s) {
             using S = decltype(s);
             return cudaFuncSetAttribute(attn_decode_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
         });
@@ -1075,7 +1104,7 @@ cudaError_t prepare_attn_decode()
 
 cudaError_t launch_attn_decode(const AttnParams& p, bool e4m3, int num_sms, cudaStream_t stream, bool pdl)
 {
-    return with_shape(p.cache.dim, e4m3, p.group, [&](auto s) { return launch<decltype(s)>(p, num_sms, stream, pdl); });
+    return with_shape(p.cache.dim, e4m3, p.group, p.pair, [&](auto s) { return launch<decltype(s)>(p, num_sms, stream, pdl); });
 }
 
 }  // namespace tovl

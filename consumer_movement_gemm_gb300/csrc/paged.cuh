@@ -76,7 +76,8 @@ struct AttnParams {
     int boxed, slots_first;
     int pieces_log;         // log2 of the boxes that make the rows of a tile
     float* part;            // workspace
-    int together_log;       // log2 of attn_decode_together
+    int together_log;       // log2 of the heads that neighbouring warps take side by side
+    int pair;               // attn_decode_pairs: they are two blocks of one key head
     int* counter;           // [24 * kMaxGrid], handle-owned, zero between calls
     long long timeout_ns;
     Ctrl ctrl;
@@ -86,13 +87,17 @@ struct AttnParams {
 struct AttnShape {
     int rows, box_bytes, warps, heads;
 };
-AttnShape attn_decode_shape(int dim, bool e4m3, int group);
+AttnShape attn_decode_shape(int dim, bool e4m3, int group, bool pair);
 // Key heads that neighbouring warps take side by side (1, 2, 4 or 8) where the
 // heads of a slot are adjacent: so many that their rows are whole 128-byte lines.
 // Read at other times, a line's halves come from memory twice.  Alone and side by
 // side, us: 64 requests of 8192 tokens, 8 heads of 64, e4m3 197 and 139, bf16 198
 // and 182; 64 of 4096, 8 heads of 80, bf16 186 and 138.
-int attn_decode_together(const AttnShape& s, int heads, int dim, bool e4m3, int group);
+int attn_decode_together(const AttnShape& s, int heads, int dim, bool e4m3);
+// bf16 heads of more than 128 columns with more than 8 query heads: two warps take
+// two blocks of 8 from one ring, which leaves the shared memory for 12 warps (their
+// own rings: 6).  FIGURES
+bool attn_decode_pairs(int dim, bool e4m3, int group);
 long long attn_decode_workspace(int heads, int group, int dim, int num_sms);
 cudaError_t prepare_attn_decode();
 cudaError_t launch_attn_decode(const AttnParams& p, bool e4m3, int num_sms, cudaStream_t stream, bool pdl);

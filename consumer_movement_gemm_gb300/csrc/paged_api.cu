@@ -59,7 +59,7 @@ bool valid_rows(const void* p, long long ld, long long width)
 // Maps of a cache's keys and values for boxes of `rows` slots, where the layout
 // allows them: whole boxes of at least 8 slots in a page (1024 bytes of shared
 // memory, the swizzle's period), strides that nest.  False: rows one by one.
-bool map_cache(tovl_ctx* h, AttnParams* p, bool e4m3, const AttnShape& shape)
+bool map_cache(tovl_ctx* h, AttnParams* p, bool e4m3, const AttnShape& shape, int together)
 {
     const int tile = shape.rows, box_bytes = shape.box_bytes;
     int rows = tile;
@@ -85,7 +85,7 @@ bool map_cache(tovl_ctx* h, AttnParams* p, bool e4m3, const AttnShape& shape)
     const auto encode = [&](CUtensorMap* map, void* base) {
         return h->encode(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, every,
                          CU_TENSOR_MAP_INTERLEAVE_NONE, box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                         p->together_log ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                         together > 1 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     };
     if (!encode(&p->k_map, c.k) || !encode(&p->v_map, c.v)) return false;
     while (rows << p->pieces_log < tile) ++p->pieces_log;
@@ -217,11 +217,14 @@ TOVL_API int tovl_attn_decode(tovl_handle h, const void* q, long long ldq, int B
     p.ctrl = h->ctrl;
     DeviceGuard g(h->device);
     const bool e4m3 = cache->type == TOVL_E4M3;
-    const AttnShape shape = attn_decode_shape(p.cache.dim, e4m3, p.group);
+    const AttnShape shape = attn_decode_shape(p.cache.dim, e4m3, p.group, false);
     const int row = p.cache.dim * (e4m3 ? 1 : 2), heads = p.cache.heads;
     const bool adjacent = heads > 1 && p.cache.head_stride == row && (p.cache.page == 1 || p.cache.slot_stride >= heads * row);
-    for (int n = adjacent ? attn_decode_together(shape, heads, p.cache.dim, e4m3, p.group) : 1; n > 1; n /= 2) ++p.together_log;
-    p.boxed = map_cache(h, &p, e4m3, shape);
+    int together = adjacent && p.group <= shape.heads ? attn_decode_together(shape, heads, p.cache.dim, e4m3) : 1;
+    p.boxed = map_cache(h, &p, e4m3, shape, together);
+    p.pair = p.boxed && attn_decode_pairs(p.cache.dim, e4m3, p.group);
+    if (p.pair) together = 2;
+    for (; together > 1; together /= 2) ++p.together_log;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     return run(h, s, "attention launch",
                [&](bool pdl) { return launch_attn_decode(p, e4m3, h->num_sms, s, pdl); });

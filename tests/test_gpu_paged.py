@@ -173,6 +173,20 @@ def test_attn_head_sizes_pages_and_layouts(h, dim, page, layout, kind):  # noqa:
         check_attn(h, q, c, table, ints(lens), slots, dim ** -0.5, 0, f"{heads} x {G}")
 
 
+# blocks of 8 or 16 query heads of one key head: two, four or eight warps share a ring; three and five do not; pages of 20
+# slots are copied row by row, without shared rings
+@pytest.mark.parametrize("heads,G,dim", [(1, 32, 128), (2, 64, 128), (1, 128, 64), (1, 16, 256), (3, 32, 192), (1, 24, 256), (1, 72, 128),
+                                         (2, 48, 128), (1, 30, 112)])
+@pytest.mark.parametrize("page,window", [(16, 0), (64, 300), (20, 0)])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_attn_many_query_heads_a_key_head(h, heads, G, dim, page, window, kind):  # noqa: F811
+    g = gen(G * 1000 + dim + page)
+    for lens in ([1], [700, 0, 31, 16], [5000, 9000], [33] * 90):
+        c, table, slots = filled(g, lens, heads, dim, page, kind)
+        q = randn(g, len(lens), heads * G, dim, scale=2)
+        check_attn(h, q, c, table, ints(lens), slots, dim ** -0.5, window, str(lens[:3]))
+
+
 @pytest.mark.parametrize("dim", [8, 24, 72, 136, 200])
 def test_attn_odd_head_sizes(h, dim):  # noqa: F811
     g = gen(dim)
