@@ -23,7 +23,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libtovl.so")
 SOURCES = ["tovl_api.cu", "fused.cu", "plan.cu", "copy.cu", "plan_static.cu", "combine.cu",
            "ops_api.cu", "norm.cu", "route.cu", "moe_decode.cu", "moe_direct.cu",
-           "matvec_q4.cu", "paged_api.cu", "page_plan.cu", "rope_append.cu", "attn_decode.cu"]
+           "matvec_q4.cu", "paged_api.cu", "page_plan.cu", "rope_append.cu", "attn_decode.cu",
+           "attn_decode_e4m3.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

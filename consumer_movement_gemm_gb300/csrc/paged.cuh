@@ -83,9 +83,9 @@ struct AttnParams {
     Ctrl ctrl;
 };
 // Rows of a tile, bytes of a box's columns, warps of a CTA, query heads that a
-// warp takes.
+// warp takes, floats of a part.
 struct AttnShape {
-    int rows, box_bytes, warps, heads;
+    int rows, box_bytes, warps, heads, part;
 };
 AttnShape attn_decode_shape(int dim, bool e4m3, int group, bool pair);
 // Key heads that neighbouring warps take side by side (1, 2, 4 or 8) where the
@@ -100,6 +100,8 @@ int attn_decode_together(const AttnShape& s, int heads, int dim, bool e4m3);
 bool attn_decode_pairs(int dim, bool e4m3, int group);
 long long attn_decode_workspace(int heads, int group, int dim, int num_sms);
 cudaError_t prepare_attn_decode();
+cudaError_t prepare_attn_decode_e4m3();
+cudaError_t launch_attn_decode_e4m3(const AttnParams& p, int num_sms, cudaStream_t stream, bool pdl);
 cudaError_t launch_attn_decode(const AttnParams& p, bool e4m3, int num_sms, cudaStream_t stream, bool pdl);
 
 }  // namespace tovl

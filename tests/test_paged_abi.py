@@ -23,7 +23,7 @@ def lib(tmp_path_factory):
                    "cudaError_t launch_page_plan(const PagePlanParams&, int, cudaStream_t, bool) { ++launches; return cudaSuccess; }\n"
                    "cudaError_t launch_rope_append(const RopeParams&, bool, int, cudaStream_t, bool) { ++launches; return cudaSuccess; }\n"
                    "cudaError_t launch_attn_decode(const AttnParams&, bool, int, cudaStream_t, bool) { ++launches; return cudaSuccess; }\n"
-                   "AttnShape attn_decode_shape(int, bool, int, bool) { return {16, 128, 8, 8}; }\n"
+                   "AttnShape attn_decode_shape(int, bool, int, bool) { return {16, 128, 8, 8, 1040}; }\n"
                    "int attn_decode_together(const AttnShape&, int, int, bool) { return 1; }\n"
                    "bool attn_decode_pairs(int, bool, int) { return false; }\n"
                    "long long attn_decode_workspace(int, int, int, int) { return 4096; }\n"
