@@ -53,7 +53,7 @@ struct Shape {
     static constexpr int JT = DP / 16;             // blocks of 16 columns
     static constexpr int kStage = 2 * kRows;
     static constexpr int kScaleStage = F8 ? 2 * kTile * 4 : 0;
-    static constexpr int kWarps = kRow > 384 && !PAIR_ ? 6 : kRow > 256 && !PAIR_ ? 8 : NT == 1 ? 12 : 8;
+    static constexpr int kWarps = kRow > 384 && !PAIR_ ? 6 : kRow > 256 && !PAIR_ ? 8 : NT == 1 || (F8 && DP <= 128) ? 12 : 8;
     static constexpr int kFit = (214 * 1024) / (kWarps * (kStage + kScaleStage));
     static constexpr int kStages = kFit > 4 ? 4 : kFit;                 // a warp's share of its ring's
     static constexpr int kThreads = kWarps * 32;
@@ -65,7 +65,7 @@ struct Shape {
     // the 16-byte pieces of row r of a block are exchanged by XOR with this
     // (so that 8 rows' pieces lie in different banks; the copies' swizzle)
     static __host__ __device__ constexpr int phase(int r) { return kBlockRow == 128 ? r & 7 : (r >> 1) & 3; }
-    static_assert(kBlockRow == 64 || kBlockRow == 128, "swizzle");
+    static_assert(kSmem + 12 * 1024 <= 227 * 1024, "shared memory, with what is static");
     static_assert(kStages << kRingLog >= 2 && kBlock % 1024 == 0 && kPart * 4 <= kRing, "ring");
 };
 
@@ -1034,6 +1034,8 @@ auto with_shape(int dim, int group, bool pair, F f)
     if (dim > 128) {
         if constexpr (!F8)
             if (pair) return dim > 192 ? f(Shape<256, false, 1, true>()) : f(Shape<192, false, 1, true>());
+        if constexpr (F8)
+            if (group > 8) return dim > 192 ? f(Shape<256, true, 2>()) : f(Shape<192, true, 2>());
         return dim > 192 ? f(Shape<256, F8, 1>()) : f(Shape<192, F8, 1>());
     }
     if (group > 8) return dim > 96 ? f(Shape<128, F8, 2>()) : dim > 64 ? f(Shape<96, F8, 2>()) : f(Shape<64, F8, 2>());

@@ -231,11 +231,11 @@ def _dense(name, t, dtype, shape):
     return t.data_ptr()
 
 
-def _count(name, t) -> int:
-    """Checks a contiguous int32 vector; returns its length."""
-    if t is None or t.dtype is not _I32 or t.dim() != 1 or not t.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous {_I32} vector")
-    return t.shape[0]
+def _ints(name, t, n) -> int:
+    """Checks a contiguous int32 tensor of n elements; returns its address."""
+    if t.dtype is not _I32 or t.numel() != n or not t.is_contiguous():
+        raise TypeError(f"{name} must be {n} contiguous elements of {_I32}")
+    return t.data_ptr()
 
 
 def _bytes(name, t) -> int:
@@ -263,10 +263,10 @@ def _heads(name, t, rows, heads, dim) -> int:
     """Checks a bf16 [rows, heads, dim] tensor whose rows are contiguous; returns the distance of its rows in elements."""
     if t is None or t.dtype is not _BF16 or t.shape != (rows, heads, dim):
         raise TypeError(f"{name} must be {_BF16} ({rows}, {heads}, {dim})")
-    s = t.stride()
-    if (s[2] != 1 and dim > 1) or (s[1] != dim and heads > 1):
+    ld, h, d = t.stride()
+    if (d != 1 and dim > 1) or (h != dim and heads > 1):
         raise TypeError(f"{name} must have contiguous heads")
-    return s[0] if rows > 1 else (heads * dim + 7) // 8 * 8
+    return ld if rows > 1 else (heads * dim + 7) // 8 * 8
 
 
 class KVCache:
@@ -522,13 +522,12 @@ class Handle:
         if _BF16 is None:
             _load_types()
         B, width = table.shape
-        cap = slots.shape[0]
+        cap, pages = slots.numel(), ring.numel()
         rc = (_lib or load()).tovl_page_plan(
-            self.h, _dense("length", length, _I32, (B,)), _dense("add", add, _I32, (B,)), B, table.data_ptr(),
-            _matrix("table", table, _I32, B, width), width, ring.data_ptr(), _count("ring", ring), page,
-            _dense("state", state, _I32, (4,)), _dense("length_out", length_out, _I32, (B,)),
-            _dense("state_out", state_out, _I32, (4,)), _dense("slots", slots, _I32, (cap,)),
-            _dense("positions", positions, _I32, (cap,)), cap, _dense("starts", starts, _I32, (B + 1,)), _stream(stream))
+            self.h, _ints("length", length, B), _ints("add", add, B), B, table.data_ptr(), _matrix("table", table, _I32, B, width),
+            width, _ints("ring", ring, pages), pages, page, _ints("state", state, 4), _ints("length_out", length_out, B),
+            _ints("state_out", state_out, 4), _ints("slots", slots, cap), _ints("positions", positions, cap), cap,
+            _ints("starts", starts, B + 1), _stream(stream))
         if rc:
             _check(self.h, rc, "tovl_page_plan")
 
@@ -548,7 +547,7 @@ class Handle:
             table = _dense("cos_sin", cos_sin, _F32, (far, rot))
         rc = (_lib or load()).tovl_rope_append(
             self.h, q.data_ptr(), _heads("q", q, T, Hq, D), k.data_ptr(), _heads("k", k, T, cache.heads, D), v.data_ptr(),
-            _heads("v", v, T, cache.heads, D), _dense("positions", positions, _I32, (T,)), _dense("slots", slots, _I32, (T,)),
+            _heads("v", v, T, cache.heads, D), _ints("positions", positions, T), _ints("slots", slots, T),
             table, far, rot, 1 if interleaved else 0, T, Hq, cache.ref, q_out.data_ptr(), _heads("q_out", q_out, T, Hq, D),
             _stream(stream))
         if rc:
@@ -572,7 +571,7 @@ class Handle:
         width = table.shape[1]
         rc = (_lib or load()).tovl_attn_decode(
             self.h, q.data_ptr(), _heads("q", q, B, Hq, D), B, Hq, cache.ref, table.data_ptr(),
-            _matrix("table", table, _I32, B, width), width, _dense("length", length, _I32, (B,)), scale, window,
+            _matrix("table", table, _I32, B, width), width, _ints("length", length, B), scale, window,
             out.data_ptr(), _heads("out", out, B, Hq, D), None if lse is None else _dense("lse", lse, _F32, (B, Hq)),
             workspace.data_ptr(), _bytes("workspace", workspace), _stream(stream))
         if rc:
