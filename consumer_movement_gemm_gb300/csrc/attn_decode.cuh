@@ -94,10 +94,10 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Parts lie in shared memory or in the workspace, where another SM may have written them.
-__device__ __forceinline__ float ld_part(const float* p)
+__device__ __forceinline__ float2 ld_part(const float2* p)
 {
-    float v;
-    asm volatile("ld.relaxed.gpu.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+    float2 v;
+    asm volatile("ld.relaxed.gpu.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p) : "memory");
     return v;
 }
 __device__ __forceinline__ float4 ld_part(const float4* p)
@@ -310,9 +310,7 @@ __device__ __forceinline__ float lse_of(float m, float l)
     return l == 0.f ? -INFINITY : (m + lg2(l) - (S::F8 ? kShift : 0.f)) * 0.693147180559945309f;
 }
 
-// Tiles that a warp gets before more CTAs share a segment.
-constexpr int kLeast = 2;
-// Tiles of a call, times groups of heads.
+// Sums of tiles stop there.
 constexpr unsigned kMostTiles = 0x7fffffffu;
 
 // CTAs that share a segment join in groups of kGroup where there are more than kFlat.
@@ -320,28 +318,57 @@ constexpr int kFlat = 24;
 constexpr int kGroup = 12;
 constexpr int kAtOnce = 4;     // segments of other CTAs that are joined at a time
 
-// What each CTA gets of the call's tiles: as much as the others, the first `rest`
-// one more; or, where all segments have `count` tiles, a part of one of them.
+// What each CTA gets of the call's tiles: `each`, the first `rest` one more; or,
+// where all segments have `count` tiles, one of `parts` parts of one of them,
+// shared out alike.
 struct Shares {
     int ctas, each, rest;
     int count, parts;          // parts == 0: the former
-    __device__ __forceinline__ int start(int c) const
-    {
-        if (!parts) return c * each + min(c, rest);
-        const int s = c / parts;
-        return s * count + count * (c - s * parts) / parts;
-    }
+    __device__ __forceinline__ int start(int c) const { return c * each + min(c, rest); }
     // the CTA that a tile belongs to
     __device__ __forceinline__ int owner(int tile) const
     {
-        if (parts) {
-            const int s = tile / count;
-            return s * parts + ((tile - s * count + 1) * parts - 1) / count;
-        }
         const int longer = rest * (each + 1);
         return tile < longer ? tile / (each + 1) : rest + (tile - longer) / each;
     }
 };
+
+// A float4 of O^T of a segment's parts, joined in their order: the sums relative to
+// the largest m of its two heads (x and z are of one, y and w of the other), six parts in
+// flight.
+__device__ __forceinline__ float4 join(const float* const* part, int n, int stats, int sums, int e, float2& m, float2& l)
+{
+    constexpr int kAhead = 6;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    m = make_float2(-INFINITY, -INFINITY), l = make_float2(0.f, 0.f);
+    for (int i = 0; i < n; i += kAhead) {
+        float2 pm[kAhead], pl[kAhead];
+        float4 v[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            pm[k] = make_float2(-INFINITY, -INFINITY), pl[k] = make_float2(0.f, 0.f), v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i + k >= n) continue;
+            const float* const q = part[i + k];
+            pm[k] = ld_part(reinterpret_cast<const float2*>(q + stats)), pl[k] = ld_part(reinterpret_cast<const float2*>(q + stats + sums));
+            v[k] = ld_part(reinterpret_cast<const float4*>(q) + e);
+        }
+        const float2 was = m;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) m.x = fmaxf(m.x, pm[k].x), m.y = fmaxf(m.y, pm[k].y);
+        const float u0 = m.x == -INFINITY ? 0.f : m.x, u1 = m.y == -INFINITY ? 0.f : m.y;
+        if (i) {
+            const float c0 = ex2(was.x - u0), c1 = ex2(was.y - u1);
+            o.x *= c0, o.y *= c1, o.z *= c0, o.w *= c1, l.x *= c0, l.y *= c1;
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const float w0 = ex2(pm[k].x - u0), w1 = ex2(pm[k].y - u1);
+            o.x += v[k].x * w0, o.y += v[k].y * w1, o.z += v[k].z * w0, o.w += v[k].w * w1;
+            l.x += pl[k].x * w0, l.y += pl[k].y * w1;
+        }
+    }
+    return o;
+}
 
 template <class S>
 __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __grid_constant__ AttnParams p)
@@ -354,7 +381,6 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
     __shared__ int s_flags[S::kWarps];
     __shared__ Open s_open[S::kWarps * 2];
     __shared__ const float* s_part[kEntries];
-    __shared__ float s_weight[kEntries * S::kHeads];
     __shared__ Joined s_joined[S::kWarps * 2];
     __shared__ uint32_t s_won;
     constexpr int kTile = S::kTile, NT = S::NT, JT = S::JT, MT = S::MT, kStages = S::kStages, CB = S::CB;
@@ -406,7 +432,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
     }
     none = __any_sync(0xffffffffu, flag & 1), equal = !__any_sync(0xffffffffu, flag & 2);
     const unsigned all = __shfl_sync(0xffffffffu, sums, S::kWarps - 1);
-    if (all > kMostTiles / groups) {
+    if (all > p.most_tiles) {
         if (tid == 0) record_error(p.ctrl, kErrUnsupported);
         return;
     }
@@ -418,10 +444,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
     if (total < 2 * few) {
         const int segments = p.B * groups;
         if (equal && segments <= grid) {
-            const int want = (first_count + turns * kLeast - 1) / (turns * kLeast), parts = min(want, grid / segments);
+            const int want = p.by_least.div(first_count + turns * kLeast - 1), parts = min(want, grid / segments);
             if (parts == want || segments * parts * 5 >= grid * 4) shares.parts = parts, shares.ctas = segments * parts;
         }
-        if (!shares.parts && total < few) shares.ctas = (total + turns * kLeast - 1) / (turns * kLeast);
+        if (!shares.parts && total < few) shares.ctas = p.by_least.div(total + turns * kLeast - 1);
     }
     // requests without tokens: nothing of theirs is in the order
     for (int b = blockIdx.x; none && b < p.B; b += gridDim.x) {
@@ -432,19 +458,24 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
             for (int i = tid; i < p.Hq; i += S::kThreads) p.lse[static_cast<long long>(b) * p.Hq + i] = -INFINITY;
     }
     if (total == 0 || cta >= shares.ctas) return;
-    if (!shares.parts) shares.each = total / shares.ctas, shares.rest = total - shares.each * shares.ctas;
-    const int cta_from = shares.start(cta), cta_to = shares.start(cta + 1);
+    int whole = total, among = shares.ctas, place = cta, offset = 0;
+    if (shares.parts) {
+        const int segment = cta / shares.parts;
+        whole = first_count, among = shares.parts, place = cta - segment * shares.parts, offset = segment * first_count;
+    }
+    shares.each = whole / among, shares.rest = whole - shares.each * among;
+    const int cta_from = offset + shares.start(place), cta_to = offset + shares.start(place + 1);
 
     // this warp's share, and the request that its first tile lies in
     Cursor<S> put;
     int warp_from;
     {
-        const int n = cta_to - cta_from, each = n / turns, rest = n - each * turns;
+        const int n = cta_to - cta_from, each = p.by_turns.div(n), rest = n - each * turns;
         put.left = each + (turn < rest ? 1 : 0);
         warp_from = cta_from + turn * each + min(turn, rest);
     }
     if (put.left > 0) {
-        const unsigned tile = static_cast<unsigned>(warp_from) / groups;
+        const unsigned tile = p.by_groups.div(warp_from);
         const int w = __popc(__ballot_sync(0xffffffffu, lane < S::kWarps && sums <= tile));
         const unsigned base = w ? __shfl_sync(0xffffffffu, sums, w - 1) : 0, reach = base + s_upto[min(w, S::kWarps - 1) * 32 + lane];
         const int i = __popc(__ballot_sync(0xffffffffu, reach <= tile));
@@ -469,9 +500,6 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
     int4* const metas = s_meta + owner * kStages;
     const uint32_t ring_u = ptx::smem_u32(ring), scales_u = ptx::smem_u32(ring_scales);
     const int tiles = put.left;
-    const auto page_of = [&](int t) {
-        return p.cache.page_shift >= 0 ? t >> p.cache.page_shift : static_cast<int>(static_cast<unsigned>(t) / static_cast<unsigned>(p.cache.page));
-    };
     // boxes: lane (k or v, column block, piece of the tile's rows)
     const int pieces_log = p.pieces_log, box_rows = kTile >> pieces_log;
     const int piece = lane & ((1 << pieces_log) - 1), box_col = (lane >> pieces_log) % CB, box_kv = (lane >> pieces_log) / CB;
@@ -487,7 +515,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
             const int row = p.boxed ? piece * box_rows : i * 32 + lane, t = put.tile * kTile + row, rows = p.boxed ? box_rows : 1;
             page_id[i] = -1;
             if (put.left > 0 && row < kTile && t < put.len && t + rows > lo) {
-                const int n = page_of(t);
+                const int n = p.by_page.div(t);
                 page_in[i] = t - n * p.cache.page;
                 page_id[i] = __ldg(p.table + put.b * p.ldt + n);
                 if (static_cast<unsigned>(page_id[i]) >= static_cast<unsigned>(p.cache.pages)) page_id[i] = -2;
@@ -557,7 +585,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
         if (warp == owner) {
             find_pages();
 #pragma unroll 1
-            for (int s = 0; s < kRingStages - 1; ++s) fetch(s);
+            for (int s = 0; s < kRingStages; ++s) fetch(s);
         }
         // fragments of k: row lane % 16, 16 bytes lane / 16; of v: the same (e4m3),
         // or row lane % 8 + 8 (lane / 16), 16 bytes lane / 8 % 2
@@ -579,12 +607,13 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
         for (int it = 0; it < tiles; ++it) {
             const auto wait = [&]() {
                 if (!p.boxed) {
-                    cp_wait<kRingStages - 2>();
+                    if (it) cp_wait<kRingStages - 2>();
+                    else cp_wait<kRingStages - 1>();
                     return true;
                 }
                 if (wait_full(full + stage, parity, p)) return true;
                 // the other copies in flight, then out
-                for (int s = 1; s < kRingStages - 1 && it + s < tiles; ++s) {
+                for (int s = 1; s < kRingStages - (it ? 1 : 0) && it + s < tiles; ++s) {
                     if (++stage == kRingStages) stage = 0, parity ^= 1;
                     wait_full(full + stage, parity, p);
                 }
@@ -648,10 +677,12 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
             }
             if (!kRingLog && !wait()) break;
             __syncwarp();
-            if (warp == owner) {
-                // into the stage of the tile before, when the ring's warps are through with it
+            if (it && warp == owner) {
+                // into the stage of the tile before, when the ring's warps are through with it.
+                // (Right behind that tile more copies are in flight, and memory is slower:
+                // 64 requests up to 16384 tokens 343 us for 330.)
                 const int to = stage == 0 ? kRingStages - 1 : stage - 1;
-                if (kRingLog && it && put.left > 0 && !wait_full(empty + to, stage == 0 ? parity ^ 1 : parity, p)) put.left = 0;
+                if (kRingLog && put.left > 0 && !wait_full(empty + to, stage == 0 ? parity ^ 1 : parity, p)) put.left = 0;
                 fetch(to);
             }
             uint8_t* const st = ring + stage * S::kStage;
@@ -898,8 +929,12 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
     uint32_t arriving = __ballot_sync(0xffffffffu, shared);
     int c0 = cta, c1 = cta, second = 0;
     if (shared) {
-        c0 = shares.owner(mine.first), c1 = shares.owner(mine.end - 1);
-        second = mine.first != shares.start(c0) ? 1 : 0;       // (of c0)
+        if (shares.parts) {
+            c0 = cta - place, c1 = c0 + shares.parts - 1;
+        } else {
+            c0 = shares.owner(mine.first), c1 = shares.owner(mine.end - 1);
+            second = mine.first != shares.start(c0) ? 1 : 0;       // (of c0)
+        }
     }
     const bool grouped = c1 - c0 >= kFlat;
     const int g0 = c0 + (cta - c0) / kGroup * kGroup;          // first CTA of this one's group
@@ -909,93 +944,50 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
 
     // First the CTA's own parts of each segment; then, of segments that CTAs share,
     // the one that arrives last joins theirs.  Many CTAs: the last of each group
-    // joins the group's, and the last of those.
-    if (any) s_part[__popc(lower)] = mine.part;      // (every warp writes the same)
-    __syncwarp();
+    // joins the group's, and the last of those.  (Every warp writes the same lists.)
     uint32_t list = leaders, won = 0;
     for (int round = -1;;) {
-        // weights of the parts: a warp for a segment, a lane for a head
-        const bool in_group = grouped && round == 0;
-        int k = 0;
-        for (uint32_t left = list; left; left &= left - 1, ++k) {
-            if (k % S::kWarps != warp) continue;
-            const int lead = __ffs(left) - 1;
-            int entry, n;
-            float* to = nullptr;
-            if (round < 0) {
-                const uint32_t next = leaders & ~((2u << lead) - 1), after = open & ~((1u << lead) - 1);
-                entry = __popc(open & ((1u << lead) - 1));
-                n = __popc(next ? after & ((next & -next) - 1) : after);
-                const int index = __shfl_sync(0xffffffffu, index_of(cta), lead);
-                if (arriving >> lead & 1) to = cta_parts + index * static_cast<long long>(S::kPart);
-            } else {
-                entry = k * kFlat;
-                // (of the lane that leads)
-                const int start = in_group ? g0 : c0, step = grouped && !in_group ? kGroup : 1;
-                const int parts = in_group ? min(kGroup, c1 + 1 - g0) : (c1 - c0) / step + 1;
-                n = __shfl_sync(0xffffffffu, parts, lead);
+        const int count = __popc(list), k = __popc(list & ((1u << lane) - 1));
+        const bool in_group = grouped && round == 0, listed = list >> lane & 1;
+        if (round < 0) {
+            if (any) s_part[__popc(lower)] = mine.part;
+            const uint32_t next = leaders & ~((2u << lane) - 1);
+            const int n = __popc(next ? open & ((next & -next) - 1) : open) - __popc(lower);
+            if (listed) s_joined[k] = {shared ? cta_parts + index_of(cta) * static_cast<long long>(S::kPart) : nullptr, __popc(lower), n, mine.b, mine.head0, mine.n_heads};
+        } else {
+            const int start = in_group ? g0 : c0, step = grouped && !in_group ? kGroup : 1;
+            const int n = in_group ? min(kGroup, c1 + 1 - g0) : (c1 - c0) / step + 1;
+            if (listed) s_joined[k] = {in_group ? group_parts + index_of(g0) * static_cast<long long>(S::kPart) : nullptr, k * kFlat, n, mine.b, mine.head0, mine.n_heads};
+            for (uint32_t left = list, i = 0; left; left &= left - 1, ++i) {
+                const int lead = __ffs(left) - 1;
                 const int index0 = __shfl_sync(0xffffffffu, index_of(start), lead), c = __shfl_sync(0xffffffffu, start, lead);
-                const int by = __shfl_sync(0xffffffffu, step, lead), beside0 = __shfl_sync(0xffffffffu, mine.beside, lead);
-                const bool group = __shfl_sync(0xffffffffu, in_group, lead);
+                const int by = __shfl_sync(0xffffffffu, step, lead), parts = __shfl_sync(0xffffffffu, n, lead), beside0 = __shfl_sync(0xffffffffu, mine.beside, lead);
                 const int index = lane ? (2 * (c + lane * by) << p.together_log) + beside0 : index0;
-                if (lane < n) s_part[entry + lane] = (by > 1 ? group_parts : cta_parts) + index * static_cast<long long>(S::kPart);
-                if (group) to = group_parts + index0 * static_cast<long long>(S::kPart);
-                __syncwarp();
+                if (lane < parts) s_part[i * kFlat + lane] = (by > 1 ? group_parts : cta_parts) + index * static_cast<long long>(S::kPart);
             }
-            constexpr int kSub = 32 / S::kHeads, kMany = (kFlat + kSub - 1) / kSub;
-            const int h = lane % S::kHeads, sub = lane / S::kHeads;
-            float pm[kMany], pl[kMany], top = -INFINITY, l = 0.f;
-#pragma unroll
-            for (int i = 0; i < kMany; ++i) {
-                pm[i] = -INFINITY, pl[i] = 0.f;
-                if (i * kSub + sub >= n) continue;
-                const float* stats = s_part[entry + i * kSub + sub] + S::kFrag * 4 + h;
-                pm[i] = ld_part(stats), pl[i] = ld_part(stats + S::kHeads);
-            }
-#pragma unroll
-            for (int i = 0; i < kMany; ++i) top = fmaxf(top, pm[i]);
-#pragma unroll
-            for (int d = S::kHeads; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            const float u = top == -INFINITY ? 0.f : top;
-#pragma unroll
-            for (int i = 0; i < kMany; ++i) {
-                pm[i] = ex2(pm[i] - u);
-                l += pl[i] * pm[i];
-            }
-#pragma unroll
-            for (int d = S::kHeads; d < 32; d *= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
-            const float unit = to ? 1.f : over<S>(l);
-#pragma unroll
-            for (int i = 0; i < kMany; ++i)
-                if (i * kSub + sub < n) s_weight[(entry + i * kSub + sub) * S::kHeads + h] = pm[i] * unit;
-            const Open& seg = s_open[lead];
-            if (sub == 0) {
-                if (to) {
-                    to[S::kFrag * 4 + h] = top, to[S::kFrag * 4 + S::kHeads + h] = l;
-                } else if (p.lse && h < seg.n_heads) {
-                    p.lse[static_cast<long long>(seg.b) * p.Hq + seg.head0 + h] = lse_of<S>(top, l);
-                }
-            }
-            if (lane == 0) s_joined[k] = {to, entry, n, seg.b, seg.head0, seg.n_heads};
         }
-        __syncthreads();
-        // the weighted sums: a warp for 32 float4
-        for (int at = tid; at < k * S::kFrag; at += S::kThreads) {
+        __syncwarp();
+        // a warp for 32 float4
+        for (int at = tid; at < count * S::kFrag; at += S::kThreads) {
             const Joined seg = s_joined[at / S::kFrag];
-            const int e = at % S::kFrag, j = e / 32 % JT, nt = e / 32 / JT;
-            const float* const weight = s_weight + seg.entry * S::kHeads + nt * 8 + 2 * (lane & 3);
-            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int i = 0; i < seg.n; ++i) {
-                const float2 w = *reinterpret_cast<const float2*>(weight + i * S::kHeads);
-                const float4 v = ld_part(reinterpret_cast<const float4*>(s_part[seg.entry + i]) + e);
-                sum.x += v.x * w.x, sum.y += v.y * w.y, sum.z += v.z * w.x, sum.w += v.w * w.y;
-            }
+            const int e = at % S::kFrag, j = e / 32 % JT, nt = e / 32 / JT, h = nt * 8 + 2 * (lane & 3);
+            float2 m, l;
+            const float4 sum = join(s_part + seg.entry, seg.n, S::kFrag * 4 + h, S::kHeads, e, m, l);
+            const bool stats = j == 0 && lane < 4;
             if (seg.to) {
                 reinterpret_cast<float4*>(seg.to)[e] = sum;
+                if (stats) {
+                    *reinterpret_cast<float2*>(seg.to + S::kFrag * 4 + h) = m;
+                    *reinterpret_cast<float2*>(seg.to + S::kFrag * 4 + S::kHeads + h) = l;
+                }
             } else {
                 __nv_bfloat16* const row = static_cast<__nv_bfloat16*>(p.out) + seg.b * p.ldo + static_cast<long long>(seg.head0 + nt * 8) * p.cache.dim;
-                store_pair<S>(row, p.cache.dim, seg.n_heads - nt * 8, j, lane, sum, 1.f, 1.f);
+                store_pair<S>(row, p.cache.dim, seg.n_heads - nt * 8, j, lane, sum, over<S>(l.x), over<S>(l.y));
+                if (stats && p.lse) {
+                    float* const lse = p.lse + static_cast<long long>(seg.b) * p.Hq + seg.head0;
+                    if (h < seg.n_heads) lse[h] = lse_of<S>(m.x, l.x);
+                    if (h + 1 < seg.n_heads) lse[h + 1] = lse_of<S>(m.y, l.y);
+                }
             }
         }
         if (round >= 0) arriving |= list & __ballot_sync(0xffffffffu, in_group);
@@ -1007,9 +999,9 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
                 bool last = false;
                 if (arriving >> lane & 1) {
                     const bool of_group = grouped && round == 0;
-                    const int count = of_group ? min(kGroup, c1 + 1 - g0) : grouped ? (c1 - c0) / kGroup + 1 : c1 - c0 + 1;
+                    const int all_of = of_group ? min(kGroup, c1 + 1 - g0) : grouped ? (c1 - c0) / kGroup + 1 : c1 - c0 + 1;
                     int* const counter = p.counter + (of_group ? kMaxGrid * 8 + (2 * g0 + (g0 == c0 ? second : 0)) * 8 : c0 * 8) + mine.beside;
-                    last = ptx::atom_add_acq_rel_gpu(counter, 1) == count - 1;
+                    last = ptx::atom_add_acq_rel_gpu(counter, 1) == all_of - 1;
                     if (last) ptx::st_relaxed_gpu(counter, 0);
                 }
                 const uint32_t who = __ballot_sync(0xffffffffu, last);

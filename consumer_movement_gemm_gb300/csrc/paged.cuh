@@ -12,6 +12,19 @@ namespace tovl {
 constexpr int kMaxRequests = 4096;     // of one page_plan call
 constexpr int kMaxHeadDim = 256;
 
+// Division by a number that the host knows, of x < 2^31.
+struct FastDiv {
+    unsigned long long m;
+    int s;
+    FastDiv() = default;
+    explicit FastDiv(unsigned d) : s(31)
+    {
+        while (1ull << (s - 31) < d) ++s;
+        m = ((1ull << s) + d - 1) / d;      // at most 2^32; m d - 2^s < d <= 2^(s - 31)
+    }
+    __device__ __forceinline__ int div(unsigned x) const { return static_cast<int>(x * m >> s); }
+};
+
 // tovl_kv_cache with strides in bytes.
 struct KvCache {
     uint8_t* k;
@@ -79,6 +92,8 @@ struct AttnParams {
     int together_log;       // log2 of the heads that neighbouring warps take side by side
     int pair;               // attn_decode_pairs: they are two blocks of one key head
     int* counter;           // [24 * kMaxGrid], handle-owned, zero between calls
+    FastDiv by_page, by_groups, by_turns, by_least;     // kLeast * turns
+    unsigned most_tiles;    // 2^31 / groups of heads
     long long timeout_ns;
     Ctrl ctrl;
 };
@@ -87,6 +102,7 @@ struct AttnParams {
 struct AttnShape {
     int rows, box_bytes, warps, heads, part;
 };
+constexpr int kLeast = 2;              // tiles that a warp gets before more CTAs share a segment
 AttnShape attn_decode_shape(int dim, bool e4m3, int group, bool pair);
 // Key heads that neighbouring warps take side by side (1, 2, 4 or 8) where the
 // heads of a slot are adjacent: so many that their rows are whole 128-byte lines.

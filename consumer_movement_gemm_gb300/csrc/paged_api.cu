@@ -224,7 +224,14 @@ TOVL_API int tovl_attn_decode(tovl_handle h, const void* q, long long ldq, int B
     p.boxed = map_cache(h, &p, e4m3, shape, together);
     p.pair = p.boxed && attn_decode_pairs(p.cache.dim, e4m3, p.group);
     if (p.pair) together = 2;
-    for (; together > 1; together /= 2) ++p.together_log;
+    for (int n = together; n > 1; n /= 2) ++p.together_log;
+    const AttnShape taken = p.pair ? attn_decode_shape(p.cache.dim, e4m3, p.group, true) : shape;
+    const int groups = heads * ((p.group + taken.heads - 1) / taken.heads) / together, turns = taken.warps / together;
+    p.by_page = FastDiv(p.cache.page);
+    p.by_groups = FastDiv(groups);
+    p.by_turns = FastDiv(turns);
+    p.by_least = FastDiv(turns * kLeast);
+    p.most_tiles = INT_MAX / groups;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     return run(h, s, "attention launch",
                [&](bool pdl) { return launch_attn_decode(p, e4m3, h->num_sms, s, pdl); });
