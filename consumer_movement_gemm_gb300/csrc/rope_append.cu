@@ -84,7 +84,7 @@ __device__ __forceinline__ uint2 to_e4m3x8(const float (&x)[8], const Scale& s)
 
 // lanes: of a row; units: groups of N rows of a token
 template <bool E4M3, int N>
-__global__ void __launch_bounds__(kMostWarps * 32) rope_append_kernel(const RopeParams p, int lanes, int units)
+__global__ void __maxnreg__(64) rope_append_kernel(const RopeParams p, int lanes, int units)
 {
     const KvCache& cache = p.cache;
     const int D = cache.dim, rows = p.Hq + 2 * cache.heads, lane = threadIdx.x & 31;
