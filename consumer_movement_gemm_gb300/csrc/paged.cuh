@@ -22,7 +22,7 @@ struct FastDiv {
         while (1ull << (s - 31) < d) ++s;
         m = ((1ull << s) + d - 1) / d;      // at most 2^32; m d - 2^s < d <= 2^(s - 31)
     }
-    __device__ __forceinline__ int div(unsigned x) const { return static_cast<int>(x * m >> s); }
+    __host__ __device__ int div(unsigned x) const { return static_cast<int>(x * m >> s); }
 };
 
 // tovl_kv_cache with strides in bytes.
@@ -110,9 +110,11 @@ AttnShape attn_decode_shape(int dim, bool e4m3, int group, bool pair);
 // side, us: 64 requests of 8192 tokens, 8 heads of 64, e4m3 197 and 139, bf16 198
 // and 182; 64 of 4096, 8 heads of 80, bf16 186 and 138.
 int attn_decode_together(const AttnShape& s, int heads, int dim, bool e4m3);
-// bf16 heads of more than 128 columns with more than 8 query heads: two warps take
-// two blocks of 8 from one ring, which leaves the shared memory for 12 warps (their
-// own rings: 6).  FIGURES
+// bf16 heads of more than 128 columns with an even number of blocks of 8 query
+// heads: two warps take two blocks from one ring, which leaves the shared memory
+// for 12 warps (with rings of their own: 6).  32 requests up to 8192 tokens, 1 head
+// of 256 for 16: 42 us, with rings of their own 46; with 16 heads a warp the sums do
+// not fit the registers.
 bool attn_decode_pairs(int dim, bool e4m3, int group);
 long long attn_decode_workspace(int heads, int group, int dim, int num_sms);
 cudaError_t prepare_attn_decode();

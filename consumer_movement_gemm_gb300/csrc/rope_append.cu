@@ -5,12 +5,13 @@
 // as two pieces of 8, half of what is rotated (or is not) apart, so that a warp's
 // accesses are whole lines.  So a lane has both numbers of every pair, (i, i +
 // rot/2) or interleaved (2 i, 2 i + 1), and eight cosines and sines, which it keeps
-// for one to four heads of its token; a CTA has one token.  Arithmetic is fp32,
+// for one or three heads of its token; a CTA has one token.  Arithmetic is fp32,
 // rounded once to bf16, or, for an e4m3 cache, to e4m3(x / scale) with scale =
 // max(max |x|, 1e-12) / 448 of the row.
 //
-// What bounds it: a launch and dependent loads (position, slot, table) for few
-// tokens; HBM for many.
+// What bounds it: a launch and dependent loads (position, slot, angles) for few
+// tokens (1 token, 32 + 2 x 8 heads of 128: 1.7 us); HBM for many (16384 tokens
+// 67 us, 6.1 TB/s, with 24 warps an SM; 72 us with the 22 of unlimited registers).
 #include <cuda_bf16.h>
 #include "common.cuh"
 #include "paged.cuh"
@@ -63,7 +64,8 @@ __device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const float
 
 // The quotients of a row by its scale, taken to 2^-46 by one residual before their
 // own rounding (Markstein 1990): a product with the inverse alone would round
-// twice, and miss ties.  16384 tokens of 48 heads of 128: FIGURES
+// twice, and miss ties.  16384 tokens, 32 + 2 x 8 heads of 128: 76 us, with the
+// product alone 73, with a division 88.
 struct Scale {
     float s, inverse;
     __device__ __forceinline__ explicit Scale(float top) : s((top < 1e-12f ? 1e-12f : top) / 448.f), inverse(1.f / s) {}
@@ -200,14 +202,13 @@ cudaError_t launch(const RopeParams& p, bool e4m3, int lanes, cudaStream_t strea
 
 cudaError_t launch_rope_append(const RopeParams& p, bool e4m3, int num_sms, cudaStream_t stream, bool pdl)
 {
-    const int lanes = (p.cache.dim + 15) / 16, per_warp = 32 / lanes, rows = p.Hq + 2 * p.cache.heads;
-    // several heads a lane where that leaves eight warps for every SM, three or four by
-    // the lanes that stay idle.  16384 tokens, 32 + 2 x 8 heads, three / four, us: of 128
-    // 72.2 / 72.7 (two 79), of 64 36.7 / 40.8, of 80 53.1 / 50.6, of 256 (8 + 2 x 2)
-    // 38.0 / 41.8; e4m3, of 128 81.5 / 87.9.  One is as good up to 256 tokens.
-    if (static_cast<long long>(p.T) * rows * lanes / 32 < 32LL * num_sms) return launch<1>(p, e4m3, lanes, stream, pdl);
-    const auto slots = [&](int n) { return ((rows + n - 1) / n + per_warp - 1) / per_warp * per_warp * n; };
-    return slots(3) <= slots(4) ? launch<3>(p, e4m3, lanes, stream, pdl) : launch<4>(p, e4m3, lanes, stream, pdl);
+    const int lanes = (p.cache.dim + 15) / 16;
+    // three heads a lane where that leaves eight warps for every SM.  16384 tokens, 32 +
+    // 2 x 8 heads, three / four, us: of 128 67.4 / 68.8 (two 74), of 64 35.3 / 37.9, of 80
+    // 49.7 / 51.3, of 256 (8 + 2 x 2) 35.7 / 38.4; e4m3, of 128 75.7 / 72.6.  Up to 256
+    // tokens one head is as good.
+    const long long warps = static_cast<long long>(p.T) * (p.Hq + 2 * p.cache.heads) * lanes / 32;
+    return warps < 32LL * num_sms ? launch<1>(p, e4m3, lanes, stream, pdl) : launch<3>(p, e4m3, lanes, stream, pdl);
 }
 
 }  // namespace tovl

@@ -415,9 +415,10 @@ typedef struct {
  *               may be length
  *   state_out   device, int32 [4]: the new state, then the number of new tokens
  *               and of lacking pages; may be state
- *   slots, positions device, int32 [cap], cap up to 2^30: for the new tokens of request 0, 1, ...
- *               in the order of their positions page * table[b][position / page]
- *               + position % page and position; behind the last -1 and 0
+ *   slots, positions device, int32 [cap], cap up to 2^30: for the new tokens of
+ *               request 0, 1, ... in the order of their positions page *
+ *               table[b][position / page] + position % page and position; behind
+ *               the last -1 and 0
  *   starts      device, int32 [B+1]: first new token of each request in slots,
  *               and their number
  * New pages are taken from the ring in the order of requests and positions;
@@ -464,9 +465,9 @@ long long tovl_attn_decode_workspace(tovl_handle h, int Hq, int heads, int dim);
  *   z[t] = scale * q[b][g] . k[t], t from max(0, length - window) (0 without a
  *   window) to length - 1, k and v of head g / (Hq / heads),
  *   out[b][g] = sum of softmax(z)[t] v[t], lse[b][g] = ln sum exp z[t]
- * with fp32 sums, rounded once to bf16.  Weights are off by 2^-15 of themselves with
- * a bf16 cache; with an e4m3 one 2^-11, and weights times scales below 2^-14 of
- * a row's largest an absolute 2^-25 of that.
+ * with fp32 sums, rounded once to bf16.  Weights are off by 2^-15 of themselves
+ * with a bf16 cache, with an e4m3 one by 2^-11, and where weight times scale is
+ * below 2^-14 of a row's largest by 2^-25 of that.
  *   q           device, bf16 [B][Hq][dim], requests ldq elements apart (a
  *               multiple of 8), 16-byte aligned; Hq a multiple of heads
  *   table       device, int32 [B][width], rows ldt apart
@@ -477,12 +478,16 @@ long long tovl_attn_decode_workspace(tovl_handle h, int Hq, int heads, int dim);
  *   lse         device, fp32 [B][Hq]; null = not wanted
  *   workspace   device, 256-byte aligned, any content; free again when the
  *               call's kernel has ended
- * Entries of the table outside the pages that hold seen tokens are not read,
- * nor are slots outside them.  A page outside [0, pages) or a length out of range sets
- * TOVL_ERR_INVALID in the status word; the request's result means nothing then.
- * Numbers that are infinite or NaN in seen rows show in the results that see
- * them.  The result of a call depends on its arguments alone (the same bits on
- * every call on the same device). */
+ * Entries of the table outside the pages that hold seen tokens are not read;
+ * what slots of those pages hold that no seen token lies in does not matter.
+ * A page outside [0, pages) or a length out of range sets TOVL_ERR_INVALID in
+ * the status word, and more than 2^31 tiles of 16 tokens and a key head set
+ * TOVL_ERR_UNSUPPORTED; the result of the request, or of all, means nothing then.
+ * Infinite and NaN keys and values that are seen show in the results that see
+ * them (an infinite value as infinite, or as NaN where its weight is 0 and in an
+ * e4m3 cache, where its scale is infinite); seen tokens whose scores are all
+ * -infinite give zeros and an lse of -inf.  The result of a call depends on its
+ * arguments alone (the same bits on every call on the same device). */
 int tovl_attn_decode(tovl_handle h, const void* q, long long ldq, int B, int Hq, const tovl_kv_cache* cache,
                      const int* table, long long ldt, int width, const int* length, float scale, int window,
                      void* out, long long ldo, float* lse, void* workspace, long long workspace_bytes, void* stream);

@@ -284,6 +284,114 @@ def test_attn_strided_rows_streams_and_a_null_lse(h):  # noqa: F811
     within(out, want, bound, "out")
 
 
+# heads whose rows are not whole 128-byte lines: two, four or eight neighbours go together
+@pytest.mark.parametrize("heads,dim,kind", [(8, 80, "bf16"), (8, 80, "e4m3"), (16, 64, "e4m3"), (4, 96, "bf16"), (8, 48, "e4m3"), (6, 80, "bf16"),
+                                            (8, 144, "bf16"), (8, 240, "e4m3"), (5, 64, "e4m3")])
+@pytest.mark.parametrize("G", [1, 8])
+def test_attn_heads_that_share_lines(h, heads, dim, kind, G):  # noqa: F811
+    g = gen(heads * 1000 + dim + G)
+    for lens in ([1], [3000, 0, 70, 900], [250] * 60, [9000]):
+        c, table, slots = filled(g, lens, heads, dim, 16, kind)
+        check_attn(h, randn(g, len(lens), heads * G, dim, scale=2), c, table, ints(lens), slots, dim ** -0.5, 0, str(lens[:3]))
+
+
+@pytest.mark.parametrize("heads,G,dim,kind", [(1, 1, 128, "bf16"), (2, 4, 64, "e4m3"), (1, 16, 256, "bf16")])
+def test_attn_every_length_of_one_request(h, heads, G, dim, kind):  # noqa: F811
+    """One CTA a head, several, all of them, and groups of them: lengths at which the shares change."""
+    g = gen(dim)
+    most = 60000
+    c, table, slots = filled(g, [most], heads, dim, 16, kind)
+    q = randn(g, 1, heads * G, dim, scale=2)
+    for n in (1, 16, 17, 32, 33, 191, 192, 193, 383, 385, 577, 1200, 1201, 3000, 4607, 4609, 9300, 9400, 20000, 29184, 29200, 58368, 58369, most):
+        check_attn(h, q, c, table, ints([n]), [slots[0][:n]], dim ** -0.5, 0, str(n))
+
+
+def test_attn_of_the_largest_batch(h):  # noqa: F811
+    """One token each: the output is its value, and the lse its score."""
+    g = gen(3)
+    B = 65536
+    c = Cache(B, 1, 1, 64, "bf16")
+    c.put("k", torch.arange(B, device=DEV), randn(g, B, 1, 64))
+    c.put("v", torch.arange(B, device=DEV), randn(g, B, 1, 64))
+    table = torch.randperm(B, generator=g, device=DEV).to(I32)[:, None]
+    lens = (torch.rand(B, generator=g, device=DEV) < 0.9).to(I32)
+    q = randn(g, B, 2, 64)
+    out, lse = torch.full_like(q, NAN), torch.full((B, 2), NAN, device=DEV)
+    h.attn_decode(q, c.cache, table, lens, 0.125, out, space(h.attn_decode_workspace(2, 1, 64)), lse=lse)
+    assert h.sync_status() == 0
+    row = table[:, 0].long()
+    v = torch.where(lens[:, None] > 0, c.v[row, 0, 0], 0)
+    within(out, v[:, None].to(D).expand(B, 2, 64), 2.0 ** -14 * v.abs()[:, None].to(D), "out")      # (a bf16 number is its own nearest)
+    z = 0.125 * (q.to(D) * c.k[row, 0].to(D)).sum(2)
+    seen = lens[:, None].expand(B, 2) > 0
+    assert torch.equal(lse == -math.inf, ~seen)
+    within(lse[seen], z[seen], 64 * U32 * (q.to(D).abs() * c.k[row, 0].to(D).abs()).sum(2)[seen] + 4 * U32 * 128, "lse")
+
+
+@pytest.mark.parametrize("kind,layout", [("bf16", "nhd"), ("e4m3", "hnd")])
+def test_a_cache_beyond_32_bit_offsets(h, kind, layout):  # noqa: F811
+    """Pages whose keys and values lie more than 2^32 bytes and elements from the first."""
+    g = gen(4)
+    heads, dim, page = 8, 128, 16
+    pages = 300000 if kind == "bf16" else 350000
+    assert pages * page * heads * dim > 2 ** 32
+    dt = BF16 if kind == "bf16" else E4M3
+    shape = (pages, page, heads, dim) if layout == "nhd" else (pages, heads, page, dim)
+    c = Cache(1, page, heads, dim, kind, layout)
+    c.k, c.v = (torch.empty(shape, dtype=dt, device=DEV) for _ in range(2))
+    if layout == "hnd":
+        c.k, c.v = c.k.transpose(1, 2), c.v.transpose(1, 2)
+    if kind != "bf16":
+        c.ks, c.vs = (torch.empty(pages, heads, page, device=DEV) for _ in range(2))
+    c.cache = tovl.KVCache(c.k, c.v, c.ks, c.vs)
+    n = 50
+    table = ints([pages - 1, 0, pages - 2, pages // 2 + 7])[None]
+    t = torch.arange(n, device=DEV)
+    slots = table[0].long()[t // page] * page + t % page
+    k, v = randn(g, n, heads, dim), randn(g, n, heads, dim)
+    h.rope_append(randn(g, n, 2 * heads, dim), k, v, t.to(I32), slots.to(I32), None, c.cache, torch.empty(n, 2 * heads, dim, dtype=BF16, device=DEV))
+    assert h.sync_status() == 0
+    if kind == "bf16":
+        assert torch.equal(c.rows("k", slots).to(BF16), k) and torch.equal(c.rows("v", slots).to(BF16), v)
+    check_attn(h, randn(g, 1, 2 * heads, dim, scale=2), c, table, ints([n]), [slots], dim ** -0.5, 0)
+
+
+def test_attn_scales_off_the_16_byte_boundaries(h):  # noqa: F811
+    """Boxes need aligned scales; without them rows are copied one by one."""
+    g = gen(7)
+    lens = [100, 40]
+    c, table, slots = filled(g, lens, 2, 64, 16, "e4m3")
+    q = randn(g, 2, 8, 64, scale=2)
+    out, _ = check_attn(h, q, c, table, ints(lens), slots, 0.125, 0)
+
+    def shifted(s):
+        t = torch.full((s.numel() + 4,), NAN, device=DEV)
+        t[1:1 + s.numel()] = s.flatten()
+        return t[1:1 + s.numel()].view(s.shape)
+    c.ks, c.vs = shifted(c.ks), shifted(c.vs)
+    c.cache = tovl.KVCache(c.k, c.v, c.ks, c.vs)
+    again, _ = check_attn(h, q, c, table, ints(lens), slots, 0.125, 0)
+    assert torch.equal(out, again)
+
+
+def test_without_programmatic_launches(h):  # noqa: F811
+    g = gen(8)
+    lens = [100, 4000]
+    c, table, slots = filled(g, lens, 2, 64, 16, "bf16")
+    q = randn(g, 2, 8, 64, scale=2)
+    out, _ = check_attn(h, q, c, table, ints(lens), slots, 0.125, 0)
+    h.set_option(tovl.OPT_PDL, 0)
+    try:
+        again, _ = check_attn(h, q, c, table, ints(lens), slots, 0.125, 0)
+        check_append(h, g, 5, 4, 2, 64, 64, 16, "bf16", "nhd", False)
+        p = Plan(3, 4, 12, 8)
+        dev = Planned(p)
+        same_plan(p, dev, p.step([9, 0, 20], 40), dev.step(h, [9, 0, 20], 40))
+    finally:
+        h.set_option(tovl.OPT_PDL, 1)
+    assert torch.equal(out, again)
+
+
 def test_attn_bad_pages_and_lengths_are_reported(h):  # noqa: F811
     """They are recognised on the device before an address is made of them."""
     g = gen(9)

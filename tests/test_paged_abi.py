@@ -39,7 +39,8 @@ def lib(tmp_path_factory):
                    "}\n"
                    'TOVL_API void* make() { auto* h = new tovl_ctx(); h->num_sms = 152; h->encode = encode; maps[12] = 0; return h; }\n'
                    'TOVL_API const long long* last_map() { return maps; }\n'
-                   'TOVL_API int count() { return launches; }\n')
+                   'TOVL_API int count() { return launches; }\n'
+                   'TOVL_API int divide(unsigned x, unsigned d) { return FastDiv(d).div(x); }\n')
     so = at / "paged.so"
     subprocess.run([tovl_build._nvcc(), *tovl_build._flags(), "-shared", "-cudart", "shared", "-o", str(so), str(src)], check=True,
                    capture_output=True)
@@ -166,6 +167,16 @@ def test_workspace_sizes(lib):
     assert lib.tovl_attn_decode_workspace(h, 8, 2, 64) == 4096
     for a in ((0, 1, 64), (8, 0, 64), (8, 3, 64), (8, 2, 0), (8, 2, 260), (8, 2, 60), (8192, 2, 64)):
         assert lib.tovl_attn_decode_workspace(h, *a) == -1, a
+
+
+def test_division_by_a_number_the_host_knows(lib):
+    import random
+    rng = random.Random(3)
+    lib.divide.argtypes = [ctypes.c_uint, ctypes.c_uint]
+    for d in [*range(1, 70), 4095, 4096, 4097, 2 ** 30 - 1, 2 ** 30, 2 ** 31 - 1, *(rng.randrange(1, 2 ** 31) for _ in range(300))]:
+        top = (2 ** 31 - 1) // d * d
+        for x in {0, 1, d - 1, d, min(d + 1, 2 ** 31 - 1), top, top - 1 if top else 0, 2 ** 31 - 1, rng.randrange(2 ** 31)}:
+            assert lib.divide(x, d) == x // d, (x, d)
 
 
 def test_null_handles_are_refused():
