@@ -645,21 +645,21 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
                 const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(p.q) + b * p.ldq;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const int h = nt * 8 + (lane >> 2);
-                    const __nv_bfloat16* row = qp + static_cast<long long>(head0 + h) * p.cache.dim;
+                    // (columns behind the last head repeat it, and their results are dropped)
+                    const int h = min(nt * 8 + (lane >> 2), n_heads - 1);
+                    const __nv_bfloat16* row = qp + static_cast<long long>(head0 + h) * p.cache.dim + (S::F8 ? 4 : 2) * (lane & 3);
                     float top = 0.f;
 #pragma unroll
                     for (int j = 0; j < JT; ++j) {
                         if constexpr (S::F8) {
-                            const int d = 16 * j + 4 * (lane & 3);
-                            const uint2 u = h < n_heads && d < p.cache.dim ? __ldg(reinterpret_cast<const uint2*>(row + d)) : make_uint2(0, 0);
+                            const uint2 u = 16 * j < p.cache.dim ? __ldg(reinterpret_cast<const uint2*>(row + 16 * j)) : make_uint2(0, 0);
                             q[nt][j][0] = u.x, q[nt][j][1] = u.y;
                             top = fmaxf(top, fmaxf(fmaxf(fabsf(bf_lo(u.x)), fabsf(bf_hi(u.x))), fmaxf(fabsf(bf_lo(u.y)), fabsf(bf_hi(u.y)))));
                         } else {
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
-                                const int d = 16 * j + 8 * i + 2 * (lane & 3);
-                                q[nt][j][i] = h < n_heads && d < p.cache.dim ? __ldg(reinterpret_cast<const uint32_t*>(row + d)) : 0u;
+                                const int d = 16 * j + 8 * i;
+                                q[nt][j][i] = d < p.cache.dim ? __ldg(reinterpret_cast<const uint32_t*>(row + d)) : 0u;
                             }
                         }
                     }
