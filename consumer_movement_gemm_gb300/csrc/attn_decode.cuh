@@ -237,11 +237,10 @@ __device__ __forceinline__ int tiles_of(const AttnParams& p, int len, int& first
     return len > 0 ? (len - 1) / TILE + 1 - first : 0;
 }
 
+// (p.most_tokens: what a table's row holds, and tiles of whole int positions)
 __device__ __forceinline__ int length_of(const AttnParams& p, int b)
 {
-    const int len = __ldg(p.length + b);
-    const long long most = static_cast<long long>(p.width) * p.cache.page;
-    return len < 0 ? 0 : len > most ? static_cast<int>(most) : len;
+    return min(max(__ldg(p.length + b), 0), p.most_tokens);
 }
 
 // A place in the order of the call: request, key head, block of its query
@@ -418,7 +417,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
     bool none = false, equal = true;
     for (int b = b0; b < min(p.B, b0 + chunk); ++b) {
         const int len = __ldg(p.length + b);
-        if (len < 0 || len > static_cast<long long>(p.width) * p.cache.page) record_error(p.ctrl, kErrInvalid);
+        if (len < 0 || len > p.most_tokens) record_error(p.ctrl, kErrInvalid);
         const int count = tiles_of<kTile>(p, length_of(p, b), unused);
         upto = min(upto + count, kMostTiles);
         none |= len <= 0;

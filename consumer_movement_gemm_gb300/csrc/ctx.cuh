@@ -78,12 +78,17 @@ inline long long ceil_div(long long a, long long b)
 
 struct DeviceGuard {
     int prev = 0;
+    bool moved;
     explicit DeviceGuard(int dev)
     {
         cudaGetDevice(&prev);
-        if (prev != dev) cudaSetDevice(dev);
+        moved = prev != dev;
+        if (moved) cudaSetDevice(dev);
     }
-    ~DeviceGuard() { cudaSetDevice(prev); }
+    ~DeviceGuard()
+    {
+        if (moved) cudaSetDevice(prev);
+    }
 };
 
 inline bool aligned(const void* p, unsigned n)

@@ -79,7 +79,8 @@ struct AttnParams {
     const int* table;       // [B][width], rows ldt apart
     const int* length;      // [B]
     long long ldq, ldo, ldt;
-    int B, Hq, group, width, window;
+    int B, Hq, group, window;
+    int most_tokens;        // of a request
     float scale_log2;       // scale * log2(e)
     KvCache cache;
     // boxed: pages are copied in boxes of 64 or 128 bytes of columns x rows of one

@@ -94,11 +94,10 @@ bool map_cache(tovl_ctx* h, AttnParams* p, bool e4m3, const AttnShape& shape, in
 
 }  // namespace
 
-TOVL_API int tovl_page_plan(tovl_handle h, const int* length, const int* add, int B, int* table, long long ldt, int width,
-                            int* ring, int pages, int page, const int* state, int* length_out, int* state_out, int* slots,
-                            int* positions, int cap, int* starts, void* stream)
+TOVL_API int tovl_page_plan(tovl_handle h, const tovl_page_plan_args* args, void* stream)
 {
-    if (!h) return TOVL_ERR_INVALID;
+    if (!h || !args) return TOVL_ERR_INVALID;
+    const auto [length, add, table, ring, state, length_out, state_out, slots, positions, starts, ldt, B, width, pages, page, cap] = *args;
     if (B < 0 || width < 1 || pages < 1 || page < 1 || cap < 0) return TOVL_ERR_INVALID;
     if (B > kMaxRequests || cap > kMaxNewTokens || static_cast<long long>(pages) * page > INT_MAX) return TOVL_ERR_UNSUPPORTED;
     if (B == 0) return TOVL_OK;
@@ -134,12 +133,10 @@ TOVL_API int tovl_page_plan(tovl_handle h, const int* length, const int* add, in
     return run(h, s, "page plan launch", [&](bool pdl) { return launch_page_plan(p, h->num_sms, s, pdl); });
 }
 
-TOVL_API int tovl_rope_append(tovl_handle h, const void* q, long long ldq, const void* k, long long ldk, const void* v,
-                              long long ldv, const int* positions, const int* slots, const float* cos_sin, int max_pos,
-                              int rot, int interleaved, int T, int Hq, const tovl_kv_cache* cache, void* q_out,
-                              long long ldqo, void* stream)
+TOVL_API int tovl_rope_append(tovl_handle h, const tovl_rope_append_args* args, void* stream)
 {
-    if (!h) return TOVL_ERR_INVALID;
+    if (!h || !args) return TOVL_ERR_INVALID;
+    const auto [q, k, v, q_out, positions, slots, cos_sin, cache, ldq, ldk, ldv, ldqo, T, Hq, max_pos, rot, interleaved] = *args;
     RopeParams p = {};
     const int rc = check_cache(cache, &p.cache);
     if (rc != TOVL_OK) return rc;
@@ -167,11 +164,12 @@ TOVL_API int tovl_rope_append(tovl_handle h, const void* q, long long ldq, const
     p.rot = rot;
     p.max_pos = max_pos;
     p.interleaved = interleaved != 0;
+    const bool e4m3 = cache->type == TOVL_E4M3;
     p.ctrl = h->ctrl;
     DeviceGuard g(h->device);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     return run(h, s, "rotary embedding launch",
-               [&](bool pdl) { return launch_rope_append(p, cache->type == TOVL_E4M3, h->num_sms, s, pdl); });
+               [&](bool pdl) { return launch_rope_append(p, e4m3, h->num_sms, s, pdl); });
 }
 
 TOVL_API long long tovl_attn_decode_workspace(tovl_handle h, int Hq, int heads, int dim)
@@ -180,11 +178,10 @@ TOVL_API long long tovl_attn_decode_workspace(tovl_handle h, int Hq, int heads, 
     return attn_decode_workspace(heads, Hq / heads, dim, h->num_sms);
 }
 
-TOVL_API int tovl_attn_decode(tovl_handle h, const void* q, long long ldq, int B, int Hq, const tovl_kv_cache* cache,
-                              const int* table, long long ldt, int width, const int* length, float scale, int window,
-                              void* out, long long ldo, float* lse, void* workspace, long long workspace_bytes, void* stream)
+TOVL_API int tovl_attn_decode(tovl_handle h, const tovl_attn_decode_args* args, void* stream)
 {
-    if (!h) return TOVL_ERR_INVALID;
+    if (!h || !args) return TOVL_ERR_INVALID;
+    const auto [q, out, lse, table, length, cache, workspace, ldq, ldo, ldt, workspace_bytes, B, Hq, width, window, scale] = *args;
     AttnParams p;
     std::memset(&p, 0, sizeof p);
     const int rc = check_cache(cache, &p.cache);
@@ -208,7 +205,8 @@ TOVL_API int tovl_attn_decode(tovl_handle h, const void* q, long long ldq, int B
     p.B = B;
     p.Hq = Hq;
     p.group = Hq / p.cache.heads;
-    p.width = width;
+    const long long held = static_cast<long long>(width) * p.cache.page;
+    p.most_tokens = held < INT_MAX - 63 ? static_cast<int>(held) : INT_MAX - 63;
     p.window = window;
     p.scale_log2 = scale * 1.44269504088896340736f;
     p.part = static_cast<float*>(workspace);

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -121,10 +122,10 @@ SIGNATURES = {
     "tovl_matvec_q4_workspace": ([_P, _I, _I], _LL),
     "tovl_matvec_q4": ([_P, _P, _I, _P, _LL, _I, _I, _P, _P, _P, _I, _I, _P, _LL, _P, _LL, _P], _I),
     "tovl_quantize_q4": ([_P, _P, _I, _I, _I, _I, _P, _P, _P, _P], _I),
-    "tovl_page_plan": ([_P, _P, _P, _I, _P, _LL, _I, _P, _I, _I, _P, _P, _P, _P, _P, _I, _P, _P], _I),
-    "tovl_rope_append": ([_P, _P, _LL, _P, _LL, _P, _LL, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _LL, _P], _I),
+    "tovl_page_plan": ([_P, _P, _P], _I),
+    "tovl_rope_append": ([_P, _P, _P], _I),
     "tovl_attn_decode_workspace": ([_P, _I, _I, _I], _LL),
-    "tovl_attn_decode": ([_P, _P, _LL, _I, _I, _P, _P, _LL, _I, _P, _F, _I, _P, _LL, _P, _P, _LL, _P], _I),
+    "tovl_attn_decode": ([_P, _P, _P], _I),
     "tovl_gemm_only": ([_P, _P, _I, _I, _P, _I, _P, _P], _I),
     "tovl_copy_only": ([_P, ctypes.POINTER(_P), _I, _I, _I, _P, _P], _I),
     "tovl_gated_copy": ([_P, _P, _P, _LL, _I, _P, _I, _I, _P], _I),
@@ -142,6 +143,11 @@ SIGNATURES = {
     "tovl_error_string": ([_I], ctypes.c_char_p),
     "tovl_last_error": ([_P], ctypes.c_char_p),
 }
+
+# the structs of arguments, packed in the order of their fields (a third of the time of as many ctypes arguments)
+_PLAN_ARGS = struct.Struct("@10Pq5i4x").pack
+_ROPE_ARGS = struct.Struct("@8P4q5i4x").pack
+_ATTN_ARGS = struct.Struct("@7P4q4if4x").pack
 
 _lib = None
 _lock = threading.Lock()
@@ -228,13 +234,6 @@ def _dense(name, t, dtype, shape):
         raise TypeError(f"{name} must be {dtype} {shape}")
     if not t.is_contiguous():
         raise TypeError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _ints(name, t, n) -> int:
-    """Checks a contiguous int32 tensor of n elements; returns its address."""
-    if t.dtype is not _I32 or t.numel() != n or not t.is_contiguous():
-        raise TypeError(f"{name} must be {n} contiguous elements of {_I32}")
     return t.data_ptr()
 
 
@@ -521,13 +520,27 @@ class Handle:
         ``length_out`` and ``state_out`` may be ``length`` and ``state``.  All int32."""
         if _BF16 is None:
             _load_types()
+        i32 = _I32
         B, width = table.shape
         cap, pages = slots.numel(), ring.numel()
+        ldt, last = table.stride()
+        if not (length.dtype is i32 and add.dtype is i32 and table.dtype is i32 and ring.dtype is i32 and state.dtype is i32 and
+                length_out.dtype is i32 and state_out.dtype is i32 and slots.dtype is i32 and positions.dtype is i32 and
+                starts.dtype is i32):
+            raise TypeError(f"tensors must be {i32}")
+        if not (length.numel() == add.numel() == length_out.numel() == B and state.numel() == state_out.numel() == 4 and
+                positions.numel() == cap and starts.numel() == B + 1):
+            raise TypeError("length, add and length_out have B elements, starts one more, state and state_out 4, positions as "
+                            "many as slots")
+        if not (length.is_contiguous() and add.is_contiguous() and ring.is_contiguous() and state.is_contiguous() and
+                length_out.is_contiguous() and state_out.is_contiguous() and slots.is_contiguous() and
+                positions.is_contiguous() and starts.is_contiguous() and (last == 1 or width == 1)):
+            raise TypeError("tensors must be contiguous, but for the distance of the table's rows")
         rc = (_lib or load()).tovl_page_plan(
-            self.h, _ints("length", length, B), _ints("add", add, B), B, table.data_ptr(), _matrix("table", table, _I32, B, width),
-            width, _ints("ring", ring, pages), pages, page, _ints("state", state, 4), _ints("length_out", length_out, B),
-            _ints("state_out", state_out, 4), _ints("slots", slots, cap), _ints("positions", positions, cap), cap,
-            _ints("starts", starts, B + 1), _stream(stream))
+            self.h, _PLAN_ARGS(length.data_ptr(), add.data_ptr(), table.data_ptr(), ring.data_ptr(), state.data_ptr(),
+                               length_out.data_ptr(), state_out.data_ptr(), slots.data_ptr(), positions.data_ptr(),
+                               starts.data_ptr(), ldt if B > 1 else width, B, width, pages, page, cap),
+            stream if stream.__class__ is int else _stream(stream))
         if rc:
             _check(self.h, rc, "tovl_page_plan")
 
@@ -540,16 +553,33 @@ class Handle:
         T, Hq, D = q.shape
         if D != cache.dim:
             raise TypeError(f"q must have {cache.dim} columns")
-        far = rot = 0
-        table = None
+        far = rot = table = 0
         if cos_sin is not None:
             far, rot = cos_sin.shape
-            table = _dense("cos_sin", cos_sin, _F32, (far, rot))
+            if cos_sin.dtype is not _F32 or not cos_sin.is_contiguous():
+                raise TypeError(f"cos_sin must be contiguous {_F32}")
+            table = cos_sin.data_ptr()
+        if not (positions.dtype is _I32 and slots.dtype is _I32 and positions.numel() == slots.numel() == T and
+                positions.is_contiguous() and slots.is_contiguous()):
+            raise TypeError(f"positions and slots must be contiguous {_I32} ({T},)")
+        heads = cache.heads
+        of_k = (T, heads, D)
+        lq, hq, dq = q.stride()
+        lk, hk, dk = k.stride()
+        lv, hv, dv = v.stride()
+        lo, ho, do = q_out.stride()
+        if not (dq == dk == dv == do == 1 and hq == hk == hv == ho == D and q.dtype is k.dtype is v.dtype is q_out.dtype
+                is _BF16 and q_out.shape == (T, Hq, D) and k.shape == of_k and v.shape == of_k):
+            # (one by one: what is wrong, or a dimension of 1 with any stride)
+            lq, lk, lv, lo = _heads("q", q, T, Hq, D), _heads("k", k, T, heads, D), _heads("v", v, T, heads, D), _heads(
+                "q_out", q_out, T, Hq, D)
+        elif T == 1:
+            lq = lo = (Hq * D + 7) // 8 * 8
+            lk = lv = (heads * D + 7) // 8 * 8
         rc = (_lib or load()).tovl_rope_append(
-            self.h, q.data_ptr(), _heads("q", q, T, Hq, D), k.data_ptr(), _heads("k", k, T, cache.heads, D), v.data_ptr(),
-            _heads("v", v, T, cache.heads, D), _ints("positions", positions, T), _ints("slots", slots, T),
-            table, far, rot, 1 if interleaved else 0, T, Hq, cache.ref, q_out.data_ptr(), _heads("q_out", q_out, T, Hq, D),
-            _stream(stream))
+            self.h, _ROPE_ARGS(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), positions.data_ptr(),
+                               slots.data_ptr(), table, cache.ref, lq, lk, lv, lo, T, Hq, far, rot, 1 if interleaved else 0),
+            stream if stream.__class__ is int else _stream(stream))
         if rc:
             _check(self.h, rc, "tovl_rope_append")
 
@@ -568,12 +598,18 @@ class Handle:
         B, Hq, D = q.shape
         if D != cache.dim:
             raise TypeError(f"q must have {cache.dim} columns")
-        width = table.shape[1]
+        rows, width = table.shape
+        ldt, last = table.stride()
+        if not (table.dtype is _I32 and length.dtype is _I32 and rows == length.numel() == B and length.is_contiguous() and
+                (last == 1 or width == 1) and (lse is None or (lse.dtype is _F32 and lse.shape == (B, Hq) and lse.is_contiguous()))):
+            raise TypeError(f"table must be {_I32} ({B}, width) with contiguous rows, length contiguous {_I32} ({B},), lse "
+                            f"contiguous {_F32} ({B}, {Hq})")
         rc = (_lib or load()).tovl_attn_decode(
-            self.h, q.data_ptr(), _heads("q", q, B, Hq, D), B, Hq, cache.ref, table.data_ptr(),
-            _matrix("table", table, _I32, B, width), width, _ints("length", length, B), scale, window,
-            out.data_ptr(), _heads("out", out, B, Hq, D), None if lse is None else _dense("lse", lse, _F32, (B, Hq)),
-            workspace.data_ptr(), _bytes("workspace", workspace), _stream(stream))
+            self.h, _ATTN_ARGS(q.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), table.data_ptr(),
+                               length.data_ptr(), cache.ref, workspace.data_ptr(), _heads("q", q, B, Hq, D),
+                               _heads("out", out, B, Hq, D), ldt if B > 1 else width, _bytes("workspace", workspace), B, Hq,
+                               width, window, scale),
+            stream if stream.__class__ is int else _stream(stream))
         if rc:
             _check(self.h, rc, "tovl_attn_decode")
 

@@ -377,9 +377,10 @@ int tovl_quantize_q4(tovl_handle h, const void* W, int E, int K, int N, int grou
  * slots for the step's new tokens, their rotary embedding with the cache
  * writes, and attention of one new token per request.  A cache is pages of
  * `page` slots that requests own through a block table: token t of request b
- * lies in slot t % page of page table[b][t / page].  None of the calls is a
- * protocol round; a batch of 0 requests or tokens does nothing.  Tensors do
- * not overlap unless said so. */
+ * lies in slot t % page of page table[b][t / page].  The calls take their
+ * arguments in a struct, read before they return (one pointer to pass where a
+ * short call's time is the host's).  None of them is a protocol round; a batch
+ * of 0 requests or tokens does nothing.  Tensors do not overlap unless said so. */
 
 /* Element (page p, slot s, head g, column d) of the keys and of the values is
  * p * page_stride + s * slot_stride + g * head_stride + d elements from k and
@@ -428,9 +429,21 @@ typedef struct {
  * cannot be (a length below 0 or add below -1, more tokens than width pages or
  * cap hold, more free pages than there are) leave everything as it was too, with
  * state_out[3] = -1, and set TOVL_ERR_INVALID in the status word. */
-int tovl_page_plan(tovl_handle h, const int* length, const int* add, int B, int* table, long long ldt, int width,
-                   int* ring, int pages, int page, const int* state, int* length_out, int* state_out, int* slots,
-                   int* positions, int cap, int* starts, void* stream);
+typedef struct {
+    const int* length;
+    const int* add;
+    int* table;
+    int* ring;
+    const int* state;
+    int* length_out;
+    int* state_out;
+    int* slots;
+    int* positions;
+    int* starts;
+    long long ldt;
+    int B, width, pages, page, cap;
+} tovl_page_plan_args;
+int tovl_page_plan(tovl_handle h, const tovl_page_plan_args* args, void* stream);
 
 /* Rotary embedding of queries and keys; keys and values to their cache slots.
  * With c and s the cosine and sine of pair i at the token's position,
@@ -451,10 +464,19 @@ int tovl_page_plan(tovl_handle h, const int* length, const int* add, int B, int*
  * Another slot or position sets TOVL_ERR_INVALID in the status word; its keys
  * and values are not written.  A NaN in a row of an e4m3 cache makes its scale
  * NaN. */
-int tovl_rope_append(tovl_handle h, const void* q, long long ldq, const void* k, long long ldk, const void* v,
-                     long long ldv, const int* positions, const int* slots, const float* cos_sin, int max_pos,
-                     int rot, int interleaved, int T, int Hq, const tovl_kv_cache* cache, void* q_out,
-                     long long ldqo, void* stream);
+typedef struct {
+    const void* q;
+    const void* k;
+    const void* v;
+    void* q_out;
+    const int* positions;
+    const int* slots;
+    const float* cos_sin;
+    const tovl_kv_cache* cache;
+    long long ldq, ldk, ldv, ldqo;
+    int T, Hq, max_pos, rot, interleaved;
+} tovl_rope_append_args;
+int tovl_rope_append(tovl_handle h, const tovl_rope_append_args* args, void* stream);
 
 /* Bytes of workspace that tovl_attn_decode needs on the handle's device, any
  * batch and lengths; -1 if the sizes are not supported. */
@@ -471,7 +493,7 @@ long long tovl_attn_decode_workspace(tovl_handle h, int Hq, int heads, int dim);
  *   q           device, bf16 [B][Hq][dim], requests ldq elements apart (a
  *               multiple of 8), 16-byte aligned; Hq a multiple of heads
  *   table       device, int32 [B][width], rows ldt apart
- *   length      device, int32 [B], 0 .. width * page; B 0 .. 65536
+ *   length      device, int32 [B], 0 .. width * page, below 2^31 - 63; B 0 .. 65536
  *   window      the last tokens that are seen; 0 = all
  *   out         device, bf16 [B][Hq][dim], ldo apart, like q; a request of
  *               length 0 gets zeros and an lse of -inf
@@ -488,9 +510,19 @@ long long tovl_attn_decode_workspace(tovl_handle h, int Hq, int heads, int dim);
  * e4m3 cache, where its scale is infinite); seen tokens whose scores are all
  * -infinite give zeros and an lse of -inf.  The result of a call depends on its
  * arguments alone (the same bits on every call on the same device). */
-int tovl_attn_decode(tovl_handle h, const void* q, long long ldq, int B, int Hq, const tovl_kv_cache* cache,
-                     const int* table, long long ldt, int width, const int* length, float scale, int window,
-                     void* out, long long ldo, float* lse, void* workspace, long long workspace_bytes, void* stream);
+typedef struct {
+    const void* q;
+    void* out;
+    float* lse;
+    const int* table;
+    const int* length;
+    const tovl_kv_cache* cache;
+    void* workspace;
+    long long ldq, ldo, ldt, workspace_bytes;
+    int B, Hq, width, window;
+    float scale;
+} tovl_attn_decode_args;
+int tovl_attn_decode(tovl_handle h, const tovl_attn_decode_args* args, void* stream);
 
 /* ---------------------------------------------------------------- controls
  * The acceptance method of the platform page, section 5, compares the fused

@@ -392,6 +392,22 @@ def test_without_programmatic_launches(h):  # noqa: F811
     assert torch.equal(out, again)
 
 
+def test_attn_lengths_near_the_largest_int(h):  # noqa: F811
+    """A table of 2^31 tokens, all in one page: a window at the end of the longest request, and a length beyond it."""
+    g = gen(10)
+    page = 1 << 20
+    c = Cache(1, page, 1, 16, "bf16")
+    c.k.copy_(randn(g, *c.k.shape))
+    c.v.copy_(randn(g, *c.v.shape))
+    table = torch.zeros(1, 2048, dtype=I32, device=DEV)
+    q = randn(g, 1, 2, 16)
+    n = 2 ** 31 - 64
+    slots = torch.arange(n - 100, n, device=DEV) % page
+    check_attn(h, q, c, table, ints([n]), [slots], 0.25, 100)
+    h.attn_decode(q, c.cache, table, ints([2 ** 31 - 1]), 0.25, torch.empty_like(q), space(h.attn_decode_workspace(2, 1, 16)), window=100)
+    assert h.sync_status() == tovl.TOVL_ERR_INVALID
+
+
 def test_attn_bad_pages_and_lengths_are_reported(h):  # noqa: F811
     """They are recognised on the device before an address is made of them."""
     g = gen(9)

@@ -40,6 +40,7 @@ def lib(tmp_path_factory):
                    'TOVL_API void* make() { auto* h = new tovl_ctx(); h->num_sms = 152; h->encode = encode; maps[12] = 0; return h; }\n'
                    'TOVL_API const long long* last_map() { return maps; }\n'
                    'TOVL_API int count() { return launches; }\n'
+                   'TOVL_API int size_of_args(int i) { return i == 0 ? sizeof(tovl_page_plan_args) : i == 1 ? sizeof(tovl_rope_append_args) : sizeof(tovl_attn_decode_args); }\n'
                    'TOVL_API int divide(unsigned x, unsigned d) { return FastDiv(d).div(x); }\n')
     so = at / "paged.so"
     subprocess.run([tovl_build._nvcc(), *tovl_build._flags(), "-shared", "-cudart", "shared", "-o", str(so), str(src)], check=True,
@@ -73,13 +74,34 @@ ATTN = dict(q=P, ldq=256, B=3, Hq=4, cache={}, table=P, ldt=5, width=5, length=P
             workspace=P, workspace_bytes=4096, stream=None)
 
 
+PACK = {"tovl_page_plan": (tovl._PLAN_ARGS, "length add table ring state length_out state_out slots positions starts ldt B width pages page cap"),
+        "tovl_rope_append": (tovl._ROPE_ARGS, "q k v q_out positions slots cos_sin cache ldq ldk ldv ldqo T Hq max_pos rot interleaved"),
+        "tovl_attn_decode": (tovl._ATTN_ARGS, "q out lse table length cache workspace ldq ldo ldt workspace_bytes B Hq width window scale")}
+
+
 def call(lib, name, base, **change):
     a = {**base, **change}
     if "cache" in a and a["cache"] is not None:
         a["cache"] = cache(**a["cache"])
     before = lib.count()
-    rc = getattr(lib, name)(lib.make(), *a.values())
+    pack, names = PACK[name]
+    rc = getattr(lib, name)(lib.make(), pack(*(0 if a[n] is None else a[n] for n in names.split())), a["stream"])
     return rc, lib.count() - before
+
+
+def test_the_binding_packs_the_structs_that_the_header_declares(lib):
+    import os
+    import re
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(tovl.__file__))), "include", "tovl.h")).read()
+    text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    for i, (name, (pack, names)) in enumerate(PACK.items()):
+        body = re.search(r"typedef struct \{([^}]*)\} " + name + "_args;", text).group(1)
+        fields = [n.strip(" *") for line in body.split(";") if line.strip()
+                  for n in re.sub(r"^\s*(const )?(void|float|int|long long|tovl_kv_cache)", "", line).split(",")]
+        assert fields == names.split(), name
+        assert pack.__self__.size == lib.size_of_args(i), name
+    for name in PACK:
+        assert getattr(lib, name)(lib.make(), None, None) == INVALID
 
 
 def test_what_fits_is_launched(lib):
