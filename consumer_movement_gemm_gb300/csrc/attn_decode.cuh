@@ -32,7 +32,7 @@
 // latency of the instructions between e4m3 row and product at three warps a
 // scheduler (4 of 65536 tokens: 90 us, 6.1 TB/s; heads of 64 5.6), and for few
 // tokens a chain of dependent steps: launch, lengths, shares, page, rows, products,
-// parts and their joins (1 request of 64 tokens 5.5 us, of 777 9.6, of 4096 11.2).
+// parts and their joins (1 request of 64 tokens 5.5 us, of 777 8.7, of 4096 10.8).
 // With eight warps instead of twelve the first takes 346 us, the third 105; with rows
 // by cp.async the first took 372 us where it took 350 with boxes.
 #pragma once
@@ -446,17 +446,20 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
         return;
     }
     const int total = all * groups, cta = blockIdx.x;
-    // CTAs that get work: all, or so many that a warp has kLeast tiles; with few
-    // segments of one length a multiple of them, so that few CTAs (or one) share a segment
+    // CTAs that get work: all, but with few tiles, in segments of one length, a multiple
+    // of the segments, so that none of them reaches into two.  A segment of up to three
+    // tiles a warp is one CTA's, because the join of CTAs costs more than two tiles; a
+    // longer one is split to a tile a warp, and from the twelfth CTA on to two, where more
+    // parts to join cost as much as they save.  One request, 8 heads: 300 tokens in one
+    // CTA a head 7.6 us, in equal parts over all CTAs 9.5; 777 in five 8.7, over all 11.7;
+    // 4096 in 12 10.8, in 19 11.6, over all 14.1.
     Shares shares = {static_cast<int>(gridDim.x), 0, 0, first_count, 0};
-    const int grid = gridDim.x, few = grid * turns * kLeast;
-    if (total < 2 * few) {
-        const int segments = p.B * groups;
-        if (equal && segments <= grid) {
-            const int want = p.by_least.div(first_count + turns * kLeast - 1), parts = min(want, grid / segments);
-            if (parts == want || segments * parts * 5 >= grid * 4) shares.parts = parts, shares.ctas = segments * parts;
-        }
-        if (!shares.parts && total < few) shares.ctas = p.by_least.div(total + turns * kLeast - 1);
+    const int grid = gridDim.x, segments = p.B * groups;
+    if (equal && segments <= grid && total < 4 * grid * turns) {
+        const int most = p.by_turns.div(first_count + turns - 1);
+        const int want = most <= 3 ? 1 : max(min(most, 12), (most + 1) / 2);
+        const int parts = min(want, grid / segments);
+        if (parts == want || segments * parts * 5 >= grid * 4) shares.parts = parts, shares.ctas = segments * parts;
     }
     // requests without tokens: nothing of theirs is in the order
     for (int b = blockIdx.x; none && b < p.B; b += gridDim.x) {

@@ -93,7 +93,7 @@ struct AttnParams {
     int together_log;       // log2 of the heads that neighbouring warps take side by side
     int pair;               // attn_decode_pairs: they are two blocks of one key head
     int* counter;           // [24 * kMaxGrid], handle-owned, zero between calls
-    FastDiv by_page, by_groups, by_turns, by_least;     // kLeast * turns
+    FastDiv by_page, by_groups, by_turns;      // turns: warps that take a segment's tiles in turn
     unsigned most_tiles;    // 2^31 / groups of heads
     long long timeout_ns;
     Ctrl ctrl;
@@ -103,7 +103,6 @@ struct AttnParams {
 struct AttnShape {
     int rows, box_bytes, warps, heads, part;
 };
-constexpr int kLeast = 2;              // tiles that a warp gets before more CTAs share a segment
 AttnShape attn_decode_shape(int dim, bool e4m3, int group, bool pair);
 // Key heads that neighbouring warps take side by side (1, 2, 4 or 8) where the
 // heads of a slot are adjacent: so many that their rows are whole 128-byte lines.

@@ -228,7 +228,6 @@ TOVL_API int tovl_attn_decode(tovl_handle h, const tovl_attn_decode_args* args, 
     p.by_page = FastDiv(p.cache.page);
     p.by_groups = FastDiv(groups);
     p.by_turns = FastDiv(turns);
-    p.by_least = FastDiv(turns * kLeast);
     p.most_tiles = INT_MAX / groups;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     return run(h, s, "attention launch",
