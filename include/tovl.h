@@ -424,6 +424,7 @@ typedef struct {
  *               and their number
  * New pages are taken from the ring in the order of requests and positions;
  * pages that a call gives back serve from the next call on, in the same order.
+ * A page is one request's: given back by two that share it, it is in the ring twice.
  * With too few free pages nothing changes: no new tokens (slots all -1),
  * length_out = length, state_out[3] = the pages that are lacking.  Counts that
  * cannot be (a length below 0 or add below -1, more tokens than width pages or
