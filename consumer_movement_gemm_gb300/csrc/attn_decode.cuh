@@ -342,41 +342,102 @@ struct Shares {
     }
 };
 
-// A float4 of O^T of a segment's parts, joined in their order: the sums relative to
-// the largest m of its two heads (x and z are of one, y and w of the other), six parts in
-// flight.
-__device__ __forceinline__ float4 join(const float* const* part, int n, int stats, int sums, int e, float2& m, float2& l)
+// U float4 of O^T of a segment's parts, 32 apart, joined in their order, six at a time:
+// the sums relative to the largest m of their two heads (x and z are of one, y and w of
+// the other).  The sums do not depend on U.
+template <int U>
+__device__ __forceinline__ void join(const float* const* part, int n, int stats, int sums, int e, float4 (&o)[U], float2& m, float2& l)
 {
     constexpr int kAhead = 6;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int u = 0; u < U; ++u) o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
     m = make_float2(-INFINITY, -INFINITY), l = make_float2(0.f, 0.f);
     for (int i = 0; i < n; i += kAhead) {
-        float2 pm[kAhead], pl[kAhead];
-        float4 v[kAhead];
+        // m and l of each part, then the weights; U > 1: a lane's each, of part lane / 4
+        // and heads 2 (lane % 4)
+        constexpr int kOwn = U == 1 ? kAhead : 1;
+        float2 w[kOwn], s[kOwn];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            pm[k] = make_float2(-INFINITY, -INFINITY), pl[k] = make_float2(0.f, 0.f), v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (i + k >= n) continue;
-            const float* const q = part[i + k];
-            pm[k] = ld_part(reinterpret_cast<const float2*>(q + stats)), pl[k] = ld_part(reinterpret_cast<const float2*>(q + stats + sums));
-            v[k] = ld_part(reinterpret_cast<const float4*>(q) + e);
+        for (int k = 0; k < kOwn; ++k) {
+            const int which = U == 1 ? k : lane / 4;
+            w[k] = make_float2(-INFINITY, -INFINITY), s[k] = make_float2(0.f, 0.f);
+            if (which >= kAhead || i + which >= n) continue;
+            const float* const q = part[i + which] + stats;
+            w[k] = ld_part(reinterpret_cast<const float2*>(q)), s[k] = ld_part(reinterpret_cast<const float2*>(q + sums));
         }
+        float4 v[kAhead][U];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                v[k][u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i + k < n) v[k][u] = ld_part(reinterpret_cast<const float4*>(part[i + k]) + e + u * 32);
+            }
         const float2 was = m;
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) m.x = fmaxf(m.x, pm[k].x), m.y = fmaxf(m.y, pm[k].y);
+        for (int k = 0; k < kOwn; ++k) m.x = fmaxf(m.x, w[k].x), m.y = fmaxf(m.y, w[k].y);
+        if (U > 1)
+#pragma unroll
+            for (int d = 4; d < 32; d *= 2) m.x = fmaxf(m.x, __shfl_xor_sync(0xffffffffu, m.x, d)), m.y = fmaxf(m.y, __shfl_xor_sync(0xffffffffu, m.y, d));
         const float u0 = m.x == -INFINITY ? 0.f : m.x, u1 = m.y == -INFINITY ? 0.f : m.y;
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k) w[k].x = ex2(w[k].x - u0), w[k].y = ex2(w[k].y - u1);
         if (i) {
             const float c0 = ex2(was.x - u0), c1 = ex2(was.y - u1);
-            o.x *= c0, o.y *= c1, o.z *= c0, o.w *= c1, l.x *= c0, l.y *= c1;
+            l.x *= c0, l.y *= c1;
+#pragma unroll
+            for (int u = 0; u < U; ++u) o[u].x *= c0, o[u].y *= c1, o[u].z *= c0, o[u].w *= c1;
         }
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            const float w0 = ex2(pm[k].x - u0), w1 = ex2(pm[k].y - u1);
-            o.x += v[k].x * w0, o.y += v[k].y * w1, o.z += v[k].z * w0, o.w += v[k].w * w1;
-            l.x += pl[k].x * w0, l.y += pl[k].y * w1;
+            float2 wk = w[k % kOwn], sk = s[k % kOwn];
+            if (U > 1) {
+                const int from = k * 4 + (lane & 3);
+                wk.x = __shfl_sync(0xffffffffu, wk.x, from), wk.y = __shfl_sync(0xffffffffu, wk.y, from);
+                sk.x = __shfl_sync(0xffffffffu, sk.x, from), sk.y = __shfl_sync(0xffffffffu, sk.y, from);
+            }
+            l.x = fmaf(sk.x, wk.x, l.x), l.y = fmaf(sk.y, wk.y, l.y);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                o[u].x = fmaf(v[k][u].x, wk.x, o[u].x), o[u].y = fmaf(v[k][u].y, wk.y, o[u].y);
+                o[u].z = fmaf(v[k][u].z, wk.x, o[u].z), o[u].w = fmaf(v[k][u].w, wk.y, o[u].w);
+            }
         }
     }
-    return o;
+}
+
+// The segments of a list, U column blocks of 16 of 8 heads a warp.
+template <class S, int U>
+__device__ __forceinline__ void join_all(const AttnParams& p, const Joined* joined, const float* const* parts, int count, int warp, int lane)
+{
+    constexpr int kOfHeads = S::JT / U, kUnits = S::NT * kOfHeads;
+    for (int at = warp; at < count * kUnits; at += S::kWarps) {
+        const Joined seg = joined[at / kUnits];
+        const int nt = at % kUnits / kOfHeads, j0 = at % kOfHeads * U, e = (nt * S::JT + j0) * 32 + lane, h = nt * 8 + 2 * (lane & 3);
+        float2 m, l;
+        float4 sum[U];
+        join<U>(parts + seg.entry, seg.n, S::kFrag * 4 + h, S::kHeads, e, sum, m, l);
+        const bool stats = j0 == 0 && lane < 4;
+        if (seg.to) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) reinterpret_cast<float4*>(seg.to)[e + u * 32] = sum[u];
+            if (stats) {
+                *reinterpret_cast<float2*>(seg.to + S::kFrag * 4 + h) = m;
+                *reinterpret_cast<float2*>(seg.to + S::kFrag * 4 + S::kHeads + h) = l;
+            }
+        } else {
+            __nv_bfloat16* const row = static_cast<__nv_bfloat16*>(p.out) + seg.b * p.ldo + static_cast<long long>(seg.head0 + nt * 8) * p.cache.dim;
+            const float i0 = over<S>(l.x), i1 = over<S>(l.y);
+#pragma unroll
+            for (int u = 0; u < U; ++u) store_pair<S>(row, p.cache.dim, seg.n_heads - nt * 8, j0 + u, lane, sum[u], i0, i1);
+            if (stats && p.lse) {
+                float* const lse = p.lse + static_cast<long long>(seg.b) * p.Hq + seg.head0;
+                if (h < seg.n_heads) lse[h] = lse_of<S>(m.x, l.x);
+                if (h + 1 < seg.n_heads) lse[h + 1] = lse_of<S>(m.y, l.y);
+            }
+        }
+    }
 }
 
 template <class S>
@@ -596,7 +657,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
     if (tiles > 0) {
         if (warp == owner) {
             find_pages();
-#pragma unroll 1
+#pragma unroll
             for (int s = 0; s < kRingStages; ++s) fetch(s);
         }
         // fragments of k: row lane % 16, 16 bytes lane / 16; of v: the same (e4m3),
@@ -979,29 +1040,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
             }
         }
         __syncwarp();
-        // a warp for 32 float4
-        for (int at = tid; at < count * S::kFrag; at += S::kThreads) {
-            const Joined seg = s_joined[at / S::kFrag];
-            const int e = at % S::kFrag, j = e / 32 % JT, nt = e / 32 / JT, h = nt * 8 + 2 * (lane & 3);
-            float2 m, l;
-            const float4 sum = join(s_part + seg.entry, seg.n, S::kFrag * 4 + h, S::kHeads, e, m, l);
-            const bool stats = j == 0 && lane < 4;
-            if (seg.to) {
-                reinterpret_cast<float4*>(seg.to)[e] = sum;
-                if (stats) {
-                    *reinterpret_cast<float2*>(seg.to + S::kFrag * 4 + h) = m;
-                    *reinterpret_cast<float2*>(seg.to + S::kFrag * 4 + S::kHeads + h) = l;
-                }
-            } else {
-                __nv_bfloat16* const row = static_cast<__nv_bfloat16*>(p.out) + seg.b * p.ldo + static_cast<long long>(seg.head0 + nt * 8) * p.cache.dim;
-                store_pair<S>(row, p.cache.dim, seg.n_heads - nt * 8, j, lane, sum, over<S>(l.x), over<S>(l.y));
-                if (stats && p.lse) {
-                    float* const lse = p.lse + static_cast<long long>(seg.b) * p.Hq + seg.head0;
-                    if (h < seg.n_heads) lse[h] = lse_of<S>(m.x, l.x);
-                    if (h + 1 < seg.n_heads) lse[h + 1] = lse_of<S>(m.y, l.y);
-                }
-            }
-        }
+        // as many column blocks a warp as leave none idle
+        constexpr int kBlocks = NT * JT;
+        if (count * kBlocks <= S::kWarps) join_all<S, 1>(p, s_joined, s_part, count, warp, lane);
+        else join_all<S, 2>(p, s_joined, s_part, count, warp, lane);
         if (round >= 0) arriving |= list & __ballot_sync(0xffffffffu, in_group);
         if (!won) {
             if (!arriving) return;
