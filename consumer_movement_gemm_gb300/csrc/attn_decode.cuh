@@ -32,7 +32,7 @@
 // latency of the instructions between e4m3 row and product at three warps a
 // scheduler (4 of 65536 tokens: 90 us, 6.1 TB/s; heads of 64 5.6), and for few
 // tokens a chain of dependent steps: launch, lengths, shares, page, rows, products,
-// parts and their joins (1 request of 64 tokens 5.5 us, of 777 8.7, of 4096 10.8).
+// parts and their joins (1 request of 64 tokens 5.5 us, of 777 9.0, of 4096 11.0).
 // With eight warps instead of twelve the first takes 346 us, the third 105; with rows
 // by cp.async the first took 372 us where it took 350 with boxes.
 #pragma once
@@ -1040,7 +1040,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
             }
         }
         __syncwarp();
-        // as many column blocks a warp as leave none idle
+        // Two column blocks a warp where one each leaves no warp idle: more loads in
+        // flight and the weights worked out once.  Two / one, us: 32 requests up to 8192
+        // tokens, 1 head of 256 for 16, 39 / 42; 1 of 32768, 1 head of 128 for 16, 16.3 / 18.4;
+        // 256 up to 2048, 8 for 64, e4m3, 101 / 104.
         constexpr int kBlocks = NT * JT;
         if (count * kBlocks <= S::kWarps) join_all<S, 1>(p, s_joined, s_part, count, warp, lane);
         else join_all<S, 2>(p, s_joined, s_part, count, warp, lane);

@@ -207,6 +207,23 @@ def test_attn_window(h, window, kind, dim):  # noqa: F811
     check_attn(h, randn(g, len(lens), 8, dim, scale=2), c, table, ints(lens), slots, dim ** -0.5, window)
 
 
+@pytest.mark.parametrize("lens,heads,G,dim,kind", [(range(300, 1900, 50), 1, 16, 256, "bf16"), (range(100, 2100, 20), 2, 8, 128, "e4m3"),
+                                                   ([16000], 1, 16, 128, "bf16"), ([9000, 8000, 100], 2, 4, 96, "bf16")],
+                         ids=lambda v: str(v)[:12])
+def test_attn_same_bits_whichever_cta_joins(h, lens, heads, G, dim, kind):  # noqa: F811
+    """The order in which the CTAs of a segment finish differs from call to call, and with it how many are joined at once."""
+    lens = list(lens)
+    g = gen(sum(lens))
+    c, table, slots = filled(g, lens, heads, dim, 16, kind)
+    q = randn(g, len(lens), heads * G, dim, scale=2)
+    first, lse = check_attn(h, q, c, table, ints(lens), slots, dim ** -0.5, 0)
+    ws = torch.empty(h.attn_decode_workspace(heads * G, heads, dim), dtype=torch.uint8, device=DEV)
+    out, stats = torch.empty_like(first), torch.empty_like(lse)
+    for _ in range(50):
+        h.attn_decode(q, c.cache, table, ints(lens), dim ** -0.5, out, ws, lse=stats)
+        assert torch.equal(out, first) and torch.equal(stats, lse)
+
+
 @pytest.mark.parametrize("lens,heads,G,dim,kind", [([70001], 1, 1, 128, "bf16"), ([70001], 1, 16, 128, "e4m3"), ([20000, 1, 50000], 4, 8, 64, "bf16"),
                                                    ([30011] * 3, 2, 5, 256, "e4m3"), ([9000] * 40, 1, 4, 80, "bf16"),
                                                    ([300] * 500, 2, 4, 128, "bf16"), ([17] * 3000, 1, 2, 64, "e4m3")],
