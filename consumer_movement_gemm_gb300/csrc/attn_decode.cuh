@@ -243,6 +243,13 @@ __device__ __forceinline__ int length_of(const AttnParams& p, int b)
     return min(max(__ldg(p.length + b), 0), p.most_tokens);
 }
 
+// a / b.  Below 2^20 (a + 1/2) / b is at least 1 / (2 b) from a whole number, and the
+// quotient of floats off by 1 / (4 b) at most.
+__device__ __forceinline__ int quotient(int a, int b)
+{
+    return a < 1 << 20 ? static_cast<int>(__fdividef(a + 0.5f, static_cast<float>(b))) : a / b;
+}
+
 // A place in the order of the call: request, key head, block of its query
 // heads, tile.
 template <class S>
@@ -259,7 +266,7 @@ struct Cursor {
     __device__ __forceinline__ void at_head(int v, int per_head)
     {
         vh = v;
-        head = per_head == 1 ? v : v / per_head;
+        head = per_head == 1 ? v : quotient(v, per_head);
         block = v - head * per_head;
     }
     // together: blocks of heads that neighbouring warps take side by side
@@ -338,7 +345,7 @@ struct Shares {
     __device__ __forceinline__ int owner(int tile) const
     {
         const int longer = rest * (each + 1);
-        return tile < longer ? tile / (each + 1) : rest + (tile - longer) / each;
+        return tile < longer ? quotient(tile, each + 1) : rest + quotient(tile - longer, each);
     }
 };
 
@@ -519,7 +526,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
     if (equal && segments <= grid && total < 4 * grid * turns) {
         const int most = p.by_turns.div(first_count + turns - 1);
         const int want = most <= 3 ? 1 : max(min(most, 12), (most + 1) / 2);
-        const int parts = min(want, grid / segments);
+        const int parts = min(want, quotient(grid, segments));
         if (parts == want || segments * parts * 5 >= grid * 4) shares.parts = parts, shares.ctas = segments * parts;
     }
     // requests without tokens: nothing of theirs is in the order
@@ -533,10 +540,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
     if (total == 0 || cta >= shares.ctas) return;
     int whole = total, among = shares.ctas, place = cta, offset = 0;
     if (shares.parts) {
-        const int segment = cta / shares.parts;
+        const int segment = quotient(cta, shares.parts);
         whole = first_count, among = shares.parts, place = cta - segment * shares.parts, offset = segment * first_count;
     }
-    shares.each = whole / among, shares.rest = whole - shares.each * among;
+    shares.each = quotient(whole, among), shares.rest = whole - shares.each * among;
     const int cta_from = offset + shares.start(place), cta_to = offset + shares.start(place + 1);
 
     // this warp's share, and the request that its first tile lies in
@@ -559,7 +566,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
             if (r < put.count * groups) break;
             r -= put.count * groups;
         }
-        const int group = r / put.count;
+        const int group = quotient(r, put.count);
         put.at_head(group * together + beside, per_head);
         put.tile = put.first + r - group * put.count;
     }
