@@ -11,8 +11,8 @@
 // state) is written by the CTA that finishes last, when all others have read it.
 //
 // What bounds it: latency (a launch, the loads of the counts, the sums, the
-// bisections, the loads of ring and table): 256 requests with one token each 3.9
-// us, prompts of 62000 tokens 3.9 us.
+// bisections, the loads of ring and table): 256 requests with one token each 3.5
+// us, prompts of 62000 tokens 4.1 us.
 #include "common.cuh"
 #include "paged.cuh"
 #include "sync.cuh"
@@ -21,12 +21,12 @@ namespace tovl {
 
 namespace {
 
-constexpr int kPlanThreads = 512;
-constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr unsigned kMostSum = 0x7fffffffu;       // the sums stop there
 
+template <int kPlanThreads>
 __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlanParams p)
 {
+    constexpr int kPlanWarps = kPlanThreads / 32;
     extern __shared__ int sums[];          // lengths; inclusive sums: tokens, pages taken, pages given back
     __shared__ unsigned s_warp[3][kPlanWarps];
     __shared__ int s_last;
@@ -174,19 +174,30 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlanP
     }
 }
 
-}  // namespace
-
-cudaError_t prepare_page_plan()
-{
-    return cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 16 * kMaxRequests);
-}
-
-cudaError_t launch_page_plan(const PagePlanParams& p, int num_sms, cudaStream_t stream, bool pdl)
+template <int kPlanThreads>
+cudaError_t launch(const PagePlanParams& p, int num_sms, cudaStream_t stream, bool pdl)
 {
     // (the pages that ended requests give back are not known here: room for a few of each)
     const long long items = p.cap > 8 * p.B ? p.cap : 8 * p.B, want = (items + kPlanThreads - 1) / kPlanThreads;
     const int grid = want < 1 ? 1 : want < num_sms ? static_cast<int>(want) : num_sms;
-    return launch_grid(page_plan_kernel, p, grid, kPlanThreads, 16 * p.B, stream, false, pdl);
+    return launch_grid(page_plan_kernel<kPlanThreads>, p, grid, kPlanThreads, 16 * p.B, stream, false, pdl);
+}
+
+}  // namespace
+
+cudaError_t prepare_page_plan()
+{
+    return cudaFuncSetAttribute(page_plan_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize, 16 * kMaxRequests);
+}
+
+// Threads of a CTA: one for each request, where there are many a few, so that sums and
+// barriers are short.  256 / 512 / 1024 threads, us: 256 requests 3.6 / 4.0 / 5.2, 1024 4.8
+// / 4.5 / 5.7, 4096 14.3 / 9.5 / 8.4.
+cudaError_t launch_page_plan(const PagePlanParams& p, int num_sms, cudaStream_t stream, bool pdl)
+{
+    if (p.B <= 256) return launch<256>(p, num_sms, stream, pdl);
+    if (p.B <= 2048) return launch<512>(p, num_sms, stream, pdl);
+    return launch<1024>(p, num_sms, stream, pdl);
 }
 
 }  // namespace tovl
