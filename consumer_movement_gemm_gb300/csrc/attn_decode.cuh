@@ -1047,13 +1047,14 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
             }
         }
         __syncwarp();
-        // Two column blocks a warp where one each leaves no warp idle: more loads in
-        // flight and the weights worked out once.  Two / one, us: 32 requests up to 8192
-        // tokens, 1 head of 256 for 16, 39 / 42; 1 of 32768, 1 head of 128 for 16, 16.3 / 18.4;
-        // 256 up to 2048, 8 for 64, e4m3, 101 / 104.
-        constexpr int kBlocks = NT * JT;
-        if (count * kBlocks <= S::kWarps) join_all<S, 1>(p, s_joined, s_part, count, warp, lane);
-        else join_all<S, 2>(p, s_joined, s_part, count, warp, lane);
+        // Two column blocks a warp, of wide parts four (where the registers hold them), if
+        // half of them each leaves no warp idle: more loads in flight, and the weights
+        // worked out once.  Two / one, us: 1 request of 32768, 1 head of 128 for 16, 16.3 /
+        // 18.4; 256 up to 2048, 8 for 64, e4m3, 101 / 104.  Four / two: 32 of 2048, 1 head
+        // of 256 for 16, e4m3, 22.5 / 24.9.
+        constexpr int kBlocks = NT * JT, kLeast = kBlocks > S::kWarps ? 2 : 1, kMost = kLeast == 2 && S::kWarps <= 8 ? 4 : 2;
+        if (count * kBlocks <= kLeast * S::kWarps) join_all<S, kLeast>(p, s_joined, s_part, count, warp, lane);
+        else join_all<S, kMost>(p, s_joined, s_part, count, warp, lane);
         if (round >= 0) arriving |= list & __ballot_sync(0xffffffffu, in_group);
         if (!won) {
             if (!arriving) return;
