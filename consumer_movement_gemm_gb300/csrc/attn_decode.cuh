@@ -22,8 +22,8 @@
 // to the warps of a grid that fills the GPU, whatever the lengths.  A warp streams
 // its tiles through a ring of its own in shared memory, across the ends of segments
 // (one request and head), without a CTA barrier; boxes of page x columns come by TMA
-// (where pages are no multiples of 8 slots, rows by cp.async).  Segments that
-// several warps share leave (m, sum, O) behind; the CTA joins its warps', and of
+// (where pages are no multiples of 8 slots or short rows lie off the 32-byte
+// sectors, rows by cp.async).  Segments that several warps share leave (m, sum, O) behind; the CTA joins its warps', and of
 // CTAs that share a segment the last to finish joins theirs, in the order of the
 // tokens, so that a call's bits depend on its arguments alone.
 //
