@@ -23,9 +23,10 @@
 // its tiles through a ring of its own in shared memory, across the ends of segments
 // (one request and head), without a CTA barrier; boxes of page x columns come by TMA
 // (where pages are no multiples of 8 slots or short rows lie off the 32-byte
-// sectors, rows by cp.async).  Segments that several warps share leave (m, sum, O) behind; the CTA joins its warps', and of
-// CTAs that share a segment the last to finish joins theirs, in the order of the
-// tokens, so that a call's bits depend on its arguments alone.
+// sectors, rows by cp.async).  Segments that several warps share leave (m, sum, O)
+// behind; the CTA joins its warps', and of CTAs that share a segment the last to
+// finish joins theirs, in the order of the tokens, so that a call's bits depend on
+// its arguments alone.
 //
 // What bounds it: HBM with bf16 rows (64 requests up to 16384 tokens, 8 heads of
 // 128 for 32: 330 us, 6.6 TB/s; 16 of 16384, 32 heads for 32: 626 us, 6.9 TB/s),
