@@ -220,9 +220,12 @@ __device__ __forceinline__ float rest(float w) { return fmaxf(w - bf_hi(__float_
 
 // The weight of e4m3 rows is exp2(score - m) times the row's scale, m the
 // largest score + log2(scale), so that the product's operand is 2^kSlack at most.  The
-// sum takes the same exponential without the scale; the shift keeps it inside
-// fp32 for any scale that a row of finite bf16 numbers can have (2^-49 .. 2^120).
+// sum takes the same exponential without the scale, 2^(kShift + kSlack) / scale at most.
+// Smaller scales than 2^kLeastScale count as that in m, so a term is below 2^97 and the
+// sum of 2^31 inside fp32; 1e-12 / 448, the least that rope_append writes, is above it.
+// The shift keeps the terms of large scales: of 2^127 down to 2^-39 of the largest.
 constexpr float kShift = 40.f;
+constexpr float kLeastScale = -48.75f;
 
 // A score may be over the maximum that weights are taken relative to by this much
 // (weights up to 256) before it becomes the maximum: a tile then costs one vote,
@@ -289,11 +292,12 @@ struct Cursor {
     }
 };
 
-// What a sum of weights divides: 1 / l, without the shift.
+// What a sum of weights divides: 1 / l, without the shift.  (__fdividef is 0 from 2^126 on.)
 template <class S>
 __device__ __forceinline__ float over(float l)
 {
-    return l == 0.f ? 0.f : __fdividef(S::F8 ? 0x1p40f : 1.f, l);
+    if (l == 0.f) return 0.f;
+    return S::F8 ? __fdividef(0x1p8f, l * 0x1p-32f) : __fdividef(1.f, l);
 }
 
 // Stores float4 j of a lane's O^T, times i0 and i1 (its two heads'): rows of out
@@ -817,7 +821,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
                     if (S::F8) {
                         ks = scales[r];
                         vs[mt][i] = scales[kTile + r] * 0x1p-40f;
-                        vl[mt][i] = fmaxf(lg2(scales[kTile + r]), -80.f);
+                        vl[mt][i] = fmaxf(lg2(scales[kTile + r]), kLeastScale);
                     }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {

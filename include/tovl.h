@@ -385,7 +385,7 @@ int tovl_quantize_q4(tovl_handle h, const void* W, int E, int K, int N, int grou
 /* Element (page p, slot s, head g, column d) of the keys and of the values is
  * p * page_stride + s * slot_stride + g * head_stride + d elements from k and
  * v.  An e4m3 cache has one fp32 scale per slot and head for each of the two:
- * a row stands for its elements times k_scale (v_scale) [p][g][s], positive
+ * a row stands for its elements times k_scale (v_scale) [p][g][s], not negative
  * and contiguous.  k and v are 16-byte aligned, dim and the strides multiples
  * of 16 bytes, strides at least dim (those of extents of 1 are not used). */
 typedef struct {
@@ -489,8 +489,9 @@ long long tovl_attn_decode_workspace(tovl_handle h, int Hq, int heads, int dim);
  *   window) to length - 1, k and v of head g / (Hq / heads),
  *   out[b][g] = sum of softmax(z)[t] v[t], lse[b][g] = ln sum exp z[t]
  * with fp32 sums, rounded once to bf16.  Weights are off by 2^-15 of themselves
- * with a bf16 cache, with an e4m3 one by 2^-11, and where weight times scale is
- * below 2^-14 of a row's largest by 2^-25 of that.
+ * with a bf16 cache, with an e4m3 one by 2^-11, and where weight times v_scale is
+ * below 2^-14 of a row's largest by 2^-25 of that, or by 2^-73 where the largest
+ * is below 2^-48.  With an e4m3 cache scores are up to 2^26 in magnitude.
  *   q           device, bf16 [B][Hq][dim], requests ldq elements apart (a
  *               multiple of 8), 16-byte aligned; Hq a multiple of heads
  *   table       device, int32 [B][width], rows ldt apart
