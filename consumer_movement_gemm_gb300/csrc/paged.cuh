@@ -94,7 +94,7 @@ struct AttnParams {
     int pair;               // attn_decode_pairs: they are two blocks of one key head
     int* counter;           // [24 * kMaxGrid], handle-owned, zero between calls
     FastDiv by_page, by_groups, by_turns;      // turns: warps that take a segment's tiles in turn
-    unsigned most_tiles;    // 2^31 / groups of heads
+    unsigned most_tiles;    // of a head: below 2^31 - 1 in all, where the kernel's sums stop
     long long timeout_ns;
     Ctrl ctrl;
 };

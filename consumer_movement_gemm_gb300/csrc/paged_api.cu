@@ -233,7 +233,7 @@ TOVL_API int tovl_attn_decode(tovl_handle h, const tovl_attn_decode_args* args, 
     p.by_page = FastDiv(p.cache.page);
     p.by_groups = FastDiv(groups);
     p.by_turns = FastDiv(turns);
-    p.most_tiles = INT_MAX / groups;
+    p.most_tiles = (INT_MAX - 1) / groups;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     return run(h, s, "attention launch",
                [&](bool pdl) { return launch_attn_decode(p, e4m3, h->num_sms, s, pdl); });

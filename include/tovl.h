@@ -505,8 +505,9 @@ long long tovl_attn_decode_workspace(tovl_handle h, int Hq, int heads, int dim);
  * Entries of the table outside the pages that hold seen tokens are not read;
  * what slots of those pages hold that no seen token lies in does not matter.
  * A page outside [0, pages) or a length out of range sets TOVL_ERR_INVALID in
- * the status word, and more than 2^31 tiles of 16 tokens and a key head set
- * TOVL_ERR_UNSUPPORTED; the result of the request, or of all, means nothing then.
+ * the status word, and 2^31 - 1 tiles or more (of 16 to 64 tokens of a key head
+ * for 8 or 16 of its query heads) set TOVL_ERR_UNSUPPORTED; the result of the
+ * request, or of all, means nothing then.
  * Infinite and NaN keys and values that are seen show in the results that see
  * them (an infinite value as infinite, or as NaN where its weight is 0 and in an
  * e4m3 cache, where its scale is infinite); seen tokens whose scores are all

@@ -7,6 +7,7 @@ import math
 import pytest
 import torch
 
+from consumer_movement_gemm_gb300 import tovl
 from tests.test_gpu_decode import BF16, D, DEV, U16, gen, h, randn, within  # noqa: F401
 from tests.test_gpu_paged import NAN, Cache, attn_reference, filled, ints, space
 
@@ -82,3 +83,24 @@ def test_attn_large_scores(h, kind, score):  # noqa: F811
         # weights of 1 but for the row's scale and their own rounding; sums of 600
         near = V.abs().mean(0) * (2.0 ** -11 + 4 * 600 * 2.0 ** -23) + U16 * V.mean(0).abs()
         within(out[b], V.mean(0).expand(2, 64), near.expand(2, 64), f"request {b}")
+
+
+# ------------------------------------------------------------------ the limit on tiles
+@pytest.mark.parametrize("heads", [1, 2])
+def test_attn_more_tiles_than_a_call_takes(h, heads):  # noqa: F811
+    """Requests of 2^31 - 64 tokens in one shared page, in tiles of 16: reported before a row is read."""
+    page, B = 1 << 16, 20
+    c = Cache(1, page, heads, 128, "bf16")
+    table = torch.zeros(B, 1 << 15, dtype=torch.int32, device=DEV)
+    q = torch.zeros(B, heads, 128, dtype=BF16, device=DEV)
+    out = torch.full_like(q, 7)
+    ws = space(h.attn_decode_workspace(heads, heads, 128))
+    for lens in ([2 ** 31 - 64] * B, [0, 1] + [2 ** 31 - 100] * (B - 2)):
+        assert sum(-(-n // 16) for n in lens) > 2 ** 31
+        h.attn_decode(q, c.cache, table, ints(lens), 0.1, out, ws)
+        assert h.sync_status() == tovl.TOVL_ERR_UNSUPPORTED
+        assert (out == 7).all()
+    # the next call is as ever
+    c.k.zero_(), c.v.fill_(3)
+    h.attn_decode(q, c.cache, table, ints([5] * B), 0.1, out, ws)
+    assert h.sync_status() == 0 and (out == 3).all()
