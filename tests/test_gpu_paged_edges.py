@@ -104,3 +104,65 @@ def test_attn_more_tiles_than_a_call_takes(h, heads):  # noqa: F811
     c.k.zero_(), c.v.fill_(3)
     h.attn_decode(q, c.cache, table, ints([5] * B), 0.1, out, ws)
     assert h.sync_status() == 0 and (out == 3).all()
+
+
+# ------------------------------------------------------------------ what lies around the outputs
+# workspaces of warps, CTAs and groups of CTAs; heads side by side; two blocks of a wide head from one ring (bf16, more than
+# 128 columns, 16 or 32 query heads); two blocks a warp; pages of 20 slots, copied row by row
+@pytest.mark.parametrize("heads,G,dim,kind", [(1, 1, 16, "bf16"), (8, 4, 128, "bf16"), (2, 12, 64, "bf16"), (8, 4, 80, "bf16"), (4, 1, 96, "bf16"),
+                                              (1, 8, 192, "bf16"), (1, 16, 256, "bf16"), (2, 32, 192, "bf16"), (1, 24, 256, "bf16"), (1, 5, 136, "bf16"),
+                                              (16, 1, 64, "e4m3"), (8, 8, 128, "e4m3"), (2, 16, 128, "e4m3"), (8, 2, 48, "e4m3"), (1, 16, 192, "e4m3"),
+                                              (1, 40, 256, "e4m3"), (2, 3, 240, "e4m3"), (8, 16, 96, "e4m3")])
+@pytest.mark.parametrize("page", [16, 20])
+def test_attn_writes_its_outputs_and_workspace_only(h, heads, G, dim, kind, page):  # noqa: F811
+    g = gen(heads * 1000 + G + dim)
+    n = h.attn_decode_workspace(heads * G, heads, dim)
+    for lens in ([60000], [0, 1, 40], [3000, 0, 777, 9000], list(range(0, 900, 9))):
+        B, Hq = len(lens), heads * G
+        c, table, slots = filled(g, lens, heads, dim, page, kind)
+        q = randn(g, B, Hq, dim, scale=2)
+        around = torch.full((n + 8192,), 0xa5, dtype=torch.uint8, device=DEV)
+        wide = torch.full((B + 2, Hq * dim + 32), 3.0, dtype=BF16, device=DEV)
+        stats = torch.full((B * Hq + 64,), 5.0, device=DEV)
+        out, lse = wide[1:B + 1, 16:16 + Hq * dim].view(B, Hq, dim), stats[32:32 + B * Hq].view(B, Hq)
+        h.attn_decode(q, c.cache, table, ints(lens), dim ** -0.5, out, around[4096:4096 + n], lse=lse)
+        assert h.sync_status() == 0
+        want, bound, wl, bl = attn_reference(q, c, slots, dim ** -0.5, 0)
+        within(out, want, bound, "out")
+        within(torch.where(wl == -math.inf, 0, lse), torch.where(wl == -math.inf, 0, wl), bl, "lse")
+        assert (around[:4096] == 0xa5).all() and (around[4096 + n:] == 0xa5).all(), "workspace"
+        out.fill_(3)
+        lse.fill_(5)
+        assert (wide == 3).all() and (stats == 5).all()
+
+
+# ------------------------------------------------------------------ roundings of an e4m3 cache
+@pytest.mark.parametrize("heads,dim,T", [(2, 128, 9), (1, 80, 5), (8, 64, 2000)])
+def test_append_quotients_round_to_even(h, heads, dim, T):  # noqa: F811
+    """Rows whose quotients are exact ties (the largest 448 times a power of two, the others odd multiples of half a
+    unit), and any others: the bytes of the fp32 quotient by the scale that was written."""
+    g = gen(dim)
+    # every number half way between two neighbours of e4m3, and its neighbours in bf16
+    grid = torch.arange(0, 127, dtype=torch.uint8).view(torch.float8_e4m3fn).float()
+    half = (grid[1:] + grid[:-1]) / 2
+    near = torch.cat([half, half * (1 - 2.0 ** -8), half * (1 + 2.0 ** -7)]).to(BF16).float()
+    pool = torch.cat([near, -near]).to(DEV)
+    x = pool[torch.randint(0, len(pool), (T, heads, dim), generator=g, device=DEV)].clamp(-448, 448)
+    x[:, :, dim // 3] = 448
+    x = x * torch.exp2(torch.randint(-20, 20, (T, heads, 1), generator=g, device=DEV).float())
+    x[T // 2:] = torch.randn(T - T // 2, heads, dim, generator=g, device=DEV)
+    x = x.to(BF16)
+    page = 16
+    c = Cache(-(-T // page), page, heads, dim, "e4m3")
+    slots = torch.arange(T, device=DEV)
+    h.rope_append(x, x, x, slots.to(torch.int32), slots.to(torch.int32), None, c.cache, torch.empty_like(x))
+    assert h.sync_status() == 0
+    for t, s in ((c.k, c.ks), (c.v, c.vs)):
+        scale = s[slots // page, :, slots % page]
+        top = x.float().abs().amax(2)
+        assert torch.equal(scale, top / torch.full_like(top, 448))
+        got = t.view(torch.uint8)[slots // page, slots % page].view(t.dtype).float()
+        want = (x.float() / scale[:, :, None]).clamp(-448, 448).to(t.dtype).float()
+        assert torch.equal(got, want)
+        ties = (x[:T // 2].float() / scale[:T // 2, :, None]).abs()[..., None] == half.to(DEV)
+        assert ties.any(3).float().mean() > 0.2
