@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
     constexpr int kTile = S::kTile, NT = S::NT, JT = S::JT, MT = S::MT, kStages = S::kStages, CB = S::CB;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (tid == 0) {
+    if (tid == 0 && p.boxed) {
         ptx::prefetch_tmap(&p.k_map);
         ptx::prefetch_tmap(&p.v_map);
     }
