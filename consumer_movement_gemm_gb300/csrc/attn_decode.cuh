@@ -340,11 +340,11 @@ constexpr int kGroup = 12;
 constexpr int kAtOnce = 4;     // segments of other CTAs that are joined at a time
 
 // What each CTA gets of the call's tiles: `each`, the first `rest` one more; or,
-// where all segments have `count` tiles, one of `parts` parts of one of them,
+// where all segments have as many tiles, one of `parts` parts of one of them,
 // shared out alike.
 struct Shares {
     int ctas, each, rest;
-    int count, parts;          // parts == 0: the former
+    int parts;                 // 0: the former
     __device__ __forceinline__ int start(int c) const { return c * each + min(c, rest); }
     // the CTA that a tile belongs to
     __device__ __forceinline__ int owner(int tile) const
@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
     // parts to join cost as much as they save.  One request, 8 heads: 300 tokens in one
     // CTA a head 7.6 us, in equal parts over all CTAs 9.5; 777 in five 8.7, over all 11.7;
     // 4096 in 12 10.8, in 19 11.6, over all 14.1.
-    Shares shares = {static_cast<int>(gridDim.x), 0, 0, first_count, 0};
+    Shares shares = {static_cast<int>(gridDim.x), 0, 0, 0};
     const int grid = gridDim.x, segments = p.B * groups;
     if (equal && segments <= grid && total < 4 * grid * turns) {
         const int most = p.by_turns.div(first_count + turns - 1);
