@@ -149,7 +149,7 @@ TOVL_API int tovl_rope_append(tovl_handle h, const tovl_rope_append_args* args, 
     if (T < 0 || Hq < 1 || rot < 0 || rot > D || (rot && (!cos_sin || max_pos < 1))) return TOVL_ERR_INVALID;
     if (rot % 16 || Hq > kMaxQueryHeads) return TOVL_ERR_UNSUPPORTED;
     if (T == 0) return TOVL_OK;
-    if (!positions || !slots || !aligned(positions, 4) || !aligned(slots, 4) || !aligned16(cos_sin)) return TOVL_ERR_INVALID;
+    if (!positions || !slots || !aligned(positions, 4) || !aligned(slots, 4) || (rot && !aligned16(cos_sin))) return TOVL_ERR_INVALID;
     const long long wide_q = static_cast<long long>(Hq) * D, wide_k = static_cast<long long>(p.cache.heads) * D;
     if (!valid_rows(q, ldq, wide_q) || !valid_rows(k, ldk, wide_k) || !valid_rows(v, ldv, wide_k) || !valid_rows(q_out, ldqo, wide_q))
         return TOVL_ERR_INVALID;

@@ -7,7 +7,7 @@ import pytest
 
 from consumer_movement_gemm_gb300 import build as tovl_build
 from consumer_movement_gemm_gb300 import tovl
-from tests.test_paged_abi import ATTN, OK, call
+from tests.test_paged_abi import ATTN, INVALID, OK, P, ROPE, call
 
 
 @pytest.fixture(scope="module")
@@ -56,3 +56,9 @@ def test_a_call_of_more_tiles_than_ints_count_is_over_the_limit(lib, heads, Hq, 
     groups = heads * -(-Hq // heads // 8) // together
     assert lib.most_tiles() < 2 ** 31 - 1
     assert lib.most_tiles() * groups < 2 ** 31 - 1 <= (lib.most_tiles() + 1) * groups
+
+
+def test_angles_are_looked_at_where_something_is_rotated(lib):
+    assert call(lib, "tovl_rope_append", ROPE, cos_sin=P + 4) == (INVALID, 0)
+    for table in (P + 4, None):
+        assert call(lib, "tovl_rope_append", ROPE, rot=0, cos_sin=table) == (OK, 1)
