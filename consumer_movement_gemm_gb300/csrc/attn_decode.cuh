@@ -423,6 +423,7 @@ __device__ __forceinline__ void join(const float* const* part, int n, int stats,
 template <class S, int U>
 __device__ __forceinline__ void join_all(const AttnParams& p, const Joined* joined, const float* const* parts, int count, int warp, int lane)
 {
+    static_assert(S::JT % U == 0, "every column block of a segment is one warp's");
     constexpr int kOfHeads = S::JT / U, kUnits = S::NT * kOfHeads;
     for (int at = warp; at < count * kUnits; at += S::kWarps) {
         const Joined seg = joined[at / kUnits];
@@ -1056,8 +1057,8 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
         // half of them each leaves no warp idle: more loads in flight, and the weights
         // worked out once.  Two / one, us: 1 request of 32768, 1 head of 128 for 16, 16.3 /
         // 18.4; 256 up to 2048, 8 for 64, e4m3, 101 / 104.  Four / two: 32 of 2048, 1 head
-        // of 256 for 16, e4m3, 22.5 / 24.9.
-        constexpr int kBlocks = NT * JT, kLeast = kBlocks > S::kWarps ? 2 : 1, kMost = kLeast == 2 && S::kWarps <= 8 ? 4 : 2;
+        // of 256 for 16, e4m3, 22.5 / 24.9.  (Six column blocks: two.)
+        constexpr int kBlocks = NT * JT, kLeast = kBlocks > S::kWarps ? 2 : 1, kMost = kLeast == 2 && S::kWarps <= 8 && JT % 4 == 0 ? 4 : 2;
         if (count * kBlocks <= kLeast * S::kWarps) join_all<S, kLeast>(p, s_joined, s_part, count, warp, lane);
         else join_all<S, kMost>(p, s_joined, s_part, count, warp, lane);
         if (round >= 0) arriving |= list & __ballot_sync(0xffffffffu, in_group);

@@ -85,6 +85,24 @@ def test_attn_large_scores(h, kind, score):  # noqa: F811
         within(out[b], V.mean(0).expand(2, 64), near.expand(2, 64), f"request {b}")
 
 
+# ------------------------------------------------------------------ joins
+# every number of columns and of blocks of query heads; requests of which many are joined in one CTA, in many
+@pytest.mark.parametrize("dim", [16, 64, 72, 80, 88, 96, 104, 128, 144, 192, 208, 256])
+@pytest.mark.parametrize("heads,G", [(3, 32), (1, 9), (2, 16), (4, 8), (8, 1)])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_attn_joins_write_every_column(h, dim, heads, G, kind):  # noqa: F811
+    if kind == "e4m3" and dim % 16:
+        dim += 8
+    g = gen(dim * 100 + G)
+    for lens in ([440] * 60, list(range(20, 700, 17)), [3000, 1000, 9000]):
+        c, table, slots = filled(g, lens, heads, dim, 16, kind)
+        q = randn(g, len(lens), heads * G, dim, scale=2)
+        out, lse = attend(h, q, c, table, lens, dim ** -0.5)
+        want, bound, wl, bl = attn_reference(q, c, slots, dim ** -0.5, 0)
+        within(out, want, bound, f"out {lens[:2]}")
+        within(lse, wl, bl, f"lse {lens[:2]}")
+
+
 # ------------------------------------------------------------------ the limit on tiles
 @pytest.mark.parametrize("heads", [1, 2])
 def test_attn_more_tiles_than_a_call_takes(h, heads):  # noqa: F811
