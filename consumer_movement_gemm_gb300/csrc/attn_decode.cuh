@@ -13,7 +13,7 @@
 // S^T's accumulators turned into P^T's fragments by an 8 x 8 transposition in
 // registers.  bf16 caches: P enters the second product as two bf16 numbers, its
 // upper bits and the rest (2^-15 is left); one bf16 P would add as much error
-// as the rounding of the result.  e4m3 caches: rows become fp16 exactly, q fp16
+// as the rounding of the result.  Exponentials below 2^-126 are 0.  e4m3 caches: rows become fp16 exactly, q fp16
 // times a power of two per head, P times the row's scale fp16 (2^-11 of
 // itself, below 2^-14 of the largest an absolute 2^-25 of that).
 //
@@ -33,7 +33,7 @@
 // latency of the instructions between e4m3 row and product at three warps a
 // scheduler (4 of 65536 tokens: 90 us, 6.1 TB/s; heads of 64 5.6), and for few
 // tokens a chain of dependent steps: launch, lengths, shares, page, rows, products,
-// parts and their joins (1 request of 64 tokens 5.5 us, of 777 9.0, of 4096 11.0).
+// parts and their joins (1 request of 64 tokens 5.1 us, of 777 8.6, of 4096 10.6).
 // With eight warps instead of twelve the first takes 346 us, the third 105; with rows
 // by cp.async the first took 372 us where it took 350 with boxes.
 #pragma once
@@ -64,6 +64,8 @@ struct Shape {
     static constexpr int JT = DP / 16;             // blocks of 16 columns
     static constexpr int kStage = 2 * kRows;
     static constexpr int kScaleStage = F8 ? 2 * kTile * 4 : 0;
+    // e4m3 with two blocks of heads: twelve warps of 168 registers (64 and 128 columns
+    // spill 16 and 104 bytes a thread), eight of 255 (256 columns: 8 bytes).
     static constexpr int kWarps = kRow > 384 && !PAIR_ ? 6 : kRow > 256 && !PAIR_ ? 8 : NT == 1 || (F8 && DP <= 128) ? 12 : 8;
     static constexpr int kFit = (214 * 1024) / (kWarps * (kStage + kScaleStage));
     static constexpr int kStages = kFit > 4 ? 4 : kFit;                 // a warp's share of its ring's
@@ -525,8 +527,8 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const __gri
     // tiles a warp is one CTA's, because the join of CTAs costs more than two tiles; a
     // longer one is split to a tile a warp, and from the twelfth CTA on to two, where more
     // parts to join cost as much as they save.  One request, 8 heads: 300 tokens in one
-    // CTA a head 7.6 us, in equal parts over all CTAs 9.5; 777 in five 8.7, over all 11.7;
-    // 4096 in 12 10.8, in 19 11.6, over all 14.1.
+    // CTA a head 7.0 us, in equal parts over all CTAs 9.4; 777 in five 8.6, over all 10.7;
+    // 4096 in 12 10.6, over all 12.1.
     Shares shares = {static_cast<int>(gridDim.x), 0, 0, 0};
     const int grid = gridDim.x, segments = p.B * groups;
     if (equal && segments <= grid && total < 4 * grid * turns) {

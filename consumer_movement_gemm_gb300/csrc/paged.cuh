@@ -113,7 +113,7 @@ int attn_decode_together(const AttnShape& s, int heads, int dim, bool e4m3);
 // bf16 heads of more than 128 columns with an even number of blocks of 8 query
 // heads: two warps take two blocks from one ring, which leaves the shared memory
 // for 12 warps (with rings of their own: 6).  32 requests up to 8192 tokens, 1 head
-// of 256 for 16: 42 us, with rings of their own 46; with 16 heads a warp the sums do
+// of 256 for 16: 39 us, with rings of their own 41; with 16 heads a warp the sums do
 // not fit the registers.
 bool attn_decode_pairs(int dim, bool e4m3, int group);
 long long attn_decode_workspace(int heads, int group, int dim, int num_sms);

@@ -62,7 +62,8 @@ bool valid_rows(const void* p, long long ld, long long width)
 // is also faster for rows of one box that start off the 32-byte sectors.  64 requests
 // of 4096 tokens, 4 heads for 16, boxes / rows, us: e4m3 of 16 50 / 33, of 48 50 / 39, of
 // 80 61 / 48, of 112 60 / 58, bf16 of 40 53 / 44; rows of two boxes: bf16 of 72 67 / 67,
-// e4m3 of 144 78 / 80.
+// e4m3 of 144 78 / 80; rows of whole sectors: e4m3 of 32 42 / 33 (the rule loses there), of
+// 64 35 / 34, of 96 50 / 49, bf16 of 16 33 / 37, of 32 33 / 36, of 48 43 / 45.
 bool map_cache(tovl_ctx* h, AttnParams* p, bool e4m3, const AttnShape& shape, int together)
 {
     const int tile = shape.rows, box_bytes = shape.box_bytes;

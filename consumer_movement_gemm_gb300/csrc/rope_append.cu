@@ -11,7 +11,8 @@
 //
 // What bounds it: a launch and dependent loads (position, slot, angles) for few
 // tokens (1 token, 32 + 2 x 8 heads of 128: 1.7 us); HBM for many (16384 tokens
-// 67 us, 6.1 TB/s, with 24 warps an SM; 72 us with the 22 of unlimited registers).
+// 67 us, 6.1 TB/s, with 24 warps an SM, whose 64 registers leave 28 bytes a thread in
+// local memory where a lane has three heads; 72 us with the 22 warps of unlimited ones).
 #include <cuda_bf16.h>
 #include "common.cuh"
 #include "paged.cuh"
@@ -205,8 +206,9 @@ cudaError_t launch_rope_append(const RopeParams& p, bool e4m3, int num_sms, cuda
     const int lanes = (p.cache.dim + 15) / 16;
     // three heads a lane where that leaves eight warps for every SM.  16384 tokens, 32 +
     // 2 x 8 heads, three / four, us: of 128 67.4 / 68.8 (two 74), of 64 35.3 / 37.9, of 80
-    // 49.7 / 51.3, of 256 (8 + 2 x 2) 35.7 / 38.4; e4m3, of 128 75.7 / 72.6.  Up to 256
-    // tokens one head is as good.
+    // 49.7 / 51.3, of 256 (8 + 2 x 2) 35.7 / 38.4; e4m3, of 64 48 / 58, of 80 62 / 69, of 96
+    // 72 / 79, of 256 48 / 57, of 192 (16 + 2 x 4) 71 / 71, of 128 75.8 / 72.3 and (64 + 2 x 8)
+    // 134 / 120: only there are four better.  Up to 256 tokens one head is as good.
     const long long warps = static_cast<long long>(p.T) * (p.Hq + 2 * p.cache.heads) * lanes / 32;
     return warps < 32LL * num_sms ? launch<1>(p, e4m3, lanes, stream, pdl) : launch<3>(p, e4m3, lanes, stream, pdl);
 }

@@ -488,8 +488,9 @@ long long tovl_attn_decode_workspace(tovl_handle h, int Hq, int heads, int dim);
  *   z[t] = scale * q[b][g] . k[t], t from max(0, length - window) (0 without a
  *   window) to length - 1, k and v of head g / (Hq / heads),
  *   out[b][g] = sum of softmax(z)[t] v[t], lse[b][g] = ln sum exp z[t]
- * with fp32 sums, rounded once to bf16.  Weights are off by 2^-15 of themselves
- * with a bf16 cache, with an e4m3 one by 2^-11, and where weight times v_scale is
+ * with fp32 sums of weights, up to 2^8 each, times values, rounded once to bf16.
+ * Weights are off by 2^-15 of themselves with a bf16 cache (0 below 2^-126 of a
+ * row's largest), with an e4m3 one by 2^-11, and where weight times v_scale is
  * below 2^-14 of a row's largest by 2^-25 of that, or by 2^-73 where the largest
  * is below 2^-48.  With an e4m3 cache scores are up to 2^26 in magnitude.
  *   q           device, bf16 [B][Hq][dim], requests ldq elements apart (a
